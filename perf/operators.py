@@ -197,6 +197,14 @@ def _handle(reqs, spec, vocab):
     return sv.Verifier(reqs, spec, vocab)
 
 
+def _cache(s):
+    """The package's description of the cache, kept beside the handle."""
+    if not own:
+        return None
+    import speculative_decoding_token_rejection_gb300 as sv
+    return sv.KVCache(k=s["k"], v=s["v"], k_scale=s["ks"], v_scale=s["vs"])
+
+
 def prepare(case, seed):
     gen = torch.Generator(device=DEV).manual_seed(seed)
     s = dict(case=case)
@@ -222,7 +230,7 @@ def prepare(case, seed):
         s["slots"] = slots
         s["key_out"] = torch.empty(T, h, d, dtype=dt, device=DEV)
         s["value_out"] = torch.empty(T, h, d, dtype=dt, device=DEV)
-        s["handle"] = _handle(1, 0, 1)
+        s["handle"], s["cache"] = _handle(1, 0, 1), _cache(s)
     elif op == "attend":
         N, b, h, hq, d = case["reqs"], case["block"], case["kv_heads"], case["q_heads"], case["dim"]
         gam, own_len = _gammas(case), _owned(case)
@@ -249,7 +257,7 @@ def prepare(case, seed):
         s["v"], s["vs"] = _fill(gen, case, blocks)
         s["out"] = torch.empty(rows, hq, d, dtype=torch.bfloat16, device=DEV)
         s["lse"] = torch.empty(rows, hq, device=DEV)
-        s["handle"] = _handle(N, case["spec"], 1)
+        s["handle"], s["cache"] = _handle(N, case["spec"], 1), _cache(s)
         s["workspace"] = None
         if own:
             s["workspace"] = s["handle"].attend_workspace(num_reqs=N, max_spec_len=case["spec"], num_q_heads=hq,
@@ -305,14 +313,13 @@ def run(state):
 
 
 def _run_own(s, case):
-    import speculative_decoding_token_rejection_gb300 as sv
     op, ver = case["op"], s["handle"]
     if op == "logprobs":
         ver.logprobs(logits=s["logits"], out_tokens=s["tokens"], cu_num_draft_tokens=s["cu"],
                      temperature=s["temperature"], num_top=case["top"], logprobs=s["logprobs"], ranks=s["ranks"],
                      entropy=s["entropy"], top_ids=s["top_ids"], top_logprobs=s["top_logprobs"])
         return {k: s[k] for k in ("logprobs", "ranks", "entropy", "top_ids", "top_logprobs")}
-    cache = sv.KVCache(k=s["k"], v=s["v"], k_scale=s["ks"], v_scale=s["vs"])
+    cache = s["cache"]
     if op == "attend":
         ver.attend(q=s["q"], cache=cache, block_tables=s["table"], seq_lens=s["seq_lens"],
                    max_seq_len=s["max_seq_len"], max_spec_len=case["spec"], cu_num_draft_tokens=s["cu"],
