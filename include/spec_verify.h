@@ -80,7 +80,8 @@ enum sv_data_status {
   SV_DATA_MISSING_DRAFT = 64,     /* draft == NULL but a random request needs draft rows */
   SV_DATA_COPY_TIMEOUT = 128,     /* a bulk row copy did not complete within its wait limit (request
                                      emits nothing); never expected on a healthy GPU */
-  SV_DATA_BAD_LIST = 256          /* a penalty, banned or stop list range of the request is invalid */
+  SV_DATA_BAD_LIST = 256,         /* a penalty, banned or stop list range of the request is invalid */
+  SV_DATA_BAD_SLOT = 512          /* a KV slot or a block-table entry outside the cache (the token is left out) */
 };
 
 /* Handle flags.  SV_FLAG_RESIDENT_ROWS: the logits entry copies both the
@@ -319,6 +320,162 @@ sv_status spec_verify_ngram_propose(spec_verify_t handle, const spec_verify_ngra
 /* Host-only validation of n-gram proposer arguments against `config`. */
 sv_status spec_verify_check_ngram_args(const spec_verify_config *config, const spec_verify_ngram_args *args);
 
+/* ---------------------------------------------------------------------------
+ * The paged 8-bit KV cache, and the verify tokens' attention over it.
+ *
+ * A cache is num_blocks pages of block_size tokens.  The K (V) row of token
+ * offset t of page b and kv head h is head_dim bytes at
+ * k (v) + b * block_stride + h * head_stride + t * token_stride, and its scale
+ * is the float at b * scale_block_stride + h * scale_head_stride +
+ * t * scale_token_stride: byte x stands for x * scale.  Head-major and
+ * token-major pages are both strides.  Slot s (the framework's slot_mapping,
+ * "How speculative decoding interacts with the KV cache", section 3.2) is page
+ * s / block_size, offset s % block_size.
+ *
+ * Quantising a row x: scale = max(max_d |x_d| / Q, 2^-64) with Q = 127 (int8)
+ * or 448 (e4m3), byte = x / scale rounded to nearest even (IEEE division).
+ * 2^-64 keeps the scale of a zero row positive.  A row that holds a NaN or an
+ * infinity gets scale NaN and zero bytes (it reads back as NaN) and raises
+ * SV_DATA_BAD_VALUES.
+ */
+enum sv_cache_format { SV_CACHE_INT8 = 0, SV_CACHE_E4M3 = 1 };
+
+typedef struct spec_verify_kv_cache {
+  void *k, *v;              /* 16-byte aligned; strides in bytes, multiples of 16 */
+  float *k_scale, *v_scale; /* strides in elements */
+  int64_t num_blocks;       /* >= 1; num_blocks * block_size <= 2^31 - 1 pages' tokens */
+  int32_t block_size;       /* >= 1 (any: a power of two is not needed) */
+  int32_t num_kv_heads;     /* >= 1 */
+  int32_t head_dim;         /* 64 or 128 */
+  int32_t format;           /* SV_CACHE_* */
+  int64_t block_stride, head_stride, token_stride;
+  int64_t scale_block_stride, scale_head_stride, scale_token_stride;
+} spec_verify_kv_cache;
+
+/* Writing tokens to the cache, and reading them back.  Row (t, h) of key
+ * (value) is head_dim elements of `dtype` at element t * token_stride +
+ * h * head_stride.  slot_mapping[t] = SV_PADDING_SLOT_ID (-1), as the verifier
+ * leaves it for rejected drafts: a write skips the token, a read gives zeros.
+ * Any other slot outside the cache does the same and raises SV_DATA_BAD_SLOT.
+ * Two tokens of one call must not share a slot. */
+typedef struct spec_verify_kv_args {
+  int64_t num_tokens; /* T >= 0 (0 is a no-op) */
+  int32_t dtype;      /* SV_F32 or SV_BF16: the elements of key and value */
+  uint32_t reserved;  /* 0 */
+  spec_verify_kv_cache cache;
+  void *key;   /* read by spec_verify_kv_write, written by spec_verify_kv_read */
+  int64_t key_token_stride, key_head_stride;
+  void *value;
+  int64_t value_token_stride, value_head_stride;
+  const int64_t *slot_mapping; /* [T] */
+  int32_t *status;             /* [1] or NULL: SV_DATA_* bits OR-ed in */
+} spec_verify_kv_args;
+
+sv_status spec_verify_kv_write(spec_verify_t handle, const spec_verify_kv_args *args, void *stream);
+sv_status spec_verify_kv_read(spec_verify_t handle, const spec_verify_kv_args *args, void *stream);
+
+/* Host-only validation of the arguments of either call against `config`. */
+sv_status spec_verify_check_kv_args(const spec_verify_config *config, const spec_verify_kv_args *args);
+
+/* Attention of the verify tokens over the cache.  The tokens are laid out as
+ * the target rows of spec_verify_args: request i owns rows s_i + i ..
+ * s_i + i + gamma_i of q, out and lse.  seq_lens[i] = L counts the request's
+ * keys, its own gamma_i + 1 verify tokens (already written) included; row j is
+ * at position L - (gamma_i + 1) + j and sees the keys 0 .. position.  Query
+ * head x reads kv head x / (num_q_heads / num_kv_heads).
+ *   s_k = scale * q . key_k;  lse = ln sum_k exp s_k;
+ *   out = sum_k exp(s_k - lse) value_k
+ * A row that sees no key (L = 0, say) gives out = 0 and lse = -infinity.
+ * Key k of request i is at page block_tables[i, k / block_size], offset
+ * k % block_size.  The first shared_prefix_len tokens (a multiple of
+ * block_size) are the same pages for every request -- entries
+ * 0 .. shared_prefix_len / block_size - 1 of row 0 of block_tables stand for
+ * all -- and are read once for the whole batch.  A page outside the cache
+ * leaves its keys out and raises SV_DATA_BAD_SLOT; a seq_len outside
+ * [0, max_seq_len] or past its block table raises SV_DATA_BAD_PARAM and gives the request's rows
+ * out = 0, lse = -infinity; a bad cu range raises SV_DATA_BAD_CU and leaves
+ * the rows unwritten.  A NaN score makes its row NaN; nothing of a key that a
+ * row does not see reaches it, whatever the cache holds there. */
+typedef struct spec_verify_attend_args {
+  int32_t num_reqs;     /* N >= 0 (0 is a no-op) */
+  int32_t max_spec_len; /* G: every gamma_i <= G */
+  int32_t num_q_heads;  /* a multiple of num_kv_heads */
+  int32_t max_seq_len;  /* >= 0; bounds every seq_len, as block_table_stride * block_size does */
+  int32_t shared_prefix_len; /* 0 .. either bound, a multiple of block_size */
+  uint32_t reserved;         /* 0 */
+  int64_t num_draft_tokens_total; /* T = cu[N-1]; must equal N*G when cu == NULL */
+  const int32_t *cu_num_draft_tokens; /* [N] inclusive prefix sums, or NULL: every gamma_i = G */
+  spec_verify_kv_cache cache;
+  const void *q; /* [T+N, num_q_heads, head_dim] bf16, any element strides, unit stride within a head */
+  int64_t q_token_stride, q_head_stride;
+  const int32_t *block_tables; /* [N, block_table_stride] */
+  int64_t block_table_stride;
+  const int32_t *seq_lens; /* [N] */
+  float scale;             /* finite */
+  uint32_t reserved2;      /* 0 */
+  void *out; /* [T+N, num_q_heads, head_dim] bf16 */
+  int64_t out_token_stride, out_head_stride;
+  float *lse;      /* [T+N, num_q_heads] contiguous, or NULL */
+  void *workspace; /* 16-byte aligned device scratch of spec_verify_attend_workspace_size bytes; contents need no
+                      initialisation and mean nothing after the call.  Calls that may run at the same time need
+                      one each. */
+  int64_t workspace_bytes;
+  int32_t *status; /* [1] or NULL: SV_DATA_* bits OR-ed in */
+} spec_verify_attend_args;
+
+sv_status spec_verify_attend(spec_verify_t handle, const spec_verify_attend_args *args, void *stream);
+
+/* Bytes of workspace a call of these sizes needs (pointers are not looked at:
+ * num_reqs, max_spec_len, num_q_heads, max_seq_len, shared_prefix_len,
+ * num_draft_tokens_total, cache.num_kv_heads and cache.head_dim are). */
+sv_status spec_verify_attend_workspace_size(spec_verify_t handle, const spec_verify_attend_args *args, int64_t *bytes);
+
+/* Host-only validation of attention arguments against `config` (the workspace's size aside). */
+sv_status spec_verify_check_attend_args(const spec_verify_config *config, const spec_verify_attend_args *args);
+
+/* Log-probabilities of the committed tokens, as a server returns them with the
+ * text.  Logits rows and out_tokens are those of spec_verify_run: token
+ * out_tokens[i, m] belongs to logits row s_i + i + m.  Entries of -1 (past the
+ * commit) are skipped: their rows are not read, and they give 0 in the float
+ * outputs and -1 in ranks and top_ids.  For the others, with x = the row
+ * divided by the request's temperature (0 counts as 1: a greedy request has
+ * the untempered distribution):
+ *   logprobs = x[token] - ln sum exp x;  ranks = 1 + #{logits > logit[token]};
+ *   entropy = -sum p ln p;  top_ids / top_logprobs = the num_top largest
+ *   logits, the lowest index first among equal ones.
+ * To score given tokens, pass max_spec_len = 0 and one token per row.  A -inf
+ * logit has probability 0.  A row with a NaN, a +inf or no finite logit raises
+ * SV_DATA_BAD_VALUES and gives NaN, ranks and top_ids -1; so do a temperature
+ * that is negative, subnormal or not finite (SV_DATA_BAD_PARAM) and a token
+ * outside [0, V) (SV_DATA_BAD_DRAFT_ID); a bad cu range (SV_DATA_BAD_CU)
+ * gives the request's outputs as for -1. */
+#define SV_MAX_TOP_LOGPROBS 32
+typedef struct spec_verify_logprobs_args {
+  int32_t num_reqs;     /* N >= 0 (0 is a no-op) */
+  int32_t max_spec_len; /* G: out_tokens has G + 1 columns */
+  int32_t vocab_size;   /* V >= 1 */
+  int32_t dtype;        /* SV_F32 or SV_BF16 logits */
+  int32_t num_top;      /* K: 0 .. min(V, SV_MAX_TOP_LOGPROBS) */
+  uint32_t reserved;    /* 0 */
+  int64_t num_draft_tokens_total;     /* T = cu[N-1]; must equal N*G when cu == NULL */
+  const int32_t *cu_num_draft_tokens; /* [N] inclusive prefix sums, or NULL: every gamma_i = G */
+  const void *logits;                 /* [T+N rows, row_stride], any alignment of the rows */
+  int64_t row_stride;                 /* elements between rows (>= V) */
+  const float *temperature;           /* [N] or NULL (= 1) */
+  const int32_t *out_tokens;          /* [N, G+1] */
+  float *logprobs;                    /* [N, G+1] out */
+  int32_t *ranks;                     /* [N, G+1] out or NULL */
+  float *entropy;                     /* [N, G+1] out or NULL */
+  int32_t *top_ids;                   /* [N, G+1, K] out (NULL only when K = 0) */
+  float *top_logprobs;                /* [N, G+1, K] out (NULL only when K = 0) */
+  int32_t *status;                    /* [1] or NULL: SV_DATA_* bits OR-ed in */
+} spec_verify_logprobs_args;
+
+sv_status spec_verify_logprobs(spec_verify_t handle, const spec_verify_logprobs_args *args, void *stream);
+
+/* Host-only validation of log-probability arguments against `config`. */
+sv_status spec_verify_check_logprobs_args(const spec_verify_config *config, const spec_verify_logprobs_args *args);
+
 /* Create a handle.  Queries the device and sets kernel attributes on it
  * (temporarily making `device` current).  *out is set only on SV_OK. */
 sv_status spec_verify_create(const spec_verify_config *config, spec_verify_t *out);
@@ -346,6 +503,9 @@ size_t spec_verify_sizeof_config(void);
 size_t spec_verify_sizeof_args(void);
 size_t spec_verify_sizeof_sample_args(void);
 size_t spec_verify_sizeof_ngram_args(void);
+size_t spec_verify_sizeof_kv_args(void);
+size_t spec_verify_sizeof_attend_args(void);
+size_t spec_verify_sizeof_logprobs_args(void);
 
 #ifdef __cplusplus
 }

@@ -28,7 +28,7 @@ SV_F32, SV_BF16 = 0, 1
 SV_MAX_SPEC_LEN = 256
 DATA_STATUS_BITS = {
     "BAD_CU": 1, "BAD_DRAFT_ID": 2, "BAD_EXPONENTIAL": 4, "EMPTY_DISTRIBUTION": 8,
-    "BAD_VALUES": 16, "BAD_PARAM": 32, "MISSING_DRAFT": 64, "COPY_TIMEOUT": 128,
+    "BAD_VALUES": 16, "BAD_PARAM": 32, "MISSING_DRAFT": 64, "COPY_TIMEOUT": 128, "BAD_LIST": 256, "BAD_SLOT": 512,
 }
 
 _P = ctypes.c_void_p
@@ -40,6 +40,8 @@ SV_FLAG_SERIAL_LAUNCH = 4
 SV_HINT_SMALL_TOP_K = 1
 SV_SMALL_TOP_K_MAX = 256
 SV_TEST_EXPIRE_COPY_WAIT = 1
+SV_CACHE_INT8, SV_CACHE_E4M3 = 0, 1
+SV_MAX_TOP_LOGPROBS = 32
 
 
 class SpecVerifyConfig(ctypes.Structure):
@@ -92,6 +94,49 @@ class SpecVerifyNgramArgs(ctypes.Structure):
     ]
 
 
+class SpecVerifyKvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("num_blocks", ctypes.c_int64),
+        ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("format", ctypes.c_int32), ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64), ("scale_block_stride", ctypes.c_int64),
+        ("scale_head_stride", ctypes.c_int64), ("scale_token_stride", ctypes.c_int64),
+    ]
+
+
+class SpecVerifyKvArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+        ("cache", SpecVerifyKvCache),
+        ("key", _P), ("key_token_stride", ctypes.c_int64), ("key_head_stride", ctypes.c_int64),
+        ("value", _P), ("value_token_stride", ctypes.c_int64), ("value_head_stride", ctypes.c_int64),
+        ("slot_mapping", _P), ("status", _P),
+    ]
+
+
+class SpecVerifyAttendArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", ctypes.c_int32), ("max_spec_len", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+        ("max_seq_len", ctypes.c_int32), ("shared_prefix_len", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+        ("num_draft_tokens_total", ctypes.c_int64), ("cu_num_draft_tokens", _P), ("cache", SpecVerifyKvCache),
+        ("q", _P), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("block_tables", _P), ("block_table_stride", ctypes.c_int64), ("seq_lens", _P),
+        ("scale", ctypes.c_float), ("reserved2", ctypes.c_uint32),
+        ("out", _P), ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("lse", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_int64), ("status", _P),
+    ]
+
+
+class SpecVerifyLogprobsArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", ctypes.c_int32), ("max_spec_len", ctypes.c_int32), ("vocab_size", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("num_top", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+        ("num_draft_tokens_total", ctypes.c_int64), ("cu_num_draft_tokens", _P),
+        ("logits", _P), ("row_stride", ctypes.c_int64), ("temperature", _P), ("out_tokens", _P),
+        ("logprobs", _P), ("ranks", _P), ("entropy", _P), ("top_ids", _P), ("top_logprobs", _P), ("status", _P),
+    ]
+
+
 class NativeLibraryMissing(RuntimeError):
     pass
 
@@ -107,7 +152,10 @@ EXPORTED = ("spec_verify_create", "spec_verify_run", "spec_verify_destroy", "spe
             "spec_verify_status_string", "spec_verify_last_error", "spec_verify_abi_version",
             "spec_verify_sizeof_config", "spec_verify_sizeof_args", "spec_verify_sample",
             "spec_verify_check_sample_args", "spec_verify_sizeof_sample_args", "spec_verify_ngram_propose",
-            "spec_verify_check_ngram_args", "spec_verify_sizeof_ngram_args")
+            "spec_verify_check_ngram_args", "spec_verify_sizeof_ngram_args", "spec_verify_kv_write",
+            "spec_verify_kv_read", "spec_verify_check_kv_args", "spec_verify_sizeof_kv_args", "spec_verify_attend",
+            "spec_verify_attend_workspace_size", "spec_verify_check_attend_args", "spec_verify_sizeof_attend_args",
+            "spec_verify_logprobs", "spec_verify_check_logprobs_args", "spec_verify_sizeof_logprobs_args")
 
 
 def load_library(path: Optional[str] = None):
@@ -145,6 +193,23 @@ def load_library(path: Optional[str] = None):
     lib.spec_verify_check_ngram_args.argtypes = [ctypes.POINTER(SpecVerifyConfig), ctypes.POINTER(SpecVerifyNgramArgs)]
     lib.spec_verify_check_ngram_args.restype = ctypes.c_int
     lib.spec_verify_sizeof_ngram_args.restype = ctypes.c_size_t
+    for name, struct in (("kv", SpecVerifyKvArgs), ("attend", SpecVerifyAttendArgs),
+                         ("logprobs", SpecVerifyLogprobsArgs)):
+        check = getattr(lib, f"spec_verify_check_{name}_args")
+        check.argtypes = [ctypes.POINTER(SpecVerifyConfig), ctypes.POINTER(struct)]
+        check.restype = ctypes.c_int
+        size = getattr(lib, f"spec_verify_sizeof_{name}_args")
+        size.restype = ctypes.c_size_t
+        if size() != ctypes.sizeof(struct):
+            raise RuntimeError("spec_verify struct layout differs from the binding")
+    for name, struct in (("kv_write", SpecVerifyKvArgs), ("kv_read", SpecVerifyKvArgs),
+                         ("attend", SpecVerifyAttendArgs), ("logprobs", SpecVerifyLogprobsArgs)):
+        fn = getattr(lib, f"spec_verify_{name}")
+        fn.argtypes = [ctypes.c_void_p, ctypes.POINTER(struct), ctypes.c_void_p]
+        fn.restype = ctypes.c_int
+    lib.spec_verify_attend_workspace_size.argtypes = [ctypes.c_void_p, ctypes.POINTER(SpecVerifyAttendArgs),
+                                                      ctypes.POINTER(ctypes.c_int64)]
+    lib.spec_verify_attend_workspace_size.restype = ctypes.c_int
     if lib.spec_verify_sizeof_config() != ctypes.sizeof(SpecVerifyConfig) or \
             lib.spec_verify_sizeof_args() != ctypes.sizeof(SpecVerifyArgs) or \
             lib.spec_verify_sizeof_sample_args() != ctypes.sizeof(SpecVerifySampleArgs) or \
@@ -413,11 +478,258 @@ def spec_verify_check_args(config: SpecVerifyConfig, args: SpecVerifyArgs) -> in
     return int(load_library().spec_verify_check_args(ctypes.byref(config), ctypes.byref(args)))
 
 
+# ----------------------------------------------------------------------------
+# the paged 8-bit KV cache, attention over it, log-probabilities
+# ----------------------------------------------------------------------------
+def _stream_handle(stream, device) -> ctypes.c_void_p:
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream(device)
+    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+class KVCache:
+    """A paged 8-bit KV cache over caller-owned tensors.
+
+    ``k`` and ``v``: int8 or float8_e4m3fn ``[num_blocks, num_kv_heads,
+    block_size, head_dim]`` with the same strides and unit stride along
+    head_dim; ``k_scale`` and ``v_scale``: float32 ``[num_blocks,
+    num_kv_heads, block_size]`` with the same strides.  A token-major cache is
+    passed as its ``permute(0, 2, 1, 3)`` / ``permute(0, 2, 1)`` view.  The
+    tensors are checked once, here; the object keeps them alive."""
+
+    def __init__(self, *, k, v, k_scale, v_scale):
+        import torch
+        formats = {torch.int8: SV_CACHE_INT8, torch.float8_e4m3fn: SV_CACHE_E4M3}
+        if k.dtype not in formats or v.dtype != k.dtype:
+            raise TypeError(f"k and v must both be int8 or float8_e4m3fn, got {k.dtype} and {v.dtype}")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError(f"k and v must have one shape [num_blocks, num_kv_heads, block_size, head_dim], got "
+                             f"{tuple(k.shape)} and {tuple(v.shape)}")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype != torch.float32:
+                raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+            if tuple(t.shape) != tuple(k.shape[:3]):
+                raise ValueError(f"{name} must have shape {tuple(k.shape[:3])}, got {tuple(t.shape)}")
+        for name, t in (("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.device != k.device:
+                raise ValueError(f"{name} is on {t.device}, expected {k.device}")
+        if k.shape[3] > 1 and k.stride(3) != 1:
+            raise ValueError("k and v must be unit-stride along head_dim")
+        # (the stride of a dimension of one element says nothing)
+        if any(n > 1 and a != b for n, a, b in zip(k.shape, k.stride(), v.stride())):
+            raise ValueError(f"k and v must have the same strides, got {k.stride()} and {v.stride()}")
+        if any(n > 1 and a != b for n, a, b in zip(k.shape, k_scale.stride(), v_scale.stride())):
+            raise ValueError(f"k_scale and v_scale must have the same strides, got {k_scale.stride()} and "
+                             f"{v_scale.stride()}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.num_blocks, self.num_kv_heads, self.block_size, self.head_dim = (int(n) for n in k.shape)
+        c = SpecVerifyKvCache()
+        c.k, c.v, c.k_scale, c.v_scale = k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
+        c.num_blocks, c.block_size = self.num_blocks, self.block_size
+        c.num_kv_heads, c.head_dim, c.format = self.num_kv_heads, self.head_dim, formats[k.dtype]
+        st = [0 if n == 1 else a for n, a in zip(k.shape, k.stride())]
+        c.block_stride, c.head_stride, c.token_stride = st[0], st[1], st[2]
+        st = [0 if n == 1 else a for n, a in zip(k.shape, k_scale.stride())]
+        c.scale_block_stride, c.scale_head_stride, c.scale_token_stride = st[0], st[1], st[2]
+        self.struct = c
+
+
+def _heads(t, name, device, shape, dtypes):
+    """A [tokens, heads, head_dim] tensor with unit stride along head_dim, any
+    other strides; returns (ptr, token_stride, head_stride)."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} dtype {t.dtype} not in {dtypes}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must be unit-stride along head_dim")
+    return t.data_ptr(), (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
+
+
+def build_kv_args(*, cache: KVCache, key, value, slot_mapping, status=None) -> SpecVerifyKvArgs:
+    """Validate tensors and fill a SpecVerifyKvArgs (no device work).  ``key``
+    and ``value``: [T, num_kv_heads, head_dim], both float32 or both bfloat16;
+    ``slot_mapping``: int64 [T]."""
+    import torch
+    device = cache.device
+    T = int(slot_mapping.numel())
+    if key.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("key must be float32 or bfloat16")
+    shape = (T, cache.num_kv_heads, cache.head_dim)
+    a = SpecVerifyKvArgs()
+    a.num_tokens, a.dtype = T, SV_BF16 if key.dtype == torch.bfloat16 else SV_F32
+    a.cache = cache.struct
+    a.key, a.key_token_stride, a.key_head_stride = _heads(key, "key", device, shape, (key.dtype,))
+    a.value, a.value_token_stride, a.value_head_stride = _heads(value, "value", device, shape, (key.dtype,))
+    a.slot_mapping = _ptr(slot_mapping, torch.int64, "slot_mapping", device, ndim=1)
+    a.status = _ptr(status, torch.int32, "status", device, numel=1)
+    return a
+
+
+def spec_verify_kv_write(handle: int, *, stream=None, **kw) -> None:
+    """Enqueue the quantisation of key and value rows into the cache.  Keyword
+    arguments are those of ``build_kv_args``."""
+    a = build_kv_args(**kw)
+    _check(load_library().spec_verify_kv_write(handle, ctypes.byref(a), _stream_handle(stream, kw["cache"].device)))
+
+
+def spec_verify_kv_read(handle: int, *, stream=None, **kw) -> None:
+    """Enqueue the reading of cache rows into key and value.  Keyword arguments
+    are those of ``build_kv_args``."""
+    a = build_kv_args(**kw)
+    for name in ("key", "value"):
+        t = kw[name]
+        if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+            raise ValueError(f"{name} is written and must not overlap itself")
+    _check(load_library().spec_verify_kv_read(handle, ctypes.byref(a), _stream_handle(stream, kw["cache"].device)))
+
+
+def spec_verify_check_kv_args(config: SpecVerifyConfig, args: SpecVerifyKvArgs) -> int:
+    """Host-only validation of cache write / read arguments; returns the sv_status code."""
+    return int(load_library().spec_verify_check_kv_args(ctypes.byref(config), ctypes.byref(args)))
+
+
+def build_attend_args(*, q, cache: KVCache, block_tables, seq_lens, max_seq_len: int, max_spec_len: int,
+                      scale: float, out, cu_num_draft_tokens=None, shared_prefix_len: int = 0, lse=None,
+                      workspace=None, status=None) -> SpecVerifyAttendArgs:
+    """Validate tensors and fill a SpecVerifyAttendArgs (no device work).
+    ``q`` and ``out``: bfloat16 [T+N, num_q_heads, head_dim];
+    ``block_tables``: int32 [N, pages]; ``seq_lens``: int32 [N]; ``lse``:
+    float32 [T+N, num_q_heads] or None; ``workspace``: a uint8 tensor of at
+    least ``spec_verify_attend_workspace_size`` bytes."""
+    import torch
+    device = cache.device
+    if block_tables.dim() != 2 or block_tables.dtype != torch.int32:
+        raise TypeError(f"block_tables must be a 2-D int32 tensor, got {tuple(block_tables.shape)} "
+                        f"{block_tables.dtype}")
+    N, width = block_tables.shape
+    if block_tables.device != device:
+        raise ValueError(f"block_tables is on {block_tables.device}, expected {device}")
+    if width > 1 and block_tables.stride(1) != 1:
+        raise ValueError("block_tables rows must be unit-stride")
+    if q.dim() != 3:
+        raise ValueError(f"q must have shape [T + N, num_q_heads, head_dim], got {tuple(q.shape)}")
+    rows, hq = int(q.shape[0]), int(q.shape[1])
+    shape = (rows, hq, cache.head_dim)
+    a = SpecVerifyAttendArgs()
+    a.num_reqs, a.max_spec_len, a.num_q_heads = N, int(max_spec_len), hq
+    a.max_seq_len, a.shared_prefix_len = int(max_seq_len), int(shared_prefix_len)
+    a.num_draft_tokens_total = rows - N
+    a.cu_num_draft_tokens = _ptr(cu_num_draft_tokens, torch.int32, "cu_num_draft_tokens", device, numel=N)
+    a.cache = cache.struct
+    a.q, a.q_token_stride, a.q_head_stride = _heads(q, "q", device, shape, (torch.bfloat16,))
+    a.block_tables = block_tables.data_ptr()
+    a.block_table_stride = block_tables.stride(0) if N > 1 else width
+    if a.block_table_stride > width:  # rows of a wider table: what lies between them is not the table's
+        a.max_seq_len = min(a.max_seq_len, width * cache.block_size)
+    a.seq_lens = _ptr(seq_lens, torch.int32, "seq_lens", device, numel=N)
+    a.scale = scale
+    a.out, a.out_token_stride, a.out_head_stride = _heads(out, "out", device, shape, (torch.bfloat16,))
+    if any(n > 1 and s == 0 for n, s in zip(out.shape, out.stride())):
+        raise ValueError("out is written and must not overlap itself")
+    a.lse = _ptr(lse, torch.float32, "lse", device, numel=rows * hq)
+    if workspace is not None:
+        a.workspace = _ptr(workspace, torch.uint8, "workspace", device)
+        a.workspace_bytes = workspace.numel()
+    a.status = _ptr(status, torch.int32, "status", device, numel=1)
+    return a
+
+
+def spec_verify_attend(handle: int, *, stream=None, **kw) -> None:
+    """Enqueue the verify tokens' attention over the cache.  Keyword arguments
+    are those of ``build_attend_args``."""
+    a = build_attend_args(**kw)
+    _check(load_library().spec_verify_attend(handle, ctypes.byref(a), _stream_handle(stream, kw["cache"].device)))
+
+
+def spec_verify_attend_workspace_size(handle: int, *, num_reqs: int, max_spec_len: int, num_q_heads: int,
+                                      num_kv_heads: int, head_dim: int, max_seq_len: int, num_tokens: int,
+                                      shared_prefix_len: int = 0) -> int:
+    """Bytes of workspace for a call of these sizes (``num_tokens`` = T + N rows of q)."""
+    a = SpecVerifyAttendArgs()
+    a.num_reqs, a.max_spec_len, a.num_q_heads = int(num_reqs), int(max_spec_len), int(num_q_heads)
+    a.max_seq_len, a.shared_prefix_len = int(max_seq_len), int(shared_prefix_len)
+    a.num_draft_tokens_total = int(num_tokens) - int(num_reqs)
+    a.cache.num_kv_heads, a.cache.head_dim = int(num_kv_heads), int(head_dim)
+    n = ctypes.c_int64()
+    _check(load_library().spec_verify_attend_workspace_size(handle, ctypes.byref(a), ctypes.byref(n)))
+    return n.value
+
+
+def spec_verify_check_attend_args(config: SpecVerifyConfig, args: SpecVerifyAttendArgs) -> int:
+    """Host-only validation of attention arguments; returns the sv_status code."""
+    return int(load_library().spec_verify_check_attend_args(ctypes.byref(config), ctypes.byref(args)))
+
+
+def build_logprobs_args(*, logits, out_tokens, logprobs, ranks=None, entropy=None, top_ids=None, top_logprobs=None,
+                        cu_num_draft_tokens=None, temperature=None, num_top: int = 0,
+                        status=None) -> SpecVerifyLogprobsArgs:
+    """Validate tensors and fill a SpecVerifyLogprobsArgs (no device work).
+    ``logits``: [T+N, V] float32 or bfloat16 rows; ``out_tokens``: int32
+    [N, G+1], as ``spec_verify_run`` leaves it."""
+    import torch
+    device = logits.device
+    if out_tokens.dim() != 2 or out_tokens.shape[1] < 1:
+        raise ValueError(f"out_tokens must have shape [N, G + 1], got {tuple(out_tokens.shape)}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must have shape [T + N, V], got {tuple(logits.shape)}")
+    N, cols = out_tokens.shape
+    rows, V = logits.shape
+    a = SpecVerifyLogprobsArgs()
+    if logits.dtype == torch.bfloat16:
+        a.dtype = SV_BF16
+    elif logits.dtype == torch.float32:
+        a.dtype = SV_F32
+    else:
+        raise TypeError("logits must be float32 or bfloat16")
+    a.num_reqs, a.max_spec_len, a.vocab_size, a.num_top = N, cols - 1, V, int(num_top)
+    a.num_draft_tokens_total = rows - N
+    a.cu_num_draft_tokens = _ptr(cu_num_draft_tokens, torch.int32, "cu_num_draft_tokens", device, numel=N)
+    a.logits, a.row_stride = _rows(logits, "logits", device, V, rows, (logits.dtype,))
+    a.temperature = _ptr(temperature, torch.float32, "temperature", device, numel=N)
+    a.out_tokens = _ptr(out_tokens, torch.int32, "out_tokens", device)
+    n = N * cols
+    a.logprobs = _ptr(logprobs, torch.float32, "logprobs", device, numel=n)
+    a.ranks = _ptr(ranks, torch.int32, "ranks", device, numel=n)
+    a.entropy = _ptr(entropy, torch.float32, "entropy", device, numel=n)
+    if num_top:
+        a.top_ids = _ptr(top_ids, torch.int32, "top_ids", device, numel=n * num_top)
+        a.top_logprobs = _ptr(top_logprobs, torch.float32, "top_logprobs", device, numel=n * num_top)
+    a.status = _ptr(status, torch.int32, "status", device, numel=1)
+    return a
+
+
+def spec_verify_logprobs(handle: int, *, stream=None, **kw) -> None:
+    """Enqueue the log-probabilities of committed tokens.  Keyword arguments
+    are those of ``build_logprobs_args``."""
+    a = build_logprobs_args(**kw)
+    _check(load_library().spec_verify_logprobs(handle, ctypes.byref(a), _stream_handle(stream, kw["logits"].device)))
+
+
+def spec_verify_check_logprobs_args(config: SpecVerifyConfig, args: SpecVerifyLogprobsArgs) -> int:
+    """Host-only validation of log-probability arguments; returns the sv_status code."""
+    return int(load_library().spec_verify_check_logprobs_args(ctypes.byref(config), ctypes.byref(args)))
+
+
 @dataclass
 class VerifyResult:
     out_tokens: "object"
     num_accepted: "object"
     status: "object"
+
+
+@dataclass
+class LogprobsResult:
+    logprobs: "object"
+    ranks: "object"
+    entropy: "object"
+    top_ids: "object"
+    top_logprobs: "object"
 
 
 class Verifier:
@@ -452,3 +764,73 @@ class Verifier:
         spec_verify_run(self.handle, stream=stream, entry=entry, draft_ids=draft_ids, target=target,
                         out_tokens=out_tokens, num_accepted=num_accepted, status=status, **kw)
         return VerifyResult(out_tokens, num_accepted, status)
+
+    def kv_write(self, *, cache: KVCache, key, value, slot_mapping, status=None, stream=None) -> None:
+        """Quantise key and value rows into the cache's slots (-1: skipped)."""
+        spec_verify_kv_write(self.handle, stream=stream, cache=cache, key=key, value=value, slot_mapping=slot_mapping,
+                             status=status)
+
+    def kv_read(self, *, cache: KVCache, slot_mapping, key_out=None, value_out=None, dtype=None, status=None,
+                stream=None):
+        """Rows of the cache's slots (-1: zeros) as (key, value) of ``dtype`` (bfloat16)."""
+        import torch
+        shape = (slot_mapping.numel(), cache.num_kv_heads, cache.head_dim)
+        if key_out is None:
+            key_out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.device)
+        if value_out is None:
+            value_out = torch.empty(shape, dtype=key_out.dtype, device=cache.device)
+        spec_verify_kv_read(self.handle, stream=stream, cache=cache, key=key_out, value=value_out,
+                            slot_mapping=slot_mapping, status=status)
+        return key_out, value_out
+
+    def attend_workspace(self, **sizes):
+        """A workspace tensor for ``attend`` calls of these sizes (the keyword
+        arguments of ``spec_verify_attend_workspace_size``), to be kept."""
+        import torch
+        n = spec_verify_attend_workspace_size(self.handle, **sizes)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=torch.device("cuda", self.device))
+
+    def attend(self, *, q, cache: KVCache, block_tables, seq_lens, max_seq_len: int, max_spec_len: int, scale: float,
+               cu_num_draft_tokens=None, shared_prefix_len: int = 0, out=None, lse=None, workspace=None, status=None,
+               stream=None):
+        """Attention of the verify tokens over the cache; returns ``out``.
+        Without ``workspace`` one is allocated for the call, on the stream that
+        is current: give one when ``stream`` is another."""
+        import torch
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if workspace is None:
+            workspace = self.attend_workspace(
+                num_reqs=block_tables.shape[0], max_spec_len=max_spec_len, num_q_heads=q.shape[1],
+                num_kv_heads=cache.num_kv_heads, head_dim=cache.head_dim, max_seq_len=max_seq_len,
+                shared_prefix_len=shared_prefix_len, num_tokens=q.shape[0])
+            if stream is not None and hasattr(stream, "cuda_stream"):
+                workspace.record_stream(stream)
+        spec_verify_attend(self.handle, stream=stream, q=q, cache=cache, block_tables=block_tables, seq_lens=seq_lens,
+                           max_seq_len=max_seq_len, max_spec_len=max_spec_len, scale=scale, out=out,
+                           cu_num_draft_tokens=cu_num_draft_tokens, shared_prefix_len=shared_prefix_len, lse=lse,
+                           workspace=workspace, status=status)
+        return out
+
+    def logprobs(self, *, logits, out_tokens, cu_num_draft_tokens=None, temperature=None, num_top: int = 0,
+                 logprobs=None, ranks=None, entropy=None, top_ids=None, top_logprobs=None, status=None,
+                 stream=None) -> LogprobsResult:
+        """Log-probabilities, ranks, entropies and the ``num_top`` best
+        alternatives of the committed tokens (``out_tokens`` of ``verify``)."""
+        import torch
+        dev, shape = logits.device, tuple(out_tokens.shape)
+        if logprobs is None:
+            logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
+        if ranks is None:
+            ranks = torch.empty(shape, dtype=torch.int32, device=dev)
+        if entropy is None:
+            entropy = torch.empty(shape, dtype=torch.float32, device=dev)
+        if top_ids is None:
+            top_ids = torch.empty(shape + (num_top,), dtype=torch.int32, device=dev)
+        if top_logprobs is None:
+            top_logprobs = torch.empty(shape + (num_top,), dtype=torch.float32, device=dev)
+        spec_verify_logprobs(self.handle, stream=stream, logits=logits, out_tokens=out_tokens, logprobs=logprobs,
+                             ranks=ranks, entropy=entropy, top_ids=top_ids, top_logprobs=top_logprobs,
+                             cu_num_draft_tokens=cu_num_draft_tokens, temperature=temperature, num_top=num_top,
+                             status=status)
+        return LogprobsResult(logprobs, ranks, entropy, top_ids, top_logprobs)

@@ -103,7 +103,11 @@ size_t spec_verify_sizeof_args(void) { return sizeof(spec_verify_args); }
 size_t spec_verify_sizeof_sample_args(void) { return sizeof(spec_verify_sample_args); }
 size_t spec_verify_sizeof_ngram_args(void) { return sizeof(spec_verify_ngram_args); }
 
-static sv_status check_config(const spec_verify_config *c) {
+static sv_status check_config(const spec_verify_config *c) { return sv::check_config(c); }
+
+}  // extern "C"
+
+sv_status sv::check_config(const spec_verify_config *c) {
   if (!c) return fail(SV_ERR_INVALID_ARG, "config is NULL");
   if (c->max_num_reqs < 1) return fail(SV_ERR_INVALID_ARG, "max_num_reqs must be >= 1");
   if (c->max_spec_len < 0 || c->max_spec_len > SV_MAX_SPEC_LEN)
@@ -119,6 +123,8 @@ static sv_status check_config(const spec_verify_config *c) {
     return fail(SV_ERR_INVALID_ARG, "max_num_reqs too large for one grid");
   return SV_OK;
 }
+
+extern "C" {
 
 sv_status spec_verify_check_args(const spec_verify_config *c, const spec_verify_args *a) {
   sv_status st = check_config(c);
@@ -204,7 +210,8 @@ sv_status spec_verify_create(const spec_verify_config *config, spec_verify_t *ou
     optin_all = optin;
     if ((e = sv::enable_stream_kernels_bf16()) != cudaSuccess || (e = sv::enable_stream_kernels_f32()) != cudaSuccess ||
         (e = sv::enable_stream_kernels_bf16_proc(optin)) != cudaSuccess ||
-        (e = sv::enable_stream_kernels_f32_proc(optin)) != cudaSuccess)
+        (e = sv::enable_stream_kernels_f32_proc(optin)) != cudaSuccess ||
+        (e = sv::enable_attend_kernels()) != cudaSuccess || (e = sv::enable_logprobs_kernels()) != cudaSuccess)
       result = fail(SV_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(e));
     if (sv::enable_probs_kernels(16) != cudaSuccess || sv::enable_logits_kernels(16, max_dyn) != cudaSuccess ||
         sv::enable_sample_kernels(16, max_dyn) != cudaSuccess) {

@@ -186,5 +186,64 @@ bool choose_logits_layout(const spec_verify_ctx *ctx, int N, int V, int elem_byt
                           bool bitmaps, bool resident, bool chained);
 
 void set_last_error(const char *fmt, ...);
+// The checks of a handle's limits; sets the last error.
+sv_status check_config(const spec_verify_config *c);
+
+// Tokens written to or read from the paged 8-bit cache (sv_cache.cu).
+struct KvParams {
+  int64_t T;
+  spec_verify_kv_cache c;
+  void *key, *value;
+  int64_t key_token, key_head, value_token, value_head;  // element strides
+  const int64_t *slots;
+  int32_t *status;
+  bool pdl;
+};
+// vec: every key / value row starts on a 16-byte boundary.
+cudaError_t launch_kv_write(const KvParams &p, bool bf16, bool vec, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvParams &p, bool bf16, bool vec, cudaStream_t stream);
+
+// The verify tokens' attention (sv_attend.cu).
+struct AttendParams {
+  int32_t N, G, Hq, group, max_seq, prefix;
+  int64_t T;
+  const int32_t *cu;
+  spec_verify_kv_cache c;
+  const uint16_t *q;
+  int64_t q_token, q_head;  // element strides
+  const int32_t *tables;
+  int64_t table_stride;
+  const int32_t *seq_lens;
+  float scale;
+  uint16_t *out;
+  int64_t out_token, out_head;
+  float *lse;
+  void *workspace;
+  int32_t *status;
+  bool pdl;
+};
+int64_t attend_workspace_bytes(const AttendParams &p, int num_sms);
+cudaError_t enable_attend_kernels();
+cudaError_t launch_attend(const AttendParams &p, int num_sms, cudaStream_t stream);
+
+// Log-probabilities of committed tokens (sv_logprobs.cu).
+struct LogprobsParams {
+  int32_t N, G, V, K;
+  int64_t T;
+  const int32_t *cu;
+  const void *logits;
+  int64_t row_stride;
+  const float *temperature;
+  const int32_t *tokens;
+  float *logprobs;
+  int32_t *ranks;
+  float *entropy;
+  int32_t *top_ids;
+  float *top_logprobs;
+  int32_t *status;
+  bool pdl;
+};
+cudaError_t enable_logprobs_kernels();
+cudaError_t launch_logprobs(const LogprobsParams &p, bool bf16, int num_sms, cudaStream_t stream);
 
 }  // namespace sv
