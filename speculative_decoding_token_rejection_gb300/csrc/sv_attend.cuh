@@ -1,0 +1,106 @@
+// sv_attend.cuh -- what the kernels of the verify tokens' attention share: the
+// division of the work, the partial results in the workspace, and how value
+// scales enter a softmax.
+//
+// Scores are kept in base 2 with the value's scale inside the exponent:
+//   t_k = (q . b_k) * (scale * log2 e * key_scale_k) + log2(value_scale_k),
+// with b_k the key's byte numbers.  With M the largest t of a row so far,
+//   w_k = 2^(t_k - M),   O = sum w_k c_k  (c_k: the value's byte numbers),
+//   l = sum w_k / value_scale_k  ( = 2^-M sum 2^(s_k) ),
+// out = O / l and lse = (M + log2 l) ln 2.  So the weights that meet the byte
+// numbers in a 16-bit product are at most 1 whatever the sizes of the value
+// rows, and a scale costs one addition and one multiplication an element.
+// Weights are rounded to f16 for that product (11 bits, steps of 2^-24 of the
+// largest): the byte numbers have 8 bits and are exact, sums are fp32, and l
+// takes the unrounded weights.
+#pragma once
+
+#include "sv_internal.h"
+#include "sv_ops.cuh"
+
+namespace sv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// How a call is cut up.  Slot s of a row holds the partial result of prefix
+// chunk s, or of private chunk s - prefix_splits.
+struct AttendPlan {
+  FastDiv page, group;
+  int32_t rows;           // (T + N) * group rows for every kv head
+  int32_t prefix_splits, prefix_chunk, prefix_tiles, prefix_items;
+  int32_t own_splits, own_chunk, own_tiles;
+  int32_t slots;          // 1: results go straight to the output
+  bool tensor_prefix;     // the prefix goes to the tensor-memory kernel
+  bool qvec;              // q rows allow 8-byte loads (16-byte ones in the tensor-memory kernel)
+  float *part_o;          // [rows * num_kv_heads][slots][D], row = token * Hq + query head
+  float2 *part_ml;        // [rows * num_kv_heads][slots]: M, l
+};
+
+// Draft range and length of request i; false (and nothing to write) for a bad
+// range.  A bad length counts as 0.
+__device__ __forceinline__ bool attend_request(const AttendParams &P, int i, int64_t &first, int &g, int &len,
+                                               uint32_t &bits) {
+  int64_t s;
+  if (!request_range(P.cu, i, P.G, P.T, s, g)) {
+    bits |= SV_DATA_BAD_CU;
+    return false;
+  }
+  first = s + i;
+  len = P.seq_lens[i];
+  if (len < 0 || len > P.max_seq) {
+    bits |= SV_DATA_BAD_PARAM;
+    len = 0;
+  }
+  return true;
+}
+
+// Prefix keys that verify token `row` sees (0 .. P.prefix), or -1 for a row
+// that belongs to no request.
+__device__ __forceinline__ int prefix_limit(const AttendParams &P, int row) {
+  int i;
+  if (!P.cu) {
+    i = row / (P.G + 1);
+  } else {  // the first request whose last row cu[i] + i is at or behind `row`
+    int lo = 0, hi = P.N - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (static_cast<int64_t>(P.cu[mid]) + mid >= row)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    i = lo;
+  }
+  int64_t first;
+  int g, len;
+  uint32_t bits = 0;
+  if (!attend_request(P, i, first, g, len, bits)) return -1;
+  const int64_t j = row - first;
+  if (j < 0 || j > g) return -1;
+  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(P.prefix), len - g + j)));
+}
+
+// log2 of a value scale and its reciprocal for the sum l.  Scale 0 stands for
+// a key that is left out.  A value scale that is not a positive number makes
+// the key's factor NaN instead: the scores of the rows that see the key become
+// NaN, and those of the others are replaced as for any key they do not see.
+__device__ __forceinline__ void value_scale_terms(float vs, float &kc, float &lv, float &inv) {
+  const bool ok = vs > 0.0f && vs < INFINITY;
+  lv = ok ? log2f(vs) : (vs == 0.0f ? -INFINITY : 0.0f);
+  inv = ok ? __frcp_rn(vs) : 1.0f;
+  if (!ok && vs != 0.0f) kc = __uint_as_float(0x7FC00000u);
+}
+
+// The power of two that brings the largest finite |q| of a tile into
+// [2^14, 2^15), where bf16 numbers are exact in f16 down to 2^-28 of it (and
+// off by 2^-40 of it at most below that).
+__device__ __forceinline__ int query_shift(uint32_t top_bits) {
+  if (top_bits == 0) return 0;
+  return min(126, 14 - (static_cast<int>(top_bits >> 23) - 127));
+}
+__device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+}  // namespace sv

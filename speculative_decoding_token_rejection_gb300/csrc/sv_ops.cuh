@@ -65,3 +65,82 @@ __device__ __forceinline__ void cache_word_to_floats(uint32_t w, float f[4]) {
 }
 
 }  // namespace sv
+
+namespace sv {
+
+// ---------------------------------------------------------------------------
+// 8-bit numbers to pairs of f16, exactly
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Bytes 0, 1 (lo) and 2, 3 (hi) of w as f16 pairs.  int8: a byte x + 128 put
+// into the low mantissa bits of 1024 is the number 1152 + x; subtracting 1152
+// is exact.
+template <int FMT>
+__device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if (FMT == SV_CACHE_INT8) {
+    w ^= 0x80808080u;
+    lo = hadd2(__byte_perm(w, 0x64646464u, 0x4140), 0xE480E480u);  // (-1152, -1152)
+    hi = hadd2(__byte_perm(w, 0x64646464u, 0x4342), 0xE480E480u);
+  } else {
+    lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w));
+    hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// asynchronous copies to shared memory; the bytes behind `n` are zeros
+// ---------------------------------------------------------------------------
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t n) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D[16x8] += A[16x16] B[16x8], f16 with fp32 sums.
+__device__ __forceinline__ void mma_16816(float d[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// n / d for n, d < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d),
+// l = ceil(log2 d), so that mul * d - 2^(31 + l) < d <= 2^l and the error of
+// n * mul / 2^(31 + l) stays below 1 / d.
+struct FastDiv {
+  uint32_t mul;
+  int32_t shift, d;
+};
+inline FastDiv fast_div(int32_t d) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;
+  const unsigned long long p = 1ull << (31 + l);
+  return FastDiv{static_cast<uint32_t>((p + d - 1) / d), 31 + l, d};
+}
+__device__ __forceinline__ int div_by(int n, const FastDiv &f) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(n)) * f.mul) >> f.shift);
+}
+
+}  // namespace sv

@@ -90,7 +90,7 @@ def attend_args():
     ("max_seq_len", 112, OK), ("max_seq_len", 113, OK), ("block_table_stride", -1, INVALID), ("block_table_stride", 1, INVALID), ("shared_prefix_len", 33, INVALID),
     ("shared_prefix_len", -16, INVALID), ("shared_prefix_len", 112, INVALID), ("shared_prefix_len", 0, OK),
     ("reserved", 1, INVALID), ("reserved2", 1, INVALID), ("q", None, INVALID), ("out", None, INVALID),
-    ("seq_lens", None, INVALID), ("block_tables", None, INVALID), ("scale", float("nan"), INVALID),
+    ("seq_lens", None, INVALID), ("block_tables", None, INVALID), ("cache.block_stride", 1 << 35, UNSUPPORTED), ("scale", float("nan"), INVALID),
     ("scale", float("inf"), INVALID), ("scale", -1.0, OK), ("q_head_stride", -1, INVALID),
     ("workspace_bytes", -1, INVALID), ("workspace", FAKE + 4, INVALID)])
 def test_check_attend_args(path, value, code):
