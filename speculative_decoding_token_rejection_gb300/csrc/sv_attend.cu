@@ -2,17 +2,24 @@
 // the warp-streaming kernel and the joining of its partial results.
 //
 // A request's rows for one kv head -- (gamma + 1) tokens times the query heads
-// of the group -- are a tile of 16 or 32 rows that all read the same keys, so
-// the private part is bound by HBM: 2 * head_dim + 8 bytes a key for 4 *
-// head_dim * rows operations.  Each warp streams keys on its own, 32 at a
-// time: lane l copies exactly the bytes that lane l will multiply into its own
-// shared-memory places (cp.async, three tiles deep), so there is no barrier
-// and no wait between warps in the loop.  That works because the order of the
-// inner dimension of a product is free: lane (g, c) of a 16x8x16 product takes
-// dimensions [c * D/4, (c + 1) * D/4) of key g, contiguous bytes, and the
-// queries are laid out once in the same order; for the second product lane
-// (g, c) takes dimensions [g * D/8, (g + 1) * D/8) of the keys whose weights it
-// computed.  Bytes become f16 in registers (exact); sums are fp32.
+// of the group -- all read the same keys, so the private part is bound by HBM:
+// 2 * head_dim + 8 bytes a key for 4 * head_dim * rows operations.  Each warp
+// streams keys on its own, 32 at a time: lane l copies exactly the bytes that
+// lane l will multiply into its own shared-memory places (cp.async, two or
+// three tiles deep), so there is no barrier and no wait between warps in the
+// loop.  That works because the order of the inner dimension of a product is
+// free: lane (g, c) of a 16x8x16 product takes 16-byte columns c, c + 4 of the
+// rows of keys g, g + 8, ..., and the queries are laid out once in the same
+// order; for the second product lane (g, c) takes dimensions [g * D/8,
+// (g + 1) * D/8) of the keys whose weights meet them.
+//
+// Both products are transposed: scores [keys x rows] = K Q^T and outputs
+// [dims x rows] = V^T P^T, so the few rows are the 8-wide side of the
+// instruction and a tile of 20 rows pays for 24, not 32; the weights turn
+// round between the products by 8x8 transposes in registers.  Bytes become
+// f16 in registers (exact); sums are fp32.  The running maximum of a row is
+// raised only when a weight would pass 2^8, so most tiles neither reduce
+// across lanes nor rescale.
 //
 // The key range of a row tile is cut over CTAs (and over a CTA's four warps)
 // when there are few row tiles; the partial results (M, l, O) of a CTA go to
@@ -28,406 +35,478 @@ namespace {
 
 constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
-constexpr int kStages = 3;
-constexpr int kKeys = 32;  // keys of a warp's tile
+constexpr int kKeys = 32;    // keys of a warp's tile
+constexpr float kRaise = 8;  // a row's maximum is raised when a weight would pass 2^kRaise
 
-template <int D>
-struct Ring {
-  static constexpr int kBytes = kKeys * 2 * D;       // keys, then values
-  static constexpr int kScales = kBytes;             // then (key scale, value scale) of key `lane`
-  static constexpr int kStage = kBytes + kKeys * 8;
+// NTM: the most 8-row groups of a row tile.  Tiles of up to 24 rows leave the
+// registers for three CTAs per SM (two copy stages), tiles of 32 rows for two
+// (three stages): either way about 100 KB of copies are in flight per SM.
+template <int D, int NTM>
+struct Layout {
+  static constexpr int kStages = NTM <= 3 ? 2 : 3;
+  static constexpr int kCtas = NTM <= 3 ? 3 : 2;
+  static constexpr int kScales = kKeys * 2 * D;  // of a stage: keys, values, then (key scale, value scale) of key `lane`
+  static constexpr int kStage = kScales + kKeys * 8;
+  static constexpr int kQuery = NTM * 8 * D * 2;
+  static constexpr int kPitch = D + 4;  // floats of an output row while the warps' results are joined
+  static constexpr int kRing = kAttendWarps * kStages * kStage;
+  static constexpr int kJoin = kAttendWarps * NTM * 8 * kPitch * 4;
+  static constexpr int kBytes = kQuery + (kRing > kJoin ? kRing : kJoin);
 };
-template <int D, int MT>
-constexpr size_t attend_smem() {
-  return static_cast<size_t>(MT) * (D / 16) * 512 + static_cast<size_t>(kAttendWarps) * kStages * Ring<D>::kStage;
-}
 
-template <int D, int FMT, int MT>
-__global__ void __launch_bounds__(kAttendThreads, 2) attend_kernel(const AttendParams P, const AttendPlan L) {
-  pdl_enter();
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int row_token[MT * 16], row_limit[MT * 16];
-  __shared__ uint32_t warp_top[kAttendWarps];
-  __shared__ float row_m[kAttendWarps][MT * 16], row_l[kAttendWarps][MT * 16];
-  constexpr int R = MT * 16;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int H = P.c.num_kv_heads;
-
-  // ---- which rows and keys ----
+struct RowTile {
   int h, k_begin, k_end, slot, r0, rows;
-  int64_t first = 0;
-  const int32_t *table = P.tables;
-  uint32_t bits = 0;
-  int len = 0, gam = 0;
-  const bool shared_part = static_cast<int>(blockIdx.x) < L.prefix_items;
-  if (shared_part) {
-    int b = blockIdx.x;
-    const int tile = b % L.prefix_tiles;
-    b /= L.prefix_tiles;
-    h = b % H;
-    slot = b / H;
-    r0 = tile * R;
-    rows = min(R, L.rows - r0);
-    k_begin = slot * L.prefix_chunk;
-    k_end = min(P.prefix, k_begin + L.prefix_chunk);
-  } else {
-    int b = blockIdx.x - L.prefix_items;
-    const int tile = b % L.own_tiles;
-    b /= L.own_tiles;
-    h = b % H;
-    b /= H;
-    const int split = b % L.own_splits;
-    const int i = b / L.own_splits;
-    const bool ok = attend_request(P, i, first, gam, len, bits);
-    if (bits && tile == 0 && h == 0 && split == 0 && tid == 0 && P.status) atomicOr(P.status, static_cast<int>(bits));
-    bits = 0;
-    if (!ok) return;
-    r0 = tile * R;
-    rows = min(R, (gam + 1) * P.group - r0);
-    if (rows <= 0) return;
-    slot = L.prefix_splits + split;
-    k_begin = P.prefix + split * L.own_chunk;
-    k_end = min(len, k_begin + L.own_chunk);
-    if (k_end <= k_begin && L.slots > 1) return;  // (the joining kernel knows)
-    table += i * P.table_stride;
-  }
-  if (tid < R) {
-    int token = -1, limit = 0x7FFFFFFF;
-    if (tid < rows) {
-      const int t = div_by(r0 + tid, L.group);
-      if (shared_part) {
-        token = t;
-        limit = prefix_limit(P, t);
-        if (limit < 0) {  // nobody's row
-          token = -1;
-          limit = 0x7FFFFFFF;
-        }
-      } else {
-        token = static_cast<int>(first) + t;
-        limit = len - gam + t;
-      }
-    }
-    row_token[tid] = token;
-    row_limit[tid] = limit;
-  }
-  __syncthreads();
+  const int32_t *table;
+  int *token;  // [rows] in shared memory: verify token of a row, or -1
+  int *limit;  // keys that the row sees are below it
+};
 
-  // ---- the queries as operand fragments ----
-  constexpr int kFrags = MT * (D / 16) * 32 / kAttendThreads;  // of a thread
+struct JoinSmem {
+  float m[kAttendWarps][32], l[kAttendWarps][32];
+  uint32_t top[kAttendWarps];
+};
+
+template <int D, int FMT, int NTM, int NT>
+__device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendPlan &L, const RowTile &T, uint8_t *smem,
+                                            JoinSmem &J) {
+  using Y = Layout<D, NTM>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+
+  // ---- the queries as operand fragments: 8 consecutive dimensions for each lane and pair of steps ----
+  constexpr int kFrags = (NT * (D / 32) * 32 + kAttendThreads - 1) / kAttendThreads;  // of a thread
   uint4 *const qfrag = reinterpret_cast<uint4 *>(smem);
   float c_tile;
   {
-    float x[kFrags][8];  // dimensions 0..3 of row g, then of row g + 8
+    uint4 x[kFrags];
     uint32_t top = 0;
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
-      const int at = f * kAttendThreads + tid, ln = at & 31, kk = (at >> 5) % (D / 16), mt = (at >> 5) / (D / 16);
-      const int dim = (ln & 3) * (D / 4) + 4 * kk;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = mt * 16 + half * 8 + (ln >> 2);
-        const int token = row_token[r];
-        uint32_t w[2] = {0, 0};
-        if (token >= 0) {
-          const int lr = r0 + r, hq = h * P.group + lr - div_by(lr, L.group) * P.group;
-          const uint16_t *src = P.q + token * P.q_token + hq * P.q_head + dim;
-          if (L.qvec) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(src);
-            w[0] = v.x;
-            w[1] = v.y;
-          } else {
-            w[0] = src[0] | static_cast<uint32_t>(src[1]) << 16;
-            w[1] = src[2] | static_cast<uint32_t>(src[3]) << 16;
-          }
+      const int at = f * kAttendThreads + tid, ln = at & 31, s2 = (at >> 5) % (D / 32), nt = (at >> 5) / (D / 32);
+      const int r = nt * 8 + (ln >> 2);
+      // steps 4q .. 4q + 3 are column q * 4 + c of 16 dimensions; s2 counts pairs of steps
+      const int dim = ((s2 >> 1) * 4 + (ln & 3)) * 16 + (s2 & 1) * 8;
+      x[f] = make_uint4(0, 0, 0, 0);
+      if (nt < NT && r < T.rows && T.token[r] >= 0) {
+        const int lr = T.r0 + r, hq = T.h * P.group + lr - div_by(lr, L.group) * P.group;
+        const uint16_t *src = P.q + T.token[r] * P.q_token + hq * P.q_head + dim;
+        if (L.qvec) {
+          x[f] = *reinterpret_cast<const uint4 *>(src);
+        } else {
+          x[f].x = src[0] | static_cast<uint32_t>(src[1]) << 16;
+          x[f].y = src[2] | static_cast<uint32_t>(src[3]) << 16;
+          x[f].z = src[4] | static_cast<uint32_t>(src[5]) << 16;
+          x[f].w = src[6] | static_cast<uint32_t>(src[7]) << 16;
         }
+      }
+      const uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = bf16_bits_to_float((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-          x[f][half * 4 + e] = v;
-          const uint32_t a = __float_as_uint(v) & 0x7FFFFFFFu;
-          if (a < 0x7F800000u) top = max(top, a);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a = w[e] << 16 & 0x7FFFFFFFu, b = w[e] & 0x7FFF0000u;
+        if (a < 0x7F800000u) top = max(top, a);
+        if (b < 0x7F800000u) top = max(top, b);
       }
     }
     top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (lane == 0) warp_top[warp] = top;
+    if (lane == 0) J.top[warp] = top;
     __syncthreads();
-    top = max(max(warp_top[0], warp_top[1]), max(warp_top[2], warp_top[3]));
+    top = max(max(J.top[0], J.top[1]), max(J.top[2], J.top[3]));
     const int shift = query_shift(top);
     const float up = pow2(shift);
     c_tile = P.scale * kLog2e * pow2(-shift);
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
-      const float *v = x[f];
-      qfrag[f * kAttendThreads + tid] = make_uint4(pack_f16(v[0] * up, v[1] * up), pack_f16(v[4] * up, v[5] * up),
-                                                   pack_f16(v[2] * up, v[3] * up), pack_f16(v[6] * up, v[7] * up));
+      uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack_f16(bf16_bits_to_float(w[e] & 0xFFFFu) * up, bf16_bits_to_float(w[e] >> 16) * up);
+      if (f * kAttendThreads + tid < NT * (D / 32) * 32)
+        qfrag[f * kAttendThreads + tid] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  int limit[MT][2], low = 0x7FFFFFFF;  // low: keys below it are seen by every row of the tile
+  int limit[NT][2], low = 0x7FFFFFFF;  // of rows nt * 8 + 2c, + 1; low: keys below it are seen by every row of the tile
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      limit[mt][half] = row_limit[mt * 16 + half * 8 + g];
-      low = min(low, limit[mt][half]);
+    for (int e = 0; e < 2; ++e) {
+      const int r = nt * 8 + 2 * c + e;
+      limit[nt][e] = r < T.rows ? T.limit[r] : 0x7FFFFFFF;
+      low = min(low, limit[nt][e]);
     }
   low = __reduce_min_sync(0xFFFFFFFFu, low);
   __syncthreads();
 
   // ---- the stream of keys ----
-  const uint32_t ring = smem_addr(smem) + MT * (D / 16) * 512 + warp * kStages * Ring<D>::kStage;
-  const uint8_t *const ring_ptr = smem + MT * (D / 16) * 512 + warp * kStages * Ring<D>::kStage;
-  const int tiles_all = (max(0, k_end - k_begin) + kKeys - 1) / kKeys;
+  uint8_t *const ring_ptr = smem + Y::kQuery + warp * Y::kStages * Y::kStage;
+  const uint32_t ring = smem_addr(ring_ptr);
+  const int tiles_all = (max(0, T.k_end - T.k_begin) + kKeys - 1) / kKeys;
   const int ntiles = (tiles_all - warp + kAttendWarps - 1) / kAttendWarps;  // tiles warp, warp + 4, ...
+  const uint8_t *const kcol = static_cast<const uint8_t *>(P.c.k) + T.h * P.c.head_stride + c * 16;
+  const uint8_t *const vcol = static_cast<const uint8_t *>(P.c.v) + T.h * P.c.head_stride + g * (D / 8);
+  const float *const kscale = P.c.k_scale + T.h * P.c.scale_head_stride;
+  const float *const vscale = P.c.v_scale + T.h * P.c.scale_head_stride;
+  uint32_t bits = 0;
   auto page_of = [&](int it) {  // of the lane's key of the warp's tile `it`
-    const int k = k_begin + (it * kAttendWarps + warp) * kKeys + lane;
-    return it < ntiles && k < k_end ? table[div_by(k, L.page)] : -1;
+    const int k = T.k_begin + (it * kAttendWarps + warp) * kKeys + lane;
+    return it < ntiles && k < T.k_end ? T.table[div_by(k, L.page)] : -1;
   };
-  auto issue = [&](int it, int page) {
+  auto issue = [&](int it, int stage, int page) {
     if (it < ntiles) {
-      const int k = k_begin + (it * kAttendWarps + warp) * kKeys + lane;
-      const bool in = k < k_end, live = in && page >= 0 && page < P.c.num_blocks;
+      const int k = T.k_begin + (it * kAttendWarps + warp) * kKeys + lane;
+      const bool in = k < T.k_end, live = in && page >= 0 && page < P.c.num_blocks;
       if (in && !live) bits = SV_DATA_BAD_SLOT;
-      int64_t at = 0, sat = 0;
+      uint32_t unit = 0;  // the row's place in units of 16 bytes (rows are 16-byte aligned, a side below 2^36 bytes)
+      int64_t sat = 0;
       if (live) {
         const int off = k - div_by(k, L.page) * P.c.block_size;
-        at = page * P.c.block_stride + h * P.c.head_stride + off * P.c.token_stride;
-        sat = page * P.c.scale_block_stride + h * P.c.scale_head_stride + off * P.c.scale_token_stride;
+        unit = static_cast<uint32_t>((page * P.c.block_stride + off * P.c.token_stride) >> 4);
+        sat = page * P.c.scale_block_stride + off * P.c.scale_token_stride;
       }
-      const uint32_t dst = ring + (it % kStages) * Ring<D>::kStage;
-      copy_async<4>(dst + Ring<D>::kScales + lane * 8, P.c.k_scale + sat, live ? 4 : 0);
-      copy_async<4>(dst + Ring<D>::kScales + lane * 8 + 4, P.c.v_scale + sat, live ? 4 : 0);
-      const uint32_t unit = live ? static_cast<uint32_t>(at >> 4) : 0xFFFFFFFFu;  // (rows are 16-byte aligned)
+      const uint32_t dead = __ballot_sync(0xFFFFFFFFu, !live);
+      const uint32_t dst = ring + stage * Y::kStage, mine = dst + lane * 16;
+      copy_async<4>(dst + Y::kScales + lane * 8, kscale + sat, live ? 4 : 0);
+      copy_async<4>(dst + Y::kScales + lane * 8 + 4, vscale + sat, live ? 4 : 0);
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, nt * 8 + g);
-        const uint8_t *src = static_cast<const uint8_t *>(P.c.k) + (u == 0xFFFFFFFFu ? 0 : static_cast<int64_t>(u) * 16 + c * (D / 4));
+      for (int x = 0; x < 4; ++x) {  // keys g, g + 8, g + 16, g + 24
+        const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, x * 8 + g);
+        const uint32_t n = dead >> (x * 8 + g) & 1u ? 0u : 16u;
+        const uint8_t *src = kcol + static_cast<uint64_t>(u) * 16;
 #pragma unroll
-        for (int q = 0; q < D / 64; ++q)
-          copy_async<16>(dst + (nt * (D / 64) + q) * 512 + lane * 16, src + (u == 0xFFFFFFFFu ? 0 : q * 16), u == 0xFFFFFFFFu ? 0 : 16);
+        for (int q = 0; q < D / 64; ++q) copy_async<16>(mine + (x * (D / 64) + q) * 512, src + q * 64, n);
       }
 #pragma unroll
       for (int x = 0; x < 8; ++x) {  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of each half of the tile
-        const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, (x >> 2) * 16 + ((x >> 1) & 1) * 8 + 2 * c + (x & 1));
-        const uint8_t *src = static_cast<const uint8_t *>(P.c.v) + (u == 0xFFFFFFFFu ? 0 : static_cast<int64_t>(u) * 16 + g * (D / 8));
-        copy_async<D / 8>(dst + kKeys * D + x * (32 * D / 8) + lane * (D / 8), src, u == 0xFFFFFFFFu ? 0 : D / 8);
+        const int key = (x >> 2) * 16 + ((x >> 1) & 1) * 8 + 2 * c + (x & 1);
+        const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, key);
+        copy_async<D / 8>(dst + kKeys * D + x * (4 * D) + lane * (D / 8), vcol + static_cast<uint64_t>(u) * 16,
+                          dead >> key & 1u ? 0u : D / 8);
       }
     }
     copy_commit();
   };
 
-  float o[MT][D / 8][4], m[MT][2], l[MT][2];
+  float o[D / 16][NT][4];  // rows nt * 8 + 2c, + 1: dimension g * D/8 + 2t, then dimension g * D/8 + 2t + 1
+  Pair l[NT], neg[NT];     // sums over the lane's keys, and the negated maxima
+  uint32_t set = 0;        // bit nt * 2 + e: the row has a maximum (without one, weights are taken against 0)
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    m[mt][0] = m[mt][1] = -INFINITY;
-    l[mt][0] = l[mt][1] = 0.0f;
+  for (int nt = 0; nt < NT; ++nt) {
+    l[nt] = neg[nt] = pair(0.0f, 0.0f);
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.0f;
+    for (int t = 0; t < D / 16; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.0f;
   }
   int page = page_of(0);
 #pragma unroll
-  for (int it = 0; it < kStages - 1; ++it) {
-    issue(it, page);
+  for (int it = 0; it < Y::kStages - 1; ++it) {
+    issue(it, it, page);
     page = page_of(it + 1);
   }
+  int stage = 0, fill = Y::kStages - 1;
   for (int it = 0; it < ntiles; ++it) {
-    copy_wait<kStages - 2>();
-    const uint8_t *const src = ring_ptr + (it % kStages) * Ring<D>::kStage;
-    const float2 sc = *reinterpret_cast<const float2 *>(src + Ring<D>::kScales + lane * 8);
+    issue(it + Y::kStages - 1, fill, page);  // (into the stage whose numbers the last step has used up)
+    page = page_of(it + Y::kStages);
+    if (++fill == Y::kStages) fill = 0;
+    copy_wait<Y::kStages - 1>();
+    const uint8_t *const src = ring_ptr + stage * Y::kStage;
+    if (++stage == Y::kStages) stage = 0;
+    const float2 sc = *reinterpret_cast<const float2 *>(src + Y::kScales + lane * 8);
     float kc = sc.x * c_tile, lv, inv;
     value_scale_terms(sc.y, kc, lv, inv);
-    // scores
-    float s[MT][4][4];
+    // scores: keys g, g + 8 of each half mt of the tile, rows 2c, 2c + 1 of each group
+    float s[2][NT][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.0f;
+      for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.0f;
 #pragma unroll
     for (int q = 0; q < D / 64; ++q) {
       uint4 kb[4];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) kb[nt] = *reinterpret_cast<const uint4 *>(src + (nt * (D / 64) + q) * 512 + lane * 16);
+      for (int x = 0; x < 4; ++x) kb[x] = *reinterpret_cast<const uint4 *>(src + (x * (D / 64) + q) * 512 + lane * 16);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint4 a[MT];
+      for (int s2 = 0; s2 < 2; ++s2) {
+        uint4 b[NT];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) a[mt] = qfrag[(mt * (D / 16) + q * 4 + x) * 32 + lane];
+        for (int nt = 0; nt < NT; ++nt) b[nt] = qfrag[(nt * (D / 32) + q * 2 + s2) * 32 + lane];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          const uint32_t w = x == 0 ? kb[nt].x : x == 1 ? kb[nt].y : x == 2 ? kb[nt].z : kb[nt].w;
-          uint32_t b0, b1;
-          bytes_to_f16<FMT>(w, b0, b1);
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma_16816(s[mt][nt], a[mt], b0, b1);
-        }
+          for (int mt = 0; mt < 2; ++mt) {
+            const uint4 &w0 = kb[mt * 2], &w1 = kb[mt * 2 + 1];
+            const uint32_t x0 = s2 ? (e ? w0.w : w0.z) : (e ? w0.y : w0.x);
+            const uint32_t x1 = s2 ? (e ? w1.w : w1.z) : (e ? w1.y : w1.x);
+            uint4 a;
+            bytes_to_f16<FMT>(x0, a.x, a.z);
+            bytes_to_f16<FMT>(x1, a.y, a.w);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816(s[mt][nt], a, e ? b[nt].z : b[nt].x, e ? b[nt].w : b[nt].y);
+          }
       }
     }
     // weights
-    float vw[4][2], iv[4][2];  // of the lane's keys: log2 and reciprocal of the value scale
-    const int k0 = k_begin + (it * kAttendWarps + warp) * kKeys;
-    const bool cut = k0 + kKeys > low;
-    {
-      float top[MT][2];
+    Pair kw[4], vw[4], iw[4];  // of keys g, g + 8, g + 16, g + 24
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) top[mt][0] = top[mt][1] = -INFINITY;
+    for (int x = 0; x < 4; ++x) {
+      const float a = __shfl_sync(0xFFFFFFFFu, kc, x * 8 + g), b = __shfl_sync(0xFFFFFFFFu, lv, x * 8 + g),
+                  d = __shfl_sync(0xFFFFFFFFu, inv, x * 8 + g);
+      kw[x] = pair(a, a);
+      vw[x] = pair(b, b);
+      iw[x] = pair(d, d);
+    }
+    // x: scores without the value's scale.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
+    Pair x[4][NT], y[4][NT];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        x[k][nt] = mul2(pair(s[k >> 1][nt][(k & 1) * 2], s[k >> 1][nt][(k & 1) * 2 + 1]), kw[k]);
+    const int k0 = T.k_begin + (it * kAttendWarps + warp) * kKeys;
+    if (k0 + kKeys > low) {  // some row does not see all of the tile
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int key = k0 + k * 8 + g;
+          x[k][nt] = pair(key < limit[nt][0] ? lo(x[k][nt]) : -INFINITY, key < limit[nt][1] ? hi(x[k][nt]) : -INFINITY);
+        }
+    }
+    // y: less the maximum, and only then the value scale's log (a score too large to hold it would lose it)
+    float most[NT][2];
+    auto weigh = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        most[nt][0] = most[nt][1] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          y[k][nt] = add2(add2(x[k][nt], neg[nt]), vw[k]);
+          most[nt][0] = fmaxf(most[nt][0], lo(y[k][nt]));
+          most[nt][1] = fmaxf(most[nt][1], hi(y[k][nt]));
+        }
+      }
+    };
+    weigh();
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) raise |= most[nt][e] > (set >> (nt * 2 + e) & 1u ? kRaise : -INFINITY);
+    if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float r[2], up[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const Pair t = add2(x[k][nt], vw[k]);
+          up[0] = fmaxf(up[0], lo(t));
+          up[1] = fmaxf(up[1], hi(t));
+        }
+        float next[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int key = nt * 8 + 2 * c + e;
-          const float kce = __shfl_sync(0xFFFFFFFFu, kc, key);
-          vw[nt][e] = __shfl_sync(0xFFFFFFFFu, lv, key);
-          iv[nt][e] = __shfl_sync(0xFFFFFFFFu, inv, key);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              // (a product of its own, rounded: subtracting a maximum that equals it gives 0)
-              float x = __fmul_rn(s[mt][nt][half * 2 + e], kce);
-              if (cut && k0 + key >= limit[mt][half]) x = -INFINITY;
-              s[mt][nt][half * 2 + e] = x;
-              top[mt][half] = fmaxf(top[mt][half], x + vw[nt][e]);
-            }
-        }
-      bool grew = false;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float t = top[mt][half];
-          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
-          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
-          top[mt][half] = fmaxf(t, m[mt][half]);
-          grew |= top[mt][half] != m[mt][half];
-        }
-      if (__any_sync(0xFFFFFFFFu, grew)) {  // (seldom after the first tiles)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float r = m[mt][half] == -INFINITY ? 0.0f : exp2_approx(m[mt][half] - top[mt][half]);
-            m[mt][half] = top[mt][half];
-            l[mt][half] *= r;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              o[mt][n][half * 2] *= r;
-              o[mt][n][half * 2 + 1] *= r;
-            }
+          for (int b = 4; b <= 16; b <<= 1) up[e] = fmaxf(up[e], __shfl_xor_sync(0xFFFFFFFFu, up[e], b));
+          const bool had = set >> (nt * 2 + e) & 1u;
+          const float old = -(e ? hi(neg[nt]) : lo(neg[nt]));
+          next[e] = had ? fmaxf(old, up[e]) : up[e];
+          r[e] = had ? exp2_approx(old - next[e]) : 1.0f;  // (nothing was added up without a maximum but NaN or zeros)
+          if (next[e] == -INFINITY) {
+            next[e] = old;
+            r[e] = 1.0f;
+          } else {
+            set |= 1u << (nt * 2 + e);
           }
+        }
+        neg[nt] = pair(-next[0], -next[1]);
+        const Pair rr = pair(r[0], r[1]);
+        l[nt] = mul2(l[nt], rr);
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+          const Pair a = mul2(pair(o[t][nt][0], o[t][nt][1]), rr), b = mul2(pair(o[t][nt][2], o[t][nt][3]), rr);
+          o[t][nt][0] = lo(a);
+          o[t][nt][1] = hi(a);
+          o[t][nt][2] = lo(b);
+          o[t][nt][3] = hi(b);
+        }
       }
+      weigh();
     }
+    uint32_t p[2][NT][2];  // weights of a half's keys 2c, 2c + 1 (then + 8) for row g
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float base = m[mt][half] == -INFINITY ? 0.0f : m[mt][half];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // (the score less the maximum first: a score too large to hold the value scale's log keeps it here)
-            float w = exp2_approx((s[mt][nt][half * 2 + e] - base) + vw[nt][e]);
-            s[mt][nt][half * 2 + e] = w;
-            l[mt][half] = fmaf(w, iv[nt][e], l[mt][half]);
-          }
+      for (int nt = 0; nt < NT; ++nt) {
+        const float a = exp2_approx(lo(y[k][nt])), b = exp2_approx(hi(y[k][nt]));
+        l[nt] = fma2(pair(a, b), iw[k], l[nt]);
+        p[k >> 1][nt][k & 1] = transpose_8x8(pack_f16(a, b));
       }
     // values
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint4 a[MT];
+    for (int j = 0; j < 2; ++j) {
+      const uint8_t *vs = src + kKeys * D + j * 4 * (4 * D) + lane * (D / 8);
+      uint32_t v[4][D / 32];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const float *x = s[mt][half * 2], *y = s[mt][half * 2 + 1];
-        a[mt] = make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(y[0], y[1]), pack_f16(y[2], y[3]));
-      }
-      const uint8_t *vs = src + kKeys * D + half * 4 * (32 * D / 8) + lane * (D / 8);
-#pragma unroll
-      for (int q = 0; q < D / 64; ++q) {  // eight dimensions of the four keys at a time
-        uint2 v[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] = *reinterpret_cast<const uint2 *>(vs + x * (32 * D / 8) + q * 8);
-#pragma unroll
-        for (int wd = 0; wd < 2; ++wd) {
-          const uint32_t v0 = wd ? v[0].y : v[0].x, v1 = wd ? v[1].y : v[1].x, v2 = wd ? v[2].y : v[2].x,
-                         v3 = wd ? v[3].y : v[3].x;
-          uint32_t b0[4], b1[4];  // (key pair, dimension)
-          bytes_to_f16<FMT>(__byte_perm(v0, v1, 0x5140), b0[0], b0[1]);
-          bytes_to_f16<FMT>(__byte_perm(v0, v1, 0x7362), b0[2], b0[3]);
-          bytes_to_f16<FMT>(__byte_perm(v2, v3, 0x5140), b1[0], b1[1]);
-          bytes_to_f16<FMT>(__byte_perm(v2, v3, 0x7362), b1[2], b1[3]);
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma_16816(o[mt][q * 8 + wd * 4 + d], a[mt], b0[d], b1[d]);
+      for (int k = 0; k < 4; ++k) {
+        if (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(vs + k * (4 * D));
+          v[k][0] = w.x;
+          v[k][1] = w.y;
+          v[k][D / 32 - 2] = w.z;
+          v[k][D / 32 - 1] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2 *>(vs + k * (4 * D));
+          v[k][0] = w.x;
+          v[k][1] = w.y;
         }
       }
+#pragma unroll
+      for (int wd = 0; wd < D / 32; ++wd)
+#pragma unroll
+        for (int t2 = 0; t2 < 2; ++t2) {
+          uint4 a;
+          bytes_to_f16<FMT>(__byte_perm(v[0][wd], v[1][wd], t2 ? 0x7362 : 0x5140), a.x, a.y);
+          bytes_to_f16<FMT>(__byte_perm(v[2][wd], v[3][wd], t2 ? 0x7362 : 0x5140), a.z, a.w);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_16816(o[wd * 2 + t2][nt], a, p[j][nt][0], p[j][nt][1]);
+        }
     }
-    issue(it + kStages - 1, page);
-    page = page_of(it + kStages);
   }
   copy_wait<0>();
   if (bits && P.status) atomicOr(P.status, static_cast<int>(bits));
 
   // ---- the four warps' results joined ----
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float x = l[mt][half];
-      x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-      x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-      if (c == 0) {
-        row_m[warp][mt * 16 + half * 8 + g] = m[mt][half];
-        row_l[warp][mt * 16 + half * 8 + g] = x;
+    for (int e = 0; e < 2; ++e) {
+      float sum = e ? hi(l[nt]) : lo(l[nt]);
+#pragma unroll
+      for (int b = 4; b <= 16; b <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, b);
+      if (g == 0) {
+        J.m[warp][nt * 8 + 2 * c + e] = set >> (nt * 2 + e) & 1u ? -(e ? hi(neg[nt]) : lo(neg[nt])) : -INFINITY;
+        J.l[warp][nt * 8 + 2 * c + e] = sum;
       }
     }
   __syncthreads();  // (every warp is done with its ring as well)
-  float *const acc = reinterpret_cast<float *>(smem);  // [warp][row][D]
+  float *const acc = reinterpret_cast<float *>(smem + Y::kQuery);  // [warp][row][kPitch]
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = mt * 16 + half * 8 + g;
-      const float top = fmaxf(fmaxf(row_m[0][r], row_m[1][r]), fmaxf(row_m[2][r], row_m[3][r]));
-      const float f = m[mt][half] == -INFINITY ? (isnan(row_l[warp][r]) ? 1.0f : 0.0f) : exp2_approx(m[mt][half] - top);
-      // column n of a product's tile t is dimension n * D/8 + t
+    for (int e = 0; e < 2; ++e) {
+      const int r = nt * 8 + 2 * c + e;
+      float *dst = acc + (warp * NT * 8 + r) * Y::kPitch + g * (D / 8);
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int n = 0; n < D / 8; n += 4)
-          *reinterpret_cast<float4 *>(acc + (warp * R + r) * D + (2 * c + e) * (D / 8) + n) =
-              make_float4(o[mt][n][half * 2 + e] * f, o[mt][n + 1][half * 2 + e] * f, o[mt][n + 2][half * 2 + e] * f,
-                          o[mt][n + 3][half * 2 + e] * f);
+      for (int t = 0; t < D / 16; t += 2)
+        *reinterpret_cast<float4 *>(dst + 2 * t) =
+            make_float4(o[t][nt][e], o[t][nt][2 + e], o[t + 1][nt][e], o[t + 1][nt][2 + e]);
     }
   __syncthreads();
-  for (int r = warp; r < rows; r += kAttendWarps) {
-    const int token = row_token[r];
+  for (int r = warp; r < T.rows; r += kAttendWarps) {
+    const int token = T.token[r];
     if (token < 0) continue;
-    const int lr = r0 + r, hq = h * P.group + lr - div_by(lr, L.group) * P.group;
-    const float top = fmaxf(fmaxf(row_m[0][r], row_m[1][r]), fmaxf(row_m[2][r], row_m[3][r]));
+    const int lr = T.r0 + r, hq = T.h * P.group + lr - div_by(lr, L.group) * P.group;
+    const float top = fmaxf(fmaxf(J.m[0][r], J.m[1][r]), fmaxf(J.m[2][r], J.m[3][r]));
     float sum = 0.0f, x[D / 32];
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) x[d] = 0.0f;
 #pragma unroll
     for (int w = 0; w < kAttendWarps; ++w) {
-      sum += row_m[w][r] == -INFINITY ? (isnan(row_l[w][r]) ? row_l[w][r] : 0.0f) : row_l[w][r] * exp2_approx(row_m[w][r] - top);
+      // (a warp whose keys the row does not see adds zeros; one with NaN scores alone has no maximum, and adds them)
+      const float f = J.m[w][r] == -INFINITY ? 1.0f : exp2_approx(J.m[w][r] - top);
+      sum = fmaf(J.l[w][r], f, sum);
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) x[d] += acc[(w * R + r) * D + d * 32 + lane];
+      for (int d = 0; d < D / 32; ++d) x[d] = fmaf(acc[(w * NT * 8 + r) * Y::kPitch + d * 32 + lane], f, x[d]);
     }
     const int64_t row = static_cast<int64_t>(token) * P.Hq + hq;
     if (L.slots > 1) {
-      float *dst = L.part_o + (row * L.slots + slot) * D;
+      float *dst = L.part_o + (row * L.slots + T.slot) * D;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) dst[d * 32 + lane] = x[d];
-      if (lane == 0) L.part_ml[row * L.slots + slot] = make_float2(top, sum);
+      if (lane == 0) L.part_ml[row * L.slots + T.slot] = make_float2(top, sum);
     } else {
       uint16_t *dst = P.out + token * P.out_token + hq * P.out_head;
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float r1 = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) dst[d * 32 + lane] = static_cast<uint16_t>(pack_bf16(sum == 0.0f ? 0.0f : x[d] * inv, 0.0f));
+      for (int d = 0; d < D / 32; ++d)
+        dst[d * 32 + lane] = static_cast<uint16_t>(pack_bf16(sum == 0.0f ? 0.0f : x[d] * r1, 0.0f));
       if (P.lse && lane == 0) P.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
   }
+}
+
+template <int D, int FMT, int NTM>
+__global__ void __launch_bounds__(kAttendThreads, Layout<D, NTM>::kCtas) attend_kernel(const AttendParams P, const AttendPlan L) {
+  pdl_enter();
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ JoinSmem join;
+  __shared__ int row_token[NTM * 8], row_limit[NTM * 8];
+  const int tid = threadIdx.x, H = P.c.num_kv_heads;
+  RowTile T;
+  T.table = P.tables;
+  T.token = row_token;
+  T.limit = row_limit;
+  int64_t first = 0;
+  int len = 0, gam = 0;
+  const bool shared_part = static_cast<int>(blockIdx.x) < L.prefix_items;
+  if (shared_part) {
+    int b = blockIdx.x;
+    const int tile = b % L.prefix_tiles;
+    b /= L.prefix_tiles;
+    T.h = b % H;
+    T.slot = b / H;
+    T.r0 = tile * NTM * 8;
+    T.rows = min(NTM * 8, L.rows - T.r0);
+    T.k_begin = T.slot * L.prefix_chunk;
+    T.k_end = min(P.prefix, T.k_begin + L.prefix_chunk);
+  } else {
+    int b = blockIdx.x - L.prefix_items;
+    const int tile = b % L.own_tiles;
+    b /= L.own_tiles;
+    T.h = b % H;
+    b /= H;
+    const int split = b % L.own_splits;
+    const int i = b / L.own_splits;
+    uint32_t bits = 0;
+    const bool ok = attend_request(P, i, first, gam, len, bits);
+    if (bits && tile == 0 && T.h == 0 && split == 0 && tid == 0 && P.status) atomicOr(P.status, static_cast<int>(bits));
+    if (!ok) return;
+    // the request's row groups, dealt evenly to as few tiles as hold them
+    const int all = (gam + 1) * P.group, groups = (all + 7) / 8, tiles = (groups + NTM - 1) / NTM;
+    if (tile >= tiles) return;
+    const int per = (groups + tiles - 1) / tiles * 8;
+    T.r0 = tile * per;
+    T.rows = min(per, all - T.r0);
+    if (T.rows <= 0) return;
+    T.slot = L.prefix_splits + split;
+    T.k_begin = P.prefix + split * L.own_chunk;
+    T.k_end = min(len, T.k_begin + L.own_chunk);
+    if (T.k_end <= T.k_begin && L.slots > 1) return;  // (the joining kernel knows)
+    T.table += i * P.table_stride;
+  }
+  if (tid < T.rows) {
+    const int t = div_by(T.r0 + tid, L.group);
+    int token = t, limit;
+    if (shared_part) {
+      limit = prefix_limit(P, t);
+      if (limit < 0) {  // nobody's row
+        token = -1;
+        limit = 0x7FFFFFFF;
+      }
+    } else {
+      token = static_cast<int>(first) + t;
+      limit = len - gam + t;
+    }
+    row_token[tid] = token;
+    row_limit[tid] = limit;
+  }
+  __syncthreads();
+  const int groups = (T.rows + 7) / 8;
+  if (groups == 1)
+    attend_tile<D, FMT, NTM, 1>(P, L, T, smem, join);
+  else if (groups == 2)
+    attend_tile<D, FMT, NTM, 2>(P, L, T, smem, join);
+  else if (groups == 3 || NTM == 3)
+    attend_tile<D, FMT, NTM, 3>(P, L, T, smem, join);
+  else
+    attend_tile<D, FMT, NTM, NTM>(P, L, T, smem, join);
 }
 
 // Joins the partial results of a row: one warp a row.  With M the largest of
@@ -503,14 +582,20 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
   return bound;
 }
 
+// Largest tile, in groups of 8 rows: 4 where a request's rows fill more than 24, else 3 (see Layout).
+int row_groups(const AttendParams &p) {
+  const int rows = (p.G + 1) * p.group;
+  return rows > 24 && rows <= 32 ? 4 : 3;
+}
+
 AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullptr) {
   AttendPlan L{};
   L.page = fast_div(std::max(1, p.c.block_size));
   L.group = fast_div(p.group);
   L.rows = static_cast<int32_t>((p.T + p.N) * p.group);
-  const int most = (p.G + 1) * p.group, R = most <= 16 && !p.prefix ? 16 : 32;
-  L.own_tiles = ceil_div(most, R);
-  L.prefix_tiles = ceil_div(L.rows, R);
+  L.row_groups = row_groups(p);
+  L.own_tiles = ceil_div((p.G + 1) * p.group, 8 * L.row_groups);
+  L.prefix_tiles = ceil_div(L.rows, 8 * L.row_groups);
   // (at least one private chunk, though no request may have private keys: its CTAs look at the requests' ranges)
   int bound = std::max(1, cut(static_cast<int64_t>(p.N) * p.c.num_kv_heads * L.own_tiles, p.max_seq - p.prefix, num_sms,
                               L.own_splits, L.own_chunk));
@@ -519,7 +604,7 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
                L.prefix_chunk);
   L.prefix_items = L.prefix_tiles * p.c.num_kv_heads * L.prefix_splits;
   L.slots = L.prefix_splits + L.own_splits;
-  L.qvec = (reinterpret_cast<uintptr_t>(p.q) & 7u) == 0 && p.q_token % 4 == 0 && p.q_head % 4 == 0;
+  L.qvec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0;
   const int64_t rows = static_cast<int64_t>(L.rows) * p.c.num_kv_heads;
   if (bytes) *bytes = bound <= 1 ? 0 : ((rows * bound * 8 + 15) & ~int64_t{15}) + rows * bound * p.c.head_dim * 4;
   L.part_ml = static_cast<float2 *>(p.workspace);
@@ -527,7 +612,7 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   return L;
 }
 
-template <int D, int FMT, int MT>
+template <int D, int FMT, int NTM>
 cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
@@ -535,11 +620,11 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stre
   if (own + L.prefix_items > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(static_cast<unsigned>(own + L.prefix_items));
   cfg.blockDim = dim3(kAttendThreads);
-  cfg.dynamicSmemBytes = attend_smem<D, MT>();
+  cfg.dynamicSmemBytes = Layout<D, NTM>::kBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<D, FMT, MT>, p, L);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<D, FMT, NTM>, p, L);
   if (e != cudaSuccess || L.slots == 1) return e;
   cfg.gridDim = dim3(p.N, std::max(1, std::min(65535, ceil_div((p.G + 1) * static_cast<int64_t>(p.Hq), kWarps))));
   cfg.blockDim = dim3(kThreads);
@@ -549,25 +634,25 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stre
 
 template <int D, int FMT>
 cudaError_t pick(const AttendParams &p, const AttendPlan &L, cudaStream_t s) {
-  return (p.G + 1) * p.group <= 16 && !p.prefix ? launch<D, FMT, 1>(p, L, s) : launch<D, FMT, 2>(p, L, s);
+  return L.row_groups == 4 ? launch<D, FMT, 4>(p, L, s) : launch<D, FMT, 3>(p, L, s);
 }
 
-template <int D, int FMT, int MT>
+template <int D, int FMT>
 cudaError_t enable() {
-  return cudaFuncSetAttribute(attend_kernel<D, FMT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(attend_smem<D, MT>()));
+  const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, FMT, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Layout<D, 3>::kBytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attend_kernel<D, FMT, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, 4>::kBytes);
 }
 
 }  // namespace
 
 cudaError_t enable_attend_kernels() {
   cudaError_t e;
-  if ((e = enable<128, SV_CACHE_INT8, 1>()) != cudaSuccess || (e = enable<128, SV_CACHE_INT8, 2>()) != cudaSuccess ||
-      (e = enable<128, SV_CACHE_E4M3, 1>()) != cudaSuccess || (e = enable<128, SV_CACHE_E4M3, 2>()) != cudaSuccess ||
-      (e = enable<64, SV_CACHE_INT8, 1>()) != cudaSuccess || (e = enable<64, SV_CACHE_INT8, 2>()) != cudaSuccess ||
-      (e = enable<64, SV_CACHE_E4M3, 1>()) != cudaSuccess)
+  if ((e = enable<128, SV_CACHE_INT8>()) != cudaSuccess || (e = enable<128, SV_CACHE_E4M3>()) != cudaSuccess ||
+      (e = enable<64, SV_CACHE_INT8>()) != cudaSuccess)
     return e;
-  return enable<64, SV_CACHE_E4M3, 2>();
+  return enable<64, SV_CACHE_E4M3>();
 }
 
 int64_t attend_workspace_bytes(const AttendParams &p, int num_sms) {
