@@ -4,13 +4,16 @@
 // A request's rows for one kv head -- (gamma + 1) tokens times the query heads
 // of the group -- all read the same keys, so the private part is bound by HBM:
 // 2 * head_dim + 8 bytes a key for 4 * head_dim * rows operations.  Each warp
-// streams keys on its own, 32 at a time: lane l copies exactly the bytes that
-// lane l will multiply into its own shared-memory places (cp.async, two or
-// three tiles deep), so there is no barrier and no wait between warps in the
-// loop.  That works because the order of the inner dimension of a product is
-// free: lane (g, c) of a 16x8x16 product takes 16-byte columns c, c + 4 of the
-// rows of keys g, g + 8, ..., and the queries are laid out once in the same
-// order; for the second product lane (g, c) takes dimensions [g * D/8,
+// streams keys on its own, 32 at a time, through shared memory of its own
+// (cp.async, two or three tiles deep), so no warp waits for another in the
+// loop.  A copy's eight (D = 64: four) neighbouring lanes take a whole row:
+// with the rows dealt to lanes the way the products read them, every 32-byte
+// sector was a request of its own, and the requests, not the bytes, set the
+// pace (256 private histories: 830 us, waiting for the data or not).  The
+// order of the inner dimension of a product is free, so lane (g, c) of a
+// 16x8x16 product takes 16-byte columns c, c + 4 of the rows of keys g, g + 8,
+// ..., the queries are laid out once in the same order, and no byte is moved
+// again; for the second product lane (g, c) takes dimensions [g * D/8,
 // (g + 1) * D/8) of the keys whose weights meet them.
 //
 // Both products are transposed: scores [keys x rows] = K Q^T and outputs
@@ -53,6 +56,17 @@ struct Layout {
   static constexpr int kJoin = kAttendWarps * NTM * 8 * kPitch * 4;
   static constexpr int kBytes = kQuery + (kRing > kJoin ? kRing : kJoin);
 };
+
+// Place of 16-byte column `col` of a tile's row.  Columns of a 128-byte line
+// change places so that the eight lanes that are served at once meet all
+// banks: for K they read columns c, c = 0 .. 3, of rows 2i and 2i + 1; for V
+// columns 2i and 2i + 1 of rows 2c (+ 1).
+template <int D, bool VALUES>
+__device__ __forceinline__ int tile_at(int row, int col) {
+  const int line = D == 128 ? row : row >> 1, in = D == 128 ? col : (row & 1) * 4 + col;
+  const int turn = VALUES ? (row >> 1 & 3) << 1 : (D == 128 ? (row & 1) << 2 : 0);
+  return line * 128 + (in ^ turn) * 16;
+}
 
 struct RowTile {
   int h, k_begin, k_end, slot, r0, rows;
@@ -140,8 +154,10 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
   const uint32_t ring = smem_addr(ring_ptr);
   const int tiles_all = (max(0, T.k_end - T.k_begin) + kKeys - 1) / kKeys;
   const int ntiles = (tiles_all - warp + kAttendWarps - 1) / kAttendWarps;  // tiles warp, warp + 4, ...
-  const uint8_t *const kcol = static_cast<const uint8_t *>(P.c.k) + T.h * P.c.head_stride + c * 16;
-  const uint8_t *const vcol = static_cast<const uint8_t *>(P.c.v) + T.h * P.c.head_stride + g * (D / 8);
+  constexpr int kCols = D / 16;  // 16-byte columns of a row, one lane each in a copy
+  const int ccol = lane % kCols;
+  const uint8_t *const kcol = static_cast<const uint8_t *>(P.c.k) + T.h * P.c.head_stride + ccol * 16;
+  const uint8_t *const vcol = static_cast<const uint8_t *>(P.c.v) + T.h * P.c.head_stride + ccol * 16;
   const float *const kscale = P.c.k_scale + T.h * P.c.scale_head_stride;
   const float *const vscale = P.c.v_scale + T.h * P.c.scale_head_stride;
   uint32_t bits = 0;
@@ -162,23 +178,16 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
         sat = page * P.c.scale_block_stride + off * P.c.scale_token_stride;
       }
       const uint32_t dead = __ballot_sync(0xFFFFFFFFu, !live);
-      const uint32_t dst = ring + stage * Y::kStage, mine = dst + lane * 16;
+      const uint32_t dst = ring + stage * Y::kStage;
       copy_async<4>(dst + Y::kScales + lane * 8, kscale + sat, live ? 4 : 0);
       copy_async<4>(dst + Y::kScales + lane * 8 + 4, vscale + sat, live ? 4 : 0);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {  // keys g, g + 8, g + 16, g + 24
-        const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, x * 8 + g);
-        const uint32_t n = dead >> (x * 8 + g) & 1u ? 0u : 16u;
-        const uint8_t *src = kcol + static_cast<uint64_t>(u) * 16;
-#pragma unroll
-        for (int q = 0; q < D / 64; ++q) copy_async<16>(mine + (x * (D / 64) + q) * 512, src + q * 64, n);
-      }
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of each half of the tile
-        const int key = (x >> 2) * 16 + ((x >> 1) & 1) * 8 + 2 * c + (x & 1);
-        const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, key);
-        copy_async<D / 8>(dst + kKeys * D + x * (4 * D) + lane * (D / 8), vcol + static_cast<uint64_t>(u) * 16,
-                          dead >> key & 1u ? 0u : D / 8);
+      for (int x = 0; x < kCols; ++x) {
+        const int row = x * (32 / kCols) + lane / kCols;
+        const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, row);
+        const uint32_t n = dead >> row & 1u ? 0u : 16u;
+        copy_async<16>(dst + tile_at<D, false>(row, ccol), kcol + static_cast<uint64_t>(u) * 16, n);
+        copy_async<16>(dst + kKeys * D + tile_at<D, true>(row, ccol), vcol + static_cast<uint64_t>(u) * 16, n);
       }
     }
     copy_commit();
@@ -201,10 +210,11 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
   }
   int stage = 0, fill = Y::kStages - 1;
   for (int it = 0; it < ntiles; ++it) {
-    issue(it + Y::kStages - 1, fill, page);  // (into the stage whose numbers the last step has used up)
+    copy_wait<Y::kStages - 2>();
+    __syncwarp();  // the tile is there for every lane, and no lane still reads the one before it
+    issue(it + Y::kStages - 1, fill, page);  // (in the place of the one before)
     page = page_of(it + Y::kStages);
     if (++fill == Y::kStages) fill = 0;
-    copy_wait<Y::kStages - 1>();
     const uint8_t *const src = ring_ptr + stage * Y::kStage;
     if (++stage == Y::kStages) stage = 0;
     const float2 sc = *reinterpret_cast<const float2 *>(src + Y::kScales + lane * 8);
@@ -220,7 +230,7 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
     for (int q = 0; q < D / 64; ++q) {
       uint4 kb[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) kb[x] = *reinterpret_cast<const uint4 *>(src + (x * (D / 64) + q) * 512 + lane * 16);
+      for (int x = 0; x < 4; ++x) kb[x] = *reinterpret_cast<const uint4 *>(src + tile_at<D, false>(x * 8 + g, q * 4 + c));
 #pragma unroll
       for (int s2 = 0; s2 < 2; ++s2) {
         uint4 b[NT];
@@ -243,22 +253,17 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
       }
     }
     // weights
-    Pair kw[4], vw[4], iw[4];  // of keys g, g + 8, g + 16, g + 24
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const float a = __shfl_sync(0xFFFFFFFFu, kc, x * 8 + g), b = __shfl_sync(0xFFFFFFFFu, lv, x * 8 + g),
-                  d = __shfl_sync(0xFFFFFFFFu, inv, x * 8 + g);
-      kw[x] = pair(a, a);
-      vw[x] = pair(b, b);
-      iw[x] = pair(d, d);
-    }
     // x: scores without the value's scale.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
-    Pair x[4][NT], y[4][NT];
+    Pair x[4][NT];
+    float vw[4];  // log2 of the value scale of keys g, g + 8, g + 16, g + 24
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) {
+      const float f = __shfl_sync(0xFFFFFFFFu, kc, k * 8 + g);
+      vw[k] = __shfl_sync(0xFFFFFFFFu, lv, k * 8 + g);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        x[k][nt] = mul2(pair(s[k >> 1][nt][(k & 1) * 2], s[k >> 1][nt][(k & 1) * 2 + 1]), kw[k]);
+        x[k][nt] = mul2(pair(s[k >> 1][nt][(k & 1) * 2], s[k >> 1][nt][(k & 1) * 2 + 1]), pair(f, f));
+    }
     const int k0 = T.k_begin + (it * kAttendWarps + warp) * kKeys;
     if (k0 + kKeys > low) {  // some row does not see all of the tile
 #pragma unroll
@@ -269,33 +274,29 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
           x[k][nt] = pair(key < limit[nt][0] ? lo(x[k][nt]) : -INFINITY, key < limit[nt][1] ? hi(x[k][nt]) : -INFINITY);
         }
     }
-    // y: less the maximum, and only then the value scale's log (a score too large to hold it would lose it)
-    float most[NT][2];
-    auto weigh = [&]() {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        most[nt][0] = most[nt][1] = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          y[k][nt] = add2(add2(x[k][nt], neg[nt]), vw[k]);
-          most[nt][0] = fmaxf(most[nt][0], lo(y[k][nt]));
-          most[nt][1] = fmaxf(most[nt][1], hi(y[k][nt]));
-        }
-      }
-    };
-    weigh();
+    // An exponent is the score less the maximum, and only then the value scale's log (a score too large to hold it
+    // would lose it).
+    auto exponent = [&](int k, int nt) { return add2(add2(x[k][nt], neg[nt]), pair(vw[k], vw[k])); };
     bool raise = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) raise |= most[nt][e] > (set >> (nt * 2 + e) & 1u ? kRaise : -INFINITY);
+      for (int k = 0; k < 4; ++k) {
+        const Pair y = exponent(k, nt);
+        most[0] = fmaxf(most[0], lo(y));
+        most[1] = fmaxf(most[1], hi(y));
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) raise |= most[e] > (set >> (nt * 2 + e) & 1u ? kRaise : -INFINITY);
+    }
     if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float r[2], up[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const Pair t = add2(x[k][nt], vw[k]);
+          const Pair t = add2(x[k][nt], pair(vw[k], vw[k]));
           up[0] = fmaxf(up[0], lo(t));
           up[1] = fmaxf(up[1], hi(t));
         }
@@ -327,32 +328,34 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
           o[t][nt][3] = hi(b);
         }
       }
-      weigh();
     }
     uint32_t p[2][NT][2];  // weights of a half's keys 2c, 2c + 1 (then + 8) for row g
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) {
+      const float d = __shfl_sync(0xFFFFFFFFu, inv, k * 8 + g);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float a = exp2_approx(lo(y[k][nt])), b = exp2_approx(hi(y[k][nt]));
-        l[nt] = fma2(pair(a, b), iw[k], l[nt]);
+        const Pair y = exponent(k, nt);
+        const float a = exp2_approx(lo(y)), b = exp2_approx(hi(y));
+        l[nt] = fma2(pair(a, b), pair(d, d), l[nt]);
         p[k >> 1][nt][k & 1] = transpose_8x8(pack_f16(a, b));
       }
+    }
     // values
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint8_t *vs = src + kKeys * D + j * 4 * (4 * D) + lane * (D / 8);
       uint32_t v[4][D / 32];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        const int row = j * 16 + (k >> 1) * 8 + 2 * c + (k & 1);
         if (D == 128) {
-          const uint4 w = *reinterpret_cast<const uint4 *>(vs + k * (4 * D));
+          const uint4 w = *reinterpret_cast<const uint4 *>(src + kKeys * D + tile_at<D, true>(row, g));
           v[k][0] = w.x;
           v[k][1] = w.y;
           v[k][D / 32 - 2] = w.z;
           v[k][D / 32 - 1] = w.w;
         } else {
-          const uint2 w = *reinterpret_cast<const uint2 *>(vs + k * (4 * D));
+          const uint2 w = *reinterpret_cast<const uint2 *>(src + kKeys * D + tile_at<D, true>(row, g >> 1) + (g & 1) * 8);
           v[k][0] = w.x;
           v[k][1] = w.y;
         }
