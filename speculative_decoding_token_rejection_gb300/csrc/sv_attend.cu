@@ -41,19 +41,21 @@ constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kKeys = 32;    // keys of a warp's tile
 constexpr float kRaise = 8;  // a row's maximum is raised when a weight would pass 2^kRaise
 
-// NTM: the most 8-row groups of a row tile.  Tiles of up to 24 rows leave the
-// registers for three CTAs per SM (two copy stages), tiles of 32 rows for two
-// (three stages): either way about 100 KB of copies are in flight per SM.
-template <int D, int NTM>
+constexpr int kGroups = 4;   // groups of 8 rows in a row tile
+constexpr int kStages = 2;   // tiles in a warp's ring
+
+// Two CTAs per SM: 255 registers hold four row groups (outputs 128), and 150
+// KB of shared memory leave the L1 cache 100 KB.  Three CTAs of up to three
+// groups (168 registers), or three stages, were slower -- 256 private
+// histories 691 and 675 us against 593 -- although more copies were in flight.
+template <int D>
 struct Layout {
-  static constexpr int kStages = NTM <= 3 ? 2 : 3;
-  static constexpr int kCtas = NTM <= 3 ? 3 : 2;
   static constexpr int kScales = kKeys * 2 * D;  // of a stage: keys, values, then (key scale, value scale) of key `lane`
   static constexpr int kStage = kScales + kKeys * 8;
-  static constexpr int kQuery = NTM * 8 * D * 2;
+  static constexpr int kQuery = kGroups * 8 * D * 2;
   static constexpr int kPitch = D + 4;  // floats of an output row while the warps' results are joined
   static constexpr int kRing = kAttendWarps * kStages * kStage;
-  static constexpr int kJoin = kAttendWarps * NTM * 8 * kPitch * 4;
+  static constexpr int kJoin = kAttendWarps * kGroups * 8 * kPitch * 4;
   static constexpr int kBytes = kQuery + (kRing > kJoin ? kRing : kJoin);
 };
 
@@ -80,10 +82,10 @@ struct JoinSmem {
   uint32_t top[kAttendWarps];
 };
 
-template <int D, int FMT, int NTM, int NT>
+template <int D, int FMT, int NT>
 __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendPlan &L, const RowTile &T, uint8_t *smem,
                                             JoinSmem &J) {
-  using Y = Layout<D, NTM>;
+  using Y = Layout<D>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
 
   // ---- the queries as operand fragments: 8 consecutive dimensions for each lane and pair of steps ----
@@ -150,7 +152,7 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
   __syncthreads();
 
   // ---- the stream of keys ----
-  uint8_t *const ring_ptr = smem + Y::kQuery + warp * Y::kStages * Y::kStage;
+  uint8_t *const ring_ptr = smem + Y::kQuery + warp * kStages * Y::kStage;
   const uint32_t ring = smem_addr(ring_ptr);
   const int tiles_all = (max(0, T.k_end - T.k_begin) + kKeys - 1) / kKeys;
   const int ntiles = (tiles_all - warp + kAttendWarps - 1) / kAttendWarps;  // tiles warp, warp + 4, ...
@@ -204,19 +206,19 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
   }
   int page = page_of(0);
 #pragma unroll
-  for (int it = 0; it < Y::kStages - 1; ++it) {
+  for (int it = 0; it < kStages - 1; ++it) {
     issue(it, it, page);
     page = page_of(it + 1);
   }
-  int stage = 0, fill = Y::kStages - 1;
+  int stage = 0, fill = kStages - 1;
   for (int it = 0; it < ntiles; ++it) {
-    copy_wait<Y::kStages - 2>();
+    copy_wait<kStages - 2>();
     __syncwarp();  // the tile is there for every lane, and no lane still reads the one before it
-    issue(it + Y::kStages - 1, fill, page);  // (in the place of the one before)
-    page = page_of(it + Y::kStages);
-    if (++fill == Y::kStages) fill = 0;
+    issue(it + kStages - 1, fill, page);  // (in the place of the one before)
+    page = page_of(it + kStages);
+    if (++fill == kStages) fill = 0;
     const uint8_t *const src = ring_ptr + stage * Y::kStage;
-    if (++stage == Y::kStages) stage = 0;
+    if (++stage == kStages) stage = 0;
     const float2 sc = *reinterpret_cast<const float2 *>(src + Y::kScales + lane * 8);
     float kc = sc.x * c_tile, lv, inv;
     value_scale_terms(sc.y, kc, lv, inv);
@@ -435,12 +437,12 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
   }
 }
 
-template <int D, int FMT, int NTM>
-__global__ void __launch_bounds__(kAttendThreads, Layout<D, NTM>::kCtas) attend_kernel(const AttendParams P, const AttendPlan L) {
+template <int D, int FMT>
+__global__ void __launch_bounds__(kAttendThreads, 2) attend_kernel(const AttendParams P, const AttendPlan L) {
   pdl_enter();
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ JoinSmem join;
-  __shared__ int row_token[NTM * 8], row_limit[NTM * 8];
+  __shared__ int row_token[kGroups * 8], row_limit[kGroups * 8];
   const int tid = threadIdx.x, H = P.c.num_kv_heads;
   RowTile T;
   T.table = P.tables;
@@ -455,8 +457,8 @@ __global__ void __launch_bounds__(kAttendThreads, Layout<D, NTM>::kCtas) attend_
     b /= L.prefix_tiles;
     T.h = b % H;
     T.slot = b / H;
-    T.r0 = tile * NTM * 8;
-    T.rows = min(NTM * 8, L.rows - T.r0);
+    T.r0 = tile * kGroups * 8;
+    T.rows = min(kGroups * 8, L.rows - T.r0);
     T.k_begin = T.slot * L.prefix_chunk;
     T.k_end = min(P.prefix, T.k_begin + L.prefix_chunk);
   } else {
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(kAttendThreads, Layout<D, NTM>::kCtas) attend_
     if (bits && tile == 0 && T.h == 0 && split == 0 && tid == 0 && P.status) atomicOr(P.status, static_cast<int>(bits));
     if (!ok) return;
     // the request's row groups, dealt evenly to as few tiles as hold them
-    const int all = (gam + 1) * P.group, groups = (all + 7) / 8, tiles = (groups + NTM - 1) / NTM;
+    const int all = (gam + 1) * P.group, groups = (all + 7) / 8, tiles = (groups + kGroups - 1) / kGroups;
     if (tile >= tiles) return;
     const int per = (groups + tiles - 1) / tiles * 8;
     T.r0 = tile * per;
@@ -503,13 +505,13 @@ __global__ void __launch_bounds__(kAttendThreads, Layout<D, NTM>::kCtas) attend_
   __syncthreads();
   const int groups = (T.rows + 7) / 8;
   if (groups == 1)
-    attend_tile<D, FMT, NTM, 1>(P, L, T, smem, join);
+    attend_tile<D, FMT, 1>(P, L, T, smem, join);
   else if (groups == 2)
-    attend_tile<D, FMT, NTM, 2>(P, L, T, smem, join);
-  else if (groups == 3 || NTM == 3)
-    attend_tile<D, FMT, NTM, 3>(P, L, T, smem, join);
+    attend_tile<D, FMT, 2>(P, L, T, smem, join);
+  else if (groups == 3)
+    attend_tile<D, FMT, 3>(P, L, T, smem, join);
   else
-    attend_tile<D, FMT, NTM, NTM>(P, L, T, smem, join);
+    attend_tile<D, FMT, 4>(P, L, T, smem, join);
 }
 
 // Joins the partial results of a row: one warp a row.  With M the largest of
@@ -585,20 +587,13 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
   return bound;
 }
 
-// Largest tile, in groups of 8 rows: 4 where a request's rows fill more than 24, else 3 (see Layout).
-int row_groups(const AttendParams &p) {
-  const int rows = (p.G + 1) * p.group;
-  return rows > 24 && rows <= 32 ? 4 : 3;
-}
-
 AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullptr) {
   AttendPlan L{};
   L.page = fast_div(std::max(1, p.c.block_size));
   L.group = fast_div(p.group);
   L.rows = static_cast<int32_t>((p.T + p.N) * p.group);
-  L.row_groups = row_groups(p);
-  L.own_tiles = ceil_div((p.G + 1) * p.group, 8 * L.row_groups);
-  L.prefix_tiles = ceil_div(L.rows, 8 * L.row_groups);
+  L.own_tiles = ceil_div((p.G + 1) * static_cast<int64_t>(p.group), 8 * kGroups);
+  L.prefix_tiles = ceil_div(L.rows, 8 * kGroups);
   // (at least one private chunk, though no request may have private keys: its CTAs look at the requests' ranges)
   int bound = std::max(1, cut(static_cast<int64_t>(p.N) * p.c.num_kv_heads * L.own_tiles, p.max_seq - p.prefix, num_sms,
                               L.own_splits, L.own_chunk));
@@ -615,7 +610,7 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   return L;
 }
 
-template <int D, int FMT, int NTM>
+template <int D, int FMT>
 cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
@@ -623,11 +618,11 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stre
   if (own + L.prefix_items > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(static_cast<unsigned>(own + L.prefix_items));
   cfg.blockDim = dim3(kAttendThreads);
-  cfg.dynamicSmemBytes = Layout<D, NTM>::kBytes;
+  cfg.dynamicSmemBytes = Layout<D>::kBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<D, FMT, NTM>, p, L);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<D, FMT>, p, L);
   if (e != cudaSuccess || L.slots == 1) return e;
   cfg.gridDim = dim3(p.N, std::max(1, std::min(65535, ceil_div((p.G + 1) * static_cast<int64_t>(p.Hq), kWarps))));
   cfg.blockDim = dim3(kThreads);
@@ -636,16 +631,8 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stre
 }
 
 template <int D, int FMT>
-cudaError_t pick(const AttendParams &p, const AttendPlan &L, cudaStream_t s) {
-  return L.row_groups == 4 ? launch<D, FMT, 4>(p, L, s) : launch<D, FMT, 3>(p, L, s);
-}
-
-template <int D, int FMT>
 cudaError_t enable() {
-  const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, FMT, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Layout<D, 3>::kBytes);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attend_kernel<D, FMT, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, 4>::kBytes);
+  return cudaFuncSetAttribute(attend_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
 }
 
 }  // namespace
@@ -667,8 +654,8 @@ int64_t attend_workspace_bytes(const AttendParams &p, int num_sms) {
 cudaError_t launch_attend(const AttendParams &p, int num_sms, cudaStream_t stream) {
   const AttendPlan L = make_plan(p, num_sms);
   const bool i8 = p.c.format == SV_CACHE_INT8;
-  if (p.c.head_dim == 128) return i8 ? pick<128, SV_CACHE_INT8>(p, L, stream) : pick<128, SV_CACHE_E4M3>(p, L, stream);
-  return i8 ? pick<64, SV_CACHE_INT8>(p, L, stream) : pick<64, SV_CACHE_E4M3>(p, L, stream);
+  if (p.c.head_dim == 128) return i8 ? launch<128, SV_CACHE_INT8>(p, L, stream) : launch<128, SV_CACHE_E4M3>(p, L, stream);
+  return i8 ? launch<64, SV_CACHE_INT8>(p, L, stream) : launch<64, SV_CACHE_E4M3>(p, L, stream);
 }
 
 }  // namespace sv

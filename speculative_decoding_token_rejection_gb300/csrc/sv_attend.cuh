@@ -30,7 +30,6 @@ struct AttendPlan {
   int32_t rows;           // (T + N) * group rows for every kv head
   int32_t prefix_splits, prefix_chunk, prefix_tiles, prefix_items;
   int32_t own_splits, own_chunk, own_tiles;
-  int32_t row_groups;     // groups of 8 rows in a row tile
   int32_t slots;          // 1: results go straight to the output
   bool qvec;              // q rows allow 16-byte loads
   float *part_o;          // [rows * num_kv_heads][slots][D], row = token * Hq + query head
