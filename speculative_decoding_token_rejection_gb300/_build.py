@@ -23,6 +23,7 @@ SOURCES = ["sv_api.cu", "sv_probs.cu", "sv_logits.cu", "sv_logits_bf16.cu", "sv_
            "sv_logits_f32_proc.cu", "sv_sample_bf16.cu", "sv_sample_f32.cu", "sv_sample_bf16_proc.cu",
            "sv_sample_f32_proc.cu", "sv_stream_bf16.cu", "sv_stream_f32.cu",
            "sv_stream_bf16_proc.cu", "sv_stream_f32_proc.cu", "sv_ngram.cu", "sv_ops_api.cu", "sv_cache.cu", "sv_attend.cu",
+           "sv_attend_prefix.cu",
            "sv_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",

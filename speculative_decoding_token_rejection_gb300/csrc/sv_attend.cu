@@ -565,6 +565,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttendParams P, co
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 constexpr int kChunkStep = kAttendWarps * kKeys;  // a CTA's four warps take 32 keys each
+constexpr int kTensorKeys = 128, kTensorRows = 96;  // the prefix goes to the tensor-memory kernel from here on
+constexpr int kTensorFixed = 3, kTensorSplits = 64;
 constexpr int kChunkMost = 2048;                  // so that the longest request is no long tail
 
 // Chunks for `keys` keys when `base` CTAs work on every chunk: enough to give
@@ -587,6 +589,24 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
   return bound;
 }
 
+// Chunks of the tensor-memory kernel, whose CTAs have an SM each: as many as
+// make the last wave of CTAs end soonest, a chunk's fixed cost counted as
+// kTensorFixed key tiles.
+void cut_tensor(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
+  const int step = prefix_key_tile(), all = ceil_div(keys, step);
+  int64_t best = INT64_MAX;
+  for (int tiles = all; tiles >= 1; --tiles) {
+    const int s = ceil_div(all, tiles);
+    if (s > kTensorSplits) break;
+    const int64_t cost = ((base * s + num_sms - 1) / num_sms) * (tiles + kTensorFixed);
+    if (cost < best) {
+      best = cost;
+      splits = s;
+      chunk = tiles * step;
+    }
+  }
+}
+
 AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullptr) {
   AttendPlan L{};
   L.page = fast_div(std::max(1, p.c.block_size));
@@ -598,9 +618,16 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   int bound = std::max(1, cut(static_cast<int64_t>(p.N) * p.c.num_kv_heads * L.own_tiles, p.max_seq - p.prefix, num_sms,
                               L.own_splits, L.own_chunk));
   L.own_splits = std::max(1, L.own_splits);
-  bound += cut(static_cast<int64_t>(p.c.num_kv_heads) * L.prefix_tiles, p.prefix, num_sms, L.prefix_splits,
+  if (p.prefix >= kTensorKeys && L.rows >= kTensorRows) {
+    L.tensor_tiles = ceil_div(L.rows, prefix_row_tile());
+    cut_tensor(static_cast<int64_t>(p.c.num_kv_heads) * L.tensor_tiles, p.prefix, num_sms, L.prefix_splits,
                L.prefix_chunk);
-  L.prefix_items = L.prefix_tiles * p.c.num_kv_heads * L.prefix_splits;
+    bound += L.prefix_splits;
+  } else {
+    bound += cut(static_cast<int64_t>(p.c.num_kv_heads) * L.prefix_tiles, p.prefix, num_sms, L.prefix_splits,
+                 L.prefix_chunk);
+    L.prefix_items = L.prefix_tiles * p.c.num_kv_heads * L.prefix_splits;
+  }
   L.slots = L.prefix_splits + L.own_splits;
   L.qvec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0;
   const int64_t rows = static_cast<int64_t>(L.rows) * p.c.num_kv_heads;
@@ -622,7 +649,8 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stre
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<D, FMT>, p, L);
+  cudaError_t e = L.tensor_tiles ? launch_prefix(p, L, stream) : cudaSuccess;
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, attend_kernel<D, FMT>, p, L);
   if (e != cudaSuccess || L.slots == 1) return e;
   cfg.gridDim = dim3(p.N, std::max(1, std::min(65535, ceil_div((p.G + 1) * static_cast<int64_t>(p.Hq), kWarps))));
   cfg.blockDim = dim3(kThreads);
@@ -640,7 +668,7 @@ cudaError_t enable() {
 cudaError_t enable_attend_kernels() {
   cudaError_t e;
   if ((e = enable<128, SV_CACHE_INT8>()) != cudaSuccess || (e = enable<128, SV_CACHE_E4M3>()) != cudaSuccess ||
-      (e = enable<64, SV_CACHE_INT8>()) != cudaSuccess)
+      (e = enable<64, SV_CACHE_INT8>()) != cudaSuccess || (e = enable_prefix_kernels()) != cudaSuccess)
     return e;
   return enable<64, SV_CACHE_E4M3>();
 }

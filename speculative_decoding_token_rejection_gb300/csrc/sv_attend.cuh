@@ -28,13 +28,22 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct AttendPlan {
   FastDiv page, group;
   int32_t rows;           // (T + N) * group rows for every kv head
-  int32_t prefix_splits, prefix_chunk, prefix_tiles, prefix_items;
+  int32_t prefix_splits, prefix_chunk;
+  int32_t prefix_tiles, prefix_items;  // prefix row tiles and CTAs of the warp-streaming kernel (0 items: not its work)
+  int32_t tensor_tiles;                // prefix row tiles of the tensor-memory kernel (0: not its work)
   int32_t own_splits, own_chunk, own_tiles;
   int32_t slots;          // 1: results go straight to the output
   bool qvec;              // q rows allow 16-byte loads
   float *part_o;          // [rows * num_kv_heads][slots][D], row = token * Hq + query head
   float2 *part_ml;        // [rows * num_kv_heads][slots]: M, l
 };
+
+// The prefix on the tensor cores' memory (sv_attend_prefix.cu): tiles of
+// prefix_row_tile() rows and prefix_key_tile() keys.
+cudaError_t enable_prefix_kernels();
+cudaError_t launch_prefix(const AttendParams &p, const AttendPlan &L, cudaStream_t stream);
+int prefix_row_tile();
+int prefix_key_tile();
 
 // Draft range and length of request i; false (and nothing to write) for a bad
 // range.  A bad length counts as 0.

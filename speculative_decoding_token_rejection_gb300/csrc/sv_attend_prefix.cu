@@ -1,0 +1,627 @@
+// sv_attend_prefix.cu -- the shared prefix of the verify tokens' attention on
+// the tensor cores' own memory (tcgen05).
+//
+// All requests' rows of a kv head meet the same prefix keys, so the work is two
+// matrix products of thousands of rows and is bound by the tensor cores and
+// what feeds them: 4 * head_dim operations a (row, key) pair, one exponential
+// each.  A CTA takes 256 rows (two accumulator tiles of 128) of one kv head
+// and a range of keys, 128 at a time:
+//
+//   warps 0-3, 4-7  softmax of a row tile, a thread a row: reads S from tensor
+//                   memory, writes the weights back over it as f16
+//   warps 8-10      bytes to f16 (exact), global memory -> registers -> shared
+//                   memory, K and V two tiles deep
+//   warp 11         issues S = Q K^T and O += P V (P from tensor memory)
+//
+// While one row tile's softmax runs, the tensor cores work for the other:
+// S0 S1 | P0 V, S0' | P1 V, S1' | ...  The products run in the order they are
+// issued, so S0' may overwrite P0, and "S0' is done" tells the softmax that
+// P0 V is too: the output may be rescaled then.
+//
+// Numbers.  x = (q . b) * (scale * log2 e * key_scale) as in sv_attend.cuh, but
+// a thread sees its row's keys one register each, so the value scales are kept
+// out of the exponent: w = 2^(x - m), l = sum w, P = w * value_scale / W with W
+// a power of two near the first tile's largest value scale, O = W * sum P b.
+// Any m gives the same quotient O / l; it is raised to the largest x + log2(
+// value_scale / W) when that passes it by 8, so P stays below 2^8.  Whether it
+// may have is seen from max x and the tile's largest value scale alone.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "sv_attend.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kRowsTile = 128;  // rows of an accumulator tile
+constexpr int kKeyTile = 128;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kLoadThreads = 96;
+constexpr int kPrefixThreads = kSoftmaxThreads + kLoadThreads + 32;
+constexpr int kPasses = (kKeyTile * 8 + kLoadThreads - 1) / kLoadThreads;  // 16-byte pieces of a thread, D = 128
+constexpr int kVectorSlots = 4;
+constexpr uint32_t kWaitPolls = 1u << 24;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kRaise = 8;
+
+struct alignas(16) Vectors {  // of one key tile; read 16 bytes at a time
+  float kc[kKeyTile], vr[kKeyTile];
+  float top[3];      // log2 of a load warp's largest value scale / W
+  uint32_t dead[4];  // keys left out, a bit each
+};
+
+struct Control {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], vec_full[kVectorSlots], s_full[2], p_full[2], done;
+  uint32_t tmem, query_top, scale_top, abort;
+};
+
+static_assert(sizeof(Vectors) % 16 == 0, "every slot starts on a 16-byte boundary");
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = kKeyTile * D * 2;  // a K, V or Q tile in f16
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kVec = 6 * kTile,
+                       kControl = kVec + kVectorSlots * static_cast<int>(sizeof(Vectors)),
+                       kBytes = kControl + static_cast<int>(sizeof(Control)) + 1024;  // (the base is rounded up to 1 KB)
+};
+
+// ---------------------------------------------------------------------------
+// tcgen05
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// D (tensor memory) = A B (+ D), both operands in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// Arrives on `bar` once every product issued so far by this thread is done.
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+// Waits for every load so far; the registers go through, so no use of them moves ahead of the wait.
+__device__ __forceinline__ void tmem_wait_load(uint32_t r[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand with rows of 128 bytes (64 f16), 8-row groups of 1 KB,
+// 16-byte columns exchanged within a group (column ^ row % 8).  `next64`:
+// bytes from 64 elements to the next 64 where those run along the operand's
+// outer dimension.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t next64) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | static_cast<uint64_t>((next64 >> 4) & 0x3FFF) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// f16 operands, fp32 sums, 128 x n; B's outer dimension contiguous or its inner one.
+constexpr uint32_t product(int n, bool b_outer_contiguous) {
+  return 1u << 4 | (b_outer_contiguous ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (128u / 16) << 24;
+}
+
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for phase `parity` of a barrier; false when the CTA gives up (a wait
+// of two seconds, or another thread that did).
+__device__ __forceinline__ bool wait(Control &C, uint64_t *bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t began = now_ns();
+  for (uint32_t it = 0; it < kWaitPolls; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*const_cast<volatile uint32_t *>(&C.abort)) return false;
+    if ((it & 15u) == 15u && now_ns() - began > kWaitNs) break;
+  }
+  *const_cast<volatile uint32_t *>(&C.abort) = 1;
+  return false;
+}
+// The same for all lanes of a warp together.
+__device__ __forceinline__ bool wait_warp(Control &C, uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, wait(C, bar, parity));
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendParams P, const AttendPlan L) {
+  pdl_enter();
+  extern __shared__ uint8_t raw[];
+  uint8_t *const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  using Y = Smem<D>;
+  Control &C = *reinterpret_cast<Control *>(smem + Y::kControl);
+  Vectors *const vec = reinterpret_cast<Vectors *>(smem + Y::kVec);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int H = P.c.num_kv_heads;
+  int b = blockIdx.x;
+  const int pair_tile = b % L.tensor_tiles;
+  b /= L.tensor_tiles;
+  const int h = b % H, slot = b / H;
+  const int r0 = pair_tile * 2 * kRowsTile;
+  const int tiles = L.rows - r0 > kRowsTile ? 2 : 1;
+  const int k_begin = slot * L.prefix_chunk, k_end = min(P.prefix, k_begin + L.prefix_chunk);
+  const int n = (k_end - k_begin + kKeyTile - 1) / kKeyTile;  // >= 1
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&C.k_full[i], kLoadThreads);
+      mbar_init(&C.k_empty[i], 1);
+      mbar_init(&C.v_full[i], kLoadThreads);
+      mbar_init(&C.v_empty[i], 1);
+      mbar_init(&C.s_full[i], 1);
+      mbar_init(&C.p_full[i], kRowsTile);
+    }
+    for (int i = 0; i < kVectorSlots; ++i) mbar_init(&C.vec_full[i], kLoadThreads);
+    mbar_init(&C.done, 1);
+    C.query_top = C.scale_top = C.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 11) tmem_alloc(&C.tmem, 512);
+  __syncthreads();
+
+  if (warp < 8) {
+    // -------------------------------------------------------------------
+    // softmax of row tile `t`
+    // -------------------------------------------------------------------
+    const int t = warp >> 2, w4 = warp & 3;
+    {  // the tile's queries: f16 with the CTA's common power of two
+      uint4 x[D / 8];  // warp w4 takes rows 32 * w4 ..; a row is D/8 lanes
+      constexpr int kLanes = D / 8, kRowsPass = 32 / kLanes, kQ = 32 / kRowsPass;
+      uint32_t top = 0;
+#pragma unroll
+      for (int f = 0; f < kQ; ++f) {
+        const int r = r0 + t * kRowsTile + w4 * 32 + f * kRowsPass + lane / kLanes;
+        x[f] = make_uint4(0, 0, 0, 0);
+        if (r < L.rows) {
+          const int token = div_by(r, L.group), hq = h * P.group + r - token * P.group;
+          const uint16_t *src = P.q + token * P.q_token + hq * P.q_head + lane % kLanes * 8;
+          if (L.qvec) {
+            x[f] = *reinterpret_cast<const uint4 *>(src);
+          } else {
+            x[f].x = src[0] | static_cast<uint32_t>(src[1]) << 16;
+            x[f].y = src[2] | static_cast<uint32_t>(src[3]) << 16;
+            x[f].z = src[4] | static_cast<uint32_t>(src[5]) << 16;
+            x[f].w = src[6] | static_cast<uint32_t>(src[7]) << 16;
+          }
+        }
+        const uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo_ = w[e] << 16 & 0x7FFFFFFFu, hi_ = w[e] & 0x7FFF0000u;
+          if (lo_ < 0x7F800000u) top = max(top, lo_);
+          if (hi_ < 0x7F800000u) top = max(top, hi_);
+        }
+      }
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (lane == 0) atomicMax(&C.query_top, top);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float up = pow2(query_shift(*const_cast<volatile uint32_t *>(&C.query_top)));
+#pragma unroll
+      for (int f = 0; f < kQ; ++f) {
+        const int r = w4 * 32 + f * kRowsPass + lane / kLanes, col = lane % kLanes;
+        uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_f16(bf16_bits_to_float(w[e] & 0xFFFFu) * up, bf16_bits_to_float(w[e] >> 16) * up);
+        *reinterpret_cast<uint4 *>(smem + Y::kQ + t * Y::kTile + (col >> 3) * (kRowsTile * 128) + r * 128 +
+                                   (((col & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+    }
+    const int row = r0 + t * kRowsTile + (tid & 127);
+    int token = -1, limit = 0x7FFFFFFF;
+    if (row < L.rows) {
+      token = div_by(row, L.group);
+      limit = prefix_limit(P, token);
+      if (limit < 0) {  // nobody's row
+        token = -1;
+        limit = 0x7FFFFFFF;
+      }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t s_addr = C.tmem + (static_cast<uint32_t>(w4 * 32) << 16) + t * 128;
+    const uint32_t o_addr = s_addr + 256;
+    float m = -INFINITY;
+    Pair l = pair(0.0f, 0.0f);
+    bool ok = t < tiles;
+    for (int i = 0; ok && i < n; ++i) {
+      const Vectors &V = vec[i % kVectorSlots];
+      ok = wait_warp(C, &C.vec_full[i % kVectorSlots], (i / kVectorSlots) & 1) && wait_warp(C, &C.s_full[t], i & 1);
+      if (!ok) break;
+      fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_load32(s_addr + q * 32, s[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_wait_load(s[q]);
+      // x, and its largest
+      float top = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 k = *reinterpret_cast<const float4 *>(&V.kc[q * 32 + j]);
+          const Pair a = mul2(pair(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])), pair(k.x, k.y));
+          const Pair c = mul2(pair(__uint_as_float(s[q][j + 2]), __uint_as_float(s[q][j + 3])), pair(k.z, k.w));
+          s[q][j] = __float_as_uint(lo(a));
+          s[q][j + 1] = __float_as_uint(hi(a));
+          s[q][j + 2] = __float_as_uint(lo(c));
+          s[q][j + 3] = __float_as_uint(hi(c));
+        }
+      const int k0 = k_begin + i * kKeyTile;
+      const uint32_t any_dead = V.dead[0] | V.dead[1] | V.dead[2] | V.dead[3];
+      if (__any_sync(0xFFFFFFFFu, any_dead || k0 + kKeyTile > limit)) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t dead = V.dead[q];
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (k0 + q * 32 + j >= limit || (dead >> j & 1u)) s[q][j] = 0xFF800000u;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])));
+      const float over = fmaxf(fmaxf(V.top[0], V.top[1]), V.top[2]);
+      const bool raise = top + over > m + kRaise || (m == -INFINITY && top > -INFINITY);
+      if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
+        float most = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) most = fmaxf(most, __uint_as_float(s[q][j]) + __log2f(V.vr[q * 32 + j]));
+        const float next = most > m + kRaise || m == -INFINITY ? most : m;
+        const float r = m == -INFINITY ? 1.0f : exp2_approx(m - next);  // (without a maximum O and l are zeros or NaN)
+        m = next;
+        l = mul2(l, pair(r, r));
+        if (i > 0) {
+#pragma unroll
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                "%14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+                  "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                : "r"(o_addr + q * 16)
+                : "memory");
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * r);
+            tmem_store16(o_addr + q * 16, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      const Pair neg = pair(-base, -base);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(&V.vr[q * 32 + j]);
+          const Pair ya = add2(pair(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])), neg);
+          const Pair yb = add2(pair(__uint_as_float(s[q][j + 2]), __uint_as_float(s[q][j + 3])), neg);
+          const Pair wa = pair(exp2_approx(lo(ya)), exp2_approx(hi(ya)));
+          const Pair wb = pair(exp2_approx(lo(yb)), exp2_approx(hi(yb)));
+          l = add2(l, wa);
+          l = add2(l, wb);
+          const Pair pa = mul2(wa, pair(v.x, v.y)), pb = mul2(wb, pair(v.z, v.w));
+          p[j / 2] = pack_f16(lo(pa), hi(pa));
+          p[j / 2 + 1] = pack_f16(lo(pb), hi(pb));
+        }
+        tmem_store16(s_addr + q * 16, p);
+      }
+      tmem_wait_store();
+      fence_before();
+      mbar_arrive(&C.p_full[t]);
+    }
+    // the partial result
+    if (ok) ok = wait_warp(C, &C.done, 0);
+    fence_after();
+    if (t < tiles) {
+      const float w = ok ? __uint_as_float(*const_cast<volatile uint32_t *>(&C.scale_top)) : 0.0f;
+      const int hq = token < 0 ? 0 : h * P.group + row - token * P.group;
+      const int64_t at = (static_cast<int64_t>(token) * P.Hq + hq) * L.slots + slot;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_load32(o_addr + q * 32, o);
+        tmem_wait_load(o);
+        if (token >= 0 && ok) {
+          float *dst = L.part_o + at * D + q * 32;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4 *>(dst + j) =
+                make_float4(__uint_as_float(o[j]) * w, __uint_as_float(o[j + 1]) * w, __uint_as_float(o[j + 2]) * w,
+                            __uint_as_float(o[j + 3]) * w);
+        }
+      }
+      if (token >= 0) L.part_ml[at] = ok ? make_float2(m, lo(l) + hi(l)) : make_float2(-INFINITY, 0.0f);
+    }
+    fence_before();
+  } else if (warp < 11) {
+    // -------------------------------------------------------------------
+    // bytes to f16 tiles
+    // -------------------------------------------------------------------
+    constexpr int kCols = D / 16, kRowsPass = kLoadThreads / kCols, kP = (kKeyTile + kRowsPass - 1) / kRowsPass;
+    static_assert(kP <= kPasses, "pieces of a thread");
+    const int lt = tid - kSoftmaxThreads, col = lt % kCols, row_in = lt / kCols;
+    const uint8_t *const kcol = static_cast<const uint8_t *>(P.c.k) + h * P.c.head_stride + col * 16;
+    const uint8_t *const vcol = static_cast<const uint8_t *>(P.c.v) + h * P.c.head_stride + col * 16;
+    const float *const kscale = P.c.k_scale + h * P.c.scale_head_stride;
+    const float *const vscale = P.c.v_scale + h * P.c.scale_head_stride;
+    uint32_t unit[kP], bad = 0;
+    uint4 kr[kP], vr[kP];
+    float ks[2], vs[2];
+    uint32_t lost[2];  // a key of the range whose page is outside the cache
+    auto places = [&](int i) {
+#pragma unroll
+      for (int p = 0; p < kP; ++p) {
+        const int r = p * kRowsPass + row_in, k = k_begin + i * kKeyTile + r;
+        unit[p] = 0xFFFFFFFFu;
+        if (i < n && r < kKeyTile && k < k_end) {
+          const int x = div_by(k, L.page), page = P.tables[x];
+          if (page >= 0 && page < P.c.num_blocks)
+            unit[p] = static_cast<uint32_t>(
+                (page * P.c.block_stride + (k - x * P.c.block_size) * P.c.token_stride) >> 4);
+        }
+      }
+    };
+    auto load = [&](const uint8_t *base, uint4 dst[kP]) {
+#pragma unroll
+      for (int p = 0; p < kP; ++p)
+        dst[p] = unit[p] == 0xFFFFFFFFu ? make_uint4(0, 0, 0, 0)
+                                        : __ldg(reinterpret_cast<const uint4 *>(base + static_cast<uint64_t>(unit[p]) * 16));
+    };
+    auto scales = [&](int i) {  // keys lt and lt + 96 of the tile
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = lt + e * kLoadThreads, k = k_begin + i * kKeyTile + r;
+        ks[e] = vs[e] = 0.0f;
+        lost[e] = 0;
+        if (i < n && r < kKeyTile && k < k_end) {
+          const int x = div_by(k, L.page), page = P.tables[x];
+          if (page >= 0 && page < P.c.num_blocks) {
+            const int64_t at = page * P.c.scale_block_stride + (k - x * P.c.block_size) * P.c.scale_token_stride;
+            ks[e] = kscale[at];
+            vs[e] = vscale[at];
+          } else {
+            bad = SV_DATA_BAD_SLOT;
+            lost[e] = 1;
+          }
+        }
+      }
+    };
+    auto store = [&](int tile_base, const uint4 src[kP]) {
+#pragma unroll
+      for (int p = 0; p < kP; ++p) {
+        const int r = p * kRowsPass + row_in;
+        if (r < kKeyTile) {
+          uint32_t w[8];
+          bytes_to_f16<FMT>(src[p].x, w[0], w[1]);
+          bytes_to_f16<FMT>(src[p].y, w[2], w[3]);
+          bytes_to_f16<FMT>(src[p].z, w[4], w[5]);
+          bytes_to_f16<FMT>(src[p].w, w[6], w[7]);
+          uint8_t *dst = smem + tile_base + (col >> 2) * (kKeyTile * 128) + r * 128;
+          const int c0 = (col & 3) * 2;
+          *reinterpret_cast<uint4 *>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4 *>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+    };
+    places(0);
+    scales(0);
+    load(kcol, kr);
+    load(vcol, vr);
+    {  // W: the power of two at the first tile's largest value scale
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (vs[e] > 0.0f && vs[e] < INFINITY) top = max(top, __float_as_uint(vs[e]));
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (lane == 0) atomicMax(&C.scale_top, top & 0xFF800000u);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t wbits = *const_cast<volatile uint32_t *>(&C.scale_top);
+    const int wexp = wbits >= 0x00800000u ? static_cast<int>(wbits >> 23) - 127 : 0;
+    const float unscale = pow2(max(-126, min(126, -wexp)));
+    const float c_tile =
+        P.scale * kLog2e * pow2(-query_shift(*const_cast<volatile uint32_t *>(&C.query_top)));
+    asm volatile("bar.sync 2, 96;" ::: "memory");
+    if (lt == 0) *const_cast<volatile uint32_t *>(&C.scale_top) = __float_as_uint(1.0f / unscale);
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      ok = wait_warp(C, &C.k_empty[st], (i >> 1 & 1) ^ 1);
+      if (!ok) break;
+      store(Y::kK + st * Y::kTile, kr);
+      {
+        Vectors &V = vec[i % kVectorSlots];
+        float most = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = lt + e * kLoadThreads;
+          float kc = ks[e] * c_tile, v = vs[e];
+          const bool good = v > 0.0f && v < INFINITY, out = lost[e] || (v == 0.0f && r < kKeyTile && k_begin + i * kKeyTile + r < k_end);
+          if (!good && v != 0.0f) kc = __uint_as_float(0x7FC00000u);
+          if (good) most = fmaxf(most, v);
+          v = good ? v * unscale : 1.0f;
+          const uint32_t dead = __ballot_sync(0xFFFFFFFFu, out);
+          if (r < kKeyTile) {
+            V.kc[r] = out ? 0.0f : kc;
+            V.vr[r] = v;
+            if (lane == 0) V.dead[r >> 5] = dead;
+          }
+        }
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+        if (lane == 0) V.top[warp - 8] = top ? log2f(__uint_as_float(top) * unscale) : -INFINITY;
+      }
+      mbar_arrive(&C.vec_full[i % kVectorSlots]);
+      fence_proxy_async_smem();
+      mbar_arrive(&C.k_full[st]);
+      places(i + 1);
+      scales(i + 1);
+      load(kcol, kr);
+      ok = wait_warp(C, &C.v_empty[st], (i >> 1 & 1) ^ 1);
+      if (!ok) break;
+      store(Y::kV + st * Y::kTile, vr);
+      fence_proxy_async_smem();
+      mbar_arrive(&C.v_full[st]);
+      load(vcol, vr);
+    }
+    if (P.status && (bad || !ok)) atomicOr(P.status, static_cast<int>(bad | (ok ? 0u : SV_DATA_COPY_TIMEOUT)));
+  } else {
+    // -------------------------------------------------------------------
+    // the products
+    // -------------------------------------------------------------------
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (lane == 0) {
+      const uint32_t tmem = C.tmem, base = smem_addr(smem);
+      constexpr uint32_t kScores = product(kKeyTile, false), kOutputs = product(D, true);
+      auto scores = [&](int t, int st) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t at = (kk >> 2) * (kRowsTile * 128) + (kk & 3) * 32;
+          mma_ss(tmem + t * 128, operand(base + Y::kQ + t * Y::kTile + at, 16),
+                 operand(base + Y::kK + st * Y::kTile + at, 16), kScores, kk > 0);
+        }
+        mma_commit(&C.s_full[t]);
+      };
+      auto outputs = [&](int t, int st, bool add) {
+#pragma unroll
+        for (int kk = 0; kk < kKeyTile / 16; ++kk)
+          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                 operand(base + Y::kV + st * Y::kTile + kk * 2048, kKeyTile * 128), kOutputs, add || kk > 0);
+      };
+      bool ok = wait(C, &C.k_full[0], 0);
+      if (ok) {
+        fence_after();
+        for (int t = 0; t < tiles; ++t) scores(t, 0);
+        mma_commit(&C.k_empty[0]);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const int st = i & 1, sn = st ^ 1;
+        ok = wait(C, &C.v_full[st], i >> 1 & 1);
+        for (int t = 0; ok && t < tiles; ++t) {
+          ok = wait(C, &C.p_full[t], i & 1);
+          if (!ok) break;
+          fence_after();
+          outputs(t, st, i > 0);
+          if (t == tiles - 1) mma_commit(&C.v_empty[st]);
+          if (i + 1 < n) {
+            if (t == 0) {
+              ok = wait(C, &C.k_full[sn], (i + 1) >> 1 & 1);
+              if (!ok) break;
+              fence_after();
+            }
+            scores(t, sn);
+            if (t == tiles - 1) mma_commit(&C.k_empty[sn]);
+          }
+        }
+      }
+      // (after a wait that gave up too: the products in flight end before the memory goes)
+      mma_commit(&C.done);
+      const uint64_t began = now_ns();
+      while (!mbar_try_wait(&C.done, 0) && now_ns() - began < kWaitNs) {
+      }
+    }
+    __syncwarp();
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  if (warp == 11) tmem_free(C.tmem, 512);
+}
+
+template <int D, int FMT>
+cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(L.tensor_tiles * p.c.num_kv_heads * L.prefix_splits));
+  cfg.blockDim = dim3(kPrefixThreads);
+  cfg.dynamicSmemBytes = Smem<D>::kBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
+  return cudaLaunchKernelEx(&cfg, prefix_kernel<D, FMT>, p, L);
+}
+template <int D, int FMT>
+cudaError_t enable() {
+  return cudaFuncSetAttribute(prefix_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+}
+
+}  // namespace
+
+cudaError_t enable_prefix_kernels() {
+  cudaError_t e;
+  if ((e = enable<128, SV_CACHE_INT8>()) != cudaSuccess || (e = enable<128, SV_CACHE_E4M3>()) != cudaSuccess ||
+      (e = enable<64, SV_CACHE_INT8>()) != cudaSuccess)
+    return e;
+  return enable<64, SV_CACHE_E4M3>();
+}
+
+int prefix_row_tile() { return 2 * kRowsTile; }
+int prefix_key_tile() { return kKeyTile; }
+
+cudaError_t launch_prefix(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
+  const bool i8 = p.c.format == SV_CACHE_INT8;
+  if (p.c.head_dim == 128) return i8 ? launch<128, SV_CACHE_INT8>(p, L, stream) : launch<128, SV_CACHE_E4M3>(p, L, stream);
+  return i8 ? launch<64, SV_CACHE_INT8>(p, L, stream) : launch<64, SV_CACHE_E4M3>(p, L, stream);
+}
+
+}  // namespace sv
