@@ -149,7 +149,7 @@ sv_status spec_verify_check_kv_args(const spec_verify_config *c, const spec_veri
   if (a->dtype != SV_F32 && a->dtype != SV_BF16) return fail(SV_ERR_INVALID_ARG, "bad dtype");
   if (a->reserved) return fail(SV_ERR_INVALID_ARG, "reserved must be 0");
   if ((st = check_cache(a->cache)) != SV_OK) return st;
-  if (a->num_tokens > INT_MAX / a->cache.num_kv_heads / 2)
+  if (a->num_tokens > INT_MAX / a->cache.num_kv_heads / 16)  // (two sides of up to eight threads a row)
     return fail(SV_ERR_UNSUPPORTED, "too many tokens for one call");
   if (a->num_tokens == 0) return SV_OK;
   if (!a->key || !a->value) return fail(SV_ERR_INVALID_ARG, "key or value is NULL");
