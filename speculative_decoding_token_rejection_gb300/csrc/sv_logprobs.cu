@@ -8,17 +8,18 @@
 // neither rescales nor waits for another thread.  Then
 //   log p = (logit - reference) / T - ln z,   entropy = ln z - ln 2 zx / z.
 //
-// The K largest come from block maxima: a block is 512 bytes of the row, one
-// 16-byte vector a lane, and its largest key takes one warp reduction.  Order
+// The K largest come from block maxima: a block is 2 KB of the row, four
+// 16-byte vectors a lane, and its largest key takes one warp reduction.  Order
 // blocks by (largest key, lower block first).  Every element of a block that
 // is not among the first K has K elements before it in the order (larger
 // value, lower index first) -- the K blocks' maxima -- so the K largest
 // elements lie in those K blocks, whatever ties there are.  They are read
-// again (from L2), K * 512 bytes a row.
+// again (from L2, K * 2 KB a row); elements that reach the last chosen block's
+// maximum -- a few more than K, unless there are many ties -- are ranked by
+// counting.
 //
 // Bound by HBM: the row is read once, 512 requests' committed tokens (2641
-// rows of 151936 bf16 logits) are 0.80 GB.  About seven instructions an element, one
-// of them an exponential.
+// rows of 151936 bf16 logits) are 0.80 GB.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -29,8 +30,10 @@
 namespace sv {
 namespace {
 
-constexpr int kMaxBlocks = 2048;  // block maxima that a CTA keeps; longer chunks have longer blocks
-constexpr int kUnroll = 4;        // vectors in flight per thread
+constexpr int kUnroll = 4;        // vectors of a lane in a group: a group is 2 KB, and a block one group
+constexpr int kGroup = 32 * kUnroll;
+constexpr int kMaxBlocks = 2048;  // block maxima that a CTA keeps; above 4 MB of row a CTA, blocks are several groups
+constexpr int kCandidates = 256;  // ranked by counting, one a thread; more (ties) are sorted into lists
 constexpr int kMaxCluster = 8;
 constexpr float kRaiseBy = 16.0f;
 constexpr float kLog2E = 1.4426950408889634f;
@@ -44,10 +47,12 @@ struct Sums {
 struct LogprobsSmem {
   unsigned long long lists[kWarps][SV_MAX_TOP_LOGPROBS];  // the warps' largest (key, lower index first)
   unsigned long long best[SV_MAX_TOP_LOGPROBS];           // the CTA's, read by the cluster's first
+  unsigned long long candidates[kCandidates];
   Sums warp_sums[kWarps], sums;
-  uint32_t block_key[kMaxBlocks];
+  alignas(16) uint32_t block_key[kMaxBlocks];
   int chosen[SV_MAX_TOP_LOGPROBS];
   uint32_t floor_key;  // key of the last chosen block
+  int count;           // candidates
 };
 
 __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
@@ -189,77 +194,105 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
 
   // ---- the pass over this CTA's vectors ----
   const int nv = row.vectors();
-  const int chunk = ((nv + C - 1) / C + 31) & ~31;  // whole warps' worth
-  const int v0 = rank * chunk, v1 = min(nv, v0 + chunk);
-  const int steps = v1 > v0 ? (v1 - v0 + 31) / 32 : 0;                 // of 32 vectors
-  const int per_block = (steps + kMaxBlocks - 1) / kMaxBlocks;         // steps a block (1 for all but huge rows)
-  const int blocks = steps ? (steps + per_block - 1) / per_block : 0;
+  const int chunk = (nv + C - 1) / C + kGroup - 1 & ~(kGroup - 1);
+  const int v0 = static_cast<int>(min(static_cast<int64_t>(nv), static_cast<int64_t>(rank) * chunk));
+  const int v1 = min(nv, v0 + chunk);
+  const int groups = (v1 - v0 + kGroup - 1) / kGroup;
+  const int per_block = max(1, (groups + kMaxBlocks - 1) / kMaxBlocks);
+  const int blocks = (groups + per_block - 1) / per_block;
+  if (P.K) {
+    if (per_block > 1)
+      for (int b = tid; b < blocks; b += kThreads) sm.block_key[b] = 0;
+    if (tid < 4 && blocks + tid < kMaxBlocks) sm.block_key[blocks + tid] = 0;  // (read four at a time)
+    if (tid == 0) sm.count = 0;
+    if (per_block > 1) __syncthreads();
+  }
+  // groups [g_lo, g_hi) hold full vectors only
+  const int g_lo = row.shift && rank == 0 ? 1 : 0;
+  const int g_hi = (min(v1, (P.V + row.shift) / Row<BF16>::kPer) - v0) / kGroup;
+  const uint4 *const mine_v = reinterpret_cast<const uint4 *>(row.base) + v0 + lane;
+  constexpr uint32_t kNone = BF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  auto fetch = [&](int gi, uint4 raw[kUnroll]) {
+    if (gi >= g_lo && gi < g_hi) {
+      const uint4 *p = mine_v + static_cast<int64_t>(gi) * kGroup;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) raw[u] = ld_stream_u4(p + u * 32);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int v = v0 + gi * kGroup + u * 32 + lane;
+        raw[u] = make_uint4(kNone, kNone, kNone, kNone);
+        if (gi < groups && v < v1) raw[u] = row.load(v);
+      }
+    }
+  };
   Sums sum{-INFINITY, 0.0f, 0.0f, 0u, 0u};
   Pair z = pair(0.0f, 0.0f), zx = z;
-  float above_f = 0.0f;
-  for (int b0 = warp; b0 < blocks; b0 += kWarps * kUnroll) {
-    uint32_t key[kUnroll];
+  bool bad = false;
+  uint4 next[kUnroll];
+  fetch(warp, next);
+  for (int gi = warp; gi < groups; gi += kWarps) {
+    uint4 raw[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) key[u] = 0;
-    for (int p = 0; p < per_block; ++p) {
-      uint4 raw[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int b = b0 + u * kWarps, v = v0 + (b * per_block + p) * 32 + lane;
-        raw[u] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
-        if (!BF16) raw[u] = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-        if (b < blocks && v < v1) raw[u] = row.load(v);
-      }
+    for (int u = 0; u < kUnroll; ++u) raw[u] = next[u];
+    fetch(gi + kWarps, next);
+    float top;
+    if (BF16) {
+      uint32_t t2 = raw[0].x, n2 = 0;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const uint4 &r = raw[u];
-        float top;
-        if (BF16) {
-          const uint32_t t2 = max_nan_bf16x2(max_nan_bf16x2(r.x, r.y), max_nan_bf16x2(r.z, r.w));
-          top = max_nan(__uint_as_float(t2 << 16), __uint_as_float(t2 & 0xFFFF0000u));
-          const uint32_t n2 = add_bf16x2(add_bf16x2(above_bf16x2(r.x, mine2), above_bf16x2(r.y, mine2)),
-                                         add_bf16x2(above_bf16x2(r.z, mine2), above_bf16x2(r.w, mine2)));
-          above_f += __uint_as_float(n2 << 16) + __uint_as_float(n2 & 0xFFFF0000u);
-        } else {
-          top = max_nan(max_nan(word_of(r, 0), word_of(r, 1)), max_nan(word_of(r, 2), word_of(r, 3)));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) above_f += word_of(r, e) > mine ? 1.0f : 0.0f;
-        }
-        if (!(top < INFINITY)) sum.bad = 1;  // NaN or +inf
-        key[u] = max(key[u], ordered_bits(top));
-        if ((top - sum.ref) * c > kRaiseBy) {  // (seldom after the first)
-          if (top > -INFINITY) {
-            sum.z = lo(z) + hi(z);
-            sum.zx = lo(zx) + hi(zx);
-            rebase(sum, top, c);
-            z = pair(sum.z, 0.0f);
-            zx = pair(sum.zx, 0.0f);
-          }
-        }
-        const Pair neg = pair(-sum.ref, -sum.ref), cc = pair(c, c);
-        if (sum.ref > -INFINITY) {
-#pragma unroll
-          for (int e = 0; e < Row<BF16>::kPer; e += 2) {
-            Pair d = mul2(add2(pair(element<BF16>(r, e), element<BF16>(r, e + 1)), neg), cc);
-            // (a masked entry: its 2^d is 0, and so is 0 * d)
-            d = pair(fmaxf(lo(d), -200.0f), fmaxf(hi(d), -200.0f));
-            const Pair w = pair(exp2_approx(lo(d)), exp2_approx(hi(d)));
-            z = add2(z, w);
-            zx = fma2(w, d, zx);
-          }
-        }
+        const uint4 &v = raw[u];
+        t2 = max_nan_bf16x2(t2, max_nan_bf16x2(max_nan_bf16x2(v.x, v.y), max_nan_bf16x2(v.z, v.w)));
+        n2 = add_bf16x2(n2, add_bf16x2(add_bf16x2(above_bf16x2(v.x, mine2), above_bf16x2(v.y, mine2)),
+                                       add_bf16x2(above_bf16x2(v.z, mine2), above_bf16x2(v.w, mine2))));
       }
+      top = max_nan(__uint_as_float(t2 << 16), __uint_as_float(t2 & 0xFFFF0000u));
+      // (counts of up to 16 a half, exact)
+      sum.above += static_cast<uint32_t>(__uint_as_float(n2 << 16) + __uint_as_float(n2 & 0xFFFF0000u));
+    } else {
+      top = word_of(raw[0], 0);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          top = max_nan(top, word_of(raw[u], e));
+          sum.above += word_of(raw[u], e) > mine ? 1u : 0u;
+        }
     }
+    const uint32_t key = ordered_bits(top);
+    bad |= !(top < INFINITY);  // +inf, or NaN, which the maxima hand on (and which no key orders)
     if (P.K) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const uint32_t k = __reduce_max_sync(0xFFFFFFFFu, key[u]);
-        if (lane == 0 && b0 + u * kWarps < blocks) sm.block_key[b0 + u * kWarps] = k;
+      const uint32_t k = __reduce_max_sync(0xFFFFFFFFu, key);
+      if (lane == 0) {
+        if (per_block == 1)
+          sm.block_key[gi] = k;
+        else
+          atomicMax(&sm.block_key[gi / per_block], k);
       }
     }
-    sum.above += static_cast<uint32_t>(above_f);
-    above_f = 0.0f;
+    if ((top - sum.ref) * c > kRaiseBy && top > -INFINITY) {  // (seldom after the first)
+      sum.z = lo(z) + hi(z);
+      sum.zx = lo(zx) + hi(zx);
+      rebase(sum, top, c);
+      z = pair(sum.z, 0.0f);
+      zx = pair(sum.zx, 0.0f);
+    }
+    if (sum.ref > -INFINITY) {
+      const Pair neg = pair(-sum.ref, -sum.ref), cc = pair(c, c);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int e = 0; e < Row<BF16>::kPer; e += 2) {
+          Pair d = mul2(add2(pair(element<BF16>(raw[u], e), element<BF16>(raw[u], e + 1)), neg), cc);
+          // (a masked entry: its 2^d is 0, and so is 0 * d)
+          d = pair(fmaxf(lo(d), -200.0f), fmaxf(hi(d), -200.0f));
+          const Pair w = pair(exp2_approx(lo(d)), exp2_approx(hi(d)));
+          z = add2(z, w);
+          zx = fma2(w, d, zx);
+        }
+    }
   }
+  sum.bad = bad;
   sum.z = lo(z) + hi(z);
   sum.zx = lo(zx) + hi(zx);
 #pragma unroll
@@ -277,91 +310,128 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
 
   // ---- the K blocks with the largest maxima, then their K largest elements ----
   const int K = P.K, kb = min(K, blocks);
-  if (warp == 0) {
-    if (lane == 0) {
-      Sums a = sm.warp_sums[0];
+  if (warp == 0) {  // (lanes 8 and up hold nothing)
+    Sums a = lane < kWarps ? sm.warp_sums[lane] : Sums{-INFINITY, 0.0f, 0.0f, 0u, 0u};
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) merge(a, sm.warp_sums[w], c);
-      sm.sums = a;
+    for (int b = kWarps / 2; b; b >>= 1) {
+      Sums o;
+      o.ref = __shfl_xor_sync(0xFFFFFFFFu, a.ref, b);
+      o.z = __shfl_xor_sync(0xFFFFFFFFu, a.z, b);
+      o.zx = __shfl_xor_sync(0xFFFFFFFFu, a.zx, b);
+      o.above = __shfl_xor_sync(0xFFFFFFFFu, a.above, b);
+      o.bad = __shfl_xor_sync(0xFFFFFFFFu, a.bad, b);
+      merge(a, o, c);
     }
-    if (K) {
-      // a lane keeps blocks lane, lane + 32, ...; its best is found again when it has been taken
-      auto lane_best = [&](uint32_t &key, uint32_t &block) {
-        key = 0;
-        block = 0xFFFFFFFFu;
-        for (int b = lane; b < blocks; b += 32)
-          if (sm.block_key[b] > key) {  // (the lower block stays among equal keys)
-            key = sm.block_key[b];
-            block = b;
+    if (lane == 0) sm.sums = a;
+  }
+  if (K) {
+    for (int b = tid; b < blocks; b += kThreads) {
+      const uint32_t key = sm.block_key[b];
+      int before = 0;
+      for (int j = 0; j < blocks; j += 4) {
+        const uint4 k = *reinterpret_cast<const uint4 *>(&sm.block_key[j]);
+        before += (k.x > key || (k.x == key && j < b)) + (k.y > key || (k.y == key && j + 1 < b)) +
+                  (k.z > key || (k.z == key && j + 2 < b)) + (k.w > key || (k.w == key && j + 3 < b));
+      }
+      if (before < kb) sm.chosen[before] = b;
+      if (before == K - 1) sm.floor_key = key;
+    }
+    __syncthreads();
+    const uint32_t floor_key = kb == K ? sm.floor_key : 0u;
+    // elements that reach the floor
+    auto fetch_again = [&](int gi, int u) {
+      const int v = v0 + gi * kGroup + u * 32 + lane;
+      return gi < groups && v < v1 ? row.load(v) : make_uint4(kNone, kNone, kNone, kNone);
+    };
+    auto reaching = [&](int gi, int u, const uint4 &r) {  // bit e: element e of the vector is the row's and reaches it
+      const int v = v0 + gi * kGroup + u * 32 + lane, x0 = v * Row<BF16>::kPer - row.shift;
+      uint32_t left = 0;
+      if (gi < groups && v < v1) {
+#pragma unroll
+        for (int e = 0; e < Row<BF16>::kPer; ++e)
+          if (x0 + e >= 0 && x0 + e < P.V && ordered_bits(element<BF16>(r, e)) >= floor_key) left |= 1u << e;
+      }
+      return left;
+    };
+    for (int k = warp; k < kb; k += kWarps)
+      for (int p = 0; p < per_block; ++p) {
+        const int gi = sm.chosen[k] * per_block + p;
+        uint4 r[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) r[u] = fetch_again(gi, u);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const uint32_t left = reaching(gi, u, r[u]);
+          if (left) {
+            int to = atomicAdd(&sm.count, __popc(left));
+            const int x0 = (v0 + gi * kGroup + u * 32 + lane) * Row<BF16>::kPer - row.shift;
+#pragma unroll
+            for (int e = 0; e < Row<BF16>::kPer; ++e)
+              if (left >> e & 1u) {
+                if (to < kCandidates) sm.candidates[to] = pack_key(element<BF16>(r[u], e), static_cast<uint32_t>(x0 + e));
+                ++to;
+              }
           }
-      };
-      uint32_t key, block;
-      lane_best(key, block);
-      for (int k = 0; k < kb; ++k) {
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, key);
-        const uint32_t first = __reduce_min_sync(0xFFFFFFFFu, key == top ? block : 0xFFFFFFFFu);
-        if (block == first && key == top) {
-          sm.chosen[k] = static_cast<int>(first);
-          if (k == kb - 1) sm.floor_key = top;
-          sm.block_key[first] = 0;
-          lane_best(key, block);
         }
-        __syncwarp();
+      }
+    if (tid < SV_MAX_TOP_LOGPROBS) sm.best[tid] = 0;
+    __syncthreads();
+    const int count = sm.count;
+    if (count <= kCandidates) {  // (their order in the array does not matter: keys are all different)
+      if (tid < count) {
+        const unsigned long long key = sm.candidates[tid];
+        int before = 0;
+        for (int j = 0; j < count; ++j) before += sm.candidates[j] > key;
+        if (before < K) sm.best[before] = key;
+      }
+    } else {
+      // many ties: every warp sorts its blocks' elements into a list of K (lane k holds the k-th), the lists are merged
+      unsigned long long list = 0;
+      for (int k = warp; k < kb; k += kWarps)
+        for (int p = 0; p < per_block; ++p)
+          for (int u = 0; u < kUnroll; ++u) {
+            const int gi = sm.chosen[k] * per_block + p;
+            const uint4 r = fetch_again(gi, u);
+            uint32_t left = reaching(gi, u, r);
+            const int x0 = (v0 + gi * kGroup + u * 32 + lane) * Row<BF16>::kPer - row.shift;
+            for (;;) {
+              unsigned long long best = 0;
+              int at_e = 0;
+#pragma unroll
+              for (int e = 0; e < Row<BF16>::kPer; ++e) {
+                const unsigned long long key = pack_key(element<BF16>(r, e), static_cast<uint32_t>(x0 + e));
+                if ((left >> e & 1u) && key > best) {
+                  best = key;
+                  at_e = e;
+                }
+              }
+              const unsigned long long top = warp_max64(best);
+              if (top <= __shfl_sync(0xFFFFFFFFu, list, K - 1)) break;  // (0 too: nothing left)
+              if (best == top) left &= ~(1u << at_e);
+              const int pos = __popc(__ballot_sync(0xFFFFFFFFu, list > top));
+              const unsigned long long before = __shfl_up_sync(0xFFFFFFFFu, list, 1);
+              list = lane > pos ? before : lane == pos ? top : list;
+            }
+          }
+      if (lane < K) sm.lists[warp][lane] = list;
+      __syncthreads();
+      if (warp == 0) {
+        // lane l takes list l % 8 from its (l / 8)-th entry on, every fourth: K rounds pick the largest head
+        int at_l = lane >> 3;
+        const unsigned long long *mine_l = sm.lists[lane & 7];
+        unsigned long long head = at_l < K ? mine_l[at_l] : 0ull;
+        for (int k = 0; k < K; ++k) {
+          const unsigned long long top = warp_max64(head);
+          if (lane == 0) sm.best[k] = top;
+          if (head == top && top) {
+            at_l += 4;
+            head = at_l < K ? mine_l[at_l] : 0ull;
+          }
+        }
       }
     }
   }
   __syncthreads();
-  if (K) {
-    unsigned long long mineL = 0;  // lane k: the warp's k-th largest
-    const uint32_t floor_key = kb == K ? sm.floor_key : 0u;
-    for (int k = warp; k < kb; k += kWarps) {
-      const int b = sm.chosen[k];
-      for (int p = 0; p < per_block; ++p) {
-        const int v = v0 + (b * per_block + p) * 32 + lane;
-        const uint4 r = v < v1 ? row.load(v) : make_uint4(0, 0, 0, 0);
-        const int x0 = v * Row<BF16>::kPer - row.shift;
-        uint32_t left = 0;  // elements that may still be taken
-#pragma unroll
-        for (int e = 0; e < Row<BF16>::kPer; ++e)
-          if (v < v1 && x0 + e >= 0 && x0 + e < P.V && ordered_bits(element<BF16>(r, e)) >= floor_key) left |= 1u << e;
-        for (;;) {
-          unsigned long long best = 0;
-          int at_e = 0;
-#pragma unroll
-          for (int e = 0; e < Row<BF16>::kPer; ++e) {
-            const unsigned long long key = pack_key(element<BF16>(r, e), static_cast<uint32_t>(x0 + e));
-            if ((left >> e & 1u) && key > best) {
-              best = key;
-              at_e = e;
-            }
-          }
-          const unsigned long long top = warp_max64(best);
-          if (top <= __shfl_sync(0xFFFFFFFFu, mineL, K - 1)) break;  // (0 too: nothing left)
-          if (best == top) left &= ~(1u << at_e);
-          const int pos = __popc(__ballot_sync(0xFFFFFFFFu, mineL > top));
-          const unsigned long long before = __shfl_up_sync(0xFFFFFFFFu, mineL, 1);
-          mineL = lane > pos ? before : lane == pos ? top : mineL;
-        }
-      }
-    }
-    if (lane < K) sm.lists[warp][lane] = mineL;
-    __syncthreads();
-    if (warp == 0) {
-      // lane l takes list l % 8 from its (l / 8)-th entry on, every fourth: K rounds pick the largest head
-      int next = lane >> 3;
-      const unsigned long long *list = sm.lists[lane & 7];
-      unsigned long long head = next < K ? list[next] : 0ull;
-      for (int k = 0; k < K; ++k) {
-        const unsigned long long top = warp_max64(head);
-        if (lane == 0) sm.best[k] = top;
-        if (head == top && top) {
-          next += 4;
-          head = next < K ? list[next] : 0ull;
-        }
-      }
-    }
-    __syncthreads();
-  }
 
   // ---- the cluster's first CTA joins and writes ----
   if (C > 1) cluster_sync();
@@ -377,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
       b.bad = ld_dsmem_u32(src + 16);
       merge(a, b, c);
     }
-    const bool bad = a.bad || a.ref == -INFINITY;
+    bad = a.bad || a.ref == -INFINITY;
     const float nan = __uint_as_float(0x7FC00000u), lnz = logf(a.z);
     // the k-th largest of the CTAs' lists (each in order): lane l takes CTA l % C from entry l / C on, every (32 / C)-th
     unsigned long long taken = 0;
