@@ -620,6 +620,7 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   L.own_splits = std::max(1, L.own_splits);
   if (p.prefix >= kTensorKeys && L.rows >= kTensorRows) {
     L.tensor_tiles = ceil_div(L.rows, prefix_row_tile());
+    L.image_tiles = ceil_div(p.prefix, prefix_key_tile());
     cut_tensor(static_cast<int64_t>(p.c.num_kv_heads) * L.tensor_tiles, p.prefix, num_sms, L.prefix_splits,
                L.prefix_chunk);
     bound += L.prefix_splits;
@@ -631,9 +632,12 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   L.slots = L.prefix_splits + L.own_splits;
   L.qvec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0;
   const int64_t rows = static_cast<int64_t>(L.rows) * p.c.num_kv_heads;
-  if (bytes) *bytes = bound <= 1 ? 0 : ((rows * bound * 8 + 15) & ~int64_t{15}) + rows * bound * p.c.head_dim * 4;
-  L.part_ml = static_cast<float2 *>(p.workspace);
-  L.part_o = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + ((rows * L.slots * 8 + 15) & ~int64_t{15}));
+  // the workspace: the prefix's tiles, then M and l, then O
+  const int64_t image = static_cast<int64_t>(L.image_tiles) * p.c.num_kv_heads * prefix_key_tile() * p.c.head_dim * 4;
+  if (bytes) *bytes = bound <= 1 ? 0 : image + ((rows * bound * 8 + 15) & ~int64_t{15}) + rows * bound * p.c.head_dim * 4;
+  L.image = static_cast<uint8_t *>(p.workspace);
+  L.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(p.workspace) + image);
+  L.part_o = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + image + ((rows * L.slots * 8 + 15) & ~int64_t{15}));
   return L;
 }
 

@@ -34,6 +34,8 @@ struct AttendPlan {
   int32_t own_splits, own_chunk, own_tiles;
   int32_t slots;          // 1: results go straight to the output
   bool qvec;              // q rows allow 16-byte loads
+  int32_t image_tiles;    // tiles of prefix_key_tile() keys of the prefix
+  uint8_t *image;         // the prefix as f16 tiles: [num_kv_heads][image_tiles][K, V]
   float *part_o;          // [rows * num_kv_heads][slots][D], row = token * Hq + query head
   float2 *part_ml;        // [rows * num_kv_heads][slots]: M, l
 };

@@ -4,13 +4,19 @@
 // All requests' rows of a kv head meet the same prefix keys, so the work is two
 // matrix products of thousands of rows and is bound by the tensor cores and
 // what feeds them: 4 * head_dim operations a (row, key) pair, one exponential
-// each.  A CTA takes 256 rows (two accumulator tiles of 128) of one kv head
-// and a range of keys, 128 at a time:
+// each.  The prefix's bytes become f16 (exact) once for the whole call: a small
+// kernel writes the K and V tiles of 128 keys to the workspace in the very
+// order the products want them in shared memory, so a tile is one bulk copy.
+// (Turned into f16 by every CTA for itself, the tiles took three warps 6000
+// cycles each, most of it page look-ups and shared-memory stores, against 2050
+// of the products: 64 requests x 5 tokens over 8192 keys 100 us.)
+// A CTA takes 256 rows (two accumulator tiles of 128) of one kv head and a
+// range of keys:
 //
 //   warps 0-3, 4-7  softmax of a row tile, a thread a row: reads S from tensor
 //                   memory, writes the weights back over it as f16
-//   warps 8-10      bytes to f16 (exact), global memory -> registers -> shared
-//                   memory, K and V two tiles deep
+//   warps 8, 9      the keys' factors, four tiles ahead
+//   warp 10         copies K and V tiles, two deep
 //   warp 11         issues S = Q K^T and O += P V (P from tensor memory)
 //
 // While one row tile's softmax runs, the tensor cores work for the other:
@@ -37,9 +43,8 @@ namespace {
 constexpr int kRowsTile = 128;  // rows of an accumulator tile
 constexpr int kKeyTile = 128;
 constexpr int kSoftmaxThreads = 256;
-constexpr int kLoadThreads = 96;
-constexpr int kPrefixThreads = kSoftmaxThreads + kLoadThreads + 32;
-constexpr int kPasses = (kKeyTile * 8 + kLoadThreads - 1) / kLoadThreads;  // 16-byte pieces of a thread, D = 128
+constexpr int kVectorThreads = 64;
+constexpr int kPrefixThreads = kSoftmaxThreads + kVectorThreads + 64;
 constexpr int kVectorSlots = 4;
 constexpr uint32_t kWaitPolls = 1u << 24;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -47,12 +52,12 @@ constexpr float kRaise = 8;
 
 struct alignas(16) Vectors {  // of one key tile; read 16 bytes at a time
   float kc[kKeyTile], vr[kKeyTile];
-  float top[3];      // log2 of a load warp's largest value scale / W
   uint32_t dead[4];  // keys left out, a bit each
+  float top[2];      // log2 of the largest value scale / W, of keys 0-31 and 64-95, and of the others
 };
 
 struct Control {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], vec_full[kVectorSlots], s_full[2], p_full[2], done;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], vec_full[kVectorSlots], vec_empty[kVectorSlots], s_full[2], p_full[2], done;
   uint32_t tmem, query_top, scale_top, abort;
 };
 
@@ -171,7 +176,44 @@ __device__ __forceinline__ bool wait_warp(Control &C, uint64_t *bar, uint32_t pa
   return __all_sync(0xFFFFFFFFu, wait(C, bar, parity));
 }
 
+// The prefix's K and V as f16 tiles of 128 keys, each in the order of its
+// shared memory: 64 dimensions after 64, rows of 128 bytes, 16-byte columns
+// exchanged by row % 8.  Keys that are not there are zeros.
 template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads) unpack_kernel(const AttendParams P, const AttendPlan L) {
+  pdl_enter();
+  constexpr int kCols = D / 16;
+  const int tile = blockIdx.x, h = blockIdx.y, side = blockIdx.z, col = threadIdx.x % kCols;
+  const uint8_t *const base = static_cast<const uint8_t *>(side ? P.c.v : P.c.k) + h * P.c.head_stride + col * 16;
+  uint8_t *const out = L.image + ((static_cast<int64_t>(h) * L.image_tiles + tile) * 2 + side) * (kKeyTile * D * 2);
+  uint4 raw[kKeyTile * kCols / kThreads];
+#pragma unroll
+  for (int p = 0; p < kKeyTile * kCols / kThreads; ++p) {
+    const int r = p * (kThreads / kCols) + threadIdx.x / kCols, k = tile * kKeyTile + r;
+    raw[p] = make_uint4(0, 0, 0, 0);
+    if (k < P.prefix) {
+      const int x = div_by(k, L.page), page = P.tables[x];
+      if (page >= 0 && page < P.c.num_blocks)
+        raw[p] = ld_stream_u4(reinterpret_cast<const uint4 *>(
+            base + page * P.c.block_stride + (k - x * P.c.block_size) * P.c.token_stride));
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kKeyTile * kCols / kThreads; ++p) {
+    const int r = p * (kThreads / kCols) + threadIdx.x / kCols;
+    uint32_t w[8];
+    bytes_to_f16<FMT>(raw[p].x, w[0], w[1]);
+    bytes_to_f16<FMT>(raw[p].y, w[2], w[3]);
+    bytes_to_f16<FMT>(raw[p].z, w[4], w[5]);
+    bytes_to_f16<FMT>(raw[p].w, w[6], w[7]);
+    uint8_t *dst = out + (col >> 2) * (kKeyTile * 128) + r * 128;
+    const int c0 = (col & 3) * 2;
+    *reinterpret_cast<uint4 *>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <int D>
 __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendParams P, const AttendPlan L) {
   pdl_enter();
   extern __shared__ uint8_t raw[];
@@ -192,14 +234,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&C.k_full[i], kLoadThreads);
+      mbar_init(&C.k_full[i], 1);
       mbar_init(&C.k_empty[i], 1);
-      mbar_init(&C.v_full[i], kLoadThreads);
+      mbar_init(&C.v_full[i], 1);
       mbar_init(&C.v_empty[i], 1);
       mbar_init(&C.s_full[i], 1);
       mbar_init(&C.p_full[i], kRowsTile);
     }
-    for (int i = 0; i < kVectorSlots; ++i) mbar_init(&C.vec_full[i], kLoadThreads);
+    for (int i = 0; i < kVectorSlots; ++i) {
+      mbar_init(&C.vec_full[i], kVectorThreads);
+      mbar_init(&C.vec_empty[i], 4 * tiles);
+    }
     mbar_init(&C.done, 1);
     C.query_top = C.scale_top = C.abort = 0;
     fence_mbar_init();
@@ -313,7 +358,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int j = 0; j < 32; j += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])));
-      const float over = fmaxf(fmaxf(V.top[0], V.top[1]), V.top[2]);
+      const float over = fmaxf(V.top[0], V.top[1]);
       const bool raise = top + over > m + kRaise || (m == -INFINITY && top > -INFINITY);
       if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
         float most = -INFINITY;
@@ -365,6 +410,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       tmem_wait_store();
       fence_before();
       mbar_arrive(&C.p_full[t]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C.vec_empty[i % kVectorSlots]);
     }
     // the partial result
     if (ok) ok = wait_warp(C, &C.done, 0);
@@ -390,80 +437,41 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       if (token >= 0) L.part_ml[at] = ok ? make_float2(m, lo(l) + hi(l)) : make_float2(-INFINITY, 0.0f);
     }
     fence_before();
-  } else if (warp < 11) {
+  } else if (warp < 10) {
     // -------------------------------------------------------------------
-    // bytes to f16 tiles
+    // the keys' factors: keys lt and lt + 64 of every tile
     // -------------------------------------------------------------------
-    constexpr int kCols = D / 16, kRowsPass = kLoadThreads / kCols, kP = (kKeyTile + kRowsPass - 1) / kRowsPass;
-    static_assert(kP <= kPasses, "pieces of a thread");
-    const int lt = tid - kSoftmaxThreads, col = lt % kCols, row_in = lt / kCols;
-    const uint8_t *const kcol = static_cast<const uint8_t *>(P.c.k) + h * P.c.head_stride + col * 16;
-    const uint8_t *const vcol = static_cast<const uint8_t *>(P.c.v) + h * P.c.head_stride + col * 16;
+    const int lt = tid - kSoftmaxThreads;
     const float *const kscale = P.c.k_scale + h * P.c.scale_head_stride;
     const float *const vscale = P.c.v_scale + h * P.c.scale_head_stride;
-    uint32_t unit[kP], bad = 0;
-    uint4 kr[kP], vr[kP];
+    uint32_t bad = 0;
     float ks[2], vs[2];
-    uint32_t lost[2];  // a key of the range whose page is outside the cache
-    auto places = [&](int i) {
+    bool in[2];  // a key of the range
+    int page[2];
+    auto key_of = [&](int i, int e) { return k_begin + i * kKeyTile + lt + e * kVectorThreads; };
+    auto pages = [&](int i) {
 #pragma unroll
-      for (int p = 0; p < kP; ++p) {
-        const int r = p * kRowsPass + row_in, k = k_begin + i * kKeyTile + r;
-        unit[p] = 0xFFFFFFFFu;
-        if (i < n && r < kKeyTile && k < k_end) {
-          const int x = div_by(k, L.page), page = P.tables[x];
-          if (page >= 0 && page < P.c.num_blocks)
-            unit[p] = static_cast<uint32_t>(
-                (page * P.c.block_stride + (k - x * P.c.block_size) * P.c.token_stride) >> 4);
-        }
-      }
+      for (int e = 0; e < 2; ++e) page[e] = i < n && key_of(i, e) < k_end ? P.tables[div_by(key_of(i, e), L.page)] : -1;
     };
-    auto load = [&](const uint8_t *base, uint4 dst[kP]) {
-#pragma unroll
-      for (int p = 0; p < kP; ++p)
-        dst[p] = unit[p] == 0xFFFFFFFFu ? make_uint4(0, 0, 0, 0)
-                                        : __ldg(reinterpret_cast<const uint4 *>(base + static_cast<uint64_t>(unit[p]) * 16));
-    };
-    auto scales = [&](int i) {  // keys lt and lt + 96 of the tile
+    auto scales = [&](int i) {  // of the tile whose pages are there
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = lt + e * kLoadThreads, k = k_begin + i * kKeyTile + r;
+        const int k = key_of(i, e);
+        in[e] = i < n && k < k_end;
         ks[e] = vs[e] = 0.0f;
-        lost[e] = 0;
-        if (i < n && r < kKeyTile && k < k_end) {
-          const int x = div_by(k, L.page), page = P.tables[x];
-          if (page >= 0 && page < P.c.num_blocks) {
-            const int64_t at = page * P.c.scale_block_stride + (k - x * P.c.block_size) * P.c.scale_token_stride;
-            ks[e] = kscale[at];
-            vs[e] = vscale[at];
-          } else {
-            bad = SV_DATA_BAD_SLOT;
-            lost[e] = 1;
-          }
+        if (in[e] && page[e] >= 0 && page[e] < P.c.num_blocks) {
+          const int64_t at = page[e] * P.c.scale_block_stride +
+                             (k - div_by(k, L.page) * P.c.block_size) * P.c.scale_token_stride;
+          ks[e] = kscale[at];
+          vs[e] = vscale[at];
+        } else if (in[e]) {
+          bad = SV_DATA_BAD_SLOT;
         }
       }
     };
-    auto store = [&](int tile_base, const uint4 src[kP]) {
-#pragma unroll
-      for (int p = 0; p < kP; ++p) {
-        const int r = p * kRowsPass + row_in;
-        if (r < kKeyTile) {
-          uint32_t w[8];
-          bytes_to_f16<FMT>(src[p].x, w[0], w[1]);
-          bytes_to_f16<FMT>(src[p].y, w[2], w[3]);
-          bytes_to_f16<FMT>(src[p].z, w[4], w[5]);
-          bytes_to_f16<FMT>(src[p].w, w[6], w[7]);
-          uint8_t *dst = smem + tile_base + (col >> 2) * (kKeyTile * 128) + r * 128;
-          const int c0 = (col & 3) * 2;
-          *reinterpret_cast<uint4 *>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4 *>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      }
-    };
-    places(0);
+    pages(0);
     scales(0);
-    load(kcol, kr);
-    load(vcol, vr);
+    pages(1);
     {  // W: the power of two at the first tile's largest value scale
       uint32_t top = 0;
 #pragma unroll
@@ -480,49 +488,63 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     const float unscale = pow2(max(-126, min(126, -wexp)));
     const float c_tile =
         P.scale * kLog2e * pow2(-query_shift(*const_cast<volatile uint32_t *>(&C.query_top)));
-    asm volatile("bar.sync 2, 96;" ::: "memory");
+    asm volatile("bar.sync 2, 64;" ::: "memory");
     if (lt == 0) *const_cast<volatile uint32_t *>(&C.scale_top) = __float_as_uint(1.0f / unscale);
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int st = i & 1;
-      ok = wait_warp(C, &C.k_empty[st], (i >> 1 & 1) ^ 1);
+      const int slot_v = i % kVectorSlots;
+      ok = wait_warp(C, &C.vec_empty[slot_v], (i / kVectorSlots & 1) ^ 1);
       if (!ok) break;
-      store(Y::kK + st * Y::kTile, kr);
-      {
-        Vectors &V = vec[i % kVectorSlots];
-        float most = 0.0f;
+      Vectors &V = vec[slot_v];
+      float most = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = lt + e * kLoadThreads;
-          float kc = ks[e] * c_tile, v = vs[e];
-          const bool good = v > 0.0f && v < INFINITY, out = lost[e] || (v == 0.0f && r < kKeyTile && k_begin + i * kKeyTile + r < k_end);
-          if (!good && v != 0.0f) kc = __uint_as_float(0x7FC00000u);
-          if (good) most = fmaxf(most, v);
-          v = good ? v * unscale : 1.0f;
-          const uint32_t dead = __ballot_sync(0xFFFFFFFFu, out);
-          if (r < kKeyTile) {
-            V.kc[r] = out ? 0.0f : kc;
-            V.vr[r] = v;
-            if (lane == 0) V.dead[r >> 5] = dead;
-          }
-        }
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
-        if (lane == 0) V.top[warp - 8] = top ? log2f(__uint_as_float(top) * unscale) : -INFINITY;
+      for (int e = 0; e < 2; ++e) {
+        const int r = lt + e * kVectorThreads;
+        float kc = ks[e] * c_tile, v = vs[e];
+        // (scale 0: a key whose page is outside the cache; keys behind the range are no row's)
+        const bool good = v > 0.0f && v < INFINITY, out = in[e] && v == 0.0f;
+        if (!good && v != 0.0f) kc = __uint_as_float(0x7FC00000u);
+        if (good) most = fmaxf(most, v);
+        const uint32_t dead = __ballot_sync(0xFFFFFFFFu, out);
+        V.kc[r] = out ? 0.0f : kc;
+        V.vr[r] = good ? v * unscale : 1.0f;
+        if (lane == 0) V.dead[r >> 5] = dead;
       }
-      mbar_arrive(&C.vec_full[i % kVectorSlots]);
-      fence_proxy_async_smem();
-      mbar_arrive(&C.k_full[st]);
-      places(i + 1);
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+      if (lane == 0) V.top[warp - 8] = top ? log2f(__uint_as_float(top) * unscale) : -INFINITY;
+      mbar_arrive(&C.vec_full[slot_v]);
       scales(i + 1);
-      load(kcol, kr);
-      ok = wait_warp(C, &C.v_empty[st], (i >> 1 & 1) ^ 1);
-      if (!ok) break;
-      store(Y::kV + st * Y::kTile, vr);
-      fence_proxy_async_smem();
-      mbar_arrive(&C.v_full[st]);
-      load(vcol, vr);
+      pages(i + 2);
     }
     if (P.status && (bad || !ok)) atomicOr(P.status, static_cast<int>(bad | (ok ? 0u : SV_DATA_COPY_TIMEOUT)));
+  } else if (warp == 10) {
+    // -------------------------------------------------------------------
+    // copies
+    // -------------------------------------------------------------------
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (lane == 0) {
+      const uint8_t *image = L.image + (static_cast<int64_t>(h) * L.image_tiles + k_begin / kKeyTile) * 2 * Y::kTile;
+      int issued = 0;  // K and V tiles alternate
+      for (; issued < 2 * n; ++issued) {
+        const int i = issued >> 1, st = i & 1;
+        const bool v = issued & 1;
+        if (!wait(C, v ? &C.v_empty[st] : &C.k_empty[st], (i >> 1 & 1) ^ 1)) break;
+        uint64_t *full = v ? &C.v_full[st] : &C.k_full[st];
+        mbar_arrive_expect_tx(full, Y::kTile);
+        bulk_g2s(smem + (v ? Y::kV : Y::kK) + st * Y::kTile, image + static_cast<int64_t>(issued) * Y::kTile, Y::kTile, full);
+      }
+      // (after a wait that gave up: the last copies end before the shared memory goes)
+      if (issued < 2 * n)
+        for (int j = max(0, issued - 4); j < issued; ++j) {
+          const uint64_t began = now_ns();
+          while (!mbar_try_wait(j & 1 ? &C.v_full[j >> 1 & 1] : &C.k_full[j >> 1 & 1], j >> 2 & 1) &&
+                 now_ns() - began < kWaitNs) {
+          }
+        }
+    }
+    __syncwarp();
   } else {
     // -------------------------------------------------------------------
     // the products
@@ -592,27 +614,28 @@ template <int D, int FMT>
 cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(L.tensor_tiles * p.c.num_kv_heads * L.prefix_splits));
-  cfg.blockDim = dim3(kPrefixThreads);
-  cfg.dynamicSmemBytes = Smem<D>::kBytes;
+  cfg.gridDim = dim3(static_cast<unsigned>(L.image_tiles), static_cast<unsigned>(p.c.num_kv_heads), 2);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
-  return cudaLaunchKernelEx(&cfg, prefix_kernel<D, FMT>, p, L);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, unpack_kernel<D, FMT>, p, L);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(L.tensor_tiles * p.c.num_kv_heads * L.prefix_splits));
+  cfg.blockDim = dim3(kPrefixThreads);
+  cfg.dynamicSmemBytes = Smem<D>::kBytes;
+  return cudaLaunchKernelEx(&cfg, prefix_kernel<D>, p, L);
 }
-template <int D, int FMT>
+template <int D>
 cudaError_t enable() {
-  return cudaFuncSetAttribute(prefix_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  return cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
 }
 
 }  // namespace
 
 cudaError_t enable_prefix_kernels() {
-  cudaError_t e;
-  if ((e = enable<128, SV_CACHE_INT8>()) != cudaSuccess || (e = enable<128, SV_CACHE_E4M3>()) != cudaSuccess ||
-      (e = enable<64, SV_CACHE_INT8>()) != cudaSuccess)
-    return e;
-  return enable<64, SV_CACHE_E4M3>();
+  const cudaError_t e = enable<128>();
+  return e != cudaSuccess ? e : enable<64>();
 }
 
 int prefix_row_tile() { return 2 * kRowsTile; }
