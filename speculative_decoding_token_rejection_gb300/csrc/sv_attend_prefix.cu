@@ -329,6 +329,50 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       for (int q = 0; q < 4; ++q) tmem_load32(s_addr + q * 32, s[q]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_wait_load(s[q]);
+      const int k0 = k_begin + i * kKeyTile;
+      const uint32_t any_dead = V.dead[0] | V.dead[1] | V.dead[2] | V.dead[3];
+      const float over = fmaxf(V.top[0], V.top[1]);
+      // Most tiles: every row sees all keys and has a maximum that holds.  One sweep then, and one fused operation an
+      // exponent (below 2^24 its exact product differs from a rounded one by less than the 2^8 that a weight may grow).
+      bool plain = !any_dead && k0 + kKeyTile <= limit && m > -16777216.0f && m < 16777216.0f;
+      if (__all_sync(0xFFFFFFFFu, plain)) {
+        const Pair neg = pair(-m, -m);
+        Pair sum = l;
+        float top = -INFINITY;
+        uint32_t p[4][16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 k = *reinterpret_cast<const float4 *>(&V.kc[q * 32 + j]);
+            const float4 v = *reinterpret_cast<const float4 *>(&V.vr[q * 32 + j]);
+            const Pair ya = fma2(pair(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])), pair(k.x, k.y), neg);
+            const Pair yb = fma2(pair(__uint_as_float(s[q][j + 2]), __uint_as_float(s[q][j + 3])), pair(k.z, k.w), neg);
+            top = fmaxf(top, fmaxf(lo(ya), hi(ya)));
+            top = fmaxf(top, fmaxf(lo(yb), hi(yb)));
+            const Pair wa = pair(exp2_approx(lo(ya)), exp2_approx(hi(ya)));
+            const Pair wb = pair(exp2_approx(lo(yb)), exp2_approx(hi(yb)));
+            sum = add2(sum, wa);
+            sum = add2(sum, wb);
+            const Pair pa = mul2(wa, pair(v.x, v.y)), pb = mul2(wb, pair(v.z, v.w));
+            p[q][j / 2] = pack_f16(lo(pa), hi(pa));
+            p[q][j / 2 + 1] = pack_f16(lo(pb), hi(pb));
+          }
+        plain = __all_sync(0xFFFFFFFFu, !(top + over > kRaise));
+        if (plain) {
+          l = sum;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_store16(s_addr + q * 16, p[q]);
+        } else {  // (the scores are still there)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_load32(s_addr + q * 32, s[q]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_wait_load(s[q]);
+        }
+      } else {
+        plain = false;
+      }
+      if (!plain) {
       // x, and its largest
       float top = -INFINITY;
 #pragma unroll
@@ -343,8 +387,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           s[q][j + 2] = __float_as_uint(lo(c));
           s[q][j + 3] = __float_as_uint(hi(c));
         }
-      const int k0 = k_begin + i * kKeyTile;
-      const uint32_t any_dead = V.dead[0] | V.dead[1] | V.dead[2] | V.dead[3];
       if (__any_sync(0xFFFFFFFFu, any_dead || k0 + kKeyTile > limit)) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -358,7 +400,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int j = 0; j < 32; j += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])));
-      const float over = fmaxf(V.top[0], V.top[1]);
       const bool raise = top + over > m + kRaise || (m == -INFINITY && top > -INFINITY);
       if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
         float most = -INFINITY;
@@ -406,6 +447,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           p[j / 2 + 1] = pack_f16(lo(pb), hi(pb));
         }
         tmem_store16(s_addr + q * 16, p);
+      }
       }
       tmem_wait_store();
       fence_before();
