@@ -24,9 +24,14 @@
 // issued, so S0' may overwrite P0, and "S0' is done" tells the softmax that
 // P0 V is too: the output may be rescaled then.
 //
+// A softmax lane holds four rows' scores of 32 keys each, the accumulator shape
+// of a small product, not one row's 128: the keys' factors are read from shared
+// memory once for four rows.  (A thread a row, those reads alone kept the
+// shared-memory path busy for 2000 cycles a tile, as long as the products:
+// 1.28 ms for 512 requests x 8 tokens over 16384 keys.)
+//
 // Numbers.  x = (q . b) * (scale * log2 e * key_scale) as in sv_attend.cuh, but
-// a thread sees its row's keys one register each, so the value scales are kept
-// out of the exponent: w = 2^(x - m), l = sum w, P = w * value_scale / W with W
+// the value scales are kept out of the exponent: w = 2^(x - m), l = sum w, P = w * value_scale / W with W
 // a power of two near the first tile's largest value scale, O = W * sum P b.
 // Any m gives the same quotient O / l; it is raised to the largest x + log2(
 // value_scale / W) when that passes it by 8, so P stays below 2^8.  Whether it
@@ -50,8 +55,8 @@ constexpr uint32_t kWaitPolls = 1u << 24;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRaise = 8;
 
-struct alignas(16) Vectors {  // of one key tile; read 16 bytes at a time
-  float kc[kKeyTile], vr[kKeyTile];
+struct alignas(16) Vectors {  // of one key tile
+  float4 pair[kKeyTile / 2];  // of two keys: their factors, then their value scales / W
   uint32_t dead[4];  // keys left out, a bit each
   float top[2];      // log2 of the largest value scale / W, of keys 0-31 and 64-95, and of the others
 };
@@ -108,34 +113,66 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t r[32]) {
+// Tensor memory in the shape of a 16x8 product's accumulator, N of them side by
+// side, for 16 of the warp's 32 lanes: register 4j, 4j + 1 of lane (g, c) are
+// columns 8j + 2c, + 1 of row g, the next two of row g + 8.
+__device__ __forceinline__ void tmem_load_128(uint32_t addr, uint32_t r[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.16x256b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
+      "}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load_32(uint32_t addr, uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+      "}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
       : "memory");
 }
 // Waits for every load so far; the registers go through, so no use of them moves ahead of the wait.
-__device__ __forceinline__ void tmem_wait_load(uint32_t r[32]) {
+__device__ __forceinline__ void tmem_wait_load(uint32_t r[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t r[16]) {
+__device__ __forceinline__ void tmem_store_32(uint32_t addr, const uint32_t r[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
+      "};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 64 columns of 16-bit pairs: register 2j of lane (g, c) is column 4j + c of row g, the next one of row g + 8.
+__device__ __forceinline__ void tmem_store_pairs(uint32_t addr, const uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
+      "};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -301,153 +338,162 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       }
       fence_proxy_async_smem();
     }
-    const int row = r0 + t * kRowsTile + (tid & 127);
-    int token = -1, limit = 0x7FFFFFFF;
-    if (row < L.rows) {
-      token = div_by(row, L.group);
-      limit = prefix_limit(P, token);
-      if (limit < 0) {  // nobody's row
-        token = -1;
-        limit = 0x7FFFFFFF;
+    // row `lane` of the warp's 32, then the lane's own four: g, g + 8, g + 16, g + 24
+    const int g = lane >> 2, c = lane & 3;
+    int my_token = -1, my_limit = 0x7FFFFFFF;
+    {
+      const int row = r0 + t * kRowsTile + w4 * 32 + lane;
+      if (row < L.rows) {
+        my_token = div_by(row, L.group);
+        my_limit = prefix_limit(P, my_token);
+        if (my_limit < 0) {  // nobody's row
+          my_token = -1;
+          my_limit = 0x7FFFFFFF;
+        }
       }
     }
+    const int low = __reduce_min_sync(0xFFFFFFFFu, my_limit);  // keys below it are seen by all rows of the warp
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t s_addr = C.tmem + (static_cast<uint32_t>(w4 * 32) << 16) + t * 128;
     const uint32_t o_addr = s_addr + 256;
-    float m = -INFINITY;
-    Pair l = pair(0.0f, 0.0f);
+    constexpr uint32_t kHalf = 16u << 16;  // the warp's second 16 rows
+    float m[4];
+    Pair l[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      m[x] = -INFINITY;
+      l[x] = pair(0.0f, 0.0f);
+    }
     bool ok = t < tiles;
     for (int i = 0; ok && i < n; ++i) {
       const Vectors &V = vec[i % kVectorSlots];
       ok = wait_warp(C, &C.vec_full[i % kVectorSlots], (i / kVectorSlots) & 1) && wait_warp(C, &C.s_full[t], i & 1);
       if (!ok) break;
       fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_load32(s_addr + q * 32, s[q]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_wait_load(s[q]);
       const int k0 = k_begin + i * kKeyTile;
       const uint32_t any_dead = V.dead[0] | V.dead[1] | V.dead[2] | V.dead[3];
+      const bool cut = any_dead || k0 + kKeyTile > low;
       const float over = fmaxf(V.top[0], V.top[1]);
-      // Most tiles: every row sees all keys and has a maximum that holds.  One sweep then, and one fused operation an
-      // exponent (below 2^24 its exact product differs from a rounded one by less than the 2^8 that a weight may grow).
-      bool plain = !any_dead && k0 + kKeyTile <= limit && m > -16777216.0f && m < 16777216.0f;
-      if (__all_sync(0xFFFFFFFFu, plain)) {
-        const Pair neg = pair(-m, -m);
-        Pair sum = l;
-        float top = -INFINITY;
-        uint32_t p[4][16];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+      for (int half = 0; half < 2; ++half) {  // rows g, g + 8 of 16
+        float *const mh = m + half * 2;
+        Pair *const lh = l + half * 2;
+        uint32_t s[64], p[32];
+        auto load_scores = [&]() {
+          tmem_load_128(s_addr + half * kHalf, s);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 k = *reinterpret_cast<const float4 *>(&V.kc[q * 32 + j]);
-            const float4 v = *reinterpret_cast<const float4 *>(&V.vr[q * 32 + j]);
-            const Pair ya = fma2(pair(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])), pair(k.x, k.y), neg);
-            const Pair yb = fma2(pair(__uint_as_float(s[q][j + 2]), __uint_as_float(s[q][j + 3])), pair(k.z, k.w), neg);
-            top = fmaxf(top, fmaxf(lo(ya), hi(ya)));
-            top = fmaxf(top, fmaxf(lo(yb), hi(yb)));
-            const Pair wa = pair(exp2_approx(lo(ya)), exp2_approx(hi(ya)));
-            const Pair wb = pair(exp2_approx(lo(yb)), exp2_approx(hi(yb)));
-            sum = add2(sum, wa);
-            sum = add2(sum, wb);
-            const Pair pa = mul2(wa, pair(v.x, v.y)), pb = mul2(wb, pair(v.z, v.w));
-            p[q][j / 2] = pack_f16(lo(pa), hi(pa));
-            p[q][j / 2 + 1] = pack_f16(lo(pb), hi(pb));
-          }
-        plain = __all_sync(0xFFFFFFFFu, !(top + over > kRaise));
+          for (int q = 0; q < 4; ++q) tmem_wait_load(s + 16 * q);
+        };
+        auto score = [&](int x, int j) {  // columns 8j + 2c, + 1 of row x
+          return pair(__uint_as_float(s[j * 4 + x * 2]), __uint_as_float(s[j * 4 + x * 2 + 1]));
+        };
+        load_scores();
+        // Most tiles: every row sees all keys and has a maximum that holds.  One sweep then, and one fused operation an
+        // exponent (below 2^24 its exact product differs from a rounded one by less than the 2^8 that a weight may grow).
+        bool plain = !cut && fabsf(mh[0]) < 16777216.0f && fabsf(mh[1]) < 16777216.0f;
+        plain = __all_sync(0xFFFFFFFFu, plain);
         if (plain) {
-          l = sum;
+          const Pair neg[2] = {pair(-mh[0], -mh[0]), pair(-mh[1], -mh[1])};
+          Pair sum[2] = {lh[0], lh[1]};
+          float top = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_store16(s_addr + q * 16, p[q]);
-        } else {  // (the scores are still there)
+          for (int j = 0; j < 16; ++j) {
+            const float4 f = V.pair[j * 4 + c];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_load32(s_addr + q * 32, s[q]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_wait_load(s[q]);
-        }
-      } else {
-        plain = false;
-      }
-      if (!plain) {
-      // x, and its largest
-      float top = -INFINITY;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 k = *reinterpret_cast<const float4 *>(&V.kc[q * 32 + j]);
-          const Pair a = mul2(pair(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])), pair(k.x, k.y));
-          const Pair c = mul2(pair(__uint_as_float(s[q][j + 2]), __uint_as_float(s[q][j + 3])), pair(k.z, k.w));
-          s[q][j] = __float_as_uint(lo(a));
-          s[q][j + 1] = __float_as_uint(hi(a));
-          s[q][j + 2] = __float_as_uint(lo(c));
-          s[q][j + 3] = __float_as_uint(hi(c));
-        }
-      if (__any_sync(0xFFFFFFFFu, any_dead || k0 + kKeyTile > limit)) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t dead = V.dead[q];
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (k0 + q * 32 + j >= limit || (dead >> j & 1u)) s[q][j] = 0xFF800000u;
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])));
-      const bool raise = top + over > m + kRaise || (m == -INFINITY && top > -INFINITY);
-      if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
-        float most = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) most = fmaxf(most, __uint_as_float(s[q][j]) + __log2f(V.vr[q * 32 + j]));
-        const float next = most > m + kRaise || m == -INFINITY ? most : m;
-        const float r = m == -INFINITY ? 1.0f : exp2_approx(m - next);  // (without a maximum O and l are zeros or NaN)
-        m = next;
-        l = mul2(l, pair(r, r));
-        if (i > 0) {
-#pragma unroll
-          for (int q = 0; q < D / 16; ++q) {
-            uint32_t o[16];
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                "%14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                  "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                : "r"(o_addr + q * 16)
-                : "memory");
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * r);
-            tmem_store16(o_addr + q * 16, o);
+            for (int x = 0; x < 2; ++x) {
+              const Pair y = fma2(score(x, j), pair(f.x, f.y), neg[x]);
+              top = fmaxf(top, fmaxf(lo(y), hi(y)));
+              const Pair w = pair(exp2_approx(lo(y)), exp2_approx(hi(y)));
+              sum[x] = add2(sum[x], w);
+              const Pair v = mul2(w, pair(f.z, f.w));
+              p[j * 2 + x] = pack_f16(lo(v), hi(v));
+            }
+          }
+          plain = __all_sync(0xFFFFFFFFu, !(top + over > kRaise));
+          if (plain) {
+            lh[0] = sum[0];
+            lh[1] = sum[1];
+          } else {
+            load_scores();  // (they are still there)
           }
         }
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-      const Pair neg = pair(-base, -base);
+        if (!plain) {
+          // x, and its largest.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
+          float top[2] = {-INFINITY, -INFINITY};
+          int limit[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t p[16];
+          for (int x = 0; x < 2; ++x) limit[x] = __shfl_sync(0xFFFFFFFFu, my_limit, half * 16 + x * 8 + g);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(&V.vr[q * 32 + j]);
-          const Pair ya = add2(pair(__uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1])), neg);
-          const Pair yb = add2(pair(__uint_as_float(s[q][j + 2]), __uint_as_float(s[q][j + 3])), neg);
-          const Pair wa = pair(exp2_approx(lo(ya)), exp2_approx(hi(ya)));
-          const Pair wb = pair(exp2_approx(lo(yb)), exp2_approx(hi(yb)));
-          l = add2(l, wa);
-          l = add2(l, wb);
-          const Pair pa = mul2(wa, pair(v.x, v.y)), pb = mul2(wb, pair(v.z, v.w));
-          p[j / 2] = pack_f16(lo(pa), hi(pa));
-          p[j / 2 + 1] = pack_f16(lo(pb), hi(pb));
+          for (int j = 0; j < 16; ++j) {
+            const float4 f = V.pair[j * 4 + c];
+            const uint32_t dead = V.dead[j >> 2] >> ((j & 3) * 8 + 2 * c);
+            const int key = k0 + j * 8 + 2 * c;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const Pair y = mul2(score(x, j), pair(f.x, f.y));
+              const float a_ = key >= limit[x] || (dead & 1u) ? -INFINITY : lo(y);
+              const float b_ = key + 1 >= limit[x] || (dead & 2u) ? -INFINITY : hi(y);
+              s[j * 4 + x * 2] = __float_as_uint(a_);
+              s[j * 4 + x * 2 + 1] = __float_as_uint(b_);
+              top[x] = fmaxf(top[x], fmaxf(a_, b_));
+            }
+          }
+          bool raise = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            raise |= top[x] + over > mh[x] + kRaise || (mh[x] == -INFINITY && top[x] > -INFINITY);
+          if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
+            float most[2] = {-INFINITY, -INFINITY}, r[2];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float4 f = V.pair[j * 4 + c];
+              const Pair lv = pair(__log2f(f.z), __log2f(f.w));
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const Pair y = add2(score(x, j), lv);
+                most[x] = fmaxf(most[x], fmaxf(lo(y), hi(y)));
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 1));
+              most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 2));
+              const float next = most[x] > mh[x] + kRaise || mh[x] == -INFINITY ? most[x] : mh[x];
+              r[x] = mh[x] == -INFINITY ? 1.0f : exp2_approx(mh[x] - next);  // (without a maximum O and l are zeros or NaN)
+              mh[x] = next;
+              lh[x] = mul2(lh[x], pair(r[x], r[x]));
+            }
+            if (i > 0) {
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[16];
+                tmem_load_32(o_addr + half * kHalf + q * 32, o);
+                tmem_wait_load(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r[e >> 1 & 1]);
+                tmem_store_32(o_addr + half * kHalf + q * 32, o);
+              }
+            }
+          }
+          Pair neg[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) neg[x] = mh[x] == -INFINITY ? pair(0.0f, 0.0f) : pair(-mh[x], -mh[x]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float4 f = V.pair[j * 4 + c];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const Pair y = add2(score(x, j), neg[x]);
+              const Pair w = pair(exp2_approx(lo(y)), exp2_approx(hi(y)));
+              lh[x] = add2(lh[x], w);
+              const Pair v = mul2(w, pair(f.z, f.w));
+              p[j * 2 + x] = pack_f16(lo(v), hi(v));
+            }
+          }
         }
-        tmem_store16(s_addr + q * 16, p);
-      }
+        tmem_store_pairs(s_addr + half * kHalf, p);
       }
       tmem_wait_store();
       fence_before();
@@ -460,23 +506,32 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     fence_after();
     if (t < tiles) {
       const float w = ok ? __uint_as_float(*const_cast<volatile uint32_t *>(&C.scale_top)) : 0.0f;
-      const int hq = token < 0 ? 0 : h * P.group + row - token * P.group;
-      const int64_t at = (static_cast<int64_t>(token) * P.Hq + hq) * L.slots + slot;
+      int64_t at[4];
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t o[32];
-        tmem_load32(o_addr + q * 32, o);
-        tmem_wait_load(o);
-        if (token >= 0 && ok) {
-          float *dst = L.part_o + at * D + q * 32;
-#pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4 *>(dst + j) =
-                make_float4(__uint_as_float(o[j]) * w, __uint_as_float(o[j + 1]) * w, __uint_as_float(o[j + 2]) * w,
-                            __uint_as_float(o[j + 3]) * w);
-        }
+      for (int x = 0; x < 4; ++x) {
+        const int row = r0 + t * kRowsTile + w4 * 32 + x * 8 + g;
+        const int token = __shfl_sync(0xFFFFFFFFu, my_token, x * 8 + g);
+        at[x] = token < 0 ? -1 : (static_cast<int64_t>(token) * P.Hq + h * P.group + row - token * P.group) * L.slots + slot;
+        float sum = lo(l[x]) + hi(l[x]);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        if (c == 0 && at[x] >= 0) L.part_ml[at[x]] = ok ? make_float2(m[x], sum) : make_float2(-INFINITY, 0.0f);
       }
-      if (token >= 0) L.part_ml[at] = ok ? make_float2(m, lo(l) + hi(l)) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t o[16];
+          tmem_load_32(o_addr + half * kHalf + q * 32, o);
+          tmem_wait_load(o);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const int x = half * 2 + (e >> 1 & 1);
+            if (ok && at[x] >= 0)
+              *reinterpret_cast<float2 *>(L.part_o + at[x] * D + q * 32 + (e >> 2) * 8 + 2 * c) =
+                  make_float2(__uint_as_float(o[e]) * w, __uint_as_float(o[e + 1]) * w);
+          }
+        }
     }
     fence_before();
   } else if (warp < 10) {
@@ -548,8 +603,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         if (!good && v != 0.0f) kc = __uint_as_float(0x7FC00000u);
         if (good) most = fmaxf(most, v);
         const uint32_t dead = __ballot_sync(0xFFFFFFFFu, out);
-        V.kc[r] = out ? 0.0f : kc;
-        V.vr[r] = good ? v * unscale : 1.0f;
+        float *const at = reinterpret_cast<float *>(&V.pair[r >> 1]) + (r & 1);
+        at[0] = out ? 0.0f : kc;
+        at[2] = good ? v * unscale : 1.0f;
         if (lane == 0) V.dead[r >> 5] = dead;
       }
       const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
