@@ -90,20 +90,28 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // D (tensor memory) = A B (+ D), both operands in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "l"(a), "l"(b), "r"(idesc), "n"(ADD ? 1 : 0)
       : "memory");
 }
 // The same with A in tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+template <bool ADD>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "r"(a), "l"(b), "r"(idesc), "n"(ADD ? 1 : 0)
       : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // Arrives on `bar` once every product issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
@@ -650,55 +658,73 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     fence_before();
     __syncthreads();
     fence_after();
-    if (lane == 0) {
-      const uint32_t tmem = C.tmem, base = smem_addr(smem);
-      constexpr uint32_t kScores = product(kKeyTile, false), kOutputs = product(D, true);
-      auto scores = [&](int t, int st) {
+    // The whole warp runs the loop, so addresses stay warp-uniform (one thread's own cost it 3700 cycles a tile to issue
+    // 2050 cycles of products); one elected lane issues.
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, C.tmem, 0), base = smem_addr(smem);
+    constexpr uint32_t kScores = product(kKeyTile, false), kOutputs = product(D, true);
+    const uint64_t queries = operand(base + Y::kQ, 16), keys = operand(base + Y::kK, 16),
+                   values = operand(base + Y::kV, kKeyTile * 128);
+    const bool leader = elected();
+    auto scores = [&](int t, int st) {
+      const uint64_t a = queries + static_cast<uint64_t>(t * (Y::kTile >> 4)), b = keys + static_cast<uint64_t>(st * (Y::kTile >> 4));
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = (kk >> 2) * (kRowsTile * 128) + (kk & 3) * 32;
-          mma_ss(tmem + t * 128, operand(base + Y::kQ + t * Y::kTile + at, 16),
-                 operand(base + Y::kK + st * Y::kTile + at, 16), kScores, kk > 0);
+          constexpr int kBlock = (kRowsTile * 128) >> 4;
+          const int at = (kk >> 2) * kBlock + (kk & 3) * 2;
+          if (kk == 0)
+            mma_ss<false>(tmem + t * 128, a + at, b + at, kScores);
+          else
+            mma_ss<true>(tmem + t * 128, a + at, b + at, kScores);
         }
         mma_commit(&C.s_full[t]);
-      };
-      auto outputs = [&](int t, int st, bool add) {
-#pragma unroll
-        for (int kk = 0; kk < kKeyTile / 16; ++kk)
-          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                 operand(base + Y::kV + st * Y::kTile + kk * 2048, kKeyTile * 128), kOutputs, add || kk > 0);
-      };
-      bool ok = wait(C, &C.k_full[0], 0);
-      if (ok) {
-        fence_after();
-        for (int t = 0; t < tiles; ++t) scores(t, 0);
-        mma_commit(&C.k_empty[0]);
       }
-      for (int i = 0; ok && i < n; ++i) {
-        const int st = i & 1, sn = st ^ 1;
-        ok = wait(C, &C.v_full[st], i >> 1 & 1);
-        for (int t = 0; ok && t < tiles; ++t) {
-          ok = wait(C, &C.p_full[t], i & 1);
-          if (!ok) break;
-          fence_after();
-          outputs(t, st, i > 0);
-          if (t == tiles - 1) mma_commit(&C.v_empty[st]);
-          if (i + 1 < n) {
-            if (t == 0) {
-              ok = wait(C, &C.k_full[sn], (i + 1) >> 1 & 1);
-              if (!ok) break;
-              fence_after();
-            }
-            scores(t, sn);
-            if (t == tiles - 1) mma_commit(&C.k_empty[sn]);
+    };
+    auto outputs = [&](int t, int st, bool add) {
+      const uint64_t b = values + static_cast<uint64_t>(st * (Y::kTile >> 4));
+      if (leader) {
+        if (add)
+          mma_ts<true>(tmem + 256 + t * 128, tmem + t * 128, b, kOutputs);
+        else
+          mma_ts<false>(tmem + 256 + t * 128, tmem + t * 128, b, kOutputs);
+#pragma unroll
+        for (int kk = 1; kk < kKeyTile / 16; ++kk)
+          mma_ts<true>(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, b + kk * (2048 >> 4), kOutputs);
+      }
+    };
+    auto commit = [&](uint64_t *bar) {
+      if (leader) mma_commit(bar);
+    };
+    bool ok = wait_warp(C, &C.k_full[0], 0);
+    if (ok) {
+      fence_after();
+      for (int t = 0; t < tiles; ++t) scores(t, 0);
+      commit(&C.k_empty[0]);
+    }
+    for (int i = 0; ok && i < n; ++i) {
+      const int st = i & 1, sn = st ^ 1;
+      ok = wait_warp(C, &C.v_full[st], i >> 1 & 1);
+      for (int t = 0; ok && t < tiles; ++t) {
+        ok = wait_warp(C, &C.p_full[t], i & 1);
+        if (!ok) break;
+        fence_after();
+        outputs(t, st, i > 0);
+        if (t == tiles - 1) commit(&C.v_empty[st]);
+        if (i + 1 < n) {
+          if (t == 0) {
+            ok = wait_warp(C, &C.k_full[sn], (i + 1) >> 1 & 1);
+            if (!ok) break;
+            fence_after();
           }
+          scores(t, sn);
+          if (t == tiles - 1) commit(&C.k_empty[sn]);
         }
       }
-      // (after a wait that gave up too: the products in flight end before the memory goes)
-      mma_commit(&C.done);
-      const uint64_t began = now_ns();
-      while (!mbar_try_wait(&C.done, 0) && now_ns() - began < kWaitNs) {
-      }
+    }
+    // (after a wait that gave up too: the products in flight end before the memory goes)
+    commit(&C.done);
+    const uint64_t began = now_ns();
+    while (!mbar_try_wait(&C.done, 0) && now_ns() - began < kWaitNs) {
     }
     __syncwarp();
     fence_before();
