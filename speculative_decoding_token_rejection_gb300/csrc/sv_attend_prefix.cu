@@ -56,7 +56,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRaise = 8;
 
 struct alignas(16) Vectors {  // of one key tile
-  float4 pair[kKeyTile / 2];  // of two keys: their factors, then their value scales / W
+  float2 kc[kKeyTile / 2], vr[kKeyTile / 2];  // of two keys: their factors; their value scales / W
   uint32_t dead[4];  // keys left out, a bit each
   float top[2];      // log2 of the largest value scale / W, of keys 0-31 and 64-95, and of the others
 };
@@ -170,18 +170,11 @@ __device__ __forceinline__ void tmem_store_32(uint32_t addr, const uint32_t r[16
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 64 columns of 16-bit pairs: register 2j of lane (g, c) is column 4j + c of row g, the next one of row g + 8.
-__device__ __forceinline__ void tmem_store_pairs(uint32_t addr, const uint32_t r[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {"
-      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
-      "};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+// 16 columns of 16-bit pairs: register 2j of lane (g, c) is column 4j + c of row g, the next one of row g + 8.
+__device__ __forceinline__ void tmem_store_pairs(uint32_t addr, const uint32_t r[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -297,6 +290,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
   if (warp == 11) tmem_alloc(&C.tmem, 512);
   __syncthreads();
 
+  // The softmax warps' scores need more registers than the others do: 256 * 208 + 128 * 88 = 384 * 168, what the CTA
+  // was launched with.
+  if (warp >= 8)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   if (warp < 8) {
     // -------------------------------------------------------------------
     // softmax of row tile `t`
@@ -384,124 +383,130 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       const uint32_t any_dead = V.dead[0] | V.dead[1] | V.dead[2] | V.dead[3];
       const bool cut = any_dead || k0 + kKeyTile > low;
       const float over = fmaxf(V.top[0], V.top[1]);
+      uint32_t s[2][64];  // rows g and g + 8 of each half of the warp's 32: the scores, then the exponents
+      auto load_scores = [&]() {
+        tmem_load_128(s_addr, s[0]);
+        tmem_load_128(s_addr + kHalf, s[1]);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {  // rows g, g + 8 of 16
-        float *const mh = m + half * 2;
-        Pair *const lh = l + half * 2;
-        uint32_t s[64], p[32];
-        auto load_scores = [&]() {
-          tmem_load_128(s_addr + half * kHalf, s);
+        for (int q = 0; q < 4; ++q) {
+          tmem_wait_load(s[0] + 16 * q);
+          tmem_wait_load(s[1] + 16 * q);
+        }
+      };
+      auto get = [&](int x, int j) {  // columns 8j + 2c, + 1 of row x
+        return pair(__uint_as_float(s[x >> 1][j * 4 + (x & 1) * 2]), __uint_as_float(s[x >> 1][j * 4 + (x & 1) * 2 + 1]));
+      };
+      auto put = [&](int x, int j, float a, float b) {
+        s[x >> 1][j * 4 + (x & 1) * 2] = __float_as_uint(a);
+        s[x >> 1][j * 4 + (x & 1) * 2 + 1] = __float_as_uint(b);
+      };
+      load_scores();
+      // Most tiles: every row sees all keys and has a maximum that holds.  One fused operation an exponent then (below
+      // 2^24 its exact product differs from a rounded one by less than the 2^8 that a weight may grow).
+      bool plain = !cut;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_wait_load(s + 16 * q);
-        };
-        auto score = [&](int x, int j) {  // columns 8j + 2c, + 1 of row x
-          return pair(__uint_as_float(s[j * 4 + x * 2]), __uint_as_float(s[j * 4 + x * 2 + 1]));
-        };
-        load_scores();
-        // Most tiles: every row sees all keys and has a maximum that holds.  One sweep then, and one fused operation an
-        // exponent (below 2^24 its exact product differs from a rounded one by less than the 2^8 that a weight may grow).
-        bool plain = !cut && fabsf(mh[0]) < 16777216.0f && fabsf(mh[1]) < 16777216.0f;
-        plain = __all_sync(0xFFFFFFFFu, plain);
-        if (plain) {
-          const Pair neg[2] = {pair(-mh[0], -mh[0]), pair(-mh[1], -mh[1])};
-          Pair sum[2] = {lh[0], lh[1]};
-          float top = -INFINITY;
+      for (int x = 0; x < 4; ++x) plain = plain && fabsf(m[x]) < 16777216.0f;
+      plain = __all_sync(0xFFFFFFFFu, plain);
+      if (plain) {
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 f = V.pair[j * 4 + c];
+        for (int j = 0; j < 16; ++j) {
+          const float2 f = V.kc[j * 4 + c];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const Pair y = fma2(score(x, j), pair(f.x, f.y), neg[x]);
-              top = fmaxf(top, fmaxf(lo(y), hi(y)));
-              const Pair w = pair(exp2_approx(lo(y)), exp2_approx(hi(y)));
-              sum[x] = add2(sum[x], w);
-              const Pair v = mul2(w, pair(f.z, f.w));
-              p[j * 2 + x] = pack_f16(lo(v), hi(v));
-            }
-          }
-          plain = __all_sync(0xFFFFFFFFu, !(top + over > kRaise));
-          if (plain) {
-            lh[0] = sum[0];
-            lh[1] = sum[1];
-          } else {
-            load_scores();  // (they are still there)
+          for (int x = 0; x < 4; ++x) {
+            const Pair y = fma2(get(x, j), pair(f.x, f.y), pair(-m[x], -m[x]));
+            put(x, j, lo(y), hi(y));
+            top[x] = fmaxf(top[x], fmaxf(lo(y), hi(y)));
           }
         }
-        if (!plain) {
-          // x, and its largest.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
-          float top[2] = {-INFINITY, -INFINITY};
-          int limit[2];
+        plain = __all_sync(0xFFFFFFFFu, !(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) + over > kRaise));
+        if (!plain) load_scores();  // (they are still there)
+      }
+      if (!plain) {
+        // x, and its largest.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        int limit[4];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) limit[x] = __shfl_sync(0xFFFFFFFFu, my_limit, half * 16 + x * 8 + g);
+        for (int x = 0; x < 4; ++x) limit[x] = __shfl_sync(0xFFFFFFFFu, my_limit, x * 8 + g);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 f = V.kc[j * 4 + c];
+          const uint32_t dead = V.dead[j >> 2] >> ((j & 3) * 8 + 2 * c);
+          const int key = k0 + j * 8 + 2 * c;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const Pair y = mul2(get(x, j), pair(f.x, f.y));
+            const float a_ = key >= limit[x] || (dead & 1u) ? -INFINITY : lo(y);
+            const float b_ = key + 1 >= limit[x] || (dead & 2u) ? -INFINITY : hi(y);
+            put(x, j, a_, b_);
+            top[x] = fmaxf(top[x], fmaxf(a_, b_));
+          }
+        }
+        bool raise = false;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) raise |= top[x] + over > m[x] + kRaise || (m[x] == -INFINITY && top[x] > -INFINITY);
+        if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
+          float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, r[4];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float4 f = V.pair[j * 4 + c];
-            const uint32_t dead = V.dead[j >> 2] >> ((j & 3) * 8 + 2 * c);
-            const int key = k0 + j * 8 + 2 * c;
+            const float2 f = V.vr[j * 4 + c];
+            const Pair lv = pair(__log2f(f.x), __log2f(f.y));
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const Pair y = mul2(score(x, j), pair(f.x, f.y));
-              const float a_ = key >= limit[x] || (dead & 1u) ? -INFINITY : lo(y);
-              const float b_ = key + 1 >= limit[x] || (dead & 2u) ? -INFINITY : hi(y);
-              s[j * 4 + x * 2] = __float_as_uint(a_);
-              s[j * 4 + x * 2 + 1] = __float_as_uint(b_);
-              top[x] = fmaxf(top[x], fmaxf(a_, b_));
+            for (int x = 0; x < 4; ++x) {
+              const Pair y = add2(get(x, j), lv);
+              most[x] = fmaxf(most[x], fmaxf(lo(y), hi(y)));
             }
           }
-          bool raise = false;
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            raise |= top[x] + over > mh[x] + kRaise || (mh[x] == -INFINITY && top[x] > -INFINITY);
-          if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
-            float most[2] = {-INFINITY, -INFINITY}, r[2];
+          for (int x = 0; x < 4; ++x) {
+            most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 1));
+            most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 2));
+            const float next = most[x] > m[x] + kRaise || m[x] == -INFINITY ? most[x] : m[x];
+            r[x] = m[x] == -INFINITY ? 1.0f : exp2_approx(m[x] - next);  // (without a maximum O and l are zeros or NaN)
+            m[x] = next;
+            l[x] = mul2(l[x], pair(r[x], r[x]));
+          }
+          if (i > 0) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float4 f = V.pair[j * 4 + c];
-              const Pair lv = pair(__log2f(f.z), __log2f(f.w));
+            for (int q = 0; q < D / 32; ++q)
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const Pair y = add2(score(x, j), lv);
-                most[x] = fmaxf(most[x], fmaxf(lo(y), hi(y)));
-              }
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 1));
-              most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 2));
-              const float next = most[x] > mh[x] + kRaise || mh[x] == -INFINITY ? most[x] : mh[x];
-              r[x] = mh[x] == -INFINITY ? 1.0f : exp2_approx(mh[x] - next);  // (without a maximum O and l are zeros or NaN)
-              mh[x] = next;
-              lh[x] = mul2(lh[x], pair(r[x], r[x]));
-            }
-            if (i > 0) {
-#pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
+              for (int half = 0; half < 2; ++half) {
                 uint32_t o[16];
                 tmem_load_32(o_addr + half * kHalf + q * 32, o);
                 tmem_wait_load(o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r[e >> 1 & 1]);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r[half * 2 + (e >> 1 & 1)]);
                 tmem_store_32(o_addr + half * kHalf + q * 32, o);
               }
-            }
-          }
-          Pair neg[2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) neg[x] = mh[x] == -INFINITY ? pair(0.0f, 0.0f) : pair(-mh[x], -mh[x]);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 f = V.pair[j * 4 + c];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const Pair y = add2(score(x, j), neg[x]);
-              const Pair w = pair(exp2_approx(lo(y)), exp2_approx(hi(y)));
-              lh[x] = add2(lh[x], w);
-              const Pair v = mul2(w, pair(f.z, f.w));
-              p[j * 2 + x] = pack_f16(lo(v), hi(v));
-            }
           }
         }
-        tmem_store_pairs(s_addr + half * kHalf, p);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const Pair neg = m[x] == -INFINITY ? pair(0.0f, 0.0f) : pair(-m[x], -m[x]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const Pair y = add2(get(x, j), neg);
+            put(x, j, lo(y), hi(y));
+          }
+        }
+      }
+      // the weights, sixteen columns of a half at a time
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t p[2][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = V.vr[(q * 4 + j) * 4 + c];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const Pair y = get(x, q * 4 + j), w = pair(exp2_approx(lo(y)), exp2_approx(hi(y)));
+            l[x] = add2(l[x], w);
+            const Pair v = mul2(w, pair(f.x, f.y));
+            p[x >> 1][j * 2 + (x & 1)] = pack_f16(lo(v), hi(v));
+          }
+        }
+        tmem_store_pairs(s_addr + q * 16, p[0]);
+        tmem_store_pairs(s_addr + kHalf + q * 16, p[1]);
       }
       tmem_wait_store();
       fence_before();
@@ -611,9 +616,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         if (!good && v != 0.0f) kc = __uint_as_float(0x7FC00000u);
         if (good) most = fmaxf(most, v);
         const uint32_t dead = __ballot_sync(0xFFFFFFFFu, out);
-        float *const at = reinterpret_cast<float *>(&V.pair[r >> 1]) + (r & 1);
-        at[0] = out ? 0.0f : kc;
-        at[2] = good ? v * unscale : 1.0f;
+        (r & 1 ? V.kc[r >> 1].y : V.kc[r >> 1].x) = out ? 0.0f : kc;
+        (r & 1 ? V.vr[r >> 1].y : V.vr[r >> 1].x) = good ? v * unscale : 1.0f;
         if (lane == 0) V.dead[r >> 5] = dead;
       }
       const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
