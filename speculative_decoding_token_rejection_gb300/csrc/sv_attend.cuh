@@ -32,7 +32,9 @@ struct AttendPlan {
   int32_t prefix_tiles, prefix_items;  // prefix row tiles and CTAs of the warp-streaming kernel (0 items: not its work)
   int32_t tensor_tiles;                // prefix row tiles of the tensor-memory kernel (0: not its work)
   int32_t own_splits, own_chunk, own_tiles;
-  int32_t slots;          // 1: results go straight to the output
+  int32_t slots;          // partial results of a row
+  bool direct;            // one: its CTAs write the output
+  bool ovec;              // output rows allow 8-byte stores
   bool qvec;              // q rows allow 16-byte loads
   int32_t image_tiles;    // tiles of prefix_key_tile() keys of the prefix
   uint8_t *image;         // the prefix as f16 tiles: [num_kv_heads][image_tiles][K, V]
