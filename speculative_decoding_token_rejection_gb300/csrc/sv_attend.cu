@@ -590,10 +590,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttendParams P, co
   uint32_t bits = 0;
   if (!attend_request(P, i, first, g, len, bits)) return;
   const int own = len > P.prefix ? (len - P.prefix + L.own_chunk - 1) / L.own_chunk : 0;
-  const int slots = L.prefix_splits + own;
   const int rows = (g + 1) * P.Hq;
   for (int r = blockIdx.y * kWarps + warp; r < rows; r += gridDim.y * kWarps) {
     const int64_t row = first * P.Hq + r;
+    const int j = r / P.Hq, hq = r - j * P.Hq, h = hq / P.group;
+    const int shared = P.prefix ? prefix_slots(L, h, (static_cast<int>(first) + j) * P.group + hq - h * P.group, kPrefixRowTile) : 0;
+    const int slots = shared + own;
     Part<D> all;
     all.m = -INFINITY;
     all.l = 0.0f;
@@ -603,12 +605,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttendParams P, co
       Part<D> part[kJoinAhead];
 #pragma unroll
       for (int u = 0; u < kJoinAhead; ++u)
-        if (s + u < slots) part[u] = load_part<D>(L, row, s + u, lane);
+        if (s + u < slots) part[u] = load_part<D>(L, row, s + u < shared ? s + u : s + u - shared + L.prefix_splits, lane);
 #pragma unroll
       for (int u = 0; u < kJoinAhead; ++u)
         if (s + u < slots) join_part<D>(all, part[u]);
     }
-    write_row<D>(P, L, first + r / P.Hq, r % P.Hq, lane, all);
+    write_row<D>(P, L, first + j, hq, lane, all);
   }
 }
 
@@ -616,8 +618,8 @@ int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 constexpr int kChunkStep = kAttendWarps * kKeys;  // a CTA's four warps take 32 keys each
 constexpr int kTensorKeys = 128, kTensorRows = 96;  // the prefix goes to the tensor-memory kernel from here on
-constexpr int kTensorFixed = 3, kTensorSplits = 64;
-constexpr int kChunkMost = 2048;                  // so that the longest request is no long tail
+constexpr int kTensorLeast = 4;  // key tiles of a CTA of that kernel, where the prefix has as many
+constexpr int kChunkMost = 8192;                  // so that the longest request is no long tail
 
 // Chunks for `keys` keys when `base` CTAs work on every chunk: enough to give
 // each SM two CTAs twice over, none below kChunkStep keys.
@@ -639,24 +641,6 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
   return bound;
 }
 
-// Chunks of the tensor-memory kernel, whose CTAs have an SM each: as many as
-// make the last wave of CTAs end soonest, a chunk's fixed cost counted as
-// kTensorFixed key tiles.
-void cut_tensor(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
-  const int step = prefix_key_tile(), all = ceil_div(keys, step);
-  int64_t best = INT64_MAX;
-  for (int tiles = all; tiles >= 1; --tiles) {
-    const int s = ceil_div(all, tiles);
-    if (s > kTensorSplits) break;
-    const int64_t cost = ((base * s + num_sms - 1) / num_sms) * (tiles + kTensorFixed);
-    if (cost < best) {
-      best = cost;
-      splits = s;
-      chunk = tiles * step;
-    }
-  }
-}
-
 AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullptr) {
   AttendPlan L{};
   L.page = fast_div(std::max(1, p.c.block_size));
@@ -668,11 +652,14 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   int bound = std::max(1, cut(static_cast<int64_t>(p.N) * p.c.num_kv_heads * L.own_tiles, p.max_seq - p.prefix, num_sms,
                               L.own_splits, L.own_chunk));
   L.own_splits = std::max(1, L.own_splits);
-  if (p.prefix >= kTensorKeys && L.rows >= kTensorRows) {
-    L.tensor_tiles = ceil_div(L.rows, prefix_row_tile());
-    L.image_tiles = ceil_div(p.prefix, prefix_key_tile());
-    cut_tensor(static_cast<int64_t>(p.c.num_kv_heads) * L.tensor_tiles, p.prefix, num_sms, L.prefix_splits,
-               L.prefix_chunk);
+  const int64_t image_tiles = ceil_div(p.prefix, kPrefixKeyTile), tensor_tiles = ceil_div(L.rows, kPrefixRowTile);
+  const int64_t units = tensor_tiles * p.c.num_kv_heads * image_tiles;
+  if (p.prefix >= kTensorKeys && L.rows >= kTensorRows && units <= 0x3FFFFFFF) {
+    L.tensor_tiles = static_cast<int32_t>(tensor_tiles);
+    L.image_tiles = static_cast<int32_t>(image_tiles);
+    L.units = static_cast<int32_t>(units);
+    L.units_cta = std::max(ceil_div(units, num_sms), std::min(kTensorLeast, L.image_tiles));
+    L.prefix_splits = L.image_tiles == 1 ? 1 : (L.image_tiles - 2) / L.units_cta + 2;  // an item's CTAs at most
     bound += L.prefix_splits;
   } else {
     bound += cut(static_cast<int64_t>(p.c.num_kv_heads) * L.prefix_tiles, p.prefix, num_sms, L.prefix_splits,
@@ -687,7 +674,7 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   L.ovec = (reinterpret_cast<uintptr_t>(p.out) & 7u) == 0 && p.out_token % 4 == 0 && p.out_head % 4 == 0;
   const int64_t rows = static_cast<int64_t>(L.rows) * p.c.num_kv_heads;
   // the workspace: the prefix's tiles, then M and l, then O
-  const int64_t image = static_cast<int64_t>(L.image_tiles) * p.c.num_kv_heads * prefix_key_tile() * p.c.head_dim * 4;
+  const int64_t image = static_cast<int64_t>(L.image_tiles) * p.c.num_kv_heads * kPrefixKeyTile * p.c.head_dim * 4;
   if (bytes) *bytes = bound <= 1 ? 0 : image + ((rows * bound * 8 + 15) & ~int64_t{15}) + rows * bound * p.c.head_dim * 4;
   L.image = static_cast<uint8_t *>(p.workspace);
   L.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(p.workspace) + image);

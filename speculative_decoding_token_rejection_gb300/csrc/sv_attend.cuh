@@ -31,23 +31,31 @@ struct AttendPlan {
   int32_t prefix_splits, prefix_chunk;
   int32_t prefix_tiles, prefix_items;  // prefix row tiles and CTAs of the warp-streaming kernel (0 items: not its work)
   int32_t tensor_tiles;                // prefix row tiles of the tensor-memory kernel (0: not its work)
+  int32_t units, units_cta;            // its (kv head, row tile, key tile) units, and a CTA's share of them
   int32_t own_splits, own_chunk, own_tiles;
   int32_t slots;          // partial results of a row
   bool direct;            // one: its CTAs write the output
   bool ovec;              // output rows allow 8-byte stores
   bool qvec;              // q rows allow 16-byte loads
-  int32_t image_tiles;    // tiles of prefix_key_tile() keys of the prefix
+  int32_t image_tiles;    // tiles of kPrefixKeyTile keys of the prefix
   uint8_t *image;         // the prefix as f16 tiles: [num_kv_heads][image_tiles][K, V]
   float *part_o;          // [rows * num_kv_heads][slots][D], row = token * Hq + query head
   float2 *part_ml;        // [rows * num_kv_heads][slots]: M, l
 };
 
 // The prefix on the tensor cores' memory (sv_attend_prefix.cu): tiles of
-// prefix_row_tile() rows and prefix_key_tile() keys.
+// kPrefixRowTile rows and kPrefixKeyTile keys.
 cudaError_t enable_prefix_kernels();
 cudaError_t launch_prefix(const AttendParams &p, const AttendPlan &L, cudaStream_t stream);
-int prefix_row_tile();
-int prefix_key_tile();
+constexpr int kPrefixRowTile = 256, kPrefixKeyTile = 128;
+
+// Partial results of the prefix that a row has: of kv head h, row `local` of
+// the (T + N) * group.
+__device__ __forceinline__ int prefix_slots(const AttendPlan &L, int h, int local, int row_tile) {
+  if (L.tensor_tiles == 0) return L.prefix_splits;
+  const int first = (h * L.tensor_tiles + local / row_tile) * L.image_tiles;
+  return (first + L.image_tiles - 1) / L.units_cta - first / L.units_cta + 1;
+}
 
 // Draft range and length of request i; false (and nothing to write) for a bad
 // range.  A bad length counts as 0.

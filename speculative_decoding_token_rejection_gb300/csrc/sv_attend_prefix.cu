@@ -10,8 +10,10 @@
 // (Turned into f16 by every CTA for itself, the tiles took three warps 6000
 // cycles each, most of it page look-ups and shared-memory stores, against 2050
 // of the products: 64 requests x 5 tokens over 8192 keys 100 us.)
-// A CTA takes 256 rows (two accumulator tiles of 128) of one kv head and a
-// range of keys:
+// An item is 256 rows (two accumulator tiles of 128) of one kv head; the units
+// of work, its key tiles, are dealt evenly over as many CTAs as there are SMs,
+// item after item, so an item's keys are cut only where one CTA's share ends.
+// In a CTA:
 //
 //   warps 0-3, 4-7  softmax of a row tile, a thread a row: reads S from tensor
 //                   memory, writes the weights back over it as f16
@@ -45,8 +47,8 @@
 namespace sv {
 namespace {
 
-constexpr int kRowsTile = 128;  // rows of an accumulator tile
-constexpr int kKeyTile = 128;
+constexpr int kRowsTile = kPrefixRowTile / 2;  // rows of an accumulator tile
+constexpr int kKeyTile = kPrefixKeyTile;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kVectorThreads = 64;
 constexpr int kPrefixThreads = kSoftmaxThreads + kVectorThreads + 64;
@@ -251,6 +253,11 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const AttendParams P, 
   }
 }
 
+// A CTA's consecutive key tiles of one item: a kv head's 256 rows.
+struct Segment {
+  int h, r0, tiles, n, k_begin, k_end, slot;
+};
+
 template <int D>
 __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendParams P, const AttendPlan L) {
   pdl_enter();
@@ -261,14 +268,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
   Vectors *const vec = reinterpret_cast<Vectors *>(smem + Y::kVec);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int H = P.c.num_kv_heads;
-  int b = blockIdx.x;
-  const int pair_tile = b % L.tensor_tiles;
-  b /= L.tensor_tiles;
-  const int h = b % H, slot = b / H;
-  const int r0 = pair_tile * 2 * kRowsTile;
-  const int tiles = L.rows - r0 > kRowsTile ? 2 : 1;
-  const int k_begin = slot * L.prefix_chunk, k_end = min(P.prefix, k_begin + L.prefix_chunk);
-  const int n = (k_end - k_begin + kKeyTile - 1) / kKeyTile;  // >= 1
+  const int T = L.image_tiles, u_end = min(L.units, static_cast<int>(blockIdx.x + 1) * L.units_cta);
+  auto segment = [&](int u) {  // the CTA's work from unit u on: key tiles of one item (kv head, 256 rows)
+    const int item = u / T, t0 = u - item * T;
+    Segment s;
+    s.h = item / L.tensor_tiles;
+    s.r0 = (item - s.h * L.tensor_tiles) * 2 * kRowsTile;
+    s.tiles = L.rows - s.r0 > kRowsTile ? 2 : 1;
+    s.n = min(T - t0, u_end - u);
+    s.k_begin = t0 * kKeyTile;
+    s.k_end = min(P.prefix, s.k_begin + s.n * kKeyTile);
+    s.slot = static_cast<int>(blockIdx.x) - item * T / L.units_cta;
+    return s;
+  };
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -281,14 +293,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     }
     for (int i = 0; i < kVectorSlots; ++i) {
       mbar_init(&C.vec_full[i], kVectorThreads);
-      mbar_init(&C.vec_empty[i], 4 * tiles);
+      mbar_init(&C.vec_empty[i], 8);
     }
     mbar_init(&C.done, 1);
     C.query_top = C.scale_top = C.abort = 0;
     fence_mbar_init();
   }
   if (warp == 11) tmem_alloc(&C.tmem, 512);
+  fence_before();
   __syncthreads();
+  fence_after();
+
+  // Between two segments every role is done with the one before: A; the tops are cleared: B; queries and factors: C.
+  auto begin = [&]() {
+    __syncthreads();
+    if (tid == 0) C.query_top = C.scale_top = 0;
+  };
+  int done_tiles = 0, done_segments = 0;  // (barrier phases run on from one segment to the next)
 
   // The softmax warps' scores need more registers than the others do: 256 * 208 + 128 * 88 = 384 * 168, what the CTA
   // was launched with.
@@ -301,6 +322,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     // softmax of row tile `t`
     // -------------------------------------------------------------------
     const int t = warp >> 2, w4 = warp & 3;
+    int mine = 0;  // key tiles of this row tile so far
+    for (int u = blockIdx.x * L.units_cta; u < u_end;) {
+    const Segment S = segment(u);
+    const int h = S.h, r0 = S.r0, tiles = S.tiles, n = S.n, k_begin = S.k_begin, slot = S.slot;
+    begin();
+    __syncthreads();
     {  // the tile's queries: f16 with the CTA's common power of two
       uint4 x[D / 8];  // warp w4 takes rows 32 * w4 ..; a row is D/8 lanes
       constexpr int kLanes = D / 8, kRowsPass = 32 / kLanes, kQ = 32 / kRowsPass;
@@ -373,10 +400,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       m[x] = -INFINITY;
       l[x] = pair(0.0f, 0.0f);
     }
-    bool ok = t < tiles;
+    bool ok = true;
     for (int i = 0; ok && i < n; ++i) {
-      const Vectors &V = vec[i % kVectorSlots];
-      ok = wait_warp(C, &C.vec_full[i % kVectorSlots], (i / kVectorSlots) & 1) && wait_warp(C, &C.s_full[t], i & 1);
+      const int it = done_tiles + i;
+      const Vectors &V = vec[it % kVectorSlots];
+      ok = wait_warp(C, &C.vec_full[it % kVectorSlots], it / kVectorSlots & 1);
+      if (t >= tiles) {  // (no rows: the factors' slot is handed back)
+        if (ok && lane == 0) mbar_arrive(&C.vec_empty[it % kVectorSlots]);
+        continue;
+      }
+      ok = ok && wait_warp(C, &C.s_full[t], (mine + i) & 1);
       if (!ok) break;
       fence_after();
       const int k0 = k_begin + i * kKeyTile;
@@ -512,10 +545,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       fence_before();
       mbar_arrive(&C.p_full[t]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&C.vec_empty[i % kVectorSlots]);
+      if (lane == 0) mbar_arrive(&C.vec_empty[it % kVectorSlots]);
     }
     // the partial result
-    if (ok) ok = wait_warp(C, &C.done, 0);
+    if (ok) ok = wait_warp(C, &C.done, done_segments & 1);
     fence_after();
     if (t < tiles) {
       const float w = ok ? __uint_as_float(*const_cast<volatile uint32_t *>(&C.scale_top)) : 0.0f;
@@ -547,14 +580,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         }
     }
     fence_before();
+    done_tiles += n;
+    ++done_segments;
+    if (t < tiles) mine += n;
+    u += n;
+    }
   } else if (warp < 10) {
     // -------------------------------------------------------------------
     // the keys' factors: keys lt and lt + 64 of every tile
     // -------------------------------------------------------------------
     const int lt = tid - kSoftmaxThreads;
+    uint32_t bad = 0;
+    bool ok = true;
+    for (int u = blockIdx.x * L.units_cta; u < u_end;) {
+    const Segment S = segment(u);
+    const int h = S.h, n = S.n, k_begin = S.k_begin, k_end = S.k_end;
+    begin();
+    __syncthreads();
     const float *const kscale = P.c.k_scale + h * P.c.scale_head_stride;
     const float *const vscale = P.c.v_scale + h * P.c.scale_head_stride;
-    uint32_t bad = 0;
     float ks[2], vs[2];
     bool in[2];  // a key of the range
     int page[2];
@@ -600,10 +644,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         P.scale * kLog2e * pow2(-query_shift(*const_cast<volatile uint32_t *>(&C.query_top)));
     asm volatile("bar.sync 2, 64;" ::: "memory");
     if (lt == 0) *const_cast<volatile uint32_t *>(&C.scale_top) = __float_as_uint(1.0f / unscale);
-    bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int slot_v = i % kVectorSlots;
-      ok = wait_warp(C, &C.vec_empty[slot_v], (i / kVectorSlots & 1) ^ 1);
+    for (int i = 0; ok && i < n; ++i) {
+      const int it = done_tiles + i, slot_v = it % kVectorSlots;
+      ok = wait_warp(C, &C.vec_empty[slot_v], (it / kVectorSlots & 1) ^ 1);
       if (!ok) break;
       Vectors &V = vec[slot_v];
       float most = 0.0f;
@@ -626,42 +669,56 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       scales(i + 1);
       pages(i + 2);
     }
+    done_tiles += n;
+    u += n;
+    }
     if (P.status && (bad || !ok)) atomicOr(P.status, static_cast<int>(bad | (ok ? 0u : SV_DATA_COPY_TIMEOUT)));
   } else if (warp == 10) {
     // -------------------------------------------------------------------
     // copies
     // -------------------------------------------------------------------
-    fence_before();
-    __syncthreads();
-    fence_after();
-    if (lane == 0) {
-      const uint8_t *image = L.image + (static_cast<int64_t>(h) * L.image_tiles + k_begin / kKeyTile) * 2 * Y::kTile;
+    bool ok = true;
+    for (int u = blockIdx.x * L.units_cta; u < u_end;) {
+      const Segment S = segment(u);
+      const uint8_t *const image = L.image + (static_cast<int64_t>(S.h) * T + S.k_begin / kKeyTile) * 2 * Y::kTile;
       int issued = 0;  // K and V tiles alternate
-      for (; issued < 2 * n; ++issued) {
-        const int i = issued >> 1, st = i & 1;
-        const bool v = issued & 1;
-        if (!wait(C, v ? &C.v_empty[st] : &C.k_empty[st], (i >> 1 & 1) ^ 1)) break;
-        uint64_t *full = v ? &C.v_full[st] : &C.k_full[st];
-        mbar_arrive_expect_tx(full, Y::kTile);
-        bulk_g2s(smem + (v ? Y::kV : Y::kK) + st * Y::kTile, image + static_cast<int64_t>(issued) * Y::kTile, Y::kTile, full);
-      }
-      // (after a wait that gave up: the last copies end before the shared memory goes)
-      if (issued < 2 * n)
-        for (int j = max(0, issued - 4); j < issued; ++j) {
-          const uint64_t began = now_ns();
-          while (!mbar_try_wait(j & 1 ? &C.v_full[j >> 1 & 1] : &C.k_full[j >> 1 & 1], j >> 2 & 1) &&
-                 now_ns() - began < kWaitNs) {
-          }
+      auto issue = [&](int most) {
+        for (; ok && issued < most; ++issued) {
+          const int it = done_tiles + (issued >> 1), st = it & 1;
+          const bool v = issued & 1;
+          ok = wait(C, v ? &C.v_empty[st] : &C.k_empty[st], (it >> 1 & 1) ^ 1);
+          if (!ok) break;
+          uint64_t *full = v ? &C.v_full[st] : &C.k_full[st];
+          mbar_arrive_expect_tx(full, Y::kTile);
+          bulk_g2s(smem + (v ? Y::kV : Y::kK) + st * Y::kTile, image + static_cast<int64_t>(issued) * Y::kTile, Y::kTile, full);
         }
+      };
+      begin();
+      if (lane == 0) issue(min(4, 2 * S.n));  // (the stages are free: the segment before is done)
+      __syncwarp();
+      __syncthreads();
+      fence_before();
+      __syncthreads();
+      fence_after();
+      if (lane == 0) {
+        issue(2 * S.n);
+        // (after a wait that gave up: the last copies end before the shared memory goes)
+        if (!ok)
+          for (int j = max(0, issued - 4); j < issued; ++j) {
+            const int it = done_tiles + (j >> 1);
+            const uint64_t began = now_ns();
+            while (!mbar_try_wait(j & 1 ? &C.v_full[it & 1] : &C.k_full[it & 1], it >> 1 & 1) && now_ns() - began < kWaitNs) {
+            }
+          }
+      }
+      __syncwarp();
+      done_tiles += S.n;
+      u += S.n;
     }
-    __syncwarp();
   } else {
     // -------------------------------------------------------------------
     // the products
     // -------------------------------------------------------------------
-    fence_before();
-    __syncthreads();
-    fence_after();
     // The whole warp runs the loop, so addresses stay warp-uniform (one thread's own cost it 3700 cycles a tile to issue
     // 2050 cycles of products); one elected lane issues.
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, C.tmem, 0), base = smem_addr(smem);
@@ -699,36 +756,52 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     auto commit = [&](uint64_t *bar) {
       if (leader) mma_commit(bar);
     };
-    bool ok = wait_warp(C, &C.k_full[0], 0);
-    if (ok) {
+    bool ok = true;
+    int second = 0;  // key tiles of the second row tile so far
+    for (int u = blockIdx.x * L.units_cta; u < u_end;) {
+      const Segment S = segment(u);
+      const int n = S.n, tiles = S.tiles;
+      begin();
+      __syncthreads();
+      fence_before();
+      __syncthreads();
       fence_after();
-      for (int t = 0; t < tiles; ++t) scores(t, 0);
-      commit(&C.k_empty[0]);
-    }
-    for (int i = 0; ok && i < n; ++i) {
-      const int st = i & 1, sn = st ^ 1;
-      ok = wait_warp(C, &C.v_full[st], i >> 1 & 1);
-      for (int t = 0; ok && t < tiles; ++t) {
-        ok = wait_warp(C, &C.p_full[t], i & 1);
-        if (!ok) break;
+      ok = ok && wait_warp(C, &C.k_full[done_tiles & 1], done_tiles >> 1 & 1);
+      if (ok) {
         fence_after();
-        outputs(t, st, i > 0);
-        if (t == tiles - 1) commit(&C.v_empty[st]);
-        if (i + 1 < n) {
-          if (t == 0) {
-            ok = wait_warp(C, &C.k_full[sn], (i + 1) >> 1 & 1);
-            if (!ok) break;
-            fence_after();
+        for (int t = 0; t < tiles; ++t) scores(t, done_tiles & 1);
+        commit(&C.k_empty[done_tiles & 1]);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const int it = done_tiles + i, st = it & 1, sn = st ^ 1;
+        ok = wait_warp(C, &C.v_full[st], it >> 1 & 1);
+        for (int t = 0; ok && t < tiles; ++t) {
+          ok = wait_warp(C, &C.p_full[t], (t ? second + i : it) & 1);
+          if (!ok) break;
+          fence_after();
+          outputs(t, st, i > 0);
+          if (t == tiles - 1) commit(&C.v_empty[st]);
+          if (i + 1 < n) {
+            if (t == 0) {
+              ok = wait_warp(C, &C.k_full[sn], (it + 1) >> 1 & 1);
+              if (!ok) break;
+              fence_after();
+            }
+            scores(t, sn);
+            if (t == tiles - 1) commit(&C.k_empty[sn]);
           }
-          scores(t, sn);
-          if (t == tiles - 1) commit(&C.k_empty[sn]);
         }
       }
-    }
-    // (after a wait that gave up too: the products in flight end before the memory goes)
-    commit(&C.done);
-    const uint64_t began = now_ns();
-    while (!mbar_try_wait(&C.done, 0) && now_ns() - began < kWaitNs) {
+      // (after a wait that gave up too: the products in flight end before the memory goes)
+      commit(&C.done);
+      const uint64_t began = now_ns();
+      while (!mbar_try_wait(&C.done, done_segments & 1) && now_ns() - began < kWaitNs) {
+      }
+      __syncwarp();
+      done_tiles += n;
+      ++done_segments;
+      if (tiles == 2) second += n;
+      u += n;
     }
     __syncwarp();
     fence_before();
@@ -749,7 +822,7 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stre
   cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, unpack_kernel<D, FMT>, p, L);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(L.tensor_tiles * p.c.num_kv_heads * L.prefix_splits));
+  cfg.gridDim = dim3(static_cast<unsigned>((L.units + L.units_cta - 1) / L.units_cta));
   cfg.blockDim = dim3(kPrefixThreads);
   cfg.dynamicSmemBytes = Smem<D>::kBytes;
   return cudaLaunchKernelEx(&cfg, prefix_kernel<D>, p, L);
@@ -765,9 +838,6 @@ cudaError_t enable_prefix_kernels() {
   const cudaError_t e = enable<128>();
   return e != cudaSuccess ? e : enable<64>();
 }
-
-int prefix_row_tile() { return 2 * kRowsTile; }
-int prefix_key_tile() { return kKeyTile; }
 
 cudaError_t launch_prefix(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
   const bool i8 = p.c.format == SV_CACHE_INT8;
