@@ -304,10 +304,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
   __syncthreads();
   fence_after();
 
-  // Between two segments every role is done with the one before: A; the tops are cleared: B; queries and factors: C.
+  // Between two segments every role but the copies', which the stages' barriers pace, is done with the one before: A; the
+  // tops are cleared: B; queries and factors are there: C.
+  auto meet = []() { asm volatile("bar.sync 3, 352;" ::: "memory"); };
   auto begin = [&]() {
-    __syncthreads();
+    meet();
     if (tid == 0) C.query_top = C.scale_top = 0;
+    meet();
   };
   int done_tiles = 0, done_segments = 0;  // (barrier phases run on from one segment to the next)
 
@@ -326,52 +329,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     for (int u = blockIdx.x * L.units_cta; u < u_end;) {
     const Segment S = segment(u);
     const int h = S.h, r0 = S.r0, tiles = S.tiles, n = S.n, k_begin = S.k_begin, slot = S.slot;
-    begin();
-    __syncthreads();
-    {  // the tile's queries: f16 with the CTA's common power of two
-      uint4 x[D / 8];  // warp w4 takes rows 32 * w4 ..; a row is D/8 lanes
-      constexpr int kLanes = D / 8, kRowsPass = 32 / kLanes, kQ = 32 / kRowsPass;
-      uint32_t top = 0;
-#pragma unroll
-      for (int f = 0; f < kQ; ++f) {
-        const int r = r0 + t * kRowsTile + w4 * 32 + f * kRowsPass + lane / kLanes;
-        x[f] = make_uint4(0, 0, 0, 0);
-        if (r < L.rows) {
-          const int token = div_by(r, L.group), hq = h * P.group + r - token * P.group;
-          const uint16_t *src = P.q + token * P.q_token + hq * P.q_head + lane % kLanes * 8;
-          if (L.qvec) {
-            x[f] = *reinterpret_cast<const uint4 *>(src);
-          } else {
-            x[f].x = src[0] | static_cast<uint32_t>(src[1]) << 16;
-            x[f].y = src[2] | static_cast<uint32_t>(src[3]) << 16;
-            x[f].z = src[4] | static_cast<uint32_t>(src[5]) << 16;
-            x[f].w = src[6] | static_cast<uint32_t>(src[7]) << 16;
-          }
-        }
-        const uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t lo_ = w[e] << 16 & 0x7FFFFFFFu, hi_ = w[e] & 0x7FFF0000u;
-          if (lo_ < 0x7F800000u) top = max(top, lo_);
-          if (hi_ < 0x7F800000u) top = max(top, hi_);
-        }
-      }
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
-      if (lane == 0) atomicMax(&C.query_top, top);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float up = pow2(query_shift(*const_cast<volatile uint32_t *>(&C.query_top)));
-#pragma unroll
-      for (int f = 0; f < kQ; ++f) {
-        const int r = w4 * 32 + f * kRowsPass + lane / kLanes, col = lane % kLanes;
-        uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = pack_f16(bf16_bits_to_float(w[e] & 0xFFFFu) * up, bf16_bits_to_float(w[e] >> 16) * up);
-        *reinterpret_cast<uint4 *>(smem + Y::kQ + t * Y::kTile + (col >> 3) * (kRowsTile * 128) + r * 128 +
-                                   (((col & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      fence_proxy_async_smem();
-    }
     // row `lane` of the warp's 32, then the lane's own four: g, g + 8, g + 16, g + 24
     const int g = lane >> 2, c = lane & 3;
     int my_token = -1, my_limit = 0x7FFFFFFF;
@@ -387,8 +344,57 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       }
     }
     const int low = __reduce_min_sync(0xFFFFFFFFu, my_limit);  // keys below it are seen by all rows of the warp
+    {  // the tile's queries: f16 with the CTA's common power of two
+      uint4 x[D / 8];  // warp w4 takes rows 32 * w4 ..; a row is D/8 lanes
+      constexpr int kLanes = D / 8, kRowsPass = 32 / kLanes, kQ = 32 / kRowsPass;
+      uint32_t top = 0;
+      auto source = [&](int f) {  // null: no such row
+        const int r = r0 + t * kRowsTile + w4 * 32 + f * kRowsPass + lane / kLanes;
+        const int token = div_by(r, L.group), hq = h * P.group + r - token * P.group;
+        return r < L.rows ? P.q + token * P.q_token + hq * P.q_head + lane % kLanes * 8 : nullptr;
+      };
+#pragma unroll
+      for (int f = 0; f < kQ; ++f) x[f] = make_uint4(0, 0, 0, 0);
+      if (L.qvec) {  // (all loads before the first use)
+#pragma unroll
+        for (int f = 0; f < kQ; ++f)
+          if (const uint16_t *src = source(f)) x[f] = *reinterpret_cast<const uint4 *>(src);
+      } else {
+#pragma unroll
+        for (int f = 0; f < kQ; ++f)
+          if (const uint16_t *src = source(f))
+            x[f] = make_uint4(src[0] | static_cast<uint32_t>(src[1]) << 16, src[2] | static_cast<uint32_t>(src[3]) << 16,
+                              src[4] | static_cast<uint32_t>(src[5]) << 16, src[6] | static_cast<uint32_t>(src[7]) << 16);
+      }
+#pragma unroll
+      for (int f = 0; f < kQ; ++f) {
+        const uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo_ = w[e] << 16 & 0x7FFFFFFFu, hi_ = w[e] & 0x7FFF0000u;
+          if (lo_ < 0x7F800000u) top = max(top, lo_);
+          if (hi_ < 0x7F800000u) top = max(top, hi_);
+        }
+      }
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      begin();
+      if (lane == 0) atomicMax(&C.query_top, top);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float up = pow2(query_shift(*const_cast<volatile uint32_t *>(&C.query_top)));
+#pragma unroll
+      for (int f = 0; f < kQ; ++f) {
+        const int r = w4 * 32 + f * kRowsPass + lane / kLanes, col = lane % kLanes;
+        uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_f16(bf16_bits_to_float(w[e] & 0xFFFFu) * up, bf16_bits_to_float(w[e] >> 16) * up);
+        *reinterpret_cast<uint4 *>(smem + Y::kQ + t * Y::kTile + (col >> 3) * (kRowsTile * 128) + r * 128 +
+                                   (((col & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+    }
     fence_before();
-    __syncthreads();
+    meet();
     fence_after();
     const uint32_t s_addr = C.tmem + (static_cast<uint32_t>(w4 * 32) << 16) + t * 128;
     const uint32_t o_addr = s_addr + 256;
@@ -595,8 +601,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     for (int u = blockIdx.x * L.units_cta; u < u_end;) {
     const Segment S = segment(u);
     const int h = S.h, n = S.n, k_begin = S.k_begin, k_end = S.k_end;
-    begin();
-    __syncthreads();
     const float *const kscale = P.c.k_scale + h * P.c.scale_head_stride;
     const float *const vscale = P.c.v_scale + h * P.c.scale_head_stride;
     float ks[2], vs[2];
@@ -626,6 +630,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     pages(0);
     scales(0);
     pages(1);
+    begin();
     {  // W: the power of two at the first tile's largest value scale
       uint32_t top = 0;
 #pragma unroll
@@ -635,7 +640,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       if (lane == 0) atomicMax(&C.scale_top, top & 0xFF800000u);
     }
     fence_before();
-    __syncthreads();
+    meet();
     fence_after();
     const uint32_t wbits = *const_cast<volatile uint32_t *>(&C.scale_top);
     const int wexp = wbits >= 0x00800000u ? static_cast<int>(wbits >> 23) - 127 : 0;
@@ -677,44 +682,32 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     // -------------------------------------------------------------------
     // copies
     // -------------------------------------------------------------------
-    bool ok = true;
-    for (int u = blockIdx.x * L.units_cta; u < u_end;) {
-      const Segment S = segment(u);
-      const uint8_t *const image = L.image + (static_cast<int64_t>(S.h) * T + S.k_begin / kKeyTile) * 2 * Y::kTile;
+    if (lane == 0) {
+      bool ok = true;
       int issued = 0;  // K and V tiles alternate
-      auto issue = [&](int most) {
-        for (; ok && issued < most; ++issued) {
-          const int it = done_tiles + (issued >> 1), st = it & 1;
-          const bool v = issued & 1;
+      for (int u = blockIdx.x * L.units_cta; ok && u < u_end; ++u) {
+        const int item = u / T, h = item / L.tensor_tiles;
+        const uint8_t *const image = L.image + (static_cast<int64_t>(h) * T + u - item * T) * 2 * Y::kTile;
+        for (int v = 0; v < 2; ++v) {
+          const int it = issued >> 1, st = it & 1;
           ok = wait(C, v ? &C.v_empty[st] : &C.k_empty[st], (it >> 1 & 1) ^ 1);
           if (!ok) break;
           uint64_t *full = v ? &C.v_full[st] : &C.k_full[st];
           mbar_arrive_expect_tx(full, Y::kTile);
-          bulk_g2s(smem + (v ? Y::kV : Y::kK) + st * Y::kTile, image + static_cast<int64_t>(issued) * Y::kTile, Y::kTile, full);
+          bulk_g2s(smem + (v ? Y::kV : Y::kK) + st * Y::kTile, image + v * Y::kTile, Y::kTile, full);
+          ++issued;
         }
-      };
-      begin();
-      if (lane == 0) issue(min(4, 2 * S.n));  // (the stages are free: the segment before is done)
-      __syncwarp();
-      __syncthreads();
-      fence_before();
-      __syncthreads();
-      fence_after();
-      if (lane == 0) {
-        issue(2 * S.n);
-        // (after a wait that gave up: the last copies end before the shared memory goes)
-        if (!ok)
-          for (int j = max(0, issued - 4); j < issued; ++j) {
-            const int it = done_tiles + (j >> 1);
-            const uint64_t began = now_ns();
-            while (!mbar_try_wait(j & 1 ? &C.v_full[it & 1] : &C.k_full[it & 1], it >> 1 & 1) && now_ns() - began < kWaitNs) {
-            }
-          }
       }
-      __syncwarp();
-      done_tiles += S.n;
-      u += S.n;
+      // (after a wait that gave up: the last copies end before the shared memory goes)
+      if (!ok)
+        for (int j = max(0, issued - 4); j < issued; ++j) {
+          const int it = j >> 1;
+          const uint64_t began = now_ns();
+          while (!mbar_try_wait(j & 1 ? &C.v_full[it & 1] : &C.k_full[it & 1], it >> 1 & 1) && now_ns() - began < kWaitNs) {
+          }
+        }
     }
+    __syncwarp();
   } else {
     // -------------------------------------------------------------------
     // the products
@@ -762,9 +755,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       const Segment S = segment(u);
       const int n = S.n, tiles = S.tiles;
       begin();
-      __syncthreads();
       fence_before();
-      __syncthreads();
+      meet();
       fence_after();
       ok = ok && wait_warp(C, &C.k_full[done_tiles & 1], done_tiles >> 1 & 1);
       if (ok) {
