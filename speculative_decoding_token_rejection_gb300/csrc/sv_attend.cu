@@ -75,6 +75,7 @@ struct RowTile {
   const int32_t *table;
   int *token;  // [rows] in shared memory: verify token of a row, or -1
   int *limit;  // keys that the row sees are below it
+  bool whole;  // every key that the rows see: the result is the output
 };
 
 // One partial result of a row: M, l and the lane's dimensions of O.
@@ -174,39 +175,39 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
     const int k = T.k_begin + (it * kAttendWarps + warp) * kKeys + lane;
     return it < ntiles && k < T.k_end ? T.table[div_by(k, L.page)] : -1;
   };
-  auto issue = [&](int it, int stage, int page) {
-    if (it < ntiles) {
-      const int k = T.k_begin + (it * kAttendWarps + warp) * kKeys + lane;
-      const bool in = k < T.k_end, live = in && page >= 0 && page < P.c.num_blocks;
-      if (in && !live) bits = SV_DATA_BAD_SLOT;
-      uint32_t unit = 0;  // the row's place in units of 16 bytes (rows are 16-byte aligned, a side below 2^36 bytes)
-      int64_t sat = 0;
-      if (live) {
-        const int off = k - div_by(k, L.page) * P.c.block_size;
-        unit = static_cast<uint32_t>((page * P.c.block_stride + off * P.c.token_stride) >> 4);
-        sat = page * P.c.scale_block_stride + off * P.c.scale_token_stride;
-      }
-      const uint32_t dead = __ballot_sync(0xFFFFFFFFu, !live);
-      const uint32_t dst = ring + stage * Y::kStage;
-      copy_async<4>(dst + Y::kScales + lane * 8, kscale + sat, live ? 4 : 0);
-      copy_async<4>(dst + Y::kScales + lane * 8 + 4, vscale + sat, live ? 4 : 0);
-#pragma unroll
-      for (int x = 0; x < kCols; ++x) {
-        const int row = x * (32 / kCols) + lane / kCols;
-        const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, row);
-        const uint32_t n = dead >> row & 1u ? 0u : 16u;
-        copy_async<16>(dst + tile_at<D, false>(row, ccol), kcol + static_cast<uint64_t>(u) * 16, n);
-        copy_async<16>(dst + kKeys * D + tile_at<D, true>(row, ccol), vcol + static_cast<uint64_t>(u) * 16, n);
-      }
-    }
-    copy_commit();
+  // Copies of a tile: the lane's key first, then the rows, a lane's neighbours taking a whole one, in kCols steps.
+  uint32_t unit = 0, dead = 0;  // the row's place in units of 16 bytes (rows are 16-byte aligned, a side below 2^36 bytes)
+  auto copy_keys = [&](int it, int stage, int page) {
+    const int k = T.k_begin + (it * kAttendWarps + warp) * kKeys + lane;
+    const bool in = k < T.k_end, live = in && page >= 0 && page < P.c.num_blocks;
+    if (in && !live) bits = SV_DATA_BAD_SLOT;
+    const int off = k - div_by(k, L.page) * P.c.block_size;
+    const uint32_t dst = ring + stage * Y::kStage + Y::kScales + lane * 8;
+    unit = live ? static_cast<uint32_t>((page * P.c.block_stride + off * P.c.token_stride) >> 4) : 0u;
+    const int64_t sat = live ? page * P.c.scale_block_stride + off * P.c.scale_token_stride : 0;
+    dead = __ballot_sync(0xFFFFFFFFu, !live);
+    copy_async<4>(dst, kscale + sat, live ? 4 : 0);
+    copy_async<4>(dst + 4, vscale + sat, live ? 4 : 0);
+  };
+  auto copy_rows = [&](int stage, int step) {
+    const uint32_t dst = ring + stage * Y::kStage;
+    const int row = step * (32 / kCols) + lane / kCols;
+    const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, row);
+    const uint32_t n = dead >> row & 1u ? 0u : 16u;
+    copy_async<16>(dst + tile_at<D, false>(row, ccol), kcol + static_cast<uint64_t>(u) * 16, n);
+    copy_async<16>(dst + kKeys * D + tile_at<D, true>(row, ccol), vcol + static_cast<uint64_t>(u) * 16, n);
   };
 
   // (the first copies are on their way before the queries are looked at)
   int page = page_of(0);
 #pragma unroll
   for (int it = 0; it < kStages - 1; ++it) {
-    issue(it, it, page);
+    if (it < ntiles) {
+      copy_keys(it, it, page);
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) copy_rows(it, x);
+    }
+    copy_commit();
     page = page_of(it + 1);
   }
 
@@ -286,9 +287,14 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
   for (int it = 0; it < ntiles; ++it) {
     copy_wait<kStages - 2>();
     __syncwarp();  // the tile is there for every lane, and no lane still reads the one before it
-    issue(it + kStages - 1, fill, page);  // (in the place of the one before)
-    page = page_of(it + kStages);
+    if (it + kStages - 1 < ntiles) {  // (in the place of the one before)
+      copy_keys(it + kStages - 1, fill, page);
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) copy_rows(fill, x);
+    }
+    copy_commit();
     if (++fill == kStages) fill = 0;
+    page = page_of(it + kStages);
     const uint8_t *const src = ring_ptr + stage * Y::kStage;
     if (++stage == kStages) stage = 0;
     const float2 sc = *reinterpret_cast<const float2 *>(src + Y::kScales + lane * 8);
@@ -495,7 +501,7 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
 #pragma unroll
       for (int d = 0; d < kDims; ++d) all.o[d] = fmaf(acc[(w * NT * 8 + r) * Y::kPitch + lane * kDims + d], f, all.o[d]);
     }
-    if (L.direct)
+    if (T.whole)
       write_row<D>(P, L, token, hq, lane, all);
     else
       store_part<D>(L, static_cast<int64_t>(token) * P.Hq + hq, T.slot, lane, all);
@@ -513,6 +519,7 @@ __global__ void __launch_bounds__(kAttendThreads, 2) attend_kernel(const AttendP
   T.table = P.tables;
   T.token = row_token;
   T.limit = row_limit;
+  T.whole = false;
   int64_t first = 0;
   int len = 0, gam = 0;
   const bool shared_part = static_cast<int>(blockIdx.x) < L.prefix_items;
@@ -548,7 +555,9 @@ __global__ void __launch_bounds__(kAttendThreads, 2) attend_kernel(const AttendP
     T.slot = L.prefix_splits + split;
     T.k_begin = P.prefix + split * L.own_chunk;
     T.k_end = min(len, T.k_begin + L.own_chunk);
-    if (T.k_end <= T.k_begin && !L.direct) return;  // (the joining kernel knows)
+    // (a request without a prefix and with one chunk of keys or none needs no joining)
+    T.whole = P.prefix == 0 && len <= L.own_chunk;
+    if (T.k_end <= T.k_begin && !(T.whole && split == 0)) return;
     T.table += i * P.table_stride;
   }
   if (tid < T.rows) {
@@ -590,6 +599,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttendParams P, co
   uint32_t bits = 0;
   if (!attend_request(P, i, first, g, len, bits)) return;
   const int own = len > P.prefix ? (len - P.prefix + L.own_chunk - 1) / L.own_chunk : 0;
+  if (P.prefix == 0 && own <= 1) return;  // (written already)
   const int rows = (g + 1) * P.Hq;
   for (int r = blockIdx.y * kWarps + warp; r < rows; r += gridDim.y * kWarps) {
     const int64_t row = first * P.Hq + r;
@@ -669,7 +679,6 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   // (Where the private part is one chunk its CTAs could join the prefix's partial results as they end.  Measured, with
   // four rows' results in flight: 203 us for 512 requests x 32 rows, against 147 and a join by itself.)
   L.slots = L.prefix_splits + L.own_splits;
-  L.direct = L.slots == 1;
   L.qvec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0;
   L.ovec = (reinterpret_cast<uintptr_t>(p.out) & 7u) == 0 && p.out_token % 4 == 0 && p.out_head % 4 == 0;
   const int64_t rows = static_cast<int64_t>(L.rows) * p.c.num_kv_heads;
@@ -696,7 +705,7 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stre
   cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
   cudaError_t e = L.tensor_tiles ? launch_prefix(p, L, stream) : cudaSuccess;
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, attend_kernel<D, FMT>, p, L);
-  if (e != cudaSuccess || L.direct) return e;
+  if (e != cudaSuccess || L.slots == 1) return e;
   cfg.gridDim = dim3(p.N, std::max(1, std::min(65535, ceil_div((p.G + 1) * static_cast<int64_t>(p.Hq), kWarps))));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = 0;

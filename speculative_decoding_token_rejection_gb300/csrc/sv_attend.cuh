@@ -34,7 +34,6 @@ struct AttendPlan {
   int32_t units, units_cta;            // its (kv head, row tile, key tile) units, and a CTA's share of them
   int32_t own_splits, own_chunk, own_tiles;
   int32_t slots;          // partial results of a row
-  bool direct;            // one: its CTAs write the output
   bool ovec;              // output rows allow 8-byte stores
   bool qvec;              // q rows allow 16-byte loads
   int32_t image_tiles;    // tiles of kPrefixKeyTile keys of the prefix

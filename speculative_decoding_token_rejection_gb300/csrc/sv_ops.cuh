@@ -103,14 +103,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// asynchronous copies to shared memory; the bytes behind `n` are zeros
+// asynchronous copies to shared memory; the bytes behind `n` are zeros.  (No
+// memory clobber: other loads may move across them.  What they write is read
+// behind copy_wait only.)
 // ---------------------------------------------------------------------------
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t n) {
   if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n));
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES));
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
