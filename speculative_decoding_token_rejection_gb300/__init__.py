@@ -481,11 +481,34 @@ def spec_verify_check_args(config: SpecVerifyConfig, args: SpecVerifyArgs) -> in
 # ----------------------------------------------------------------------------
 # the paged 8-bit KV cache, attention over it, log-probabilities
 # ----------------------------------------------------------------------------
-def _stream_handle(stream, device) -> ctypes.c_void_p:
-    if stream is None:
-        import torch
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+# A small call costs more on the host than on the GPU, so these calls check a
+# tensor with a few comparisons and look for the reason only if one fails, and
+# fill a structure by position.
+def _stream_handle(stream, device) -> int:
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None and device.index is not None:
+        return raw(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _done(code: int) -> None:
+    if code:
+        _check(code)
+
+
+def _vector(t, dtype, name, device, numel):
+    """Pointer of a contiguous tensor of `numel` elements (as _ptr, whose messages it gives)."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.device == device:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, dtype, name, device, numel=numel)
 
 
 class KVCache:
@@ -536,19 +559,19 @@ class KVCache:
         self.struct = c
 
 
-def _heads(t, name, device, shape, dtypes):
+def _heads(t, name, device, shape, dtype):
     """A [tokens, heads, head_dim] tensor with unit stride along head_dim, any
     other strides; returns (ptr, token_stride, head_stride)."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {tuple(t.shape)}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} dtype {t.dtype} not in {dtypes}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    st = t.stride()
-    if st[2] != 1 and shape[2] > 1:
+    a, b, c = t.stride()
+    if c != 1 and shape[2] > 1:
         raise ValueError(f"{name} must be unit-stride along head_dim")
-    return t.data_ptr(), (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
+    return t.data_ptr(), (a if shape[0] > 1 else 0), (b if shape[1] > 1 else 0)
 
 
 def build_kv_args(*, cache: KVCache, key, value, slot_mapping, status=None) -> SpecVerifyKvArgs:
@@ -557,25 +580,24 @@ def build_kv_args(*, cache: KVCache, key, value, slot_mapping, status=None) -> S
     ``slot_mapping``: int64 [T]."""
     import torch
     device = cache.device
-    T = int(slot_mapping.numel())
-    if key.dtype not in (torch.float32, torch.bfloat16):
+    T = slot_mapping.numel()
+    dtype = key.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError("key must be float32 or bfloat16")
+    if slot_mapping.dim() != 1:
+        raise ValueError(f"slot_mapping must be 1-D, got shape {tuple(slot_mapping.shape)}")
     shape = (T, cache.num_kv_heads, cache.head_dim)
-    a = SpecVerifyKvArgs()
-    a.num_tokens, a.dtype = T, SV_BF16 if key.dtype == torch.bfloat16 else SV_F32
-    a.cache = cache.struct
-    a.key, a.key_token_stride, a.key_head_stride = _heads(key, "key", device, shape, (key.dtype,))
-    a.value, a.value_token_stride, a.value_head_stride = _heads(value, "value", device, shape, (key.dtype,))
-    a.slot_mapping = _ptr(slot_mapping, torch.int64, "slot_mapping", device, ndim=1)
-    a.status = _ptr(status, torch.int32, "status", device, numel=1)
-    return a
+    return SpecVerifyKvArgs(T, SV_BF16 if dtype is torch.bfloat16 else SV_F32, 0, cache.struct,
+                            *_heads(key, "key", device, shape, dtype), *_heads(value, "value", device, shape, dtype),
+                            _vector(slot_mapping, torch.int64, "slot_mapping", device, T),
+                            _vector(status, torch.int32, "status", device, 1))
 
 
 def spec_verify_kv_write(handle: int, *, stream=None, **kw) -> None:
     """Enqueue the quantisation of key and value rows into the cache.  Keyword
     arguments are those of ``build_kv_args``."""
     a = build_kv_args(**kw)
-    _check(load_library().spec_verify_kv_write(handle, ctypes.byref(a), _stream_handle(stream, kw["cache"].device)))
+    _done(load_library().spec_verify_kv_write(handle, a, _stream_handle(stream, kw["cache"].device)))
 
 
 def spec_verify_kv_read(handle: int, *, stream=None, **kw) -> None:
@@ -584,9 +606,9 @@ def spec_verify_kv_read(handle: int, *, stream=None, **kw) -> None:
     a = build_kv_args(**kw)
     for name in ("key", "value"):
         t = kw[name]
-        if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        if 0 in t.stride() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
             raise ValueError(f"{name} is written and must not overlap itself")
-    _check(load_library().spec_verify_kv_read(handle, ctypes.byref(a), _stream_handle(stream, kw["cache"].device)))
+    _done(load_library().spec_verify_kv_read(handle, a, _stream_handle(stream, kw["cache"].device)))
 
 
 def spec_verify_check_kv_args(config: SpecVerifyConfig, args: SpecVerifyKvArgs) -> int:
@@ -604,47 +626,41 @@ def build_attend_args(*, q, cache: KVCache, block_tables, seq_lens, max_seq_len:
     least ``spec_verify_attend_workspace_size`` bytes."""
     import torch
     device = cache.device
-    if block_tables.dim() != 2 or block_tables.dtype != torch.int32:
+    if block_tables.dim() != 2 or block_tables.dtype is not torch.int32:
         raise TypeError(f"block_tables must be a 2-D int32 tensor, got {tuple(block_tables.shape)} "
                         f"{block_tables.dtype}")
     N, width = block_tables.shape
+    between, unit = block_tables.stride()
     if block_tables.device != device:
         raise ValueError(f"block_tables is on {block_tables.device}, expected {device}")
-    if width > 1 and block_tables.stride(1) != 1:
+    if width > 1 and unit != 1:
         raise ValueError("block_tables rows must be unit-stride")
     if q.dim() != 3:
         raise ValueError(f"q must have shape [T + N, num_q_heads, head_dim], got {tuple(q.shape)}")
-    rows, hq = int(q.shape[0]), int(q.shape[1])
+    rows, hq, _ = q.shape
     shape = (rows, hq, cache.head_dim)
-    a = SpecVerifyAttendArgs()
-    a.num_reqs, a.max_spec_len, a.num_q_heads = N, int(max_spec_len), hq
-    a.max_seq_len, a.shared_prefix_len = int(max_seq_len), int(shared_prefix_len)
-    a.num_draft_tokens_total = rows - N
-    a.cu_num_draft_tokens = _ptr(cu_num_draft_tokens, torch.int32, "cu_num_draft_tokens", device, numel=N)
-    a.cache = cache.struct
-    a.q, a.q_token_stride, a.q_head_stride = _heads(q, "q", device, shape, (torch.bfloat16,))
-    a.block_tables = block_tables.data_ptr()
-    a.block_table_stride = block_tables.stride(0) if N > 1 else width
-    if a.block_table_stride > width:  # rows of a wider table: what lies between them is not the table's
-        a.max_seq_len = min(a.max_seq_len, width * cache.block_size)
-    a.seq_lens = _ptr(seq_lens, torch.int32, "seq_lens", device, numel=N)
-    a.scale = scale
-    a.out, a.out_token_stride, a.out_head_stride = _heads(out, "out", device, shape, (torch.bfloat16,))
-    if any(n > 1 and s == 0 for n, s in zip(out.shape, out.stride())):
+    if N <= 1:
+        between = width
+    elif between > width:  # rows of a wider table: what lies between them is not the table's
+        max_seq_len = min(max_seq_len, width * cache.block_size)
+    if 0 in out.stride() and any(n > 1 and s == 0 for n, s in zip(out.shape, out.stride())):
         raise ValueError("out is written and must not overlap itself")
-    a.lse = _ptr(lse, torch.float32, "lse", device, numel=rows * hq)
-    if workspace is not None:
-        a.workspace = _ptr(workspace, torch.uint8, "workspace", device)
-        a.workspace_bytes = workspace.numel()
-    a.status = _ptr(status, torch.int32, "status", device, numel=1)
-    return a
+    bf16, i32 = torch.bfloat16, torch.int32
+    return SpecVerifyAttendArgs(
+        N, int(max_spec_len), hq, int(max_seq_len), int(shared_prefix_len), 0, rows - N,
+        _vector(cu_num_draft_tokens, i32, "cu_num_draft_tokens", device, N), cache.struct,
+        *_heads(q, "q", device, shape, bf16), block_tables.data_ptr(), between,
+        _vector(seq_lens, i32, "seq_lens", device, N), float(scale), 0, *_heads(out, "out", device, shape, bf16),
+        _vector(lse, torch.float32, "lse", device, rows * hq),
+        None if workspace is None else _vector(workspace, torch.uint8, "workspace", device, workspace.numel()),
+        0 if workspace is None else workspace.numel(), _vector(status, i32, "status", device, 1))
 
 
 def spec_verify_attend(handle: int, *, stream=None, **kw) -> None:
     """Enqueue the verify tokens' attention over the cache.  Keyword arguments
     are those of ``build_attend_args``."""
     a = build_attend_args(**kw)
-    _check(load_library().spec_verify_attend(handle, ctypes.byref(a), _stream_handle(stream, kw["cache"].device)))
+    _done(load_library().spec_verify_attend(handle, a, _stream_handle(stream, kw["cache"].device)))
 
 
 def spec_verify_attend_workspace_size(handle: int, *, num_reqs: int, max_spec_len: int, num_q_heads: int,
@@ -673,42 +689,32 @@ def build_logprobs_args(*, logits, out_tokens, logprobs, ranks=None, entropy=Non
     ``logits``: [T+N, V] float32 or bfloat16 rows; ``out_tokens``: int32
     [N, G+1], as ``spec_verify_run`` leaves it."""
     import torch
-    device = logits.device
+    device, dtype = logits.device, logits.dtype
     if out_tokens.dim() != 2 or out_tokens.shape[1] < 1:
         raise ValueError(f"out_tokens must have shape [N, G + 1], got {tuple(out_tokens.shape)}")
     if logits.dim() != 2:
         raise ValueError(f"logits must have shape [T + N, V], got {tuple(logits.shape)}")
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError("logits must be float32 or bfloat16")
     N, cols = out_tokens.shape
     rows, V = logits.shape
-    a = SpecVerifyLogprobsArgs()
-    if logits.dtype == torch.bfloat16:
-        a.dtype = SV_BF16
-    elif logits.dtype == torch.float32:
-        a.dtype = SV_F32
-    else:
-        raise TypeError("logits must be float32 or bfloat16")
-    a.num_reqs, a.max_spec_len, a.vocab_size, a.num_top = N, cols - 1, V, int(num_top)
-    a.num_draft_tokens_total = rows - N
-    a.cu_num_draft_tokens = _ptr(cu_num_draft_tokens, torch.int32, "cu_num_draft_tokens", device, numel=N)
-    a.logits, a.row_stride = _rows(logits, "logits", device, V, rows, (logits.dtype,))
-    a.temperature = _ptr(temperature, torch.float32, "temperature", device, numel=N)
-    a.out_tokens = _ptr(out_tokens, torch.int32, "out_tokens", device)
-    n = N * cols
-    a.logprobs = _ptr(logprobs, torch.float32, "logprobs", device, numel=n)
-    a.ranks = _ptr(ranks, torch.int32, "ranks", device, numel=n)
-    a.entropy = _ptr(entropy, torch.float32, "entropy", device, numel=n)
-    if num_top:
-        a.top_ids = _ptr(top_ids, torch.int32, "top_ids", device, numel=n * num_top)
-        a.top_logprobs = _ptr(top_logprobs, torch.float32, "top_logprobs", device, numel=n * num_top)
-    a.status = _ptr(status, torch.int32, "status", device, numel=1)
-    return a
+    n, i32, f32, num_top = N * cols, torch.int32, torch.float32, int(num_top)
+    return SpecVerifyLogprobsArgs(
+        N, cols - 1, V, SV_BF16 if dtype is torch.bfloat16 else SV_F32, num_top, 0, rows - N,
+        _vector(cu_num_draft_tokens, i32, "cu_num_draft_tokens", device, N),
+        *_rows(logits, "logits", device, V, rows, (dtype,)), _vector(temperature, f32, "temperature", device, N),
+        _vector(out_tokens, i32, "out_tokens", device, n), _vector(logprobs, f32, "logprobs", device, n),
+        _vector(ranks, i32, "ranks", device, n), _vector(entropy, f32, "entropy", device, n),
+        _vector(top_ids, i32, "top_ids", device, n * num_top) if num_top else None,
+        _vector(top_logprobs, f32, "top_logprobs", device, n * num_top) if num_top else None,
+        _vector(status, i32, "status", device, 1))
 
 
 def spec_verify_logprobs(handle: int, *, stream=None, **kw) -> None:
     """Enqueue the log-probabilities of committed tokens.  Keyword arguments
     are those of ``build_logprobs_args``."""
     a = build_logprobs_args(**kw)
-    _check(load_library().spec_verify_logprobs(handle, ctypes.byref(a), _stream_handle(stream, kw["logits"].device)))
+    _done(load_library().spec_verify_logprobs(handle, a, _stream_handle(stream, kw["logits"].device)))
 
 
 def spec_verify_check_logprobs_args(config: SpecVerifyConfig, args: SpecVerifyLogprobsArgs) -> int:
