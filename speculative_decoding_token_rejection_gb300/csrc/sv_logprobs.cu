@@ -51,7 +51,7 @@ struct LogprobsSmem {
   Sums warp_sums[kWarps], sums;
   alignas(16) uint32_t block_key[kMaxBlocks];
   int chosen[SV_MAX_TOP_LOGPROBS];
-  uint32_t floor_key;  // key of the last chosen block
+  float floor;         // largest element of the last chosen block
   int count;           // candidates
 };
 
@@ -145,6 +145,30 @@ __device__ __forceinline__ float element(const uint4 &r, int e) {
 }
 
 template <bool BF16>
+__device__ __forceinline__ float largest(const uint4 &r) {
+  if (!BF16) return max_nan(max_nan(word_of(r, 0), word_of(r, 1)), max_nan(word_of(r, 2), word_of(r, 3)));
+  const uint32_t t = max_nan_bf16x2(max_nan_bf16x2(r.x, r.y), max_nan_bf16x2(r.z, r.w));
+  return max_nan(__uint_as_float(t << 16), __uint_as_float(t & 0xFFFF0000u));
+}
+// The number that an ordered key stands for.
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+// A block maximum's place in the order (largest key, lower block first).  A
+// bf16's key has 16 bits: the block's number goes below them, and one
+// comparison decides; an fp32's needs the block as well where keys are equal.
+template <bool BF16>
+__device__ __forceinline__ uint32_t block_order(uint32_t key, int block) {
+  return BF16 ? (key & 0xFFFF0000u) | static_cast<uint32_t>(0xFFFF - block) : key;
+}
+static_assert(kMaxBlocks <= 0x10000, "a block's number fits 16 bits");
+template <bool BF16>
+__device__ __forceinline__ bool block_before(uint32_t key, int block, uint32_t other, int other_block) {
+  return BF16 ? key > other : key > other || (key == other && block < other_block);
+}
+
+template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsParams P) {
   pdl_enter();
   __shared__ LogprobsSmem sm;
@@ -229,13 +253,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
   Sums sum{-INFINITY, 0.0f, 0.0f, 0u, 0u};
   Pair z = pair(0.0f, 0.0f), zx = z;
   bool bad = false;
-  uint4 next[kUnroll];
-  fetch(warp, next);
-  for (int gi = warp; gi < groups; gi += kWarps) {
-    uint4 raw[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) raw[u] = next[u];
-    fetch(gi + kWarps, next);
+  auto take = [&](int gi, const uint4 raw[kUnroll]) {
     float top;
     if (BF16) {
       uint32_t t2 = raw[0].x, n2 = 0;
@@ -265,9 +283,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
       const uint32_t k = __reduce_max_sync(0xFFFFFFFFu, key);
       if (lane == 0) {
         if (per_block == 1)
-          sm.block_key[gi] = k;
+          sm.block_key[gi] = block_order<BF16>(k, gi);
         else
-          atomicMax(&sm.block_key[gi / per_block], k);
+          atomicMax(&sm.block_key[gi / per_block], block_order<BF16>(k, gi / per_block));
       }
     }
     if ((top - sum.ref) * c > kRaiseBy && top > -INFINITY) {  // (seldom after the first)
@@ -291,6 +309,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
           zx = fma2(w, d, zx);
         }
     }
+  };
+  // two groups in turn, each fetched while the other is taken
+  uint4 even[kUnroll], odd[kUnroll];
+  fetch(warp, even);
+  for (int gi = warp; gi < groups; gi += 2 * kWarps) {
+    fetch(gi + kWarps, odd);
+    take(gi, even);
+    if (gi + kWarps >= groups) break;
+    fetch(gi + 2 * kWarps, even);
+    take(gi + kWarps, odd);
   }
   sum.bad = bad;
   sum.z = lo(z) + hi(z);
@@ -330,14 +358,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
       int before = 0;
       for (int j = 0; j < blocks; j += 4) {
         const uint4 k = *reinterpret_cast<const uint4 *>(&sm.block_key[j]);
-        before += (k.x > key || (k.x == key && j < b)) + (k.y > key || (k.y == key && j + 1 < b)) +
-                  (k.z > key || (k.z == key && j + 2 < b)) + (k.w > key || (k.w == key && j + 3 < b));
+        before += block_before<BF16>(k.x, j, key, b) + block_before<BF16>(k.y, j + 1, key, b) +
+                  block_before<BF16>(k.z, j + 2, key, b) + block_before<BF16>(k.w, j + 3, key, b);
       }
       if (before < kb) sm.chosen[before] = b;
-      if (before == K - 1) sm.floor_key = key;
+      if (before == K - 1) sm.floor = key_value(BF16 ? key & 0xFFFF0000u : key);
     }
     __syncthreads();
-    const uint32_t floor_key = kb == K ? sm.floor_key : 0u;
+    const float floor = kb == K ? sm.floor : -INFINITY;
     // elements that reach the floor
     auto fetch_again = [&](int gi, int u) {
       const int v = v0 + gi * kGroup + u * 32 + lane;
@@ -346,10 +374,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
     auto reaching = [&](int gi, int u, const uint4 &r) {  // bit e: element e of the vector is the row's and reaches it
       const int v = v0 + gi * kGroup + u * 32 + lane, x0 = v * Row<BF16>::kPer - row.shift;
       uint32_t left = 0;
-      if (gi < groups && v < v1) {
+      if (gi < groups && v < v1 && largest<BF16>(r) >= floor) {  // (for one lane in dozens)
 #pragma unroll
         for (int e = 0; e < Row<BF16>::kPer; ++e)
-          if (x0 + e >= 0 && x0 + e < P.V && ordered_bits(element<BF16>(r, e)) >= floor_key) left |= 1u << e;
+          if (x0 + e >= 0 && x0 + e < P.V && element<BF16>(r, e) >= floor) left |= 1u << e;
       }
       return left;
     };
