@@ -150,8 +150,8 @@ __device__ __forceinline__ float largest(const uint4 &r) {
   const uint32_t t = max_nan_bf16x2(max_nan_bf16x2(r.x, r.y), max_nan_bf16x2(r.z, r.w));
   return max_nan(__uint_as_float(t << 16), __uint_as_float(t & 0xFFFF0000u));
 }
-// The number that an ordered key stands for.
-__device__ __forceinline__ float key_value(uint32_t key) {
+// The number that an ordered key stands for (-0 comes back as +0).
+__device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
@@ -169,7 +169,7 @@ __device__ __forceinline__ bool block_before(uint32_t key, int block, uint32_t o
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsParams P) {
+__global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const LogprobsParams P) {
   pdl_enter();
   __shared__ LogprobsSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
                   block_before<BF16>(k.z, j + 2, key, b) + block_before<BF16>(k.w, j + 3, key, b);
       }
       if (before < kb) sm.chosen[before] = b;
-      if (before == K - 1) sm.floor = key_value(BF16 ? key & 0xFFFF0000u : key);
+      if (before == K - 1) sm.floor = logit_of(BF16 ? key & 0xFFFF0000u : key);
     }
     __syncthreads();
     const float floor = kb == K ? sm.floor : -INFINITY;
@@ -497,8 +497,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
     }
     if (lane < K) {
       const uint32_t x = key_index(taken);
-      const float v = bad ? 0.0f : BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t *>(row_ptr)[x])
-                                        : reinterpret_cast<const float *>(row_ptr)[x];
+      const float v = bad ? 0.0f : logit_of(static_cast<uint32_t>(taken >> 32));
       P.top_ids[place * K + lane] = bad ? -1 : static_cast<int32_t>(x);
       P.top_logprobs[place * K + lane] = bad ? nan : (v - a.ref) / t - lnz;
     }
