@@ -395,12 +395,19 @@ sv_status spec_verify_check_kv_args(const spec_verify_config *config, const spec
  * [0, max_seq_len] or past its block table raises SV_DATA_BAD_PARAM and gives the request's rows
  * out = 0, lse = -infinity; a bad cu range raises SV_DATA_BAD_CU and leaves
  * the rows unwritten.  A NaN score makes its row NaN; nothing of a key that a
- * row does not see reaches it, whatever the cache holds there. */
+ * row does not see reaches it, whatever its scales are (in an e4m3 cache its
+ * bytes are numbers, as spec_verify_kv_write leaves them; behind seq_len they
+ * may be anything).  SV_DATA_COPY_TIMEOUT: a wait inside a kernel ran out and
+ * the outputs are not the result; never expected on a healthy GPU.
+ *
+ * The products take 16-bit operands: the cache's numbers and q (scaled by a
+ * power of two) are exact in them, the softmax's weights are rounded to 11
+ * bits.  Scores, sums and outputs are fp32 until out is rounded to bf16. */
 typedef struct spec_verify_attend_args {
   int32_t num_reqs;     /* N >= 0 (0 is a no-op) */
   int32_t max_spec_len; /* G: every gamma_i <= G */
   int32_t num_q_heads;  /* a multiple of num_kv_heads */
-  int32_t max_seq_len;  /* >= 0; bounds every seq_len, as block_table_stride * block_size does */
+  int32_t max_seq_len;  /* 0 .. 2^30; bounds every seq_len, as block_table_stride * block_size does */
   int32_t shared_prefix_len; /* 0 .. either bound, a multiple of block_size */
   uint32_t reserved;         /* 0 */
   int64_t num_draft_tokens_total; /* T = cu[N-1]; must equal N*G when cu == NULL */
@@ -416,9 +423,9 @@ typedef struct spec_verify_attend_args {
   void *out; /* [T+N, num_q_heads, head_dim] bf16 */
   int64_t out_token_stride, out_head_stride;
   float *lse;      /* [T+N, num_q_heads] contiguous, or NULL */
-  void *workspace; /* 16-byte aligned device scratch of spec_verify_attend_workspace_size bytes; contents need no
-                      initialisation and mean nothing after the call.  Calls that may run at the same time need
-                      one each. */
+  void *workspace; /* 16-byte aligned device scratch of spec_verify_attend_workspace_size bytes (0 for many calls
+                      without a shared prefix); contents need no initialisation and mean nothing after the call.
+                      Calls that may run at the same time need one each. */
   int64_t workspace_bytes;
   int32_t *status; /* [1] or NULL: SV_DATA_* bits OR-ed in */
 } spec_verify_attend_args;

@@ -65,6 +65,7 @@ sv_status check_attend_sizes(const spec_verify_config *c, const spec_verify_atte
   if (a->cache.num_kv_heads > 65535 || a->num_q_heads > 65535)
     return fail(SV_ERR_UNSUPPORTED, "more than 65535 heads");
   if (a->max_seq_len < 0) return fail(SV_ERR_INVALID_ARG, "max_seq_len < 0");
+  if (a->max_seq_len > (1 << 30)) return fail(SV_ERR_UNSUPPORTED, "max_seq_len %d > 2^30", a->max_seq_len);
   if (a->shared_prefix_len < 0 || a->shared_prefix_len > a->max_seq_len)
     return fail(SV_ERR_INVALID_ARG, "shared_prefix_len must be in [0, max_seq_len]");
   const int64_t rows = (a->num_draft_tokens_total + a->num_reqs) * static_cast<int64_t>(a->num_q_heads);

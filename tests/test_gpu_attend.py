@@ -182,6 +182,10 @@ CASES = {
                                                   prefix=144, uniform=True, kv_heads=1, group=3),
     "prefix, many rows, some inside it": dict(gammas=[3] * 64, lens=[300 - 4 * i for i in range(64)], prefix=272,
                                               group=4, kv_heads=1),
+    "prefix, one row tile": dict(gammas=[0] * 25, lens=[400 + i for i in range(25)], prefix=384, kv_heads=3, group=4,
+                                 uniform=True),
+    "prefix, a last row tile of its own": dict(gammas=[0] * 75, lens=[25730 + i % 5 for i in range(75)], prefix=25728,
+                                               kv_heads=1, group=4, dim=64, fmt="e4m3", uniform=True),
     "prefix, long": dict(gammas=[7] * 32, lens=[9000 + i for i in range(32)], prefix=8992, kv_heads=1, group=8,
                          uniform=True),
 }
@@ -307,6 +311,29 @@ def test_bad_pages_lengths_and_ranges():
     c["cu"][1] = 0
     out, lse, status = run(c)
     assert status & bits["BAD_CU"] and torch.equal(out[:2], clean[:2])
+
+
+def test_bad_page_in_a_shared_prefix():
+    """Its keys are left out of every row, in both ways of reading a prefix."""
+    for N in (3, 60):
+        c = make([4] * N, [400 + i for i in range(N)], prefix=384, uniform=True, seed=18)
+        cut = dict(c, table=torch.cat([c["table"][:, :5], c["table"][:, 6:]], 1), lens=[n - 16 for n in c["lens"]],
+                   prefix=368, seq_lens=c["seq_lens"] - 16)
+        ref, rlse, tol, ltol = reference(cut)
+        c["table"][:, 5] = c["cache"].num_blocks
+        out, lse, status = run(c)
+        assert status == sv.DATA_STATUS_BITS["BAD_SLOT"]
+        assert bool(((out.double() - ref).abs() <= tol).all()) and bool(((lse - rlse).abs() <= ltol).all())
+
+
+def test_calls_of_other_sizes_share_a_workspace():
+    a = make([4] * 60, [700 + i for i in range(60)], prefix=640, uniform=True, seed=19)
+    b = make([2, 0, 5], [3000, 20, 900], seed=20)
+    want_a, want_b = run(a), run(b)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    for c, want in ((a, want_a), (b, want_b), (a, want_a)):
+        got = run(c, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_offsets_beyond_32_bits():

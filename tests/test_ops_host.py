@@ -87,7 +87,7 @@ def attend_args():
     ("max_spec_len", -1, INVALID), ("num_draft_tokens_total", 5, INVALID), ("num_draft_tokens_total", -1, INVALID),
     ("num_q_heads", 7, INVALID), ("num_q_heads", 0, INVALID), ("cache.num_kv_heads", 0, INVALID),
     ("cache.num_kv_heads", 3, INVALID), ("cache.head_dim", 96, UNSUPPORTED), ("max_seq_len", -1, INVALID),
-    ("max_seq_len", 112, OK), ("max_seq_len", 113, OK), ("block_table_stride", -1, INVALID), ("block_table_stride", 1, INVALID), ("shared_prefix_len", 33, INVALID),
+    ("max_seq_len", 112, OK), ("max_seq_len", 113, OK), ("max_seq_len", 1 << 30, OK), ("max_seq_len", (1 << 30) + 1, UNSUPPORTED), ("block_table_stride", -1, INVALID), ("block_table_stride", 1, INVALID), ("shared_prefix_len", 33, INVALID),
     ("shared_prefix_len", -16, INVALID), ("shared_prefix_len", 112, INVALID), ("shared_prefix_len", 0, OK),
     ("reserved", 1, INVALID), ("reserved2", 1, INVALID), ("q", None, INVALID), ("out", None, INVALID),
     ("seq_lens", None, INVALID), ("block_tables", None, INVALID), ("cache.block_stride", 1 << 35, UNSUPPORTED), ("scale", float("nan"), INVALID),
