@@ -151,7 +151,7 @@ __device__ __forceinline__ void write_row(const AttendParams &P, const AttendPla
 
 struct JoinSmem {
   float m[kAttendWarps][32], l[kAttendWarps][32];
-  uint32_t top[kAttendWarps];
+  uint32_t top[kGroups * 8];  // largest finite |q| of a row
 };
 
 template <int D, int FMT, int NT>
@@ -215,10 +215,9 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
   // ---- the queries as operand fragments: 8 consecutive dimensions for each lane and pair of steps ----
   constexpr int kFrags = (NT * (D / 32) * 32 + kAttendThreads - 1) / kAttendThreads;  // of a thread
   uint4 *const qfrag = reinterpret_cast<uint4 *>(smem);
-  float c_tile;
+  const float c_all = P.scale * kLog2e;
   {
     uint4 x[kFrags];
-    uint32_t top = 0;
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
       const int at = f * kAttendThreads + tid, ln = at & 31, s2 = (at >> 5) % (D / 32), nt = (at >> 5) / (D / 32);
@@ -238,31 +237,38 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
           x[f].w = src[6] | static_cast<uint32_t>(src[7]) << 16;
         }
       }
+    }
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) {
+      const int at = f * kAttendThreads + tid, r = (at >> 5) / (D / 32) * 8 + (lane >> 2);
       const uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+      uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t a = w[e] << 16 & 0x7FFFFFFFu, b = w[e] & 0x7FFF0000u;
         if (a < 0x7F800000u) top = max(top, a);
         if (b < 0x7F800000u) top = max(top, b);
       }
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      if (c == 0 && r < NT * 8) atomicMax(&J.top[r], top);
     }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (lane == 0) J.top[warp] = top;
     __syncthreads();
-    top = max(max(J.top[0], J.top[1]), max(J.top[2], J.top[3]));
-    const int shift = query_shift(top);
-    const float up = pow2(shift);
-    c_tile = P.scale * kLog2e * pow2(-shift);
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
+      const int at = f * kAttendThreads + tid, r = (at >> 5) / (D / 32) * 8 + (lane >> 2);
+      const float up = pow2(query_shift(r < NT * 8 ? J.top[r] : 0u));
       uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         w[e] = pack_f16(bf16_bits_to_float(w[e] & 0xFFFFu) * up, bf16_bits_to_float(w[e] >> 16) * up);
-      if (f * kAttendThreads + tid < NT * (D / 32) * 32)
-        qfrag[f * kAttendThreads + tid] = make_uint4(w[0], w[1], w[2], w[3]);
+      if (at < NT * (D / 32) * 32) qfrag[at] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+  bool shifted = false;  // some row of the tile was multiplied by a power of two
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) shifted |= query_shift(J.top[nt * 8 + g]) != 0;
+  shifted = __any_sync(0xFFFFFFFFu, shifted);
   int limit[NT][2], low = 0x7FFFFFFF;  // of rows nt * 8 + 2c, + 1; low: keys below it are seen by every row of the tile
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -299,7 +305,7 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
     const uint8_t *const src = ring_ptr + stage * Y::kStage;
     if (++stage == kStages) stage = 0;
     const float2 sc = *reinterpret_cast<const float2 *>(src + Y::kScales + lane * 8);
-    float kc = sc.x * c_tile, lv, inv;
+    float kc = sc.x * c_all, lv, inv;
     value_scale_terms(sc.y, kc, lv, inv);
     // scores: keys g, g + 8 of each half mt of the tile, rows 2c, 2c + 1 of each group
     float s[2][NT][4];
@@ -344,6 +350,14 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         x[k][nt] = mul2(pair(s[k >> 1][nt][(k & 1) * 2], s[k >> 1][nt][(k & 1) * 2 + 1]), pair(f, f));
+    }
+    if (shifted) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const Pair back = pair(pow2(-query_shift(J.top[nt * 8 + 2 * c])), pow2(-query_shift(J.top[nt * 8 + 2 * c + 1])));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k][nt] = mul2(x[k][nt], back);
+      }
     }
     const int k0 = T.k_begin + (it * kAttendWarps + warp) * kKeys;
     if (k0 + kKeys > low) {  // some row does not see all of the tile
@@ -565,6 +579,7 @@ __global__ void __launch_bounds__(kAttendThreads, 2) attend_kernel(const AttendP
     T.whole = P.prefix == 0 && len <= L.own_chunk;
     if (T.k_end <= T.k_begin && !(T.whole && split == 0)) return;
   }
+  if (tid < kGroups * 8) join.top[tid] = 0;
   if (tid < T.rows) {
     const int t = div_by(T.r0 + tid, L.group);
     int token = t, limit;

@@ -111,12 +111,17 @@ __device__ __forceinline__ void value_scale_terms(float vs, float &kc, float &lv
   if (!ok && vs != 0.0f) kc = __uint_as_float(0x7FC00000u);
 }
 
-// The power of two that brings the largest finite |q| of a tile into
-// [2^14, 2^15), where bf16 numbers are exact in f16 down to 2^-28 of it (and
-// off by 2^-40 of it at most below that).
+// The exponent of the power of two that a row of q, whose largest finite |q| has
+// these bits, is multiplied by on its way to f16: a multiple of 16 that brings
+// the largest into [2^-1, 2^15).  bf16 numbers are exact there down to 2^-14
+// (2^-13 of the row's largest at least), and off by 2^-25 at most below.  Every
+// row has its own, so that nothing of a row (an idle request's, say) reaches
+// another; it is 0 for rows from 0.5 to 32767, and the code that puts another
+// one right runs only for tiles that hold such a row.
 __device__ __forceinline__ int query_shift(uint32_t top_bits) {
   if (top_bits == 0) return 0;
-  return min(126, 14 - (static_cast<int>(top_bits >> 23) - 127));
+  const int e = static_cast<int>(top_bits >> 23) - 127;
+  return max(-120, min(112, -16 * ((e + 1 + 256) / 16 - 16)));  // (both ends and their negatives are in pow2's range)
 }
 __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);

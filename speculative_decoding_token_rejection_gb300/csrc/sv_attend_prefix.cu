@@ -53,6 +53,7 @@ constexpr int kSoftmaxThreads = 256;
 constexpr int kVectorThreads = 64;
 constexpr int kPrefixThreads = kSoftmaxThreads + kVectorThreads + 64;
 constexpr int kVectorSlots = 4;
+constexpr int kWSlots = 8;  // the factors run at most four tiles, so four segments, ahead
 constexpr uint32_t kWaitPolls = 1u << 24;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRaise = 8;
@@ -64,8 +65,11 @@ struct alignas(16) Vectors {  // of one key tile
 };
 
 struct Control {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], vec_full[kVectorSlots], vec_empty[kVectorSlots], s_full[2], p_full[2], done;
-  uint32_t tmem, query_top, scale_top, abort;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], vec_full[kVectorSlots], vec_empty[kVectorSlots], s_full[2], p_full[2], q_full, done;
+  uint32_t tmem, abort;
+  float w[kWSlots];        // W of a segment
+  float w_of_warp[2][2];
+  float back[2 * kRowsTile];  // what undoes a row's power of two
 };
 
 static_assert(sizeof(Vectors) % 16 == 0, "every slot starts on a 16-byte boundary");
@@ -295,8 +299,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       mbar_init(&C.vec_full[i], kVectorThreads);
       mbar_init(&C.vec_empty[i], 8);
     }
+    mbar_init(&C.q_full, kSoftmaxThreads);
     mbar_init(&C.done, 1);
-    C.query_top = C.scale_top = C.abort = 0;
+    C.abort = 0;
     fence_mbar_init();
   }
   if (warp == 11) tmem_alloc(&C.tmem, 512);
@@ -304,14 +309,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
   __syncthreads();
   fence_after();
 
-  // Between two segments every role but the copies', which the stages' barriers pace, is done with the one before: A; the
-  // tops are cleared: B; queries and factors are there: C.
-  auto meet = []() { asm volatile("bar.sync 3, 352;" ::: "memory"); };
-  auto begin = [&]() {
-    meet();
-    if (tid == 0) C.query_top = C.scale_top = 0;
-    meet();
-  };
+  // Roles pass from one segment to the next on their own: the copies and the factors run ahead as far as their rings
+  // allow, the products wait for the queries, and the softmax warps, which write those, have seen the products end.
   int done_tiles = 0, done_segments = 0;  // (barrier phases run on from one segment to the next)
 
   // The softmax warps' scores need more registers than the others do: 256 * 208 + 128 * 88 = 384 * 168, what the CTA
@@ -329,25 +328,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     for (int u = blockIdx.x * L.units_cta; u < u_end;) {
     const Segment S = segment(u);
     const int h = S.h, r0 = S.r0, tiles = S.tiles, n = S.n, k_begin = S.k_begin, slot = S.slot;
-    // row `lane` of the warp's 32, then the lane's own four: g, g + 8, g + 16, g + 24
-    const int g = lane >> 2, c = lane & 3;
-    int my_token = -1, my_limit = 0x7FFFFFFF;
-    {
-      const int row = r0 + t * kRowsTile + w4 * 32 + lane;
-      if (row < L.rows) {
-        my_token = div_by(row, L.group);
-        my_limit = prefix_limit(P, my_token);
-        if (my_limit < 0) {  // nobody's row
-          my_token = -1;
-          my_limit = 0x7FFFFFFF;
-        }
-      }
-    }
-    const int low = __reduce_min_sync(0xFFFFFFFFu, my_limit);  // keys below it are seen by all rows of the warp
+    bool shifted = false;  // some row of the warp was multiplied by a power of two
     {  // the tile's queries: f16 with the CTA's common power of two
       uint4 x[D / 8];  // warp w4 takes rows 32 * w4 ..; a row is D/8 lanes
       constexpr int kLanes = D / 8, kRowsPass = 32 / kLanes, kQ = 32 / kRowsPass;
-      uint32_t top = 0;
       auto source = [&](int f) {  // null: no such row
         const int r = r0 + t * kRowsTile + w4 * 32 + f * kRowsPass + lane / kLanes;
         const int token = div_by(r, L.group), hq = h * P.group + r - token * P.group;
@@ -368,23 +352,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       }
 #pragma unroll
       for (int f = 0; f < kQ; ++f) {
-        const uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+        uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w}, top = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t lo_ = w[e] << 16 & 0x7FFFFFFFu, hi_ = w[e] & 0x7FFF0000u;
           if (lo_ < 0x7F800000u) top = max(top, lo_);
           if (hi_ < 0x7F800000u) top = max(top, hi_);
         }
-      }
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
-      begin();
-      if (lane == 0) atomicMax(&C.query_top, top);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float up = pow2(query_shift(*const_cast<volatile uint32_t *>(&C.query_top)));
 #pragma unroll
-      for (int f = 0; f < kQ; ++f) {
-        const int r = w4 * 32 + f * kRowsPass + lane / kLanes, col = lane % kLanes;
-        uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+        for (int b = kLanes / 2; b; b >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, b));
+        const int shift = query_shift(top), r = w4 * 32 + f * kRowsPass + lane / kLanes, col = lane % kLanes;
+        shifted |= shift != 0;
+        if (col == 0) C.back[t * kRowsTile + r] = pow2(-shift);
+        const float up = pow2(shift);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           w[e] = pack_f16(bf16_bits_to_float(w[e] & 0xFFFFu) * up, bf16_bits_to_float(w[e] >> 16) * up);
@@ -392,10 +372,26 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
                                    (((col & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_proxy_async_smem();
+      fence_before();
+      mbar_arrive(&C.q_full);
     }
-    fence_before();
-    meet();
-    fence_after();
+    shifted = __any_sync(0xFFFFFFFFu, shifted);  // (and the warp's entries of C.back are there)
+    __syncwarp();
+    // row `lane` of the warp's 32, then the lane's own four: g, g + 8, g + 16, g + 24
+    const int g = lane >> 2, c = lane & 3;
+    int my_token = -1, my_limit = 0x7FFFFFFF;
+    {
+      const int row = r0 + t * kRowsTile + w4 * 32 + lane;
+      if (row < L.rows) {
+        my_token = div_by(row, L.group);
+        my_limit = prefix_limit(P, my_token);
+        if (my_limit < 0) {  // nobody's row
+          my_token = -1;
+          my_limit = 0x7FFFFFFF;
+        }
+      }
+    }
+    const int low = __reduce_min_sync(0xFFFFFFFFu, my_limit);  // keys below it are seen by all rows of the warp
     const uint32_t s_addr = C.tmem + (static_cast<uint32_t>(w4 * 32) << 16) + t * 128;
     const uint32_t o_addr = s_addr + 256;
     constexpr uint32_t kHalf = 16u << 16;  // the warp's second 16 rows
@@ -420,7 +416,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       fence_after();
       const int k0 = k_begin + i * kKeyTile;
       const uint32_t any_dead = V.dead[0] | V.dead[1] | V.dead[2] | V.dead[3];
-      const bool cut = any_dead || k0 + kKeyTile > low;
+      const bool cut = any_dead || k0 + kKeyTile > low || shifted;
       const float over = fmaxf(V.top[0], V.top[1]);
       uint32_t s[2][64];  // rows g and g + 8 of each half of the warp's 32: the scores, then the exponents
       auto load_scores = [&]() {
@@ -465,8 +461,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         // x, and its largest.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         int limit[4];
+        Pair back[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) limit[x] = __shfl_sync(0xFFFFFFFFu, my_limit, x * 8 + g);
+        for (int x = 0; x < 4; ++x) {
+          limit[x] = __shfl_sync(0xFFFFFFFFu, my_limit, x * 8 + g);
+          const float f = C.back[t * kRowsTile + w4 * 32 + x * 8 + g];
+          back[x] = pair(f, f);
+        }
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const float2 f = V.kc[j * 4 + c];
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           const int key = k0 + j * 8 + 2 * c;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const Pair y = mul2(get(x, j), pair(f.x, f.y));
+            const Pair y = mul2(mul2(get(x, j), pair(f.x, f.y)), back[x]);  // (the key's scale may keep it finite)
             const float a_ = key >= limit[x] || (dead & 1u) ? -INFINITY : lo(y);
             const float b_ = key + 1 >= limit[x] || (dead & 2u) ? -INFINITY : hi(y);
             put(x, j, a_, b_);
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     if (ok) ok = wait_warp(C, &C.done, done_segments & 1);
     fence_after();
     if (t < tiles) {
-      const float w = ok ? __uint_as_float(*const_cast<volatile uint32_t *>(&C.scale_top)) : 0.0f;
+      const float w = ok ? *const_cast<volatile float *>(&C.w[done_segments % kWSlots]) : 0.0f;
       int64_t at[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -630,25 +631,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     pages(0);
     scales(0);
     pages(1);
-    begin();
-    {  // W: the power of two at the first tile's largest value scale
+    // W: the power of two at the first tile's largest value scale
+    float unscale;
+    {
       uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (vs[e] > 0.0f && vs[e] < INFINITY) top = max(top, __float_as_uint(vs[e]));
       top = __reduce_max_sync(0xFFFFFFFFu, top);
-      if (lane == 0) atomicMax(&C.scale_top, top & 0xFF800000u);
+      volatile float *const two = C.w_of_warp[done_segments & 1];
+      if (lane == 0) two[warp - 8] = __uint_as_float(top);
+      asm volatile("bar.sync 2, 64;" ::: "memory");
+      const uint32_t bits_w = __float_as_uint(fmaxf(two[0], two[1]));
+      const int e = bits_w >= 0x00800000u ? static_cast<int>(bits_w >> 23) - 127 : 0;
+      unscale = pow2(max(-126, min(126, -e)));
+      if (lt == 0) *const_cast<volatile float *>(&C.w[done_segments % kWSlots]) = 1.0f / unscale;
     }
-    fence_before();
-    meet();
-    fence_after();
-    const uint32_t wbits = *const_cast<volatile uint32_t *>(&C.scale_top);
-    const int wexp = wbits >= 0x00800000u ? static_cast<int>(wbits >> 23) - 127 : 0;
-    const float unscale = pow2(max(-126, min(126, -wexp)));
-    const float c_tile =
-        P.scale * kLog2e * pow2(-query_shift(*const_cast<volatile uint32_t *>(&C.query_top)));
-    asm volatile("bar.sync 2, 64;" ::: "memory");
-    if (lt == 0) *const_cast<volatile uint32_t *>(&C.scale_top) = __float_as_uint(1.0f / unscale);
+    const float c_all = P.scale * kLog2e;
     for (int i = 0; ok && i < n; ++i) {
       const int it = done_tiles + i, slot_v = it % kVectorSlots;
       ok = wait_warp(C, &C.vec_empty[slot_v], (it / kVectorSlots & 1) ^ 1);
@@ -658,7 +657,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = lt + e * kVectorThreads;
-        float kc = ks[e] * c_tile, v = vs[e];
+        float kc = ks[e] * c_all, v = vs[e];
         // (scale 0: a key whose page is outside the cache; keys behind the range are no row's)
         const bool good = v > 0.0f && v < INFINITY, out = in[e] && v == 0.0f;
         if (!good && v != 0.0f) kc = __uint_as_float(0x7FC00000u);
@@ -675,6 +674,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       pages(i + 2);
     }
     done_tiles += n;
+    ++done_segments;
     u += n;
     }
     if (P.status && (bad || !ok)) atomicOr(P.status, static_cast<int>(bad | (ok ? 0u : SV_DATA_COPY_TIMEOUT)));
@@ -754,11 +754,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     for (int u = blockIdx.x * L.units_cta; u < u_end;) {
       const Segment S = segment(u);
       const int n = S.n, tiles = S.tiles;
-      begin();
-      fence_before();
-      meet();
-      fence_after();
-      ok = ok && wait_warp(C, &C.k_full[done_tiles & 1], done_tiles >> 1 & 1);
+      ok = ok && wait_warp(C, &C.q_full, done_segments & 1) &&
+           wait_warp(C, &C.k_full[done_tiles & 1], done_tiles >> 1 & 1);
       if (ok) {
         fence_after();
         for (int t = 0; t < tiles; ++t) scores(t, done_tiles & 1);

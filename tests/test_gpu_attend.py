@@ -247,6 +247,21 @@ def test_nan_in_a_row_of_q_stays_in_it():
         assert torch.equal(out, clean)
 
 
+def test_rows_of_very_different_sizes():
+    """Every row has its own range: one of 1e30 (an idle request's left-overs, say) takes nothing from its neighbours."""
+    for kw in (dict(gammas=[3, 1, 2], lens=[100, 90, 40]),
+               dict(gammas=[4] * 40, lens=[330] * 40, prefix=320, uniform=True)):
+        c = make(seed=21, **kw)
+        c["q"] = c["q"].clone()
+        c["q"][1, 2] *= 1e30
+        c["q"][2] *= 1e-30
+        c["q"][3, 1] *= 3e5
+        c["q"][4] = 0
+        c["q"][5, 0] = 3.3e38
+        c["scale"] = 1e-3
+        check(c)
+
+
 def test_nan_key_reaches_only_the_rows_that_see_it():
     for kw in (dict(gammas=[3, 3], lens=[100, 90], block=16),
                dict(gammas=[3] * 40, lens=[100] * 40, prefix=64, uniform=True, block=16)):
