@@ -106,6 +106,26 @@ __device__ __forceinline__ unsigned long long warp_max64(unsigned long long v) {
   return static_cast<unsigned long long>(top) << 32 | l;
 }
 
+// A vector that the row does not fill, from its elements x .. ; the rest is -inf.  (Not inlined: four of them at each of
+// the loop's loads were most of the kernel's instructions, and fetching those stalled it.)
+template <bool BF16>
+__device__ __noinline__ uint4 edge_vector(const uint8_t *at, int x, int V) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (BF16) {
+      const uint16_t *p = reinterpret_cast<const uint16_t *>(at) + 2 * e;
+      const int y = x + 2 * e;
+      w[e] = (y >= 0 && y < V ? p[0] : 0xFF80u) | static_cast<uint32_t>(y + 1 >= 0 && y + 1 < V ? p[1] : 0xFF80u) << 16;
+    } else {
+      const uint32_t *p = reinterpret_cast<const uint32_t *>(at) + e;
+      const int y = x + e;
+      w[e] = y >= 0 && y < V ? *p : 0xFF800000u;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The row as 16-byte vectors: vector v holds elements v * kPer - shift ..
 template <bool BF16>
 struct Row {
@@ -113,24 +133,11 @@ struct Row {
   const uint8_t *base;  // of vector 0 (the 16-byte boundary at or below the row)
   int shift, V;
   __device__ __forceinline__ int vectors() const { return (V + shift + kPer - 1) / kPer; }
-  // A vector that the row does not fill is put together from its elements; the rest is -inf.
   __device__ __forceinline__ uint4 load(int v) const {
     const int x = v * kPer - shift;
-    if (x >= 0 && x + kPer <= V) return ld_stream_u4(reinterpret_cast<const uint4 *>(base) + v);
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (BF16) {
-        const uint16_t *p = reinterpret_cast<const uint16_t *>(base) + static_cast<int64_t>(v) * kPer + 2 * e;
-        const int y = x + 2 * e;
-        w[e] = (y >= 0 && y < V ? p[0] : 0xFF80u) | static_cast<uint32_t>(y + 1 >= 0 && y + 1 < V ? p[1] : 0xFF80u) << 16;
-      } else {
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(base) + static_cast<int64_t>(v) * kPer + e;
-        const int y = x + e;
-        w[e] = y >= 0 && y < V ? *p : 0xFF800000u;
-      }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    const uint8_t *at = base + static_cast<int64_t>(v) * 16;
+    if (x >= 0 && x + kPer <= V) return ld_stream_u4(reinterpret_cast<const uint4 *>(at));
+    return edge_vector<BF16>(at, x, V);
   }
 };
 
