@@ -175,6 +175,18 @@ __device__ __forceinline__ bool block_before(uint32_t key, int block, uint32_t o
   return BF16 ? key > other : key > other || (key == other && block < other_block);
 }
 
+// The elements of a vector at x0 .. that are the row's and reach the floor, among the candidates.  (Not inlined: there
+// are a few calls a row, from four places.)
+template <bool BF16>
+__device__ __noinline__ void take_candidates(LogprobsSmem &sm, uint4 r, int x0, int V, float floor) {
+  for (int e = 0; e < Row<BF16>::kPer; ++e) {
+    const float v = element<BF16>(r, e);
+    if (x0 + e < 0 || x0 + e >= V || !(v >= floor)) continue;
+    const int to = atomicAdd(&sm.count, 1);
+    if (to < kCandidates) sm.candidates[to] = pack_key(v, static_cast<uint32_t>(x0 + e));
+  }
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const LogprobsParams P) {
   pdl_enter();
@@ -395,19 +407,9 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) r[u] = fetch_again(gi, u);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const uint32_t left = reaching(gi, u, r[u]);
-          if (left) {
-            int to = atomicAdd(&sm.count, __popc(left));
-            const int x0 = (v0 + gi * kGroup + u * 32 + lane) * Row<BF16>::kPer - row.shift;
-#pragma unroll
-            for (int e = 0; e < Row<BF16>::kPer; ++e)
-              if (left >> e & 1u) {
-                if (to < kCandidates) sm.candidates[to] = pack_key(element<BF16>(r[u], e), static_cast<uint32_t>(x0 + e));
-                ++to;
-              }
-          }
-        }
+        for (int u = 0; u < kUnroll; ++u)
+          if (gi < groups && largest<BF16>(r[u]) >= floor)  // (for one lane in dozens)
+            take_candidates<BF16>(sm, r[u], (v0 + gi * kGroup + u * 32 + lane) * Row<BF16>::kPer - row.shift, P.V, floor);
       }
     if (tid < SV_MAX_TOP_LOGPROBS) sm.best[tid] = 0;
     __syncthreads();
