@@ -226,34 +226,31 @@ __device__ __forceinline__ bool wait_warp(Control &C, uint64_t *bar, uint32_t pa
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const AttendParams P, const AttendPlan L) {
   pdl_enter();
-  constexpr int kCols = D / 16;
+  // a thread takes eight bytes of a row and gives one 16-byte column: neighbouring lanes fill whole lines
+  constexpr int kCols = D / 8, kPieces = kKeyTile * kCols / kThreads;
   const int tile = blockIdx.x, h = blockIdx.y, side = blockIdx.z, col = threadIdx.x % kCols;
-  const uint8_t *const base = static_cast<const uint8_t *>(side ? P.c.v : P.c.k) + h * P.c.head_stride + col * 16;
+  const uint8_t *const base = static_cast<const uint8_t *>(side ? P.c.v : P.c.k) + h * P.c.head_stride + col * 8;
   uint8_t *const out = L.image + ((static_cast<int64_t>(h) * L.image_tiles + tile) * 2 + side) * (kKeyTile * D * 2);
-  uint4 raw[kKeyTile * kCols / kThreads];
+  uint2 raw[kPieces];
 #pragma unroll
-  for (int p = 0; p < kKeyTile * kCols / kThreads; ++p) {
+  for (int p = 0; p < kPieces; ++p) {
     const int r = p * (kThreads / kCols) + threadIdx.x / kCols, k = tile * kKeyTile + r;
-    raw[p] = make_uint4(0, 0, 0, 0);
+    raw[p] = make_uint2(0, 0);
     if (k < P.prefix) {
       const int x = div_by(k, L.page), page = P.tables[x];
       if (page >= 0 && page < P.c.num_blocks)
-        raw[p] = ld_stream_u4(reinterpret_cast<const uint4 *>(
+        raw[p] = __ldg(reinterpret_cast<const uint2 *>(
             base + page * P.c.block_stride + (k - x * P.c.block_size) * P.c.token_stride));
     }
   }
 #pragma unroll
-  for (int p = 0; p < kKeyTile * kCols / kThreads; ++p) {
+  for (int p = 0; p < kPieces; ++p) {
     const int r = p * (kThreads / kCols) + threadIdx.x / kCols;
-    uint32_t w[8];
+    uint32_t w[4];
     bytes_to_f16<FMT>(raw[p].x, w[0], w[1]);
     bytes_to_f16<FMT>(raw[p].y, w[2], w[3]);
-    bytes_to_f16<FMT>(raw[p].z, w[4], w[5]);
-    bytes_to_f16<FMT>(raw[p].w, w[6], w[7]);
-    uint8_t *dst = out + (col >> 2) * (kKeyTile * 128) + r * 128;
-    const int c0 = (col & 3) * 2;
-    *reinterpret_cast<uint4 *>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4 *>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+    *reinterpret_cast<uint4 *>(out + (col >> 3) * (kKeyTile * 128) + r * 128 + (((col & 7) ^ (r & 7)) << 4)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 

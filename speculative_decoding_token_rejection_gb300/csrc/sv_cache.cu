@@ -26,15 +26,12 @@ __device__ __forceinline__ void load_elements(const void *base, int64_t at, floa
   if (BF16) {
     const uint16_t *p = static_cast<const uint16_t *>(base) + at;
     if (VEC) {
+      uint32_t w[8];
+      ld_stream_32(p, w);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint4 r = ld_stream_u4(reinterpret_cast<const uint4 *>(p) + v);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x[v * 8 + 2 * c] = __uint_as_float(w[c] << 16);
-          x[v * 8 + 2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u);
-        }
+      for (int c = 0; c < 8; ++c) {
+        x[2 * c] = __uint_as_float(w[c] << 16);
+        x[2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u);
       }
     } else {
 #pragma unroll
@@ -44,12 +41,11 @@ __device__ __forceinline__ void load_elements(const void *base, int64_t at, floa
     const float *p = static_cast<const float *>(base) + at;
     if (VEC) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float4 r = ld_stream_f4(reinterpret_cast<const float4 *>(p) + v);
-        x[4 * v] = r.x;
-        x[4 * v + 1] = r.y;
-        x[4 * v + 2] = r.z;
-        x[4 * v + 3] = r.w;
+      for (int v = 0; v < 2; ++v) {
+        uint32_t w[8];
+        ld_stream_32(p + 8 * v, w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[8 * v + c] = __uint_as_float(w[c]);
       }
     } else {
 #pragma unroll
@@ -63,11 +59,10 @@ __device__ __forceinline__ void store_elements(void *base, int64_t at, const flo
   if (BF16) {
     uint16_t *p = static_cast<uint16_t *>(base) + at;
     if (VEC) {
+      uint32_t w[8];
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
-        reinterpret_cast<uint4 *>(p)[v] =
-            make_uint4(pack_bf16(x[8 * v], x[8 * v + 1]), pack_bf16(x[8 * v + 2], x[8 * v + 3]),
-                       pack_bf16(x[8 * v + 4], x[8 * v + 5]), pack_bf16(x[8 * v + 6], x[8 * v + 7]));
+      for (int c = 0; c < 8; ++c) w[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
+      st_32(p, w);
     } else {
 #pragma unroll
       for (int c = 0; c < kPer; ++c) p[c] = static_cast<uint16_t>(pack_bf16(x[c], 0.0f));
@@ -76,8 +71,12 @@ __device__ __forceinline__ void store_elements(void *base, int64_t at, const flo
     float *p = static_cast<float *>(base) + at;
     if (VEC) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        reinterpret_cast<float4 *>(p)[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+      for (int v = 0; v < 2; ++v) {
+        uint32_t w[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = __float_as_uint(x[8 * v + c]);
+        st_32(p + 8 * v, w);
+      }
     } else {
 #pragma unroll
       for (int c = 0; c < kPer; ++c) p[c] = x[c];

@@ -199,7 +199,7 @@ struct KvParams {
   int32_t *status;
   bool pdl;
 };
-// vec: every key / value row starts on a 16-byte boundary.
+// vec: every key / value row starts on a 32-byte boundary.
 cudaError_t launch_kv_write(const KvParams &p, bool bf16, bool vec, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvParams &p, bool bf16, bool vec, cudaStream_t stream);
 

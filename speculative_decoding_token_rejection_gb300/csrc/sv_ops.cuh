@@ -149,6 +149,19 @@ __device__ __forceinline__ int div_by(int n, const FastDiv &f) {
 
 namespace sv {
 
+// 32 bytes at once, from and to 32-byte boundaries: a whole sector a lane, where
+// two 16-byte accesses would touch every sector twice.
+__device__ __forceinline__ void ld_stream_32(const void *p, uint32_t r[8]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st_32(void *p, const uint32_t r[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Two fp32 numbers in one register pair, one instruction for both.
 struct Pair {
   unsigned long long v;

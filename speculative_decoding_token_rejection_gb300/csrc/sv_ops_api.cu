@@ -124,10 +124,10 @@ sv_status run_kv(spec_verify_t h, const spec_verify_kv_args *a, void *stream, bo
   p.status = a->status;
   p.pdl = !(h->cfg.flags & SV_FLAG_SERIAL_LAUNCH);
   const bool bf16 = a->dtype == SV_BF16;
-  const int per16 = bf16 ? 8 : 4;
-  const bool vec = aligned16(a->key) && aligned16(a->value) && a->key_token_stride % per16 == 0 &&
-                   a->key_head_stride % per16 == 0 && a->value_token_stride % per16 == 0 &&
-                   a->value_head_stride % per16 == 0;
+  const int per32 = bf16 ? 16 : 8;
+  const bool vec = ((reinterpret_cast<uintptr_t>(a->key) | reinterpret_cast<uintptr_t>(a->value)) & 31u) == 0 &&
+                   a->key_token_stride % per32 == 0 && a->key_head_stride % per32 == 0 &&
+                   a->value_token_stride % per32 == 0 && a->value_head_stride % per32 == 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = write ? sv::launch_kv_write(p, bf16, vec, s) : sv::launch_kv_read(p, bf16, vec, s);
   if (e != cudaSuccess) return fail(SV_ERR_CUDA, "KV cache launch: %s", cudaGetErrorString(e));
