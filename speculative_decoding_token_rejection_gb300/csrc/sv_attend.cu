@@ -649,6 +649,7 @@ int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 constexpr int kChunkStep = kAttendWarps * kKeys;  // a CTA's four warps take 32 keys each
 constexpr int kTensorKeys = 128, kTensorRows = 96;  // the prefix goes to the tensor-memory kernel from here on
 constexpr int kTensorLeast = 4;  // key tiles of a CTA of that kernel, where the prefix has as many
+constexpr int kTensorBegin = 7;  // and what beginning another (kv head, row tile) costs it, in key tiles
 constexpr int kChunkMost = 8192;                  // so that the longest request is no long tail
 
 // Chunks for `keys` keys when `base` CTAs work on every chunk: enough to give
@@ -683,10 +684,16 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
                               L.own_splits, L.own_chunk));
   L.own_splits = std::max(1, L.own_splits);
   const int64_t image_tiles = ceil_div(p.prefix, kPrefixKeyTile), tensor_tiles = ceil_div(L.rows, kPrefixRowTile);
-  const int64_t units = tensor_tiles * p.c.num_kv_heads * image_tiles;
+  const int64_t items = tensor_tiles * p.c.num_kv_heads, tiles = items * image_tiles;
+  // an item begun costs a CTA about kTensorBegin tiles' time: so many empty units lie between two items where CTAs get
+  // more than the least, and one that begins a second item gets fewer tiles (64 requests x 5 tokens over 8192 keys: 123
+  // us the whole call, with no empty units 132, with 4 of them 126, with 10 125; 512 x 8 over 16384: 1073 to 1078 all)
+  const int64_t gap = tiles > static_cast<int64_t>(num_sms) * kTensorLeast ? kTensorBegin : 0;
+  const int64_t units = items * (image_tiles + gap) - gap;
   if (p.prefix >= kTensorKeys && L.rows >= kTensorRows && units <= 0x3FFFFFFF) {
     L.tensor_tiles = static_cast<int32_t>(tensor_tiles);
     L.image_tiles = static_cast<int32_t>(image_tiles);
+    L.period = static_cast<int32_t>(image_tiles + gap);
     L.units = static_cast<int32_t>(units);
     L.units_cta = std::max(ceil_div(units, num_sms), std::min(kTensorLeast, L.image_tiles));
     L.prefix_splits = L.image_tiles == 1 ? 1 : (L.image_tiles - 2) / L.units_cta + 2;  // an item's CTAs at most

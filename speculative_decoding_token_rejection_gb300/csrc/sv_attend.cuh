@@ -31,7 +31,8 @@ struct AttendPlan {
   int32_t prefix_splits, prefix_chunk;
   int32_t prefix_tiles, prefix_items;  // prefix row tiles and CTAs of the warp-streaming kernel (0 items: not its work)
   int32_t tensor_tiles;                // prefix row tiles of the tensor-memory kernel (0: not its work)
-  int32_t units, units_cta;            // its (kv head, row tile, key tile) units, and a CTA's share of them
+  // its (kv head, row tile)s, one each `period` units, of which the first image_tiles are key tiles; a CTA's share
+  int32_t units, units_cta, period;
   int32_t own_splits, own_chunk, own_tiles;
   int32_t slots;          // partial results of a row
   bool ovec;              // output rows allow 8-byte stores
@@ -52,7 +53,7 @@ constexpr int kPrefixRowTile = 256, kPrefixKeyTile = 128;
 // the (T + N) * group.
 __device__ __forceinline__ int prefix_slots(const AttendPlan &L, int h, int local, int row_tile) {
   if (L.tensor_tiles == 0) return L.prefix_splits;
-  const int first = (h * L.tensor_tiles + local / row_tile) * L.image_tiles;
+  const int first = (h * L.tensor_tiles + local / row_tile) * L.period;
   return (first + L.image_tiles - 1) / L.units_cta - first / L.units_cta + 1;
 }
 

@@ -11,11 +11,12 @@
 // cycles each, most of it page look-ups and shared-memory stores, against 2050
 // of the products: 64 requests x 5 tokens over 8192 keys 100 us.)
 // An item is 256 rows (two accumulator tiles of 128) of one kv head; the units
-// of work, its key tiles, are dealt evenly over as many CTAs as there are SMs,
-// item after item, so an item's keys are cut only where one CTA's share ends.
+// of work, its key tiles, are dealt over as many CTAs as there are SMs, item
+// after item, so an item's keys are cut only where one CTA's share ends; empty
+// units between the items stand for the time that beginning another one takes.
 // In a CTA:
 //
-//   warps 0-3, 4-7  softmax of a row tile, a thread a row: reads S from tensor
+//   warps 0-3, 4-7  softmax of a row tile, 32 rows a warp: reads S from tensor
 //                   memory, writes the weights back over it as f16
 //   warps 8, 9      the keys' factors, four tiles ahead
 //   warp 10         copies K and V tiles, two deep
@@ -33,11 +34,17 @@
 // 1.28 ms for 512 requests x 8 tokens over 16384 keys.)
 //
 // Numbers.  x = (q . b) * (scale * log2 e * key_scale) as in sv_attend.cuh, but
-// the value scales are kept out of the exponent: w = 2^(x - m), l = sum w, P = w * value_scale / W with W
-// a power of two near the first tile's largest value scale, O = W * sum P b.
-// Any m gives the same quotient O / l; it is raised to the largest x + log2(
-// value_scale / W) when that passes it by 8, so P stays below 2^8.  Whether it
-// may have is seen from max x and the tile's largest value scale alone.
+// the value scales are kept out of the exponent: w = 2^(x - m), l = sum w,
+// P = w * value_scale / W with W a power of two near the first tile's largest
+// value scale, O = W * sum P b.  Any m gives the same quotient O / l; it is
+// raised to the largest x + log2(value_scale / W) when that passes it by 8, so
+// P stays below 2^8.  Whether it may have is seen from max x and the tile's
+// largest value scale alone.
+//
+// Measured: 512 requests x 8 tokens over 16384 keys, 829 us of the call's 1.07
+// ms: 1.33 PFLOP/s, 70 % of a plain matrix product's rate.  A key tile takes a
+// CTA 3400 cycles, of which a softmax warp works for 1800 and waits for its row
+// tile's products for 1250; a segment adds 25000 (queries in, results out).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -271,7 +278,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
   const int H = P.c.num_kv_heads;
   const int T = L.image_tiles, u_end = min(L.units, static_cast<int>(blockIdx.x + 1) * L.units_cta);
   auto segment = [&](int u) {  // the CTA's work from unit u on: key tiles of one item (kv head, 256 rows)
-    const int item = u / T, t0 = u - item * T;
+    const int item = u / L.period, t0 = u - item * L.period;
     Segment s;
     s.h = item / L.tensor_tiles;
     s.r0 = (item - s.h * L.tensor_tiles) * 2 * kRowsTile;
@@ -279,9 +286,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     s.n = min(T - t0, u_end - u);
     s.k_begin = t0 * kKeyTile;
     s.k_end = min(P.prefix, s.k_begin + s.n * kKeyTile);
-    s.slot = static_cast<int>(blockIdx.x) - item * T / L.units_cta;
+    s.slot = static_cast<int>(blockIdx.x) - item * L.period / L.units_cta;
     return s;
   };
+  auto tile_from = [&](int u) {  // the first key tile's unit from u on
+    const int t = u % L.period;
+    return t < T ? u : u + L.period - t;
+  };
+  const int u_begin = tile_from(blockIdx.x * L.units_cta);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -322,272 +334,272 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     // -------------------------------------------------------------------
     const int t = warp >> 2, w4 = warp & 3;
     int mine = 0;  // key tiles of this row tile so far
-    for (int u = blockIdx.x * L.units_cta; u < u_end;) {
-    const Segment S = segment(u);
-    const int h = S.h, r0 = S.r0, tiles = S.tiles, n = S.n, k_begin = S.k_begin, slot = S.slot;
-    bool shifted = false;  // some row of the warp was multiplied by a power of two
-    {  // the tile's queries: f16 with the CTA's common power of two
-      uint4 x[D / 8];  // warp w4 takes rows 32 * w4 ..; a row is D/8 lanes
-      constexpr int kLanes = D / 8, kRowsPass = 32 / kLanes, kQ = 32 / kRowsPass;
-      auto source = [&](int f) {  // null: no such row
-        const int r = r0 + t * kRowsTile + w4 * 32 + f * kRowsPass + lane / kLanes;
-        const int token = div_by(r, L.group), hq = h * P.group + r - token * P.group;
-        return r < L.rows ? P.q + token * P.q_token + hq * P.q_head + lane % kLanes * 8 : nullptr;
-      };
+    for (int u = u_begin; u < u_end;) {
+      const Segment S = segment(u);
+      const int h = S.h, r0 = S.r0, tiles = S.tiles, n = S.n, k_begin = S.k_begin, slot = S.slot;
+      bool shifted = false;  // some row of the warp was multiplied by a power of two
+      {  // the tile's queries: f16, each row with its own power of two
+        uint4 x[D / 8];  // warp w4 takes rows 32 * w4 ..; a row is D/8 lanes
+        constexpr int kLanes = D / 8, kRowsPass = 32 / kLanes, kQ = 32 / kRowsPass;
+        auto source = [&](int f) {  // null: no such row
+          const int r = r0 + t * kRowsTile + w4 * 32 + f * kRowsPass + lane / kLanes;
+          const int token = div_by(r, L.group), hq = h * P.group + r - token * P.group;
+          return r < L.rows ? P.q + token * P.q_token + hq * P.q_head + lane % kLanes * 8 : nullptr;
+        };
 #pragma unroll
-      for (int f = 0; f < kQ; ++f) x[f] = make_uint4(0, 0, 0, 0);
-      if (L.qvec) {  // (all loads before the first use)
+        for (int f = 0; f < kQ; ++f) x[f] = make_uint4(0, 0, 0, 0);
+        if (L.qvec) {  // (all loads before the first use)
 #pragma unroll
-        for (int f = 0; f < kQ; ++f)
-          if (const uint16_t *src = source(f)) x[f] = *reinterpret_cast<const uint4 *>(src);
-      } else {
+          for (int f = 0; f < kQ; ++f)
+            if (const uint16_t *src = source(f)) x[f] = *reinterpret_cast<const uint4 *>(src);
+        } else {
 #pragma unroll
-        for (int f = 0; f < kQ; ++f)
-          if (const uint16_t *src = source(f))
-            x[f] = make_uint4(src[0] | static_cast<uint32_t>(src[1]) << 16, src[2] | static_cast<uint32_t>(src[3]) << 16,
-                              src[4] | static_cast<uint32_t>(src[5]) << 16, src[6] | static_cast<uint32_t>(src[7]) << 16);
-      }
-#pragma unroll
-      for (int f = 0; f < kQ; ++f) {
-        uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w}, top = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t lo_ = w[e] << 16 & 0x7FFFFFFFu, hi_ = w[e] & 0x7FFF0000u;
-          if (lo_ < 0x7F800000u) top = max(top, lo_);
-          if (hi_ < 0x7F800000u) top = max(top, hi_);
+          for (int f = 0; f < kQ; ++f)
+            if (const uint16_t *src = source(f))
+              x[f] = make_uint4(src[0] | static_cast<uint32_t>(src[1]) << 16, src[2] | static_cast<uint32_t>(src[3]) << 16,
+                                src[4] | static_cast<uint32_t>(src[5]) << 16, src[6] | static_cast<uint32_t>(src[7]) << 16);
         }
 #pragma unroll
-        for (int b = kLanes / 2; b; b >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, b));
-        const int shift = query_shift(top), r = w4 * 32 + f * kRowsPass + lane / kLanes, col = lane % kLanes;
-        shifted |= shift != 0;
-        if (col == 0) C.back[t * kRowsTile + r] = pow2(-shift);
-        const float up = pow2(shift);
+        for (int f = 0; f < kQ; ++f) {
+          uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w}, top = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = pack_f16(bf16_bits_to_float(w[e] & 0xFFFFu) * up, bf16_bits_to_float(w[e] >> 16) * up);
-        *reinterpret_cast<uint4 *>(smem + Y::kQ + t * Y::kTile + (col >> 3) * (kRowsTile * 128) + r * 128 +
-                                   (((col & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      fence_proxy_async_smem();
-      fence_before();
-      mbar_arrive(&C.q_full);
-    }
-    shifted = __any_sync(0xFFFFFFFFu, shifted);  // (and the warp's entries of C.back are there)
-    __syncwarp();
-    // row `lane` of the warp's 32, then the lane's own four: g, g + 8, g + 16, g + 24
-    const int g = lane >> 2, c = lane & 3;
-    int my_token = -1, my_limit = 0x7FFFFFFF;
-    {
-      const int row = r0 + t * kRowsTile + w4 * 32 + lane;
-      if (row < L.rows) {
-        my_token = div_by(row, L.group);
-        my_limit = prefix_limit(P, my_token);
-        if (my_limit < 0) {  // nobody's row
-          my_token = -1;
-          my_limit = 0x7FFFFFFF;
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo_ = w[e] << 16 & 0x7FFFFFFFu, hi_ = w[e] & 0x7FFF0000u;
+            if (lo_ < 0x7F800000u) top = max(top, lo_);
+            if (hi_ < 0x7F800000u) top = max(top, hi_);
+          }
+#pragma unroll
+          for (int b = kLanes / 2; b; b >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, b));
+          const int shift = query_shift(top), r = w4 * 32 + f * kRowsPass + lane / kLanes, col = lane % kLanes;
+          shifted |= shift != 0;
+          if (col == 0) C.back[t * kRowsTile + r] = pow2(-shift);
+          const float up = pow2(shift);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_f16(bf16_bits_to_float(w[e] & 0xFFFFu) * up, bf16_bits_to_float(w[e] >> 16) * up);
+          *reinterpret_cast<uint4 *>(smem + Y::kQ + t * Y::kTile + (col >> 3) * (kRowsTile * 128) + r * 128 +
+                                     (((col & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        fence_proxy_async_smem();
+        fence_before();
+        mbar_arrive(&C.q_full);
       }
-    }
-    const int low = __reduce_min_sync(0xFFFFFFFFu, my_limit);  // keys below it are seen by all rows of the warp
-    const uint32_t s_addr = C.tmem + (static_cast<uint32_t>(w4 * 32) << 16) + t * 128;
-    const uint32_t o_addr = s_addr + 256;
-    constexpr uint32_t kHalf = 16u << 16;  // the warp's second 16 rows
-    float m[4];
-    Pair l[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      m[x] = -INFINITY;
-      l[x] = pair(0.0f, 0.0f);
-    }
-    bool ok = true;
-    for (int i = 0; ok && i < n; ++i) {
-      const int it = done_tiles + i;
-      const Vectors &V = vec[it % kVectorSlots];
-      ok = wait_warp(C, &C.vec_full[it % kVectorSlots], it / kVectorSlots & 1);
-      if (t >= tiles) {  // (no rows: the factors' slot is handed back)
-        if (ok && lane == 0) mbar_arrive(&C.vec_empty[it % kVectorSlots]);
-        continue;
-      }
-      ok = ok && wait_warp(C, &C.s_full[t], (mine + i) & 1);
-      if (!ok) break;
-      fence_after();
-      const int k0 = k_begin + i * kKeyTile;
-      const uint32_t any_dead = V.dead[0] | V.dead[1] | V.dead[2] | V.dead[3];
-      const bool cut = any_dead || k0 + kKeyTile > low || shifted;
-      const float over = fmaxf(V.top[0], V.top[1]);
-      uint32_t s[2][64];  // rows g and g + 8 of each half of the warp's 32: the scores, then the exponents
-      auto load_scores = [&]() {
-        tmem_load_128(s_addr, s[0]);
-        tmem_load_128(s_addr + kHalf, s[1]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_wait_load(s[0] + 16 * q);
-          tmem_wait_load(s[1] + 16 * q);
-        }
-      };
-      auto get = [&](int x, int j) {  // columns 8j + 2c, + 1 of row x
-        return pair(__uint_as_float(s[x >> 1][j * 4 + (x & 1) * 2]), __uint_as_float(s[x >> 1][j * 4 + (x & 1) * 2 + 1]));
-      };
-      auto put = [&](int x, int j, float a, float b) {
-        s[x >> 1][j * 4 + (x & 1) * 2] = __float_as_uint(a);
-        s[x >> 1][j * 4 + (x & 1) * 2 + 1] = __float_as_uint(b);
-      };
-      load_scores();
-      // Most tiles: every row sees all keys and has a maximum that holds.  One fused operation an exponent then (below
-      // 2^24 its exact product differs from a rounded one by less than the 2^8 that a weight may grow).
-      bool plain = !cut;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) plain = plain && fabsf(m[x]) < 16777216.0f;
-      plain = __all_sync(0xFFFFFFFFu, plain);
-      if (plain) {
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 f = V.kc[j * 4 + c];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const Pair y = fma2(get(x, j), pair(f.x, f.y), pair(-m[x], -m[x]));
-            put(x, j, lo(y), hi(y));
-            top[x] = fmaxf(top[x], fmaxf(lo(y), hi(y)));
+      shifted = __any_sync(0xFFFFFFFFu, shifted);  // (and the warp's entries of C.back are there)
+      __syncwarp();
+      // row `lane` of the warp's 32, then the lane's own four: g, g + 8, g + 16, g + 24
+      const int g = lane >> 2, c = lane & 3;
+      int my_token = -1, my_limit = 0x7FFFFFFF;
+      {
+        const int row = r0 + t * kRowsTile + w4 * 32 + lane;
+        if (row < L.rows) {
+          my_token = div_by(row, L.group);
+          my_limit = prefix_limit(P, my_token);
+          if (my_limit < 0) {  // nobody's row
+            my_token = -1;
+            my_limit = 0x7FFFFFFF;
           }
         }
-        plain = __all_sync(0xFFFFFFFFu, !(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) + over > kRaise));
-        if (!plain) load_scores();  // (they are still there)
       }
-      if (!plain) {
-        // x, and its largest.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        int limit[4];
-        Pair back[4];
+      const int low = __reduce_min_sync(0xFFFFFFFFu, my_limit);  // keys below it are seen by all rows of the warp
+      const uint32_t s_addr = C.tmem + (static_cast<uint32_t>(w4 * 32) << 16) + t * 128;
+      const uint32_t o_addr = s_addr + 256;
+      constexpr uint32_t kHalf = 16u << 16;  // the warp's second 16 rows
+      float m[4];
+      Pair l[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          limit[x] = __shfl_sync(0xFFFFFFFFu, my_limit, x * 8 + g);
-          const float f = C.back[t * kRowsTile + w4 * 32 + x * 8 + g];
-          back[x] = pair(f, f);
+      for (int x = 0; x < 4; ++x) {
+        m[x] = -INFINITY;
+        l[x] = pair(0.0f, 0.0f);
+      }
+      bool ok = true;
+      for (int i = 0; ok && i < n; ++i) {
+        const int it = done_tiles + i;
+        const Vectors &V = vec[it % kVectorSlots];
+        ok = wait_warp(C, &C.vec_full[it % kVectorSlots], it / kVectorSlots & 1);
+        if (t >= tiles) {  // (no rows: the factors' slot is handed back)
+          if (ok && lane == 0) mbar_arrive(&C.vec_empty[it % kVectorSlots]);
+          continue;
         }
+        ok = ok && wait_warp(C, &C.s_full[t], (mine + i) & 1);
+        if (!ok) break;
+        fence_after();
+        const int k0 = k_begin + i * kKeyTile;
+        const uint32_t any_dead = V.dead[0] | V.dead[1] | V.dead[2] | V.dead[3];
+        const bool cut = any_dead || k0 + kKeyTile > low || shifted;
+        const float over = fmaxf(V.top[0], V.top[1]);
+        uint32_t s[2][64];  // rows g and g + 8 of each half of the warp's 32: the scores, then the exponents
+        auto load_scores = [&]() {
+          tmem_load_128(s_addr, s[0]);
+          tmem_load_128(s_addr + kHalf, s[1]);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 f = V.kc[j * 4 + c];
-          const uint32_t dead = V.dead[j >> 2] >> ((j & 3) * 8 + 2 * c);
-          const int key = k0 + j * 8 + 2 * c;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const Pair y = mul2(mul2(get(x, j), pair(f.x, f.y)), back[x]);  // (the key's scale may keep it finite)
-            const float a_ = key >= limit[x] || (dead & 1u) ? -INFINITY : lo(y);
-            const float b_ = key + 1 >= limit[x] || (dead & 2u) ? -INFINITY : hi(y);
-            put(x, j, a_, b_);
-            top[x] = fmaxf(top[x], fmaxf(a_, b_));
+          for (int q = 0; q < 4; ++q) {
+            tmem_wait_load(s[0] + 16 * q);
+            tmem_wait_load(s[1] + 16 * q);
           }
-        }
-        bool raise = false;
+        };
+        auto get = [&](int x, int j) {  // columns 8j + 2c, + 1 of row x
+          return pair(__uint_as_float(s[x >> 1][j * 4 + (x & 1) * 2]), __uint_as_float(s[x >> 1][j * 4 + (x & 1) * 2 + 1]));
+        };
+        auto put = [&](int x, int j, float a, float b) {
+          s[x >> 1][j * 4 + (x & 1) * 2] = __float_as_uint(a);
+          s[x >> 1][j * 4 + (x & 1) * 2 + 1] = __float_as_uint(b);
+        };
+        load_scores();
+        // Most tiles: every row sees all keys and has a maximum that holds.  One fused operation an exponent then (below
+        // 2^24 its exact product differs from a rounded one by less than the 2^8 that a weight may grow).
+        bool plain = !cut;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) raise |= top[x] + over > m[x] + kRaise || (m[x] == -INFINITY && top[x] > -INFINITY);
-        if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
-          float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, r[4];
+        for (int x = 0; x < 4; ++x) plain = plain && fabsf(m[x]) < 16777216.0f;
+        plain = __all_sync(0xFFFFFFFFu, plain);
+        if (plain) {
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float2 f = V.vr[j * 4 + c];
-            const Pair lv = pair(__log2f(f.x), __log2f(f.y));
+            const float2 f = V.kc[j * 4 + c];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const Pair y = add2(get(x, j), lv);
-              most[x] = fmaxf(most[x], fmaxf(lo(y), hi(y)));
+              const Pair y = fma2(get(x, j), pair(f.x, f.y), pair(-m[x], -m[x]));
+              put(x, j, lo(y), hi(y));
+              top[x] = fmaxf(top[x], fmaxf(lo(y), hi(y)));
+            }
+          }
+          plain = __all_sync(0xFFFFFFFFu, !(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) + over > kRaise));
+          if (!plain) load_scores();  // (they are still there)
+        }
+        if (!plain) {
+          // x, and its largest.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          int limit[4];
+          Pair back[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            limit[x] = __shfl_sync(0xFFFFFFFFu, my_limit, x * 8 + g);
+            const float f = C.back[t * kRowsTile + w4 * 32 + x * 8 + g];
+            back[x] = pair(f, f);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 f = V.kc[j * 4 + c];
+            const uint32_t dead = V.dead[j >> 2] >> ((j & 3) * 8 + 2 * c);
+            const int key = k0 + j * 8 + 2 * c;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const Pair y = mul2(mul2(get(x, j), pair(f.x, f.y)), back[x]);  // (the key's scale may keep it finite)
+              const float a_ = key >= limit[x] || (dead & 1u) ? -INFINITY : lo(y);
+              const float b_ = key + 1 >= limit[x] || (dead & 2u) ? -INFINITY : hi(y);
+              put(x, j, a_, b_);
+              top[x] = fmaxf(top[x], fmaxf(a_, b_));
+            }
+          }
+          bool raise = false;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) raise |= top[x] + over > m[x] + kRaise || (m[x] == -INFINITY && top[x] > -INFINITY);
+          if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
+            float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, r[4];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 f = V.vr[j * 4 + c];
+              const Pair lv = pair(__log2f(f.x), __log2f(f.y));
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const Pair y = add2(get(x, j), lv);
+                most[x] = fmaxf(most[x], fmaxf(lo(y), hi(y)));
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 1));
+              most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 2));
+              const float next = most[x] > m[x] + kRaise || m[x] == -INFINITY ? most[x] : m[x];
+              r[x] = m[x] == -INFINITY ? 1.0f : exp2_approx(m[x] - next);  // (without a maximum O and l are zeros or NaN)
+              m[x] = next;
+              l[x] = mul2(l[x], pair(r[x], r[x]));
+            }
+            if (i > 0) {
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  uint32_t o[16];
+                  tmem_load_32(o_addr + half * kHalf + q * 32, o);
+                  tmem_wait_load(o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r[half * 2 + (e >> 1 & 1)]);
+                  tmem_store_32(o_addr + half * kHalf + q * 32, o);
+                }
             }
           }
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 1));
-            most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 2));
-            const float next = most[x] > m[x] + kRaise || m[x] == -INFINITY ? most[x] : m[x];
-            r[x] = m[x] == -INFINITY ? 1.0f : exp2_approx(m[x] - next);  // (without a maximum O and l are zeros or NaN)
-            m[x] = next;
-            l[x] = mul2(l[x], pair(r[x], r[x]));
-          }
-          if (i > 0) {
+            const Pair neg = m[x] == -INFINITY ? pair(0.0f, 0.0f) : pair(-m[x], -m[x]);
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q)
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint32_t o[16];
-                tmem_load_32(o_addr + half * kHalf + q * 32, o);
-                tmem_wait_load(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r[half * 2 + (e >> 1 & 1)]);
-                tmem_store_32(o_addr + half * kHalf + q * 32, o);
-              }
+            for (int j = 0; j < 16; ++j) {
+              const Pair y = add2(get(x, j), neg);
+              put(x, j, lo(y), hi(y));
+            }
           }
         }
+        // the weights, sixteen columns of a half at a time
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[2][8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = V.vr[(q * 4 + j) * 4 + c];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const Pair y = get(x, q * 4 + j), w = pair(exp2_approx(lo(y)), exp2_approx(hi(y)));
+              l[x] = add2(l[x], w);
+              const Pair v = mul2(w, pair(f.x, f.y));
+              p[x >> 1][j * 2 + (x & 1)] = pack_f16(lo(v), hi(v));
+            }
+          }
+          tmem_store_pairs(s_addr + q * 16, p[0]);
+          tmem_store_pairs(s_addr + kHalf + q * 16, p[1]);
+        }
+        tmem_wait_store();
+        fence_before();
+        mbar_arrive(&C.p_full[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C.vec_empty[it % kVectorSlots]);
+      }
+      // the partial result
+      if (ok) ok = wait_warp(C, &C.done, done_segments & 1);
+      fence_after();
+      if (t < tiles) {
+        const float w = ok ? *const_cast<volatile float *>(&C.w[done_segments % kWSlots]) : 0.0f;
+        int64_t at[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const Pair neg = m[x] == -INFINITY ? pair(0.0f, 0.0f) : pair(-m[x], -m[x]);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const Pair y = add2(get(x, j), neg);
-            put(x, j, lo(y), hi(y));
-          }
+          const int row = r0 + t * kRowsTile + w4 * 32 + x * 8 + g;
+          const int token = __shfl_sync(0xFFFFFFFFu, my_token, x * 8 + g);
+          at[x] = token < 0 ? -1 : (static_cast<int64_t>(token) * P.Hq + h * P.group + row - token * P.group) * L.slots + slot;
+          float sum = lo(l[x]) + hi(l[x]);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+          if (c == 0 && at[x] >= 0) L.part_ml[at[x]] = ok ? make_float2(m[x], sum) : make_float2(-INFINITY, 0.0f);
         }
-      }
-      // the weights, sixteen columns of a half at a time
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t p[2][8];
+        for (int q = 0; q < D / 32; ++q)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = V.vr[(q * 4 + j) * 4 + c];
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[16];
+            tmem_load_32(o_addr + half * kHalf + q * 32, o);
+            tmem_wait_load(o);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const Pair y = get(x, q * 4 + j), w = pair(exp2_approx(lo(y)), exp2_approx(hi(y)));
-            l[x] = add2(l[x], w);
-            const Pair v = mul2(w, pair(f.x, f.y));
-            p[x >> 1][j * 2 + (x & 1)] = pack_f16(lo(v), hi(v));
+            for (int e = 0; e < 16; e += 2) {
+              const int x = half * 2 + (e >> 1 & 1);
+              if (ok && at[x] >= 0)
+                *reinterpret_cast<float2 *>(L.part_o + at[x] * D + q * 32 + (e >> 2) * 8 + 2 * c) =
+                    make_float2(__uint_as_float(o[e]) * w, __uint_as_float(o[e + 1]) * w);
+            }
           }
-        }
-        tmem_store_pairs(s_addr + q * 16, p[0]);
-        tmem_store_pairs(s_addr + kHalf + q * 16, p[1]);
       }
-      tmem_wait_store();
       fence_before();
-      mbar_arrive(&C.p_full[t]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&C.vec_empty[it % kVectorSlots]);
-    }
-    // the partial result
-    if (ok) ok = wait_warp(C, &C.done, done_segments & 1);
-    fence_after();
-    if (t < tiles) {
-      const float w = ok ? *const_cast<volatile float *>(&C.w[done_segments % kWSlots]) : 0.0f;
-      int64_t at[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = r0 + t * kRowsTile + w4 * 32 + x * 8 + g;
-        const int token = __shfl_sync(0xFFFFFFFFu, my_token, x * 8 + g);
-        at[x] = token < 0 ? -1 : (static_cast<int64_t>(token) * P.Hq + h * P.group + row - token * P.group) * L.slots + slot;
-        float sum = lo(l[x]) + hi(l[x]);
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-        if (c == 0 && at[x] >= 0) L.part_ml[at[x]] = ok ? make_float2(m[x], sum) : make_float2(-INFINITY, 0.0f);
-      }
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t o[16];
-          tmem_load_32(o_addr + half * kHalf + q * 32, o);
-          tmem_wait_load(o);
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const int x = half * 2 + (e >> 1 & 1);
-            if (ok && at[x] >= 0)
-              *reinterpret_cast<float2 *>(L.part_o + at[x] * D + q * 32 + (e >> 2) * 8 + 2 * c) =
-                  make_float2(__uint_as_float(o[e]) * w, __uint_as_float(o[e + 1]) * w);
-          }
-        }
-    }
-    fence_before();
-    done_tiles += n;
-    ++done_segments;
-    if (t < tiles) mine += n;
-    u += n;
+      done_tiles += n;
+      ++done_segments;
+      if (t < tiles) mine += n;
+      u = tile_from(u + n);
     }
   } else if (warp < 10) {
     // -------------------------------------------------------------------
@@ -596,83 +608,83 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     const int lt = tid - kSoftmaxThreads;
     uint32_t bad = 0;
     bool ok = true;
-    for (int u = blockIdx.x * L.units_cta; u < u_end;) {
-    const Segment S = segment(u);
-    const int h = S.h, n = S.n, k_begin = S.k_begin, k_end = S.k_end;
-    const float *const kscale = P.c.k_scale + h * P.c.scale_head_stride;
-    const float *const vscale = P.c.v_scale + h * P.c.scale_head_stride;
-    float ks[2], vs[2];
-    bool in[2];  // a key of the range
-    int page[2];
-    auto key_of = [&](int i, int e) { return k_begin + i * kKeyTile + lt + e * kVectorThreads; };
-    auto pages = [&](int i) {
+    for (int u = u_begin; u < u_end;) {
+      const Segment S = segment(u);
+      const int h = S.h, n = S.n, k_begin = S.k_begin, k_end = S.k_end;
+      const float *const kscale = P.c.k_scale + h * P.c.scale_head_stride;
+      const float *const vscale = P.c.v_scale + h * P.c.scale_head_stride;
+      float ks[2], vs[2];
+      bool in[2];  // a key of the range
+      int page[2];
+      auto key_of = [&](int i, int e) { return k_begin + i * kKeyTile + lt + e * kVectorThreads; };
+      auto pages = [&](int i) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) page[e] = i < n && key_of(i, e) < k_end ? P.tables[div_by(key_of(i, e), L.page)] : -1;
-    };
-    auto scales = [&](int i) {  // of the tile whose pages are there
+        for (int e = 0; e < 2; ++e) page[e] = i < n && key_of(i, e) < k_end ? P.tables[div_by(key_of(i, e), L.page)] : -1;
+      };
+      auto scales = [&](int i) {  // of the tile whose pages are there
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k = key_of(i, e);
-        in[e] = i < n && k < k_end;
-        ks[e] = vs[e] = 0.0f;
-        if (in[e] && page[e] >= 0 && page[e] < P.c.num_blocks) {
-          const int64_t at = page[e] * P.c.scale_block_stride +
-                             (k - div_by(k, L.page) * P.c.block_size) * P.c.scale_token_stride;
-          ks[e] = kscale[at];
-          vs[e] = vscale[at];
-        } else if (in[e]) {
-          bad = SV_DATA_BAD_SLOT;
+        for (int e = 0; e < 2; ++e) {
+          const int k = key_of(i, e);
+          in[e] = i < n && k < k_end;
+          ks[e] = vs[e] = 0.0f;
+          if (in[e] && page[e] >= 0 && page[e] < P.c.num_blocks) {
+            const int64_t at = page[e] * P.c.scale_block_stride +
+                               (k - div_by(k, L.page) * P.c.block_size) * P.c.scale_token_stride;
+            ks[e] = kscale[at];
+            vs[e] = vscale[at];
+          } else if (in[e]) {
+            bad = SV_DATA_BAD_SLOT;
+          }
         }
-      }
-    };
-    pages(0);
-    scales(0);
-    pages(1);
-    // W: the power of two at the first tile's largest value scale
-    float unscale;
-    {
-      uint32_t top = 0;
+      };
+      pages(0);
+      scales(0);
+      pages(1);
+      // W: the power of two at the first tile's largest value scale
+      float unscale;
+      {
+        uint32_t top = 0;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (vs[e] > 0.0f && vs[e] < INFINITY) top = max(top, __float_as_uint(vs[e]));
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
-      volatile float *const two = C.w_of_warp[done_segments & 1];
-      if (lane == 0) two[warp - 8] = __uint_as_float(top);
-      asm volatile("bar.sync 2, 64;" ::: "memory");
-      const uint32_t bits_w = __float_as_uint(fmaxf(two[0], two[1]));
-      const int e = bits_w >= 0x00800000u ? static_cast<int>(bits_w >> 23) - 127 : 0;
-      unscale = pow2(max(-126, min(126, -e)));
-      if (lt == 0) *const_cast<volatile float *>(&C.w[done_segments % kWSlots]) = 1.0f / unscale;
-    }
-    const float c_all = P.scale * kLog2e;
-    for (int i = 0; ok && i < n; ++i) {
-      const int it = done_tiles + i, slot_v = it % kVectorSlots;
-      ok = wait_warp(C, &C.vec_empty[slot_v], (it / kVectorSlots & 1) ^ 1);
-      if (!ok) break;
-      Vectors &V = vec[slot_v];
-      float most = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = lt + e * kVectorThreads;
-        float kc = ks[e] * c_all, v = vs[e];
-        // (scale 0: a key whose page is outside the cache; keys behind the range are no row's)
-        const bool good = v > 0.0f && v < INFINITY, out = in[e] && v == 0.0f;
-        if (!good && v != 0.0f) kc = __uint_as_float(0x7FC00000u);
-        if (good) most = fmaxf(most, v);
-        const uint32_t dead = __ballot_sync(0xFFFFFFFFu, out);
-        (r & 1 ? V.kc[r >> 1].y : V.kc[r >> 1].x) = out ? 0.0f : kc;
-        (r & 1 ? V.vr[r >> 1].y : V.vr[r >> 1].x) = good ? v * unscale : 1.0f;
-        if (lane == 0) V.dead[r >> 5] = dead;
+        for (int e = 0; e < 2; ++e)
+          if (vs[e] > 0.0f && vs[e] < INFINITY) top = max(top, __float_as_uint(vs[e]));
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        volatile float *const two = C.w_of_warp[done_segments & 1];
+        if (lane == 0) two[warp - 8] = __uint_as_float(top);
+        asm volatile("bar.sync 2, 64;" ::: "memory");
+        const uint32_t bits_w = __float_as_uint(fmaxf(two[0], two[1]));
+        const int e = bits_w >= 0x00800000u ? static_cast<int>(bits_w >> 23) - 127 : 0;
+        unscale = pow2(max(-126, min(126, -e)));
+        if (lt == 0) *const_cast<volatile float *>(&C.w[done_segments % kWSlots]) = 1.0f / unscale;
       }
-      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
-      if (lane == 0) V.top[warp - 8] = top ? log2f(__uint_as_float(top) * unscale) : -INFINITY;
-      mbar_arrive(&C.vec_full[slot_v]);
-      scales(i + 1);
-      pages(i + 2);
-    }
-    done_tiles += n;
-    ++done_segments;
-    u += n;
+      const float c_all = P.scale * kLog2e;
+      for (int i = 0; ok && i < n; ++i) {
+        const int it = done_tiles + i, slot_v = it % kVectorSlots;
+        ok = wait_warp(C, &C.vec_empty[slot_v], (it / kVectorSlots & 1) ^ 1);
+        if (!ok) break;
+        Vectors &V = vec[slot_v];
+        float most = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = lt + e * kVectorThreads;
+          float kc = ks[e] * c_all, v = vs[e];
+          // (scale 0: a key whose page is outside the cache; keys behind the range are no row's)
+          const bool good = v > 0.0f && v < INFINITY, out = in[e] && v == 0.0f;
+          if (!good && v != 0.0f) kc = __uint_as_float(0x7FC00000u);
+          if (good) most = fmaxf(most, v);
+          const uint32_t dead = __ballot_sync(0xFFFFFFFFu, out);
+          (r & 1 ? V.kc[r >> 1].y : V.kc[r >> 1].x) = out ? 0.0f : kc;
+          (r & 1 ? V.vr[r >> 1].y : V.vr[r >> 1].x) = good ? v * unscale : 1.0f;
+          if (lane == 0) V.dead[r >> 5] = dead;
+        }
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+        if (lane == 0) V.top[warp - 8] = top ? log2f(__uint_as_float(top) * unscale) : -INFINITY;
+        mbar_arrive(&C.vec_full[slot_v]);
+        scales(i + 1);
+        pages(i + 2);
+      }
+      done_tiles += n;
+      ++done_segments;
+      u = tile_from(u + n);
     }
     if (P.status && (bad || !ok)) atomicOr(P.status, static_cast<int>(bad | (ok ? 0u : SV_DATA_COPY_TIMEOUT)));
   } else if (warp == 10) {
@@ -682,9 +694,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     if (lane == 0) {
       bool ok = true;
       int issued = 0;  // K and V tiles alternate
-      for (int u = blockIdx.x * L.units_cta; ok && u < u_end; ++u) {
-        const int item = u / T, h = item / L.tensor_tiles;
-        const uint8_t *const image = L.image + (static_cast<int64_t>(h) * T + u - item * T) * 2 * Y::kTile;
+      for (int u = u_begin; ok && u < u_end; u = tile_from(u + 1)) {
+        const int item = u / L.period, h = item / L.tensor_tiles;
+        const uint8_t *const image = L.image + (static_cast<int64_t>(h) * T + u - item * L.period) * 2 * Y::kTile;
         for (int v = 0; v < 2; ++v) {
           const int it = issued >> 1, st = it & 1;
           ok = wait(C, v ? &C.v_empty[st] : &C.k_empty[st], (it >> 1 & 1) ^ 1);
@@ -748,7 +760,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     };
     bool ok = true;
     int second = 0;  // key tiles of the second row tile so far
-    for (int u = blockIdx.x * L.units_cta; u < u_end;) {
+    for (int u = u_begin; u < u_end;) {
       const Segment S = segment(u);
       const int n = S.n, tiles = S.tiles;
       ok = ok && wait_warp(C, &C.q_full, done_segments & 1) &&
@@ -787,7 +799,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       done_tiles += n;
       ++done_segments;
       if (tiles == 2) second += n;
-      u += n;
+      u = tile_from(u + n);
     }
     __syncwarp();
     fence_before();
