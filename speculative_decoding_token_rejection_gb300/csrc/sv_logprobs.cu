@@ -77,6 +77,11 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// The number that an ordered key stands for (-0 comes back as +0).
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
 // Sums with another reference; c = log2 e / T.
 __device__ __forceinline__ void rebase(Sums &s, float ref, float c) {
   if (s.ref == ref) return;
@@ -98,6 +103,18 @@ __device__ __forceinline__ void merge(Sums &a, Sums b, float c) {
   a.zx += b.zx;
   a.above += b.above;
   a.bad |= b.bad;
+}
+
+// A warp's sums together, in every lane: the common reference first, so that a lane changes its own once.
+__device__ __forceinline__ void merge_warp(Sums &s, float c) {
+  rebase(s, logit_of(__reduce_max_sync(0xFFFFFFFFu, ordered_bits(s.ref))), c);
+#pragma unroll
+  for (int b = 16; b; b >>= 1) {
+    s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, b);
+    s.zx += __shfl_xor_sync(0xFFFFFFFFu, s.zx, b);
+  }
+  s.above = __reduce_add_sync(0xFFFFFFFFu, s.above);
+  s.bad = __reduce_or_sync(0xFFFFFFFFu, s.bad);
 }
 
 __device__ __forceinline__ unsigned long long warp_max64(unsigned long long v) {
@@ -156,10 +173,6 @@ __device__ __forceinline__ float largest(const uint4 &r) {
   if (!BF16) return max_nan(max_nan(word_of(r, 0), word_of(r, 1)), max_nan(word_of(r, 2), word_of(r, 3)));
   const uint32_t t = max_nan_bf16x2(max_nan_bf16x2(r.x, r.y), max_nan_bf16x2(r.z, r.w));
   return max_nan(__uint_as_float(t << 16), __uint_as_float(t & 0xFFFF0000u));
-}
-// The number that an ordered key stands for (-0 comes back as +0).
-__device__ __forceinline__ float logit_of(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
 // A block maximum's place in the order (largest key, lower block first).  A
@@ -342,16 +355,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
   sum.bad = bad;
   sum.z = lo(z) + hi(z);
   sum.zx = lo(zx) + hi(zx);
-#pragma unroll
-  for (int b = 16; b; b >>= 1) {
-    Sums o;
-    o.ref = __shfl_xor_sync(0xFFFFFFFFu, sum.ref, b);
-    o.z = __shfl_xor_sync(0xFFFFFFFFu, sum.z, b);
-    o.zx = __shfl_xor_sync(0xFFFFFFFFu, sum.zx, b);
-    o.above = __shfl_xor_sync(0xFFFFFFFFu, sum.above, b);
-    o.bad = __shfl_xor_sync(0xFFFFFFFFu, sum.bad, b);
-    merge(sum, o, c);
-  }
+  merge_warp(sum, c);
   if (lane == 0) sm.warp_sums[warp] = sum;
   __syncthreads();
 
@@ -359,16 +363,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
   const int K = P.K, kb = min(K, blocks);
   if (warp == 0) {  // (lanes 8 and up hold nothing)
     Sums a = lane < kWarps ? sm.warp_sums[lane] : Sums{-INFINITY, 0.0f, 0.0f, 0u, 0u};
-#pragma unroll
-    for (int b = kWarps / 2; b; b >>= 1) {
-      Sums o;
-      o.ref = __shfl_xor_sync(0xFFFFFFFFu, a.ref, b);
-      o.z = __shfl_xor_sync(0xFFFFFFFFu, a.z, b);
-      o.zx = __shfl_xor_sync(0xFFFFFFFFu, a.zx, b);
-      o.above = __shfl_xor_sync(0xFFFFFFFFu, a.above, b);
-      o.bad = __shfl_xor_sync(0xFFFFFFFFu, a.bad, b);
-      merge(a, o, c);
-    }
+    merge_warp(a, c);
     if (lane == 0) sm.sums = a;
   }
   if (K) {
