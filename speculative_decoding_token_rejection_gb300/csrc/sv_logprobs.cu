@@ -342,15 +342,16 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
         }
     }
   };
-  // two groups in turn, each fetched while the other is taken
-  uint4 even[kUnroll], odd[kUnroll];
-  fetch(warp, even);
-  for (int gi = warp; gi < groups; gi += 2 * kWarps) {
-    fetch(gi + kWarps, odd);
-    take(gi, even);
-    if (gi + kWarps >= groups) break;
-    fetch(gi + 2 * kWarps, even);
-    take(gi + kWarps, odd);
+  // a group is fetched while the one before it is taken (one copy of the code: two in turn, without the moves, are twice
+  // the instructions to fetch)
+  uint4 now[kUnroll], next[kUnroll];
+  fetch(warp, now);
+#pragma unroll 1
+  for (int gi = warp; gi < groups; gi += kWarps) {
+    fetch(gi + kWarps, next);
+    take(gi, now);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) now[u] = next[u];
   }
   sum.bad = bad;
   sum.z = lo(z) + hi(z);
