@@ -377,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
                   block_before<BF16>(k.z, j + 2, key, b) + block_before<BF16>(k.w, j + 3, key, b);
       }
       if (before < kb) sm.chosen[before] = b;
-      if (before == K - 1) sm.floor = logit_of(BF16 ? key & 0xFFFF0000u : key);
+      // (a negative bf16's key has ones in its lower half)
+      if (before == K - 1) sm.floor = logit_of(!BF16 ? key : key & 0x80000000u ? key & 0xFFFF0000u : key | 0xFFFFu);
     }
     __syncthreads();
     const float floor = kb == K ? sm.floor : -INFINITY;

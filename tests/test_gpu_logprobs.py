@@ -223,3 +223,12 @@ def test_after_a_verification():
     tok = res.out_tokens.cpu()
     assert torch.equal(r.ranks.cpu() >= 1, tok >= 0)
     check(dict(logits=target, tokens=tok, gam=torch.full((N,), G), G=G, temperature=None, cu=None), 4)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [3, 20])
+def test_most_blocks_masked(dtype, K):
+    c = make(320, 0, 40000, dtype, seed=29)
+    c["logits"][:, 9:39990] = -float("inf")  # 19 entries left, in the first and the last block
+    c["tokens"][c["tokens"] >= 0] = 7
+    check(c, K)
