@@ -16,10 +16,17 @@
 // elements lie in those K blocks, whatever ties there are.  They are read
 // again (from L2, K * 2 KB a row); elements that reach the last chosen block's
 // maximum -- a few more than K, unless there are many ties -- are ranked by
-// counting.
+// counting.  A CTA with fewer than K blocks (short rows, or a row cut over a
+// cluster) takes the K-th largest maximum of parts of blocks instead: no
+// element below it is among the K largest, and the CTA's few blocks are all
+// read again.  (With every element a candidate, 64 tokens of V = 151936 with 20
+// alternatives took 82 us, now 21; two of V = 92471 with 32 40, now 17.)
 //
 // Bound by HBM: the row is read once, 512 requests' committed tokens (2641
-// rows of 151936 bf16 logits) are 0.80 GB.
+// rows of 151936 bf16 logits) are 0.80 GB and take 161 us with 20 alternatives,
+// 5.0 TB/s or 74 % of the copy rate; without alternatives 130 us.  Fetching
+// instructions stalled it most: ragged vectors, candidates and a second copy of
+// the loop's body in line cost 25 us together, so the loop is kept short.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -200,6 +207,19 @@ __device__ __noinline__ void take_candidates(LogprobsSmem &sm, uint4 r, int x0, 
   }
 }
 
+// The maxima of a group's parts: of each lane's vectors, or of each four lanes'.
+template <bool BF16>
+__device__ __noinline__ void part_maxima(LogprobsSmem &sm, uint32_t key, int gi, int parts) {
+  const int lane = threadIdx.x & 31;
+  if (parts == 8) {
+    key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, 1));
+    key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, 2));
+    if (lane & 3) return;
+  }
+  const int b = gi * parts + lane * parts / 32;
+  sm.block_key[b] = block_order<BF16>(key, b);
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const LogprobsParams P) {
   pdl_enter();
@@ -255,7 +275,9 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
   const int v1 = min(nv, v0 + chunk);
   const int groups = (v1 - v0 + kGroup - 1) / kGroup;
   const int per_block = max(1, (groups + kMaxBlocks - 1) / kMaxBlocks);
-  const int blocks = (groups + per_block - 1) / per_block;
+  // fewer blocks than alternatives: parts of them, 32 or 8 of a group, give the floor
+  const int parts = P.K <= groups ? 0 : groups <= kThreads / 32 ? 32 : 8;
+  const int blocks = parts ? groups * parts : (groups + per_block - 1) / per_block;
   if (P.K) {
     if (per_block > 1)
       for (int b = tid; b < blocks; b += kThreads) sm.block_key[b] = 0;
@@ -311,7 +333,9 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
     }
     const uint32_t key = ordered_bits(top);
     bad |= !(top < INFINITY);  // +inf, or NaN, which the maxima hand on (and which no key orders)
-    if (P.K) {
+    if (parts) {
+      part_maxima<BF16>(sm, key, gi, parts);
+    } else if (P.K) {
       const uint32_t k = __reduce_max_sync(0xFFFFFFFFu, key);
       if (lane == 0) {
         if (per_block == 1)
@@ -397,9 +421,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
       }
       return left;
     };
-    for (int k = warp; k < kb; k += kWarps)
+    const int again = parts ? groups : kb;  // (parts cross in index order: all groups are looked at)
+    for (int k = warp; k < again; k += kWarps)
       for (int p = 0; p < per_block; ++p) {
-        const int gi = sm.chosen[k] * per_block + p;
+        const int gi = parts ? k : sm.chosen[k] * per_block + p;
         uint4 r[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) r[u] = fetch_again(gi, u);
@@ -421,10 +446,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
     } else {
       // many ties: every warp sorts its blocks' elements into a list of K (lane k holds the k-th), the lists are merged
       unsigned long long list = 0;
-      for (int k = warp; k < kb; k += kWarps)
+      for (int k = warp; k < again; k += kWarps)
         for (int p = 0; p < per_block; ++p)
           for (int u = 0; u < kUnroll; ++u) {
-            const int gi = sm.chosen[k] * per_block + p;
+            const int gi = parts ? k : sm.chosen[k] * per_block + p;
             const uint4 r = fetch_again(gi, u);
             uint32_t left = reaching(gi, u, r);
             const int x0 = (v0 + gi * kGroup + u * 32 + lane) * Row<BF16>::kPer - row.shift;

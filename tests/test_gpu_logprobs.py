@@ -232,3 +232,33 @@ def test_most_blocks_masked(dtype, K):
     c["logits"][:, 9:39990] = -float("inf")  # 19 entries left, in the first and the last block
     c["tokens"][c["tokens"] >= 0] = 7
     check(c, K)
+
+
+# Rows, or their shares in a cluster, with fewer 2 KB blocks than alternatives: parts of blocks decide.
+FEW = {
+    "one block": (dict(N=5, G=1, V=1000, dtype=torch.bfloat16), 32),
+    "less than one block": (dict(N=3, G=0, V=40, dtype=torch.float32), 32),
+    "fewer lanes than alternatives": (dict(N=3, G=0, V=100, dtype=torch.bfloat16, shift=5), 32),
+    "eight blocks and one entry": (dict(N=400, G=0, V=8193, dtype=torch.bfloat16), 9),
+    "nine blocks, four lanes a part": (dict(N=400, G=0, V=9215, dtype=torch.bfloat16, pad=1), 32),
+    "blocks one short": (dict(N=350, G=0, V=31 * 512, dtype=torch.float32, shift=3, pad=1), 32),
+    "as many blocks as alternatives": (dict(N=350, G=0, V=32 * 512, dtype=torch.float32), 32),
+    "shares of a cluster": (dict(N=2, G=1, V=92471, dtype=torch.bfloat16, pad=8, temps=[0.7]), 32),
+    "shares of a cluster, fp32": (dict(N=2, G=1, V=50001, dtype=torch.float32, pad=3), 31),
+    "ties": (dict(N=350, G=0, V=7001, dtype=torch.bfloat16, levels=8), 32),
+    "ties in shares": (dict(N=2, G=0, V=60001, dtype=torch.float32, levels=16), 32),
+}
+
+
+@pytest.mark.parametrize("name", FEW)
+def test_few_blocks(name):
+    kw, K = FEW[name]
+    check(make(seed=100 + len(name), **kw), K)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_few_blocks_with_masked_entries(dtype):
+    c = make(4, 1, 6000, dtype, seed=31)
+    c["logits"][:, 20:5990] = -float("inf")  # 30 entries left, fewer than alternatives
+    c["tokens"][c["tokens"] >= 0] = 7
+    check(c, 32)
