@@ -5,7 +5,7 @@
 // of the group -- all read the same keys, so the private part is bound by HBM:
 // 2 * head_dim + 8 bytes a key for 4 * head_dim * rows operations.  Each warp
 // streams keys on its own, 32 at a time, through shared memory of its own
-// (cp.async, two or three tiles deep), so no warp waits for another in the
+// (cp.async, two tiles deep), so no warp waits for another in the
 // loop.  A copy's eight (D = 64: four) neighbouring lanes take a whole row:
 // with the rows dealt to lanes the way the products read them, every 32-byte
 // sector was a request of its own, and the requests, not the bytes, set the
@@ -27,6 +27,10 @@
 // The key range of a row tile is cut over CTAs (and over a CTA's four warps)
 // when there are few row tiles; the partial results (M, l, O) of a CTA go to
 // the workspace and a second kernel joins them.
+//
+// Measured: 256 requests of 1 to 9 tokens over up to 8192 keys of their own
+// (32 heads over 8 of 128, e4m3), 491 us, 4.5 TB/s or 67 % of the copy rate.
+// Eight warps an SM cannot hide their own latencies: issue slots are 36 % busy.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
