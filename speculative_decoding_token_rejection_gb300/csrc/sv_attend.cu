@@ -178,7 +178,7 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
   uint32_t bits = 0;
   auto page_of = [&](int it) {  // of the lane's key of the warp's tile `it`
     const int k = T.k_begin + (it * kAttendWarps + warp) * kKeys + lane;
-    return it < ntiles && k < T.k_end ? T.table[div_by(k, L.page)] : -1;
+    return it < ntiles && k < T.k_end ? (k < P.row0 ? P.tables : T.table)[div_by(k, L.page)] : -1;
   };
   // Copies of a tile: the lane's key first, then the rows, a lane's neighbours taking a whole one, in kCols steps.
   uint32_t unit = 0, dead = 0;  // the row's place in units of 16 bytes (rows are 16-byte aligned, a side below 2^36 bytes)
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kAttendThreads, 2) attend_kernel(const AttendP
     T.table += i * P.table_stride;
     T.k_begin = P.prefix + split * L.own_chunk;
     const int k = T.k_begin + tid;
-    T.page = k < P.max_seq ? T.table[div_by(k, L.page)] : -1;  // (tables hold max_seq keys, whatever the length)
+    T.page = k < P.max_seq ? (k < P.row0 ? P.tables : T.table)[div_by(k, L.page)] : -1;  // (tables hold max_seq keys, whatever the length)
     uint32_t bits = 0;
     const bool ok = attend_request(P, i, first, gam, len, bits);
     if (bits && tile == 0 && T.h == 0 && split == 0 && tid == 0 && P.status) atomicOr(P.status, static_cast<int>(bits));
@@ -676,6 +676,19 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
   return bound;
 }
 
+// A prefix of fewer keys than a CTA's warps take at once is read by every
+// request for itself (from L2): that adds no more than one step to its keys,
+// and saves the CTAs that would share it, the partial results and the join
+// (512 requests x 8 tokens, prefix 32: 136 us against 275; 64 x 5, 64: 29
+// against 40; 8 x 4, 64: 12.6 against 13.3).
+AttendParams short_prefix(AttendParams p) {
+  if (p.prefix < kTensorKeys) {
+    p.row0 = p.prefix;
+    p.prefix = 0;
+  }
+  return p;
+}
+
 AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullptr) {
   AttendPlan L{};
   L.page = fast_div(std::max(1, p.c.block_size));
@@ -761,13 +774,14 @@ cudaError_t enable_attend_kernels() {
   return enable<64, SV_CACHE_E4M3>();
 }
 
-int64_t attend_workspace_bytes(const AttendParams &p, int num_sms) {
+int64_t attend_workspace_bytes(const AttendParams &a, int num_sms) {
   int64_t bytes = 0;
-  make_plan(p, num_sms, &bytes);
+  make_plan(short_prefix(a), num_sms, &bytes);
   return bytes;
 }
 
-cudaError_t launch_attend(const AttendParams &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_attend(const AttendParams &a, int num_sms, cudaStream_t stream) {
+  const AttendParams p = short_prefix(a);
   const AttendPlan L = make_plan(p, num_sms);
   const bool i8 = p.c.format == SV_CACHE_INT8;
   if (p.c.head_dim == 128) return i8 ? launch<128, SV_CACHE_INT8>(p, L, num_sms, stream) : launch<128, SV_CACHE_E4M3>(p, L, num_sms, stream);

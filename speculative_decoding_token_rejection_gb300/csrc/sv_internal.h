@@ -206,6 +206,7 @@ cudaError_t launch_kv_read(const KvParams &p, bool bf16, bool vec, cudaStream_t 
 // The verify tokens' attention (sv_attend.cu).
 struct AttendParams {
   int32_t N, G, Hq, group, max_seq, prefix;
+  int32_t row0;  // keys below it have their pages in row 0 of the tables, though every request reads them itself
   int64_t T;
   const int32_t *cu;
   spec_verify_kv_cache c;

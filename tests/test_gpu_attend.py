@@ -422,3 +422,15 @@ def test_no_lse_and_small_workspace():
         with pytest.raises(sv.SpecVerifyError) as ei:
             run(c, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
         assert ei.value.code == sv.SV_ERR_CAPACITY
+
+
+@pytest.mark.parametrize("prefix", [16, 48, 112, 320])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_only_the_first_row_names_the_prefix_pages(prefix, fmt):
+    c = make([2, 0, 4, 1, 3], [prefix + 40, prefix, prefix + 3, prefix + 300, prefix - 5], prefix=prefix, fmt=fmt, seed=33)
+    want = run(c)
+    c["table"][1:, :prefix // 16] = torch.tensor([-7, 1 << 30], dtype=torch.int32, device="cuda").repeat(
+        prefix // 16)[:prefix // 16]
+    got = run(c)
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check(poison(make([2, 0, 4, 1, 3], c["lens"], prefix=prefix, fmt=fmt, seed=33)))
