@@ -390,7 +390,7 @@ sv_status spec_verify_check_kv_args(const spec_verify_config *config, const spec
  * k % block_size.  The first shared_prefix_len tokens (a multiple of
  * block_size) are the same pages for every request -- entries
  * 0 .. shared_prefix_len / block_size - 1 of row 0 of block_tables stand for
- * all -- and are read once for the whole batch.  A page outside the cache
+ * all -- and are read once for the whole batch where that pays.  A page outside the cache
  * leaves its keys out and raises SV_DATA_BAD_SLOT; a seq_len outside
  * [0, max_seq_len] or past its block table raises SV_DATA_BAD_PARAM and gives the request's rows
  * out = 0, lse = -infinity; a bad cu range raises SV_DATA_BAD_CU and leaves

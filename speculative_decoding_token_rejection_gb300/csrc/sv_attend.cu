@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttendParams P, co
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 constexpr int kChunkStep = kAttendWarps * kKeys;  // a CTA's four warps take 32 keys each
-constexpr int kTensorKeys = 128, kTensorRows = 96;  // the prefix goes to the tensor-memory kernel from here on
+constexpr int kTensorRows = 96;  // a shared prefix goes to the tensor-memory kernel from here on
 constexpr int kTensorLeast = 4;  // key tiles of a CTA of that kernel, where the prefix has as many
 constexpr int kTensorBegin = 7;  // and what beginning another (kv head, row tile) costs it, in key tiles
 constexpr int kChunkMost = 8192;                  // so that the longest request is no long tail
@@ -676,13 +676,21 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
   return bound;
 }
 
-// A prefix of fewer keys than a CTA's warps take at once is read by every
-// request for itself (from L2): that adds no more than one step to its keys,
-// and saves the CTAs that would share it, the partial results and the join
-// (512 requests x 8 tokens, prefix 32: 136 us against 275; 64 x 5, 64: 29
-// against 40; 8 x 4, 64: 12.6 against 13.3).
+// A short prefix is read by every request for itself (from L2), which saves the
+// CTAs that would share it, the partial results and the join.  In keys of the
+// private CTAs that is worth about 2^19 for a call of the tensor-memory kernel
+// (2^16 without it), and 10 for each row; one step of keys always.  Measured,
+// us a call, shared | by each request: 64 requests x 5 tokens (32 heads over
+// 8), prefix 128 57 | 31, 512 67 | 41, 1024 72 | 55, 2032 85 | 84; 512 x 8, 256
+// 266 | 194, 512 283 | 254, 1024 312 | 371; 512 x 1, 128 91 | 70, 512 99 | 118;
+// 8 x 4, 1024 37 | 18; 20 x 1 (80 rows), 256 14.5 | 14.1, 1024 19.5 | 21.5.
 AttendParams short_prefix(AttendParams p) {
-  if (p.prefix < kTensorKeys) {
+  const int64_t ctas = static_cast<int64_t>(p.N) * p.c.num_kv_heads *
+                       ceil_div((p.G + 1) * static_cast<int64_t>(p.group), 8 * kGroups);
+  // (the rows there may be, so that calls with fewer tokens choose alike)
+  const int64_t rows = static_cast<int64_t>(p.N) * (p.G + 1) * p.group, fixed = rows >= kTensorRows ? 1 << 19 : 1 << 16;
+  const int64_t keys = (fixed + 10 * rows * p.c.num_kv_heads) / std::max<int64_t>(1, ctas);
+  if (p.prefix < std::clamp<int64_t>(keys, 128, 2048)) {
     p.row0 = p.prefix;
     p.prefix = 0;
   }
@@ -707,7 +715,7 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   // us the whole call, with no empty units 132, with 4 of them 126, with 10 125; 512 x 8 over 16384: 1073 to 1078 all)
   const int64_t gap = tiles > static_cast<int64_t>(num_sms) * kTensorLeast ? kTensorBegin : 0;
   const int64_t units = items * (image_tiles + gap) - gap;
-  if (p.prefix >= kTensorKeys && L.rows >= kTensorRows && units <= 0x3FFFFFFF) {
+  if (p.prefix > 0 && L.rows >= kTensorRows && units <= 0x3FFFFFFF) {
     L.tensor_tiles = static_cast<int32_t>(tensor_tiles);
     L.image_tiles = static_cast<int32_t>(image_tiles);
     L.period = static_cast<int32_t>(image_tiles + gap);

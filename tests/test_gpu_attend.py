@@ -434,3 +434,50 @@ def test_only_the_first_row_names_the_prefix_pages(prefix, fmt):
     got = run(c)
     assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     check(poison(make([2, 0, 4, 1, 3], c["lens"], prefix=prefix, fmt=fmt, seed=33)))
+
+
+# Short prefixes are read by each request for itself: the same with prefixes that are shared at these sizes.
+LONGER = 2112  # a multiple of every block size here
+
+
+def long_make(gammas, lens, *, prefix=0, **kw):
+    more = LONGER if prefix else 0
+    return make(gammas, [n + more for n in lens], prefix=prefix + more, **kw)
+
+
+@pytest.mark.parametrize("name", [n for n in CASES if 0 < CASES[n].get("prefix", 0) < 2048])
+def test_longer_prefixes(name):
+    check(poison(long_make(seed=len(name), **CASES[name])))
+
+
+@pytest.mark.parametrize("test, args", [
+    (test_small_and_large_queries, (1e-3, "int8")), (test_small_and_large_queries, (30.0, "e4m3")),
+    (test_small_and_large_queries, (3000.0, "int8")), (test_value_scales_of_many_sizes, ()),
+    (test_nan_in_a_row_of_q_stays_in_it, ()), (test_rows_of_very_different_sizes, ()),
+    (test_strided_and_unaligned_queries_and_outputs, ())], ids=lambda x: getattr(x, "__name__", str(x)))
+def test_the_same_with_longer_prefixes(test, args, monkeypatch):
+    short = make
+    monkeypatch.setitem(globals(), "make", lambda gammas, lens, *, prefix=0, **kw: short(
+        gammas, [n + (LONGER if prefix else 0) for n in lens], prefix=prefix + (LONGER if prefix else 0), **kw))
+    test(*args)
+
+
+def test_bad_page_in_a_longer_prefix():
+    for N in (3, 60):
+        c = make([4] * N, [2500 + i for i in range(N)], prefix=2496, uniform=True, seed=18)
+        cut = dict(c, table=torch.cat([c["table"][:, :5], c["table"][:, 6:]], 1), lens=[n - 16 for n in c["lens"]],
+                   prefix=2480, seq_lens=c["seq_lens"] - 16)
+        ref, rlse, tol, ltol = reference(cut)
+        c["table"][:, 5] = c["cache"].num_blocks
+        out, lse, status = run(c)
+        assert status == sv.DATA_STATUS_BITS["BAD_SLOT"]
+        assert bool(((out.double() - ref).abs() <= tol).all()) and bool(((lse - rlse).abs() <= ltol).all())
+
+
+@pytest.mark.parametrize("kv_heads, group, gamma", [(1, 1, 0), (2, 4, 3), (1, 16, 2), (8, 1, 0)])
+def test_prefixes_around_the_choice(kv_heads, group, gamma):
+    """Shared or read by each request, a prefix gives the same result."""
+    N = 30
+    for prefix in (96, 128, 256, 480, 1024, 2032, 2048):
+        check(make([gamma] * N, [prefix + 5 * i for i in range(N)], prefix=prefix, kv_heads=kv_heads, group=group,
+                   uniform=True, seed=prefix))
