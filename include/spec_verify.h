@@ -432,7 +432,8 @@ typedef struct spec_verify_attend_args {
 
 sv_status spec_verify_attend(spec_verify_t handle, const spec_verify_attend_args *args, void *stream);
 
-/* Bytes of workspace a call of these sizes needs (pointers are not looked at:
+/* Bytes of workspace that calls of these sizes need, and such with fewer draft
+ * tokens or a smaller max_seq_len (pointers are not looked at:
  * num_reqs, max_spec_len, num_q_heads, max_seq_len, shared_prefix_len,
  * num_draft_tokens_total, cache.num_kv_heads and cache.head_dim are). */
 sv_status spec_verify_attend_workspace_size(spec_verify_t handle, const spec_verify_attend_args *args, int64_t *bytes);

@@ -782,10 +782,23 @@ cudaError_t enable_attend_kernels() {
   return enable<64, SV_CACHE_E4M3>();
 }
 
-int64_t attend_workspace_bytes(const AttendParams &a, int num_sms) {
-  int64_t bytes = 0;
-  make_plan(short_prefix(a), num_sms, &bytes);
-  return bytes;
+int64_t attend_workspace_bytes(const AttendParams &a, int num_sms, bool fewer) {
+  AttendParams p = short_prefix(a);
+  int64_t most = 0;
+  make_plan(p, num_sms, &most);
+  if (!fewer || p.prefix == 0) return most;
+  // Fewer tokens may have more partial results each.  Calls of one plan need the most with the most rows: 256 a row tile
+  // of the tensor-memory kernel, and below kTensorRows 32 a row tile.
+  const auto with = [&](int64_t rows) {
+    p.T = std::min(a.T, rows / p.group - p.N);
+    if (p.T < 0) return;
+    int64_t bytes = 0;
+    make_plan(p, num_sms, &bytes);
+    most = std::max(most, bytes);
+  };
+  for (const int64_t rows : {8 * kGroups, 16 * kGroups, kTensorRows - 1}) with(rows);
+  for (int64_t rows = kPrefixRowTile; rows < (a.T + a.N) * a.group; rows += kPrefixRowTile) with(rows);
+  return most;
 }
 
 cudaError_t launch_attend(const AttendParams &a, int num_sms, cudaStream_t stream) {

@@ -223,7 +223,8 @@ struct AttendParams {
   int32_t *status;
   bool pdl;
 };
-int64_t attend_workspace_bytes(const AttendParams &p, int num_sms);
+// `fewer`: what calls with fewer draft tokens need as well.
+int64_t attend_workspace_bytes(const AttendParams &p, int num_sms, bool fewer);
 cudaError_t enable_attend_kernels();
 cudaError_t launch_attend(const AttendParams &p, int num_sms, cudaStream_t stream);
 

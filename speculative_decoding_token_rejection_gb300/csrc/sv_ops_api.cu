@@ -206,7 +206,7 @@ sv_status spec_verify_attend_workspace_size(spec_verify_t h, const spec_verify_a
   b.cu_num_draft_tokens = &any;
   const sv_status st = check_attend_sizes(&h->cfg, &b);
   if (st != SV_OK) return st;
-  *bytes = a->num_reqs == 0 ? 0 : sv::attend_workspace_bytes(attend_params(h, a), h->num_sms);
+  *bytes = a->num_reqs == 0 ? 0 : sv::attend_workspace_bytes(attend_params(h, a), h->num_sms, true);
   return SV_OK;
 }
 
@@ -216,7 +216,7 @@ sv_status spec_verify_attend(spec_verify_t h, const spec_verify_attend_args *a, 
   if (st != SV_OK) return st;
   if (a->num_reqs == 0) return SV_OK;
   const sv::AttendParams p = attend_params(h, a);
-  const int64_t need = sv::attend_workspace_bytes(p, h->num_sms);
+  const int64_t need = sv::attend_workspace_bytes(p, h->num_sms, false);
   if (need > 0 && (!a->workspace || a->workspace_bytes < need))
     return fail(SV_ERR_CAPACITY, "workspace of %lld bytes, the call needs %lld", static_cast<long long>(a->workspace_bytes),
                 static_cast<long long>(need));

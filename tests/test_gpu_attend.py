@@ -481,3 +481,23 @@ def test_prefixes_around_the_choice(kv_heads, group, gamma):
     for prefix in (96, 128, 256, 480, 1024, 2032, 2048):
         check(make([gamma] * N, [prefix + 5 * i for i in range(N)], prefix=prefix, kv_heads=kv_heads, group=group,
                    uniform=True, seed=prefix))
+
+
+@pytest.mark.parametrize("kv_heads, group", [(1, 4), (2, 4), (1, 16)])
+def test_a_workspace_holds_for_fewer_draft_tokens(kv_heads, group):
+    N, G, prefix = 33, 7, 4096
+    ver = verifier()
+
+    def size(tokens):
+        return sv.spec_verify_attend_workspace_size(ver.handle, num_reqs=N, max_spec_len=G, num_q_heads=kv_heads * group,
+                                                    num_kv_heads=kv_heads, head_dim=64, max_seq_len=prefix + 70,
+                                                    shared_prefix_len=prefix, num_tokens=tokens)
+
+    sizes = [size(n) for n in range(N, N * (G + 1) + 1)]
+    assert sizes == sorted(sizes)
+    ws = torch.empty(sizes[-1], dtype=torch.uint8, device="cuda")
+    lens = [prefix + 70] + [prefix + i for i in range(N - 1)]
+    for few in (0, 1, 2, 3, 6):  # one request with G drafts, the others with `few`
+        c = make([G] + [few] * (N - 1), lens, prefix=prefix, kv_heads=kv_heads, group=group, dim=64, seed=few)
+        want, got = run(c), run(c, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
