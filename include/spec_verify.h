@@ -397,8 +397,13 @@ sv_status spec_verify_check_kv_args(const spec_verify_config *config, const spec
  * the rows unwritten.  A NaN score makes its row NaN; nothing of a key that a
  * row does not see reaches it, whatever its scales are (in an e4m3 cache its
  * bytes are numbers, as spec_verify_kv_write leaves them; behind seq_len they
- * may be anything).  SV_DATA_COPY_TIMEOUT: a wait inside a kernel ran out and
- * the outputs are not the result; never expected on a healthy GPU.
+ * may be anything).  Scales may be any floats: a value scale of 0 or below is
+ * taken as it stands, one of less than 2^-64, the writer's smallest, as 0, and
+ * one that is NaN or infinite makes out NaN, not lse, in the rows that see its
+ * key (for the heads that read it).  A key whose value scale is less than
+ * 2^-100 of the largest that a row sees may drop out of the row's lse.
+ * SV_DATA_COPY_TIMEOUT: a wait inside a kernel ran out and the outputs are not
+ * the result; never expected on a healthy GPU.
  *
  * The products take 16-bit operands: the cache's numbers and q (scaled by a
  * power of two) are exact in them, the softmax's weights are rounded to 11

@@ -47,6 +47,7 @@ constexpr float kRaise = 8;  // a row's maximum is raised when a weight would pa
 
 constexpr int kGroups = 4;   // groups of 8 rows in a row tile
 constexpr int kStages = 2;   // tiles in a warp's ring
+static_assert(kStages == 2, "the mask of a tile's keys that are left out is that of the copy before it");
 
 // Two CTAs per SM: 255 registers hold four row groups (outputs 128), and 150
 // KB of shared memory leave the L1 cache 100 KB.  Three CTAs of up to three
@@ -72,6 +73,12 @@ __device__ __forceinline__ int tile_at(int row, int col) {
   const int line = D == 128 ? row : row >> 1, in = D == 128 ? col : (row & 1) * 4 + col;
   const int turn = VALUES ? (row >> 1 & 3) << 1 : (D == 128 ? (row & 1) << 2 : 0);
   return line * 128 + (in ^ turn) * 16;
+}
+
+// The four bytes' numbers with the other sign (int8: -128, which the writer does not give, becomes 127).
+template <int FMT>
+__device__ __forceinline__ uint32_t negated(uint32_t w) {
+  return FMT == SV_CACHE_INT8 ? __vnegss4(w) : w ^ 0x80808080u;
 }
 
 struct RowTile {
@@ -156,10 +163,15 @@ __device__ __forceinline__ void write_row(const AttendParams &P, const AttendPla
 struct JoinSmem {
   float m[kAttendWarps][32], l[kAttendWarps][32];
   uint32_t top[kGroups * 8];  // largest finite |q| of a row
+  uint32_t none[kGroups * 8];  // the row sees a value scale that is no number
+  int token[kGroups * 8], limit[kGroups * 8];
 };
 
-template <int D, int FMT, int NT>
-__device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendPlan &L, const RowTile &T, uint8_t *smem,
+// ANY false: for value scales that kv_write gives to finite rows, and pages inside the cache.  Returns true, with nothing
+// written, if the CTA met another one: ANY true then takes any.  (With the rare case in the one loop, as a branch of
+// its own in each tile, the values' loads stayed behind it: 256 private histories 526 us against 477.)
+template <int D, int FMT, int NT, bool ANY>
+__device__ __forceinline__ bool attend_tile(const AttendParams &P, const AttendPlan &L, const RowTile &T, uint8_t *smem,
                                             JoinSmem &J) {
   using Y = Layout<D>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -295,9 +307,11 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
     for (int t = 0; t < D / 16; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.0f;
   }
   int stage = 0, fill = kStages - 1;
+  bool strange = false;
   for (int it = 0; it < ntiles; ++it) {
     copy_wait<kStages - 2>();
     __syncwarp();  // the tile is there for every lane, and no lane still reads the one before it
+    const uint32_t gone = ANY ? dead : 0u;  // the tile's keys that are left out
     if (it + kStages - 1 < ntiles) {  // (in the place of the one before)
       copy_keys(it + kStages - 1, fill, page);
 #pragma unroll
@@ -306,11 +320,19 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
     copy_commit();
     if (++fill == kStages) fill = 0;
     page = page_of(it + kStages);
-    const uint8_t *const src = ring_ptr + stage * Y::kStage;
+    uint8_t *const src = ring_ptr + stage * Y::kStage;
     if (++stage == kStages) stage = 0;
     const float2 sc = *reinterpret_cast<const float2 *>(src + Y::kScales + lane * 8);
-    float kc = sc.x * c_all, lv, inv;
-    value_scale_terms(sc.y, kc, lv, inv);
+    const float kc = sc.x * c_all;
+    const int k0 = T.k_begin + (it * kAttendWarps + warp) * kKeys;
+    float lv, inv;
+    if (ANY) {
+      value_scale_terms(sc.y, lv, inv);
+    } else {
+      lv = log2f(sc.y);
+      inv = __frcp_rn(fmaxf(sc.y, kLeastScale));  // (0 behind the range: weight 0 times a number)
+      strange |= !usual_scale(sc.y) && k0 + lane < T.k_end;  // (it is 0 for a page outside the cache)
+    }
     // scores: keys g, g + 8 of each half mt of the tile, rows 2c, 2c + 1 of each group
     float s[2][NT][4];
 #pragma unroll
@@ -343,6 +365,21 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
           }
       }
     }
+    const uint32_t odd = ANY ? __ballot_sync(0xFFFFFFFFu, !usual_scale(sc.y)) & ~gone : 0u;
+    if (ANY && odd) {  // the lane puts its key's value right in the ring
+      if (odd >> lane & 1u) {
+#pragma unroll 1
+        for (int col = 0; col < kCols; ++col) {
+          uint4 &w = *reinterpret_cast<uint4 *>(src + kKeys * D + tile_at<D, true>(lane, col));
+          w = usual_scale(-sc.y) ? make_uint4(negated<FMT>(w.x), negated<FMT>(w.y), negated<FMT>(w.z), negated<FMT>(w.w))
+                                 : make_uint4(0, 0, 0, 0);
+        }
+      }
+      const uint32_t none = __ballot_sync(0xFFFFFFFFu, !(fabsf(sc.y) < INFINITY)) & odd;
+      if (none && lane < T.rows && k0 + __ffs(none) - 1 < T.limit[lane])
+        J.none[lane] = 1;  // (the first such key decides which rows see one)
+      __syncwarp();
+    }
     // weights
     // x: scores without the value's scale.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
     Pair x[4][NT];
@@ -363,13 +400,12 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
         for (int k = 0; k < 4; ++k) x[k][nt] = mul2(x[k][nt], back);
       }
     }
-    const int k0 = T.k_begin + (it * kAttendWarps + warp) * kKeys;
-    if (k0 + kKeys > low) {  // some row does not see all of the tile
+    if (k0 + kKeys > low || (ANY && gone)) {  // some row does not see all of the tile
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int key = k0 + k * 8 + g;
+          const int key = ANY && (gone >> (k * 8 + g) & 1u) ? 0x7FFFFFFF : k0 + k * 8 + g;
           x[k][nt] = pair(key < limit[nt][0] ? lo(x[k][nt]) : -INFINITY, key < limit[nt][1] ? hi(x[k][nt]) : -INFINITY);
         }
     }
@@ -472,6 +508,7 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
     }
   }
   copy_wait<0>();
+  if (!ANY && __syncthreads_or(strange)) return true;
   if (bits && P.status) atomicOr(P.status, static_cast<int>(bits));
 
   // ---- the four warps' results joined ----
@@ -520,24 +557,26 @@ __device__ __forceinline__ void attend_tile(const AttendParams &P, const AttendP
 #pragma unroll
       for (int d = 0; d < kDims; ++d) all.o[d] = fmaf(acc[(w * NT * 8 + r) * Y::kPitch + lane * kDims + d], f, all.o[d]);
     }
+    if (ANY && J.none[r]) {
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) all.o[d] = __uint_as_float(0x7FC00000u);
+    }
     if (T.whole)
       write_row<D>(P, L, token, hq, lane, all);
     else
       store_part<D>(L, static_cast<int64_t>(token) * P.Hq + hq, T.slot, lane, all);
   }
+  return false;
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kAttendThreads, 2) attend_kernel(const AttendParams P, const AttendPlan L) {
-  pdl_enter();
+template <int D, int FMT, bool ANY>
+__device__ __forceinline__ bool attend_block(const AttendParams &P, const AttendPlan &L, JoinSmem &join) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ JoinSmem join;
-  __shared__ int row_token[kGroups * 8], row_limit[kGroups * 8];
   const int tid = threadIdx.x, H = P.c.num_kv_heads;
   RowTile T;
   T.table = P.tables;
-  T.token = row_token;
-  T.limit = row_limit;
+  T.token = join.token;
+  T.limit = join.limit;
   T.whole = false;
   int64_t first = 0;
   int len = 0, gam = 0;
@@ -569,21 +608,21 @@ __global__ void __launch_bounds__(kAttendThreads, 2) attend_kernel(const AttendP
     uint32_t bits = 0;
     const bool ok = attend_request(P, i, first, gam, len, bits);
     if (bits && tile == 0 && T.h == 0 && split == 0 && tid == 0 && P.status) atomicOr(P.status, static_cast<int>(bits));
-    if (!ok) return;
+    if (!ok) return false;
     // the request's row groups, dealt evenly to as few tiles as hold them
     const int all = (gam + 1) * P.group, groups = (all + 7) / 8, tiles = (groups + kGroups - 1) / kGroups;
-    if (tile >= tiles) return;
+    if (tile >= tiles) return false;
     const int per = (groups + tiles - 1) / tiles * 8;
     T.r0 = tile * per;
     T.rows = min(per, all - T.r0);
-    if (T.rows <= 0) return;
+    if (T.rows <= 0) return false;
     T.slot = L.prefix_splits + split;
     T.k_end = min(len, T.k_begin + L.own_chunk);
     // (a request without a prefix and with one chunk of keys or none needs no joining)
     T.whole = P.prefix == 0 && len <= L.own_chunk;
-    if (T.k_end <= T.k_begin && !(T.whole && split == 0)) return;
+    if (T.k_end <= T.k_begin && !(T.whole && split == 0)) return false;
   }
-  if (tid < kGroups * 8) join.top[tid] = 0;
+  if (tid < kGroups * 8) join.top[tid] = join.none[tid] = 0;
   if (tid < T.rows) {
     const int t = div_by(T.r0 + tid, L.group);
     int token = t, limit;
@@ -597,19 +636,23 @@ __global__ void __launch_bounds__(kAttendThreads, 2) attend_kernel(const AttendP
       token = static_cast<int>(first) + t;
       limit = len - gam + t;
     }
-    row_token[tid] = token;
-    row_limit[tid] = limit;
+    join.token[tid] = token;
+    join.limit[tid] = limit;
   }
   __syncthreads();
   const int groups = (T.rows + 7) / 8;
-  if (groups == 1)
-    attend_tile<D, FMT, 1>(P, L, T, smem, join);
-  else if (groups == 2)
-    attend_tile<D, FMT, 2>(P, L, T, smem, join);
-  else if (groups == 3)
-    attend_tile<D, FMT, 3>(P, L, T, smem, join);
-  else
-    attend_tile<D, FMT, 4>(P, L, T, smem, join);
+  if (groups == 1) return attend_tile<D, FMT, 1, ANY>(P, L, T, smem, join);
+  if (groups == 2) return attend_tile<D, FMT, 2, ANY>(P, L, T, smem, join);
+  if (groups == 3) return attend_tile<D, FMT, 3, ANY>(P, L, T, smem, join);
+  return attend_tile<D, FMT, 4, ANY>(P, L, T, smem, join);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kAttendThreads, 2)
+    attend_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ AttendPlan L) {
+  pdl_enter();
+  __shared__ JoinSmem join;
+  if (attend_block<D, FMT, false>(P, L, join)) attend_block<D, FMT, true>(P, L, join);
 }
 
 // Joins the partial results of a row: one warp a row.

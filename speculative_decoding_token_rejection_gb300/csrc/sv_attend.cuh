@@ -10,6 +10,8 @@
 // out = O / l and lse = (M + log2 l) ln 2.  So the weights that meet the byte
 // numbers in a 16-bit product are at most 1 whatever the sizes of the value
 // rows, and a scale costs one addition and one multiplication an element.
+// (Zero, negative and other unusual scales: value_scale_terms.)  A key whose
+// scale is more than 2^100 below a row's largest may drop out of l.
 // Weights are rounded to f16 for that product (11 bits, steps of 2^-24 of the
 // largest): the byte numbers have 8 bits and are exact, sums are fp32, and l
 // takes the unrounded weights.
@@ -101,15 +103,18 @@ __device__ __forceinline__ int prefix_limit(const AttendParams &P, int row) {
   return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(P.prefix), len - g + j)));
 }
 
-// log2 of a value scale and its reciprocal for the sum l.  Scale 0 stands for
-// a key that is left out.  A value scale that is not a positive number makes
-// the key's factor NaN instead: the scores of the rows that see the key become
-// NaN, and those of the others are replaced as for any key they do not see.
-__device__ __forceinline__ void value_scale_terms(float vs, float &kc, float &lv, float &inv) {
-  const bool ok = vs > 0.0f && vs < INFINITY;
-  lv = ok ? log2f(vs) : (vs == 0.0f ? -INFINITY : 0.0f);
-  inv = ok ? __frcp_rn(vs) : 1.0f;
-  if (!ok && vs != 0.0f) kc = __uint_as_float(0x7FC00000u);
+// A value scale may be any float, and its key counts in l whatever it is.  Its
+// size enters a softmax as kLeastScale at least, the smallest that kv_write
+// gives; one below that counts as zero, as does one that is no number, and the
+// rows that see a key of the latter get NaN outputs.
+constexpr float kLeastScale = 0x1p-64f, kLeastLog2 = -64.0f;
+__device__ __forceinline__ bool usual_scale(float vs) { return vs >= kLeastScale && vs < INFINITY; }
+// log2 of its size, and the size's reciprocal for the sum l.
+__device__ __forceinline__ void value_scale_terms(float vs, float &lv, float &inv) {
+  const float a = fabsf(vs);
+  const bool ok = usual_scale(a);
+  lv = ok ? log2f(a) : kLeastLog2;
+  inv = ok ? __frcp_rn(a) : 1.0f / kLeastScale;
 }
 
 // The exponent of the power of two that a row of q, whose largest finite |q| has

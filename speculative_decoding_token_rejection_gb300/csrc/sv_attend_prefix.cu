@@ -35,11 +35,12 @@
 //
 // Numbers.  x = (q . b) * (scale * log2 e * key_scale) as in sv_attend.cuh, but
 // the value scales are kept out of the exponent: w = 2^(x - m), l = sum w,
-// P = w * value_scale / W with W a power of two near the first tile's largest
-// value scale, O = W * sum P b.  Any m gives the same quotient O / l; it is
-// raised to the largest x + log2(value_scale / W) when that passes it by 8, so
-// P stays below 2^8.  Whether it may have is seen from max x and the tile's
-// largest value scale alone.
+// P = w * value_scale / W, O = W * sum P b.  Any m gives the same quotient O / l;
+// it is raised to the largest x + log2(value_scale / W) when that passes it by
+// 8, so P stays below 2^8.  Whether it may have is seen from max x and the
+// tile's largest value scale alone.  W is 2^28, the middle of the scales that
+// kv_write gives (2^-64 to 2^121): w and l stay within fp32 for any of them.
+// (One near the first tile's scales sent later ones out of range.)
 //
 // Measured: 512 requests x 8 tokens over 16384 keys, 829 us of the call's 1.07
 // ms: 1.33 PFLOP/s, 70 % of a plain matrix product's rate.  A key tile takes a
@@ -60,22 +61,22 @@ constexpr int kSoftmaxThreads = 256;
 constexpr int kVectorThreads = 64;
 constexpr int kPrefixThreads = kSoftmaxThreads + kVectorThreads + 64;
 constexpr int kVectorSlots = 4;
-constexpr int kWSlots = 8;  // the factors run at most four tiles, so four segments, ahead
 constexpr uint32_t kWaitPolls = 1u << 24;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRaise = 8;
+constexpr float kScaleUnit = 0x1p28f;  // W
+constexpr float kLeastUnits = kLeastLog2 - 28;  // log2 of the size that a scale counts as at least, in W
 
 struct alignas(16) Vectors {  // of one key tile
   float2 kc[kKeyTile / 2], vr[kKeyTile / 2];  // of two keys: their factors; their value scales / W
   uint32_t dead[4];  // keys left out, a bit each
+  uint32_t none[4];  // keys whose value scale is no number
   float top[2];      // log2 of the largest value scale / W, of keys 0-31 and 64-95, and of the others
 };
 
 struct Control {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], vec_full[kVectorSlots], vec_empty[kVectorSlots], s_full[2], p_full[2], q_full, done;
   uint32_t tmem, abort;
-  float w[kWSlots];        // W of a segment
-  float w_of_warp[2][2];
   float back[2 * kRowsTile];  // what undoes a row's power of two
 };
 
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         l[x] = pair(0.0f, 0.0f);
       }
       bool ok = true;
+      uint32_t nan_rows = 0;  // bit x: the row sees a value scale that is no number
       for (int i = 0; ok && i < n; ++i) {
         const int it = done_tiles + i;
         const Vectors &V = vec[it % kVectorSlots];
@@ -425,7 +427,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         fence_after();
         const int k0 = k_begin + i * kKeyTile;
         const uint32_t any_dead = V.dead[0] | V.dead[1] | V.dead[2] | V.dead[3];
-        const bool cut = any_dead || k0 + kKeyTile > low || shifted;
+        const uint32_t any_none = V.none[0] | V.none[1] | V.none[2] | V.none[3];
+        const bool cut = any_dead || any_none || k0 + kKeyTile > low || shifted;
         const float over = fmaxf(V.top[0], V.top[1]);
         uint32_t s[2][64];  // rows g and g + 8 of each half of the warp's 32: the scores, then the exponents
         auto load_scores = [&]() {
@@ -491,6 +494,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
               top[x] = fmaxf(top[x], fmaxf(a_, b_));
             }
           }
+          if (any_none) {  // the first such key decides which rows see one
+            const int key = k0 + (V.none[0]   ? __ffs(V.none[0])
+                                  : V.none[1] ? 32 + __ffs(V.none[1])
+                                  : V.none[2] ? 64 + __ffs(V.none[2])
+                                              : 96 + __ffs(V.none[3])) - 1;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) nan_rows |= key < limit[x] ? 1u << x : 0u;
+          }
           bool raise = false;
 #pragma unroll
           for (int x = 0; x < 4; ++x) raise |= top[x] + over > m[x] + kRaise || (m[x] == -INFINITY && top[x] > -INFINITY);
@@ -499,7 +510,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const float2 f = V.vr[j * 4 + c];
-              const Pair lv = pair(__log2f(f.x), __log2f(f.y));
+              const Pair lv = pair(fmaxf(__log2f(fabsf(f.x)), kLeastUnits), fmaxf(__log2f(fabsf(f.y)), kLeastUnits));
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const Pair y = add2(get(x, j), lv);
@@ -567,7 +578,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       if (ok) ok = wait_warp(C, &C.done, done_segments & 1);
       fence_after();
       if (t < tiles) {
-        const float w = ok ? *const_cast<volatile float *>(&C.w[done_segments % kWSlots]) : 0.0f;
         int64_t at[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -589,9 +599,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               const int x = half * 2 + (e >> 1 & 1);
+              const float by = nan_rows >> x & 1u ? __uint_as_float(0x7FC00000u) : kScaleUnit;
               if (ok && at[x] >= 0)
                 *reinterpret_cast<float2 *>(L.part_o + at[x] * D + q * 32 + (e >> 2) * 8 + 2 * c) =
-                    make_float2(__uint_as_float(o[e]) * w, __uint_as_float(o[e + 1]) * w);
+                    make_float2(__uint_as_float(o[e]) * by, __uint_as_float(o[e + 1]) * by);
             }
           }
       }
@@ -614,7 +625,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       const float *const kscale = P.c.k_scale + h * P.c.scale_head_stride;
       const float *const vscale = P.c.v_scale + h * P.c.scale_head_stride;
       float ks[2], vs[2];
-      bool in[2];  // a key of the range
+      bool out[2];  // a key of the range whose page is outside the cache (those behind the range are no row's)
       int page[2];
       auto key_of = [&](int i, int e) { return k_begin + i * kKeyTile + lt + e * kVectorThreads; };
       auto pages = [&](int i) {
@@ -625,14 +636,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int k = key_of(i, e);
-          in[e] = i < n && k < k_end;
+          const bool in = i < n && k < k_end;
+          out[e] = false;
           ks[e] = vs[e] = 0.0f;
-          if (in[e] && page[e] >= 0 && page[e] < P.c.num_blocks) {
+          if (in && page[e] >= 0 && page[e] < P.c.num_blocks) {
             const int64_t at = page[e] * P.c.scale_block_stride +
                                (k - div_by(k, L.page) * P.c.block_size) * P.c.scale_token_stride;
             ks[e] = kscale[at];
             vs[e] = vscale[at];
-          } else if (in[e]) {
+          } else if (in) {
+            out[e] = true;
             bad = SV_DATA_BAD_SLOT;
           }
         }
@@ -640,22 +653,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       pages(0);
       scales(0);
       pages(1);
-      // W: the power of two at the first tile's largest value scale
-      float unscale;
-      {
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (vs[e] > 0.0f && vs[e] < INFINITY) top = max(top, __float_as_uint(vs[e]));
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        volatile float *const two = C.w_of_warp[done_segments & 1];
-        if (lane == 0) two[warp - 8] = __uint_as_float(top);
-        asm volatile("bar.sync 2, 64;" ::: "memory");
-        const uint32_t bits_w = __float_as_uint(fmaxf(two[0], two[1]));
-        const int e = bits_w >= 0x00800000u ? static_cast<int>(bits_w >> 23) - 127 : 0;
-        unscale = pow2(max(-126, min(126, -e)));
-        if (lt == 0) *const_cast<volatile float *>(&C.w[done_segments % kWSlots]) = 1.0f / unscale;
-      }
       const float c_all = P.scale * kLog2e;
       for (int i = 0; ok && i < n; ++i) {
         const int it = done_tiles + i, slot_v = it % kVectorSlots;
@@ -666,24 +663,24 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = lt + e * kVectorThreads;
-          float kc = ks[e] * c_all, v = vs[e];
-          // (scale 0: a key whose page is outside the cache; keys behind the range are no row's)
-          const bool good = v > 0.0f && v < INFINITY, out = in[e] && v == 0.0f;
-          if (!good && v != 0.0f) kc = __uint_as_float(0x7FC00000u);
-          if (good) most = fmaxf(most, v);
-          const uint32_t dead = __ballot_sync(0xFFFFFFFFu, out);
-          (r & 1 ? V.kc[r >> 1].y : V.kc[r >> 1].x) = out ? 0.0f : kc;
-          (r & 1 ? V.vr[r >> 1].y : V.vr[r >> 1].x) = good ? v * unscale : 1.0f;
-          if (lane == 0) V.dead[r >> 5] = dead;
+          const float v = vs[e];
+          const bool number = fabsf(v) < INFINITY;
+          if (number) most = fmaxf(most, fabsf(v));
+          (r & 1 ? V.kc[r >> 1].y : V.kc[r >> 1].x) = ks[e] * c_all;
+          (r & 1 ? V.vr[r >> 1].y : V.vr[r >> 1].x) = number && fabsf(v) >= kLeastScale ? v * (1.0f / kScaleUnit) : 0.0f;
+          const uint32_t dead = __ballot_sync(0xFFFFFFFFu, out[e]), none = __ballot_sync(0xFFFFFFFFu, !number);
+          if (lane == 0) {
+            V.dead[r >> 5] = dead;
+            V.none[r >> 5] = none;
+          }
         }
         const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
-        if (lane == 0) V.top[warp - 8] = top ? log2f(__uint_as_float(top) * unscale) : -INFINITY;
+        if (lane == 0) V.top[warp - 8] = log2f(fmaxf(__uint_as_float(top), kLeastScale) * (1.0f / kScaleUnit));
         mbar_arrive(&C.vec_full[slot_v]);
         scales(i + 1);
         pages(i + 2);
       }
       done_tiles += n;
-      ++done_segments;
       u = tile_from(u + n);
     }
     if (P.status && (bad || !ok)) atomicOr(P.status, static_cast<int>(bad | (ok ? 0u : SV_DATA_COPY_TIMEOUT)));
