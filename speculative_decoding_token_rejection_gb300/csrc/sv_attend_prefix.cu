@@ -704,14 +704,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           ++issued;
         }
       }
-      // (after a wait that gave up: the last copies end before the shared memory goes)
-      if (!ok)
-        for (int j = max(0, issued - 4); j < issued; ++j) {
-          const int it = j >> 1;
-          const uint64_t began = now_ns();
-          while (!mbar_try_wait(j & 1 ? &C.v_full[it & 1] : &C.k_full[it & 1], it >> 1 & 1) && now_ns() - began < kWaitNs) {
-          }
+      // (the last copies end before the shared memory goes: where another role has given up, nobody else waits for them)
+      for (int j = max(0, issued - 4); j < issued; ++j) {
+        const int it = j >> 1;
+        const uint64_t began = now_ns();
+        while (!mbar_try_wait(j & 1 ? &C.v_full[it & 1] : &C.k_full[it & 1], it >> 1 & 1) && now_ns() - began < kWaitNs) {
         }
+      }
     }
     __syncwarp();
   } else {
