@@ -132,6 +132,11 @@ enum sv_data_status {
  * SV_DATA_COPY_TIMEOUT and emit nothing.  Only calls whose rows are copied
  * (SV_FLAG_RESIDENT_ROWS, or unaligned rows) are affected. */
 #define SV_TEST_EXPIRE_COPY_WAIT 1u
+/* SV_TEST_EXPIRE_PRODUCT_WAIT (attention calls): where a shared prefix is met
+ * by the tensor cores, the first wait for a tile's weights gives up at once, as
+ * if they had not come within its limit.  What is in flight still ends before
+ * the CTA does. */
+#define SV_TEST_EXPIRE_PRODUCT_WAIT 2u
 
 typedef struct spec_verify_ctx *spec_verify_t;
 
@@ -402,8 +407,8 @@ sv_status spec_verify_check_kv_args(const spec_verify_config *config, const spec
  * one that is NaN or infinite makes out NaN, not lse, in the rows that see its
  * key (for the heads that read it).  A key whose value scale is less than
  * 2^-100 of the largest that a row sees may drop out of the row's lse.
- * SV_DATA_COPY_TIMEOUT: a wait inside a kernel ran out and the outputs are not
- * the result; never expected on a healthy GPU.
+ * SV_DATA_COPY_TIMEOUT: a wait inside a kernel ran out and out and lse are NaN
+ * in the rows it was for; never expected on a healthy GPU.
  *
  * The products take 16-bit operands: the cache's numbers and q (scaled by a
  * power of two) are exact in them, the softmax's weights are rounded to 11
@@ -424,7 +429,7 @@ typedef struct spec_verify_attend_args {
   int64_t block_table_stride;
   const int32_t *seq_lens; /* [N] */
   float scale;             /* finite */
-  uint32_t reserved2;      /* 0 */
+  uint32_t test_flags;     /* 0, or SV_TEST_EXPIRE_PRODUCT_WAIT (tests only) */
   void *out; /* [T+N, num_q_heads, head_dim] bf16 */
   int64_t out_token_stride, out_head_stride;
   float *lse;      /* [T+N, num_q_heads] contiguous, or NULL */

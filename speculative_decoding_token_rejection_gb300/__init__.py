@@ -40,6 +40,7 @@ SV_FLAG_SERIAL_LAUNCH = 4
 SV_HINT_SMALL_TOP_K = 1
 SV_SMALL_TOP_K_MAX = 256
 SV_TEST_EXPIRE_COPY_WAIT = 1
+SV_TEST_EXPIRE_PRODUCT_WAIT = 2
 SV_CACHE_INT8, SV_CACHE_E4M3 = 0, 1
 SV_MAX_TOP_LOGPROBS = 32
 
@@ -121,10 +122,12 @@ class SpecVerifyAttendArgs(ctypes.Structure):
         ("num_draft_tokens_total", ctypes.c_int64), ("cu_num_draft_tokens", _P), ("cache", SpecVerifyKvCache),
         ("q", _P), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
         ("block_tables", _P), ("block_table_stride", ctypes.c_int64), ("seq_lens", _P),
-        ("scale", ctypes.c_float), ("reserved2", ctypes.c_uint32),
+        ("scale", ctypes.c_float), ("test_flags", ctypes.c_uint32),
         ("out", _P), ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
         ("lse", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_int64), ("status", _P),
     ]
+    # the name that test_flags had while it was reserved
+    reserved2 = property(lambda self: self.test_flags, lambda self, value: setattr(self, "test_flags", value))
 
 
 class SpecVerifyLogprobsArgs(ctypes.Structure):
@@ -618,7 +621,7 @@ def spec_verify_check_kv_args(config: SpecVerifyConfig, args: SpecVerifyKvArgs) 
 
 def build_attend_args(*, q, cache: KVCache, block_tables, seq_lens, max_seq_len: int, max_spec_len: int,
                       scale: float, out, cu_num_draft_tokens=None, shared_prefix_len: int = 0, lse=None,
-                      workspace=None, status=None) -> SpecVerifyAttendArgs:
+                      workspace=None, status=None, test_flags: int = 0) -> SpecVerifyAttendArgs:
     """Validate tensors and fill a SpecVerifyAttendArgs (no device work).
     ``q`` and ``out``: bfloat16 [T+N, num_q_heads, head_dim];
     ``block_tables``: int32 [N, pages]; ``seq_lens``: int32 [N]; ``lse``:
@@ -650,7 +653,7 @@ def build_attend_args(*, q, cache: KVCache, block_tables, seq_lens, max_seq_len:
         N, int(max_spec_len), hq, int(max_seq_len), int(shared_prefix_len), 0, rows - N,
         _vector(cu_num_draft_tokens, i32, "cu_num_draft_tokens", device, N), cache.struct,
         *_heads(q, "q", device, shape, bf16), block_tables.data_ptr(), between,
-        _vector(seq_lens, i32, "seq_lens", device, N), float(scale), 0, *_heads(out, "out", device, shape, bf16),
+        _vector(seq_lens, i32, "seq_lens", device, N), float(scale), int(test_flags), *_heads(out, "out", device, shape, bf16),
         _vector(lse, torch.float32, "lse", device, rows * hq),
         None if workspace is None else _vector(workspace, torch.uint8, "workspace", device, workspace.numel()),
         0 if workspace is None else workspace.numel(), _vector(status, i32, "status", device, 1))

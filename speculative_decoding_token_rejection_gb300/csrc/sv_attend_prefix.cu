@@ -210,22 +210,41 @@ __device__ __forceinline__ uint64_t now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Waits for phase `parity` of a barrier; false when the CTA gives up (a wait
-// of two seconds, or another thread that did).
-__device__ __forceinline__ bool wait(Control &C, uint64_t *bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t began = now_ns();
-  for (uint32_t it = 0; it < kWaitPolls; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*const_cast<volatile uint32_t *>(&C.abort)) return false;
-    if ((it & 15u) == 15u && now_ns() - began > kWaitNs) break;
-  }
+// The CTA gives up: no wait begins anew, rows that are not done become NaN, and
+// the status word says so at the end.
+__device__ __forceinline__ void give_up(Control &C) {
   *const_cast<volatile uint32_t *>(&C.abort) = 1;
+  __threadfence_block();
+}
+__device__ __forceinline__ bool gave_up(const Control &C) { return *const_cast<const volatile uint32_t *>(&C.abort) != 0; }
+// Waits for phase `parity` of a barrier; false when the CTA gives up (a wait
+// of two seconds, `expire`, or another thread that did).
+__device__ __forceinline__ bool wait(Control &C, uint64_t *bar, uint32_t parity, bool expire = false) {
+  if (!expire) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t began = now_ns();
+    for (uint32_t it = 0; it < kWaitPolls; ++it) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (gave_up(C)) return false;
+      if ((it & 15u) == 15u && now_ns() - began > kWaitNs) break;
+    }
+  }
+  give_up(C);
   return false;
 }
 // The same for all lanes of a warp together.
-__device__ __forceinline__ bool wait_warp(Control &C, uint64_t *bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, wait(C, bar, parity));
+__device__ __forceinline__ bool wait_warp(Control &C, uint64_t *bar, uint32_t parity, bool expire = false) {
+  return __all_sync(0xFFFFFFFFu, wait(C, bar, parity, expire));
+}
+// Waits for what is in flight, also in a CTA that has given up: shared and
+// tensor memory must not go before it.
+__device__ __forceinline__ void settle(Control &C, uint64_t *bar, uint32_t parity) {
+  const uint64_t began = now_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (now_ns() - began > kWaitNs) {
+      give_up(C);
+      return;
+    }
 }
 
 // The prefix's K and V as f16 tiles of 128 keys, each in the order of its
@@ -335,6 +354,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
     // -------------------------------------------------------------------
     const int t = warp >> 2, w4 = warp & 3;
     int mine = 0;  // key tiles of this row tile so far
+    bool ok = true;
     for (int u = u_begin; u < u_end;) {
       const Segment S = segment(u);
       const int h = S.h, r0 = S.r0, tiles = S.tiles, n = S.n, k_begin = S.k_begin, slot = S.slot;
@@ -412,7 +432,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         m[x] = -INFINITY;
         l[x] = pair(0.0f, 0.0f);
       }
-      bool ok = true;
       uint32_t nan_rows = 0;  // bit x: the row sees a value scale that is no number
       for (int i = 0; ok && i < n; ++i) {
         const int it = done_tiles + i;
@@ -574,8 +593,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         __syncwarp();
         if (lane == 0) mbar_arrive(&C.vec_empty[it % kVectorSlots]);
       }
-      // the partial result
-      if (ok) ok = wait_warp(C, &C.done, done_segments & 1);
+      // the partial result: NaN from a CTA that has given up (its products may have ended early)
+      if (ok) ok = wait_warp(C, &C.done, done_segments & 1) && !__any_sync(0xFFFFFFFFu, gave_up(C));
       fence_after();
       if (t < tiles) {
         int64_t at[4];
@@ -587,10 +606,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           float sum = lo(l[x]) + hi(l[x]);
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-          if (c == 0 && at[x] >= 0) L.part_ml[at[x]] = ok ? make_float2(m[x], sum) : make_float2(-INFINITY, 0.0f);
+          if (c == 0 && at[x] >= 0)
+            L.part_ml[at[x]] = ok ? make_float2(m[x], sum) : make_float2(-INFINITY, __uint_as_float(0x7FC00000u));
         }
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q)
+        for (int q = 0; ok && q < D / 32; ++q)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t o[16];
@@ -600,7 +620,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
             for (int e = 0; e < 16; e += 2) {
               const int x = half * 2 + (e >> 1 & 1);
               const float by = nan_rows >> x & 1u ? __uint_as_float(0x7FC00000u) : kScaleUnit;
-              if (ok && at[x] >= 0)
+              if (at[x] >= 0)
                 *reinterpret_cast<float2 *>(L.part_o + at[x] * D + q * 32 + (e >> 2) * 8 + 2 * c) =
                     make_float2(__uint_as_float(o[e]) * by, __uint_as_float(o[e + 1]) * by);
             }
@@ -683,7 +703,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
       done_tiles += n;
       u = tile_from(u + n);
     }
-    if (P.status && (bad || !ok)) atomicOr(P.status, static_cast<int>(bad | (ok ? 0u : SV_DATA_COPY_TIMEOUT)));
+    if (P.status && bad) atomicOr(P.status, static_cast<int>(bad));
   } else if (warp == 10) {
     // -------------------------------------------------------------------
     // copies
@@ -704,12 +724,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           ++issued;
         }
       }
-      // (the last copies end before the shared memory goes: where another role has given up, nobody else waits for them)
+      // (nobody else may wait for the last ones)
       for (int j = max(0, issued - 4); j < issued; ++j) {
         const int it = j >> 1;
-        const uint64_t began = now_ns();
-        while (!mbar_try_wait(j & 1 ? &C.v_full[it & 1] : &C.k_full[it & 1], it >> 1 & 1) && now_ns() - began < kWaitNs) {
-        }
+        settle(C, j & 1 ? &C.v_full[it & 1] : &C.k_full[it & 1], it >> 1 & 1);
       }
     }
     __syncwarp();
@@ -770,7 +788,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         const int it = done_tiles + i, st = it & 1, sn = st ^ 1;
         ok = wait_warp(C, &C.v_full[st], it >> 1 & 1);
         for (int t = 0; ok && t < tiles; ++t) {
-          ok = wait_warp(C, &C.p_full[t], (t ? second + i : it) & 1);
+          ok = wait_warp(C, &C.p_full[t], (t ? second + i : it) & 1, P.expire);
           if (!ok) break;
           fence_after();
           outputs(t, st, i > 0);
@@ -786,11 +804,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           }
         }
       }
-      // (after a wait that gave up too: the products in flight end before the memory goes)
       commit(&C.done);
-      const uint64_t began = now_ns();
-      while (!mbar_try_wait(&C.done, done_segments & 1) && now_ns() - began < kWaitNs) {
-      }
+      settle(C, &C.done, done_segments & 1);
       __syncwarp();
       done_tiles += n;
       ++done_segments;
@@ -802,7 +817,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
   }
   __syncthreads();
   fence_after();
-  if (warp == 11) tmem_free(C.tmem, 512);
+  if (warp == 11) {
+    tmem_free(C.tmem, 512);
+    if (lane == 0 && gave_up(C) && P.status) atomicOr(P.status, static_cast<int>(SV_DATA_COPY_TIMEOUT));
+  }
 }
 
 template <int D, int FMT>

@@ -216,6 +216,7 @@ struct AttendParams {
   int64_t table_stride;
   const int32_t *seq_lens;
   float scale;
+  bool expire;  // SV_TEST_EXPIRE_PRODUCT_WAIT
   uint16_t *out;
   int64_t out_token, out_head;
   float *lse;

@@ -96,6 +96,7 @@ sv::AttendParams attend_params(const spec_verify_t h, const spec_verify_attend_a
   p.table_stride = a->block_table_stride;
   p.seq_lens = a->seq_lens;
   p.scale = a->scale;
+  p.expire = (a->test_flags & SV_TEST_EXPIRE_PRODUCT_WAIT) != 0;
   p.out = static_cast<uint16_t *>(a->out);
   p.out_token = a->out_token_stride;
   p.out_head = a->out_head_stride;
@@ -173,7 +174,9 @@ sv_status spec_verify_check_attend_args(const spec_verify_config *c, const spec_
   if (st != SV_OK) return st;
   if (!a) return fail(SV_ERR_INVALID_ARG, "args is NULL");
   if ((st = check_attend_sizes(c, a)) != SV_OK) return st;
-  if (a->reserved || a->reserved2) return fail(SV_ERR_INVALID_ARG, "reserved must be 0");
+  if (a->reserved) return fail(SV_ERR_INVALID_ARG, "reserved must be 0");
+  if (a->test_flags & ~SV_TEST_EXPIRE_PRODUCT_WAIT)
+    return fail(SV_ERR_INVALID_ARG, "unknown test_flags 0x%x", a->test_flags);
   if (a->num_reqs == 0) return SV_OK;
   if ((st = check_cache(a->cache)) != SV_OK) return st;
   const spec_verify_kv_cache &c8 = a->cache;

@@ -199,3 +199,11 @@ def test_binding_refusals():
                       (dict(logits=torch.zeros(100, 6).t()), ValueError)):
         with pytest.raises(error):
             sv.build_logprobs_args(**{**good, **kw})
+
+
+@pytest.mark.parametrize("value,code", [(0, OK), (sv.SV_TEST_EXPIRE_PRODUCT_WAIT, OK), (sv.SV_TEST_EXPIRE_COPY_WAIT, INVALID),
+                                        (3, INVALID), (4, INVALID)])
+def test_attend_test_flags(value, code):
+    a = attend_args()
+    a.test_flags = value
+    assert sv.spec_verify_check_attend_args(cfg(), a) == code
