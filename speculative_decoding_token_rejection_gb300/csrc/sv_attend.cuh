@@ -77,30 +77,43 @@ __device__ __forceinline__ bool attend_request(const AttendParams &P, int i, int
   return true;
 }
 
+// The request whose range of verify tokens holds `row`, or -1.  The ranges that
+// are in order need not be found by a search over all of them, which one bad
+// entry misleads: then they are looked through.
+__device__ __forceinline__ int request_of_row(const AttendParams &P, int row) {
+  if (!P.cu) return row / (P.G + 1);
+  const auto holds = [&](int64_t s, int64_t e, int i) {
+    return s >= 0 && e >= s && e <= P.T && e - s <= P.G && s + i <= row && row <= e + i;
+  };
+  int lo = 0, hi = P.N - 1;  // the first request whose last row cu[i] + i is at or behind `row`
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(P.cu[mid]) + mid >= row)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  if (holds(lo ? P.cu[lo - 1] : 0, P.cu[lo], lo)) return lo;
+  int at = -1;
+  int32_t s = 0;
+#pragma unroll 4
+  for (int i = 0; i < P.N; ++i) {
+    const int32_t e = P.cu[i];
+    if (holds(s, e, i)) at = i;
+    s = e;
+  }
+  return at;
+}
+
 // Prefix keys that verify token `row` sees (0 .. P.prefix), or -1 for a row
 // that belongs to no request.
 __device__ __forceinline__ int prefix_limit(const AttendParams &P, int row) {
-  int i;
-  if (!P.cu) {
-    i = row / (P.G + 1);
-  } else {  // the first request whose last row cu[i] + i is at or behind `row`
-    int lo = 0, hi = P.N - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (static_cast<int64_t>(P.cu[mid]) + mid >= row)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    i = lo;
-  }
+  const int i = request_of_row(P, row);
   int64_t first;
   int g, len;
   uint32_t bits = 0;
-  if (!attend_request(P, i, first, g, len, bits)) return -1;
-  const int64_t j = row - first;
-  if (j < 0 || j > g) return -1;
-  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(P.prefix), len - g + j)));
+  if (i < 0 || !attend_request(P, i, first, g, len, bits)) return -1;
+  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(P.prefix), len - g + (row - first))));
 }
 
 // A value scale may be any float, and its key counts in l whatever it is.  Its

@@ -1,0 +1,32 @@
+"""Attention with a prefix that is shared by the batch -- unpacked once, met by
+every request's rows on the tensor cores, joined with the private keys -- in
+the ways a call may be made: launch modes, streams, graphs, workspaces, and bad
+data.  Each case takes the shortest prefix that a call of its sizes shares."""
+import pytest
+import torch
+
+import speculative_decoding_token_rejection_gb300 as sv
+from test_gpu_attend import run
+from test_gpu_attend_scales import shared
+
+pytestmark = pytest.mark.gpu
+
+BITS = sv.DATA_STATUS_BITS
+
+
+@pytest.mark.parametrize("entry, value", [(9, 140), (14, 2), (19, 0), (19, -5), (29, 160)])
+def test_a_bad_range_leaves_the_others_right(entry, value):
+    """Requests whose own range is in order get their result, whatever stands in the entries of others."""
+    N, G = 40, 4
+    c = shared([G] * N, [5 + i for i in range(N)], seed=23)
+    ws = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")
+    want, want_lse, _ = run(c, workspace=ws)
+    assert c["cu"][entry] == G * (entry + 1)
+    c["cu"][entry] = value
+    ws.fill_(0xFF)
+    out, lse, status = run(c, workspace=ws)
+    assert status == BITS["BAD_CU"]
+    for i in range(N):
+        if i not in (entry, entry + 1):
+            rows = slice(i * (G + 1), (i + 1) * (G + 1))
+            assert torch.equal(out[rows], want[rows]) and torch.equal(lse[rows], want_lse[rows]), i
