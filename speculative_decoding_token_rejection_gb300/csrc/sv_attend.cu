@@ -640,6 +640,10 @@ __device__ __forceinline__ bool attend_block(const AttendParams &P, const Attend
     join.limit[tid] = limit;
   }
   __syncthreads();
+  if (shared_part) {  // (keys behind every row's are not read: what is there may be no numbers)
+    const int r = tid & 31;
+    T.k_end = min(T.k_end, __reduce_max_sync(0xFFFFFFFFu, r < T.rows && join.token[r] >= 0 ? join.limit[r] : 0));
+  }
   const int groups = (T.rows + 7) / 8;
   if (groups == 1) return attend_tile<D, FMT, 1, ANY>(P, L, T, smem, join);
   if (groups == 2) return attend_tile<D, FMT, 2, ANY>(P, L, T, smem, join);

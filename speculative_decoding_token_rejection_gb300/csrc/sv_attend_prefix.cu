@@ -249,7 +249,9 @@ __device__ __forceinline__ void settle(Control &C, uint64_t *bar, uint32_t parit
 
 // The prefix's K and V as f16 tiles of 128 keys, each in the order of its
 // shared memory: 64 dimensions after 64, rows of 128 bytes, 16-byte columns
-// exchanged by row % 8.  Keys that are not there are zeros.
+// exchanged by row % 8.  Keys that are not there are zeros, and so are e4m3
+// values that are no numbers: they lie behind every request's length, and a
+// weight of 0 times one would be NaN.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const AttendParams P, const AttendPlan L) {
   pdl_enter();
@@ -268,6 +270,10 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const AttendParams P, 
       if (page >= 0 && page < P.c.num_blocks)
         raw[p] = __ldg(reinterpret_cast<const uint2 *>(
             base + page * P.c.block_stride + (k - x * P.c.block_size) * P.c.token_stride));
+      if (FMT == SV_CACHE_E4M3 && side) {
+        raw[p].x &= ~__vcmpeq4(raw[p].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        raw[p].y &= ~__vcmpeq4(raw[p].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      }
     }
   }
 #pragma unroll

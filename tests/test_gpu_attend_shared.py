@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import speculative_decoding_token_rejection_gb300 as sv
-from test_gpu_attend import run
+from test_gpu_attend import check, make, run
 from test_gpu_attend_scales import shared
 
 pytestmark = pytest.mark.gpu
@@ -30,3 +30,19 @@ def test_a_bad_range_leaves_the_others_right(entry, value):
         if i not in (entry, entry + 1):
             rows = slice(i * (G + 1), (i + 1) * (G + 1))
             assert torch.equal(out[rows], want[rows]) and torch.equal(lse[rows], want_lse[rows]), i
+
+
+@pytest.mark.parametrize("many", [True, False])
+def test_bytes_behind_every_length_may_be_anything(many):
+    """Pages of the prefix that no request's tokens reach yet: NaN scales and bytes."""
+    if many:
+        c = shared([4] * 40, [-60 - i for i in range(40)], uniform=True, fmt="e4m3", seed=24)
+    else:
+        c = make([1, 0], [1500, 1421], prefix=2400, group=2, fmt="e4m3", seed=24)
+    cache, b, last = c["cache"], c["cache"].block_size, max(c["lens"])
+    for t in range(last, c["prefix"]):
+        page, off = int(c["table"][0, t // b]), t % b
+        for data, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+            scale[page, :, off] = float("nan")
+            data.view(torch.uint8)[page, :, off] = 0x7F if t % 2 else 0xFF
+    check(c)
