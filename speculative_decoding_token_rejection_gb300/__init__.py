@@ -644,6 +644,9 @@ def build_attend_args(*, q, cache: KVCache, block_tables, seq_lens, max_seq_len:
     shape = (rows, hq, cache.head_dim)
     if N <= 1:
         between = width
+    elif between < width:  # (the row stride is what the library takes for a row's length)
+        raise ValueError(f"block_tables rows must not overlap (stride {between} for {width} pages); an expanded table "
+                         f"has to be made contiguous")
     elif between > width:  # rows of a wider table: what lies between them is not the table's
         max_seq_len = min(max_seq_len, width * cache.block_size)
     if 0 in out.stride() and any(n > 1 and s == 0 for n, s in zip(out.shape, out.stride())):

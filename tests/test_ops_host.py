@@ -207,3 +207,19 @@ def test_attend_test_flags(value, code):
     a = attend_args()
     a.test_flags = value
     assert sv.spec_verify_check_attend_args(cfg(), a) == code
+
+
+def test_expanded_block_tables_are_refused():
+    q = torch.zeros(6, 4, 64, dtype=torch.bfloat16)
+    good = dict(q=q, out=torch.zeros_like(q), cache=sv.KVCache(**tensors()), seq_lens=torch.zeros(3, dtype=torch.int32),
+                max_seq_len=40, max_spec_len=1, scale=1.0)
+    table = torch.zeros(1, 3, dtype=torch.int32)
+    for bad in (table.expand(3, -1), torch.zeros(20, dtype=torch.int32).as_strided((3, 3), (2, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            sv.build_attend_args(**good, block_tables=bad)
+    for fine in (table.expand(3, -1).contiguous(), torch.zeros(3, 5, dtype=torch.int32)[:, :3], torch.zeros(3, 0, dtype=torch.int32)):
+        a = sv.build_attend_args(**good, block_tables=fine)
+        assert a.block_table_stride >= fine.shape[1]
+    one = sv.build_attend_args(**{**good, "q": q[:2], "out": good["out"][:2], "seq_lens": good["seq_lens"][:1]},
+                               block_tables=table.expand(1, -1))
+    assert one.block_table_stride == 3
