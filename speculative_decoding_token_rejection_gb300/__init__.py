@@ -14,6 +14,7 @@ allocation for convenience.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import pathlib
 from dataclasses import dataclass
@@ -497,6 +498,19 @@ def _stream_handle(stream, device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _allocated_on(stream, device):
+    """The context in which outputs and scratch of a call on ``stream`` are
+    allocated: memory of the stream's own pool, which nothing pending on another
+    stream still uses and which nobody else gets while the call runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream, device)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _done(code: int) -> None:
     if code:
         _check(code)
@@ -787,10 +801,11 @@ class Verifier:
         """Rows of the cache's slots (-1: zeros) as (key, value) of ``dtype`` (bfloat16)."""
         import torch
         shape = (slot_mapping.numel(), cache.num_kv_heads, cache.head_dim)
-        if key_out is None:
-            key_out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.device)
-        if value_out is None:
-            value_out = torch.empty(shape, dtype=key_out.dtype, device=cache.device)
+        with _allocated_on(stream, cache.device):
+            if key_out is None:
+                key_out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.device)
+            if value_out is None:
+                value_out = torch.empty(shape, dtype=key_out.dtype, device=cache.device)
         spec_verify_kv_read(self.handle, stream=stream, cache=cache, key=key_out, value=value_out,
                             slot_mapping=slot_mapping, status=status)
         return key_out, value_out
@@ -806,18 +821,16 @@ class Verifier:
                cu_num_draft_tokens=None, shared_prefix_len: int = 0, out=None, lse=None, workspace=None, status=None,
                stream=None):
         """Attention of the verify tokens over the cache; returns ``out``.
-        Without ``workspace`` one is allocated for the call, on the stream that
-        is current: give one when ``stream`` is another."""
+        Without ``workspace`` one is allocated for the call."""
         import torch
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        if workspace is None:
-            workspace = self.attend_workspace(
-                num_reqs=block_tables.shape[0], max_spec_len=max_spec_len, num_q_heads=q.shape[1],
-                num_kv_heads=cache.num_kv_heads, head_dim=cache.head_dim, max_seq_len=max_seq_len,
-                shared_prefix_len=shared_prefix_len, num_tokens=q.shape[0])
-            if stream is not None and hasattr(stream, "cuda_stream"):
-                workspace.record_stream(stream)
+        with _allocated_on(stream, cache.device):
+            if out is None:
+                out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            if workspace is None:
+                workspace = self.attend_workspace(
+                    num_reqs=block_tables.shape[0], max_spec_len=max_spec_len, num_q_heads=q.shape[1],
+                    num_kv_heads=cache.num_kv_heads, head_dim=cache.head_dim, max_seq_len=max_seq_len,
+                    shared_prefix_len=shared_prefix_len, num_tokens=q.shape[0])
         spec_verify_attend(self.handle, stream=stream, q=q, cache=cache, block_tables=block_tables, seq_lens=seq_lens,
                            max_seq_len=max_seq_len, max_spec_len=max_spec_len, scale=scale, out=out,
                            cu_num_draft_tokens=cu_num_draft_tokens, shared_prefix_len=shared_prefix_len, lse=lse,
@@ -831,16 +844,17 @@ class Verifier:
         alternatives of the committed tokens (``out_tokens`` of ``verify``)."""
         import torch
         dev, shape = logits.device, tuple(out_tokens.shape)
-        if logprobs is None:
-            logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
-        if ranks is None:
-            ranks = torch.empty(shape, dtype=torch.int32, device=dev)
-        if entropy is None:
-            entropy = torch.empty(shape, dtype=torch.float32, device=dev)
-        if top_ids is None:
-            top_ids = torch.empty(shape + (num_top,), dtype=torch.int32, device=dev)
-        if top_logprobs is None:
-            top_logprobs = torch.empty(shape + (num_top,), dtype=torch.float32, device=dev)
+        with _allocated_on(stream, dev):
+            if logprobs is None:
+                logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
+            if ranks is None:
+                ranks = torch.empty(shape, dtype=torch.int32, device=dev)
+            if entropy is None:
+                entropy = torch.empty(shape, dtype=torch.float32, device=dev)
+            if top_ids is None:
+                top_ids = torch.empty(shape + (num_top,), dtype=torch.int32, device=dev)
+            if top_logprobs is None:
+                top_logprobs = torch.empty(shape + (num_top,), dtype=torch.float32, device=dev)
         spec_verify_logprobs(self.handle, stream=stream, logits=logits, out_tokens=out_tokens, logprobs=logprobs,
                              ranks=ranks, entropy=entropy, top_ids=top_ids, top_logprobs=top_logprobs,
                              cu_num_draft_tokens=cu_num_draft_tokens, temperature=temperature, num_top=num_top,
