@@ -362,7 +362,8 @@ typedef struct spec_verify_kv_cache {
  * h * head_stride.  slot_mapping[t] = SV_PADDING_SLOT_ID (-1), as the verifier
  * leaves it for rejected drafts: a write skips the token, a read gives zeros.
  * Any other slot outside the cache does the same and raises SV_DATA_BAD_SLOT.
- * Two tokens of one call must not share a slot. */
+ * Two tokens of one call must not share a slot.  Rows that share a scale (a
+ * scale stride of 0 along more than one element) can be read, not written. */
 typedef struct spec_verify_kv_args {
   int64_t num_tokens; /* T >= 0 (0 is a no-op) */
   int32_t dtype;      /* SV_F32 or SV_BF16: the elements of key and value */

@@ -112,6 +112,10 @@ sv_status run_kv(spec_verify_t h, const spec_verify_kv_args *a, void *stream, bo
   const sv_status st = spec_verify_check_kv_args(&h->cfg, a);
   if (st != SV_OK) return st;
   if (a->num_tokens == 0) return SV_OK;
+  const spec_verify_kv_cache &c = a->cache;
+  if (write && ((c.num_blocks > 1 && c.scale_block_stride == 0) || (c.num_kv_heads > 1 && c.scale_head_stride == 0) ||
+                (c.block_size > 1 && c.scale_token_stride == 0)))
+    return fail(SV_ERR_INVALID_ARG, "rows that share a scale (a scale stride of 0) can be read, not written");
   sv::KvParams p{};
   p.T = a->num_tokens;
   p.c = a->cache;

@@ -191,3 +191,21 @@ def test_the_verifiers_rollback_keeps_rejected_drafts_out(ver):
     written = (numbers(cache.k) != 0).any(-1).reshape(-1)[:N * (G + 1)].reshape(N, G + 1)
     keep = torch.arange(G + 1) <= res.num_accepted.cpu()[:, None]
     assert torch.equal(written, keep) and not bool(keep.all())
+
+
+def test_rows_that_share_a_scale_are_read_not_written(ver):
+    """One scale for all tokens of a page and head, expanded: a write would have its tokens race for it."""
+    full = make_cache(3, 2, 16, 64, "int8")
+    full.k.copy_(torch.randint(-127, 128, full.k.shape, dtype=torch.int8))
+    one = torch.tensor([0.5, 0.25, 2.0, 1.0, 3.0, 0.125], device="cuda").view(3, 2, 1)
+    slots, x = torch.arange(48, device="cuda"), torch.ones(48, 2, 64, device="cuda")
+    for scale in (one.expand(3, 2, 16), one[:, :1].expand(3, 2, 16), torch.ones(1, 1, 1, device="cuda").expand(3, 2, 16)):
+        cache = sv.KVCache(k=full.k, v=full.v, k_scale=scale, v_scale=scale)
+        key, _ = ver.kv_read(cache=cache, slot_mapping=slots, dtype=torch.float32)
+        want = (full.k.float() * scale[..., None]).permute(0, 2, 1, 3).reshape(48, 2, 64)
+        assert torch.equal(key, want)
+        with pytest.raises(sv.SpecVerifyError) as ei:
+            ver.kv_write(cache=cache, key=x, value=x, slot_mapping=slots)
+        assert ei.value.code == sv.SV_ERR_INVALID_ARG
+        none = torch.empty(0, 2, 64, device="cuda")
+        ver.kv_write(cache=cache, key=none, value=none, slot_mapping=slots[:0])
