@@ -408,6 +408,8 @@ sv_status spec_verify_check_kv_args(const spec_verify_config *config, const spec
  * one that is NaN or infinite makes out NaN, not lse, in the rows that see its
  * key (for the heads that read it).  A key whose value scale is less than
  * 2^-100 of the largest that a row sees may drop out of the row's lse.
+ * A key scale times `scale` may be 2^96 in size; with a larger one a row of q
+ * below 2^-1 may become NaN though its scores are numbers.
  * SV_DATA_COPY_TIMEOUT: a wait inside a kernel ran out and out and lse are NaN
  * in the rows it was for; never expected on a healthy GPU.
  *

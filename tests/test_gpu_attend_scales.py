@@ -183,3 +183,16 @@ def test_zero_rows_before_large_ones(form):
             c["cache"].v_scale[page, :, off] = LEAST
             c["cache"].v[page, :, off] = 0
     check(c)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_tiny_queries_and_huge_keys(form):
+    """Key scales up to the stated 2^96 (with the call's own), queries as small as makes the scores ordinary ones."""
+    c = FORMS[form](8)
+    c["q"] = (c["q"].float() * 2.0 ** -97).to(torch.bfloat16)
+    k = c["cache"].k_scale
+    k.mul_(2.0 ** 97)
+    most = 2.0 ** 95 / c["scale"]
+    k.clamp_(max=most)
+    k[some(c, 0.01)] = most
+    check(c)
