@@ -413,9 +413,12 @@ sv_status spec_verify_check_kv_args(const spec_verify_config *config, const spec
  * SV_DATA_COPY_TIMEOUT: a wait inside a kernel ran out and out and lse are NaN
  * in the rows it was for; never expected on a healthy GPU.
  *
- * The products take 16-bit operands: the cache's numbers and q (scaled by a
- * power of two) are exact in them, the softmax's weights are rounded to 11
- * bits.  Scores, sums and outputs are fp32 until out is rounded to bf16. */
+ * The products take 16-bit operands (f16).  The cache's numbers are exact in
+ * them.  So is q, times a power of two of its row's own, but for elements below
+ * 2^-13 of the row's largest, which may lose 2^-25 of it.  The softmax's weights
+ * are rounded to 11 bits, in steps of 2^-24 of the largest product of a weight
+ * and its value's scale.  Exponentials are the GPU's fast ones (relative error
+ * 2^-22).  Scores, sums and outputs are fp32 until out is rounded to bf16. */
 typedef struct spec_verify_attend_args {
   int32_t num_reqs;     /* N >= 0 (0 is a no-op) */
   int32_t max_spec_len; /* G: every gamma_i <= G */
