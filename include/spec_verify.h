@@ -415,7 +415,7 @@ sv_status spec_verify_check_kv_args(const spec_verify_config *config, const spec
  *
  * The products take 16-bit operands (f16).  The cache's numbers are exact in
  * them.  So is q, times a power of two of its row's own, but for elements below
- * 2^-13 of the row's largest, which may lose 2^-25 of it.  The softmax's weights
+ * 2^-13 of the row's largest, which may be off by 2^-24 of it.  The softmax's weights
  * are rounded to 11 bits, in steps of 2^-24 of the largest product of a weight
  * and its value's scale.  Exponentials are the GPU's fast ones (relative error
  * 2^-22).  Scores, sums and outputs are fp32 until out is rounded to bf16. */
