@@ -724,20 +724,36 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
 }
 
 // A short prefix is read by every request for itself (from L2), which saves the
-// CTAs that would share it, the partial results and the join.  In keys of the
-// private CTAs that is worth about 2^19 for a call of the tensor-memory kernel
-// (2^16 without it), and 10 for each row; one step of keys always.  Measured,
-// us a call, shared | by each request: 64 requests x 5 tokens (32 heads over
-// 8), prefix 128 57 | 31, 512 67 | 41, 1024 72 | 55, 2032 85 | 84; 512 x 8, 256
-// 266 | 194, 512 283 | 254, 1024 312 | 371; 512 x 1, 128 91 | 70, 512 99 | 118;
-// 8 x 4, 1024 37 | 18; 20 x 1 (80 rows), 256 14.5 | 14.1, 1024 19.5 | 21.5.
+// kernels that would share it, the partial results and the join.  A call's time
+// for it, fitted to both sides of 56 calls' sizes at prefixes of 128 to 16384
+// keys (head_dim 64 and 128, int8, private ranges of 128 and 1024 keys): read
+// by each, a key costs a private CTA 24 ps and 7 for each of its row groups;
+// shared on the tensor cores, a key costs a kv head 75 ps and 64 for each row
+// tile, and the kernels 31 us and 950 ps a row to begin and end.  So a prefix is
+// shared from the length where the two are equal, and always beyond 16384, the
+// longest that was measured.  (On the whole table this loses 4 % at most to the
+// better side.)  Fewer rows share it in CTAs like the private ones, whose keys cost
+// two and a half times as much by the fit, and 0.2 us (5 us at most are lost).
+// Measured, us a call, shared | by each request (32 heads over 8 of 128, 128
+// private keys): 8 requests x 4 tokens, prefix 2048 57 | 25, 8192 65 | 42; 64 x 5,
+// 1024 77 | 50, 2048 84 | 78, 4096 94 | 136; 512 x 8, 512 305 | 257, 1024 335 | 365;
+// 512 x 1, 256 118 | 95, 512 120 | 126; 2 x 5 (40 rows), 4096 33 | 29, 16384 48 | 38;
+// 16 x 1 (64 rows), 256 17 | 17, 1024 19 | 22.
 AttendParams short_prefix(AttendParams p) {
-  const int64_t ctas = static_cast<int64_t>(p.N) * p.c.num_kv_heads *
-                       ceil_div((p.G + 1) * static_cast<int64_t>(p.group), 8 * kGroups);
+  const int64_t H = p.c.num_kv_heads, own = (p.G + 1) * static_cast<int64_t>(p.group), own_tiles = ceil_div(own, 8 * kGroups);
   // (the rows there may be, so that calls with fewer tokens choose alike)
-  const int64_t rows = static_cast<int64_t>(p.N) * (p.G + 1) * p.group, fixed = rows >= kTensorRows ? 1 << 19 : 1 << 16;
-  const int64_t keys = (fixed + 10 * rows * p.c.num_kv_heads) / std::max<int64_t>(1, ctas);
-  if (p.prefix < std::clamp<int64_t>(keys, 128, 2048)) {
+  const int64_t rows = p.N * own;
+  int64_t saved = p.N * H * own_tiles * (24 + 7 * ceil_div(ceil_div(own, 8), own_tiles)), begin, most;  // ps a key; ps; keys
+  if (rows >= kTensorRows) {
+    saved -= H * (75 + 64 * static_cast<int64_t>(ceil_div(rows, kPrefixRowTile)));
+    begin = 31000000 + 950 * rows * H;
+    most = 16384 + 1;
+  } else {
+    saved -= H * 5 * (24 * ceil_div(rows, 8 * kGroups) + 7 * ceil_div(rows, 8)) / 2;
+    begin = 200000;
+    most = INT64_MAX;
+  }
+  if (p.prefix < (saved > 0 ? std::min(most, 128 + begin / saved) : most)) {
     p.row0 = p.prefix;
     p.prefix = 0;
   }

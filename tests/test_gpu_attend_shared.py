@@ -7,7 +7,7 @@ import torch
 
 import speculative_decoding_token_rejection_gb300 as sv
 from test_gpu_attend import check, make, run
-from test_gpu_attend_scales import shared
+from test_gpu_attend_scales import shared, shared_prefix
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,13 @@ def test_bytes_behind_every_length_may_be_anything(many):
             scale[page, :, off] = float("nan")
             data.view(torch.uint8)[page, :, off] = 0x7F if t % 2 else 0xFF
     check(c)
+
+
+@pytest.mark.parametrize("kw, least, most", [
+    (dict(gammas=[3] * 8, kv_heads=8), 16384, 16400), (dict(gammas=[4] * 64, kv_heads=8), 1024, 4096),
+    (dict(gammas=[7] * 512, kv_heads=8), 512, 1024), (dict(gammas=[0] * 512, kv_heads=8), 256, 640),
+    (dict(gammas=[3] * 64, kv_heads=1, group=8), 8192, 16400), (dict(gammas=[3] * 64, kv_heads=8, dim=64), 1024, 4096)])
+def test_a_prefix_is_shared_from_where_that_pays(kw, least, most):
+    """Between two lengths at which the two ways were measured: at the first reading by each request won, at the other
+    sharing did (or it is the first above all that were measured)."""
+    assert least < shared_prefix(**kw) <= most
