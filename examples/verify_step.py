@@ -127,5 +127,8 @@ def run(requests=8, gamma=4, prompt=64, steps=4, vocab=2000, q_heads=8, kv_heads
     return texts, logprobs, computed.tolist()
 
 
+# Sizes at which attention computes the prompt once for the batch (in smaller calls every request reads it for itself).
+SHARED = dict(requests=512, prompt=768, q_heads=8, kv_heads=8)
+
 if __name__ == "__main__":
     run()

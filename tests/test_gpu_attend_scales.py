@@ -40,9 +40,9 @@ def shared_prefix(gammas, *, kv_heads=2, group=4, dim=128, block=16, uniform=Tru
 
 
 def shared(gammas, own, **kw):
-    """A call with a prefix that is shared; `own`: tokens behind it (before its end if negative)."""
+    """A call with a prefix that is shared; `own`: tokens behind it (before its end if negative; None: no tokens at all)."""
     prefix = shared_prefix(gammas, **kw)
-    return make(gammas, [prefix + n for n in own], prefix=prefix, **kw)
+    return make(gammas, [0 if n is None else prefix + n for n in own], prefix=prefix, **kw)
 
 
 FORMS = {
