@@ -211,7 +211,7 @@ sv_status spec_verify_create(const spec_verify_config *config, spec_verify_t *ou
     if ((e = sv::enable_stream_kernels_bf16()) != cudaSuccess || (e = sv::enable_stream_kernels_f32()) != cudaSuccess ||
         (e = sv::enable_stream_kernels_bf16_proc(optin)) != cudaSuccess ||
         (e = sv::enable_stream_kernels_f32_proc(optin)) != cudaSuccess ||
-        (e = sv::enable_attend_kernels()) != cudaSuccess || (e = sv::enable_logprobs_kernels()) != cudaSuccess)
+        (e = sv::enable_attend_kernels()) != cudaSuccess)
       result = fail(SV_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(e));
     if (sv::enable_probs_kernels(16) != cudaSuccess || sv::enable_logits_kernels(16, max_dyn) != cudaSuccess ||
         sv::enable_sample_kernels(16, max_dyn) != cudaSuccess) {

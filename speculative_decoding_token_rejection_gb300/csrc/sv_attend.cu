@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttendParams P, co
   for (int r = blockIdx.y * kWarps + warp; r < rows; r += gridDim.y * kWarps) {
     const int64_t row = first * P.Hq + r;
     const int j = r / P.Hq, hq = r - j * P.Hq, h = hq / P.group;
-    const int shared = P.prefix ? prefix_slots(L, h, (static_cast<int>(first) + j) * P.group + hq - h * P.group, kPrefixRowTile) : 0;
+    const int shared = P.prefix ? prefix_slots(L, h, (static_cast<int>(first) + j) * P.group + hq - h * P.group) : 0;
     const int slots = shared + own;
     Part<D> all;
     all.m = -INFINITY;

@@ -53,9 +53,9 @@ constexpr int kPrefixRowTile = 256, kPrefixKeyTile = 128;
 
 // Partial results of the prefix that a row has: of kv head h, row `local` of
 // the (T + N) * group.
-__device__ __forceinline__ int prefix_slots(const AttendPlan &L, int h, int local, int row_tile) {
+__device__ __forceinline__ int prefix_slots(const AttendPlan &L, int h, int local) {
   if (L.tensor_tiles == 0) return L.prefix_splits;
-  const int first = (h * L.tensor_tiles + local / row_tile) * L.period;
+  const int first = (h * L.tensor_tiles + local / kPrefixRowTile) * L.period;
   return (first + L.image_tiles - 1) / L.units_cta - first / L.units_cta + 1;
 }
 

@@ -301,7 +301,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
   Control &C = *reinterpret_cast<Control *>(smem + Y::kControl);
   Vectors *const vec = reinterpret_cast<Vectors *>(smem + Y::kVec);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int H = P.c.num_kv_heads;
   const int T = L.image_tiles, u_end = min(L.units, static_cast<int>(blockIdx.x + 1) * L.units_cta);
   auto segment = [&](int u) {  // the CTA's work from unit u on: key tiles of one item (kv head, 256 rows)
     const int item = u / L.period, t0 = u - item * L.period;

@@ -184,7 +184,7 @@ __device__ __forceinline__ void numbers_of(uint32_t w, float f[4]) {
     f[2] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7542)) - 8388736.0f;
     f[3] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7543)) - 8388736.0f;
   } else {
-    cache_word_to_floats<FMT>(w, f);
+    e4m3_word_to_floats(w, f);
   }
 }
 

@@ -246,7 +246,6 @@ struct LogprobsParams {
   int32_t *status;
   bool pdl;
 };
-cudaError_t enable_logprobs_kernels();
 cudaError_t launch_logprobs(const LogprobsParams &p, bool bf16, int num_sms, cudaStream_t stream);
 
 }  // namespace sv

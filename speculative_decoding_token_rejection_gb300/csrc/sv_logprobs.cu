@@ -544,8 +544,6 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) logprobs_kernel(const 
 
 }  // namespace
 
-cudaError_t enable_logprobs_kernels() { return cudaSuccess; }
-
 cudaError_t launch_logprobs(const LogprobsParams &p, bool bf16, int num_sms, cudaStream_t stream) {
   const int64_t places = static_cast<int64_t>(p.N) * (p.G + 1);
   // Rows are split over a cluster while the call has fewer than two CTAs per

@@ -49,19 +49,13 @@ __device__ __forceinline__ float f16_bits_to_float(uint16_t h) {
   asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(h));
   return f;
 }
-// The four numbers that the four bytes of w stand for (scale aside).
-template <int FMT>
-__device__ __forceinline__ void cache_word_to_floats(uint32_t w, float f[4]) {
-  if (FMT == SV_CACHE_INT8) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) f[c] = static_cast<float>(static_cast<int8_t>(w >> (8 * c)));
-  } else {
-    const uint32_t a = e4m3x2_to_f16x2(static_cast<uint16_t>(w)), b = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
-    f[0] = f16_bits_to_float(static_cast<uint16_t>(a));
-    f[1] = f16_bits_to_float(static_cast<uint16_t>(a >> 16));
-    f[2] = f16_bits_to_float(static_cast<uint16_t>(b));
-    f[3] = f16_bits_to_float(static_cast<uint16_t>(b >> 16));
-  }
+// The four numbers of the four e4m3 bytes of w.
+__device__ __forceinline__ void e4m3_word_to_floats(uint32_t w, float f[4]) {
+  const uint32_t a = e4m3x2_to_f16x2(static_cast<uint16_t>(w)), b = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+  f[0] = f16_bits_to_float(static_cast<uint16_t>(a));
+  f[1] = f16_bits_to_float(static_cast<uint16_t>(a >> 16));
+  f[2] = f16_bits_to_float(static_cast<uint16_t>(b));
+  f[3] = f16_bits_to_float(static_cast<uint16_t>(b >> 16));
 }
 
 }  // namespace sv
