@@ -829,7 +829,8 @@ class Verifier:
             if workspace is None:
                 workspace = self.attend_workspace(
                     num_reqs=block_tables.shape[0], max_spec_len=max_spec_len, num_q_heads=q.shape[1],
-                    num_kv_heads=cache.num_kv_heads, head_dim=cache.head_dim, max_seq_len=max_seq_len,
+                    num_kv_heads=cache.num_kv_heads, head_dim=cache.head_dim,
+                    max_seq_len=min(max_seq_len, block_tables.shape[-1] * cache.block_size),  # (the call's own bound)
                     shared_prefix_len=shared_prefix_len, num_tokens=q.shape[0])
         spec_verify_attend(self.handle, stream=stream, q=q, cache=cache, block_tables=block_tables, seq_lens=seq_lens,
                            max_seq_len=max_seq_len, max_spec_len=max_spec_len, scale=scale, out=out,

@@ -1,4 +1,4 @@
-"""Outputs and scratch that a call on another stream allocates for itself come
+"""Outputs and scratch that a call allocates for itself.  On another stream they come
 from that stream's memory pool: what is handed out there is neither still in
 use on another stream nor given away while the call runs."""
 import pytest
@@ -72,3 +72,22 @@ def test_logprobs(call_stream):
         assert torch.equal(getattr(got, name), getattr(want, name))
         assert pool_of(getattr(got, name)) == stream.cuda_stream
     ver.close()
+
+
+def test_the_workspace_goes_by_what_the_tables_hold(monkeypatch):
+    """max_seq_len is an upper bound: the workspace of a call's own is that of the lengths its block tables allow."""
+    c = make([3, 1, 0], [3000, 90, 17], seed=15)
+    made = []
+    original = sv.Verifier.attend_workspace
+
+    def small(self, **kw):
+        assert kw["max_seq_len"] <= 3008
+        made.append(original(self, **kw))
+        return made[-1]
+
+    monkeypatch.setattr(sv.Verifier, "attend_workspace", small)
+    outs = [verifier().attend(q=c["q"], cache=c["cache"], block_tables=c["table"], seq_lens=c["seq_lens"], max_seq_len=most,
+                              max_spec_len=3, scale=c["scale"], cu_num_draft_tokens=c["cu"]) for most in (3000, 3008, 1 << 30)]
+    assert made[1].numel() == made[2].numel()
+    assert torch.equal(outs[1], outs[2])
+    assert torch.equal(outs[0], run(c)[0])
