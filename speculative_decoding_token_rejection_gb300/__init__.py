@@ -801,11 +801,12 @@ class Verifier:
         """Rows of the cache's slots (-1: zeros) as (key, value) of ``dtype`` (bfloat16)."""
         import torch
         shape = (slot_mapping.numel(), cache.num_kv_heads, cache.head_dim)
-        with _allocated_on(stream, cache.device):
-            if key_out is None:
-                key_out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.device)
-            if value_out is None:
-                value_out = torch.empty(shape, dtype=key_out.dtype, device=cache.device)
+        if key_out is None or value_out is None:
+            with _allocated_on(stream, cache.device):
+                if key_out is None:
+                    key_out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.device)
+                if value_out is None:
+                    value_out = torch.empty(shape, dtype=key_out.dtype, device=cache.device)
         spec_verify_kv_read(self.handle, stream=stream, cache=cache, key=key_out, value=value_out,
                             slot_mapping=slot_mapping, status=status)
         return key_out, value_out
@@ -823,15 +824,16 @@ class Verifier:
         """Attention of the verify tokens over the cache; returns ``out``.
         Without ``workspace`` one is allocated for the call."""
         import torch
-        with _allocated_on(stream, cache.device):
-            if out is None:
-                out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-            if workspace is None:
-                workspace = self.attend_workspace(
-                    num_reqs=block_tables.shape[0], max_spec_len=max_spec_len, num_q_heads=q.shape[1],
-                    num_kv_heads=cache.num_kv_heads, head_dim=cache.head_dim,
-                    max_seq_len=min(max_seq_len, block_tables.shape[-1] * cache.block_size),  # (the call's own bound)
-                    shared_prefix_len=shared_prefix_len, num_tokens=q.shape[0])
+        if out is None or workspace is None:
+            with _allocated_on(stream, cache.device):
+                if out is None:
+                    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+                if workspace is None:
+                    workspace = self.attend_workspace(
+                        num_reqs=block_tables.shape[0], max_spec_len=max_spec_len, num_q_heads=q.shape[1],
+                        num_kv_heads=cache.num_kv_heads, head_dim=cache.head_dim,
+                        max_seq_len=min(max_seq_len, block_tables.shape[-1] * cache.block_size),  # (the call's own bound)
+                        shared_prefix_len=shared_prefix_len, num_tokens=q.shape[0])
         spec_verify_attend(self.handle, stream=stream, q=q, cache=cache, block_tables=block_tables, seq_lens=seq_lens,
                            max_seq_len=max_seq_len, max_spec_len=max_spec_len, scale=scale, out=out,
                            cu_num_draft_tokens=cu_num_draft_tokens, shared_prefix_len=shared_prefix_len, lse=lse,
@@ -845,17 +847,18 @@ class Verifier:
         alternatives of the committed tokens (``out_tokens`` of ``verify``)."""
         import torch
         dev, shape = logits.device, tuple(out_tokens.shape)
-        with _allocated_on(stream, dev):
-            if logprobs is None:
-                logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
-            if ranks is None:
-                ranks = torch.empty(shape, dtype=torch.int32, device=dev)
-            if entropy is None:
-                entropy = torch.empty(shape, dtype=torch.float32, device=dev)
-            if top_ids is None:
-                top_ids = torch.empty(shape + (num_top,), dtype=torch.int32, device=dev)
-            if top_logprobs is None:
-                top_logprobs = torch.empty(shape + (num_top,), dtype=torch.float32, device=dev)
+        if logprobs is None or ranks is None or entropy is None or top_ids is None or top_logprobs is None:
+            with _allocated_on(stream, dev):
+                if logprobs is None:
+                    logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
+                if ranks is None:
+                    ranks = torch.empty(shape, dtype=torch.int32, device=dev)
+                if entropy is None:
+                    entropy = torch.empty(shape, dtype=torch.float32, device=dev)
+                if top_ids is None:
+                    top_ids = torch.empty(shape + (num_top,), dtype=torch.int32, device=dev)
+                if top_logprobs is None:
+                    top_logprobs = torch.empty(shape + (num_top,), dtype=torch.float32, device=dev)
         spec_verify_logprobs(self.handle, stream=stream, logits=logits, out_tokens=out_tokens, logprobs=logprobs,
                              ranks=ranks, entropy=entropy, top_ids=top_ids, top_logprobs=top_logprobs,
                              cu_num_draft_tokens=cu_num_draft_tokens, temperature=temperature, num_top=num_top,
