@@ -535,8 +535,9 @@ class KVCache:
     block_size, head_dim]`` with the same strides and unit stride along
     head_dim; ``k_scale`` and ``v_scale``: float32 ``[num_blocks,
     num_kv_heads, block_size]`` with the same strides.  A token-major cache is
-    passed as its ``permute(0, 2, 1, 3)`` / ``permute(0, 2, 1)`` view.  The
-    tensors are checked once, here; the object keeps them alive."""
+    passed as its ``permute(0, 2, 1, 3)`` / ``permute(0, 2, 1)`` view.  Scales
+    may be any floats; expanded ones are read but not written.  The tensors are
+    checked once, here; the object keeps them alive."""
 
     def __init__(self, *, k, v, k_scale, v_scale):
         import torch

@@ -42,9 +42,9 @@
 // kv_write gives (2^-64 to 2^121): w and l stay within fp32 for any of them.
 // (One near the first tile's scales sent later ones out of range.)
 //
-// Measured: 512 requests x 8 tokens over 16384 keys, 829 us of the call's 1.07
-// ms: 1.33 PFLOP/s, 70 % of a plain matrix product's rate.  A key tile takes a
-// CTA 3400 cycles, of which a softmax warp works for 1800 and waits for its row
+// Measured: 512 requests x 8 tokens over 16384 keys, 805 us of the call's 1.03
+// ms: 1.37 PFLOP/s, 72 % of a plain matrix product's rate.  A key tile takes a
+// CTA about 3300 cycles, of which a softmax warp works for 1800 and waits for its row
 // tile's products for 1250; a segment adds 25000 (queries in, results out).
 #include <algorithm>
 #include <cmath>
