@@ -383,8 +383,10 @@ sv_status spec_verify_kv_read(spec_verify_t handle, const spec_verify_kv_args *a
 /* Host-only validation of the arguments of either call against `config`. */
 sv_status spec_verify_check_kv_args(const spec_verify_config *config, const spec_verify_kv_args *args);
 
-/* Attention of the verify tokens over the cache.  The tokens are laid out as
- * the target rows of spec_verify_args: request i owns rows s_i + i ..
+/* Attention of the verify tokens over the cache, whose sides may each span 256
+ * GB from the first page to the last (but no more than 2^32 times the largest
+ * power of two that divides the block and token strides).  The tokens are laid
+ * out as the target rows of spec_verify_args: request i owns rows s_i + i ..
  * s_i + i + gamma_i of q, out and lse.  seq_lens[i] = L counts the request's
  * keys, its own gamma_i + 1 verify tokens (already written) included; row j is
  * at position L - (gamma_i + 1) + j and sees the keys 0 .. position.  Query

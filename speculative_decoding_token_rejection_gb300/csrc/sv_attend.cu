@@ -193,14 +193,14 @@ __device__ __forceinline__ bool attend_tile(const AttendParams &P, const AttendP
     return it < ntiles && k < T.k_end ? (k < P.row0 ? P.tables : T.table)[div_by(k, L.page)] : -1;
   };
   // Copies of a tile: the lane's key first, then the rows, a lane's neighbours taking a whole one, in kCols steps.
-  uint32_t unit = 0, dead = 0;  // the row's place in units of 16 bytes (rows are 16-byte aligned, a side below 2^36 bytes)
+  uint32_t unit = 0, dead = 0;  // the row's place in units of L.unit_bytes
   auto copy_keys = [&](int it, int stage, int page) {
     const int k = T.k_begin + (it * kAttendWarps + warp) * kKeys + lane;
     const bool in = k < T.k_end, live = in && page >= 0 && page < P.c.num_blocks;
     if (in && !live) bits = SV_DATA_BAD_SLOT;
     const int off = k - div_by(k, L.page) * P.c.block_size;
     const uint32_t dst = ring + stage * Y::kStage + Y::kScales + lane * 8;
-    unit = live ? static_cast<uint32_t>((page * P.c.block_stride + off * P.c.token_stride) >> 4) : 0u;
+    unit = live ? page * L.block_units + off * L.token_units : 0u;
     const int64_t sat = live ? page * P.c.scale_block_stride + off * P.c.scale_token_stride : 0;
     dead = __ballot_sync(0xFFFFFFFFu, !live);
     copy_async<4>(dst, kscale + sat, live ? 4 : 0);
@@ -211,8 +211,9 @@ __device__ __forceinline__ bool attend_tile(const AttendParams &P, const AttendP
     const int row = step * (32 / kCols) + lane / kCols;
     const uint32_t u = __shfl_sync(0xFFFFFFFFu, unit, row);
     const uint32_t n = dead >> row & 1u ? 0u : 16u;
-    copy_async<16>(dst + tile_at<D, false>(row, ccol), kcol + static_cast<uint64_t>(u) * 16, n);
-    copy_async<16>(dst + kKeys * D + tile_at<D, true>(row, ccol), vcol + static_cast<uint64_t>(u) * 16, n);
+    const uint64_t at = static_cast<uint64_t>(u) * L.unit_bytes;
+    copy_async<16>(dst + tile_at<D, false>(row, ccol), kcol + at, n);
+    copy_async<16>(dst + kKeys * D + tile_at<D, true>(row, ccol), vcol + at, n);
   };
 
   // (the first copies are on their way before the queries are looked at)
@@ -794,6 +795,9 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   // (Where the private part is one chunk its CTAs could join the prefix's partial results as they end.  Measured, with
   // four rows' results in flight: 203 us for 512 requests x 32 rows, against 147 and a join by itself.)
   L.slots = L.prefix_splits + L.own_splits;
+  L.unit_bytes = cache_unit(p.c);
+  L.block_units = static_cast<uint32_t>(p.c.block_stride / L.unit_bytes);
+  L.token_units = static_cast<uint32_t>(p.c.token_stride / L.unit_bytes);
   L.qvec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0;
   L.ovec = (reinterpret_cast<uintptr_t>(p.out) & 7u) == 0 && p.out_token % 4 == 0 && p.out_head % 4 == 0;
   const int64_t rows = static_cast<int64_t>(L.rows) * p.c.num_kv_heads;

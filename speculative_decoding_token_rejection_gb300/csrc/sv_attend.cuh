@@ -37,6 +37,7 @@ struct AttendPlan {
   int32_t units, units_cta, period;
   int32_t own_splits, own_chunk, own_tiles;
   int32_t slots;          // partial results of a row
+  uint32_t unit_bytes, block_units, token_units;  // a cache row's place in units that divide both strides
   bool ovec;              // output rows allow 8-byte stores
   bool qvec;              // q rows allow 16-byte loads
   int32_t image_tiles;    // tiles of kPrefixKeyTile keys of the prefix

@@ -224,6 +224,12 @@ struct AttendParams {
   int32_t *status;
   bool pdl;
 };
+// The largest power of two that divides the strides between a cache's pages and
+// tokens: attention counts a row's place in 32 bits of them.
+inline uint32_t cache_unit(const spec_verify_kv_cache &c) {
+  const uint64_t any = static_cast<uint64_t>(c.block_stride | c.token_stride) | uint64_t{1} << 30;
+  return static_cast<uint32_t>(any & (~any + 1));
+}
 // `fewer`: what calls with fewer draft tokens need as well.
 int64_t attend_workspace_bytes(const AttendParams &p, int num_sms, bool fewer);
 cudaError_t enable_attend_kernels();

@@ -184,10 +184,11 @@ sv_status spec_verify_check_attend_args(const spec_verify_config *c, const spec_
   if (a->num_reqs == 0) return SV_OK;
   if ((st = check_cache(a->cache)) != SV_OK) return st;
   const spec_verify_kv_cache &c8 = a->cache;
-  if (c8.block_stride > (int64_t{1} << 36) || c8.head_stride > (int64_t{1} << 36) || c8.token_stride > (int64_t{1} << 36) ||
-      static_cast<double>(c8.num_blocks - 1) * c8.block_stride + static_cast<double>(c8.num_kv_heads - 1) * c8.head_stride +
-              static_cast<double>(c8.block_size - 1) * c8.token_stride >= 68719476000.0)
-    return fail(SV_ERR_UNSUPPORTED, "a side of the cache spans more than 64 GB");
+  const double span = static_cast<double>(c8.num_blocks - 1) * c8.block_stride +
+                      static_cast<double>(c8.block_size - 1) * c8.token_stride;
+  if (span + static_cast<double>(c8.num_kv_heads - 1) * c8.head_stride >= 0x1p38 || span >= 0x1p32 * sv::cache_unit(c8))
+    return fail(SV_ERR_UNSUPPORTED, "a side of the cache spans more than 256 GB, or 2^32 units of %u bytes",
+                sv::cache_unit(c8));
   if (a->shared_prefix_len % a->cache.block_size)
     return fail(SV_ERR_INVALID_ARG, "shared_prefix_len must be a multiple of block_size");
   if (a->block_table_stride < 0 ||

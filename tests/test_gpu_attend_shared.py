@@ -217,3 +217,20 @@ def test_a_workspace_holds_for_fewer_draft_tokens(kv_heads, group):
         c = make([G] + [few] * (N - 1), lens, prefix=prefix, kv_heads=kv_heads, group=group, dim=64, seed=few)
         want, got = run(c), run(c, workspace=ws)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("name", ["private", "shared"])
+def test_pages_far_apart(name):
+    """One layer's pages of a cache that holds many layers' side by side: 72 GB from the first to the last."""
+    c = make([1, 0, 2], [200, 40, 135], block=64, seed=14) if name == "private" else \
+        shared([1] * 200, [5 + i % 9 for i in range(200)], kv_heads=8, group=2, block=128, seed=14)
+    old = c["cache"]
+    n, h, b, d = old.k.shape
+    stride = (72 << 30) // n // 128 * 128
+    room = torch.empty((n - 1) * stride + 2 * h * b * d, dtype=torch.int8, device="cuda")
+    k, v = (room[at:].as_strided((n, h, b, d), (stride, b * d, d, 1)) for at in (0, h * b * d))
+    k.copy_(old.k)
+    v.copy_(old.v)
+    want = run(c)
+    got = run(dict(c, cache=sv.KVCache(k=k, v=v, k_scale=old.k_scale, v_scale=old.v_scale)))
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -223,3 +223,16 @@ def test_expanded_block_tables_are_refused():
     one = sv.build_attend_args(**{**good, "q": q[:2], "out": good["out"][:2], "seq_lens": good["seq_lens"][:1]},
                                block_tables=table.expand(1, -1))
     assert one.block_table_stride == 3
+
+
+@pytest.mark.parametrize("strides,code", [
+    (dict(block_stride=1 << 34), OK),  # nine pages of 16 GB
+    (dict(block_stride=1 << 34, token_stride=144), UNSUPPORTED),  # only 16 divides both: 64 GB at most
+    (dict(block_stride=1 << 32, token_stride=144), OK), (dict(block_stride=(1 << 34) + 64), OK),
+    (dict(block_stride=(1 << 34) + 16), UNSUPPORTED), (dict(block_stride=1 << 60), UNSUPPORTED),
+    (dict(head_stride=1 << 37), OK), (dict(head_stride=1 << 38), UNSUPPORTED)])
+def test_spans_of_a_cache(strides, code):
+    a = attend_args()
+    for name, value in strides.items():
+        setattr(a.cache, name, value)
+    assert sv.spec_verify_check_attend_args(cfg(), a) == code
