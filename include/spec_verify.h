@@ -81,7 +81,8 @@ enum sv_data_status {
   SV_DATA_COPY_TIMEOUT = 128,     /* a bulk row copy did not complete within its wait limit (request
                                      emits nothing); never expected on a healthy GPU */
   SV_DATA_BAD_LIST = 256,         /* a penalty, banned or stop list range of the request is invalid */
-  SV_DATA_BAD_SLOT = 512          /* a KV slot or a block-table entry outside the cache (the token is left out) */
+  SV_DATA_BAD_SLOT = 512,         /* a KV slot or a block-table entry outside the cache (the token is left out) */
+  SV_DATA_NO_PAGES = 1024         /* the free pages do not suffice for a request (it gets none) */
 };
 
 /* Handle flags.  SV_FLAG_RESIDENT_ROWS: the logits entry copies both the
@@ -459,6 +460,208 @@ sv_status spec_verify_attend_workspace_size(spec_verify_t handle, const spec_ver
 /* Host-only validation of attention arguments against `config` (the workspace's size aside). */
 sv_status spec_verify_check_attend_args(const spec_verify_config *config, const spec_verify_attend_args *args);
 
+/* ---------------------------------------------------------------------------
+ * The same cache in 4 bits, and attention over it.
+ *
+ * Every 16 elements of a row share an e4m3 scale, and the row has a float scale
+ * besides: nibble x of group j stands for x * group_j * scale.  The nibbles are
+ * E2M1 numbers (a sign, 0, 0.5, 1, 1.5, 2, 3, 4 or 6) or signed whole numbers
+ * (-8 .. 7, of which the writer gives -7 .. 7).  Element 2i is the low half of
+ * byte i, element 2i + 1 the high one.  The K (V) row of token offset t of page
+ * b and kv head h is head_dim / 2 bytes at k (v) + b * block_stride +
+ * h * head_stride + t * token_stride, its head_dim / 16 group scales are at
+ * k_group (v_group) + b * group_block_stride + ..., and its scale as in the
+ * 8-bit cache.  A row of head_dim 128 takes 76 bytes, against 132.
+ *
+ * Quantising a row x, all in fp32 with IEEE divisions: scale = max(max_d |x_d| /
+ * (448 Q), 2^-64) with Q = 6 (E2M1) or 7 (whole numbers); group_j =
+ * max_(d in j) |x_d| / (Q * scale) rounded to e4m3; nibble = x_d / (group_j *
+ * scale) rounded to the nearest number of the format (ties to the even code,
+ * at most Q in size), 0 where group_j is 0.  A row that holds a NaN or an
+ * infinity gets scale NaN and zero bytes (it reads back as NaN) and raises
+ * SV_DATA_BAD_VALUES.
+ */
+enum sv_cache4_format { SV_CACHE_E2M1 = 16, SV_CACHE_INT4 = 17 };
+
+typedef struct spec_verify_kv4_cache {
+  void *k, *v;              /* rows on 32-byte boundaries; strides in bytes, multiples of 32 */
+  void *k_group, *v_group;  /* rows on boundaries of head_dim / 16 bytes; strides in bytes, multiples of that */
+  float *k_scale, *v_scale; /* strides in elements */
+  int64_t num_blocks;       /* >= 1; num_blocks * block_size <= 2^31 - 1 pages' tokens */
+  int32_t block_size;       /* >= 1 (any: a power of two is not needed) */
+  int32_t num_kv_heads;     /* >= 1 */
+  int32_t head_dim;         /* 64 or 128 */
+  int32_t format;           /* SV_CACHE_E2M1 or SV_CACHE_INT4 */
+  int64_t block_stride, head_stride, token_stride;
+  int64_t group_block_stride, group_head_stride, group_token_stride;
+  int64_t scale_block_stride, scale_head_stride, scale_token_stride;
+} spec_verify_kv4_cache;
+
+/* As spec_verify_kv_args.  (A scale or group stride of 0 along more than one
+ * element: such rows can be read, not written.) */
+typedef struct spec_verify_kv4_args {
+  int64_t num_tokens; /* T >= 0 (0 is a no-op) */
+  int32_t dtype;      /* SV_F32 or SV_BF16: the elements of key and value */
+  uint32_t reserved;  /* 0 */
+  spec_verify_kv4_cache cache;
+  void *key; /* read by spec_verify_kv4_write, written by spec_verify_kv4_read */
+  int64_t key_token_stride, key_head_stride;
+  void *value;
+  int64_t value_token_stride, value_head_stride;
+  const int64_t *slot_mapping; /* [T] */
+  int32_t *status;             /* [1] or NULL: SV_DATA_* bits OR-ed in */
+} spec_verify_kv4_args;
+
+sv_status spec_verify_kv4_write(spec_verify_t handle, const spec_verify_kv4_args *args, void *stream);
+sv_status spec_verify_kv4_read(spec_verify_t handle, const spec_verify_kv4_args *args, void *stream);
+
+/* Host-only validation of the arguments of either call against `config`. */
+sv_status spec_verify_check_kv4_args(const spec_verify_config *config, const spec_verify_kv4_args *args);
+
+/* Attention of the verify tokens over the 4-bit cache: layout, masks, errors
+ * and outputs are those of spec_verify_attend.  Group scales are numbers, as
+ * spec_verify_kv4_write leaves them (those of keys at or behind seq_len may be
+ * anything); the rows' scales may be any floats, as there.  A nibble times its
+ * group scale is exact in the 16-bit products' operands, so what that call
+ * rounds to fewer bits is what this one does. */
+typedef struct spec_verify_attend4_args {
+  int32_t num_reqs;
+  int32_t max_spec_len;
+  int32_t num_q_heads;
+  int32_t max_seq_len;
+  int32_t shared_prefix_len;
+  uint32_t reserved; /* 0 */
+  int64_t num_draft_tokens_total;
+  const int32_t *cu_num_draft_tokens;
+  spec_verify_kv4_cache cache;
+  const void *q;
+  int64_t q_token_stride, q_head_stride;
+  const int32_t *block_tables;
+  int64_t block_table_stride;
+  const int32_t *seq_lens;
+  float scale;
+  uint32_t test_flags; /* 0, or SV_TEST_EXPIRE_PRODUCT_WAIT (tests only) */
+  void *out;
+  int64_t out_token_stride, out_head_stride;
+  float *lse;
+  void *workspace; /* of spec_verify_attend4_workspace_size bytes */
+  int64_t workspace_bytes;
+  int32_t *status;
+} spec_verify_attend4_args;
+
+sv_status spec_verify_attend4(spec_verify_t handle, const spec_verify_attend4_args *args, void *stream);
+
+/* As spec_verify_attend_workspace_size. */
+sv_status spec_verify_attend4_workspace_size(spec_verify_t handle, const spec_verify_attend4_args *args,
+                                             int64_t *bytes);
+
+/* Host-only validation of attention arguments against `config` (the workspace's size aside). */
+sv_status spec_verify_check_attend4_args(const spec_verify_config *config, const spec_verify_attend4_args *args);
+
+/* ---------------------------------------------------------------------------
+ * Block tables and slot maps from request lengths.
+ *
+ * Request i has n = num_new_tokens[i] tokens for this step behind the
+ * p = num_computed_tokens[i] whose keys are in the cache; its rows follow those
+ * of request i - 1 (for n = gamma_i + 1 this is the verify tokens' layout of the
+ * other calls).  It needs ceil((p + n) / block_size) pages.  Those it holds are
+ * entries 0 .. held_pages[i] - 1 of its block table (they must hold its computed
+ * tokens; pages that a rejection left over stay with it), and missing ones
+ * come from the free pages, a ring: with free_range = (head, tail) they are
+ * free_pages[x % free_capacity] for x = head .. tail - 1.  Requests take pages
+ * from the head in their order; where the pages wanted by the requests up to i
+ * are more than there are, request i takes none and raises SV_DATA_NO_PAGES.
+ * p < 0: the request is done (or the place is idle).  The pages it held go to the
+ * tail, in order, free from the next call on, and its rows are idle.
+ *   seq_lens = p + n, positions = p .. p + n - 1 and slot_mapping their slots.
+ * Idle rows -- of requests that are done or got no pages, and behind the last
+ * request's -- have position and slot -1, and their requests seq_lens 0.
+ * n < 0 (taken as 0), held_pages outside [0, table_width] or too few for p, or a
+ * length that needs more than table_width pages (or passes 2^31 - 1) raise
+ * SV_DATA_BAD_PARAM, and rows that pass num_rows SV_DATA_BAD_CU; such a request
+ * is treated as one that got no pages and does not count among those wanted.
+ * With a free_range that is negative or wider than free_capacity, or a page
+ * outside it, no page is given or taken back (SV_DATA_BAD_PARAM).
+ * held_pages_out may be held_pages, free_range_out free_range and seq_lens
+ * num_computed_tokens.  Nothing depends on the order in which threads run. */
+typedef struct spec_verify_plan_args {
+  int32_t num_reqs;    /* N >= 0 (0: only idle rows); at most the handle's max_num_reqs */
+  int32_t block_size;  /* >= 1 */
+  int32_t table_width; /* pages in a row of block_tables, >= 0 */
+  uint32_t reserved;   /* 0 */
+  int64_t num_rows;    /* R: 0 .. 2^31 - 1 - 65536 */
+  const int32_t *num_new_tokens;      /* [N] */
+  const int32_t *num_computed_tokens; /* [N] */
+  int32_t *block_tables;              /* [N, block_table_stride] in/out */
+  int64_t block_table_stride;         /* >= table_width */
+  const int32_t *held_pages;          /* [N] */
+  int32_t *held_pages_out;            /* [N] */
+  int32_t *free_pages;                /* [free_capacity] in/out */
+  int64_t free_capacity;              /* 1 .. 2^31 - 1: no fewer than there are pages */
+  const int64_t *free_range;          /* [2]: head, tail */
+  int64_t *free_range_out;            /* [2] */
+  int32_t *positions;                 /* [R] out */
+  int64_t *slot_mapping;              /* [R] out */
+  int32_t *seq_lens;                  /* [N] out */
+  int32_t *cu_num_draft_tokens;       /* [N] out or NULL: prefix sums of n - 1 (2^31 - 1 at most), for calls on
+                                         batches without n = 0 */
+  void *workspace; /* 16-byte aligned device scratch of spec_verify_plan_workspace_size bytes; contents need no
+                      initialisation.  Calls that may run at the same time need one each. */
+  int64_t workspace_bytes;
+  int32_t *status; /* [1] or NULL: SV_DATA_* bits OR-ed in */
+} spec_verify_plan_args;
+
+sv_status spec_verify_plan_step(spec_verify_t handle, const spec_verify_plan_args *args, void *stream);
+sv_status spec_verify_plan_workspace_size(spec_verify_t handle, int32_t num_reqs, int64_t *bytes);
+
+/* Host-only validation of the arguments against `config` (the workspace's size aside). */
+sv_status spec_verify_check_plan_args(const spec_verify_config *config, const spec_verify_plan_args *args);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions of queries and keys, with a norm of each head before it.
+ *
+ * With a weight w, a head's row x becomes x / sqrt(mean x^2 + eps) * w first.
+ * Pair i < rotary_dim / 2 of its elements (a, b) then becomes
+ * magnitude * (a cos t - b sin t, b cos t + a sin t), t = position * f_i, and
+ * elements from rotary_dim on stay as they are.  The pair is (i, i + rotary_dim
+ * / 2), or (2i, 2i + 1) with SV_ROTATE_INTERLEAVED.  Frequencies are given as
+ * turns[i] = f_i / (2 pi) * 2^64, rounded: the product with a position, modulo
+ * 2^64, is the angle as a fraction of a turn, exact however far the position is.
+ * Scalings for long contexts are a matter of these numbers and of `magnitude`.
+ * The arithmetic is fp32, rounded once at the end.  Rows of a negative position
+ * (idle ones) are neither read nor written.  Outputs may be the inputs
+ * themselves (same strides); other overlaps are not allowed. */
+#define SV_ROTATE_INTERLEAVED 1u
+#define SV_MAX_ROTATE_HEAD_DIM 512
+typedef struct spec_verify_rotate_args {
+  int64_t num_tokens;  /* T >= 0 (0 is a no-op) */
+  int32_t dtype;       /* SV_F32 or SV_BF16: the elements of every row and of the weights */
+  int32_t head_dim;    /* 1 .. SV_MAX_ROTATE_HEAD_DIM */
+  int32_t rotary_dim;  /* even, 0 .. head_dim */
+  int32_t num_q_heads; /* >= 0; q is not looked at when 0 */
+  int32_t num_k_heads; /* >= 0; key is not looked at when 0 */
+  uint32_t flags;      /* 0 or SV_ROTATE_INTERLEAVED */
+  const void *q;       /* [T, num_q_heads, head_dim], strides in elements, unit stride within a head */
+  int64_t q_token_stride, q_head_stride;
+  void *q_out;
+  int64_t q_out_token_stride, q_out_head_stride;
+  const void *key; /* [T, num_k_heads, head_dim] */
+  int64_t key_token_stride, key_head_stride;
+  void *key_out;
+  int64_t key_out_token_stride, key_out_head_stride;
+  const int32_t *positions;     /* [T] */
+  const uint64_t *turns;        /* [rotary_dim / 2] */
+  const void *q_weight;         /* [head_dim] or NULL: no norm */
+  const void *key_weight;       /* [head_dim] or NULL */
+  float magnitude;              /* finite */
+  float eps;                    /* >= 0, finite */
+} spec_verify_rotate_args;
+
+sv_status spec_verify_rotate(spec_verify_t handle, const spec_verify_rotate_args *args, void *stream);
+
+/* Host-only validation of the arguments against `config`. */
+sv_status spec_verify_check_rotate_args(const spec_verify_config *config, const spec_verify_rotate_args *args);
+
 /* Log-probabilities of the committed tokens, as a server returns them with the
  * text.  Logits rows and out_tokens are those of spec_verify_run: token
  * out_tokens[i, m] belongs to logits row s_i + i + m.  Entries of -1 (past the
@@ -532,6 +735,10 @@ size_t spec_verify_sizeof_ngram_args(void);
 size_t spec_verify_sizeof_kv_args(void);
 size_t spec_verify_sizeof_attend_args(void);
 size_t spec_verify_sizeof_logprobs_args(void);
+size_t spec_verify_sizeof_kv4_args(void);
+size_t spec_verify_sizeof_attend4_args(void);
+size_t spec_verify_sizeof_plan_args(void);
+size_t spec_verify_sizeof_rotate_args(void);
 
 #ifdef __cplusplus
 }

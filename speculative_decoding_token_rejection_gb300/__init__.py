@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import pathlib
 from dataclasses import dataclass
 from typing import Optional
@@ -30,6 +31,7 @@ SV_MAX_SPEC_LEN = 256
 DATA_STATUS_BITS = {
     "BAD_CU": 1, "BAD_DRAFT_ID": 2, "BAD_EXPONENTIAL": 4, "EMPTY_DISTRIBUTION": 8,
     "BAD_VALUES": 16, "BAD_PARAM": 32, "MISSING_DRAFT": 64, "COPY_TIMEOUT": 128, "BAD_LIST": 256, "BAD_SLOT": 512,
+    "NO_PAGES": 1024,
 }
 
 _P = ctypes.c_void_p
@@ -44,6 +46,9 @@ SV_TEST_EXPIRE_COPY_WAIT = 1
 SV_TEST_EXPIRE_PRODUCT_WAIT = 2
 SV_CACHE_INT8, SV_CACHE_E4M3 = 0, 1
 SV_MAX_TOP_LOGPROBS = 32
+SV_CACHE_E2M1, SV_CACHE_INT4 = 16, 17
+SV_ROTATE_INTERLEAVED = 1
+SV_MAX_ROTATE_HEAD_DIM = 512
 
 
 class SpecVerifyConfig(ctypes.Structure):
@@ -141,6 +146,56 @@ class SpecVerifyLogprobsArgs(ctypes.Structure):
     ]
 
 
+class SpecVerifyKv4Cache(ctypes.Structure):
+    _fields_ = [
+        ("k", _P), ("v", _P), ("k_group", _P), ("v_group", _P), ("k_scale", _P), ("v_scale", _P),
+        ("num_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32), ("block_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("group_block_stride", ctypes.c_int64),
+        ("group_head_stride", ctypes.c_int64), ("group_token_stride", ctypes.c_int64),
+        ("scale_block_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+        ("scale_token_stride", ctypes.c_int64),
+    ]
+
+
+def _over_four_bits(struct):
+    """The fields of an 8-bit call's arguments, with a 4-bit cache in the place of its cache."""
+    return [(name, SpecVerifyKv4Cache if kind is SpecVerifyKvCache else kind) for name, kind in struct._fields_]
+
+
+class SpecVerifyKv4Args(ctypes.Structure):
+    _fields_ = _over_four_bits(SpecVerifyKvArgs)
+
+
+class SpecVerifyAttend4Args(ctypes.Structure):
+    _fields_ = _over_four_bits(SpecVerifyAttendArgs)
+
+
+class SpecVerifyPlanArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", ctypes.c_int32), ("block_size", ctypes.c_int32), ("table_width", ctypes.c_int32),
+        ("reserved", ctypes.c_uint32), ("num_rows", ctypes.c_int64), ("num_new_tokens", _P),
+        ("num_computed_tokens", _P), ("block_tables", _P), ("block_table_stride", ctypes.c_int64), ("held_pages", _P),
+        ("held_pages_out", _P), ("free_pages", _P), ("free_capacity", ctypes.c_int64), ("free_range", _P),
+        ("free_range_out", _P), ("positions", _P), ("slot_mapping", _P), ("seq_lens", _P), ("cu_num_draft_tokens", _P),
+        ("workspace", _P), ("workspace_bytes", ctypes.c_int64), ("status", _P),
+    ]
+
+
+class SpecVerifyRotateArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64), ("dtype", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_k_heads", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("q", _P), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("q_out", _P), ("q_out_token_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+        ("key", _P), ("key_token_stride", ctypes.c_int64), ("key_head_stride", ctypes.c_int64),
+        ("key_out", _P), ("key_out_token_stride", ctypes.c_int64), ("key_out_head_stride", ctypes.c_int64),
+        ("positions", _P), ("turns", _P), ("q_weight", _P), ("key_weight", _P), ("magnitude", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
 class NativeLibraryMissing(RuntimeError):
     pass
 
@@ -159,7 +214,12 @@ EXPORTED = ("spec_verify_create", "spec_verify_run", "spec_verify_destroy", "spe
             "spec_verify_check_ngram_args", "spec_verify_sizeof_ngram_args", "spec_verify_kv_write",
             "spec_verify_kv_read", "spec_verify_check_kv_args", "spec_verify_sizeof_kv_args", "spec_verify_attend",
             "spec_verify_attend_workspace_size", "spec_verify_check_attend_args", "spec_verify_sizeof_attend_args",
-            "spec_verify_logprobs", "spec_verify_check_logprobs_args", "spec_verify_sizeof_logprobs_args")
+            "spec_verify_logprobs", "spec_verify_check_logprobs_args", "spec_verify_sizeof_logprobs_args",
+            "spec_verify_kv4_write", "spec_verify_kv4_read", "spec_verify_check_kv4_args",
+            "spec_verify_sizeof_kv4_args", "spec_verify_attend4", "spec_verify_attend4_workspace_size",
+            "spec_verify_check_attend4_args", "spec_verify_sizeof_attend4_args", "spec_verify_plan_step",
+            "spec_verify_plan_workspace_size", "spec_verify_check_plan_args", "spec_verify_sizeof_plan_args",
+            "spec_verify_rotate", "spec_verify_check_rotate_args", "spec_verify_sizeof_rotate_args")
 
 
 def load_library(path: Optional[str] = None):
@@ -198,7 +258,9 @@ def load_library(path: Optional[str] = None):
     lib.spec_verify_check_ngram_args.restype = ctypes.c_int
     lib.spec_verify_sizeof_ngram_args.restype = ctypes.c_size_t
     for name, struct in (("kv", SpecVerifyKvArgs), ("attend", SpecVerifyAttendArgs),
-                         ("logprobs", SpecVerifyLogprobsArgs)):
+                         ("logprobs", SpecVerifyLogprobsArgs), ("kv4", SpecVerifyKv4Args),
+                         ("attend4", SpecVerifyAttend4Args), ("plan", SpecVerifyPlanArgs),
+                         ("rotate", SpecVerifyRotateArgs)):
         check = getattr(lib, f"spec_verify_check_{name}_args")
         check.argtypes = [ctypes.POINTER(SpecVerifyConfig), ctypes.POINTER(struct)]
         check.restype = ctypes.c_int
@@ -207,13 +269,21 @@ def load_library(path: Optional[str] = None):
         if size() != ctypes.sizeof(struct):
             raise RuntimeError("spec_verify struct layout differs from the binding")
     for name, struct in (("kv_write", SpecVerifyKvArgs), ("kv_read", SpecVerifyKvArgs),
-                         ("attend", SpecVerifyAttendArgs), ("logprobs", SpecVerifyLogprobsArgs)):
+                         ("attend", SpecVerifyAttendArgs), ("logprobs", SpecVerifyLogprobsArgs),
+                         ("kv4_write", SpecVerifyKv4Args), ("kv4_read", SpecVerifyKv4Args),
+                         ("attend4", SpecVerifyAttend4Args), ("plan_step", SpecVerifyPlanArgs),
+                         ("rotate", SpecVerifyRotateArgs)):
         fn = getattr(lib, f"spec_verify_{name}")
         fn.argtypes = [ctypes.c_void_p, ctypes.POINTER(struct), ctypes.c_void_p]
         fn.restype = ctypes.c_int
     lib.spec_verify_attend_workspace_size.argtypes = [ctypes.c_void_p, ctypes.POINTER(SpecVerifyAttendArgs),
                                                       ctypes.POINTER(ctypes.c_int64)]
     lib.spec_verify_attend_workspace_size.restype = ctypes.c_int
+    lib.spec_verify_attend4_workspace_size.argtypes = [ctypes.c_void_p, ctypes.POINTER(SpecVerifyAttend4Args),
+                                                       ctypes.POINTER(ctypes.c_int64)]
+    lib.spec_verify_attend4_workspace_size.restype = ctypes.c_int
+    lib.spec_verify_plan_workspace_size.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]
+    lib.spec_verify_plan_workspace_size.restype = ctypes.c_int
     if lib.spec_verify_sizeof_config() != ctypes.sizeof(SpecVerifyConfig) or \
             lib.spec_verify_sizeof_args() != ctypes.sizeof(SpecVerifyArgs) or \
             lib.spec_verify_sizeof_sample_args() != ctypes.sizeof(SpecVerifySampleArgs) or \
@@ -539,6 +609,9 @@ class KVCache:
     may be any floats; expanded ones are read but not written.  The tensors are
     checked once, here; the object keeps them alive."""
 
+    _kv_args, _attend_args = SpecVerifyKvArgs, SpecVerifyAttendArgs
+    _write, _read, _attend = "spec_verify_kv_write", "spec_verify_kv_read", "spec_verify_attend"
+
     def __init__(self, *, k, v, k_scale, v_scale):
         import torch
         formats = {torch.int8: SV_CACHE_INT8, torch.float8_e4m3fn: SV_CACHE_E4M3}
@@ -577,6 +650,58 @@ class KVCache:
         self.struct = c
 
 
+class KVCache4:
+    """A paged 4-bit KV cache over caller-owned tensors, taken by the same calls as ``KVCache``.
+
+    ``k`` and ``v``: uint8 ``[num_blocks, num_kv_heads, block_size, head_dim /
+    2]``, element 2i of a row in the low half of byte i; ``k_group`` and
+    ``v_group``: float8_e4m3fn ``[..., head_dim / 16]``, a scale for every 16
+    elements; ``k_scale`` and ``v_scale``: float32 ``[num_blocks, num_kv_heads,
+    block_size]``.  K and V have the same strides, unit ones along a row.
+    ``format``: "e2m1" or "int4".  A token-major cache is passed as its permuted
+    views.  The tensors are checked once, here; the object keeps them alive."""
+
+    _kv_args, _attend_args = SpecVerifyKv4Args, SpecVerifyAttend4Args
+    _write, _read, _attend = "spec_verify_kv4_write", "spec_verify_kv4_read", "spec_verify_attend4"
+
+    def __init__(self, *, k, v, k_group, v_group, k_scale, v_scale, format):
+        import torch
+        formats = {"e2m1": SV_CACHE_E2M1, "int4": SV_CACHE_INT4}
+        if format not in formats:
+            raise ValueError(f"format must be 'e2m1' or 'int4', got {format!r}")
+        if k.dim() != 4:
+            raise ValueError(f"k must have shape [num_blocks, num_kv_heads, block_size, head_dim / 2], got "
+                             f"{tuple(k.shape)}")
+        lead, dim = tuple(k.shape[:3]), 2 * k.shape[3]
+        strides = []
+        for names, pair, dtype, shape in ((("k", "v"), (k, v), torch.uint8, tuple(k.shape)),
+                                          (("k_group", "v_group"), (k_group, v_group), torch.float8_e4m3fn,
+                                           lead + (dim // 16,)),
+                                          (("k_scale", "v_scale"), (k_scale, v_scale), torch.float32, lead)):
+            for name, t in zip(names, pair):
+                if t.dtype != dtype:
+                    raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+                if tuple(t.shape) != shape:
+                    raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+                if t.device != k.device:
+                    raise ValueError(f"{name} is on {t.device}, expected {k.device}")
+                if len(shape) == 4 and shape[3] > 1 and t.stride(3) != 1:
+                    raise ValueError(f"{name} must be unit-stride along a row")
+            # (the stride of a dimension of one element says nothing)
+            a, b = ([0 if n == 1 else x for n, x in zip(lead, t.stride())] for t in pair)
+            if a != b:
+                raise ValueError(f"{names[0]} and {names[1]} must have the same strides, got {pair[0].stride()} and "
+                                 f"{pair[1].stride()}")
+            strides += a
+        self.k, self.v, self.k_group, self.v_group = k, v, k_group, v_group
+        self.k_scale, self.v_scale, self.format = k_scale, v_scale, format
+        self.device, self.head_dim = k.device, int(dim)
+        self.num_blocks, self.num_kv_heads, self.block_size = (int(n) for n in lead)
+        self.struct = SpecVerifyKv4Cache(k.data_ptr(), v.data_ptr(), k_group.data_ptr(), v_group.data_ptr(),
+                                         k_scale.data_ptr(), v_scale.data_ptr(), self.num_blocks, self.block_size,
+                                         self.num_kv_heads, self.head_dim, formats[format], *strides)
+
+
 def _heads(t, name, device, shape, dtype):
     """A [tokens, heads, head_dim] tensor with unit stride along head_dim, any
     other strides; returns (ptr, token_stride, head_stride)."""
@@ -592,9 +717,9 @@ def _heads(t, name, device, shape, dtype):
     return t.data_ptr(), (a if shape[0] > 1 else 0), (b if shape[1] > 1 else 0)
 
 
-def build_kv_args(*, cache: KVCache, key, value, slot_mapping, status=None) -> SpecVerifyKvArgs:
-    """Validate tensors and fill a SpecVerifyKvArgs (no device work).  ``key``
-    and ``value``: [T, num_kv_heads, head_dim], both float32 or both bfloat16;
+def build_kv_args(*, cache, key, value, slot_mapping, status=None):
+    """Validate tensors and fill a SpecVerifyKvArgs, or a SpecVerifyKv4Args for a
+    ``KVCache4`` (no device work).  ``key`` and ``value``: [T, num_kv_heads, head_dim], both float32 or both bfloat16;
     ``slot_mapping``: int64 [T]."""
     import torch
     device = cache.device
@@ -605,17 +730,18 @@ def build_kv_args(*, cache: KVCache, key, value, slot_mapping, status=None) -> S
     if slot_mapping.dim() != 1:
         raise ValueError(f"slot_mapping must be 1-D, got shape {tuple(slot_mapping.shape)}")
     shape = (T, cache.num_kv_heads, cache.head_dim)
-    return SpecVerifyKvArgs(T, SV_BF16 if dtype is torch.bfloat16 else SV_F32, 0, cache.struct,
-                            *_heads(key, "key", device, shape, dtype), *_heads(value, "value", device, shape, dtype),
-                            _vector(slot_mapping, torch.int64, "slot_mapping", device, T),
-                            _vector(status, torch.int32, "status", device, 1))
+    return cache._kv_args(T, SV_BF16 if dtype is torch.bfloat16 else SV_F32, 0, cache.struct,
+                          *_heads(key, "key", device, shape, dtype), *_heads(value, "value", device, shape, dtype),
+                          _vector(slot_mapping, torch.int64, "slot_mapping", device, T),
+                          _vector(status, torch.int32, "status", device, 1))
 
 
 def spec_verify_kv_write(handle: int, *, stream=None, **kw) -> None:
     """Enqueue the quantisation of key and value rows into the cache.  Keyword
     arguments are those of ``build_kv_args``."""
     a = build_kv_args(**kw)
-    _done(load_library().spec_verify_kv_write(handle, a, _stream_handle(stream, kw["cache"].device)))
+    cache = kw["cache"]
+    _done(getattr(load_library(), cache._write)(handle, a, _stream_handle(stream, cache.device)))
 
 
 def spec_verify_kv_read(handle: int, *, stream=None, **kw) -> None:
@@ -626,7 +752,8 @@ def spec_verify_kv_read(handle: int, *, stream=None, **kw) -> None:
         t = kw[name]
         if 0 in t.stride() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
             raise ValueError(f"{name} is written and must not overlap itself")
-    _done(load_library().spec_verify_kv_read(handle, a, _stream_handle(stream, kw["cache"].device)))
+    cache = kw["cache"]
+    _done(getattr(load_library(), cache._read)(handle, a, _stream_handle(stream, cache.device)))
 
 
 def spec_verify_check_kv_args(config: SpecVerifyConfig, args: SpecVerifyKvArgs) -> int:
@@ -634,10 +761,11 @@ def spec_verify_check_kv_args(config: SpecVerifyConfig, args: SpecVerifyKvArgs) 
     return int(load_library().spec_verify_check_kv_args(ctypes.byref(config), ctypes.byref(args)))
 
 
-def build_attend_args(*, q, cache: KVCache, block_tables, seq_lens, max_seq_len: int, max_spec_len: int,
+def build_attend_args(*, q, cache, block_tables, seq_lens, max_seq_len: int, max_spec_len: int,
                       scale: float, out, cu_num_draft_tokens=None, shared_prefix_len: int = 0, lse=None,
-                      workspace=None, status=None, test_flags: int = 0) -> SpecVerifyAttendArgs:
-    """Validate tensors and fill a SpecVerifyAttendArgs (no device work).
+                      workspace=None, status=None, test_flags: int = 0):
+    """Validate tensors and fill a SpecVerifyAttendArgs, or a
+    SpecVerifyAttend4Args for a ``KVCache4`` (no device work).
     ``q`` and ``out``: bfloat16 [T+N, num_q_heads, head_dim];
     ``block_tables``: int32 [N, pages]; ``seq_lens``: int32 [N]; ``lse``:
     float32 [T+N, num_q_heads] or None; ``workspace``: a uint8 tensor of at
@@ -667,7 +795,7 @@ def build_attend_args(*, q, cache: KVCache, block_tables, seq_lens, max_seq_len:
     if 0 in out.stride() and any(n > 1 and s == 0 for n, s in zip(out.shape, out.stride())):
         raise ValueError("out is written and must not overlap itself")
     bf16, i32 = torch.bfloat16, torch.int32
-    return SpecVerifyAttendArgs(
+    return cache._attend_args(
         N, int(max_spec_len), hq, int(max_seq_len), int(shared_prefix_len), 0, rows - N,
         _vector(cu_num_draft_tokens, i32, "cu_num_draft_tokens", device, N), cache.struct,
         *_heads(q, "q", device, shape, bf16), block_tables.data_ptr(), between,
@@ -681,20 +809,27 @@ def spec_verify_attend(handle: int, *, stream=None, **kw) -> None:
     """Enqueue the verify tokens' attention over the cache.  Keyword arguments
     are those of ``build_attend_args``."""
     a = build_attend_args(**kw)
-    _done(load_library().spec_verify_attend(handle, a, _stream_handle(stream, kw["cache"].device)))
+    cache = kw["cache"]
+    _done(getattr(load_library(), cache._attend)(handle, a, _stream_handle(stream, cache.device)))
 
 
 def spec_verify_attend_workspace_size(handle: int, *, num_reqs: int, max_spec_len: int, num_q_heads: int,
-                                      num_kv_heads: int, head_dim: int, max_seq_len: int, num_tokens: int,
-                                      shared_prefix_len: int = 0) -> int:
-    """Bytes of workspace for a call of these sizes (``num_tokens`` = T + N rows of q)."""
-    a = SpecVerifyAttendArgs()
+                                      max_seq_len: int, num_tokens: int, num_kv_heads: int = 0, head_dim: int = 0,
+                                      shared_prefix_len: int = 0, cache=None) -> int:
+    """Bytes of workspace for a call of these sizes (``num_tokens`` = T + N rows of q) on ``cache``, or on an 8-bit
+    cache with ``num_kv_heads`` heads of ``head_dim``."""
+    if cache is not None:
+        num_kv_heads, head_dim = cache.num_kv_heads, cache.head_dim
+    four = isinstance(cache, KVCache4)
+    a = SpecVerifyAttend4Args() if four else SpecVerifyAttendArgs()
     a.num_reqs, a.max_spec_len, a.num_q_heads = int(num_reqs), int(max_spec_len), int(num_q_heads)
     a.max_seq_len, a.shared_prefix_len = int(max_seq_len), int(shared_prefix_len)
     a.num_draft_tokens_total = int(num_tokens) - int(num_reqs)
     a.cache.num_kv_heads, a.cache.head_dim = int(num_kv_heads), int(head_dim)
     n = ctypes.c_int64()
-    _check(load_library().spec_verify_attend_workspace_size(handle, ctypes.byref(a), ctypes.byref(n)))
+    lib = load_library()
+    size = lib.spec_verify_attend4_workspace_size if four else lib.spec_verify_attend_workspace_size
+    _check(size(handle, ctypes.byref(a), ctypes.byref(n)))
     return n.value
 
 
@@ -741,6 +876,205 @@ def spec_verify_logprobs(handle: int, *, stream=None, **kw) -> None:
 def spec_verify_check_logprobs_args(config: SpecVerifyConfig, args: SpecVerifyLogprobsArgs) -> int:
     """Host-only validation of log-probability arguments; returns the sv_status code."""
     return int(load_library().spec_verify_check_logprobs_args(ctypes.byref(config), ctypes.byref(args)))
+
+
+def spec_verify_check_kv4_args(config: SpecVerifyConfig, args: SpecVerifyKv4Args) -> int:
+    """Host-only validation of 4-bit cache write / read arguments; returns the sv_status code."""
+    return int(load_library().spec_verify_check_kv4_args(ctypes.byref(config), ctypes.byref(args)))
+
+
+def spec_verify_check_attend4_args(config: SpecVerifyConfig, args: SpecVerifyAttend4Args) -> int:
+    """Host-only validation of attention arguments over a 4-bit cache; returns the sv_status code."""
+    return int(load_library().spec_verify_check_attend4_args(ctypes.byref(config), ctypes.byref(args)))
+
+
+# ----------------------------------------------------------------------------
+# block tables and slots from request lengths, rotary positions
+# ----------------------------------------------------------------------------
+def build_plan_args(*, num_new_tokens, num_computed_tokens, block_tables, held_pages, held_pages_out, free_pages,
+                    free_range, free_range_out, block_size: int, num_rows: int, positions, slot_mapping, seq_lens,
+                    workspace, cu_num_draft_tokens=None, status=None) -> SpecVerifyPlanArgs:
+    """Validate tensors and fill a SpecVerifyPlanArgs (no device work).  All
+    tensors are int32 but ``slot_mapping`` and the two ranges (int64);
+    ``block_tables`` is [N, pages], ``free_pages`` a ring of at least as many
+    entries as there are pages; ``workspace``: a uint8 tensor of at least
+    ``spec_verify_plan_workspace_size`` bytes."""
+    import torch
+    device, i32, i64 = num_new_tokens.device, torch.int32, torch.int64
+    N, R = num_new_tokens.numel(), int(num_rows)
+    if block_tables.dim() != 2 or block_tables.dtype is not i32 or block_tables.shape[0] != N:
+        raise ValueError(f"block_tables must be an int32 tensor [{N}, pages], got {tuple(block_tables.shape)} "
+                         f"{block_tables.dtype}")
+    if block_tables.device != device:
+        raise ValueError(f"block_tables is on {block_tables.device}, expected {device}")
+    width = block_tables.shape[1]
+    between, unit = block_tables.stride()
+    if width > 1 and unit != 1:
+        raise ValueError("block_tables rows must be unit-stride")
+    if N <= 1:
+        between = width
+    elif between < width:
+        raise ValueError(f"block_tables rows must not overlap (stride {between} for {width} pages)")
+    return SpecVerifyPlanArgs(
+        N, int(block_size), width, 0, R, _vector(num_new_tokens, i32, "num_new_tokens", device, N),
+        _vector(num_computed_tokens, i32, "num_computed_tokens", device, N), block_tables.data_ptr(), between,
+        _vector(held_pages, i32, "held_pages", device, N), _vector(held_pages_out, i32, "held_pages_out", device, N),
+        _vector(free_pages, i32, "free_pages", device, free_pages.numel()), free_pages.numel(),
+        _vector(free_range, i64, "free_range", device, 2), _vector(free_range_out, i64, "free_range_out", device, 2),
+        _vector(positions, i32, "positions", device, R), _vector(slot_mapping, i64, "slot_mapping", device, R),
+        _vector(seq_lens, i32, "seq_lens", device, N),
+        _vector(cu_num_draft_tokens, i32, "cu_num_draft_tokens", device, N),
+        _vector(workspace, torch.uint8, "workspace", device, workspace.numel()), workspace.numel(),
+        _vector(status, i32, "status", device, 1))
+
+
+def spec_verify_plan_step(handle: int, *, stream=None, **kw) -> None:
+    """Enqueue a step's block tables, positions and slots.  Keyword arguments
+    are those of ``build_plan_args``."""
+    a = build_plan_args(**kw)
+    _done(load_library().spec_verify_plan_step(handle, a, _stream_handle(stream, kw["num_new_tokens"].device)))
+
+
+def spec_verify_plan_workspace_size(handle: int, *, num_reqs: int) -> int:
+    """Bytes of workspace for a call with ``num_reqs`` requests (or fewer)."""
+    n = ctypes.c_int64()
+    _check(load_library().spec_verify_plan_workspace_size(handle, int(num_reqs), ctypes.byref(n)))
+    return n.value
+
+
+def spec_verify_check_plan_args(config: SpecVerifyConfig, args: SpecVerifyPlanArgs) -> int:
+    """Host-only validation of a step's arguments; returns the sv_status code."""
+    return int(load_library().spec_verify_check_plan_args(ctypes.byref(config), ctypes.byref(args)))
+
+
+_TEN_50 = 10 ** 50
+_TWO_PI = 2 * 314159265358979323846264338327950288419716939937510  # (times 10^50)
+
+
+class RotaryFrequencies:
+    """The frequencies of rotary positions, on a device.
+
+    Pair i of ``rotary_dim`` / 2 turns by base ** (-2 i / rotary_dim) radians a
+    position.  ``scaling`` for contexts longer than the trained ones:
+
+    * "linear": all frequencies divided by ``factor``;
+    * "ntk": the base times factor ** (rotary_dim / (rotary_dim - 2)), so that
+      the slowest pair is stretched by ``factor`` and the fastest is kept;
+    * "yarn": pairs that turn more than ``fast`` times over ``trained_len``
+      positions are kept, those that turn less than ``slow`` times are stretched
+      by ``factor``, with a ramp between, and rotated elements are multiplied by
+      0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023).
+
+    ``inverse`` gives the radians themselves instead, ``magnitude`` the factor of
+    the rotated elements."""
+
+    def __init__(self, rotary_dim: int, *, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                 trained_len: Optional[int] = None, fast: float = 32.0, slow: float = 1.0, inverse=None,
+                 magnitude: Optional[float] = None, device="cuda"):
+        import torch
+        if rotary_dim < 0 or rotary_dim % 2:
+            raise ValueError(f"rotary_dim must be even and not negative, got {rotary_dim}")
+        if scaling not in (None, "linear", "ntk", "yarn"):
+            raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+        if not (math.isfinite(base) and base > 1 and math.isfinite(factor) and factor > 0):
+            raise ValueError("base must be above 1 and factor above 0")
+        d, half, scale = rotary_dim, rotary_dim // 2, 1.0
+        if inverse is not None:
+            if scaling is not None:
+                raise ValueError("inverse frequencies are taken as they are: scaling must be None")
+            inv = [float(f) for f in inverse]
+            if len(inv) != half or not all(math.isfinite(f) for f in inv):
+                raise ValueError(f"inverse must hold {half} finite numbers")
+        else:
+            if scaling == "ntk":
+                if d <= 2:
+                    raise ValueError("'ntk' needs a rotary_dim above 2")
+                base = base * factor ** (d / (d - 2))
+            inv = [base ** (-2.0 * i / d) for i in range(half)]
+            if scaling == "linear":
+                inv = [f / factor for f in inv]
+            elif scaling == "yarn":
+                if not trained_len or trained_len < 1 or not fast > slow > 0:
+                    raise ValueError("'yarn' needs trained_len and fast > slow > 0")
+
+                def place(turns):  # the (fractional) pair that turns so often over trained_len
+                    return d * math.log(trained_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+                low, high = max(math.floor(place(fast)), 0), min(math.ceil(place(slow)), d - 1)
+                ramp = [min(max((i - low) / max(high - low, 0.001), 0.0), 1.0) for i in range(half)]
+                inv = [f / factor * r + f * (1.0 - r) for f, r in zip(inv, ramp)]
+                scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+        self.rotary_dim, self.inverse = int(rotary_dim), tuple(inv)
+        self.magnitude = float(scale if magnitude is None else magnitude)
+        # the fraction of a turn that a position adds, times 2^64 (as a signed word): f = n / d, pi to 50 digits
+        words = []
+        for f in inv:
+            n, d = f.as_integer_ratio()
+            words.append(((n * _TEN_50 << 65) + d * _TWO_PI) // (2 * d * _TWO_PI) % (1 << 64))
+        self.turns = torch.tensor([w - (1 << 64) if w >> 63 else w for w in words], dtype=torch.int64).to(device)
+        self.device = self.turns.device
+
+
+def build_rotate_args(*, positions, frequencies: RotaryFrequencies, q=None, key=None, q_out=None, key_out=None,
+                      q_weight=None, key_weight=None, eps: float = 1e-6,
+                      interleaved: bool = False) -> SpecVerifyRotateArgs:
+    """Validate tensors and fill a SpecVerifyRotateArgs (no device work).  ``q``
+    and ``key``: [T, heads, head_dim], both float32 or both bfloat16, as are the
+    weights [head_dim]; ``positions``: int32 [T]."""
+    import torch
+    x = q if q is not None else key
+    if x is None:
+        raise ValueError("q or key must be given")
+    if x.dim() != 3:
+        raise ValueError(f"q and key must have shape [T, heads, head_dim], got {tuple(x.shape)}")
+    device, dtype = x.device, x.dtype
+    T, _, D = x.shape
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError("q and key must be float32 or bfloat16")
+    if frequencies.device != device:
+        raise ValueError(f"frequencies are on {frequencies.device}, expected {device}")
+    sides = []
+    for name, t, out in (("q", q, q_out), ("key", key, key_out)):
+        if t is None:
+            sides.append((0, None, 0, 0, None, 0, 0))
+            continue
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have shape [T, heads, head_dim], got {tuple(t.shape)}")
+        shape = (T, t.shape[1], D)
+        if 0 in out.stride() and any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
+            raise ValueError(f"{name}_out is written and must not overlap itself")
+        src, dst = _heads(t, name, device, shape, dtype), _heads(out, f"{name}_out", device, shape, dtype)
+        if src[0] == dst[0] and src != dst and t.numel():
+            raise ValueError(f"{name}_out must be {name} itself or other memory")
+        sides.append((shape[1],) + src + dst)
+    (hq, *q_part), (hk, *key_part) = sides
+    return SpecVerifyRotateArgs(
+        T, SV_BF16 if dtype is torch.bfloat16 else SV_F32, D, frequencies.rotary_dim, hq, hk,
+        SV_ROTATE_INTERLEAVED if interleaved else 0, *q_part, *key_part,
+        _vector(positions, torch.int32, "positions", device, T), frequencies.turns.data_ptr(),
+        _vector(q_weight, dtype, "q_weight", device, D), _vector(key_weight, dtype, "key_weight", device, D),
+        frequencies.magnitude, float(eps))
+
+
+def spec_verify_rotate(handle: int, *, stream=None, **kw) -> None:
+    """Enqueue the rotation (and norms) of queries and keys.  Keyword arguments
+    are those of ``build_rotate_args``."""
+    a = build_rotate_args(**kw)
+    _done(load_library().spec_verify_rotate(handle, a, _stream_handle(stream, kw["positions"].device)))
+
+
+def spec_verify_check_rotate_args(config: SpecVerifyConfig, args: SpecVerifyRotateArgs) -> int:
+    """Host-only validation of a rotation's arguments; returns the sv_status code."""
+    return int(load_library().spec_verify_check_rotate_args(ctypes.byref(config), ctypes.byref(args)))
+
+
+@dataclass
+class PlanResult:
+    positions: "object"
+    slot_mapping: "object"
+    seq_lens: "object"
+    held_pages: "object"
+    free_range: "object"
 
 
 @dataclass
@@ -792,12 +1126,12 @@ class Verifier:
                         out_tokens=out_tokens, num_accepted=num_accepted, status=status, **kw)
         return VerifyResult(out_tokens, num_accepted, status)
 
-    def kv_write(self, *, cache: KVCache, key, value, slot_mapping, status=None, stream=None) -> None:
-        """Quantise key and value rows into the cache's slots (-1: skipped)."""
+    def kv_write(self, *, cache, key, value, slot_mapping, status=None, stream=None) -> None:
+        """Quantise key and value rows into the slots of a ``KVCache`` or ``KVCache4`` (-1: skipped)."""
         spec_verify_kv_write(self.handle, stream=stream, cache=cache, key=key, value=value, slot_mapping=slot_mapping,
                              status=status)
 
-    def kv_read(self, *, cache: KVCache, slot_mapping, key_out=None, value_out=None, dtype=None, status=None,
+    def kv_read(self, *, cache, slot_mapping, key_out=None, value_out=None, dtype=None, status=None,
                 stream=None):
         """Rows of the cache's slots (-1: zeros) as (key, value) of ``dtype`` (bfloat16)."""
         import torch
@@ -814,12 +1148,13 @@ class Verifier:
 
     def attend_workspace(self, **sizes):
         """A workspace tensor for ``attend`` calls of these sizes (the keyword
-        arguments of ``spec_verify_attend_workspace_size``), to be kept."""
+        arguments of ``spec_verify_attend_workspace_size``: with ``cache``, or
+        for an 8-bit one with its heads), to be kept."""
         import torch
         n = spec_verify_attend_workspace_size(self.handle, **sizes)
         return torch.empty(max(n, 16), dtype=torch.uint8, device=torch.device("cuda", self.device))
 
-    def attend(self, *, q, cache: KVCache, block_tables, seq_lens, max_seq_len: int, max_spec_len: int, scale: float,
+    def attend(self, *, q, cache, block_tables, seq_lens, max_seq_len: int, max_spec_len: int, scale: float,
                cu_num_draft_tokens=None, shared_prefix_len: int = 0, out=None, lse=None, workspace=None, status=None,
                stream=None):
         """Attention of the verify tokens over the cache; returns ``out``.
@@ -831,8 +1166,7 @@ class Verifier:
                     out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
                 if workspace is None:
                     workspace = self.attend_workspace(
-                        num_reqs=block_tables.shape[0], max_spec_len=max_spec_len, num_q_heads=q.shape[1],
-                        num_kv_heads=cache.num_kv_heads, head_dim=cache.head_dim,
+                        cache=cache, num_reqs=block_tables.shape[0], max_spec_len=max_spec_len, num_q_heads=q.shape[1],
                         max_seq_len=min(max_seq_len, block_tables.shape[-1] * cache.block_size),  # (the call's own bound)
                         shared_prefix_len=shared_prefix_len, num_tokens=q.shape[0])
         spec_verify_attend(self.handle, stream=stream, q=q, cache=cache, block_tables=block_tables, seq_lens=seq_lens,
@@ -865,3 +1199,54 @@ class Verifier:
                              cu_num_draft_tokens=cu_num_draft_tokens, temperature=temperature, num_top=num_top,
                              status=status)
         return LogprobsResult(logprobs, ranks, entropy, top_ids, top_logprobs)
+
+    def plan_workspace(self, *, num_reqs: int):
+        """A workspace tensor for ``plan_step`` calls of up to ``num_reqs`` requests, to be kept."""
+        import torch
+        n = spec_verify_plan_workspace_size(self.handle, num_reqs=num_reqs)
+        return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", self.device))
+
+    def plan_step(self, *, num_new_tokens, num_computed_tokens, block_tables, held_pages, free_pages, free_range,
+                  block_size: int, num_rows: int, positions=None, slot_mapping=None, seq_lens=None,
+                  held_pages_out=None, free_range_out=None, cu_num_draft_tokens=None, workspace=None, status=None,
+                  stream=None) -> PlanResult:
+        """Pages for a step's new tokens, and their positions and slots: what
+        ``rotate``, ``kv_write`` and ``attend`` take.  ``block_tables`` and
+        ``free_pages`` are updated, and so are ``held_pages`` and ``free_range``
+        unless their outputs are given.  Requests with a negative
+        ``num_computed_tokens`` are done: their pages go back."""
+        import torch
+        dev = num_new_tokens.device
+        if positions is None or slot_mapping is None or seq_lens is None or workspace is None:
+            with _allocated_on(stream, dev):
+                if positions is None:
+                    positions = torch.empty(num_rows, dtype=torch.int32, device=dev)
+                if slot_mapping is None:
+                    slot_mapping = torch.empty(num_rows, dtype=torch.int64, device=dev)
+                if seq_lens is None:
+                    seq_lens = torch.empty(num_new_tokens.numel(), dtype=torch.int32, device=dev)
+                if workspace is None:
+                    workspace = self.plan_workspace(num_reqs=num_new_tokens.numel())
+        if held_pages_out is None:
+            held_pages_out = held_pages
+        if free_range_out is None:
+            free_range_out = free_range
+        spec_verify_plan_step(self.handle, stream=stream, num_new_tokens=num_new_tokens,
+                              num_computed_tokens=num_computed_tokens, block_tables=block_tables,
+                              held_pages=held_pages, held_pages_out=held_pages_out, free_pages=free_pages,
+                              free_range=free_range, free_range_out=free_range_out, block_size=block_size,
+                              num_rows=num_rows, positions=positions, slot_mapping=slot_mapping, seq_lens=seq_lens,
+                              cu_num_draft_tokens=cu_num_draft_tokens, workspace=workspace, status=status)
+        return PlanResult(positions, slot_mapping, seq_lens, held_pages_out, free_range_out)
+
+    def rotate(self, *, positions, frequencies: RotaryFrequencies, q=None, key=None, q_out=None, key_out=None,
+               q_weight=None, key_weight=None, eps: float = 1e-6, interleaved: bool = False, stream=None):
+        """Queries and keys turned to their positions, with a norm of each head
+        before it where a weight is given; in place without outputs.  Rows of a
+        negative position are left alone.  Returns (q, key) as written."""
+        q_out = q if q_out is None else q_out
+        key_out = key if key_out is None else key_out
+        spec_verify_rotate(self.handle, stream=stream, positions=positions, frequencies=frequencies, q=q, key=key,
+                           q_out=q_out, key_out=key_out, q_weight=q_weight, key_weight=key_weight, eps=eps,
+                           interleaved=interleaved)
+        return q_out, key_out

@@ -90,76 +90,6 @@ struct RowTile {
   int page;    // of the lane's key of its warp's first tile, looked up before the request's length was there
 };
 
-// One partial result of a row: M, l and the lane's dimensions of O.
-template <int D>
-struct Part {
-  float m, l, o[D / 32];
-};
-constexpr int kJoinAhead = 4;  // partial results of a row in flight
-template <int D>
-__device__ __forceinline__ Part<D> load_part(const AttendPlan &L, int64_t row, int s, int lane) {
-  Part<D> p;
-  const float2 ml = __ldcg(L.part_ml + row * L.slots + s);
-  p.m = ml.x;
-  p.l = ml.y;
-  const float *src = L.part_o + (row * L.slots + s) * D;
-  if (D == 128) {
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
-    p.o[0] = v.x;
-    p.o[1] = v.y;
-    p.o[D / 32 - 2] = v.z;
-    p.o[D / 32 - 1] = v.w;
-  } else {
-    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src) + lane);
-    p.o[0] = v.x;
-    p.o[1] = v.y;
-  }
-  return p;
-}
-template <int D>
-__device__ __forceinline__ void store_part(const AttendPlan &L, int64_t row, int s, int lane, const Part<D> &p) {
-  float *dst = L.part_o + (row * L.slots + s) * D;
-  if (D == 128)
-    reinterpret_cast<float4 *>(dst)[lane] = make_float4(p.o[0], p.o[1], p.o[D / 32 - 2], p.o[D / 32 - 1]);
-  else
-    reinterpret_cast<float2 *>(dst)[lane] = make_float2(p.o[0], p.o[1]);
-  if (lane == 0) L.part_ml[row * L.slots + s] = make_float2(p.m, p.l);
-}
-// a joined with b: with M the larger maximum, O = sum 2^(M_s - M) O_s and l likewise.  A part without a maximum is
-// zeros, or NaN where all its scores are, and is added as it is.
-template <int D>
-__device__ __forceinline__ void join_part(Part<D> &a, const Part<D> &b) {
-  const float m = fmaxf(a.m, b.m);
-  const float fa = a.m == -INFINITY ? 1.0f : exp2_approx(a.m - m), fb = b.m == -INFINITY ? 1.0f : exp2_approx(b.m - m);
-  a.m = m;
-  a.l = fmaf(a.l, fa, b.l * fb);
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d) a.o[d] = fmaf(a.o[d], fa, b.o[d] * fb);
-}
-template <int D>
-__device__ __forceinline__ void write_row(const AttendParams &P, const AttendPlan &L, int64_t token, int hq, int lane,
-                                          const Part<D> &p) {
-  const float r = p.l == 0.0f ? 0.0f : 1.0f / p.l;
-  float x[D / 32];
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d) x[d] = p.l == 0.0f ? 0.0f : p.o[d] * r;
-  uint16_t *dst = P.out + token * P.out_token + hq * P.out_head + lane * (D / 32);
-  const uint32_t w0 = pack_bf16(x[0], x[1]), w1 = pack_bf16(x[D / 32 - 2], x[D / 32 - 1]);
-  if (L.ovec && D == 128) {
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
-  } else if (L.ovec) {
-    *reinterpret_cast<uint32_t *>(dst) = w0;
-  } else {
-    dst[0] = static_cast<uint16_t>(w0);
-    dst[1] = static_cast<uint16_t>(w0 >> 16);
-    if (D == 128) {
-      dst[2] = static_cast<uint16_t>(w1);
-      dst[3] = static_cast<uint16_t>(w1 >> 16);
-    }
-  }
-  if (P.lse && lane == 0) P.lse[token * P.Hq + hq] = p.l == 0.0f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
-}
-
 struct JoinSmem {
   float m[kAttendWarps][32], l[kAttendWarps][32];
   uint32_t top[kGroups * 8];  // largest finite |q| of a row
@@ -740,12 +670,19 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
 // 1024 77 | 50, 2048 84 | 78, 4096 94 | 136; 512 x 8, 512 305 | 257, 1024 335 | 365;
 // 512 x 1, 256 118 | 95, 512 120 | 126; 2 x 5 (40 rows), 4096 33 | 29, 16384 48 | 38;
 // 16 x 1 (64 rows), 256 17 | 17, 1024 19 | 22.
+bool four_bits(const AttendParams &p) { return p.c.format == SV_CACHE_E2M1 || p.c.format == SV_CACHE_INT4; }
+int own_rows(const AttendParams &p) { return four_bits(p) ? kOwnRows4 : 8 * kGroups; }
+
 AttendParams short_prefix(AttendParams p) {
   const int64_t H = p.c.num_kv_heads, own = (p.G + 1) * static_cast<int64_t>(p.group), own_tiles = ceil_div(own, 8 * kGroups);
   // (the rows there may be, so that calls with fewer tokens choose alike)
   const int64_t rows = p.N * own;
   int64_t saved = p.N * H * own_tiles * (24 + 7 * ceil_div(ceil_div(own, 8), own_tiles)), begin, most;  // ps a key; ps; keys
-  if (rows >= kTensorRows) {
+  if (four_bits(p) && rows < kTensorRows) {  // (few rows read it each for themselves)
+    saved = 0;
+    begin = 0;
+    most = INT64_MAX;
+  } else if (rows >= kTensorRows) {
     saved -= H * (75 + 64 * static_cast<int64_t>(ceil_div(rows, kPrefixRowTile)));
     begin = 31000000 + 950 * rows * H;
     most = 16384 + 1;
@@ -766,7 +703,7 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   L.page = fast_div(std::max(1, p.c.block_size));
   L.group = fast_div(p.group);
   L.rows = static_cast<int32_t>((p.T + p.N) * p.group);
-  L.own_tiles = ceil_div((p.G + 1) * static_cast<int64_t>(p.group), 8 * kGroups);
+  L.own_tiles = ceil_div((p.G + 1) * static_cast<int64_t>(p.group), own_rows(p));
   L.prefix_tiles = ceil_div(L.rows, 8 * kGroups);
   // (at least one private chunk, though no request may have private keys: its CTAs look at the requests' ranges)
   int bound = std::max(1, cut(static_cast<int64_t>(p.N) * p.c.num_kv_heads * L.own_tiles, p.max_seq - p.prefix, num_sms,
@@ -811,7 +748,7 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
 }
 
 template <int D, int FMT>
-cudaError_t launch(const AttendParams &p, const AttendPlan &L, int num_sms, cudaStream_t stream) {
+cudaError_t launch_own(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
   const int64_t own = static_cast<int64_t>(p.N) * p.c.num_kv_heads * L.own_tiles * L.own_splits;
@@ -822,8 +759,21 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, int num_sms, cuda
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
+  return cudaLaunchKernelEx(&cfg, attend_kernel<D, FMT>, p, L);
+}
+
+template <int D>
+cudaError_t launch(const AttendParams &p, const AttendPlan &L, int num_sms, cudaStream_t stream) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
   cudaError_t e = L.tensor_tiles ? launch_prefix(p, L, stream) : cudaSuccess;
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, attend_kernel<D, FMT>, p, L);
+  if (e == cudaSuccess)
+    e = four_bits(p)                      ? launch_own4(p, L, stream)
+        : p.c.format == SV_CACHE_INT8 ? launch_own<D, SV_CACHE_INT8>(p, L, stream)
+                                      : launch_own<D, SV_CACHE_E4M3>(p, L, stream);
   if (e != cudaSuccess || L.slots == 1) return e;
   // a warp takes two rows where there are rows for more than eight waves of CTAs (512 requests x 256 rows: 1084 us the
   // whole call against 1108 with one row a warp; 64 x 160: 138.5 against 137.4)
@@ -844,7 +794,8 @@ cudaError_t enable() {
 cudaError_t enable_attend_kernels() {
   cudaError_t e;
   if ((e = enable<128, SV_CACHE_INT8>()) != cudaSuccess || (e = enable<128, SV_CACHE_E4M3>()) != cudaSuccess ||
-      (e = enable<64, SV_CACHE_INT8>()) != cudaSuccess || (e = enable_prefix_kernels()) != cudaSuccess)
+      (e = enable<64, SV_CACHE_INT8>()) != cudaSuccess || (e = enable_prefix_kernels()) != cudaSuccess ||
+      (e = enable_own4_kernels()) != cudaSuccess)
     return e;
   return enable<64, SV_CACHE_E4M3>();
 }
@@ -871,9 +822,7 @@ int64_t attend_workspace_bytes(const AttendParams &a, int num_sms, bool fewer) {
 cudaError_t launch_attend(const AttendParams &a, int num_sms, cudaStream_t stream) {
   const AttendParams p = short_prefix(a);
   const AttendPlan L = make_plan(p, num_sms);
-  const bool i8 = p.c.format == SV_CACHE_INT8;
-  if (p.c.head_dim == 128) return i8 ? launch<128, SV_CACHE_INT8>(p, L, num_sms, stream) : launch<128, SV_CACHE_E4M3>(p, L, num_sms, stream);
-  return i8 ? launch<64, SV_CACHE_INT8>(p, L, num_sms, stream) : launch<64, SV_CACHE_E4M3>(p, L, num_sms, stream);
+  return p.c.head_dim == 128 ? launch<128>(p, L, num_sms, stream) : launch<64>(p, L, num_sms, stream);
 }
 
 }  // namespace sv

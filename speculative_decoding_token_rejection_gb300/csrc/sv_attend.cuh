@@ -147,4 +147,114 @@ __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+
+// One partial result of a row: M, l and the lane's dimensions of O.
+template <int D>
+struct Part {
+  float m, l, o[D / 32];
+};
+constexpr int kJoinAhead = 4;  // partial results of a row in flight
+template <int D>
+__device__ __forceinline__ Part<D> load_part(const AttendPlan &L, int64_t row, int s, int lane) {
+  Part<D> p;
+  const float2 ml = __ldcg(L.part_ml + row * L.slots + s);
+  p.m = ml.x;
+  p.l = ml.y;
+  const float *src = L.part_o + (row * L.slots + s) * D;
+  if (D == 128) {
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+    p.o[0] = v.x;
+    p.o[1] = v.y;
+    p.o[D / 32 - 2] = v.z;
+    p.o[D / 32 - 1] = v.w;
+  } else {
+    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src) + lane);
+    p.o[0] = v.x;
+    p.o[1] = v.y;
+  }
+  return p;
+}
+template <int D>
+__device__ __forceinline__ void store_part(const AttendPlan &L, int64_t row, int s, int lane, const Part<D> &p) {
+  float *dst = L.part_o + (row * L.slots + s) * D;
+  if (D == 128)
+    reinterpret_cast<float4 *>(dst)[lane] = make_float4(p.o[0], p.o[1], p.o[D / 32 - 2], p.o[D / 32 - 1]);
+  else
+    reinterpret_cast<float2 *>(dst)[lane] = make_float2(p.o[0], p.o[1]);
+  if (lane == 0) L.part_ml[row * L.slots + s] = make_float2(p.m, p.l);
+}
+// a joined with b: with M the larger maximum, O = sum 2^(M_s - M) O_s and l likewise.  A part without a maximum is
+// zeros, or NaN where all its scores are, and is added as it is.
+template <int D>
+__device__ __forceinline__ void join_part(Part<D> &a, const Part<D> &b) {
+  const float m = fmaxf(a.m, b.m);
+  const float fa = a.m == -INFINITY ? 1.0f : exp2_approx(a.m - m), fb = b.m == -INFINITY ? 1.0f : exp2_approx(b.m - m);
+  a.m = m;
+  a.l = fmaf(a.l, fa, b.l * fb);
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) a.o[d] = fmaf(a.o[d], fa, b.o[d] * fb);
+}
+template <int D>
+__device__ __forceinline__ void write_row(const AttendParams &P, const AttendPlan &L, int64_t token, int hq, int lane,
+                                          const Part<D> &p) {
+  const float r = p.l == 0.0f ? 0.0f : 1.0f / p.l;
+  float x[D / 32];
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) x[d] = p.l == 0.0f ? 0.0f : p.o[d] * r;
+  uint16_t *dst = P.out + token * P.out_token + hq * P.out_head + lane * (D / 32);
+  const uint32_t w0 = pack_bf16(x[0], x[1]), w1 = pack_bf16(x[D / 32 - 2], x[D / 32 - 1]);
+  if (L.ovec && D == 128) {
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
+  } else if (L.ovec) {
+    *reinterpret_cast<uint32_t *>(dst) = w0;
+  } else {
+    dst[0] = static_cast<uint16_t>(w0);
+    dst[1] = static_cast<uint16_t>(w0 >> 16);
+    if (D == 128) {
+      dst[2] = static_cast<uint16_t>(w1);
+      dst[3] = static_cast<uint16_t>(w1 >> 16);
+    }
+  }
+  if (P.lse && lane == 0) P.lse[token * P.Hq + hq] = p.l == 0.0f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
+}
+
+// A CTA of the private part: a request's row tile of one kv head over one chunk of its keys.
+struct OwnTile {
+  int64_t first;        // the request's first row
+  int i, h, gam, len;   // the request, the kv head, its drafts and keys
+  int r0, rows;         // of the request's (gam + 1) * group rows
+  int split, k_begin, k_end;
+  bool whole;           // every key that the rows see: the result is the output
+};
+// False: nothing to do.  `most` rows a tile; the request's groups of 8 rows are dealt evenly to as few tiles as hold them.
+__device__ __forceinline__ bool own_tile(const AttendParams &P, const AttendPlan &L, int b, int most, OwnTile &T) {
+  const int tile = b % L.own_tiles;
+  b /= L.own_tiles;
+  T.h = b % P.c.num_kv_heads;
+  b /= P.c.num_kv_heads;
+  T.split = b % L.own_splits;
+  T.i = b / L.own_splits;
+  T.k_begin = P.prefix + T.split * L.own_chunk;
+  uint32_t bits = 0;
+  const bool ok = attend_request(P, T.i, T.first, T.gam, T.len, bits);
+  if (bits && tile == 0 && T.h == 0 && T.split == 0 && threadIdx.x == 0 && P.status)
+    atomicOr(P.status, static_cast<int>(bits));
+  if (!ok) return false;
+  const int all = (T.gam + 1) * P.group, groups = (all + 7) / 8, tiles = (groups * 8 + most - 1) / most;
+  if (tile >= tiles) return false;
+  const int per = (groups + tiles - 1) / tiles * 8;
+  T.r0 = tile * per;
+  T.rows = min(per, all - T.r0);
+  if (T.rows <= 0) return false;
+  T.k_end = min(T.len, T.k_begin + L.own_chunk);
+  // (a request without a prefix and with one chunk of keys or none needs no joining)
+  T.whole = P.prefix == 0 && T.len <= L.own_chunk;
+  return T.k_end > T.k_begin || (T.whole && T.split == 0);
+}
+
+// The private part over the 4-bit cache (sv_attend4.cu): tiles of kOwnRows4 rows.
+constexpr int kOwnRows4 = 64;
+cudaError_t enable_own4_kernels();
+cudaError_t launch_own4(const AttendParams &p, const AttendPlan &L, cudaStream_t stream);
+
 }  // namespace sv

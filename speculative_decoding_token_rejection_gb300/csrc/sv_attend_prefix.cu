@@ -51,6 +51,8 @@
 #include <cstdint>
 
 #include "sv_attend.cuh"
+#include "sv_cache4.cuh"
+#include "sv_tensor.cuh"
 
 namespace sv {
 namespace {
@@ -61,8 +63,6 @@ constexpr int kSoftmaxThreads = 256;
 constexpr int kVectorThreads = 64;
 constexpr int kPrefixThreads = kSoftmaxThreads + kVectorThreads + 64;
 constexpr int kVectorSlots = 4;
-constexpr uint32_t kWaitPolls = 1u << 24;
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRaise = 8;
 constexpr float kScaleUnit = 0x1p28f;  // W
 constexpr float kLeastUnits = kLeastLog2 - 28;  // log2 of the size that a scale counts as at least, in W
@@ -90,51 +90,6 @@ struct Smem {
                        kBytes = kControl + static_cast<int>(sizeof(Control)) + 1024;  // (the base is rounded up to 1 KB)
 };
 
-// ---------------------------------------------------------------------------
-// tcgen05
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
-}
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// D (tensor memory) = A B (+ D), both operands in shared memory.
-template <bool ADD>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "n"(ADD ? 1 : 0)
-      : "memory");
-}
-// The same with A in tensor memory.
-template <bool ADD>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "n"(ADD ? 1 : 0)
-      : "memory");
-}
-// One lane of a converged warp.
-__device__ __forceinline__ bool elected() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-// Arrives on `bar` once every product issued so far by this thread is done.
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
 // Tensor memory in the shape of a 16x8 product's accumulator, N of them side by
 // side, for 16 of the warp's 32 lanes: register 4j, 4j + 1 of lane (g, c) are
 // columns 8j + 2c, + 1 of row g, the next two of row g + 8.
@@ -167,14 +122,6 @@ __device__ __forceinline__ void tmem_load_32(uint32_t addr, uint32_t r[16]) {
       : "r"(addr)
       : "memory");
 }
-// Waits for every load so far; the registers go through, so no use of them moves ahead of the wait.
-__device__ __forceinline__ void tmem_wait_load(uint32_t r[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
 __device__ __forceinline__ void tmem_store_32(uint32_t addr, const uint32_t r[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {"
@@ -190,63 +137,6 @@ __device__ __forceinline__ void tmem_store_pairs(uint32_t addr, const uint32_t r
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Shared-memory operand with rows of 128 bytes (64 f16), 8-row groups of 1 KB,
-// 16-byte columns exchanged within a group (column ^ row % 8).  `next64`:
-// bytes from 64 elements to the next 64 where those run along the operand's
-// outer dimension.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t next64) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | static_cast<uint64_t>((next64 >> 4) & 0x3FFF) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
-}
-// f16 operands, fp32 sums, 128 x n; B's outer dimension contiguous or its inner one.
-constexpr uint32_t product(int n, bool b_outer_contiguous) {
-  return 1u << 4 | (b_outer_contiguous ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (128u / 16) << 24;
-}
-
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// The CTA gives up: no wait begins anew, rows that are not done become NaN, and
-// the status word says so at the end.
-__device__ __forceinline__ void give_up(Control &C) {
-  *const_cast<volatile uint32_t *>(&C.abort) = 1;
-  __threadfence_block();
-}
-__device__ __forceinline__ bool gave_up(const Control &C) { return *const_cast<const volatile uint32_t *>(&C.abort) != 0; }
-// Waits for phase `parity` of a barrier; false when the CTA gives up (a wait
-// of two seconds, `expire`, or another thread that did).
-__device__ __forceinline__ bool wait(Control &C, uint64_t *bar, uint32_t parity, bool expire = false) {
-  if (!expire) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t began = now_ns();
-    for (uint32_t it = 0; it < kWaitPolls; ++it) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if (gave_up(C)) return false;
-      if ((it & 15u) == 15u && now_ns() - began > kWaitNs) break;
-    }
-  }
-  give_up(C);
-  return false;
-}
-// The same for all lanes of a warp together.
-__device__ __forceinline__ bool wait_warp(Control &C, uint64_t *bar, uint32_t parity, bool expire = false) {
-  return __all_sync(0xFFFFFFFFu, wait(C, bar, parity, expire));
-}
-// Waits for what is in flight, also in a CTA that has given up: shared and
-// tensor memory must not go before it.
-__device__ __forceinline__ void settle(Control &C, uint64_t *bar, uint32_t parity) {
-  const uint64_t began = now_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (now_ns() - began > kWaitNs) {
-      give_up(C);
-      return;
-    }
-}
-
 // The prefix's K and V as f16 tiles of 128 keys, each in the order of its
 // shared memory: 64 dimensions after 64, rows of 128 bytes, 16-byte columns
 // exchanged by row % 8.  Keys that are not there are zeros, and so are e4m3
@@ -282,6 +172,44 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const AttendParams P, 
     uint32_t w[4];
     bytes_to_f16<FMT>(raw[p].x, w[0], w[1]);
     bytes_to_f16<FMT>(raw[p].y, w[2], w[3]);
+    *reinterpret_cast<uint4 *>(out + (col >> 3) * (kKeyTile * 128) + r * 128 + (((col & 7) ^ (r & 7)) << 4)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The same from the 4-bit cache: a thread takes half a group.  Behind the prefix's end nothing is read.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads) unpack4_kernel(const AttendParams P, const AttendPlan L) {
+  pdl_enter();
+  constexpr int kCols = D / 8, kPieces = kKeyTile * kCols / kThreads;
+  const int tile = blockIdx.x, h = blockIdx.y, side = blockIdx.z, col = threadIdx.x % kCols;
+  const uint8_t *const base = static_cast<const uint8_t *>(side ? P.c.v : P.c.k) + h * P.c.head_stride + col * 4;
+  const uint8_t *const group = (side ? P.v_group : P.k_group) + h * P.group_head + (col >> 1);
+  uint8_t *const out = L.image + ((static_cast<int64_t>(h) * L.image_tiles + tile) * 2 + side) * (kKeyTile * D * 2);
+  uint32_t raw[kPieces], g[kPieces];
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const int r = p * (kThreads / kCols) + threadIdx.x / kCols, k = tile * kKeyTile + r;
+    raw[p] = g[p] = 0;
+    if (k < P.prefix) {
+      const int x = div_by(k, L.page), page = P.tables[x], off = k - x * P.c.block_size;
+      if (page >= 0 && page < P.c.num_blocks) {
+        raw[p] = __ldg(reinterpret_cast<const uint32_t *>(base + page * P.c.block_stride + off * P.c.token_stride));
+        g[p] = group[page * P.group_block + off * P.group_token];
+        // (a value behind every request's length may have a scale that is no number: a weight of 0 times it would be NaN)
+        if (side && (g[p] & 0x7Fu) == 0x7Fu) g[p] = 0;
+      }
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const int r = p * (kThreads / kCols) + threadIdx.x / kCols;
+    uint32_t w[8];
+    group_to_f16<FMT>(make_uint2(raw[p], 0), group_factors<FMT>(g[p]), w);
+    if (FMT == SV_CACHE_INT4) {  // (whole numbers times their scale: 3584 at most)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = hmul2(w[e], 0x4C004C00u);  // (16)
+    }
     *reinterpret_cast<uint4 *>(out + (col >> 3) * (kKeyTile * 128) + r * 128 + (((col & 7) ^ (r & 7)) << 4)) =
         make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -828,7 +756,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
   }
 }
 
-template <int D, int FMT>
+template <int D>
 cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
@@ -837,7 +765,12 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stre
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, unpack_kernel<D, FMT>, p, L);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg,
+                                           p.c.format == SV_CACHE_INT8   ? unpack_kernel<D, SV_CACHE_INT8>
+                                           : p.c.format == SV_CACHE_E4M3 ? unpack_kernel<D, SV_CACHE_E4M3>
+                                           : p.c.format == SV_CACHE_INT4 ? unpack4_kernel<D, SV_CACHE_INT4>
+                                                                         : unpack4_kernel<D, SV_CACHE_E2M1>,
+                                           p, L);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>((L.units + L.units_cta - 1) / L.units_cta));
   cfg.blockDim = dim3(kPrefixThreads);
@@ -857,9 +790,7 @@ cudaError_t enable_prefix_kernels() {
 }
 
 cudaError_t launch_prefix(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
-  const bool i8 = p.c.format == SV_CACHE_INT8;
-  if (p.c.head_dim == 128) return i8 ? launch<128, SV_CACHE_INT8>(p, L, stream) : launch<128, SV_CACHE_E4M3>(p, L, stream);
-  return i8 ? launch<64, SV_CACHE_INT8>(p, L, stream) : launch<64, SV_CACHE_E4M3>(p, L, stream);
+  return p.c.head_dim == 128 ? launch<128>(p, L, stream) : launch<64>(p, L, stream);
 }
 
 }  // namespace sv

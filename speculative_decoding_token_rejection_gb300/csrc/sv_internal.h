@@ -189,6 +189,20 @@ void set_last_error(const char *fmt, ...);
 // The checks of a handle's limits; sets the last error.
 sv_status check_config(const spec_verify_config *c);
 
+// n / d for n, d < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d),
+// l = ceil(log2 d), so that mul * d - 2^(31 + l) < d <= 2^l and the error of
+// n * mul / 2^(31 + l) stays below 1 / d.
+struct FastDiv {
+  uint32_t mul;
+  int32_t shift, d;
+};
+inline FastDiv fast_div(int32_t d) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;
+  const unsigned long long p = 1ull << (31 + l);
+  return FastDiv{static_cast<uint32_t>((p + d - 1) / d), 31 + l, d};
+}
+
 // Tokens written to or read from the paged 8-bit cache (sv_cache.cu).
 struct KvParams {
   int64_t T;
@@ -209,7 +223,9 @@ struct AttendParams {
   int32_t row0;  // keys below it have their pages in row 0 of the tables, though every request reads them itself
   int64_t T;
   const int32_t *cu;
-  spec_verify_kv_cache c;
+  spec_verify_kv_cache c;  // (of a 4-bit cache: what it has in common, and its format)
+  const uint8_t *k_group, *v_group;  // of a 4-bit cache
+  int64_t group_block, group_head, group_token;
   const uint16_t *q;
   int64_t q_token, q_head;  // element strides
   const int32_t *tables;
@@ -234,6 +250,67 @@ inline uint32_t cache_unit(const spec_verify_kv_cache &c) {
 int64_t attend_workspace_bytes(const AttendParams &p, int num_sms, bool fewer);
 cudaError_t enable_attend_kernels();
 cudaError_t launch_attend(const AttendParams &p, int num_sms, cudaStream_t stream);
+// What the calls over an 8-bit and a 4-bit cache share (sv_ops_api.cu).
+AttendParams attend_params(const spec_verify_t h, const spec_verify_attend_args *a);
+sv_status check_attend_sizes(const spec_verify_config *c, const spec_verify_attend_args *a);
+sv_status check_attend_call(const spec_verify_attend_args *a);
+sv_status run_attend(spec_verify_t h, const AttendParams &p, int64_t workspace_bytes, void *stream);
+
+// Tokens written to or read from the paged 4-bit cache (sv_cache4.cu).
+struct Kv4Params {
+  int64_t T;
+  spec_verify_kv4_cache c;
+  void *key, *value;
+  int64_t key_token, key_head, value_token, value_head;  // element strides
+  const int64_t *slots;
+  int32_t *status;
+  bool pdl;
+};
+cudaError_t launch_kv4_write(const Kv4Params &p, bool bf16, bool vec, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4Params &p, bool bf16, bool vec, cudaStream_t stream);
+
+// Block tables, positions and slots of a step (sv_plan.cu).
+struct PlanParams {
+  int32_t N, block, width;
+  FastDiv page;
+  int64_t R;
+  const int32_t *fresh, *computed;
+  int32_t *tables;
+  int64_t table_stride;
+  const int32_t *held;
+  int32_t *held_out;
+  int32_t *ring;
+  int64_t capacity;
+  const int64_t *range;
+  int64_t *range_out;
+  int32_t *positions;
+  int64_t *slots;
+  int32_t *seq_lens, *cu;
+  void *workspace;
+  int32_t *status;
+  bool pdl;
+};
+int64_t plan_workspace_bytes(int32_t num_reqs);
+cudaError_t launch_plan(const PlanParams &p, cudaStream_t stream);
+
+// Rotary positions and norms (sv_rotate.cu).
+struct RotateSide {
+  const void *in;
+  void *out;
+  const void *weight;  // null: no norm
+  int64_t in_token, in_head, out_token, out_head;  // element strides
+};
+struct RotateParams {
+  int64_t T;
+  int32_t D, rotary, Hq, Hk;
+  bool interleaved;
+  RotateSide q, k;
+  const int32_t *positions;
+  const uint64_t *turns;
+  float magnitude, eps;
+  bool pdl;
+};
+cudaError_t launch_rotate(const RotateParams &p, bool bf16, int num_sms, cudaStream_t stream);
 
 // Log-probabilities of committed tokens (sv_logprobs.cu).
 struct LogprobsParams {

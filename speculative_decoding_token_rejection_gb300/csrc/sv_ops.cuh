@@ -7,6 +7,7 @@
 
 #include "spec_verify.h"
 #include "sv_device.cuh"
+#include "sv_internal.h"
 
 namespace sv {
 
@@ -122,19 +123,7 @@ __device__ __forceinline__ void mma_16816(float d[4], const uint4 &a, uint32_t b
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// n / d for n, d < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d),
-// l = ceil(log2 d), so that mul * d - 2^(31 + l) < d <= 2^l and the error of
-// n * mul / 2^(31 + l) stays below 1 / d.
-struct FastDiv {
-  uint32_t mul;
-  int32_t shift, d;
-};
-inline FastDiv fast_div(int32_t d) {
-  int l = 0;
-  while ((1ll << l) < d) ++l;
-  const unsigned long long p = 1ull << (31 + l);
-  return FastDiv{static_cast<uint32_t>((p + d - 1) / d), 31 + l, d};
-}
+// n / d by the factors of fast_div.
 __device__ __forceinline__ int div_by(int n, const FastDiv &f) {
   return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(n)) * f.mul) >> f.shift);
 }

@@ -54,59 +54,6 @@ sv_status check_layout(const spec_verify_config *c, int32_t N, int32_t G, int64_
   return SV_OK;
 }
 
-sv_status check_attend_sizes(const spec_verify_config *c, const spec_verify_attend_args *a) {
-  const sv_status st = check_layout(c, a->num_reqs, a->max_spec_len, a->num_draft_tokens_total,
-                                    a->cu_num_draft_tokens);
-  if (st != SV_OK) return st;
-  if (a->cache.num_kv_heads < 1 || a->num_q_heads < 1 || a->num_q_heads % a->cache.num_kv_heads)
-    return fail(SV_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
-  if (a->cache.head_dim != 64 && a->cache.head_dim != 128)
-    return fail(SV_ERR_UNSUPPORTED, "head_dim %d is not 64 or 128", a->cache.head_dim);
-  if (a->cache.num_kv_heads > 65535 || a->num_q_heads > 65535)
-    return fail(SV_ERR_UNSUPPORTED, "more than 65535 heads");
-  if (a->max_seq_len < 0) return fail(SV_ERR_INVALID_ARG, "max_seq_len < 0");
-  if (a->max_seq_len > (1 << 30)) return fail(SV_ERR_UNSUPPORTED, "max_seq_len %d > 2^30", a->max_seq_len);
-  if (a->shared_prefix_len < 0 || a->shared_prefix_len > a->max_seq_len)
-    return fail(SV_ERR_INVALID_ARG, "shared_prefix_len must be in [0, max_seq_len]");
-  const int64_t rows = (a->num_draft_tokens_total + a->num_reqs) * static_cast<int64_t>(a->num_q_heads);
-  if (rows > INT_MAX / 2) return fail(SV_ERR_UNSUPPORTED, "too many (token, query head) rows for one call");
-  return SV_OK;
-}
-
-sv::AttendParams attend_params(const spec_verify_t h, const spec_verify_attend_args *a) {
-  sv::AttendParams p{};
-  p.N = a->num_reqs;
-  p.G = a->max_spec_len;
-  p.Hq = a->num_q_heads;
-  p.group = a->num_q_heads / a->cache.num_kv_heads;
-  p.max_seq = a->max_seq_len;
-  p.prefix = a->shared_prefix_len;
-  p.T = a->num_draft_tokens_total;
-  p.cu = a->cu_num_draft_tokens;
-  p.c = a->cache;
-  p.q = static_cast<const uint16_t *>(a->q);
-  p.q_token = a->q_token_stride;
-  p.q_head = a->q_head_stride;
-  p.tables = a->block_tables;
-  // (what the tables hold bounds the lengths too; sizes alone, without a cache, know no tables)
-  if (a->cache.block_size > 0 && a->block_tables) {
-    const int64_t held = a->block_table_stride * static_cast<int64_t>(a->cache.block_size);
-    if (held < p.max_seq) p.max_seq = static_cast<int32_t>(held);
-  }
-  p.table_stride = a->block_table_stride;
-  p.seq_lens = a->seq_lens;
-  p.scale = a->scale;
-  p.expire = (a->test_flags & SV_TEST_EXPIRE_PRODUCT_WAIT) != 0;
-  p.out = static_cast<uint16_t *>(a->out);
-  p.out_token = a->out_token_stride;
-  p.out_head = a->out_head_stride;
-  p.lse = a->lse;
-  p.workspace = a->workspace;
-  p.status = a->status;
-  p.pdl = !(h->cfg.flags & SV_FLAG_SERIAL_LAUNCH);
-  return p;
-}
-
 sv_status run_kv(spec_verify_t h, const spec_verify_kv_args *a, void *stream, bool write) {
   if (!h) return fail(SV_ERR_INVALID_ARG, "handle is NULL");
   const sv_status st = spec_verify_check_kv_args(&h->cfg, a);
@@ -140,6 +87,101 @@ sv_status run_kv(spec_verify_t h, const spec_verify_kv_args *a, void *stream, bo
 }
 
 }  // namespace
+
+namespace sv {
+
+sv_status check_attend_sizes(const spec_verify_config *c, const spec_verify_attend_args *a) {
+  const sv_status st = check_layout(c, a->num_reqs, a->max_spec_len, a->num_draft_tokens_total,
+                                    a->cu_num_draft_tokens);
+  if (st != SV_OK) return st;
+  if (a->cache.num_kv_heads < 1 || a->num_q_heads < 1 || a->num_q_heads % a->cache.num_kv_heads)
+    return fail(SV_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
+  if (a->cache.head_dim != 64 && a->cache.head_dim != 128)
+    return fail(SV_ERR_UNSUPPORTED, "head_dim %d is not 64 or 128", a->cache.head_dim);
+  if (a->cache.num_kv_heads > 65535 || a->num_q_heads > 65535)
+    return fail(SV_ERR_UNSUPPORTED, "more than 65535 heads");
+  if (a->max_seq_len < 0) return fail(SV_ERR_INVALID_ARG, "max_seq_len < 0");
+  if (a->max_seq_len > (1 << 30)) return fail(SV_ERR_UNSUPPORTED, "max_seq_len %d > 2^30", a->max_seq_len);
+  if (a->shared_prefix_len < 0 || a->shared_prefix_len > a->max_seq_len)
+    return fail(SV_ERR_INVALID_ARG, "shared_prefix_len must be in [0, max_seq_len]");
+  const int64_t rows = (a->num_draft_tokens_total + a->num_reqs) * static_cast<int64_t>(a->num_q_heads);
+  if (rows > INT_MAX / 2) return fail(SV_ERR_UNSUPPORTED, "too many (token, query head) rows for one call");
+  return SV_OK;
+}
+
+AttendParams attend_params(const spec_verify_t h, const spec_verify_attend_args *a) {
+  AttendParams p{};
+  p.N = a->num_reqs;
+  p.G = a->max_spec_len;
+  p.Hq = a->num_q_heads;
+  p.group = a->num_q_heads / a->cache.num_kv_heads;
+  p.max_seq = a->max_seq_len;
+  p.prefix = a->shared_prefix_len;
+  p.T = a->num_draft_tokens_total;
+  p.cu = a->cu_num_draft_tokens;
+  p.c = a->cache;
+  p.q = static_cast<const uint16_t *>(a->q);
+  p.q_token = a->q_token_stride;
+  p.q_head = a->q_head_stride;
+  p.tables = a->block_tables;
+  // (what the tables hold bounds the lengths too; sizes alone, without a cache, know no tables)
+  if (a->cache.block_size > 0 && a->block_tables) {
+    const int64_t held = a->block_table_stride * static_cast<int64_t>(a->cache.block_size);
+    if (held < p.max_seq) p.max_seq = static_cast<int32_t>(held);
+  }
+  p.table_stride = a->block_table_stride;
+  p.seq_lens = a->seq_lens;
+  p.scale = a->scale;
+  p.expire = (a->test_flags & SV_TEST_EXPIRE_PRODUCT_WAIT) != 0;
+  p.out = static_cast<uint16_t *>(a->out);
+  p.out_token = a->out_token_stride;
+  p.out_head = a->out_head_stride;
+  p.lse = a->lse;
+  p.workspace = a->workspace;
+  p.status = a->status;
+  p.pdl = !(h->cfg.flags & SV_FLAG_SERIAL_LAUNCH);
+  return p;
+}
+
+// Of the arguments behind the sizes and the cache's description.
+sv_status check_attend_call(const spec_verify_attend_args *a) {
+  if (a->reserved) return fail(SV_ERR_INVALID_ARG, "reserved must be 0");
+  if (a->test_flags & ~SV_TEST_EXPIRE_PRODUCT_WAIT)
+    return fail(SV_ERR_INVALID_ARG, "unknown test_flags 0x%x", a->test_flags);
+  if (a->num_reqs == 0) return SV_OK;
+  const spec_verify_kv_cache &c8 = a->cache;
+  const double span = static_cast<double>(c8.num_blocks - 1) * c8.block_stride +
+                      static_cast<double>(c8.block_size - 1) * c8.token_stride;
+  if (span + static_cast<double>(c8.num_kv_heads - 1) * c8.head_stride >= 0x1p38 || span >= 0x1p32 * cache_unit(c8))
+    return fail(SV_ERR_UNSUPPORTED, "a side of the cache spans more than 256 GB, or 2^32 units of %u bytes",
+                cache_unit(c8));
+  if (a->shared_prefix_len % a->cache.block_size)
+    return fail(SV_ERR_INVALID_ARG, "shared_prefix_len must be a multiple of block_size");
+  if (a->block_table_stride < 0 ||
+      a->shared_prefix_len > a->block_table_stride * static_cast<int64_t>(a->cache.block_size))
+    return fail(SV_ERR_INVALID_ARG, "shared_prefix_len exceeds block_table_stride * block_size");
+  if (a->max_seq_len > 0 && !a->block_tables) return fail(SV_ERR_INVALID_ARG, "block_tables is NULL");
+  if (!a->seq_lens) return fail(SV_ERR_INVALID_ARG, "seq_lens is NULL");
+  if (!a->q || !a->out) return fail(SV_ERR_INVALID_ARG, "q or out is NULL");
+  if (a->q_token_stride < 0 || a->q_head_stride < 0 || a->out_token_stride < 0 || a->out_head_stride < 0)
+    return fail(SV_ERR_INVALID_ARG, "a q or out stride < 0");
+  if (!std::isfinite(a->scale)) return fail(SV_ERR_INVALID_ARG, "scale is not finite");
+  if (a->workspace_bytes < 0) return fail(SV_ERR_INVALID_ARG, "workspace_bytes < 0");
+  if (a->workspace && !aligned16(a->workspace)) return fail(SV_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  return SV_OK;
+}
+
+sv_status run_attend(spec_verify_t h, const AttendParams &p, int64_t workspace_bytes, void *stream) {
+  const int64_t need = attend_workspace_bytes(p, h->num_sms, false);
+  if (need > 0 && (!p.workspace || workspace_bytes < need))
+    return fail(SV_ERR_CAPACITY, "workspace of %lld bytes, the call needs %lld", static_cast<long long>(workspace_bytes),
+                static_cast<long long>(need));
+  const cudaError_t e = launch_attend(p, h->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SV_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+  return SV_OK;
+}
+
+}  // namespace sv
 
 extern "C" {
 
@@ -177,32 +219,9 @@ sv_status spec_verify_check_attend_args(const spec_verify_config *c, const spec_
   sv_status st = sv::check_config(c);
   if (st != SV_OK) return st;
   if (!a) return fail(SV_ERR_INVALID_ARG, "args is NULL");
-  if ((st = check_attend_sizes(c, a)) != SV_OK) return st;
-  if (a->reserved) return fail(SV_ERR_INVALID_ARG, "reserved must be 0");
-  if (a->test_flags & ~SV_TEST_EXPIRE_PRODUCT_WAIT)
-    return fail(SV_ERR_INVALID_ARG, "unknown test_flags 0x%x", a->test_flags);
-  if (a->num_reqs == 0) return SV_OK;
-  if ((st = check_cache(a->cache)) != SV_OK) return st;
-  const spec_verify_kv_cache &c8 = a->cache;
-  const double span = static_cast<double>(c8.num_blocks - 1) * c8.block_stride +
-                      static_cast<double>(c8.block_size - 1) * c8.token_stride;
-  if (span + static_cast<double>(c8.num_kv_heads - 1) * c8.head_stride >= 0x1p38 || span >= 0x1p32 * sv::cache_unit(c8))
-    return fail(SV_ERR_UNSUPPORTED, "a side of the cache spans more than 256 GB, or 2^32 units of %u bytes",
-                sv::cache_unit(c8));
-  if (a->shared_prefix_len % a->cache.block_size)
-    return fail(SV_ERR_INVALID_ARG, "shared_prefix_len must be a multiple of block_size");
-  if (a->block_table_stride < 0 ||
-      a->shared_prefix_len > a->block_table_stride * static_cast<int64_t>(a->cache.block_size))
-    return fail(SV_ERR_INVALID_ARG, "shared_prefix_len exceeds block_table_stride * block_size");
-  if (a->max_seq_len > 0 && !a->block_tables) return fail(SV_ERR_INVALID_ARG, "block_tables is NULL");
-  if (!a->seq_lens) return fail(SV_ERR_INVALID_ARG, "seq_lens is NULL");
-  if (!a->q || !a->out) return fail(SV_ERR_INVALID_ARG, "q or out is NULL");
-  if (a->q_token_stride < 0 || a->q_head_stride < 0 || a->out_token_stride < 0 || a->out_head_stride < 0)
-    return fail(SV_ERR_INVALID_ARG, "a q or out stride < 0");
-  if (!std::isfinite(a->scale)) return fail(SV_ERR_INVALID_ARG, "scale is not finite");
-  if (a->workspace_bytes < 0) return fail(SV_ERR_INVALID_ARG, "workspace_bytes < 0");
-  if (a->workspace && !aligned16(a->workspace)) return fail(SV_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
-  return SV_OK;
+  if ((st = sv::check_attend_sizes(c, a)) != SV_OK) return st;
+  if (a->num_reqs > 0 && (st = check_cache(a->cache)) != SV_OK) return st;
+  return sv::check_attend_call(a);
 }
 
 sv_status spec_verify_attend_workspace_size(spec_verify_t h, const spec_verify_attend_args *a, int64_t *bytes) {
@@ -212,9 +231,9 @@ sv_status spec_verify_attend_workspace_size(spec_verify_t h, const spec_verify_a
   spec_verify_attend_args b = *a;
   static const int32_t any = 0;
   b.cu_num_draft_tokens = &any;
-  const sv_status st = check_attend_sizes(&h->cfg, &b);
+  const sv_status st = sv::check_attend_sizes(&h->cfg, &b);
   if (st != SV_OK) return st;
-  *bytes = a->num_reqs == 0 ? 0 : sv::attend_workspace_bytes(attend_params(h, a), h->num_sms, true);
+  *bytes = a->num_reqs == 0 ? 0 : sv::attend_workspace_bytes(sv::attend_params(h, a), h->num_sms, true);
   return SV_OK;
 }
 
@@ -223,14 +242,7 @@ sv_status spec_verify_attend(spec_verify_t h, const spec_verify_attend_args *a, 
   const sv_status st = spec_verify_check_attend_args(&h->cfg, a);
   if (st != SV_OK) return st;
   if (a->num_reqs == 0) return SV_OK;
-  const sv::AttendParams p = attend_params(h, a);
-  const int64_t need = sv::attend_workspace_bytes(p, h->num_sms, false);
-  if (need > 0 && (!a->workspace || a->workspace_bytes < need))
-    return fail(SV_ERR_CAPACITY, "workspace of %lld bytes, the call needs %lld", static_cast<long long>(a->workspace_bytes),
-                static_cast<long long>(need));
-  const cudaError_t e = sv::launch_attend(p, h->num_sms, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return fail(SV_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
-  return SV_OK;
+  return sv::run_attend(h, sv::attend_params(h, a), a->workspace_bytes, stream);
 }
 
 sv_status spec_verify_check_logprobs_args(const spec_verify_config *c, const spec_verify_logprobs_args *a) {
