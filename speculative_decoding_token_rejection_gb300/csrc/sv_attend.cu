@@ -671,7 +671,7 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
 // 512 x 1, 256 118 | 95, 512 120 | 126; 2 x 5 (40 rows), 4096 33 | 29, 16384 48 | 38;
 // 16 x 1 (64 rows), 256 17 | 17, 1024 19 | 22.
 bool four_bits(const AttendParams &p) { return p.c.format == SV_CACHE_E2M1 || p.c.format == SV_CACHE_INT4; }
-int own_rows(const AttendParams &p) { return four_bits(p) ? kOwnRows4 : 8 * kGroups; }
+int own_rows(const AttendParams &p) { return four_bits(p) ? own4_rows(p) : 8 * kGroups; }
 
 AttendParams short_prefix(AttendParams p) {
   const int64_t H = p.c.num_kv_heads, own = (p.G + 1) * static_cast<int64_t>(p.group), own_tiles = ceil_div(own, 8 * kGroups);

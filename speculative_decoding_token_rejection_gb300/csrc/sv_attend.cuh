@@ -252,8 +252,10 @@ __device__ __forceinline__ bool own_tile(const AttendParams &P, const AttendPlan
   return T.k_end > T.k_begin || (T.whole && T.split == 0);
 }
 
-// The private part over the 4-bit cache (sv_attend4.cu): tiles of kOwnRows4 rows.
+// The private part over the 4-bit cache (sv_attend4.cu): tiles of at most kOwnRows4 rows, or of half as many where every
+// request's rows fit.
 constexpr int kOwnRows4 = 64;
+inline int own4_rows(const AttendParams &p) { return (p.G + 1) * static_cast<int64_t>(p.group) <= kOwnRows4 / 2 ? kOwnRows4 / 2 : kOwnRows4; }
 cudaError_t enable_own4_kernels();
 cudaError_t launch_own4(const AttendParams &p, const AttendPlan &L, cudaStream_t stream);
 

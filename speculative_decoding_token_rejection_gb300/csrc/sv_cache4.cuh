@@ -41,10 +41,10 @@ __device__ __forceinline__ void e2m1_word_to_f16(uint32_t w, uint32_t r[4]) {
       : "r"(w));
 }
 
-// What a group's scale (an e4m3 byte) gives the products: for E2M1 the scale
-// twice; for whole numbers a = g / 16 and b = -1032 a.
+// What a group's scale (an e4m3 byte) gives the products, twice each: for E2M1 the
+// scale; for whole numbers a = g / 16, b = -1032 a, c = a / 16 and d = -72 a.
 struct GroupFactors {
-  uint32_t a, b;
+  uint32_t a, b, c, d;
 };
 template <int FMT>
 __device__ __forceinline__ GroupFactors group_factors(uint32_t g) {
@@ -52,6 +52,8 @@ __device__ __forceinline__ GroupFactors group_factors(uint32_t g) {
   const uint32_t both = e4m3x2_to_f16x2(static_cast<uint16_t>(g | g << 8));
   f.a = FMT == SV_CACHE_INT4 ? hmul2(both, 0x2C002C00u) : both;   // (1/16)
   f.b = FMT == SV_CACHE_INT4 ? hmul2(f.a, 0xE408E408u) : 0u;      // (-1032)
+  f.c = FMT == SV_CACHE_INT4 ? hmul2(f.a, 0x2C002C00u) : 0u;
+  f.d = FMT == SV_CACHE_INT4 ? hmul2(f.a, 0xD480D480u) : 0u;      // (-72)
   return f;
 }
 
@@ -75,6 +77,31 @@ __device__ __forceinline__ void group_to_f16(uint2 w, GroupFactors f, uint32_t r
     e2m1_word_to_f16(w.y, r + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = hmul2(r[i], f.a);
+  }
+}
+
+// The same with the pairs that take the fewest instructions.  Whole numbers: (0,
+// 4), (1, 5), (2, 6), (3, 7) of every eight; a nibble in the second place of a
+// byte is 16 x + 1152 in the mantissa of 1024, which c and d undo.
+template <int FMT>
+__host__ __device__ constexpr bool mixed() {
+  return FMT == SV_CACHE_INT4;
+}
+// The element at place `at` of that order.
+__device__ __forceinline__ int mixed_place(int at) { return (at & ~7) | (at >> 1 & 3) | (at & 1) << 2; }
+template <int FMT>
+__device__ __forceinline__ void group_to_f16_mixed(uint2 w, GroupFactors f, uint32_t r[8]) {
+  if (FMT == SV_CACHE_INT4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t u = i ? w.y : w.x, v = u >> 8;
+      r[4 * i] = hfma2((u & 0x000F000Fu) ^ 0x64086408u, f.a, f.b);
+      r[4 * i + 1] = hfma2((u & 0x00F000F0u) ^ 0x64806480u, f.c, f.d);
+      r[4 * i + 2] = hfma2((v & 0x000F000Fu) ^ 0x64086408u, f.a, f.b);
+      r[4 * i + 3] = hfma2((v & 0x00F000F0u) ^ 0x64806480u, f.c, f.d);
+    }
+  } else {
+    group_to_f16<FMT>(w, f, r);
   }
 }
 

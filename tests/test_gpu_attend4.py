@@ -7,8 +7,8 @@ there.  A score is a sum of D exact products in fp32, off by at most e = 2^-24 *
 (D + 32) * max_k scale * sum_d |q_d k_d|; weights are off by 2 e relative, plus
 2^-20 for the exponential and the sums, and rounded to 11 bits before they meet
 the values; the bf16 output adds half a step.  A weight that underflows 16 bits
-loses 2^-25 of the largest product of a weight and its value's scale, times the
-value's number without that scale.  |lse - exact| <= e + 2^-20 * (1 + |exact|)."""
+loses 2^-25 of the largest product of a weight and its value's scale (a scale's
+size enters the exponent as 2^-64 at least), times the value's number without it.  |lse - exact| <= e + 2^-20 * (1 + |exact|)."""
 import math
 
 import pytest
@@ -125,7 +125,7 @@ def reference(c):
             p = torch.exp(a - torch.where(torch.isinf(z), torch.zeros_like(z), z)[..., None])
             o, e = torch.matmul(p, v), 2.0 ** -24 * (d + 32) * big
             w = (2 * e + 2.0 ** -20 + 2.0 ** -11)[..., None] * torch.matmul(p, v.abs()) + 2.0 ** -8 * o.abs()
-            most = (p * vs.abs()[:, None, :]).amax(-1, keepdim=True)
+            most = (p * vs.abs().clamp_min(2.0 ** -64)[:, None, :]).amax(-1, keepdim=True)
             w = w + 2.0 ** -25 * most * torch.matmul((a > -math.inf).double(), vn.abs())
             y = e + 2.0 ** -20 * (1 + torch.where(torch.isinf(z), torch.zeros_like(z), z).abs())
             for dst, src in ((out, o), (tol, w)):
