@@ -521,7 +521,8 @@ sv_status spec_verify_check_kv4_args(const spec_verify_config *config, const spe
 /* Attention of the verify tokens over the 4-bit cache: layout, masks, errors
  * and outputs are those of spec_verify_attend.  Group scales are numbers, as
  * spec_verify_kv4_write leaves them (those of keys at or behind seq_len may be
- * anything); the rows' scales may be any floats, as there.  A nibble times its
+ * anything); the rows' scales may be any floats, as there.  Strides between
+ * pages and between tokens are below 4 GB.  A nibble times its
  * group scale is exact in the 16-bit products' operands, so what that call
  * rounds to fewer bits is what this one does. */
 typedef struct spec_verify_attend4_args {

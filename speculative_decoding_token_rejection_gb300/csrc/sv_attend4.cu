@@ -5,18 +5,18 @@
 // HBM (152 bytes a key for head_dim 128) as long as unpacking a key costs little
 // and is done once for all of its rows.  Both products are transposed, keys and
 // dimensions on the 128-wide side of the instruction, the few rows on the narrow
-// one: S^T [keys x rows] = K Q^T and O^T [dims x rows] += V^T P^T.  A thread takes
+// one: S^T [keys x rows] = K Q^T and O^T [dims x rows] += V^T P^T.  Two threads take
 // a key, from its bytes to its weights:
 //
 //   K row    global -> registers -> f16 -> tensor memory (A of the first product)
 //   V row    global -> registers -> f16 -> shared memory (A of the second, which
 //            wants dimensions outside: 64 of them a 128-byte line per key)
-//   scores   tensor memory -> registers: all rows of the thread's key
+//   scores   tensor memory -> registers: half of the rows each
 //   weights  registers -> shared memory (B of the second product)
 //
-// so no byte is exchanged between threads, and one thread issues the products,
-// which run while all unpack: V during the first, the next tile's K during the
-// second.  A tile is 128 keys, its bytes are loaded a tile ahead.
+// so no byte is exchanged between threads.  Warps 0-3 unpack K, warps 4-7 V; one
+// thread of either issues the products that wait for it.  A tile is 128 keys, its
+// bytes are loaded a tile ahead.
 //
 // Numbers, as in the kernel for the shared prefix: x = (q . n) * (scale * log2 e *
 // key_scale), w = 2^(x - m), l = sum w, P = w * value_scale / W, O = W * sum P n_v.
@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "sv_attend.cuh"
 #include "sv_cache4.cuh"
@@ -37,7 +38,7 @@
 namespace sv {
 namespace {
 
-constexpr int kOwnThreads = 128, kOwnKeys = 128;  // a thread a key
+constexpr int kOwnKeys = 128, kOwnThreads = 2 * kOwnKeys;  // two threads a key
 constexpr float kRaise = 8;
 constexpr float kScaleUnit = 0x1p28f;           // W
 constexpr float kLeastUnits = kLeastLog2 - 28;  // log2 of the size that a scale counts as at least, in W
@@ -47,12 +48,13 @@ struct OwnControl {
   uint32_t tmem, abort;
   uint32_t huge;                       // some |m| is so large that its two parts are subtracted one after the other
   alignas(16) float neg[kOwnRows4];    // negated m, 0 without one
+  alignas(16) float zero[kOwnRows4];
   alignas(16) float negx[kOwnRows4], negu[kOwnRows4];  // its parts, negated
   alignas(16) float back[kOwnRows4];   // what undoes a row's power of two
   alignas(16) int limit[kOwnRows4];    // keys that the row sees are below it
   alignas(16) float factor[kOwnRows4]; // of a raised maximum; at the end, of the outputs
   float mx[kOwnRows4], mu[kOwnRows4];  // m = mx + mu, mx -inf without one
-  float part[kOwnThreads / 32][kOwnRows4];
+  float part[4][kOwnRows4];            // of the four warps that hold a row
   uint32_t none[kOwnRows4];            // the row sees a value scale that is no number
 };
 
@@ -66,30 +68,8 @@ struct OwnSmem {
 };
 __device__ __forceinline__ int line_at(int line, int col) { return line * 128 + ((col ^ (line & 7)) << 4); }
 
-__device__ __forceinline__ void tmem_store_row(uint32_t addr, const uint32_t r[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
-      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
-      "};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 // Sixteen columns of the thread's lane.
-__device__ __forceinline__ void tmem_load_row(uint32_t addr, uint32_t r[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
-      "}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_store_16(uint32_t addr, const uint32_t r[16]) {
+__device__ __forceinline__ void tmem_store_row(uint32_t addr, const uint32_t r[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
       "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
@@ -98,6 +78,32 @@ __device__ __forceinline__ void tmem_store_16(uint32_t addr, const uint32_t r[16
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// Eight columns of the thread's lane.
+__device__ __forceinline__ void tmem_load_row(uint32_t addr, float r[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(addr)
+               : "memory");
+}
+// Waits for every load so far; the registers go through, so no use of them moves ahead of the wait.
+__device__ __forceinline__ void tmem_wait_row(float r[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store_8(uint32_t addr, const float r[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "f"(r[0]),
+               "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// A barrier of the warps that unpack the keys.
+__device__ __forceinline__ void sync_keys() { asm volatile("bar.sync 1, %0;" ::"n"(kOwnKeys) : "memory"); }
 
 // Eight values of every lane combined over the warp, in nine exchanges: lane 4i
 // gets that of value i.
@@ -115,41 +121,36 @@ __device__ __forceinline__ float reduce_eight(float v[8], int lane) {
   return both(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
 }
 
-// A cache row on its way: nibbles, group scales, the row's scale.
+// A cache row on its way: nibbles and group scales.
 template <int D>
 struct RawRow {
   uint32_t w[D / 8], g[D / 64];
-  float scale;
 };
+// (Volatile: they stay where they are written, a tile ahead of their use.)
+__device__ __forceinline__ uint32_t load_word(const void *p) {
+  uint32_t r;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
 template <int D>
-__device__ __forceinline__ void load_row(RawRow<D> &r, const uint8_t *data, const uint8_t *group, const float *scale) {
+__device__ __forceinline__ void load_row(RawRow<D> &r, const uint8_t *data, const uint8_t *group) {
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) ld_stream_32(data + 32 * i, r.w + 8 * i);
-  if (D == 128) {
-    const uint2 g = __ldg(reinterpret_cast<const uint2 *>(group));
-    r.g[0] = g.x;
-    r.g[D / 64 - 1] = g.y;
-  } else {
-    r.g[0] = __ldg(reinterpret_cast<const uint32_t *>(group));
-  }
-  r.scale = __ldg(scale);
+  if (D == 128)
+    asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(r.g[0]), "=r"(r.g[D / 64 - 1]) : "l"(group));
+  else
+    r.g[0] = load_word(group);
 }
-template <int D>
-__device__ __forceinline__ void zero_row(RawRow<D> &r) {
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) r.w[i] = 0;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) r.g[i] = 0;
-  r.scale = 0.0f;
-}
-// Group j of a row as f16 pairs, in the order of mixed_place.
-template <int D, int FMT>
-__device__ __forceinline__ void unpack_group(const RawRow<D> &r, int j, uint32_t h[8]) {
-  group_to_f16_mixed<FMT>(make_uint2(r.w[2 * j], r.w[2 * j + 1]), group_factors<FMT>(r.g[j >> 2] >> (8 * (j & 3)) & 0xFFu), h);
+// p + a * x + b * y
+__device__ __forceinline__ const uint8_t *step(const void *p, uint32_t a, uint32_t x, uint32_t b, uint32_t y) {
+  uint64_t r;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(a), "r"(x), "l"(p));
+  asm("mad.wide.u32 %0, %1, %2, %0;" : "+l"(r) : "r"(b), "r"(y));
+  return reinterpret_cast<const uint8_t *>(r);
 }
 
 template <int D, int FMT, int NMAX>
-__global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
+__global__ void __launch_bounds__(kOwnThreads, 2)
     own4_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ AttendPlan L) {
   pdl_enter();
   OwnTile T;
@@ -159,49 +160,53 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
   using Y = OwnSmem<D, NMAX>;
   OwnControl &C = *reinterpret_cast<OwnControl *>(smem + Y::kControl);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int mine = tid & (kOwnKeys - 1), side = tid / kOwnKeys;  // the thread's key of a tile; 0: its K row, 1: its V row
   constexpr uint32_t kS = 64, kO = 64 + NMAX, kCols = NMAX <= 32 ? 128 : 256;  // columns of tensor memory: K, S, O
-  const int n16 = (T.rows + 15) / 16, n8 = (T.rows + 7) / 8;
+  constexpr int kHalf = NMAX / 2;                                              // rows of a side at most
+  const int n8 = (T.rows + 7) / 8, n16 = (T.rows + 15) / 16;
+  const int row0 = side * ((n8 + 1) / 2) * 8, mine8 = side ? n8 / 2 : (n8 + 1) / 2;  // the side's rows, in eights
 
   // ---- the first tile's bytes are on their way before anything else ----
   const int ntiles = (max(0, T.k_end - T.k_begin) + kOwnKeys - 1) / kOwnKeys;
   const int32_t *const table = P.tables + T.i * P.table_stride;
-  const uint8_t *const kdata = static_cast<const uint8_t *>(P.c.k) + T.h * P.c.head_stride;
-  const uint8_t *const vdata = static_cast<const uint8_t *>(P.c.v) + T.h * P.c.head_stride;
-  const uint8_t *const kgroup = P.k_group + T.h * P.group_head, *const vgroup = P.v_group + T.h * P.group_head;
-  const float *const kscale = P.c.k_scale + T.h * P.c.scale_head_stride;
-  const float *const vscale = P.c.v_scale + T.h * P.c.scale_head_stride;
-  uint32_t bits = 0;
+  bool bad = false;  // some page was outside the cache
+  // (Nothing here is loaded under a condition: registers that a branch fills otherwise would be waited for at its end.  A
+  // key that is not there takes a place that is, and counts for nothing later.)
   auto page_of = [&](int it) {  // of the thread's key of tile `it`
-    const int k = T.k_begin + it * kOwnKeys + tid;
-    return k < T.k_end ? (k < P.row0 ? P.tables : table)[div_by(k, L.page)] : -1;
+    const int k = max(T.k_begin, min(T.k_begin + it * kOwnKeys + mine, T.k_end - 1));
+    return static_cast<int>(load_word((k < P.row0 ? P.tables : table) + div_by(k, L.page)));
   };
-  RawRow<D> kraw, vraw;
-  int64_t at_data = 0, at_group = 0, at_scale = 0;
-  bool live = false;  // of the key whose bytes are in kraw and vraw (or on their way)
-  auto place = [&](int it, int page) {
-    const int k = T.k_begin + it * kOwnKeys + tid, off = k - div_by(k, L.page) * P.c.block_size;
-    live = k < T.k_end && page >= 0 && page < P.c.num_blocks;
-    if (k < T.k_end && !live) bits = SV_DATA_BAD_SLOT;
-    at_data = page * P.c.block_stride + off * P.c.token_stride;
-    at_group = page * P.group_block + off * P.group_token;
-    at_scale = page * P.c.scale_block_stride + off * P.c.scale_token_stride;
+  RawRow<D> row;
+  uint32_t ks = 0, vs = 0;
+  bool live = false;  // of the key whose bytes are in `row` (or on their way)
+  // (either side's addresses are the warp's own: kept apart, they take no registers of the threads)
+  auto load = [&](auto values, int it, int page) {
+    const int k = T.k_begin + it * kOwnKeys + mine;
+    const bool in = k < T.k_end;
+    live = in && static_cast<uint32_t>(page) < static_cast<uint32_t>(P.c.num_blocks);
+    bad |= in && !live;
+    const uint32_t p = live ? page : 0, off = live ? k - div_by(k, L.page) * P.c.block_size : 0;
+    load_row<D>(row,
+                step(static_cast<const uint8_t *>(values.value ? P.c.v : P.c.k) + T.h * P.c.head_stride,
+                     static_cast<uint32_t>(P.c.block_stride), p, static_cast<uint32_t>(P.c.token_stride), off),
+                step((values.value ? P.v_group : P.k_group) + T.h * P.group_head, static_cast<uint32_t>(P.group_block), p,
+                     static_cast<uint32_t>(P.group_token), off));
+    const uint32_t scale_page = static_cast<uint32_t>(P.c.scale_block_stride * 4),
+                   scale_token = static_cast<uint32_t>(P.c.scale_token_stride * 4);
+    ks = load_word(step(P.c.k_scale + T.h * P.c.scale_head_stride, scale_page, p, scale_token, off));
+    vs = load_word(step(P.c.v_scale + T.h * P.c.scale_head_stride, scale_page, p, scale_token, off));
   };
-  auto load_keys = [&]() {
-    if (live)
-      load_row<D>(kraw, kdata + at_data, kgroup + at_group, kscale + at_scale);
+  constexpr std::false_type keys{};
+  constexpr std::true_type values{};
+  int page = 0;
+  if (ntiles > 0) {
+    page = page_of(0);
+    if (side == 0)
+      load(keys, 0, page);
     else
-      zero_row<D>(kraw);
-  };
-  auto load_values = [&]() {
-    if (live)
-      load_row<D>(vraw, vdata + at_data, vgroup + at_group, vscale + at_scale);
-    else
-      zero_row<D>(vraw);
-  };
-  place(0, page_of(0));
-  load_keys();
-  load_values();
-  int page = page_of(1);
+      load(values, 0, page);
+    page = page_of(1);
+  }
 
   if (tid == 0) {
     mbar_init(&C.s_full, 1);
@@ -213,14 +218,14 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
   if (tid < kOwnRows4) {
     const int j = div_by(T.r0 + tid, L.group);
     C.limit[tid] = tid < T.rows ? T.len - T.gam + j : 0x7FFFFFFF;
-    C.neg[tid] = C.negx[tid] = C.negu[tid] = C.mu[tid] = 0.0f;
+    C.zero[tid] = C.neg[tid] = C.negx[tid] = C.negu[tid] = C.mu[tid] = 0.0f;
     C.mx[tid] = -INFINITY;
     C.none[tid] = 0;
   }
   // ---- the queries: f16, each row with its own power of two, dimensions in the order of the unpacked keys ----
   bool shifted = false;
   {
-    constexpr int kCh = D / 8, kRowsPass = kOwnThreads / kCh, kPass = NMAX / kRowsPass;
+    constexpr int kCh = D / 8, kRowsPass = kOwnThreads / kCh, kPass = (NMAX + kRowsPass - 1) / kRowsPass;
     const int col = tid % kCh;
     uint4 x[kPass];
 #pragma unroll
@@ -250,7 +255,6 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
       for (int b = kCh / 2; b; b >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, b));
       const int shift = query_shift(top);
       shifted |= shift != 0;
-      if (col == 0) C.back[r] = pow2(-shift);
       const float up = pow2(shift);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -263,8 +267,11 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
         w[2] = c;
         w[3] = d;
       }
-      *reinterpret_cast<uint4 *>(smem + Y::kQ + (col >> 3) * (NMAX * 128) + line_at(r, col & 7)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      if (r < NMAX) {
+        if (col == 0) C.back[r] = pow2(-shift);
+        *reinterpret_cast<uint4 *>(smem + Y::kQ + (col >> 3) * (NMAX * 128) + line_at(r, col & 7)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
   }
   fence_proxy_async_smem();
@@ -275,148 +282,146 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
   for (int r = lane; r < T.rows; r += 32) low = min(low, C.limit[r]);
   low = __reduce_min_sync(0xFFFFFFFFu, low);
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, C.tmem, 0), base = smem_addr(smem);
-  const uint32_t mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);  // the warp's lanes
-  const bool leader = warp == 0 && elected();
-  const uint32_t scores = product(n16 * 16, false), outputs = product(n16 * 16, true, D, true);
-  const uint64_t queries = operand(base + Y::kQ, 16), values = operand(base + Y::kV, Y::kLines),
-                 weights = operand(base + Y::kP, Y::kLines);
-
-  float l[NMAX];  // sums over the thread's keys
+  const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // the warp's part of tensor memory
+  const bool leader = elected();
+  float l[kHalf];  // sums over the thread's keys
 #pragma unroll
-  for (int r = 0; r < NMAX; ++r) l[r] = 0.0f;
+  for (int r = 0; r < kHalf; ++r) l[r] = 0.0f;
   const float c_all = P.scale * unit4<FMT>() * kLog2e;
   bool force = true;  // some row has no maximum
   bool ok = true;
   int it = 0;
   for (; it < ntiles; ++it) {
-    // ---- the tile's keys to tensor memory; scores ----
-    const float kc = kraw.scale * c_all;
+    // ---- the tile's keys to tensor memory, its values to shared memory ----
     const bool dead = !live;
-    const int key = T.k_begin + it * kOwnKeys + tid;
+    const float kc = __uint_as_float(ks) * c_all, v_scale = dead ? 0.0f : __uint_as_float(vs);
 #pragma unroll
-    for (int half = 0; half < D / 64; ++half) {
-      uint32_t h[32];
+    for (int i = 0; i < D / 64; ++i) row.g[i] = dead ? 0u : row.g[i];  // (zeros)
+    const int key = T.k_begin + it * kOwnKeys + mine;
+    if (side == 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) unpack_group<D, FMT>(kraw, half * 4 + j, h + 8 * j);
-      tmem_store_row(mine + half * 32, h);
-    }
-    tmem_wait_store();
-    fence_before();
-    __syncthreads();
-    if (leader) {
-      fence_after();
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t b = queries + static_cast<uint64_t>((kk >> 2) * (NMAX * 128 >> 4) + (kk & 3) * 2);
-        if (kk == 0)
-          mma_ts<false>(tmem + kS, tmem, b, scores);
-        else
-          mma_ts<true>(tmem + kS, tmem + kk * 8, b, scores);
+      for (int two = 0; two < D / 32; ++two) {
+        uint32_t h[16];
+        groups_to_f16_mixed<FMT>(row.w + 4 * two, row.g[two >> 1] >> (16 * (two & 1)), h);
+        tmem_store_row(lanes + two * 16, h);
       }
-      mma_commit(&C.s_full);
-    }
-    __syncwarp();
-    const bool more = it + 1 < ntiles;
-    // (vraw is still this tile's: its place is taken over below)
-    const float vs = vraw.scale;
-    if (more) place(it + 1, page);
-    if (more) load_keys();
-    page = page_of(it + 2);
-    // ---- the values to shared memory, once the products of the tile before are done with it ----
-    if (it > 0) ok = wait(C, &C.o_full, (it - 1) & 1);
+      if (it + 1 < ntiles) load(keys, it + 1, page);
+      tmem_wait_store();
+      fence_before();
+      sync_keys();
+      if (warp == 0) {
+        fence_after();
+        const uint64_t q_operand = operand(base + Y::kQ, 16);
+        const uint32_t score_shape = product(n16 * 16, false);
+        if (leader) {
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      uint32_t h[8];
-      unpack_group<D, FMT>(vraw, j, h);
-      uint8_t *const dst = smem + Y::kV + (j >> 2) * Y::kLines;
-      *reinterpret_cast<uint4 *>(dst + line_at(tid, (2 * j) & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4 *>(dst + line_at(tid, (2 * j + 1) & 7)) = make_uint4(h[4], h[5], h[6], h[7]);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t b = q_operand + static_cast<uint64_t>((kk >> 2) * (NMAX * 128 >> 4) + (kk & 3) * 2);
+            if (kk == 0)
+              mma_ts<false>(tmem + kS, tmem, b, score_shape);
+            else
+              mma_ts<true>(tmem + kS, tmem + kk * 8, b, score_shape);
+          }
+          mma_commit(&C.s_full);
+        }
+      }
+      __syncwarp();
+    } else {
+      if (it > 0) ok = wait(C, &C.o_full, (it - 1) & 1) && ok;  // (the products of the tile before are done with them)
+      const uint32_t line = base + Y::kV + mine * 128 + ((mine & 7) << 4);
+#pragma unroll
+      for (int two = 0; two < D / 32; ++two) {
+        uint32_t h[16];
+        groups_to_f16_mixed<FMT>(row.w + 4 * two, row.g[two >> 1] >> (16 * (two & 1)), h);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((line ^ ((two & 1) * 64 + c * 16)) + (two >> 1) * Y::kLines),
+                       "r"(h[4 * c]), "r"(h[4 * c + 1]), "r"(h[4 * c + 2]), "r"(h[4 * c + 3])
+                       : "memory");
+      }
+      if (it + 1 < ntiles) load(values, it + 1, page);
     }
-    if (more) load_values();
-    // ---- weights ----
-    const bool number = fabsf(vs) < INFINITY;
-    const float vr = number && fabsf(vs) >= kLeastScale ? vs * (1.0f / kScaleUnit) : 0.0f;
+    page = page_of(it + 2);
+    // ---- weights: half of the rows for either thread of a key ----
+    const bool number = fabsf(v_scale) < INFINITY;
+    const float vr = number && fabsf(v_scale) >= kLeastScale ? v_scale * (1.0f / kScaleUnit) : 0.0f;
     const float lv = fmaxf(__log2f(fabsf(vr)), kLeastUnits);
     const bool cut = T.k_begin + (it + 1) * kOwnKeys > low || __any_sync(0xFFFFFFFFu, dead);
-    if (!number) {
+    if (side == 0 && !number) {
       for (int r = 0; r < T.rows; ++r)
         if (key < C.limit[r]) C.none[r] = 1;
     }
-    float x[NMAX];
-    auto load_scores = [&]() {  // a product of its own, rounded: subtracting a maximum that equals it gives 0
+    // Two eights of the side's rows at a time: columns 16 g .. of its part of S (the first eight again where there is one).
+    auto load_scores = [&](int g, float x[16]) {
+      const uint32_t at = lanes + kS + row0 + g * 16;
+      tmem_load_row(at, x);
+      tmem_load_row(2 * g + 1 < mine8 ? at + 8 : at, x + 8);
+      tmem_wait_row(x);
+      tmem_wait_row(x + 8);
+    };
+    // Scores in base 2, -inf where the row does not see the key.  (A product of its own, rounded: subtracting a maximum
+    // that equals it gives 0.)
+    auto exact_scores = [&](int g, float x[16]) {
+      load_scores(g, x);
 #pragma unroll
-      for (int c = 0; c < NMAX / 16; ++c)
-        if (c < n16) tmem_load_row(mine + kS + c * 16, reinterpret_cast<uint32_t *>(x) + c * 16);
+      for (int e = 0; e < 16; ++e) {
+        const int r = row0 + g * 16 + e;
+        const float y = x[e] * kc * C.back[r];
+        x[e] = dead || key >= C.limit[r] ? -INFINITY : y;
+      }
+    };
+    // x * by - m of the side's rows 16 g ..
+    auto exponents = [&](int g, float x[16], float by, const float *neg) {
+      load_scores(g, x);
 #pragma unroll
-      for (int c = 0; c < NMAX / 16; ++c)
-        if (c < n16) tmem_wait_load(reinterpret_cast<uint32_t *>(x) + c * 16);
-#pragma unroll
-      for (int c = 0; c < NMAX / 8; ++c)
-        if (c < n8) {
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const Pair y = mul2(pair(x[c * 8 + e], x[c * 8 + e + 1]), pair(kc, kc));
-            x[c * 8 + e] = lo(y);
-            x[c * 8 + e + 1] = hi(y);
-          }
-          if (shifted) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[c * 8 + e] *= C.back[c * 8 + e];
-          }
-          if (cut) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (dead || key >= C.limit[c * 8 + e]) x[c * 8 + e] = -INFINITY;
-          }
-        }
+      for (int e = 0; e < 16; e += 4) {
+        const float4 m = *reinterpret_cast<const float4 *>(neg + row0 + g * 16 + e);
+        const Pair a = fma2(pair(x[e], x[e + 1]), pair(by, by), pair(m.x, m.y));
+        const Pair b = fma2(pair(x[e + 2], x[e + 3]), pair(by, by), pair(m.z, m.w));
+        x[e] = lo(a);
+        x[e + 1] = hi(a);
+        x[e + 2] = lo(b);
+        x[e + 3] = hi(b);
+      }
     };
     ok = wait(C, &C.s_full, it & 1, P.expire) && ok;
     fence_after();
-    load_scores();
-    auto subtract = [&]() {
-      float top = -INFINITY;
-      if (C.huge) {
+    // Most tiles: every row sees all keys, needs no power of two and has an m that holds, below 2^20 in size.  One fused
+    // operation an exponent then (its exact product differs from a rounded one by less than 2^-4).
+    const bool general = cut || shifted || C.huge;
+    float top = -INFINITY;
+    if (!general) {
+#pragma unroll 1
+      for (int g = 0; 2 * g < mine8; ++g) {
+        float x[16];
+        exponents(g, x, kc, C.neg);
 #pragma unroll
-        for (int c = 0; c < NMAX / 8; ++c)
-          if (c < n8) {
+        for (int e = 0; e < 8; e += 2) top = max3(top, x[e], x[e + 1]);
+        if (2 * g + 1 < mine8) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[c * 8 + e] = x[c * 8 + e] + C.negx[c * 8 + e];
-          }
-      }
-      const float *const last = C.huge ? C.negu : C.neg;
-#pragma unroll
-      for (int c = 0; c < NMAX / 8; ++c)
-        if (c < n8) {
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const float4 m = *reinterpret_cast<const float4 *>(last + c * 8 + e);
-            const Pair a = add2(pair(x[c * 8 + e], x[c * 8 + e + 1]), pair(m.x, m.y));
-            const Pair b = add2(pair(x[c * 8 + e + 2], x[c * 8 + e + 3]), pair(m.z, m.w));
-            x[c * 8 + e] = lo(a);
-            x[c * 8 + e + 1] = hi(a);
-            x[c * 8 + e + 2] = lo(b);
-            x[c * 8 + e + 3] = hi(b);
-            top = fmaxf(fmaxf(top, fmaxf(lo(a), hi(a))), fmaxf(lo(b), hi(b)));
-          }
+          for (int e = 8; e < 16; e += 2) top = max3(top, x[e], x[e + 1]);
         }
-      return top;
-    };
-    const bool raise = subtract() + lv > kRaise;
-    if (__syncthreads_or(raise || force || !ok)) {  // (seldom after the first tile)
+      }
+    }
+    if (__syncthreads_or(top + lv > kRaise || general || force || !ok)) {  // (seldom after the first tile)
       // (whoever gave up did so before the barrier, and nobody waits before the next one)
       if (gave_up(C)) break;
-      load_scores();
       // a row's largest x, then the largest of x less that with the value's scale
       auto largest = [&](bool scaled) {
+#pragma unroll 1
+        for (int g = 0; 2 * g < mine8; ++g) {
+          float x[16];
+          exact_scores(g, x);
+          if (scaled) {
 #pragma unroll
-        for (int c = 0; c < NMAX / 8; ++c)
-          if (c < n8) {
-            float t[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = scaled ? (x[c * 8 + e] + C.negx[c * 8 + e]) + lv : x[c * 8 + e];
-            const float most = reduce_eight<true>(t, lane);
-            if ((lane & 3) == 0) C.part[warp][c * 8 + (lane >> 2)] = most;
+            for (int e = 0; e < 16; ++e) x[e] = (x[e] + C.negx[row0 + g * 16 + e]) + lv;
           }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float most = reduce_eight<true>(x + 8 * c, lane);
+            if ((lane & 3) == 0 && 2 * g + c < mine8) C.part[warp & 3][row0 + g * 16 + c * 8 + (lane >> 2)] = most;
+          }
+        }
         __syncthreads();
         return tid < n8 * 8 ? fmaxf(fmaxf(C.part[0][tid], C.part[1][tid]), fmaxf(C.part[2][tid], C.part[3][tid])) : 0.0f;
       };
@@ -446,53 +451,83 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
         if (fabsf(C.negx[tid]) >= 1048576.0f) C.huge = 1;
       }
       force = __syncthreads_or(unset);
+      if (it > 0) ok = wait(C, &C.o_full, (it - 1) & 1) && ok;
+      fence_after();
 #pragma unroll
-      for (int r = 0; r < NMAX; ++r)
-        if ((r >> 3) < n8) l[r] *= C.factor[r];
-      if (it > 0) {
+      for (int c = 0; c < kHalf / 8; ++c)
+        if (c < mine8) {
 #pragma unroll
-        for (int c = 0; c < NMAX / 16; ++c)
-          if (c < n16) {
-            uint32_t o[16];
-            tmem_load_row(mine + kO + c * 16, o);
-            tmem_wait_load(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * C.factor[c * 16 + e]);
-            tmem_store_16(mine + kO + c * 16, o);
-          }
-        tmem_wait_store();
-      }
-      subtract();
-    }
-#pragma unroll
-    for (int c = 0; c < NMAX / 8; ++c)
-      if (c < n8) {
-        uint32_t p[4];
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const Pair w = pair(exp2_approx(x[c * 8 + e]), exp2_approx(x[c * 8 + e + 1]));
-          const Pair s = add2(pair(l[c * 8 + e], l[c * 8 + e + 1]), w), v = mul2(w, pair(vr, vr));
-          l[c * 8 + e] = lo(s);
-          l[c * 8 + e + 1] = hi(s);
-          p[e >> 1] = pack_f16(lo(v), hi(v));
+          for (int e = 0; e < 8; ++e) l[c * 8 + e] *= C.factor[row0 + c * 8 + e];
         }
-        *reinterpret_cast<uint4 *>(smem + Y::kP + line_at(tid, c)) = make_uint4(p[0], p[1], p[2], p[3]);
+      if (it > 0) {
+#pragma unroll 1
+        for (int c = 0; c < mine8; ++c) {
+          float o[8];
+          tmem_load_row(lanes + kO + row0 + c * 8, o);
+          tmem_wait_row(o);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] *= C.factor[row0 + c * 8 + e];
+          tmem_store_8(lanes + kO + row0 + c * 8, o);
+        }
+      }
+      if (general || C.huge) {  // the exponents take the scores' place
+#pragma unroll 1
+        for (int g = 0; 2 * g < mine8; ++g) {
+          float x[16];
+          exact_scores(g, x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = (x[e] + C.negx[row0 + g * 16 + e]) + C.negu[row0 + g * 16 + e];
+          tmem_store_8(lanes + kS + row0 + g * 16, x);
+          if (2 * g + 1 < mine8) tmem_store_8(lanes + kS + row0 + g * 16 + 8, x + 8);
+        }
+      }
+      tmem_wait_store();
+    }
+    const bool done = general || C.huge;
+    const float by = done ? 1.0f : kc;
+    const float *const neg = done ? C.zero : C.neg;
+    const uint32_t line = base + Y::kP + mine * 128 + ((mine & 7) << 4);
+#pragma unroll
+    for (int g = 0; g < kHalf / 16; ++g)
+      if (2 * g < mine8) {
+        float x[16];
+        exponents(g, x, by, neg);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (2 * g + c < mine8) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const Pair w = pair(exp2_approx(x[c * 8 + e]), exp2_approx(x[c * 8 + e + 1]));
+              float *const sum = l + g * 16 + c * 8 + e;
+              const Pair s = add2(pair(sum[0], sum[1]), w), v = mul2(w, pair(vr, vr));
+              sum[0] = lo(s);
+              sum[1] = hi(s);
+              p[e >> 1] = pack_f16(lo(v), hi(v));
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line ^ (row0 * 2 + (g << 5) + (c << 4))), "r"(p[0]),
+                         "r"(p[1]), "r"(p[2]), "r"(p[3])
+                         : "memory");
+          }
       }
     // ---- outputs ----
     fence_proxy_async_smem();
     fence_before();
     __syncthreads();
-    if (leader) {
+    if (warp == 4) {
       fence_after();
-#pragma unroll
-      for (int kk = 0; kk < kOwnKeys / 16; ++kk) {
-        const uint64_t step = static_cast<uint64_t>(kk * (2048 >> 4));
-        if (kk == 0 && it == 0)
-          mma_ss<false>(tmem + kO, values, weights, outputs);
+      const uint64_t v_operand = operand(base + Y::kV, Y::kLines), p_operand = operand(base + Y::kP, Y::kLines);
+      const uint32_t output_shape = product(n16 * 16, true, D, true);
+      if (leader) {
+        if (it == 0)
+          mma_ss<false>(tmem + kO, v_operand, p_operand, output_shape);
         else
-          mma_ss<true>(tmem + kO, values + step, weights + step, outputs);
+          mma_ss<true>(tmem + kO, v_operand, p_operand, output_shape);
+#pragma unroll
+        for (int kk = 1; kk < kOwnKeys / 16; ++kk)
+          mma_ss<true>(tmem + kO, v_operand + kk * (2048 >> 4), p_operand + kk * (2048 >> 4), output_shape);
+        mma_commit(&C.o_full);
       }
-      mma_commit(&C.o_full);
     }
     __syncwarp();
   }
@@ -503,10 +538,10 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
     fence_after();
   }
 #pragma unroll
-  for (int c = 0; c < NMAX / 8; ++c)
-    if (c < n8) {
+  for (int c = 0; c < kHalf / 8; ++c)
+    if (c < mine8) {
       const float sum = reduce_eight<false>(l + c * 8, lane);
-      if ((lane & 3) == 0) C.part[warp][c * 8 + (lane >> 2)] = sum;
+      if ((lane & 3) == 0) C.part[warp & 3][row0 + c * 8 + (lane >> 2)] = sum;
     }
   __syncthreads();
   const bool lost = gave_up(C);
@@ -515,11 +550,11 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
     const int lr = T.r0 + tid, j = div_by(lr, L.group), hq = T.h * P.group + lr - j * P.group;
     const float m = lost ? -INFINITY : C.mx[tid] + C.mu[tid];
     const float sum = lost ? nan : (C.part[0][tid] + C.part[1][tid]) + (C.part[2][tid] + C.part[3][tid]);
-    const int64_t row = (T.first + j) * P.Hq + hq;
+    const int64_t at = (T.first + j) * P.Hq + hq;
     if (T.whole) {
-      if (P.lse) P.lse[row] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+      if (P.lse) P.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     } else {
-      L.part_ml[row * L.slots + L.prefix_splits + T.split] = make_float2(m, sum);
+      L.part_ml[at * L.slots + L.prefix_splits + T.split] = make_float2(m, sum);
     }
     // (a row without keys that count has the output 0.  Some w was 2^-log2(value_scale / W) at least, so sum is above
     // 2^-101 otherwise, and far below 2^126.)
@@ -527,33 +562,32 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 3 : 2)
   }
   __syncthreads();
   // a lane holds a dimension: lane i of the tensor memory for head_dim 128, for 64 the first half of each warp's
-  const int at = D == 128 ? tid : warp * 16 + (lane & 15);
+  const int at = D == 128 ? mine : (warp & 3) * 16 + (lane & 15);
   const int dim = mixed<FMT>() ? mixed_place(at) : at;
+#pragma unroll 1
+  for (int c = 0; c < mine8; ++c) {
+    float o[8];
+    if (it > 0) {
+      tmem_load_row(lanes + kO + row0 + c * 8, o);
+      tmem_wait_row(o);
+    }
 #pragma unroll
-  for (int c = 0; c < NMAX / 16; ++c)
-    if (c < n16) {
-      uint32_t o[16];
-      if (it > 0) {
-        tmem_load_row(mine + kO + c * 16, o);
-        tmem_wait_load(o);
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = c * 16 + e;
-        if (r < T.rows && (D == 128 || lane < 16)) {
-          const int lr = T.r0 + r, j = div_by(lr, L.group), hq = T.h * P.group + lr - j * P.group;
-          const float f = C.factor[r], y = it > 0 ? __uint_as_float(o[e]) * f * (kScaleUnit * unit4<FMT>()) : lost ? nan : 0.0f;
-          if (T.whole)
-            P.out[(T.first + j) * P.out_token + hq * P.out_head + dim] =
-                static_cast<uint16_t>(pack_bf16(f == 0.0f ? 0.0f : y, 0.0f));
-          else
-            L.part_o[(((T.first + j) * P.Hq + hq) * L.slots + L.prefix_splits + T.split) * D + dim] = y;
-        }
+    for (int e = 0; e < 8; ++e) {
+      const int r = row0 + c * 8 + e;
+      if (r < T.rows && (D == 128 || lane < 16)) {
+        const int lr = T.r0 + r, j = div_by(lr, L.group), hq = T.h * P.group + lr - j * P.group;
+        const float f = C.factor[r], y = it > 0 ? o[e] * f * (kScaleUnit * unit4<FMT>()) : lost ? nan : 0.0f;
+        if (T.whole)
+          P.out[(T.first + j) * P.out_token + hq * P.out_head + dim] =
+              static_cast<uint16_t>(pack_bf16(f == 0.0f ? 0.0f : y, 0.0f));
+        else
+          L.part_o[(((T.first + j) * P.Hq + hq) * L.slots + L.prefix_splits + T.split) * D + dim] = y;
       }
     }
+  }
   if (P.status) {
-    if (lost) bits |= SV_DATA_COPY_TIMEOUT;
-    bits = __reduce_or_sync(0xFFFFFFFFu, bits);
+    const uint32_t bits = __reduce_or_sync(0xFFFFFFFFu, (bad ? static_cast<uint32_t>(SV_DATA_BAD_SLOT) : 0u) |
+                                                            (lost ? static_cast<uint32_t>(SV_DATA_COPY_TIMEOUT) : 0u));
     if (lane == 0 && bits) atomicOr(P.status, static_cast<int>(bits));
   }
   fence_before();

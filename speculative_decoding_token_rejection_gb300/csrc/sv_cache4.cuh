@@ -32,6 +32,12 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
+// (x & m) ^ c in one operation.
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t m, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(x), "r"(m), "r"(c));
+  return r;
+}
 // The four pairs of f16 of the four bytes of w (E2M1, two to a byte, the low half first).
 __device__ __forceinline__ void e2m1_word_to_f16(uint32_t w, uint32_t r[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -95,13 +101,31 @@ __device__ __forceinline__ void group_to_f16_mixed(uint2 w, GroupFactors f, uint
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t u = i ? w.y : w.x, v = u >> 8;
-      r[4 * i] = hfma2((u & 0x000F000Fu) ^ 0x64086408u, f.a, f.b);
-      r[4 * i + 1] = hfma2((u & 0x00F000F0u) ^ 0x64806480u, f.c, f.d);
-      r[4 * i + 2] = hfma2((v & 0x000F000Fu) ^ 0x64086408u, f.a, f.b);
-      r[4 * i + 3] = hfma2((v & 0x00F000F0u) ^ 0x64806480u, f.c, f.d);
+      r[4 * i] = hfma2(and_xor(u, 0x000F000Fu, 0x64086408u), f.a, f.b);
+      r[4 * i + 1] = hfma2(and_xor(u, 0x00F000F0u, 0x64806480u), f.c, f.d);
+      r[4 * i + 2] = hfma2(and_xor(v, 0x000F000Fu, 0x64086408u), f.a, f.b);
+      r[4 * i + 3] = hfma2(and_xor(v, 0x00F000F0u, 0x64806480u), f.c, f.d);
     }
   } else {
     group_to_f16<FMT>(w, f, r);
+  }
+}
+
+// Two groups, 32 elements of a row, in that order; the low half of g holds their scales.
+template <int FMT>
+__device__ __forceinline__ void groups_to_f16_mixed(const uint32_t w[4], uint32_t g, uint32_t r[16]) {
+  const uint32_t two = e4m3x2_to_f16x2(static_cast<uint16_t>(g));
+  const uint32_t a = FMT == SV_CACHE_INT4 ? hmul2(two, 0x2C002C00u) : two;                         // (1/16)
+  const uint32_t b = hmul2(a, 0xE408E408u), c = hmul2(a, 0x2C002C00u), d = hmul2(a, 0xD480D480u);  // (-1032, 1/16, -72)
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t one = q ? 0x3232u : 0x1010u;
+    GroupFactors f;
+    f.a = __byte_perm(a, 0, one);
+    f.b = FMT == SV_CACHE_INT4 ? __byte_perm(b, 0, one) : 0u;
+    f.c = FMT == SV_CACHE_INT4 ? __byte_perm(c, 0, one) : 0u;
+    f.d = FMT == SV_CACHE_INT4 ? __byte_perm(d, 0, one) : 0u;
+    group_to_f16_mixed<FMT>(make_uint2(w[2 * q], w[2 * q + 1]), f, r + 8 * q);
   }
 }
 

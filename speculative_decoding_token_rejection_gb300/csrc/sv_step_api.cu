@@ -181,6 +181,11 @@ sv_status spec_verify_check_attend4_args(const spec_verify_config *c, const spec
   const spec_verify_attend_args b = common(*a);
   if ((st = sv::check_attend_sizes(c, &b)) != SV_OK) return st;
   if (a->num_reqs > 0 && (st = check_cache4(a->cache)) != SV_OK) return st;
+  const spec_verify_kv4_cache &c4 = a->cache;
+  if (a->num_reqs > 0 && (c4.block_stride > UINT32_MAX || c4.token_stride > UINT32_MAX ||
+                          c4.group_block_stride > UINT32_MAX || c4.group_token_stride > UINT32_MAX ||
+                          c4.scale_block_stride > UINT32_MAX / 4 || c4.scale_token_stride > UINT32_MAX / 4))
+    return fail(SV_ERR_UNSUPPORTED, "a stride between a cache's pages or tokens is 4 GB or more");
   return sv::check_attend_call(&b);
 }
 
