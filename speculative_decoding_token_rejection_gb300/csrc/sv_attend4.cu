@@ -5,18 +5,19 @@
 // HBM (152 bytes a key for head_dim 128) as long as unpacking a key costs little
 // and is done once for all of its rows.  Both products are transposed, keys and
 // dimensions on the 128-wide side of the instruction, the few rows on the narrow
-// one: S^T [keys x rows] = K Q^T and O^T [dims x rows] += V^T P^T.  Two threads take
+// one: S^T [keys x rows] = K Q^T and O^T [dims x rows] += V^T P^T.  A thread takes
 // a key, from its bytes to its weights:
 //
 //   K row    global -> registers -> f16 -> tensor memory (A of the first product)
 //   V row    global -> registers -> f16 -> shared memory (A of the second, which
 //            wants dimensions outside: 64 of them a 128-byte line per key)
-//   scores   tensor memory -> registers: half of the rows each
+//   scores   tensor memory -> registers: all rows of the thread's key
 //   weights  registers -> shared memory (B of the second product)
 //
-// so no byte is exchanged between threads.  Warps 0-3 unpack K, warps 4-7 V; one
-// thread of either issues the products that wait for it.  A tile is 128 keys, its
-// bytes are loaded a tile ahead.
+// so no byte is exchanged between threads, and one thread issues the products,
+// which run while all unpack: V during the first, the next tile's K during the
+// second.  A tile is 128 keys, its bytes are loaded a tile ahead.  Four CTAs an SM
+// (three with more than 32 rows) hide each other's waits.
 //
 // Numbers, as in the kernel for the shared prefix: x = (q . n) * (scale * log2 e *
 // key_scale), w = 2^(x - m), l = sum w, P = w * value_scale / W, O = W * sum P n_v.
@@ -38,14 +39,14 @@
 namespace sv {
 namespace {
 
-constexpr int kOwnKeys = 128, kOwnThreads = 2 * kOwnKeys;  // two threads a key
+constexpr int kOwnKeys = 128, kOwnThreads = kOwnKeys;  // a thread a key
 constexpr float kRaise = 8;
 constexpr float kScaleUnit = 0x1p28f;           // W
 constexpr float kLeastUnits = kLeastLog2 - 28;  // log2 of the size that a scale counts as at least, in W
 
 struct OwnControl {
-  uint64_t s_full, o_full;
-  uint32_t tmem, abort;
+  uint64_t k_empty, s_full, o_full;
+  uint32_t tmem, tmem_keys, abort;
   uint32_t huge;                       // some |m| is so large that its two parts are subtracted one after the other
   alignas(16) float neg[kOwnRows4];    // negated m, 0 without one
   alignas(16) float zero[kOwnRows4];
@@ -58,12 +59,12 @@ struct OwnControl {
   uint32_t none[kOwnRows4];            // the row sees a value scale that is no number
 };
 
-// Shared memory: [D / 64][128 keys][128 bytes] of V, [128 keys][128 bytes] of weights (up to 64 rows), [D / 64][NMAX
-// rows][128 bytes] of queries.  16-byte columns of a line are exchanged by line % 8.
+// Shared memory: [D / 64][128 keys][128 bytes] of V, weights of up to 64 rows in 128-byte lines, [D / 64][NMAX rows][128
+// bytes] of queries.  With up to 32 rows, keys k and k + 64 share a line of weights: four CTAs' memory fits an SM.  16-byte columns of a line are exchanged by line % 8.
 template <int D, int NMAX>
 struct OwnSmem {
   static constexpr int kLines = kOwnKeys * 128;
-  static constexpr int kV = 0, kP = D / 64 * kLines, kQ = kP + kLines, kControl = kQ + D / 64 * NMAX * 128,
+  static constexpr int kV = 0, kP = D / 64 * kLines, kQ = kP + kLines * NMAX / kOwnRows4, kControl = kQ + D / 64 * NMAX * 128,
                        kBytes = kControl + static_cast<int>(sizeof(OwnControl)) + 1024;  // (the base is rounded up to 1 KB)
 };
 __device__ __forceinline__ int line_at(int line, int col) { return line * 128 + ((col ^ (line & 7)) << 4); }
@@ -102,9 +103,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// A barrier of the warps that unpack the keys.
-__device__ __forceinline__ void sync_keys() { asm volatile("bar.sync 1, %0;" ::"n"(kOwnKeys) : "memory"); }
-
 // Eight values of every lane combined over the warp, in nine exchanges: lane 4i
 // gets that of value i.
 template <bool MAX>
@@ -150,7 +148,7 @@ __device__ __forceinline__ const uint8_t *step(const void *p, uint32_t a, uint32
 }
 
 template <int D, int FMT, int NMAX>
-__global__ void __launch_bounds__(kOwnThreads, 2)
+__global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
     own4_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ AttendPlan L) {
   pdl_enter();
   OwnTile T;
@@ -160,11 +158,11 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
   using Y = OwnSmem<D, NMAX>;
   OwnControl &C = *reinterpret_cast<OwnControl *>(smem + Y::kControl);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int mine = tid & (kOwnKeys - 1), side = tid / kOwnKeys;  // the thread's key of a tile; 0: its K row, 1: its V row
-  constexpr uint32_t kS = 64, kO = 64 + NMAX, kCols = NMAX <= 32 ? 128 : 256;  // columns of tensor memory: K, S, O
-  constexpr int kHalf = NMAX / 2;                                              // rows of a side at most
+  // Tensor memory: K, S and O.  Where all of them pass 128 columns, which is a quarter of what an SM has, K goes there in
+  // two halves of 32 columns, allocated by themselves: three CTAs' 160 columns fit an SM.
+  constexpr int kHalves = D == 128 && NMAX > 32 ? 2 : 1;
+  constexpr uint32_t kKeyCols = D / 2 / kHalves, kS = 0, kO = NMAX, kOwnCols = NMAX <= 32 ? 64 : 128;
   const int n8 = (T.rows + 7) / 8, n16 = (T.rows + 15) / 16;
-  const int row0 = side * ((n8 + 1) / 2) * 8, mine8 = side ? n8 / 2 : (n8 + 1) / 2;  // the side's rows, in eights
 
   // ---- the first tile's bytes are on their way before anything else ----
   const int ntiles = (max(0, T.k_end - T.k_begin) + kOwnKeys - 1) / kOwnKeys;
@@ -173,48 +171,55 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
   // (Nothing here is loaded under a condition: registers that a branch fills otherwise would be waited for at its end.  A
   // key that is not there takes a place that is, and counts for nothing later.)
   auto page_of = [&](int it) {  // of the thread's key of tile `it`
-    const int k = max(T.k_begin, min(T.k_begin + it * kOwnKeys + mine, T.k_end - 1));
+    const int k = max(T.k_begin, min(T.k_begin + it * kOwnKeys + tid, T.k_end - 1));
     return static_cast<int>(load_word((k < P.row0 ? P.tables : table) + div_by(k, L.page)));
   };
-  RawRow<D> row;
+  RawRow<D> krow, vrow;
   uint32_t ks = 0, vs = 0;
-  bool live = false;  // of the key whose bytes are in `row` (or on their way)
-  // (either side's addresses are the warp's own: kept apart, they take no registers of the threads)
-  auto load = [&](auto values, int it, int page) {
-    const int k = T.k_begin + it * kOwnKeys + mine;
+  // The key whose rows are in krow and vrow (or on their way): whether it is there, and where.
+  bool live = false;
+  uint32_t at_page = 0, at_off = 0;
+  auto place = [&](int it, int page) {
+    const int k = T.k_begin + it * kOwnKeys + tid;
     const bool in = k < T.k_end;
     live = in && static_cast<uint32_t>(page) < static_cast<uint32_t>(P.c.num_blocks);
     bad |= in && !live;
-    const uint32_t p = live ? page : 0, off = live ? k - div_by(k, L.page) * P.c.block_size : 0;
-    load_row<D>(row,
-                step(static_cast<const uint8_t *>(values.value ? P.c.v : P.c.k) + T.h * P.c.head_stride,
-                     static_cast<uint32_t>(P.c.block_stride), p, static_cast<uint32_t>(P.c.token_stride), off),
-                step((values.value ? P.v_group : P.k_group) + T.h * P.group_head, static_cast<uint32_t>(P.group_block), p,
-                     static_cast<uint32_t>(P.group_token), off));
-    const uint32_t scale_page = static_cast<uint32_t>(P.c.scale_block_stride * 4),
-                   scale_token = static_cast<uint32_t>(P.c.scale_token_stride * 4);
-    ks = load_word(step(P.c.k_scale + T.h * P.c.scale_head_stride, scale_page, p, scale_token, off));
-    vs = load_word(step(P.c.v_scale + T.h * P.c.scale_head_stride, scale_page, p, scale_token, off));
+    at_page = live ? page : 0;
+    at_off = live ? k - div_by(k, L.page) * P.c.block_size : 0;
   };
-  constexpr std::false_type keys{};
-  constexpr std::true_type values{};
+  auto load = [&](RawRow<D> &row, const void *data, const uint8_t *group) {
+    load_row<D>(row,
+                step(static_cast<const uint8_t *>(data) + T.h * P.c.head_stride, static_cast<uint32_t>(P.c.block_stride),
+                     at_page, static_cast<uint32_t>(P.c.token_stride), at_off),
+                step(group + T.h * P.group_head, static_cast<uint32_t>(P.group_block), at_page,
+                     static_cast<uint32_t>(P.group_token), at_off));
+  };
+  auto load_scale = [&](const float *scale) {
+    return load_word(step(scale + T.h * P.c.scale_head_stride, static_cast<uint32_t>(P.c.scale_block_stride * 4), at_page,
+                          static_cast<uint32_t>(P.c.scale_token_stride * 4), at_off));
+  };
   int page = 0;
   if (ntiles > 0) {
-    page = page_of(0);
-    if (side == 0)
-      load(keys, 0, page);
-    else
-      load(values, 0, page);
+    place(0, page_of(0));
+    load(krow, P.c.k, P.k_group);
+    load(vrow, P.c.v, P.v_group);
+    ks = load_scale(P.c.k_scale);
+    vs = load_scale(P.c.v_scale);
     page = page_of(1);
   }
 
   if (tid == 0) {
+    mbar_init(&C.k_empty, 1);
     mbar_init(&C.s_full, 1);
     mbar_init(&C.o_full, 1);
     C.abort = C.huge = 0;
     fence_mbar_init();
   }
-  if (warp == 0) tmem_alloc(&C.tmem, kCols);
+  if (warp == 0) {
+    tmem_get(&C.tmem, kOwnCols);
+    tmem_get(&C.tmem_keys, kKeyCols);
+    tmem_no_more();
+  }
   if (tid < kOwnRows4) {
     const int j = div_by(T.r0 + tid, L.group);
     C.limit[tid] = tid < T.rows ? T.len - T.gam + j : 0x7FFFFFFF;
@@ -281,101 +286,116 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
   int low = 0x7FFFFFFF;  // keys below it are seen by every row
   for (int r = lane; r < T.rows; r += 32) low = min(low, C.limit[r]);
   low = __reduce_min_sync(0xFFFFFFFFu, low);
-  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, C.tmem, 0), base = smem_addr(smem);
-  const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // the warp's part of tensor memory
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, C.tmem, 0), tmem_keys = __shfl_sync(0xFFFFFFFFu, C.tmem_keys, 0);
+  const uint32_t base = smem_addr(smem), lanes = static_cast<uint32_t>(warp * 32) << 16;  // the warp's part of tensor memory
   const bool leader = elected();
-  float l[kHalf];  // sums over the thread's keys
+
+  float l[NMAX];  // sums over the thread's keys
 #pragma unroll
-  for (int r = 0; r < kHalf; ++r) l[r] = 0.0f;
+  for (int r = 0; r < NMAX; ++r) l[r] = 0.0f;
   const float c_all = P.scale * unit4<FMT>() * kLog2e;
+  // Half (or all) of the keys in krow to tensor memory, and their part of the scores.
+  constexpr int kTwos = D / 32 / kHalves;  // pairs of groups in it
+  auto unpack_keys = [&](int half) {
+#pragma unroll
+    for (int two = 0; two < kTwos; ++two) {
+      const int at = half * kTwos + two;
+      uint32_t h[16];
+      groups_to_f16_mixed<FMT>(krow.w + 4 * at, live ? krow.g[at >> 1] >> (16 * (at & 1)) : 0u, h);
+      tmem_store_row(tmem_keys + lanes + two * 16, h);
+    }
+    tmem_wait_store();
+    fence_before();
+    __syncthreads();
+    if (warp == 0) {
+      fence_after();
+      const uint64_t queries = operand(base + Y::kQ, 16);
+      const uint32_t shape = product(n16 * 16, false);
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < 2 * kTwos; ++kk) {
+          const int at = half * 2 * kTwos + kk;
+          const uint64_t b = queries + static_cast<uint64_t>((at >> 2) * (NMAX * 128 >> 4) + (at & 3) * 2);
+          if (at == 0)
+            mma_ts<false>(tmem + kS, tmem_keys, b, shape);
+          else
+            mma_ts<true>(tmem + kS, tmem_keys + kk * 8, b, shape);
+        }
+        mma_commit(half == kHalves - 1 ? &C.s_full : &C.k_empty);
+      }
+    }
+  };
+  // Half (or all) of the values in vrow to shared memory.
+  const uint32_t p_line = base + Y::kP + (NMAX <= 32 ? (tid & 63) * 128 + (((tid >> 6 << 2) ^ (tid & 7)) << 4)
+                                                     : tid * 128 + ((tid & 7) << 4));
+  const uint32_t v_line = base + Y::kV + tid * 128 + ((tid & 7) << 4);
+  auto unpack_values = [&](int half) {
+#pragma unroll
+    for (int two = half * kTwos; two < (half + 1) * kTwos; ++two) {
+      uint32_t h[16];
+      groups_to_f16_mixed<FMT>(vrow.w + 4 * two, live ? vrow.g[two >> 1] >> (16 * (two & 1)) : 0u, h);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((v_line ^ ((two & 1) * 64 + c * 16)) + (two >> 1) * Y::kLines),
+                     "r"(h[4 * c]), "r"(h[4 * c + 1]), "r"(h[4 * c + 2]), "r"(h[4 * c + 3])
+                     : "memory");
+    }
+  };
   bool force = true;  // some row has no maximum
   bool ok = true;
   int it = 0;
   for (; it < ntiles; ++it) {
-    // ---- the tile's keys to tensor memory, its values to shared memory ----
     const bool dead = !live;
     const float kc = __uint_as_float(ks) * c_all, v_scale = dead ? 0.0f : __uint_as_float(vs);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) row.g[i] = dead ? 0u : row.g[i];  // (zeros)
-    const int key = T.k_begin + it * kOwnKeys + mine;
-    if (side == 0) {
-#pragma unroll
-      for (int two = 0; two < D / 32; ++two) {
-        uint32_t h[16];
-        groups_to_f16_mixed<FMT>(row.w + 4 * two, row.g[two >> 1] >> (16 * (two & 1)), h);
-        tmem_store_row(lanes + two * 16, h);
-      }
-      if (it + 1 < ntiles) load(keys, it + 1, page);
-      tmem_wait_store();
-      fence_before();
-      sync_keys();
-      if (warp == 0) {
-        fence_after();
-        const uint64_t q_operand = operand(base + Y::kQ, 16);
-        const uint32_t score_shape = product(n16 * 16, false);
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t b = q_operand + static_cast<uint64_t>((kk >> 2) * (NMAX * 128 >> 4) + (kk & 3) * 2);
-            if (kk == 0)
-              mma_ts<false>(tmem + kS, tmem, b, score_shape);
-            else
-              mma_ts<true>(tmem + kS, tmem + kk * 8, b, score_shape);
-          }
-          mma_commit(&C.s_full);
-        }
-      }
-      __syncwarp();
-    } else {
-      if (it > 0) ok = wait(C, &C.o_full, (it - 1) & 1) && ok;  // (the products of the tile before are done with them)
-      const uint32_t line = base + Y::kV + mine * 128 + ((mine & 7) << 4);
-#pragma unroll
-      for (int two = 0; two < D / 32; ++two) {
-        uint32_t h[16];
-        groups_to_f16_mixed<FMT>(row.w + 4 * two, row.g[two >> 1] >> (16 * (two & 1)), h);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((line ^ ((two & 1) * 64 + c * 16)) + (two >> 1) * Y::kLines),
-                       "r"(h[4 * c]), "r"(h[4 * c + 1]), "r"(h[4 * c + 2]), "r"(h[4 * c + 3])
-                       : "memory");
-      }
-      if (it + 1 < ntiles) load(values, it + 1, page);
+    const int key = T.k_begin + it * kOwnKeys + tid;
+    const bool more = it + 1 < ntiles;
+    unpack_keys(0);
+    if (it > 0) ok = wait(C, &C.o_full, (it - 1) & 1) && ok;  // (the values' and weights' place is free, and O is there)
+    unpack_values(0);
+    if (kHalves == 2) {
+      ok = wait(C, &C.k_empty, it & 1) && ok;
+      fence_after();
+      unpack_keys(1);
+      unpack_values(1);
     }
-    page = page_of(it + 2);
-    // ---- weights: half of the rows for either thread of a key ----
+    if (more) {
+      place(it + 1, page);
+      load(krow, P.c.k, P.k_group);
+      load(vrow, P.c.v, P.v_group);
+      ks = load_scale(P.c.k_scale);
+      vs = load_scale(P.c.v_scale);
+      page = page_of(it + 2);
+    }
+    ok = wait(C, &C.s_full, it & 1, P.expire) && ok;
+    fence_after();
+    // ---- weights ----
     const bool number = fabsf(v_scale) < INFINITY;
     const float vr = number && fabsf(v_scale) >= kLeastScale ? v_scale * (1.0f / kScaleUnit) : 0.0f;
     const float lv = fmaxf(__log2f(fabsf(vr)), kLeastUnits);
-    const bool cut = T.k_begin + (it + 1) * kOwnKeys > low || __any_sync(0xFFFFFFFFu, dead);
-    if (side == 0 && !number) {
+    const uint32_t s_mine = tmem + lanes + kS;
+    if (!number) {
       for (int r = 0; r < T.rows; ++r)
         if (key < C.limit[r]) C.none[r] = 1;
     }
-    // Two eights of the side's rows at a time: columns 16 g .. of its part of S (the first eight again where there is one).
+    // Two eights of rows at a time: columns 16 g .. (the first eight again where there is one).
     auto load_scores = [&](int g, float x[16]) {
-      const uint32_t at = lanes + kS + row0 + g * 16;
+      const uint32_t at = s_mine + g * 16;
       tmem_load_row(at, x);
-      tmem_load_row(2 * g + 1 < mine8 ? at + 8 : at, x + 8);
+      tmem_load_row(2 * g + 1 < n8 ? at + 8 : at, x + 8);
       tmem_wait_row(x);
       tmem_wait_row(x + 8);
     };
-    // Scores in base 2, -inf where the row does not see the key.  (A product of its own, rounded: subtracting a maximum
-    // that equals it gives 0.)
-    auto exact_scores = [&](int g, float x[16]) {
-      load_scores(g, x);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = row0 + g * 16 + e;
-        const float y = x[e] * kc * C.back[r];
-        x[e] = dead || key >= C.limit[r] ? -INFINITY : y;
-      }
+    auto store_scores = [&](int g, const float x[16]) {
+      tmem_store_8(s_mine + g * 16, x);
+      if (2 * g + 1 < n8) tmem_store_8(s_mine + g * 16 + 8, x + 8);
     };
-    // x * by - m of the side's rows 16 g ..
-    auto exponents = [&](int g, float x[16], float by, const float *neg) {
+    // x * by - m
+    float by = kc;
+    auto exponents = [&](int g, float x[16], const float *neg) {
       load_scores(g, x);
 #pragma unroll
       for (int e = 0; e < 16; e += 4) {
-        const float4 m = *reinterpret_cast<const float4 *>(neg + row0 + g * 16 + e);
+        const float4 m = *reinterpret_cast<const float4 *>(neg + g * 16 + e);
         const Pair a = fma2(pair(x[e], x[e + 1]), pair(by, by), pair(m.x, m.y));
         const Pair b = fma2(pair(x[e + 2], x[e + 3]), pair(by, by), pair(m.z, m.w));
         x[e] = lo(a);
@@ -384,117 +404,133 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
         x[e + 3] = hi(b);
       }
     };
-    ok = wait(C, &C.s_full, it & 1, P.expire) && ok;
-    fence_after();
-    // Most tiles: every row sees all keys, needs no power of two and has an m that holds, below 2^20 in size.  One fused
-    // operation an exponent then (its exact product differs from a rounded one by less than 2^-4).
-    const bool general = cut || shifted || C.huge;
-    float top = -INFINITY;
-    if (!general) {
+    const float *neg = C.neg;
+    // Rows that do not see every key, or have a power of two: their scores in base 2 take the place of the products.
+    if (T.k_begin + (it + 1) * kOwnKeys > low || shifted || __any_sync(0xFFFFFFFFu, dead)) {
 #pragma unroll 1
-      for (int g = 0; 2 * g < mine8; ++g) {
+      for (int g = 0; 2 * g < n8; ++g) {
         float x[16];
-        exponents(g, x, kc, C.neg);
+        load_scores(g, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int r = g * 16 + e;
+          x[e] = dead || key >= C.limit[r] ? -INFINITY : x[e] * kc * C.back[r];
+        }
+        store_scores(g, x);
+      }
+      tmem_wait_store();
+      by = 1.0f;
+    }
+    // (Below 2^20 a fused operation's exact product differs from a rounded one by less than 2^-4.)
+    const bool huge = C.huge;
+    float top = -INFINITY;
+    if (!huge) {
+#pragma unroll 1
+      for (int g = 0; 2 * g < n8; ++g) {
+        float x[16];
+        exponents(g, x, neg);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) top = max3(top, x[e], x[e + 1]);
-        if (2 * g + 1 < mine8) {
+        if (2 * g + 1 < n8) {
 #pragma unroll
           for (int e = 8; e < 16; e += 2) top = max3(top, x[e], x[e + 1]);
         }
       }
     }
-    if (__syncthreads_or(top + lv > kRaise || general || force || !ok)) {  // (seldom after the first tile)
+    if (__syncthreads_or(top + lv > kRaise || huge || force || !ok)) {  // (seldom after the first tile)
       // (whoever gave up did so before the barrier, and nobody waits before the next one)
       if (gave_up(C)) break;
-      // a row's largest x, then the largest of x less that with the value's scale
-      auto largest = [&](bool scaled) {
+      // The rows' largest (x + part) + add, to the threads that keep the rows' m.
+      auto largest = [&](const float *part, float add) {
 #pragma unroll 1
-        for (int g = 0; 2 * g < mine8; ++g) {
+        for (int g = 0; 2 * g < n8; ++g) {
           float x[16];
-          exact_scores(g, x);
-          if (scaled) {
+          exponents(g, x, C.zero);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = (x[e] + C.negx[row0 + g * 16 + e]) + lv;
-          }
+          for (int e = 0; e < 16; ++e) x[e] = (x[e] + part[g * 16 + e]) + add;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const float most = reduce_eight<true>(x + 8 * c, lane);
-            if ((lane & 3) == 0 && 2 * g + c < mine8) C.part[warp & 3][row0 + g * 16 + c * 8 + (lane >> 2)] = most;
+            if ((lane & 3) == 0 && 2 * g + c < n8) C.part[warp][g * 16 + c * 8 + (lane >> 2)] = most;
           }
         }
         __syncthreads();
         return tid < n8 * 8 ? fmaxf(fmaxf(C.part[0][tid], C.part[1][tid]), fmaxf(C.part[2][tid], C.part[3][tid])) : 0.0f;
       };
-      const float top_x = largest(false);
-      float mx = 0.0f;
-      if (tid < n8 * 8) {
-        mx = fmaxf(C.mx[tid], top_x);
-        C.negx[tid] = mx == -INFINITY ? 0.0f : -mx;
+      float mx = 0.0f, mu = 0.0f;
+      // first with m in one number, then, where one is too large for that, its two parts one after the other
+#pragma unroll 1
+      for (int round = huge ? 1 : 0; round < 3; ++round) {
+        const float most = largest(round == 2 ? C.negx : C.zero, round == 1 ? 0.0f : lv);
+        if (tid < n8 * 8) {
+          if (round == 2) {
+            mu = most;
+          } else {
+            mx = round == 0 ? most : fmaxf(C.mx[tid], most);
+            if (round == 0 && fabsf(mx) >= 1048576.0f && fabsf(mx) < INFINITY) C.huge = 1;
+            if (round == 1) C.negx[tid] = mx == -INFINITY ? 0.0f : -mx;
+          }
+        }
+        __syncthreads();
+        if (round == 0 && !C.huge) break;
       }
-      __syncthreads();
-      const float top_u = largest(true);
-      bool unset = false;
+      bool unset = false, raised = false;
       if (tid < n8 * 8) {
         const bool had = C.mx[tid] != -INFINITY;
         const float old = had ? (C.mx[tid] - mx) + C.mu[tid] : 0.0f;  // of the sums so far, less mx
-        if (!had || top_u > old + kRaise) {
-          C.factor[tid] = had ? exp2_approx(old - top_u) : 1.0f;  // (without a maximum O and l are zeros or NaN)
+        raised = !had || mu > old + kRaise;
+        C.factor[tid] = had && raised ? exp2_approx(old - mu) : 1.0f;  // (without a maximum O and l are zeros or NaN)
+        if (raised) {
           C.mx[tid] = mx;
-          C.mu[tid] = mx == -INFINITY ? 0.0f : top_u;
-        } else {
-          C.factor[tid] = 1.0f;
+          C.mu[tid] = mx == -INFINITY ? 0.0f : mu;
         }
         unset = C.mx[tid] == -INFINITY;
         C.negx[tid] = unset ? 0.0f : -C.mx[tid];
         C.negu[tid] = -C.mu[tid];
         C.neg[tid] = C.negx[tid] + C.negu[tid];
-        if (fabsf(C.negx[tid]) >= 1048576.0f) C.huge = 1;
       }
       force = __syncthreads_or(unset);
-      if (it > 0) ok = wait(C, &C.o_full, (it - 1) & 1) && ok;
-      fence_after();
-#pragma unroll
-      for (int c = 0; c < kHalf / 8; ++c)
-        if (c < mine8) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) l[c * 8 + e] *= C.factor[row0 + c * 8 + e];
-        }
       if (it > 0) {
+        ok = wait(C, &C.o_full, (it - 1) & 1) && ok;
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < NMAX / 8; ++c)
+          if (c < n8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) l[c * 8 + e] *= C.factor[c * 8 + e];
+          }
 #pragma unroll 1
-        for (int c = 0; c < mine8; ++c) {
+        for (int c = 0; c < n8; ++c) {
           float o[8];
-          tmem_load_row(lanes + kO + row0 + c * 8, o);
+          tmem_load_row(tmem + lanes + kO + c * 8, o);
           tmem_wait_row(o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] *= C.factor[row0 + c * 8 + e];
-          tmem_store_8(lanes + kO + row0 + c * 8, o);
+          for (int e = 0; e < 8; ++e) o[e] *= C.factor[c * 8 + e];
+          tmem_store_8(tmem + lanes + kO + c * 8, o);
         }
       }
-      if (general || C.huge) {  // the exponents take the scores' place
+      if (C.huge) {  // the exponents take the scores' place
 #pragma unroll 1
-        for (int g = 0; 2 * g < mine8; ++g) {
+        for (int g = 0; 2 * g < n8; ++g) {
           float x[16];
-          exact_scores(g, x);
+          exponents(g, x, C.negx);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = (x[e] + C.negx[row0 + g * 16 + e]) + C.negu[row0 + g * 16 + e];
-          tmem_store_8(lanes + kS + row0 + g * 16, x);
-          if (2 * g + 1 < mine8) tmem_store_8(lanes + kS + row0 + g * 16 + 8, x + 8);
+          for (int e = 0; e < 16; ++e) x[e] = x[e] + C.negu[g * 16 + e];
+          store_scores(g, x);
         }
+        by = 1.0f;
+        neg = C.zero;
       }
       tmem_wait_store();
     }
-    const bool done = general || C.huge;
-    const float by = done ? 1.0f : kc;
-    const float *const neg = done ? C.zero : C.neg;
-    const uint32_t line = base + Y::kP + mine * 128 + ((mine & 7) << 4);
 #pragma unroll
-    for (int g = 0; g < kHalf / 16; ++g)
-      if (2 * g < mine8) {
+    for (int g = 0; g < NMAX / 16; ++g)
+      if (2 * g < n8) {
         float x[16];
-        exponents(g, x, by, neg);
+        exponents(g, x, neg);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          if (2 * g + c < mine8) {
+          if (2 * g + c < n8) {
             uint32_t p[4];
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
@@ -505,7 +541,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
               sum[1] = hi(s);
               p[e >> 1] = pack_f16(lo(v), hi(v));
             }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line ^ (row0 * 2 + (g << 5) + (c << 4))), "r"(p[0]),
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_line ^ ((g << 5) + (c << 4))), "r"(p[0]),
                          "r"(p[1]), "r"(p[2]), "r"(p[3])
                          : "memory");
           }
@@ -514,7 +550,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
     fence_proxy_async_smem();
     fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == 0) {
       fence_after();
       const uint64_t v_operand = operand(base + Y::kV, Y::kLines), p_operand = operand(base + Y::kP, Y::kLines);
       const uint32_t output_shape = product(n16 * 16, true, D, true);
@@ -525,7 +561,9 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
           mma_ss<true>(tmem + kO, v_operand, p_operand, output_shape);
 #pragma unroll
         for (int kk = 1; kk < kOwnKeys / 16; ++kk)
-          mma_ss<true>(tmem + kO, v_operand + kk * (2048 >> 4), p_operand + kk * (2048 >> 4), output_shape);
+          mma_ss<true>(tmem + kO, v_operand + kk * (2048 >> 4),
+                       p_operand + (NMAX <= 32 ? (kk & 3) * (2048 >> 4) + (kk >> 2) * (64 >> 4) : kk * (2048 >> 4)),
+                       output_shape);
         mma_commit(&C.o_full);
       }
     }
@@ -538,10 +576,10 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
     fence_after();
   }
 #pragma unroll
-  for (int c = 0; c < kHalf / 8; ++c)
-    if (c < mine8) {
+  for (int c = 0; c < NMAX / 8; ++c)
+    if (c < n8) {
       const float sum = reduce_eight<false>(l + c * 8, lane);
-      if ((lane & 3) == 0) C.part[warp & 3][row0 + c * 8 + (lane >> 2)] = sum;
+      if ((lane & 3) == 0) C.part[warp][c * 8 + (lane >> 2)] = sum;
     }
   __syncthreads();
   const bool lost = gave_up(C);
@@ -562,18 +600,18 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
   }
   __syncthreads();
   // a lane holds a dimension: lane i of the tensor memory for head_dim 128, for 64 the first half of each warp's
-  const int at = D == 128 ? mine : (warp & 3) * 16 + (lane & 15);
+  const int at = D == 128 ? tid : warp * 16 + (lane & 15);
   const int dim = mixed<FMT>() ? mixed_place(at) : at;
 #pragma unroll 1
-  for (int c = 0; c < mine8; ++c) {
+  for (int c = 0; c < n8; ++c) {
     float o[8];
     if (it > 0) {
-      tmem_load_row(lanes + kO + row0 + c * 8, o);
+      tmem_load_row(tmem + lanes + kO + c * 8, o);
       tmem_wait_row(o);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int r = row0 + c * 8 + e;
+      const int r = c * 8 + e;
       if (r < T.rows && (D == 128 || lane < 16)) {
         const int lr = T.r0 + r, j = div_by(lr, L.group), hq = T.h * P.group + lr - j * P.group;
         const float f = C.factor[r], y = it > 0 ? o[e] * f * (kScaleUnit * unit4<FMT>()) : lost ? nan : 0.0f;
@@ -593,7 +631,10 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 0) tmem_free(tmem, kCols);
+  if (warp == 0) {
+    tmem_free(tmem, kOwnCols);
+    tmem_free(tmem_keys, kKeyCols);
+  }
 }
 
 template <int D, int FMT, int NMAX>

@@ -8,10 +8,17 @@
 
 namespace sv {
 
-__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols) {
+// Columns of tensor memory (a power of two, 32 at least) for a CTA, by a whole warp, and the end of asking.
+__device__ __forceinline__ void tmem_get(uint32_t *dst, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
                : "memory");
+}
+__device__ __forceinline__ void tmem_no_more() {
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols) {
+  tmem_get(dst, cols);
+  tmem_no_more();
 }
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
