@@ -44,7 +44,16 @@ constexpr float kRaise = 8;
 constexpr float kScaleUnit = 0x1p28f;           // W
 constexpr float kLeastUnits = kLeastLog2 - 28;  // log2 of the size that a scale counts as at least, in W
 
+// Where the kv head's rows are, in shared memory: worked out from the arguments for every tile, the multiplications of a
+// warp's own registers took 2500 of 8000 cycles a tile.
+struct alignas(16) OwnPlaces {
+  const uint8_t *k, *v, *k_group, *v_group, *k_scale, *v_scale;
+  uint32_t page, token, group_page, group_token, scale_page, scale_token;  // bytes from one to the next
+  const int32_t *table, *table0;
+};
+
 struct OwnControl {
+  OwnPlaces at;
   uint64_t k_empty, s_full, o_full;
   uint32_t tmem, tmem_keys, abort;
   uint32_t huge;                       // some |m| is so large that its two parts are subtracted one after the other
@@ -140,7 +149,7 @@ __device__ __forceinline__ void load_row(RawRow<D> &r, const uint8_t *data, cons
     r.g[0] = load_word(group);
 }
 // p + a * x + b * y
-__device__ __forceinline__ const uint8_t *step(const void *p, uint32_t a, uint32_t x, uint32_t b, uint32_t y) {
+__device__ __forceinline__ const uint8_t *step(const uint8_t *p, uint32_t a, uint32_t x, uint32_t b, uint32_t y) {
   uint64_t r;
   asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(a), "r"(x), "l"(p));
   asm("mad.wide.u32 %0, %1, %2, %0;" : "+l"(r) : "r"(b), "r"(y));
@@ -166,45 +175,49 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
 
   // ---- the first tile's bytes are on their way before anything else ----
   const int ntiles = (max(0, T.k_end - T.k_begin) + kOwnKeys - 1) / kOwnKeys;
-  const int32_t *const table = P.tables + T.i * P.table_stride;
+  if (tid == 0) {
+    OwnPlaces &A = C.at;
+    A.k = static_cast<const uint8_t *>(P.c.k) + T.h * P.c.head_stride;
+    A.v = static_cast<const uint8_t *>(P.c.v) + T.h * P.c.head_stride;
+    A.k_group = P.k_group + T.h * P.group_head;
+    A.v_group = P.v_group + T.h * P.group_head;
+    A.k_scale = reinterpret_cast<const uint8_t *>(P.c.k_scale + T.h * P.c.scale_head_stride);
+    A.v_scale = reinterpret_cast<const uint8_t *>(P.c.v_scale + T.h * P.c.scale_head_stride);
+    A.page = static_cast<uint32_t>(P.c.block_stride);
+    A.token = static_cast<uint32_t>(P.c.token_stride);
+    A.group_page = static_cast<uint32_t>(P.group_block);
+    A.group_token = static_cast<uint32_t>(P.group_token);
+    A.scale_page = static_cast<uint32_t>(P.c.scale_block_stride * 4);
+    A.scale_token = static_cast<uint32_t>(P.c.scale_token_stride * 4);
+    A.table = P.tables + T.i * P.table_stride;
+    A.table0 = P.tables;
+  }
+  __syncthreads();
   bool bad = false;  // some page was outside the cache
   // (Nothing here is loaded under a condition: registers that a branch fills otherwise would be waited for at its end.  A
   // key that is not there takes a place that is, and counts for nothing later.)
   auto page_of = [&](int it) {  // of the thread's key of tile `it`
     const int k = max(T.k_begin, min(T.k_begin + it * kOwnKeys + tid, T.k_end - 1));
-    return static_cast<int>(load_word((k < P.row0 ? P.tables : table) + div_by(k, L.page)));
+    return static_cast<int>(load_word((k < P.row0 ? C.at.table0 : C.at.table) + div_by(k, L.page)));
   };
   RawRow<D> krow, vrow;
   uint32_t ks = 0, vs = 0;
-  // The key whose rows are in krow and vrow (or on their way): whether it is there, and where.
-  bool live = false;
-  uint32_t at_page = 0, at_off = 0;
-  auto place = [&](int it, int page) {
+  bool live = false;  // the key whose rows are in krow and vrow (or on their way) is there
+  auto load = [&](int it, int page) {
     const int k = T.k_begin + it * kOwnKeys + tid;
     const bool in = k < T.k_end;
     live = in && static_cast<uint32_t>(page) < static_cast<uint32_t>(P.c.num_blocks);
     bad |= in && !live;
-    at_page = live ? page : 0;
-    at_off = live ? k - div_by(k, L.page) * P.c.block_size : 0;
-  };
-  auto load = [&](RawRow<D> &row, const void *data, const uint8_t *group) {
-    load_row<D>(row,
-                step(static_cast<const uint8_t *>(data) + T.h * P.c.head_stride, static_cast<uint32_t>(P.c.block_stride),
-                     at_page, static_cast<uint32_t>(P.c.token_stride), at_off),
-                step(group + T.h * P.group_head, static_cast<uint32_t>(P.group_block), at_page,
-                     static_cast<uint32_t>(P.group_token), at_off));
-  };
-  auto load_scale = [&](const float *scale) {
-    return load_word(step(scale + T.h * P.c.scale_head_stride, static_cast<uint32_t>(P.c.scale_block_stride * 4), at_page,
-                          static_cast<uint32_t>(P.c.scale_token_stride * 4), at_off));
+    const uint32_t p = live ? page : 0, off = live ? k - div_by(k, L.page) * P.c.block_size : 0;
+    const OwnPlaces &A = C.at;
+    load_row<D>(krow, step(A.k, A.page, p, A.token, off), step(A.k_group, A.group_page, p, A.group_token, off));
+    load_row<D>(vrow, step(A.v, A.page, p, A.token, off), step(A.v_group, A.group_page, p, A.group_token, off));
+    ks = load_word(step(A.k_scale, A.scale_page, p, A.scale_token, off));
+    vs = load_word(step(A.v_scale, A.scale_page, p, A.scale_token, off));
   };
   int page = 0;
   if (ntiles > 0) {
-    place(0, page_of(0));
-    load(krow, P.c.k, P.k_group);
-    load(vrow, P.c.v, P.v_group);
-    ks = load_scale(P.c.k_scale);
-    vs = load_scale(P.c.v_scale);
+    load(0, page_of(0));
     page = page_of(1);
   }
 
@@ -359,11 +372,7 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
       unpack_values(1);
     }
     if (more) {
-      place(it + 1, page);
-      load(krow, P.c.k, P.k_group);
-      load(vrow, P.c.v, P.v_group);
-      ks = load_scale(P.c.k_scale);
-      vs = load_scale(P.c.v_scale);
+      load(it + 1, page);
       page = page_of(it + 2);
     }
     ok = wait(C, &C.s_full, it & 1, P.expire) && ok;
@@ -421,135 +430,143 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
       tmem_wait_store();
       by = 1.0f;
     }
+    // Weights with the m there is; in the first tile, or where a weight passes 2^8 with it (seldom), with a new one.
     // (Below 2^20 a fused operation's exact product differs from a rounded one by less than 2^-4.)
-    const bool huge = C.huge;
-    float top = -INFINITY;
-    if (!huge) {
+    bool fresh = force || C.huge, stop = false;
+    for (;;) {
+      if (fresh) {
+        const bool huge = C.huge;
+        // The rows' largest (x + part) + add, to the threads that keep the rows' m.
+        auto largest = [&](const float *part, float add) {
 #pragma unroll 1
-      for (int g = 0; 2 * g < n8; ++g) {
-        float x[16];
-        exponents(g, x, neg);
+          for (int g = 0; 2 * g < n8; ++g) {
+            float x[16];
+            exponents(g, x, C.zero);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) top = max3(top, x[e], x[e + 1]);
-        if (2 * g + 1 < n8) {
+            for (int e = 0; e < 16; ++e) x[e] = (x[e] + part[g * 16 + e]) + add;
 #pragma unroll
-          for (int e = 8; e < 16; e += 2) top = max3(top, x[e], x[e + 1]);
-        }
-      }
-    }
-    if (__syncthreads_or(top + lv > kRaise || huge || force || !ok)) {  // (seldom after the first tile)
-      // (whoever gave up did so before the barrier, and nobody waits before the next one)
-      if (gave_up(C)) break;
-      // The rows' largest (x + part) + add, to the threads that keep the rows' m.
-      auto largest = [&](const float *part, float add) {
-#pragma unroll 1
-        for (int g = 0; 2 * g < n8; ++g) {
-          float x[16];
-          exponents(g, x, C.zero);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = (x[e] + part[g * 16 + e]) + add;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float most = reduce_eight<true>(x + 8 * c, lane);
-            if ((lane & 3) == 0 && 2 * g + c < n8) C.part[warp][g * 16 + c * 8 + (lane >> 2)] = most;
-          }
-        }
-        __syncthreads();
-        return tid < n8 * 8 ? fmaxf(fmaxf(C.part[0][tid], C.part[1][tid]), fmaxf(C.part[2][tid], C.part[3][tid])) : 0.0f;
-      };
-      float mx = 0.0f, mu = 0.0f;
-      // first with m in one number, then, where one is too large for that, its two parts one after the other
-#pragma unroll 1
-      for (int round = huge ? 1 : 0; round < 3; ++round) {
-        const float most = largest(round == 2 ? C.negx : C.zero, round == 1 ? 0.0f : lv);
-        if (tid < n8 * 8) {
-          if (round == 2) {
-            mu = most;
-          } else {
-            mx = round == 0 ? most : fmaxf(C.mx[tid], most);
-            if (round == 0 && fabsf(mx) >= 1048576.0f && fabsf(mx) < INFINITY) C.huge = 1;
-            if (round == 1) C.negx[tid] = mx == -INFINITY ? 0.0f : -mx;
-          }
-        }
-        __syncthreads();
-        if (round == 0 && !C.huge) break;
-      }
-      bool unset = false, raised = false;
-      if (tid < n8 * 8) {
-        const bool had = C.mx[tid] != -INFINITY;
-        const float old = had ? (C.mx[tid] - mx) + C.mu[tid] : 0.0f;  // of the sums so far, less mx
-        raised = !had || mu > old + kRaise;
-        C.factor[tid] = had && raised ? exp2_approx(old - mu) : 1.0f;  // (without a maximum O and l are zeros or NaN)
-        if (raised) {
-          C.mx[tid] = mx;
-          C.mu[tid] = mx == -INFINITY ? 0.0f : mu;
-        }
-        unset = C.mx[tid] == -INFINITY;
-        C.negx[tid] = unset ? 0.0f : -C.mx[tid];
-        C.negu[tid] = -C.mu[tid];
-        C.neg[tid] = C.negx[tid] + C.negu[tid];
-      }
-      force = __syncthreads_or(unset);
-      if (it > 0) {
-        ok = wait(C, &C.o_full, (it - 1) & 1) && ok;
-        fence_after();
-#pragma unroll
-        for (int c = 0; c < NMAX / 8; ++c)
-          if (c < n8) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) l[c * 8 + e] *= C.factor[c * 8 + e];
-          }
-#pragma unroll 1
-        for (int c = 0; c < n8; ++c) {
-          float o[8];
-          tmem_load_row(tmem + lanes + kO + c * 8, o);
-          tmem_wait_row(o);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] *= C.factor[c * 8 + e];
-          tmem_store_8(tmem + lanes + kO + c * 8, o);
-        }
-      }
-      if (C.huge) {  // the exponents take the scores' place
-#pragma unroll 1
-        for (int g = 0; 2 * g < n8; ++g) {
-          float x[16];
-          exponents(g, x, C.negx);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = x[e] + C.negu[g * 16 + e];
-          store_scores(g, x);
-        }
-        by = 1.0f;
-        neg = C.zero;
-      }
-      tmem_wait_store();
-    }
-#pragma unroll
-    for (int g = 0; g < NMAX / 16; ++g)
-      if (2 * g < n8) {
-        float x[16];
-        exponents(g, x, neg);
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (2 * g + c < n8) {
-            uint32_t p[4];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const Pair w = pair(exp2_approx(x[c * 8 + e]), exp2_approx(x[c * 8 + e + 1]));
-              float *const sum = l + g * 16 + c * 8 + e;
-              const Pair s = add2(pair(sum[0], sum[1]), w), v = mul2(w, pair(vr, vr));
-              sum[0] = lo(s);
-              sum[1] = hi(s);
-              p[e >> 1] = pack_f16(lo(v), hi(v));
+            for (int c = 0; c < 2; ++c) {
+              const float most = reduce_eight<true>(x + 8 * c, lane);
+              if ((lane & 3) == 0 && 2 * g + c < n8) C.part[warp][g * 16 + c * 8 + (lane >> 2)] = most;
             }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_line ^ ((g << 5) + (c << 4))), "r"(p[0]),
-                         "r"(p[1]), "r"(p[2]), "r"(p[3])
-                         : "memory");
           }
+          __syncthreads();
+          return tid < n8 * 8 ? fmaxf(fmaxf(C.part[0][tid], C.part[1][tid]), fmaxf(C.part[2][tid], C.part[3][tid])) : 0.0f;
+        };
+        float mx = 0.0f, mu = 0.0f;
+        // first with m in one number, then, where one is too large for that, its two parts one after the other
+#pragma unroll 1
+        for (int round = huge ? 1 : 0; round < 3; ++round) {
+          const float most = largest(round == 2 ? C.negx : C.zero, round == 1 ? 0.0f : lv);
+          if (tid < n8 * 8) {
+            if (round == 2) {
+              mu = most;
+            } else {
+              mx = round == 0 ? most : fmaxf(C.mx[tid], most);
+              if (round == 0 && fabsf(mx) >= 1048576.0f && fabsf(mx) < INFINITY) C.huge = 1;
+              if (round == 1) C.negx[tid] = mx == -INFINITY ? 0.0f : -mx;
+            }
+          }
+          __syncthreads();
+          if (round == 0 && !C.huge) break;
+        }
+        bool unset = false, raised = false;
+        if (tid < n8 * 8) {
+          const bool had = C.mx[tid] != -INFINITY;
+          const float old = had ? (C.mx[tid] - mx) + C.mu[tid] : 0.0f;  // of the sums so far, less mx
+          raised = !had || mu > old + kRaise;
+          C.factor[tid] = had && raised ? exp2_approx(old - mu) : 1.0f;  // (without a maximum O and l are zeros or NaN)
+          if (raised) {
+            C.mx[tid] = mx;
+            C.mu[tid] = mx == -INFINITY ? 0.0f : mu;
+          }
+          unset = C.mx[tid] == -INFINITY;
+          C.negx[tid] = unset ? 0.0f : -C.mx[tid];
+          C.negu[tid] = -C.mu[tid];
+          C.neg[tid] = C.negx[tid] + C.negu[tid];
+        }
+        force = __syncthreads_or(unset);
+        if (it > 0) {
+          ok = wait(C, &C.o_full, (it - 1) & 1) && ok;
+          fence_after();
+#pragma unroll
+          for (int c = 0; c < NMAX / 8; ++c)
+            if (c < n8) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) l[c * 8 + e] *= C.factor[c * 8 + e];
+            }
+#pragma unroll 1
+          for (int c = 0; c < n8; ++c) {
+            float o[8];
+            tmem_load_row(tmem + lanes + kO + c * 8, o);
+            tmem_wait_row(o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] *= C.factor[c * 8 + e];
+            tmem_store_8(tmem + lanes + kO + c * 8, o);
+          }
+        }
+        if (C.huge) {  // the exponents take the scores' place
+#pragma unroll 1
+          for (int g = 0; 2 * g < n8; ++g) {
+            float x[16];
+            exponents(g, x, C.negx);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = x[e] + C.negu[g * 16 + e];
+            store_scores(g, x);
+          }
+          by = 1.0f;
+          neg = C.zero;
+        }
+        tmem_wait_store();
       }
+      float top = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < NMAX / 16; ++g)
+        if (2 * g < n8) {
+          float x[16];
+          exponents(g, x, neg);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (2 * g + c < n8) {
+              uint32_t p[4];
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                top = max3(top, x[c * 8 + e], x[c * 8 + e + 1]);
+                const Pair w = pair(exp2_approx(x[c * 8 + e]), exp2_approx(x[c * 8 + e + 1]));
+                float *const sum = l + g * 16 + c * 8 + e;
+                const Pair s = add2(pair(sum[0], sum[1]), w), v = mul2(w, pair(vr, vr));
+                sum[0] = lo(s);
+                sum[1] = hi(s);
+                p[e >> 1] = pack_f16(lo(v), hi(v));
+              }
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_line ^ ((g << 5) + (c << 4))), "r"(p[0]),
+                           "r"(p[1]), "r"(p[2]), "r"(p[3])
+                           : "memory");
+            }
+        }
+      fence_proxy_async_smem();
+      fence_before();
+      if (!__syncthreads_or((!fresh && top + lv > kRaise) || !ok)) break;
+      // (whoever gave up did so before the barrier, and nobody waits before the next one)
+      stop = gave_up(C);
+      if (stop) break;
+      // The sums as they were.  (What the subtraction loses is 2^-24 of a weight that comes again; beside one that is no
+      // number of fp32 the sums so far, below 2^106, are nothing.)
+#pragma unroll
+      for (int g = 0; g < NMAX / 16; ++g)
+        if (2 * g < n8) {
+          float x[16];
+          exponents(g, x, neg);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float w = exp2_approx(x[e]);
+            if (2 * g + (e >> 3) < n8) l[g * 16 + e] = x[e] < 127.0f ? l[g * 16 + e] - w : 0.0f;
+          }
+        }
+      fresh = true;
+    }
+    if (stop) break;
     // ---- outputs ----
-    fence_proxy_async_smem();
-    fence_before();
-    __syncthreads();
     if (warp == 0) {
       fence_after();
       const uint64_t v_operand = operand(base + Y::kV, Y::kLines), p_operand = operand(base + Y::kP, Y::kLines);

@@ -105,7 +105,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 template <typename C>
 __device__ __forceinline__ bool wait(C &c, uint64_t *bar, uint32_t parity, bool expire = false) {
   if (!expire) {
-    if (mbar_try_wait_for(bar, parity, 2000)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t began = now_ns();
     for (uint32_t it = 0; it < kWaitPolls; ++it) {
       if (mbar_try_wait(bar, parity)) return true;
