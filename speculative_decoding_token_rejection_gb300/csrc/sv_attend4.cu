@@ -148,6 +148,7 @@ __device__ __forceinline__ void load_row(RawRow<D> &r, const uint8_t *data, cons
   else
     r.g[0] = load_word(group);
 }
+__device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // p + a * x + b * y
 __device__ __forceinline__ const uint8_t *step(const uint8_t *p, uint32_t a, uint32_t x, uint32_t b, uint32_t y) {
   uint64_t r;
@@ -202,23 +203,43 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
   };
   RawRow<D> krow, vrow;
   uint32_t ks = 0, vs = 0;
-  bool live = false;  // the key whose rows are in krow and vrow (or on their way) is there
-  auto load = [&](int it, int page) {
+  // Whether the key of the rows in krow and vrow (or on their way) is there; the same of the tile behind it, and where
+  // that one's key is: its bytes go to the L2 cache a tile before they are loaded.
+  bool live = false, next_live = false;
+  uint32_t next_page = 0, next_off = 0;
+  auto place = [&](int it, int page) {
     const int k = T.k_begin + it * kOwnKeys + tid;
     const bool in = k < T.k_end;
-    live = in && static_cast<uint32_t>(page) < static_cast<uint32_t>(P.c.num_blocks);
-    bad |= in && !live;
-    const uint32_t p = live ? page : 0, off = live ? k - div_by(k, L.page) * P.c.block_size : 0;
+    next_live = in && static_cast<uint32_t>(page) < static_cast<uint32_t>(P.c.num_blocks);
+    bad |= in && !next_live;
+    next_page = next_live ? page : 0;
+    next_off = next_live ? k - div_by(k, L.page) * P.c.block_size : 0;
+  };
+  auto load = [&]() {
     const OwnPlaces &A = C.at;
+    const uint32_t p = next_page, off = next_off;
+    live = next_live;
     load_row<D>(krow, step(A.k, A.page, p, A.token, off), step(A.k_group, A.group_page, p, A.group_token, off));
     load_row<D>(vrow, step(A.v, A.page, p, A.token, off), step(A.v_group, A.group_page, p, A.group_token, off));
     ks = load_word(step(A.k_scale, A.scale_page, p, A.scale_token, off));
     vs = load_word(step(A.v_scale, A.scale_page, p, A.scale_token, off));
   };
+  auto prefetch = [&]() {
+    const OwnPlaces &A = C.at;
+    const uint32_t p = next_page, off = next_off;
+    prefetch_line(step(A.k, A.page, p, A.token, off));
+    prefetch_line(step(A.v, A.page, p, A.token, off));
+    prefetch_line(step(A.k_group, A.group_page, p, A.group_token, off));
+    prefetch_line(step(A.v_group, A.group_page, p, A.group_token, off));
+    prefetch_line(step(A.k_scale, A.scale_page, p, A.scale_token, off));
+    prefetch_line(step(A.v_scale, A.scale_page, p, A.scale_token, off));
+  };
   int page = 0;
   if (ntiles > 0) {
-    load(0, page_of(0));
-    page = page_of(1);
+    place(0, page_of(0));
+    load();
+    place(1, page_of(1));
+    page = page_of(2);
   }
 
   if (tid == 0) {
@@ -372,8 +393,10 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
       unpack_values(1);
     }
     if (more) {
-      load(it + 1, page);
-      page = page_of(it + 2);
+      load();
+      place(it + 2, page);
+      prefetch();
+      page = page_of(it + 3);
     }
     ok = wait(C, &C.s_full, it & 1, P.expire) && ok;
     fence_after();
