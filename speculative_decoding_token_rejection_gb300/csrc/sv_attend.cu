@@ -633,13 +633,14 @@ constexpr int kTensorRows = 96;  // a shared prefix goes to the tensor-memory ke
 constexpr int kTensorLeast = 4;  // key tiles of a CTA of that kernel, where the prefix has as many
 constexpr int kTensorBegin = 7;  // and what beginning another (kv head, row tile) costs it, in key tiles
 constexpr int kChunkMost = 8192;                  // so that the longest request is no long tail
+constexpr int kChunkFew = 4096;                   // the same over a 4-bit cache, where a chunk's CTAs do not fill the SMs
 
 // Chunks for `keys` keys when `base` CTAs work on every chunk: enough to give
 // each SM two CTAs twice over, none below kChunkStep keys.
 // Returns the chunk count before chunks were rounded up to whole steps: no
 // fewer than `splits`, and never fewer for more keys, so that a workspace
 // sized for longer requests always holds.
-int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
+int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk, int most_keys = kChunkMost) {
   if (keys <= 0) {
     splits = 0;
     chunk = kChunkStep;
@@ -647,7 +648,7 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk) {
   }
   const int64_t want = std::max<int64_t>(1, 4LL * num_sms / std::max<int64_t>(1, base));
   const int most = ceil_div(keys, kChunkStep);
-  splits = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(want, ceil_div(keys, kChunkMost))));
+  splits = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(want, ceil_div(keys, most_keys))));
   const int bound = splits;
   chunk = ceil_div(ceil_div(keys, splits), kChunkStep) * kChunkStep;
   splits = ceil_div(keys, chunk);
@@ -706,8 +707,9 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   L.own_tiles = ceil_div((p.G + 1) * static_cast<int64_t>(p.group), own_rows(p));
   L.prefix_tiles = ceil_div(L.rows, 8 * kGroups);
   // (at least one private chunk, though no request may have private keys: its CTAs look at the requests' ranges)
-  int bound = std::max(1, cut(static_cast<int64_t>(p.N) * p.c.num_kv_heads * L.own_tiles, p.max_seq - p.prefix, num_sms,
-                              L.own_splits, L.own_chunk));
+  const int64_t base = static_cast<int64_t>(p.N) * p.c.num_kv_heads * L.own_tiles;
+  int bound = std::max(1, cut(base, p.max_seq - p.prefix, num_sms, L.own_splits, L.own_chunk,
+                              four_bits(p) && base < 4LL * num_sms ? kChunkFew : kChunkMost));
   L.own_splits = std::max(1, L.own_splits);
   const int64_t image_tiles = ceil_div(p.prefix, kPrefixKeyTile), tensor_tiles = ceil_div(L.rows, kPrefixRowTile);
   const int64_t items = tensor_tiles * p.c.num_kv_heads, tiles = items * image_tiles;

@@ -66,6 +66,7 @@ struct OwnControl {
   float mx[kOwnRows4], mu[kOwnRows4];  // m = mx + mu, mx -inf without one
   float part[4][kOwnRows4];            // of the four warps that hold a row
   uint32_t none[kOwnRows4];            // the row sees a value scale that is no number
+  int64_t to[kOwnRows4];               // the row's place in the output, or its partial result's
 };
 
 // Shared memory: [D / 64][128 keys][128 bytes] of V, weights of up to 64 rows in 128-byte lines, [D / 64][NMAX rows][128
@@ -629,11 +630,13 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
     const float m = lost ? -INFINITY : C.mx[tid] + C.mu[tid];
     const float sum = lost ? nan : (C.part[0][tid] + C.part[1][tid]) + (C.part[2][tid] + C.part[3][tid]);
     const int64_t at = (T.first + j) * P.Hq + hq;
+    const int64_t slot = at * L.slots + L.prefix_splits + T.split;
     if (T.whole) {
       if (P.lse) P.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     } else {
-      L.part_ml[at * L.slots + L.prefix_splits + T.split] = make_float2(m, sum);
+      L.part_ml[slot] = make_float2(m, sum);
     }
+    C.to[tid] = T.whole ? (T.first + j) * P.out_token + hq * P.out_head : slot * D;
     // (a row without keys that count has the output 0.  Some w was 2^-log2(value_scale / W) at least, so sum is above
     // 2^-101 otherwise, and far below 2^126.)
     C.factor[tid] = lost || C.none[tid] ? nan : !T.whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -642,24 +645,27 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
   // a lane holds a dimension: lane i of the tensor memory for head_dim 128, for 64 the first half of each warp's
   const int at = D == 128 ? tid : warp * 16 + (lane & 15);
   const int dim = mixed<FMT>() ? mixed_place(at) : at;
+  const float scale = it > 0 ? kScaleUnit * unit4<FMT>() : lost ? nan : 0.0f;
 #pragma unroll 1
   for (int c = 0; c < n8; ++c) {
     float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 1.0f;
     if (it > 0) {
       tmem_load_row(tmem + lanes + kO + c * 8, o);
       tmem_wait_row(o);
     }
+    if (D == 128 || lane < 16) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int r = c * 8 + e;
-      if (r < T.rows && (D == 128 || lane < 16)) {
-        const int lr = T.r0 + r, j = div_by(lr, L.group), hq = T.h * P.group + lr - j * P.group;
-        const float f = C.factor[r], y = it > 0 ? o[e] * f * (kScaleUnit * unit4<FMT>()) : lost ? nan : 0.0f;
-        if (T.whole)
-          P.out[(T.first + j) * P.out_token + hq * P.out_head + dim] =
-              static_cast<uint16_t>(pack_bf16(f == 0.0f ? 0.0f : y, 0.0f));
-        else
-          L.part_o[(((T.first + j) * P.Hq + hq) * L.slots + L.prefix_splits + T.split) * D + dim] = y;
+      for (int e = 0; e < 8; ++e) {
+        const int r = c * 8 + e;
+        if (r < T.rows) {
+          const float f = C.factor[r], y = f == 0.0f ? 0.0f : o[e] * f * scale;
+          if (T.whole)
+            P.out[C.to[r] + dim] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
+          else
+            L.part_o[C.to[r] + dim] = y;
+        }
       }
     }
   }
