@@ -99,33 +99,51 @@ __global__ void __launch_bounds__(kThreads) rotate_any_kernel(const RotateParams
   }
 }
 
-// Sixteen bytes of a row: VE elements.
+// Sixteen bytes of a row.
 template <bool BF16>
-struct Vector {
-  static constexpr int kElements = BF16 ? 8 : 4;
-};
+constexpr int vector_elements() {
+  return BF16 ? 8 : 4;
+}
 template <bool BF16>
 __device__ __forceinline__ uint4 load_vector(const void *p, int64_t at) {
   return *reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + at * (BF16 ? 2 : 4));
 }
-template <bool BF16>
-__device__ __forceinline__ void numbers(const uint4 &v, float *x) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The elements of two vectors, first and second ones of the pairs apart: i of
+// either vector, or neighbours (those of the first vector first).
+template <bool BF16, bool INTERLEAVED>
+__device__ __forceinline__ void split(const uint4 v[2], float *a, float *b) {
+  constexpr int VE = vector_elements<BF16>();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (BF16) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    } else {
-      x[i] = __uint_as_float(w[i]);
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    float x[VE];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (BF16) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[(2 * i + 1) % VE] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        x[i] = __uint_as_float(w[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      if (INTERLEAVED)
+        (i & 1 ? b : a)[k * (VE / 2) + (i >> 1)] = x[i];
+      else
+        (k ? b : a)[i] = x[i];
     }
   }
 }
-template <bool BF16>
-__device__ __forceinline__ void store_vector(void *p, int64_t at, const float *x) {
+template <bool BF16, bool INTERLEAVED>
+__device__ __forceinline__ void store_split(void *p, int64_t at, int k, const float *a, const float *b) {
+  constexpr int VE = vector_elements<BF16>();
+  float x[VE];
+#pragma unroll
+  for (int i = 0; i < VE; ++i) x[i] = INTERLEAVED ? (i & 1 ? b : a)[k * (VE / 2) + (i >> 1)] : (k ? b : a)[i];
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = BF16 ? pack_bf16(x[2 * i], x[2 * i + 1]) : __float_as_uint(x[i]);
+  for (int i = 0; i < 4; ++i) w[i] = BF16 ? pack_bf16(x[2 * i], x[(2 * i + 1) % VE]) : __float_as_uint(x[i]);
   *reinterpret_cast<uint4 *>(static_cast<char *>(p) + at * (BF16 ? 2 : 4)) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -133,12 +151,19 @@ __device__ __forceinline__ void store_vector(void *p, int64_t at, const float *x
 // times), whose pairs lie in them: elements i .. and i + rotary / 2 .., or
 // neighbouring ones, or such as stay.  `lanes` neighbouring lanes share a row,
 // and walk `heads` heads of one token, kAhead rows' loads in flight.
-constexpr int kAhead = 4;
+//
+// 4096 tokens x 40 heads x 128 bf16: 13.7 us (89 % of the copy rate), with norms
+// 20.3; 32768 tokens with norms 126 (79 %).  A row's norm is a chain (load, sum,
+// shuffles, root) that more rows in flight hide: four of bf16 rows with norms on
+// two CTAs an SM, where two rows on three CTAs took 21.8 and 149 us.  Without
+// norms, or in fp32 (whose rows are twice the registers), more CTAs are better:
+// 15.3 us with four rows, and 80 against 90 for a prompt's keys (18000 fp32 tokens).
+constexpr int rows_ahead(bool bf16, bool norm) { return bf16 && norm ? 4 : 2; }
 template <bool BF16, bool INTERLEAVED, bool NORM, int UNITS>
-__global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_constant__ RotateParams P, const int lanes,
-                                                            const int heads, const FastDiv parts) {
+__global__ void __launch_bounds__(kThreads, NORM && BF16 ? 2 : 3)
+    rotate_kernel(const __grid_constant__ RotateParams P, const int lanes, const int heads, const FastDiv parts) {
   pdl_enter();
-  constexpr int VE = Vector<BF16>::kElements;
+  constexpr int VE = vector_elements<BF16>(), kAhead = rows_ahead(BF16, NORM);
   const int lane = threadIdx.x & 31, col = lane & (lanes - 1);
   const uint32_t group = lanes == 32 ? 0xFFFFFFFFu : ((1u << lanes) - 1u) << (lane & ~(lanes - 1));
   const int item = static_cast<int>((blockIdx.x * static_cast<uint32_t>(kThreads) + threadIdx.x) / lanes);
@@ -147,38 +172,34 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
   const int32_t position = P.positions[token];
   if (position < 0) return;
   const int last = min(first + heads, P.Hq + P.Hk);
+  const float mean = 1.0f / static_cast<float>(P.D);
 
-  int at[UNITS][2];  // where the lane's vectors begin, -1 for none
+  int at[UNITS][2];     // where the lane's vectors begin, -1 for none
+  bool turns[UNITS][2]; // their pairs are turned (in the half layout both vectors' are or none)
   float c[UNITS][VE], s[UNITS][VE];
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
     const int unit = u * lanes + col, turned = P.rotary / (2 * VE);
-    if (INTERLEAVED) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        at[u][v] = (2 * unit + v) * VE < P.D ? (2 * unit + v) * VE : -1;
-#pragma unroll
-        for (int e = 0; e < VE / 2; ++e) {
-          const int i = (2 * unit + v) * (VE / 2) + e;
-          s[u][v * (VE / 2) + e] = 0.0f;
-          c[u][v * (VE / 2) + e] = 1.0f;
-          if (2 * i < P.rotary) angle(position, P.turns[i], P.magnitude, s[u][v * (VE / 2) + e], c[u][v * (VE / 2) + e]);
-        }
-      }
-    } else {
-      const int rest = P.rotary + (unit - turned) * 2 * VE;
-      at[u][0] = unit < turned ? unit * VE : rest < P.D ? rest : -1;
-      at[u][1] = unit < turned ? unit * VE + P.rotary / 2 : rest + VE < P.D ? rest + VE : -1;
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        s[u][e] = 0.0f;
-        c[u][e] = 1.0f;
-        if (unit < turned) angle(position, P.turns[unit * VE + e], P.magnitude, s[u][e], c[u][e]);
+    for (int v = 0; v < 2; ++v) {
+      const int rest = P.rotary + (unit - turned) * 2 * VE + v * VE, pair = (2 * unit + v) * VE;
+      if (INTERLEAVED) {
+        at[u][v] = pair < P.D ? pair : -1;
+        turns[u][v] = pair < P.rotary;
+      } else {
+        at[u][v] = unit < turned ? unit * VE + v * (P.rotary / 2) : rest < P.D ? rest : -1;
+        turns[u][v] = unit < turned;
       }
     }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      s[u][e] = 0.0f;
+      c[u][e] = 1.0f;
+      if (turns[u][INTERLEAVED ? e / (VE / 2) : 0]) angle(position, P.turns[unit * VE + e], P.magnitude, s[u][e], c[u][e]);
+    }
   }
-  float w[NORM ? UNITS : 1][2][VE];
-  const void *held = nullptr;  // the weights in w
+  float wa[NORM ? UNITS : 1][VE], wb[NORM ? UNITS : 1][VE];
+  const void *held = nullptr;  // the weights in wa and wb
   for (int h = first; h < last; h += kAhead) {
     uint4 raw[kAhead][UNITS][2];
 #pragma unroll
@@ -194,57 +215,75 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
           if (h + k < last && at[u][v] >= 0) raw[k][u][v] = load_vector<BF16>(S.in, from + at[u][v]);
         }
     }
+    float r[kAhead];
+    if (NORM) {  // all rows' sums before the first is needed
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        Pair sum = pair(0.0f, 0.0f);
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          float a[VE], b[VE];
+          split<BF16, INTERLEAVED>(raw[k][u], a, b);
+#pragma unroll
+          for (int e = 0; e < VE; e += 2) {
+            sum = fma2(pair(a[e], a[e + 1]), pair(a[e], a[e + 1]), sum);
+            sum = fma2(pair(b[e], b[e + 1]), pair(b[e], b[e + 1]), sum);
+          }
+        }
+        r[k] = lo(sum) + hi(sum);
+      }
+      for (int i = lanes >> 1; i; i >>= 1)
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) r[k] += __shfl_xor_sync(group, r[k], i);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) r[k] = rsqrtf(fmaf(r[k], mean, P.eps));
+    }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (h + k >= last) break;
       const bool key = h + k >= P.Hq;
       const RotateSide &S = key ? P.k : P.q;
       const int64_t to = token * S.out_token + (h + k - (key ? P.Hq : 0)) * S.out_head;
-      float x[UNITS][2][VE];
+      const bool norm = NORM && S.weight;
+      float a[UNITS][VE], b[UNITS][VE];
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u)
+      for (int u = 0; u < UNITS; ++u) split<BF16, INTERLEAVED>(raw[k][u], a[u], b[u]);
+      if (norm && S.weight != held) {
+        held = S.weight;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) numbers<BF16>(raw[k][u][v], x[u][v]);
-      if (NORM && S.weight) {
-        if (S.weight != held) {
-          held = S.weight;
+        for (int u = 0; u < UNITS; ++u) {
+          uint4 w[2];
 #pragma unroll
-          for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-              if (at[u][v] >= 0) numbers<BF16>(load_vector<BF16>(held, at[u][v]), w[u][v]);
+          for (int v = 0; v < 2; ++v)
+            w[v] = at[u][v] >= 0 ? load_vector<BF16>(held, at[u][v]) : make_uint4(0, 0, 0, 0);
+          split<BF16, INTERLEAVED>(w, wa[u], wb[u]);
         }
-        float sum = 0.0f;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) sum = fmaf(x[u][0][e], x[u][0][e], fmaf(x[u][1][e], x[u][1][e], sum));
-        for (int b = lanes >> 1; b; b >>= 1) sum += __shfl_xor_sync(group, sum, b);
-        const float r = __frsqrt_rn(sum / static_cast<float>(P.D) + P.eps);
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            x[u][0][e] = x[u][0][e] * r * w[u][0][e];
-            x[u][1][e] = x[u][1][e] * r * w[u][1][e];
-          }
       }
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
-        float y[2][VE];
+        float p[VE], q[VE];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          // (pairs side by side lie in one vector, the first VE / 2 of them in the first one)
-          float &a = INTERLEAVED ? x[u][e / (VE / 2)][2 * (e % (VE / 2))] : x[u][0][e];
-          float &b = INTERLEAVED ? x[u][e / (VE / 2)][2 * (e % (VE / 2)) + 1] : x[u][1][e];
-          float &p = INTERLEAVED ? y[e / (VE / 2)][2 * (e % (VE / 2))] : y[0][e];
-          float &q = INTERLEAVED ? y[e / (VE / 2)][2 * (e % (VE / 2)) + 1] : y[1][e];
-          p = a * c[u][e] - b * s[u][e];
-          q = b * c[u][e] + a * s[u][e];
+        for (int e = 0; e < VE; e += 2) {
+          Pair x = pair(a[u][e], a[u][e + 1]), y = pair(b[u][e], b[u][e + 1]);
+          if (norm) {
+            x = mul2(x, mul2(pair(wa[u][e], wa[u][e + 1]), pair(r[k], r[k])));
+            y = mul2(y, mul2(pair(wb[u][e], wb[u][e + 1]), pair(r[k], r[k])));
+          }
+          // (what stays keeps clear of its neighbours: an infinity times a sine of zero is no number)
+          if (turns[u][INTERLEAVED ? e / (VE / 2) : 0]) {
+            const Pair cc = pair(c[u][e], c[u][e + 1]), ss = pair(s[u][e], s[u][e + 1]);
+            const Pair t = fma2(y, pair(-lo(ss), -hi(ss)), mul2(x, cc));
+            y = fma2(y, cc, mul2(x, ss));
+            x = t;
+          }
+          p[e] = lo(x);
+          p[e + 1] = hi(x);
+          q[e] = lo(y);
+          q[e + 1] = hi(y);
         }
 #pragma unroll
         for (int v = 0; v < 2; ++v)
-          if (at[u][v] >= 0) store_vector<BF16>(S.out, to + at[u][v], y[v]);
+          if (at[u][v] >= 0) store_split<BF16, INTERLEAVED>(S.out, to + at[u][v], v, p, q);
       }
     }
   }
@@ -293,9 +332,10 @@ cudaError_t launch_rotate(const RotateParams &p, bool bf16, int num_sms, cudaStr
   int lanes = 1;
   while (lanes < need && lanes < 32) lanes *= 2;
   const int units = (need + lanes - 1) / lanes;
-  // a token's heads are cut over more lanes while that fills the SMs (1024 threads each), no finer than kAhead heads
+  // a token's heads are cut over more lanes while that fills the SMs (1024 threads each), no finer than a step's rows
+  const int step = rows_ahead(bf16, p.q.weight || p.k.weight);
   int parts = static_cast<int>((num_sms * 1024LL + p.T * lanes - 1) / (p.T * lanes));
-  if (parts > (all + kAhead - 1) / kAhead) parts = (all + kAhead - 1) / kAhead;
+  if (parts > (all + step - 1) / step) parts = (all + step - 1) / step;
   const int heads = (all + parts - 1) / parts;
   parts = (all + heads - 1) / heads;
   cfg.gridDim = dim3(static_cast<unsigned>((p.T * parts * lanes + kThreads - 1) / kThreads));

@@ -210,3 +210,19 @@ def test_no_tokens_and_no_heads(ver):
     ver.rotate(q=torch.empty(5, 0, 64, device="cuda"), positions=torch.zeros(5, dtype=torch.int32, device="cuda"),
                frequencies=f)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,r,at", [(128, 64, 100), (128, 64, 64), (80, 20, 33), (128, 0, 5), (64, 32, 63)])
+def test_an_infinity_in_what_stays_stays_alone(ver, D, r, at, dtype, interleaved):
+    q, key, pos, _ = inputs(30, 4, 1, D, dtype, at)
+    q[:, 1, at], q[:, 2, at] = math.inf, math.nan
+    f = sv.RotaryFrequencies(r)
+    qo = torch.empty_like(q)
+    ver.rotate(q=q, positions=pos, frequencies=f, q_out=qo, interleaved=interleaved)
+    live = pos >= 0
+    assert bool((qo[live, 1, at] == math.inf).all()) and bool(qo[live, 2, at].isnan().all())
+    clean, want = q.clone(), qo.clone()
+    clean[:, 1:3, at] = want[:, 1:3, at] = 0
+    check(want, clean, pos, f, interleaved=interleaved)
