@@ -5,8 +5,15 @@
 // pages given back), then every row finds its request.  One CTA does the sums
 // and the requests' outputs, 1024 requests at a time; a row's request is the
 // last one that begins at or before it, found by writing requests to the places
-// where they begin and taking a running maximum.  With few rows the same CTA
-// does those too, otherwise a second kernel does, kRowsCta rows a CTA.
+// where they begin and taking a running maximum.  A small step's rows, and the
+// pages given back, are the same CTA's work, otherwise a second kernel's:
+// kRowsCta rows or kBackCta requests a CTA.
+//
+// Bound by latency.  4 requests x 5 rows: 5.8 us for the launch and the chain
+// (7.2 as two kernels); 512 requests that hold 512 pages each, 2700 rows, a
+// tenth done: 9.3 us (26 in one CTA); 64 prompts, 0.5 million rows: 11.9 us;
+// 4096 requests: 18.0 us.  One CTA is the faster up to 250 requests of 64
+// pages (6.8 us against 9.0) or 16 of 1024 (7.8, 8.0; 32: 10.3 against 8.0).
 //
 // A page newly given to a request is written to its table by the first row that
 // lies in it, which has just read it from the ring.
@@ -21,11 +28,13 @@ namespace {
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr int kRowsCta = 1024;      // rows of a CTA of the second kernel, and of a step of the first
 constexpr int kRowsThreads = 256;
-constexpr int kRowsOne = 4096;      // requests and rows that one CTA does by itself
+constexpr int kBackCta = 4;         // requests of a CTA of the second kernel that gives pages back
+constexpr int kRowsOne = 2048;      // rows that one CTA does by itself
+constexpr int64_t kPagesOne = 20480;  // and block table entries, which may all be given back
 
 struct Workspace {  // of every request
   int32_t *end;    // its last row + 1 (at most R)
-  int32_t *start;  // place in the ring of the first page it is given
+  int32_t *start;  // place in the ring of the first page it is given; ~place of the first it gives back
   int32_t *held;   // pages held before
 };
 __device__ __forceinline__ Workspace workspace_of(const PlanParams &P) {
@@ -119,6 +128,19 @@ __device__ __forceinline__ int request_behind(const int32_t *end, int n, int64_t
   return lo;
 }
 
+// The pages of a request that is done go to the places behind the ring's end, by `threads` threads.
+__device__ __forceinline__ void give_back(const PlanParams &P, const Workspace &W, int i, int thread, int threads) {
+  if (W.start[i] >= 0) return;
+  const int64_t to = ~W.start[i];
+  const int count = W.held[i];
+  const int32_t *const row = P.tables + i * P.table_stride;
+#pragma unroll 8
+  for (int k = thread; k < count; k += threads) {
+    const int64_t at = to + k;  // (more pages than the ring has places would come round more than once)
+    P.ring[at < P.capacity ? at : at % P.capacity] = row[k];
+  }
+}
+
 template <bool ROWS>
 __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanParams P) {
   pdl_enter();
@@ -147,7 +169,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
       bits |= SV_DATA_BAD_PARAM;
     }
     if (n < 0) n = 0;
-    const int64_t len = p + n, need = len / P.block + (len % P.block != 0);
+    const int64_t len = p + n;
+    const uint32_t pages = static_cast<uint32_t>(len) / static_cast<uint32_t>(P.block);  // (both counts are below 2^31)
+    const int64_t need = pages + (pages * static_cast<uint32_t>(P.block) != static_cast<uint32_t>(len));
     if (good && (need > P.width || len > 0x7FFFFFFF || static_cast<int64_t>(held) * P.block < p)) {
       good = false;
       bits |= SV_DATA_BAD_PARAM;
@@ -177,27 +201,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
     }
     const bool takes = good && want > 0;
     if (in) {
-      const int64_t place = from + x.want - want;  // (below twice the capacity)
+      int64_t place = 0;
+      if (takes) place = from + x.want - want;  // (below twice the capacity)
       W.end[i] = static_cast<int32_t>(min(x.rows, P.R));
-      W.start[i] = takes ? static_cast<int32_t>(place < P.capacity ? place : place - P.capacity) : 0;
+      W.start[i] = returns ? ~static_cast<int32_t>((to + x.back - held) % P.capacity)
+                           : static_cast<int32_t>(place < P.capacity ? place : place - P.capacity);
       W.held[i] = held;
       if (P.cu) P.cu[i] = static_cast<int32_t>(min(x.rows - (i + 1), int64_t{0x7FFFFFFF}));
       P.held_out[i] = returns ? 0 : takes ? static_cast<int32_t>(need) : held;
       P.seq_lens[i] = good ? static_cast<int32_t>(len) : 0;
     }
     if (takes) atomicMax(&given, static_cast<unsigned long long>(x.want));
-    // pages that are given back: a warp copies its lanes' requests one after another
-    const int64_t behind = to + x.back - held;
-    for (uint32_t give = __ballot_sync(0xFFFFFFFFu, returns); give; give &= give - 1) {
-      const int who = __ffs(give) - 1, count = __shfl_sync(0xFFFFFFFFu, held, who);
-      const int64_t at = __shfl_sync(0xFFFFFFFFu, behind, who);
-      const int32_t *const row = P.tables + static_cast<int64_t>(base + warp * 32 + who) * P.table_stride;
-#pragma unroll 8
-      for (int k = lane; k < count; k += 32) {
-        const int64_t x_at = at + k;
-        P.ring[x_at < P.capacity ? x_at : x_at % P.capacity] = row[k];
-      }
-    }
     __syncthreads();  // (the sums have been read, and the outputs are there)
   }
   if (P.N == 0) __syncthreads();
@@ -209,14 +223,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
     bits = __reduce_or_sync(0xFFFFFFFFu, bits);
     if (lane == 0 && bits) atomicOr(P.status, static_cast<int>(bits));
   }
-  if (ROWS)
+  if (ROWS) {
+    int warps = 1;  // of a request
+    while (warps < kPlanWarps && warps * P.N < kPlanWarps) warps *= 2;
+    const int at_once = kPlanWarps / warps;
+    for (int i = warp % at_once; i < P.N; i += at_once) give_back(P, W, i, (warp / at_once) * 32 + lane, warps * 32);
     for (int r0 = 0; r0 < P.R; r0 += kRowsCta) do_rows<kPlanThreads>(P, W, r0, 0, P.N - 1, mark, warp_last);
+  }
 }
 
-__global__ void __launch_bounds__(kRowsThreads) plan_rows_kernel(const PlanParams P) {
+// The first `rows_ctas` CTAs take rows, the others requests that give pages back.
+__global__ void __launch_bounds__(kRowsThreads) plan_rows_kernel(const PlanParams P, int rows_ctas) {
   pdl_enter();
   __shared__ int32_t mark[kRowsCta], warp_last[kRowsThreads / 32], range[2];
   const Workspace W = workspace_of(P);
+  if (static_cast<int>(blockIdx.x) >= rows_ctas) {
+    const int first = (blockIdx.x - rows_ctas) * kBackCta;
+    for (int i = first; i < min(first + kBackCta, P.N); ++i) give_back(P, W, i, threadIdx.x, kRowsThreads);
+    return;
+  }
   const int r0 = blockIdx.x * kRowsCta, warp = threadIdx.x >> 5;
   if (warp < 2) {
     const int i = request_behind(W.end, P.N, warp ? min(r0 + static_cast<int64_t>(kRowsCta), P.R) - 1 : r0);
@@ -233,7 +258,7 @@ int64_t plan_workspace_bytes(int32_t n) { return 12 * static_cast<int64_t>(n) + 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
-  const bool one = p.R <= kRowsOne && p.N <= kRowsOne;
+  const bool one = p.R <= kRowsOne && static_cast<int64_t>(p.N) * (p.width + 1) <= kPagesOne;
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = stream;
@@ -241,10 +266,10 @@ cudaError_t launch_plan(const PlanParams &p, cudaStream_t stream) {
   cfg.numAttrs = launch_attrs(attr, 0, p.pdl);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, one ? plan_requests_kernel<true> : plan_requests_kernel<false>, p);
   if (e != cudaSuccess || one) return e;
-  if (p.R == 0) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>((p.R + kRowsCta - 1) / kRowsCta));
+  const int64_t rows = (static_cast<int64_t>(p.R) + kRowsCta - 1) / kRowsCta;
+  cfg.gridDim = dim3(static_cast<unsigned>(rows + (static_cast<int64_t>(p.N) + kBackCta - 1) / kBackCta));
   cfg.blockDim = dim3(kRowsThreads);
-  return cudaLaunchKernelEx(&cfg, plan_rows_kernel, p);
+  return cudaLaunchKernelEx(&cfg, plan_rows_kernel, p, static_cast<int>(rows));
 }
 
 }  // namespace sv
