@@ -13,6 +13,14 @@ A batch of requests shares a system prompt.  A step takes each request's drafts:
 6. the accepted tokens' cache rows are read back, as a server does that moves a
    request                                                      kv_read
 
+serve() does such steps for requests that come and go, over a 4-bit cache whose
+pages they take and give back: before the keys are written,
+
+0. every request's missing pages are taken from the free ones, those of requests
+   that are done go back, and rows get their positions and slots    plan_step
+   queries and keys get a norm of each head and turn to their
+   positions                                                        rotate
+
 The model is one attention layer with random weights; its drafts come from a
 noisy copy of its own head, so some are accepted.  Run it on a GPU:
 
@@ -127,8 +135,113 @@ def run(requests=8, gamma=4, prompt=64, steps=4, vocab=2000, q_heads=8, kv_heads
     return texts, logprobs, computed.tolist()
 
 
+def serve(places=4, requests=10, gamma=3, prompt=60, new_tokens=20, vocab=1000, q_heads=8, kv_heads=2, dim=64, block=16,
+          fmt="e2m1", seed=0, device="cuda", say=print):
+    """Requests with prompts of up to `prompt` tokens, of which `places` run at once; each gets `new_tokens` and a step's
+    surplus.  Returns their texts and what the cache's books say at the end."""
+    device = torch.device(device, torch.cuda.current_device())
+    gen = torch.Generator(device=device).manual_seed(seed)
+    model = Model(vocab, q_heads, kv_heads, dim, gen, device)
+    N, G = places, gamma
+    longest = prompt + new_tokens + 2 * (G + 1)
+    ver = sv.Verifier(N, max(G, prompt - 1), vocab, device=device.index)
+    frequencies = sv.RotaryFrequencies(dim, device=device)
+    norms = torch.rand(2, dim, generator=gen, device=device).add_(0.5).to(torch.bfloat16)
+
+    def i32(*shape, fill=0):
+        return torch.full(shape, fill, dtype=torch.int32, device=device)
+
+    # a cache of as many pages as the places may need, all of them free
+    width = -(-longest // block)
+    lead = (N * width, kv_heads, block)
+    sides = {x: torch.zeros(*lead, dim // 2, dtype=torch.uint8, device=device) for x in "kv"}
+    groups = {x + "_group": torch.zeros(*lead, dim // 16, device=device).to(torch.float8_e4m3fn) for x in "kv"}
+    scales = {x + "_scale": torch.zeros(lead, device=device) for x in "kv"}
+    cache = sv.KVCache4(**sides, **groups, **scales, format=fmt)
+    tables, held, computed = i32(N, width), i32(N), i32(N, fill=-1)
+    free, span = torch.arange(N * width, dtype=torch.int32, device=device), torch.tensor([0, N * width], device=device)
+    workspace = ver.plan_workspace(num_reqs=N)
+    status = i32(1)
+
+    waiting = [torch.randint(0, vocab, (int(n),), generator=gen, device=device) for n in
+               torch.randint(1, prompt + 1, (requests,), generator=gen, device=device)]
+    texts, running = [[] for _ in waiting], [None] * N  # the request in each place
+    coming = list(range(requests))
+    last = torch.zeros(N, dtype=torch.long, device=device)
+
+    def prepare(new):
+        """The plan of a step of new[i] tokens a request, and a function of the tokens to the rows' target logits."""
+        cu = i32(N)
+        most = max(new) - 1
+        plan = ver.plan_step(num_new_tokens=torch.tensor(new, dtype=torch.int32, device=device),
+                             num_computed_tokens=computed, block_tables=tables, held_pages=held, free_pages=free,
+                             free_range=span, block_size=block, num_rows=sum(new), cu_num_draft_tokens=cu,
+                             workspace=workspace, status=status)
+
+        def forward(tokens):
+            q, key, value = model.project(tokens)
+            ver.rotate(q=q, key=key, positions=plan.positions, frequencies=frequencies, q_weight=norms[0],
+                       key_weight=norms[1])
+            ver.kv_write(cache=cache, key=key, value=value, slot_mapping=plan.slot_mapping, status=status)
+            return model.logits(ver.attend(q=q, cache=cache, block_tables=tables, seq_lens=plan.seq_lens,
+                                           max_seq_len=width * block, max_spec_len=most, scale=dim ** -0.5,
+                                           cu_num_draft_tokens=cu, status=status))
+        return plan, forward
+
+    step = 0
+    while coming or any(x is not None for x in running):
+        new = [1] * N
+        arriving = [i for i in range(N) if running[i] is None][:len(coming)]
+        if arriving:  # prompts of requests that come; the others go on by a token
+            for i in arriving:
+                running[i] = coming.pop(0)
+                new[i], computed[i] = len(waiting[running[i]]), 0
+            tokens = torch.cat([waiting[running[i]] if i in arriving else last[i:i + 1] for i in range(N)])
+            plan, forward = prepare(new)
+            target = forward(tokens)[torch.tensor(new, device=device).cumsum(0) - 1]
+            drafts = dict(draft_ids=i32(0), draft=target[:0], max_spec_len=0)
+            slots = None
+        else:
+            new = [G + 1] * N
+            tokens = torch.zeros(N, G + 1, dtype=torch.long, device=device)
+            tokens[:, 0] = last
+            draft = torch.empty(N, G, vocab, dtype=torch.bfloat16, device=device)
+            plan, forward = prepare(new)
+            for j in range(G):
+                noisy = forward(tokens.view(-1)).view(N, G + 1, vocab)[:, j].float()
+                noisy = noisy + 0.5 * torch.randn(noisy.shape, generator=gen, device=device)
+                draft[:, j] = noisy.to(torch.bfloat16)
+                tokens[:, j + 1] = draft[:, j].float().argmax(-1)
+            target = forward(tokens.view(-1))
+            drafts = dict(draft_ids=tokens[:, 1:].reshape(-1).to(torch.int32).contiguous(), draft=draft.view(N * G, vocab),
+                          max_spec_len=G)
+            slots = plan.slot_mapping
+        live = plan.seq_lens > 0
+        after = torch.where(live, plan.seq_lens, computed)
+        result = ver.verify(entry="logits", target=target.contiguous(), num_reqs=N, seed=seed, offset=step, status=status,
+                            num_computed_tokens=after, slot_mapping=slots, **drafts)
+        computed.copy_(torch.where(live, after, computed))
+        last = result.out_tokens.gather(1, result.num_accepted[:, None].long())[:, 0].long()
+        accepted = result.num_accepted.tolist()
+        for i, request in enumerate(running):
+            if request is None:
+                continue
+            texts[request] += result.out_tokens[i, :accepted[i] + 1].tolist()
+            if len(texts[request]) >= new_tokens:  # its pages go back in the next step, or to the next request here
+                running[i], computed[i] = None, -1
+        say(f"step {step}: {'prompts' if arriving else 'drafts'}, running {running}, free pages {int(span[1] - span[0])}")
+        step += 1
+    # the last ones' pages
+    ver.plan_step(num_new_tokens=i32(N), num_computed_tokens=computed, block_tables=tables, held_pages=held, free_pages=free,
+                  free_range=span, block_size=block, num_rows=0, workspace=workspace, status=status)
+    assert int(status.item()) == 0
+    ver.close()
+    return texts, held.tolist(), span.tolist(), free.tolist()
+
+
 # Sizes at which attention computes the prompt once for the batch (in smaller calls every request reads it for itself).
 SHARED = dict(requests=512, prompt=768, q_heads=8, kv_heads=8)
 
 if __name__ == "__main__":
     run()
+    serve()
