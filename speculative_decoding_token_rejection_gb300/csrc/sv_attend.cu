@@ -671,6 +671,10 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk, int most_k
 // 1024 77 | 50, 2048 84 | 78, 4096 94 | 136; 512 x 8, 512 305 | 257, 1024 335 | 365;
 // 512 x 1, 256 118 | 95, 512 120 | 126; 2 x 5 (40 rows), 4096 33 | 29, 16384 48 | 38;
 // 16 x 1 (64 rows), 256 17 | 17, 1024 19 | 22.
+// Over the 4-bit cache few rows share a prefix on the tensor cores too, from the
+// same length: 16 requests x 1 token (64 rows) 4096 42 | 35, 8192 45 | 53, 16384 68 | 104,
+// 65536 176 | 303; 80 x 1 of one query head a kv head, 1024 46 | 43, 4096 51 | 124, 16384
+// 78 | 355; 8 x 2, 16384 70 | 56, 65536 178 | 179; 4 x 5, 65536 179 | 93 (never shared).
 bool four_bits(const AttendParams &p) { return p.c.format == SV_CACHE_E2M1 || p.c.format == SV_CACHE_INT4; }
 int own_rows(const AttendParams &p) { return four_bits(p) ? own4_rows(p) : 8 * kGroups; }
 
@@ -679,20 +683,19 @@ AttendParams short_prefix(AttendParams p) {
   // (the rows there may be, so that calls with fewer tokens choose alike)
   const int64_t rows = p.N * own;
   int64_t saved = p.N * H * own_tiles * (24 + 7 * ceil_div(ceil_div(own, 8), own_tiles)), begin, most;  // ps a key; ps; keys
-  if (four_bits(p) && rows < kTensorRows) {  // (few rows read it each for themselves)
-    saved = 0;
-    begin = 0;
-    most = INT64_MAX;
-  } else if (rows >= kTensorRows) {
+  if (four_bits(p) || rows >= kTensorRows) {
     saved -= H * (75 + 64 * static_cast<int64_t>(ceil_div(rows, kPrefixRowTile)));
     begin = 31000000 + 950 * rows * H;
-    most = 16384 + 1;
+    most = rows >= kTensorRows ? 16384 + 1 : INT64_MAX;
   } else {
     saved -= H * 5 * (24 * ceil_div(rows, 8 * kGroups) + 7 * ceil_div(rows, 8)) / 2;
     begin = 200000;
     most = INT64_MAX;
   }
-  if (p.prefix < (saved > 0 ? std::min(most, 128 + begin / saved) : most)) {
+  // (the 4-bit cache's prefix is shared on the tensor cores or not at all: make_plan's units must be countable)
+  const bool many = four_bits(p) && ceil_div(rows, kPrefixRowTile) * H *
+                                            (ceil_div(p.prefix, kPrefixKeyTile) + kTensorBegin) > 0x3FFFFFFF;
+  if (many || p.prefix < (saved > 0 ? std::min(most, 128 + begin / saved) : most)) {
     p.row0 = p.prefix;
     p.prefix = 0;
   }
@@ -718,7 +721,7 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   // us the whole call, with no empty units 132, with 4 of them 126, with 10 125; 512 x 8 over 16384: 1073 to 1078 all)
   const int64_t gap = tiles > static_cast<int64_t>(num_sms) * kTensorLeast ? kTensorBegin : 0;
   const int64_t units = items * (image_tiles + gap) - gap;
-  if (p.prefix > 0 && L.rows >= kTensorRows && units <= 0x3FFFFFFF) {
+  if (p.prefix > 0 && (four_bits(p) || L.rows >= kTensorRows) && units <= 0x3FFFFFFF) {
     L.tensor_tiles = static_cast<int32_t>(tensor_tiles);
     L.image_tiles = static_cast<int32_t>(image_tiles);
     L.period = static_cast<int32_t>(image_tiles + gap);

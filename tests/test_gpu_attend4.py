@@ -483,3 +483,22 @@ def test_a_workspace_holds_for_fewer_draft_tokens():
         c = make([G] + [few] * (N - 1), lens, prefix=prefix, kv_heads=kv_heads, group=group, dim=64, seed=few)
         want, got = run(c), run(c, workspace=ws)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kw,G", [
+    (dict(gammas=[0] * 16, lens=[16384 + i for i in range(16)], prefix=16384, kv_heads=8), 0),
+    # ragged batches: there may be rows enough to share it, but few are there
+    (dict(gammas=[0] * 40, lens=[16400 + i for i in range(40)], prefix=16400, group=1), 4),
+    (dict(gammas=[0] * 30 + [3], lens=[0] * 20 + [16400] * 10 + [16403], prefix=16400, group=2, dim=64), 8),
+])
+def test_a_prefix_that_few_rows_share(kw, G, fmt):
+    c = make(seed=25, fmt=fmt, **kw)
+    c["G"] = max(G, c["G"])
+    check(poison(c))
+
+
+@pytest.mark.parametrize("gammas", [[8] + [0] * 9, [15, 3, 0, 0, 0, 1], [40] + [0] * 20, [5] * 4 + [8]])
+def test_ragged_batches_with_a_few_long_requests(gammas):
+    """Tiles of fewer rows than the longest request has, or not."""
+    check(poison(make(gammas, [700 + 50 * i for i in range(len(gammas))], group=4, kv_heads=1, seed=26)))
