@@ -66,7 +66,7 @@ struct OwnControl {
   float mx[kOwnRows4], mu[kOwnRows4];  // m = mx + mu, mx -inf without one
   float part[4][kOwnRows4];            // of the four warps that hold a row
   uint32_t none[kOwnRows4];            // the row sees a value scale that is no number
-  int64_t to[kOwnRows4];               // the row's place in the output, or its partial result's
+  alignas(16) int64_t to[kOwnRows4];   // the row's place in the output, or its partial result's
 };
 
 // Shared memory: [D / 64][128 keys][128 bytes] of V, weights of up to 64 rows in 128-byte lines, [D / 64][NMAX rows][128
@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int r = g * 16 + e;
-          x[e] = dead || key >= C.limit[r] ? -INFINITY : x[e] * kc * C.back[r];
+          const float back = C.back[r];  // (no branches: their loads would come one after another, 160 cycles each)
+          x[e] = static_cast<int>(dead) | static_cast<int>(key >= C.limit[r]) ? -INFINITY : x[e] * kc * back;
         }
         store_scores(g, x);
       }
@@ -656,15 +657,21 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
       tmem_wait_row(o);
     }
     if (D == 128 || lane < 16) {
+      float f[8];
+      int64_t to[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int r = c * 8 + e;
-        if (r < T.rows) {
-          const float f = C.factor[r], y = f == 0.0f ? 0.0f : o[e] * f * scale;
+        f[e] = C.factor[c * 8 + e];
+        to[e] = C.to[c * 8 + e] + dim;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = f[e] == 0.0f ? 0.0f : o[e] * f[e] * scale;
+        if (c * 8 + e < T.rows) {
           if (T.whole)
-            P.out[C.to[r] + dim] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
+            P.out[to[e]] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
           else
-            L.part_o[C.to[r] + dim] = y;
+            L.part_o[to[e]] = y;
         }
       }
     }
