@@ -590,8 +590,19 @@ __global__ void __launch_bounds__(kAttendThreads, 2)
   if (attend_block<D, FMT, false>(P, L, join)) attend_block<D, FMT, true>(P, L, join);
 }
 
-// Joins the partial results of a row: one warp a row.
 template <int D>
+__device__ __forceinline__ Part<D> no_part() {
+  Part<D> p;
+  p.m = -INFINITY;
+  p.l = 0.0f;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) p.o[d] = 0.0f;
+  return p;
+}
+
+// Joins the partial results of a row: one warp a row, or (MANY) eight, which take
+// an eighth of them each.
+template <int D, bool MANY>
 __global__ void __launch_bounds__(kThreads) join_kernel(const AttendParams P, const AttendPlan L) {
   pdl_enter();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -603,24 +614,31 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttendParams P, co
   const int own = len > P.prefix ? (len - P.prefix + L.own_chunk - 1) / L.own_chunk : 0;
   if (P.prefix == 0 && own <= 1) return;  // (written already)
   const int rows = (g + 1) * P.Hq;
-  for (int r = blockIdx.y * kWarps + warp; r < rows; r += gridDim.y * kWarps) {
+  constexpr int kRowsCta = MANY ? 1 : kWarps;
+  for (int r = blockIdx.y * kRowsCta + (MANY ? 0 : warp); r < rows; r += gridDim.y * kRowsCta) {
     const int64_t row = first * P.Hq + r;
     const int j = r / P.Hq, hq = r - j * P.Hq, h = hq / P.group;
     const int shared = P.prefix ? prefix_slots(L, h, (static_cast<int>(first) + j) * P.group + hq - h * P.group) : 0;
-    const int slots = shared + own;
-    Part<D> all;
-    all.m = -INFINITY;
-    all.l = 0.0f;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) all.o[d] = 0.0f;
-    for (int s = 0; s < slots; s += kJoinAhead) {
+    const int slots = shared + own, each = MANY ? (slots + kWarps - 1) / kWarps : slots;
+    const int begin = MANY ? warp * each : 0, end = min(slots, begin + each);
+    Part<D> all = no_part<D>();
+    for (int s = begin; s < end; s += kJoinAhead) {
       Part<D> part[kJoinAhead];
 #pragma unroll
       for (int u = 0; u < kJoinAhead; ++u)
-        if (s + u < slots) part[u] = load_part<D>(L, row, s + u < shared ? s + u : s + u - shared + L.prefix_splits, lane);
+        if (s + u < end) part[u] = load_part<D>(L, row, s + u < shared ? s + u : s + u - shared + L.prefix_splits, lane);
 #pragma unroll
       for (int u = 0; u < kJoinAhead; ++u)
-        if (s + u < slots) join_part<D>(all, part[u]);
+        if (s + u < end) join_part<D>(all, part[u]);
+    }
+    if (MANY) {
+      __shared__ Part<D> parts[kWarps][32];
+      __syncthreads();  // (the row before has been read)
+      parts[warp][lane] = all;
+      __syncthreads();
+      if (warp != 0) continue;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) join_part<D>(all, parts[w][lane]);
     }
     write_row<D>(P, L, first + j, hq, lane, all);
   }
@@ -633,6 +651,7 @@ constexpr int kTensorRows = 96;  // a shared prefix goes to the tensor-memory ke
 constexpr int kTensorLeast = 4;  // key tiles of a CTA of that kernel, where the prefix has as many
 constexpr int kTensorBegin = 7;  // and what beginning another (kv head, row tile) costs it, in key tiles
 constexpr int kChunkMost = 8192;                  // so that the longest request is no long tail
+constexpr int kJoinMany = 16;  // partial results of a row that eight warps join, or half as many where rows are few
 constexpr int kChunkFew = 4096;                   // the same over a 4-bit cache, where a chunk's CTAs do not fill the SMs
 
 // Chunks for `keys` keys when `base` CTAs work on every chunk: enough to give
@@ -783,10 +802,13 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, int num_sms, cuda
   // a warp takes two rows where there are rows for more than eight waves of CTAs (512 requests x 256 rows: 1084 us the
   // whole call against 1108 with one row a warp; 64 x 160: 138.5 against 137.4)
   const int64_t rows = (p.G + 1) * static_cast<int64_t>(p.Hq), each = rows * p.N > 320LL * num_sms ? 2 : 1;
-  cfg.gridDim = dim3(p.N, std::max(1, std::min(65535, ceil_div(rows, kWarps * each))));
+  // eight warps a row (4-bit cache), us a call against one: 1 request x 5 tokens over 1000 keys (8 partial results) 11.1
+  // and 11.5, over 4000 13.9 and 17.0, over 16000 20.7 and 27.7; 4 x 5 over 1000 14.8 and 14.2; 16 x 5 26.6 and 21.1
+  const bool many = four_bits(p) && L.slots >= (rows * p.N <= 2LL * num_sms ? kJoinMany / 2 : kJoinMany);
+  cfg.gridDim = dim3(p.N, std::max(1, std::min(65535, ceil_div(rows, many ? 1 : kWarps * each))));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, L);
+  return cudaLaunchKernelEx(&cfg, many ? join_kernel<D, true> : join_kernel<D, false>, p, L);
 }
 
 template <int D, int FMT>
