@@ -6,6 +6,7 @@
 // one integer product, no table of angles, no loss at far positions.  Its sine
 // and cosine cost some forty instructions, so a thread keeps those of its pairs
 // in registers and walks the heads of its token.
+#include <algorithm>
 #include <cstdint>
 
 #include "sv_internal.h"
@@ -153,14 +154,15 @@ __device__ __forceinline__ void store_split(void *p, int64_t at, int k, const fl
 // and walk `heads` heads of one token, kAhead rows' loads in flight.
 //
 // 4096 tokens x 40 heads x 128 bf16: 13.7 us (89 % of the copy rate), with norms
-// 20.3; 32768 tokens with norms 126 (79 %).  A row's norm is a chain (load, sum,
+// 17.0; 32768 tokens with norms 126 (79 %).  A row's norm is a chain (load, sum,
 // shuffles, root) that more rows in flight hide: four of bf16 rows with norms on
-// two CTAs an SM, where two rows on three CTAs took 21.8 and 149 us.  Without
+// two CTAs an SM, where two rows on three CTAs took a quarter longer.  Without
 // norms, or in fp32 (whose rows are twice the registers), more CTAs are better:
 // 15.3 us with four rows, and 80 against 90 for a prompt's keys (18000 fp32 tokens).
 constexpr int rows_ahead(bool bf16, bool norm) { return bf16 && norm ? 4 : 2; }
+constexpr int rotate_ctas(bool bf16, bool norm) { return bf16 && norm ? 2 : 3; }  // of an SM
 template <bool BF16, bool INTERLEAVED, bool NORM, int UNITS>
-__global__ void __launch_bounds__(kThreads, NORM && BF16 ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, rotate_ctas(BF16, NORM))
     rotate_kernel(const __grid_constant__ RotateParams P, const int lanes, const int heads, const FastDiv parts) {
   pdl_enter();
   constexpr int VE = vector_elements<BF16>(), kAhead = rows_ahead(BF16, NORM);
@@ -332,10 +334,23 @@ cudaError_t launch_rotate(const RotateParams &p, bool bf16, int num_sms, cudaStr
   int lanes = 1;
   while (lanes < need && lanes < 32) lanes *= 2;
   const int units = (need + lanes - 1) / lanes;
-  // a token's heads are cut over more lanes while that fills the SMs (1024 threads each), no finer than a step's rows
-  const int step = rows_ahead(bf16, p.q.weight || p.k.weight);
-  int parts = static_cast<int>((num_sms * 1024LL + p.T * lanes - 1) / (p.T * lanes));
-  if (parts > (all + step - 1) / step) parts = (all + step - 1) / step;
+  // A token's heads are cut into parts, no finer than a step's rows: without norms until 1024 threads an SM are there,
+  // with them, and with fewer CTAs on an SM, where the waves of CTAs times a CTA's steps (and the angles, about one more)
+  // are the fewest: 4096 tokens x 40 heads in 0.8 waves of 5 steps 17.0 us, in 2.1 waves of 2 steps 20.3.
+  const bool norm = p.q.weight || p.k.weight;
+  const int step = rows_ahead(bf16, norm), most = (all + step - 1) / step;
+  int parts = static_cast<int>(std::min<int64_t>(most, (num_sms * 1024LL + p.T * lanes - 1) / (p.T * lanes)));
+  if (norm) {
+    int64_t least = INT64_MAX;
+    for (int n = 1; n <= most; ++n) {
+      const int64_t ctas = (p.T * n * lanes + kThreads - 1) / kThreads, at_once = num_sms * rotate_ctas(bf16, norm);
+      const int64_t time = (ctas + at_once - 1) / at_once * (((all + n - 1) / n + step - 1) / step + 1);
+      if (time < least) {
+        least = time;
+        parts = n;
+      }
+    }
+  }
   const int heads = (all + parts - 1) / parts;
   parts = (all + heads - 1) / heads;
   cfg.gridDim = dim3(static_cast<unsigned>((p.T * parts * lanes + kThreads - 1) / kThreads));
