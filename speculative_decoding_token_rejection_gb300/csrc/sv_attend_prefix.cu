@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const AttendParams P, 
   }
 }
 
-// The same from the 4-bit cache: a thread takes half a group.  Behind the prefix's end nothing is read.
+// The same from the 4-bit cache: a thread takes half a group.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) unpack4_kernel(const AttendParams P, const AttendPlan L) {
   pdl_enter();
@@ -186,20 +186,27 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(const AttendParams P,
   const uint8_t *const base = static_cast<const uint8_t *>(side ? P.c.v : P.c.k) + h * P.c.head_stride + col * 4;
   const uint8_t *const group = (side ? P.v_group : P.k_group) + h * P.group_head + (col >> 1);
   uint8_t *const out = L.image + ((static_cast<int64_t>(h) * L.image_tiles + tile) * 2 + side) * (kKeyTile * D * 2);
+  // (no load under a condition: they would come one after another)
   uint32_t raw[kPieces], g[kPieces];
+  int page[kPieces];
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p)
+    page[p] = P.tables[div_by(min(tile * kKeyTile + p * (kThreads / kCols) + static_cast<int>(threadIdx.x) / kCols, P.prefix - 1),
+                              L.page)];
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
-    const int r = p * (kThreads / kCols) + threadIdx.x / kCols, k = tile * kKeyTile + r;
-    raw[p] = g[p] = 0;
-    if (k < P.prefix) {
-      const int x = div_by(k, L.page), page = P.tables[x], off = k - x * P.c.block_size;
-      if (page >= 0 && page < P.c.num_blocks) {
-        raw[p] = __ldg(reinterpret_cast<const uint32_t *>(base + page * P.c.block_stride + off * P.c.token_stride));
-        g[p] = group[page * P.group_block + off * P.group_token];
-        // (a value behind every request's length may have a scale that is no number: a weight of 0 times it would be NaN)
-        if (side && (g[p] & 0x7Fu) == 0x7Fu) g[p] = 0;
-      }
-    }
+    const int k = min(tile * kKeyTile + p * (kThreads / kCols) + static_cast<int>(threadIdx.x) / kCols, P.prefix - 1);
+    const int off = k - div_by(k, L.page) * P.c.block_size;
+    const int64_t at = static_cast<uint32_t>(page[p]) < static_cast<uint32_t>(P.c.num_blocks) ? page[p] : 0;
+    raw[p] = __ldg(reinterpret_cast<const uint32_t *>(base + at * P.c.block_stride + off * P.c.token_stride));
+    g[p] = __ldg(group + at * P.group_block + off * P.group_token);
+  }
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const int k = tile * kKeyTile + p * (kThreads / kCols) + static_cast<int>(threadIdx.x) / kCols;
+    if (k >= P.prefix || static_cast<uint32_t>(page[p]) >= static_cast<uint32_t>(P.c.num_blocks)) raw[p] = g[p] = 0;
+    // (a value behind every request's length may have a scale that is no number: a weight of 0 times it would be NaN)
+    if (side && (g[p] & 0x7Fu) == 0x7Fu) g[p] = 0;
   }
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
