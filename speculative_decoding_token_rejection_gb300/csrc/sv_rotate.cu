@@ -342,9 +342,10 @@ cudaError_t launch_rotate(const RotateParams &p, bool bf16, int num_sms, cudaStr
   int parts = static_cast<int>(std::min<int64_t>(most, (num_sms * 1024LL + p.T * lanes - 1) / (p.T * lanes)));
   if (norm) {
     int64_t least = INT64_MAX;
-    for (int n = 1; n <= most; ++n) {
+    for (int steps = 1; steps <= most; steps += 1 + steps / 64) {
+      const int n = (most + steps - 1) / steps;
       const int64_t ctas = (p.T * n * lanes + kThreads - 1) / kThreads, at_once = num_sms * rotate_ctas(bf16, norm);
-      const int64_t time = (ctas + at_once - 1) / at_once * (((all + n - 1) / n + step - 1) / step + 1);
+      const int64_t time = (ctas + at_once - 1) / at_once * (steps + 1);
       if (time < least) {
         least = time;
         parts = n;
