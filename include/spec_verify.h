@@ -524,7 +524,8 @@ sv_status spec_verify_check_kv4_args(const spec_verify_config *config, const spe
  * anything); the rows' scales may be any floats, as there.  Strides between
  * pages and between tokens are below 4 GB.  A nibble times its
  * group scale is exact in the 16-bit products' operands, so what that call
- * rounds to fewer bits is what this one does. */
+ * rounds to fewer bits is what this one does.  SV_TEST_EXPIRE_PRODUCT_WAIT makes
+ * the private keys' first wait for a product give up too. */
 typedef struct spec_verify_attend4_args {
   int32_t num_reqs;
   int32_t max_spec_len;
@@ -629,7 +630,9 @@ sv_status spec_verify_check_plan_args(const spec_verify_config *config, const sp
  * turns[i] = f_i / (2 pi) * 2^64, rounded: the product with a position, modulo
  * 2^64, is the angle as a fraction of a turn, exact however far the position is.
  * Scalings for long contexts are a matter of these numbers and of `magnitude`.
- * The arithmetic is fp32, rounded once at the end.  Rows of a negative position
+ * The arithmetic is fp32, rounded once at the end.  (With a norm, a row whose sum
+ * of squares passes the range of fp32 becomes zeros, and NaN where an element or
+ * its pair's other one is not finite.)  Rows of a negative position
  * (idle ones) are neither read nor written.  Outputs may be the inputs
  * themselves (same strides); other overlaps are not allowed. */
 #define SV_ROTATE_INTERLEAVED 1u

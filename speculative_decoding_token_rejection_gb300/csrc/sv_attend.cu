@@ -652,7 +652,9 @@ constexpr int kTensorLeast = 4;  // key tiles of a CTA of that kernel, where the
 constexpr int kTensorBegin = 7;  // and what beginning another (kv head, row tile) costs it, in key tiles
 constexpr int kChunkMost = 8192;                  // so that the longest request is no long tail
 constexpr int kJoinMany = 16;  // partial results of a row that eight warps join, or half as many where rows are few
-constexpr int kChunkFew = 4096;                   // the same over a 4-bit cache, where a chunk's CTAs do not fill the SMs
+// The same over a 4-bit cache, where a chunk's CTAs do not fill the SMs: 6 requests x 64 rows over 60000 to 131072 keys 310
+// us against 350 with 8192; 64 x 20 over 8192 loses most by it, 200 against 193.
+constexpr int kChunkFew = 4096;
 
 // Chunks for `keys` keys when `base` CTAs work on every chunk: enough to give
 // each SM two CTAs twice over, none below kChunkStep keys.

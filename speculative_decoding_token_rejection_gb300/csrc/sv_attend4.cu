@@ -19,6 +19,18 @@
 // second.  A tile is 128 keys, its bytes are loaded a tile ahead.  Four CTAs an SM
 // (three with more than 32 rows) hide each other's waits.
 //
+// What bounds it are instructions, about 800 a warp and tile: unpacking 256
+// elements a thread, 4 to 6 for a weight, addresses.  2.1 of an SM's 4 issue slots
+// a cycle are filled, as the pipes of conversions and 16-bit products take an
+// instruction every other cycle.  256 requests x 4096 keys x 8 heads of 128 (1.28
+// GB): 4 rows a head 312 us (0.60 of the copy rate), 20 rows 348, 32 rows 357, 64
+// rows 499.  By CTAs an SM (152 requests x 4 rows): one 385 us, two 241, three 225,
+// four 196.  Lost: 256 threads, two a key, that exchange maxima; K loaded long
+// before V (350 us against 331); chunks of 2048 keys (396 against 361); anything
+// that spills in the loop.  Gained: bytes prefetched to L2 a tile before they are
+// loaded (350 to 331 us); places in shared memory.  One tile alone takes 8.7 us,
+// dependent loads (length, page, bytes) and code met for the first time.
+//
 // Numbers, as in the kernel for the shared prefix: x = (q . n) * (scale * log2 e *
 // key_scale), w = 2^(x - m), l = sum w, P = w * value_scale / W, O = W * sum P n_v.
 // Any m gives the same quotient O / l; a row's is raised to the largest x +

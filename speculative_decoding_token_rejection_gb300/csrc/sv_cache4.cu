@@ -11,6 +11,11 @@
 //
 // A thread takes one group: its maximum needs no neighbour, the row's takes
 // three shuffles (two for head_dim 64), and its 16 nibbles are one 8-byte access.
+//
+// Reading 131072 tokens x 8 heads x 128 as bf16: 142 us, 537 MB written at 3.8
+// TB/s beside 151 MB read; filling as much memory alone takes 135 (4.0 TB/s).
+// Writing and reading 4096 x 8 x 128: 9.9 us, two launches with 2.5 us of work
+// each.
 #include <cstdint>
 
 #include "sv_cache4.cuh"
