@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kRowsThreads) plan_rows_kernel(const PlanParam
   const int r0 = blockIdx.x * kRowsCta, warp = threadIdx.x >> 5;
   if (warp < 2) {
     const int i = request_behind(W.end, P.N, warp ? min(r0 + static_cast<int64_t>(kRowsCta), P.R) - 1 : r0);
-    if ((threadIdx.x & 31) == 0) range[warp] = min(i, P.N - 1);
+    if ((threadIdx.x & 31) == 0) range[warp] = warp ? min(i, P.N - 1) : i;
   }
   __syncthreads();
   do_rows<kRowsThreads>(P, W, r0, range[0], range[1], mark, warp_last);

@@ -156,6 +156,7 @@ def test_idle_rows_behind_the_last_request(ver, pad):
 
 def test_no_requests_and_no_rows(ver):
     check(ver, state([], [], pad=5))
+    check(ver, state([], [], pad=5000))
     check(ver, state([0, 0], [5, -1]))
     check(ver, state([], []))
 
