@@ -194,13 +194,12 @@ sv_status spec_verify_attend4_workspace_size(spec_verify_t h, const spec_verify_
   if (!a || !bytes) return fail(SV_ERR_INVALID_ARG, "args or bytes is NULL");
   spec_verify_attend4_args any = *a;
   any.cache.format = SV_CACHE_E2M1;  // (the formats need the same)
-  const sv::AttendParams p = attend4_params(h, &any);
   spec_verify_attend_args b = common(any);
   static const int32_t cu = 0;  // (a ragged call's T is known without its prefix sums)
   b.cu_num_draft_tokens = &cu;
   const sv_status st = sv::check_attend_sizes(&h->cfg, &b);
   if (st != SV_OK) return st;
-  *bytes = a->num_reqs == 0 ? 0 : sv::attend_workspace_bytes(p, h->num_sms, true);
+  *bytes = a->num_reqs == 0 ? 0 : sv::attend_workspace_bytes(attend4_params(h, &any), h->num_sms, true);
   return SV_OK;
 }
 

@@ -502,3 +502,21 @@ def test_a_prefix_that_few_rows_share(kw, G, fmt):
 def test_ragged_batches_with_a_few_long_requests(gammas):
     """Tiles of fewer rows than the longest request has, or not."""
     check(poison(make(gammas, [700 + 50 * i for i in range(len(gammas))], group=4, kv_heads=1, seed=26)))
+
+
+def test_workspace_size_refuses_what_the_call_does():
+    import ctypes
+    lib, n = sv.load_library(), ctypes.c_int64()
+
+    def size(**kw):
+        a = sv.SpecVerifyAttend4Args()
+        a.num_reqs, a.max_spec_len, a.num_q_heads, a.max_seq_len, a.num_draft_tokens_total = 3, 2, 8, 100, 6
+        a.cache.num_kv_heads, a.cache.head_dim = 2, 128
+        for name, value in kw.items():
+            setattr(a.cache if hasattr(a.cache, name) else a, name, value)
+        return lib.spec_verify_attend4_workspace_size(verifier().handle, ctypes.byref(a), ctypes.byref(n))
+
+    assert size() == 0
+    for kw in (dict(num_kv_heads=0), dict(num_kv_heads=3), dict(num_reqs=-1), dict(max_seq_len=-1), dict(head_dim=0)):
+        assert size(**kw) != 0
+    assert size(num_reqs=0, num_draft_tokens_total=0, num_kv_heads=1) == 0 and n.value == 0
