@@ -344,6 +344,7 @@ cudaError_t launch_rotate(const RotateParams &p, bool bf16, int num_sms, cudaStr
     int64_t least = INT64_MAX;
     for (int steps = 1; steps <= most; steps += 1 + steps / 64) {
       const int n = (most + steps - 1) / steps;
+      if (n > 1 && p.T * n * lanes > INT32_MAX) continue;  // (a thread's number is an int)
       const int64_t ctas = (p.T * n * lanes + kThreads - 1) / kThreads, at_once = num_sms * rotate_ctas(bf16, norm);
       const int64_t time = (ctas + at_once - 1) / at_once * (steps + 1);
       if (time < least) {
