@@ -153,12 +153,13 @@ __device__ __forceinline__ void store_split(void *p, int64_t at, int k, const fl
 // neighbouring ones, or such as stay.  `lanes` neighbouring lanes share a row,
 // and walk `heads` heads of one token, kAhead rows' loads in flight.
 //
-// 4096 tokens x 40 heads x 128 bf16: 13.7 us (89 % of the copy rate), with norms
-// 17.0; 32768 tokens with norms 126 (79 %).  A row's norm is a chain (load, sum,
+// 50001 fp32 tokens x 10 heads x 128: 80 us (94 % of the copy rate).  4096 tokens x
+// 40 heads x 128 bf16 that lie in L2: 13.7 us, with norms 17.0 (20.6 from HBM);
+// 32768 tokens with norms 126 (79 %).  A row's norm is a chain (load, sum,
 // shuffles, root) that more rows in flight hide: four of bf16 rows with norms on
 // two CTAs an SM, where two rows on three CTAs took a quarter longer.  Without
 // norms, or in fp32 (whose rows are twice the registers), more CTAs are better:
-// 15.3 us with four rows, and 80 against 90 for 50001 fp32 tokens x 10 heads.
+// 15.3 us with four rows, and 90 for the fp32 tokens.
 constexpr int rows_ahead(bool bf16, bool norm) { return bf16 && norm ? 4 : 2; }
 constexpr int rotate_ctas(bool bf16, bool norm) { return bf16 && norm ? 2 : 3; }  // of an SM
 template <bool BF16, bool INTERLEAVED, bool NORM, int UNITS>
