@@ -488,6 +488,7 @@ def test_a_workspace_holds_for_fewer_draft_tokens():
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("kw,G", [
     (dict(gammas=[0] * 16, lens=[16384 + i for i in range(16)], prefix=16384, kv_heads=8), 0),
+    (dict(gammas=[0] * 20, lens=[70000 + 40 * i for i in range(20)], prefix=70000, kv_heads=1, group=1, dim=64), 0),
     # ragged batches: there may be rows enough to share it, but few are there
     (dict(gammas=[0] * 40, lens=[16400 + i for i in range(40)], prefix=16400, group=1), 4),
     (dict(gammas=[0] * 30 + [3], lens=[0] * 20 + [16400] * 10 + [16403], prefix=16400, group=2, dim=64), 8),

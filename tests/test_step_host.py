@@ -78,7 +78,9 @@ def attend_args():
     ("block_table_stride", 1, INVALID), ("shared_prefix_len", 33, INVALID), ("shared_prefix_len", 0, OK),
     ("reserved", 1, INVALID), ("test_flags", sv.SV_TEST_EXPIRE_PRODUCT_WAIT, OK), ("test_flags", 1, INVALID),
     ("q", None, INVALID), ("out", None, INVALID), ("seq_lens", None, INVALID), ("block_tables", None, INVALID),
-    ("cache.block_stride", 1 << 35, UNSUPPORTED), ("scale", float("nan"), INVALID), ("scale", -1.0, OK),
+    ("cache.block_stride", 1 << 35, UNSUPPORTED), ("cache.token_stride", 1 << 32, UNSUPPORTED),
+    ("cache.group_block_stride", 1 << 32, UNSUPPORTED), ("cache.scale_block_stride", 1 << 30, UNSUPPORTED),
+    ("cache.scale_token_stride", (1 << 30) - 1, OK), ("cache.block_stride", (1 << 32) - 32, OK), ("scale", float("nan"), INVALID), ("scale", -1.0, OK),
     ("workspace_bytes", -1, INVALID), ("workspace", FAKE + 4, INVALID)])
 def test_check_attend4_args(path, value, code):
     a = attend_args()
