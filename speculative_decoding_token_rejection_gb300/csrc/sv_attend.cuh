@@ -252,13 +252,14 @@ __device__ __forceinline__ bool own_tile(const AttendParams &P, const AttendPlan
   return T.k_end > T.k_begin || (T.whole && T.split == 0);
 }
 
-// The private part over the 4-bit cache (sv_attend4.cu): tiles of at most kOwnRows4 rows, or of half as many (a CTA more
-// an SM) where every request's rows fit, or those of most: requests of 20 rows on average and 36 at most 438 us against
-// 459 in larger tiles, of 24 and 44 480 against 467, of 36 and 64 541 against 491 (256 requests of up to 8192 keys).
+// The private part over the 4-bit cache (sv_attend4.cu): tiles of 16 rows where every request's rows fit, of 32 where they
+// do or most requests' do, else of 64.  256 requests x 4096 keys, 16 rows each: 289 us in tiles of 16, 327 in tiles of 32;
+// but ragged ones of 12 rows on average and 20 at most 384 against 361.  Requests of 20 rows on average and 36 at most 410
+// us in tiles of 32, 459 in tiles of 64, of 24 and 44 480 against 467, of 36 and 64 541 against 491 (up to 8192 keys).
 constexpr int kOwnRows4 = 64, kOwnRowsMean = 24;
 inline int own4_rows(const AttendParams &p) {
   const int64_t most = (p.G + 1) * static_cast<int64_t>(p.group), all = (p.T + p.N) * p.group;
-  return most <= kOwnRows4 / 2 || all <= static_cast<int64_t>(p.N) * kOwnRowsMean ? kOwnRows4 / 2 : kOwnRows4;
+  return most <= 16 ? 16 : most <= 32 || all <= static_cast<int64_t>(p.N) * kOwnRowsMean ? 32 : kOwnRows4;
 }
 cudaError_t enable_own4_kernels();
 cudaError_t launch_own4(const AttendParams &p, const AttendPlan &L, cudaStream_t stream);

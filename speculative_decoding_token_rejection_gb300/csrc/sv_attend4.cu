@@ -16,16 +16,16 @@
 //
 // so no byte is exchanged between threads, and one thread issues the products,
 // which run while all unpack: V during the first, the next tile's K during the
-// second.  A tile is 128 keys, its bytes are loaded a tile ahead.  Four CTAs an SM
-// (three with more than 32 rows) hide each other's waits.
+// second.  A tile is 128 keys, its bytes are loaded a tile ahead.  Three to five
+// CTAs an SM hide each other's waits.
 //
 // What bounds it are instructions, about 800 a warp and tile: unpacking 256
 // elements a thread, 4 to 6 for a weight, addresses.  2.1 of an SM's 4 issue slots
 // a cycle are filled, as the pipes of conversions and 16-bit products take an
 // instruction every other cycle.  256 requests x 4096 keys x 8 heads of 128 (1.28
-// GB): 4 rows a head 312 us (0.60 of the copy rate), 20 rows 348, 32 rows 357, 64
-// rows 499.  By CTAs an SM (152 requests x 4 rows): one 385 us, two 241, three 225,
-// four 196.  Lost: 256 threads, two a key, that exchange maxima; K loaded long
+// GB): 4 rows a head 281 us (0.67 of the copy rate), 16 rows 289, 20 rows 337, 32
+// rows 345, 64 rows 500.  By CTAs an SM (152 requests x 4 rows, tiles of 32): one
+// 385 us, two 241, three 225, four 196.  Lost: 256 threads, two a key, that exchange maxima; K loaded long
 // before V (350 us against 331); chunks of 2048 keys (396 against 361); anything
 // that spills in the loop.  Gained: bytes prefetched to L2 a tile before they are
 // loaded (350 to 331 us); places in shared memory.  One tile alone takes 8.7 us,
@@ -64,30 +64,32 @@ struct alignas(16) OwnPlaces {
   const int32_t *table, *table0;
 };
 
+template <int ROWS>
 struct OwnControl {
   OwnPlaces at;
   uint64_t k_empty, s_full, o_full;
   uint32_t tmem, tmem_keys, abort;
   uint32_t huge;                       // some |m| is so large that its two parts are subtracted one after the other
-  alignas(16) float neg[kOwnRows4];    // negated m, 0 without one
-  alignas(16) float zero[kOwnRows4];
-  alignas(16) float negx[kOwnRows4], negu[kOwnRows4];  // its parts, negated
-  alignas(16) float back[kOwnRows4];   // what undoes a row's power of two
-  alignas(16) int limit[kOwnRows4];    // keys that the row sees are below it
-  alignas(16) float factor[kOwnRows4]; // of a raised maximum; at the end, of the outputs
-  float mx[kOwnRows4], mu[kOwnRows4];  // m = mx + mu, mx -inf without one
-  float part[4][kOwnRows4];            // of the four warps that hold a row
-  uint32_t none[kOwnRows4];            // the row sees a value scale that is no number
-  alignas(16) int64_t to[kOwnRows4];   // the row's place in the output, or its partial result's
+  alignas(16) float neg[ROWS];    // negated m, 0 without one
+  alignas(16) float zero[ROWS];
+  alignas(16) float negx[ROWS], negu[ROWS];  // its parts, negated
+  alignas(16) float back[ROWS];   // what undoes a row's power of two
+  alignas(16) int limit[ROWS];    // keys that the row sees are below it
+  alignas(16) float factor[ROWS]; // of a raised maximum; at the end, of the outputs
+  float mx[ROWS], mu[ROWS];  // m = mx + mu, mx -inf without one
+  float part[4][ROWS];            // of the four warps that hold a row
+  uint32_t none[ROWS];            // the row sees a value scale that is no number
+  alignas(16) int64_t to[ROWS];   // the row's place in the output, or its partial result's
 };
 
 // Shared memory: [D / 64][128 keys][128 bytes] of V, weights of up to 64 rows in 128-byte lines, [D / 64][NMAX rows][128
-// bytes] of queries.  With up to 32 rows, keys k and k + 64 share a line of weights: four CTAs' memory fits an SM.  16-byte columns of a line are exchanged by line % 8.
+// bytes] of queries.  Two keys of up to 32 rows, four of up to 16, share a line of weights, 64 or 32 keys apart: so four or
+// five CTAs' memory fits an SM.  16-byte columns of a line are exchanged by line % 8.
 template <int D, int NMAX>
 struct OwnSmem {
   static constexpr int kLines = kOwnKeys * 128;
   static constexpr int kV = 0, kP = D / 64 * kLines, kQ = kP + kLines * NMAX / kOwnRows4, kControl = kQ + D / 64 * NMAX * 128,
-                       kBytes = kControl + static_cast<int>(sizeof(OwnControl)) + 1024;  // (the base is rounded up to 1 KB)
+                       kBytes = kControl + static_cast<int>(sizeof(OwnControl<NMAX>)) + 1024;  // (the base is rounded up to 1 KB)
 };
 __device__ __forceinline__ int line_at(int line, int col) { return line * 128 + ((col ^ (line & 7)) << 4); }
 
@@ -170,8 +172,12 @@ __device__ __forceinline__ const uint8_t *step(const uint8_t *p, uint32_t a, uin
   return reinterpret_cast<const uint8_t *>(r);
 }
 
+// CTAs of an SM: what their registers, shared and tensor memory allow.  (Four of 16 rows and head_dim 128: 96 registers, as
+// a fifth would leave, spill in the loop, 406 us against 278 for 256 requests x 4096 keys.  Head_dim 64: five 190, four 205,
+// but with 32 rows five 275 against 250.)
+constexpr int own4_ctas(int d, int nmax) { return nmax == 64 ? 3 : nmax == 16 && d == 64 ? 5 : 4; }
 template <int D, int FMT, int NMAX>
-__global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
+__global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
     own4_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ AttendPlan L) {
   pdl_enter();
   OwnTile T;
@@ -179,12 +185,12 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
   extern __shared__ uint8_t raw[];
   uint8_t *const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   using Y = OwnSmem<D, NMAX>;
-  OwnControl &C = *reinterpret_cast<OwnControl *>(smem + Y::kControl);
+  OwnControl<NMAX> &C = *reinterpret_cast<OwnControl<NMAX> *>(smem + Y::kControl);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // Tensor memory: K, S and O.  Where all of them pass 128 columns, which is a quarter of what an SM has, K goes there in
   // two halves of 32 columns, allocated by themselves: three CTAs' 160 columns fit an SM.
   constexpr int kHalves = D == 128 && NMAX > 32 ? 2 : 1;
-  constexpr uint32_t kKeyCols = D / 2 / kHalves, kS = 0, kO = NMAX, kOwnCols = NMAX <= 32 ? 64 : 128;
+  constexpr uint32_t kKeyCols = D / 2 / kHalves, kS = 0, kO = NMAX, kOwnCols = 2 * NMAX;
   const int n8 = (T.rows + 7) / 8, n16 = (T.rows + 15) / 16;
 
   // ---- the first tile's bytes are on their way before anything else ----
@@ -267,7 +273,7 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
     tmem_get(&C.tmem_keys, kKeyCols);
     tmem_no_more();
   }
-  if (tid < kOwnRows4) {
+  if (tid < NMAX) {
     const int j = div_by(T.r0 + tid, L.group);
     C.limit[tid] = tid < T.rows ? T.len - T.gam + j : 0x7FFFFFFF;
     C.zero[tid] = C.neg[tid] = C.negx[tid] = C.negu[tid] = C.mu[tid] = 0.0f;
@@ -373,8 +379,9 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
     }
   };
   // Half (or all) of the values in vrow to shared memory.
-  const uint32_t p_line = base + Y::kP + (NMAX <= 32 ? (tid & 63) * 128 + (((tid >> 6 << 2) ^ (tid & 7)) << 4)
-                                                     : tid * 128 + ((tid & 7) << 4));
+  // (kShare keys to a line of weights, kShareLines apart)
+  constexpr int kShare = 64 / NMAX, kShareLines = kOwnKeys / kShare;
+  const uint32_t p_line = base + Y::kP + tid % kShareLines * 128 + (((tid / kShareLines * (NMAX / 8)) ^ (tid & 7)) << 4);
   const uint32_t v_line = base + Y::kV + tid * 128 + ((tid & 7) << 4);
   auto unpack_values = [&](int half) {
 #pragma unroll
@@ -616,7 +623,7 @@ __global__ void __launch_bounds__(kOwnThreads, NMAX <= 32 ? 4 : 3)
 #pragma unroll
         for (int kk = 1; kk < kOwnKeys / 16; ++kk)
           mma_ss<true>(tmem + kO, v_operand + kk * (2048 >> 4),
-                       p_operand + (NMAX <= 32 ? (kk & 3) * (2048 >> 4) + (kk >> 2) * (64 >> 4) : kk * (2048 >> 4)),
+                       p_operand + kk % (8 / kShare) * (2048 >> 4) + kk / (8 / kShare) * (2 * NMAX >> 4),
                        output_shape);
         mma_commit(&C.o_full);
       }
@@ -718,13 +725,18 @@ cudaError_t launch(const AttendParams &p, const AttendPlan &L, cudaStream_t stre
 }
 template <int D, int FMT>
 cudaError_t pick(const AttendParams &p, const AttendPlan &L, cudaStream_t stream) {
-  return own4_rows(p) == 32 ? launch<D, FMT, 32>(p, L, stream) : launch<D, FMT, 64>(p, L, stream);
+  const int rows = own4_rows(p);
+  return rows == 16   ? launch<D, FMT, 16>(p, L, stream)
+         : rows == 32 ? launch<D, FMT, 32>(p, L, stream)
+                      : launch<D, FMT, 64>(p, L, stream);
 }
 
 template <int D, int FMT>
 cudaError_t enable() {
-  const cudaError_t e = cudaFuncSetAttribute(own4_kernel<D, FMT, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             OwnSmem<D, 32>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(own4_kernel<D, FMT, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       OwnSmem<D, 16>::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(own4_kernel<D, FMT, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, OwnSmem<D, 32>::kBytes);
   return e != cudaSuccess ? e
                           : cudaFuncSetAttribute(own4_kernel<D, FMT, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  OwnSmem<D, 64>::kBytes);
