@@ -25,11 +25,12 @@
 // instruction every other cycle.  256 requests x 4096 keys x 8 heads of 128 (1.28
 // GB): 4 rows a head 281 us (0.67 of the copy rate), 16 rows 289, 20 rows 337, 32
 // rows 345, 64 rows 500.  By CTAs an SM (152 requests x 4 rows, tiles of 32): one
-// 385 us, two 241, three 225, four 196.  Lost: 256 threads, two a key, that exchange maxima; K loaded long
-// before V (350 us against 331); chunks of 2048 keys (396 against 361); anything
-// that spills in the loop.  Gained: bytes prefetched to L2 a tile before they are
-// loaded (350 to 331 us); places in shared memory.  One tile alone takes 8.7 us,
-// dependent loads (length, page, bytes) and code met for the first time.
+// 385 us, two 241, three 225, four 196.  Lost: 256 threads, two a key, that
+// exchange maxima; K loaded long before V (350 us against 331); chunks of 2048 keys
+// (396 against 361); anything that spills in the loop.  Gained: bytes prefetched to
+// L2 a tile before they are loaded (350 to 331 us); places in shared memory.  One
+// tile alone takes 8.1 us, dependent loads (length, page, bytes) and code met for
+// the first time.
 //
 // Numbers, as in the kernel for the shared prefix: x = (q . n) * (scale * log2 e *
 // key_scale), w = 2^(x - m), l = sum w, P = w * value_scale / W, O = W * sum P n_v.
