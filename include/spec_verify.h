@@ -498,7 +498,8 @@ typedef struct spec_verify_kv4_cache {
 } spec_verify_kv4_cache;
 
 /* As spec_verify_kv_args.  (A scale or group stride of 0 along more than one
- * element: such rows can be read, not written.) */
+ * element: such rows can be read, not written.  Where two tokens are written to
+ * one slot, each part of the row is of either.) */
 typedef struct spec_verify_kv4_args {
   int64_t num_tokens; /* T >= 0 (0 is a no-op) */
   int32_t dtype;      /* SV_F32 or SV_BF16: the elements of key and value */
@@ -574,14 +575,17 @@ sv_status spec_verify_check_attend4_args(const spec_verify_config *config, const
  * from the head in their order; where the pages wanted by the requests up to i
  * are more than there are, request i takes none and raises SV_DATA_NO_PAGES.
  * p < 0: the request is done (or the place is idle).  The pages it held go to the
- * tail, in order, free from the next call on, and its rows are idle.
+ * tail, in order, free from the next call on, and its rows are idle.  The first
+ * num_shared_pages entries of every table (a prefix that the batch shares) are
+ * nobody's own: they stay, and count as held.  Any other page is in one table.
  *   seq_lens = p + n, positions = p .. p + n - 1 and slot_mapping their slots.
  * Idle rows -- of requests that are done or got no pages, and behind the last
  * request's -- have position and slot -1, and their requests seq_lens 0.
- * n < 0 (taken as 0), held_pages outside [0, table_width] or too few for p, or a
- * length that needs more than table_width pages (or passes 2^31 - 1) raise
- * SV_DATA_BAD_PARAM, and rows that pass num_rows SV_DATA_BAD_CU; such a request
- * is treated as one that got no pages and does not count among those wanted.
+ * n < 0 (taken as 0), held_pages outside [0, table_width] or, with p >= 0, too
+ * few for p or fewer than num_shared_pages, or a length that needs more than
+ * table_width pages (or passes 2^31 - 1) raise SV_DATA_BAD_PARAM, and rows that
+ * pass num_rows SV_DATA_BAD_CU; such a request is treated as one that got no
+ * pages and does not count among those wanted.
  * With a free_range that is negative or wider than free_capacity, or a page
  * outside it, no page is given or taken back (SV_DATA_BAD_PARAM).
  * held_pages_out may be held_pages, free_range_out free_range and seq_lens
@@ -590,7 +594,7 @@ typedef struct spec_verify_plan_args {
   int32_t num_reqs;    /* N >= 0 (0: only idle rows); at most the handle's max_num_reqs */
   int32_t block_size;  /* >= 1 */
   int32_t table_width; /* pages in a row of block_tables, >= 0 */
-  uint32_t reserved;   /* 0 */
+  int32_t num_shared_pages; /* 0 .. table_width */
   int64_t num_rows;    /* R: 0 .. 2^31 - 1 - 65536 */
   const int32_t *num_new_tokens;      /* [N] */
   const int32_t *num_computed_tokens; /* [N] */

@@ -174,7 +174,7 @@ class SpecVerifyAttend4Args(ctypes.Structure):
 class SpecVerifyPlanArgs(ctypes.Structure):
     _fields_ = [
         ("num_reqs", ctypes.c_int32), ("block_size", ctypes.c_int32), ("table_width", ctypes.c_int32),
-        ("reserved", ctypes.c_uint32), ("num_rows", ctypes.c_int64), ("num_new_tokens", _P),
+        ("num_shared_pages", ctypes.c_int32), ("num_rows", ctypes.c_int64), ("num_new_tokens", _P),
         ("num_computed_tokens", _P), ("block_tables", _P), ("block_table_stride", ctypes.c_int64), ("held_pages", _P),
         ("held_pages_out", _P), ("free_pages", _P), ("free_capacity", ctypes.c_int64), ("free_range", _P),
         ("free_range_out", _P), ("positions", _P), ("slot_mapping", _P), ("seq_lens", _P), ("cu_num_draft_tokens", _P),
@@ -893,7 +893,8 @@ def spec_verify_check_attend4_args(config: SpecVerifyConfig, args: SpecVerifyAtt
 # ----------------------------------------------------------------------------
 def build_plan_args(*, num_new_tokens, num_computed_tokens, block_tables, held_pages, held_pages_out, free_pages,
                     free_range, free_range_out, block_size: int, num_rows: int, positions, slot_mapping, seq_lens,
-                    workspace, cu_num_draft_tokens=None, status=None) -> SpecVerifyPlanArgs:
+                    workspace, num_shared_pages: int = 0, cu_num_draft_tokens=None,
+                    status=None) -> SpecVerifyPlanArgs:
     """Validate tensors and fill a SpecVerifyPlanArgs (no device work).  All
     tensors are int32 but ``slot_mapping`` and the two ranges (int64);
     ``block_tables`` is [N, pages], ``free_pages`` a ring of at least as many
@@ -916,7 +917,7 @@ def build_plan_args(*, num_new_tokens, num_computed_tokens, block_tables, held_p
     elif between < width:
         raise ValueError(f"block_tables rows must not overlap (stride {between} for {width} pages)")
     return SpecVerifyPlanArgs(
-        N, int(block_size), width, 0, R, _vector(num_new_tokens, i32, "num_new_tokens", device, N),
+        N, int(block_size), width, int(num_shared_pages), R, _vector(num_new_tokens, i32, "num_new_tokens", device, N),
         _vector(num_computed_tokens, i32, "num_computed_tokens", device, N), block_tables.data_ptr(), between,
         _vector(held_pages, i32, "held_pages", device, N), _vector(held_pages_out, i32, "held_pages_out", device, N),
         _vector(free_pages, i32, "free_pages", device, free_pages.numel()), free_pages.numel(),
@@ -1208,13 +1209,14 @@ class Verifier:
 
     def plan_step(self, *, num_new_tokens, num_computed_tokens, block_tables, held_pages, free_pages, free_range,
                   block_size: int, num_rows: int, positions=None, slot_mapping=None, seq_lens=None,
-                  held_pages_out=None, free_range_out=None, cu_num_draft_tokens=None, workspace=None, status=None,
-                  stream=None) -> PlanResult:
+                  num_shared_pages: int = 0, held_pages_out=None, free_range_out=None, cu_num_draft_tokens=None,
+                  workspace=None, status=None, stream=None) -> PlanResult:
         """Pages for a step's new tokens, and their positions and slots: what
         ``rotate``, ``kv_write`` and ``attend`` take.  ``block_tables`` and
         ``free_pages`` are updated, and so are ``held_pages`` and ``free_range``
         unless their outputs are given.  Requests with a negative
-        ``num_computed_tokens`` are done: their pages go back."""
+        ``num_computed_tokens`` are done: their pages go back, but for the first
+        ``num_shared_pages``, which all tables share."""
         import torch
         dev = num_new_tokens.device
         if positions is None or slot_mapping is None or seq_lens is None or workspace is None:
@@ -1235,8 +1237,9 @@ class Verifier:
                               num_computed_tokens=num_computed_tokens, block_tables=block_tables,
                               held_pages=held_pages, held_pages_out=held_pages_out, free_pages=free_pages,
                               free_range=free_range, free_range_out=free_range_out, block_size=block_size,
-                              num_rows=num_rows, positions=positions, slot_mapping=slot_mapping, seq_lens=seq_lens,
-                              cu_num_draft_tokens=cu_num_draft_tokens, workspace=workspace, status=status)
+                              num_rows=num_rows, num_shared_pages=num_shared_pages, positions=positions,
+                              slot_mapping=slot_mapping, seq_lens=seq_lens, cu_num_draft_tokens=cu_num_draft_tokens,
+                              workspace=workspace, status=status)
         return PlanResult(positions, slot_mapping, seq_lens, held_pages_out, free_range_out)
 
     def rotate(self, *, positions, frequencies: RotaryFrequencies, q=None, key=None, q_out=None, key_out=None,

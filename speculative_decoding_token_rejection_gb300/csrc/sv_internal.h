@@ -271,7 +271,7 @@ cudaError_t launch_kv4_read(const Kv4Params &p, bool bf16, bool vec, cudaStream_
 
 // Block tables, positions and slots of a step (sv_plan.cu).
 struct PlanParams {
-  int32_t N, block, width;
+  int32_t N, block, width, shared;
   FastDiv page;
   int64_t R;
   const int32_t *fresh, *computed;

@@ -132,8 +132,8 @@ __device__ __forceinline__ int request_behind(const int32_t *end, int n, int64_t
 __device__ __forceinline__ void give_back(const PlanParams &P, const Workspace &W, int i, int thread, int threads) {
   if (W.start[i] >= 0) return;
   const int64_t to = ~W.start[i];
-  const int count = W.held[i];
-  const int32_t *const row = P.tables + i * P.table_stride;
+  const int count = W.held[i] - P.shared;
+  const int32_t *const row = P.tables + i * P.table_stride + P.shared;
 #pragma unroll 8
   for (int k = thread; k < count; k += threads) {
     const int64_t at = to + k;  // (more pages than the ring has places would come round more than once)
@@ -172,13 +172,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
     const int64_t len = p + n;
     const uint32_t pages = static_cast<uint32_t>(len) / static_cast<uint32_t>(P.block);  // (both counts are below 2^31)
     const int64_t need = pages + (pages * static_cast<uint32_t>(P.block) != static_cast<uint32_t>(len));
-    if (good && (need > P.width || len > 0x7FFFFFFF || static_cast<int64_t>(held) * P.block < p)) {
+    if (good && (need > P.width || len > 0x7FFFFFFF || static_cast<int64_t>(held) * P.block < p || held < P.shared)) {
       good = false;
       bits |= SV_DATA_BAD_PARAM;
     }
     const int64_t want = good && need > held ? need - held : 0;
-    const bool returns = in && done && pool && holds && held > 0;
-    Sums x = warp_scan(Sums{n, want, returns ? held : 0});
+    const bool returns = in && done && pool && holds && held > P.shared;
+    const int back = returns ? held - P.shared : 0;
+    Sums x = warp_scan(Sums{n, want, back});
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
     if (warp == 0) warp_sums[lane] = warp_scan(warp_sums[lane]);
@@ -204,11 +205,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
       int64_t place = 0;
       if (takes) place = from + x.want - want;  // (below twice the capacity)
       W.end[i] = static_cast<int32_t>(min(x.rows, P.R));
-      W.start[i] = returns ? ~static_cast<int32_t>((to + x.back - held) % P.capacity)
+      W.start[i] = returns ? ~static_cast<int32_t>((to + x.back - back) % P.capacity)
                            : static_cast<int32_t>(place < P.capacity ? place : place - P.capacity);
       W.held[i] = held;
       if (P.cu) P.cu[i] = static_cast<int32_t>(min(x.rows - (i + 1), int64_t{0x7FFFFFFF}));
-      P.held_out[i] = returns ? 0 : takes ? static_cast<int32_t>(need) : held;
+      P.held_out[i] = returns ? P.shared : takes ? static_cast<int32_t>(need) : held;
       P.seq_lens[i] = good ? static_cast<int32_t>(len) : 0;
     }
     if (takes) atomicMax(&given, static_cast<unsigned long long>(x.want));

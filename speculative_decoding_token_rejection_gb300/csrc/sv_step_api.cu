@@ -220,7 +220,8 @@ sv_status spec_verify_check_plan_args(const spec_verify_config *c, const spec_ve
     return fail(SV_ERR_CAPACITY, "num_reqs %d > handle max %d", a->num_reqs, c->max_num_reqs);
   if (a->block_size < 1) return fail(SV_ERR_INVALID_ARG, "block_size < 1");
   if (a->table_width < 0) return fail(SV_ERR_INVALID_ARG, "table_width < 0");
-  if (a->reserved) return fail(SV_ERR_INVALID_ARG, "reserved must be 0");
+  if (a->num_shared_pages < 0 || a->num_shared_pages > a->table_width)
+    return fail(SV_ERR_INVALID_ARG, "num_shared_pages must be in [0, table_width]");
   if (a->num_rows < 0) return fail(SV_ERR_INVALID_ARG, "num_rows < 0");
   if (a->num_rows > INT_MAX - 65536) return fail(SV_ERR_UNSUPPORTED, "too many rows for one call");
   if (a->block_table_stride < a->table_width)
@@ -263,6 +264,7 @@ sv_status spec_verify_plan_step(spec_verify_t h, const spec_verify_plan_args *a,
   p.N = a->num_reqs;
   p.block = a->block_size;
   p.width = a->table_width;
+  p.shared = a->num_shared_pages;
   p.page = sv::fast_div(a->block_size);
   p.R = a->num_rows;
   p.fresh = a->num_new_tokens;

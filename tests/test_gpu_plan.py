@@ -21,7 +21,7 @@ def books(c):
     """(outputs, status) of a state dict of lists and CPU tensors."""
     b, R, C = c["block"], c["rows"], len(c["ring"])
     table, ring = c["table"].clone(), list(c["ring"])
-    width = table.shape[1]
+    width, shared = table.shape[1], c.get("shared", 0)
     head, tail = c["range"]
     pool = head >= 0 and head <= tail and tail - head <= C
     status = 0 if pool else BITS["BAD_PARAM"]
@@ -38,7 +38,7 @@ def books(c):
         row += n
         cu.append(min(row - (i + 1), 2 ** 31 - 1))
         need = -(-(p + n) // b)
-        if good and (need > width or p + n > 2 ** 31 - 1 or h * b < p):
+        if good and (need > width or p + n > 2 ** 31 - 1 or h * b < p or h < shared):
             good = False
             status |= BITS["BAD_PARAM"]
         if good and row > R:
@@ -49,11 +49,11 @@ def books(c):
             if not pool or wanted > tail - head:
                 good = False
                 status |= BITS["NO_PAGES"]
-        if p < 0 and pool and 0 < h <= width:
-            for x in table[i, :h].tolist():
+        if p < 0 and pool and shared < h <= width:
+            for x in table[i, shared:h].tolist():
                 ring[end % C] = x
                 end += 1
-            h = 0
+            h = shared
         if good and need > h:
             table[i, h:need] = torch.tensor([c["ring"][(begin + x) % C] for x in range(need - h)], dtype=torch.int32)
             begin += need - h
@@ -106,6 +106,8 @@ def call(ver, c, in_place=False, stream=None, wide=0):
     positions = torch.full((c["rows"],), 77, dtype=torch.int32, device="cuda")
     slots = torch.full((c["rows"],), 77, dtype=torch.int64, device="cuda")
     torch.cuda.synchronize()
+    if "shared" in c:
+        outs["num_shared_pages"] = c["shared"]
     r = ver.plan_step(num_new_tokens=new, num_computed_tokens=past, block_tables=table, held_pages=held,
                       free_pages=ring, free_range=span, block_size=c["block"], num_rows=c["rows"], positions=positions,
                       slot_mapping=slots, cu_num_draft_tokens=cu, status=status, stream=stream, **outs)
@@ -285,3 +287,20 @@ def test_small_workspace(ver):
                       free_pages=t, free_range=torch.zeros(2, dtype=torch.int64, device="cuda"), block_size=16,
                       num_rows=0, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert ei.value.code == sv.SV_ERR_CAPACITY
+
+
+@pytest.mark.parametrize("N", [5, 60, 700])
+def test_pages_that_all_share_stay(ver, N):
+    """A prefix of three pages at the head of every table: done requests give back only what is their own."""
+    new, past, *_ = rand(N, N, 9, 400, done=0.3)
+    past = [p if p < 0 else p + 48 for p in past]
+    held = [3 + i % 7 if p < 0 else -(-p // 16) for i, p in enumerate(past)]
+    c = state(new, past, held=held, pad=7, spare=N + 5)
+    c["table"][:, :3] = torch.tensor([9000, 9001, 9002], dtype=torch.int32)
+    c["shared"] = 3
+    check(ver, c)
+    check(ver, c, in_place=True)
+    c["held"][0], c["past"][0] = 2, 20  # (a live request that does not hold them)
+    check(ver, c, BITS["BAD_PARAM"])
+    c["held"][0], c["past"][0] = 2, -1  # (an idle place need not)
+    check(ver, c)

@@ -18,16 +18,24 @@ pytestmark = pytest.mark.gpu
 class Server:
     """N requests' device state, and one step of it."""
 
-    def __init__(self, N, heads, group, dim, block, width, fmt, seed):
+    def __init__(self, N, heads, group, dim, block, width, fmt, seed, shared=0):
+        self.shared = shared  # pages of a prefix at the head of every table
         self.N, self.heads, self.group, self.dim, self.block, self.width = N, heads, group, dim, block, width
         self.ver = sv.Verifier(N, 63, 8)
         self.cache = cache4.make_cache4(N * width, heads, block, dim, fmt)
         i32 = dict(dtype=torch.int32, device="cuda")
         self.tables, self.held = torch.zeros(N, width, **i32), torch.zeros(N, **i32)
         gen = torch.Generator().manual_seed(seed)
-        self.free = torch.randperm(N * width, generator=gen).to(torch.int32).cuda()
-        self.span = torch.tensor([0, N * width], device="cuda")
+        pages = torch.randperm(N * width, generator=gen).to(torch.int32).cuda()
+        self.free = pages[shared:].contiguous()
+        self.tables[:, :shared] = pages[:shared]
+        self.held += shared
+        self.span = torch.tensor([0, N * width - shared], device="cuda")
         self.computed = torch.zeros(N, **i32)
+        if shared:
+            rows = torch.randn(2, shared * block, heads, dim, generator=gen).cuda()
+            slots = (pages[:shared, None].long() * block + torch.arange(block, device="cuda")).flatten()
+            self.ver.kv_write(cache=self.cache, key=rows[0], value=rows[1], slot_mapping=slots)
         self.new = torch.zeros(N, **i32)
         self.status = torch.zeros(1, **i32)
         self.frequencies = sv.RotaryFrequencies(dim, scaling="yarn", factor=4.0, trained_len=64)
@@ -38,32 +46,35 @@ class Server:
         hq = self.heads * self.group
         q, key, value = qkv[:, :hq], qkv[:, hq:hq + self.heads], qkv[:, hq + self.heads:]
         p = self.ver.plan_step(num_new_tokens=self.new, num_computed_tokens=self.computed, block_tables=self.tables,
-                               held_pages=self.held, free_pages=self.free, free_range=self.span, block_size=self.block,
-                               num_rows=rows, cu_num_draft_tokens=cu, status=self.status, stream=stream)
+                               held_pages=self.held, free_pages=self.free, free_range=self.span, num_rows=rows,
+                               block_size=self.block, num_shared_pages=self.shared, cu_num_draft_tokens=cu,
+                               status=self.status, stream=stream)
         q, key = self.ver.rotate(q=q, key=key, positions=p.positions, frequencies=self.frequencies, q_weight=self.norms[0],
                                  key_weight=self.norms[1], stream=stream)
         self.ver.kv_write(cache=self.cache, key=key, value=value, slot_mapping=p.slot_mapping, status=self.status,
                           stream=stream)
         out = self.ver.attend(q=q, cache=self.cache, block_tables=self.tables, seq_lens=p.seq_lens,
                               max_seq_len=self.width * self.block, max_spec_len=most, scale=self.dim ** -0.5,
-                              cu_num_draft_tokens=cu, status=self.status, stream=stream)
+                              shared_prefix_len=self.shared * self.block, cu_num_draft_tokens=cu, status=self.status, stream=stream)
         return p, q, key, value, out
 
 
 @pytest.mark.parametrize("kw", [dict(N=5, heads=2, group=4, dim=128, block=16, width=12, fmt="e2m1"),
-                                dict(N=40, heads=1, group=3, dim=64, block=7, width=20, fmt="int4")])
+                                dict(N=40, heads=1, group=3, dim=64, block=7, width=20, fmt="int4"),
+                                dict(N=30, heads=2, group=2, dim=64, block=64, width=260, fmt="e2m1", shared=257)])
 def test_steps_against_books_and_formulas(kw):
     """Prompts, verify steps, rollbacks, a request that ends and one that takes its place."""
     s = Server(seed=1, **kw)
     N, block = s.N, s.block
     gen = torch.Generator().manual_seed(2)
-    new, past = torch.randint(1, 60, (N,), generator=gen).tolist(), [0] * N
+    begin = s.shared * block
+    new, past = torch.randint(1, 60, (N,), generator=gen).tolist(), [begin] * N
     for step in range(5):
         rows, most = sum(new), max(new) - 1
         s.new.copy_(torch.tensor(new))
         s.computed.copy_(torch.tensor(past))
         want, bits = plan.books(dict(new=new, past=past, held=s.held.tolist(), block=block, table=s.tables.cpu(),
-                                     ring=s.free.tolist(), range=s.span.tolist(), rows=rows))
+                                     ring=s.free.tolist(), range=s.span.tolist(), rows=rows, shared=s.shared))
         assert bits == 0
         qkv = (2 * torch.randn(rows, s.heads * (s.group + 2), s.dim, generator=gen)).cuda().to(torch.bfloat16)
         given = qkv.clone()
@@ -92,7 +103,7 @@ def test_steps_against_books_and_formulas(kw):
         # drafts are rejected, a request ends, another begins
         for i in range(N):
             if past[i] < 0:
-                past[i], new[i] = 0, 1 + (7 * i + step) % 30
+                past[i], new[i] = begin, 1 + (7 * i + step) % 30
             else:
                 past[i] = want["seq"][i] - (int(torch.randint(0, 4, (1,), generator=gen)) % new[i] if step else 0)
                 new[i] = 1 + int(torch.randint(0, 6, (1,), generator=gen))

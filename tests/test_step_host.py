@@ -108,7 +108,8 @@ def plan_args():
 @pytest.mark.parametrize("path,value,code", [
     ("num_reqs", 3, OK), ("num_reqs", -1, INVALID), ("num_reqs", 9, CAPACITY), ("num_reqs", 0, OK),
     ("block_size", 0, INVALID), ("block_size", 1, OK), ("table_width", -1, INVALID), ("table_width", 8, INVALID),
-    ("table_width", 0, OK), ("reserved", 1, INVALID), ("num_rows", -1, INVALID), ("num_rows", 0, OK),
+    ("table_width", 0, OK), ("num_shared_pages", -1, INVALID), ("num_shared_pages", 7, OK),
+    ("num_shared_pages", 8, INVALID), ("num_rows", -1, INVALID), ("num_rows", 0, OK),
     ("num_rows", 1 << 31, UNSUPPORTED), ("free_capacity", 0, INVALID), ("free_capacity", 1 << 31, UNSUPPORTED),
     ("workspace_bytes", -1, INVALID), ("workspace", FAKE + 8, INVALID), ("cu_num_draft_tokens", FAKE, OK)] + [
         (name, None, INVALID) for name in ("num_new_tokens", "num_computed_tokens", "block_tables", "held_pages",
