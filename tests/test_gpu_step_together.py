@@ -55,7 +55,8 @@ class Server:
                           stream=stream)
         out = self.ver.attend(q=q, cache=self.cache, block_tables=self.tables, seq_lens=p.seq_lens,
                               max_seq_len=self.width * self.block, max_spec_len=most, scale=self.dim ** -0.5,
-                              shared_prefix_len=self.shared * self.block, cu_num_draft_tokens=cu, status=self.status, stream=stream)
+                              shared_prefix_len=self.shared * self.block, cu_num_draft_tokens=cu, status=self.status,
+                              stream=stream)
         return p, q, key, value, out
 
 
