@@ -94,6 +94,9 @@ struct OwnSmem {
 };
 __device__ __forceinline__ int line_at(int line, int col) { return line * 128 + ((col ^ (line & 7)) << 4); }
 
+// Tensor memory is reached by whole warps (.aligned): behind a branch that lanes take apart, and behind a wait, which they
+// leave one by one, a __syncwarp() comes first.
+
 // Sixteen columns of the thread's lane.
 __device__ __forceinline__ void tmem_store_row(uint32_t addr, const uint32_t r[16]) {
   asm volatile(
@@ -270,6 +273,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
     fence_mbar_init();
   }
   if (warp == 0) {
+    __syncwarp();
     tmem_get(&C.tmem, kOwnCols);
     tmem_get(&C.tmem_keys, kKeyCols);
     tmem_no_more();
@@ -351,6 +355,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
   // Half (or all) of the keys in krow to tensor memory, and their part of the scores.
   constexpr int kTwos = D / 32 / kHalves;  // pairs of groups in it
   auto unpack_keys = [&](int half) {
+    __syncwarp();
 #pragma unroll
     for (int two = 0; two < kTwos; ++two) {
       const int at = half * kTwos + two;
@@ -430,6 +435,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
       for (int r = 0; r < T.rows; ++r)
         if (key < C.limit[r]) C.none[r] = 1;
     }
+    __syncwarp();
     // Two eights of rows at a time: columns 16 g .. (the first eight again where there is one).
     auto load_scores = [&](int g, float x[16]) {
       const uint32_t at = s_mine + g * 16;
@@ -494,6 +500,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
               const float most = reduce_eight<true>(x + 8 * c, lane);
               if ((lane & 3) == 0 && 2 * g + c < n8) C.part[warp][g * 16 + c * 8 + (lane >> 2)] = most;
             }
+            __syncwarp();
           }
           __syncthreads();
           return tid < n8 * 8 ? fmaxf(fmaxf(C.part[0][tid], C.part[1][tid]), fmaxf(C.part[2][tid], C.part[3][tid])) : 0.0f;
@@ -533,6 +540,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
         force = __syncthreads_or(unset);
         if (it > 0) {
           ok = wait(C, &C.o_full, (it - 1) & 1) && ok;
+          __syncwarp();
           fence_after();
 #pragma unroll
           for (int c = 0; c < NMAX / 8; ++c)
@@ -695,6 +703,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
         }
       }
     }
+    __syncwarp();
   }
   if (P.status) {
     const uint32_t bits = __reduce_or_sync(0xFFFFFFFFu, (bad ? static_cast<uint32_t>(SV_DATA_BAD_SLOT) : 0u) |
