@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
       stop = gave_up(C);
       if (stop) break;
       // The sums as they were.  (What the subtraction loses is 2^-24 of a weight that comes again; beside one that is no
-      // number of fp32 the sums so far, below 2^106, are nothing.)
+      // number of fp32 the sums so far, below 2^106, are nothing.  A NaN of a key before stays.)
 #pragma unroll
       for (int g = 0; g < NMAX / 16; ++g)
         if (2 * g < n8) {
@@ -613,7 +613,8 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float w = exp2_approx(x[e]);
-            if (2 * g + (e >> 3) < n8) l[g * 16 + e] = x[e] < 127.0f ? l[g * 16 + e] - w : 0.0f;
+            float &sum = l[g * 16 + e];
+            if (2 * g + (e >> 3) < n8) sum = x[e] < 127.0f || sum != sum ? sum - w : 0.0f;
           }
         }
       fresh = true;

@@ -19,6 +19,11 @@ def places(c, i, keys):
     return c["table"][i].long()[t // c["cache"].block_size], t % c["cache"].block_size
 
 
+def crowd(*lens):
+    """Lengths of a batch so large that a request's keys are one CTA's work, tile after tile."""
+    return dict(gammas=[3] * 320, lens=[*lens] + [4] * (320 - len(lens)), kv_heads=1, uniform=True)
+
+
 @pytest.mark.parametrize("dim, rows", FORMS)
 def test_every_third_value_scale_is_no_number(dim, rows):
     c = make([3, 3, 0], [700, 300, 50], kv_heads=2, group=rows // 4, dim=dim, seed=rows)
@@ -52,11 +57,11 @@ def test_every_other_page_is_outside(dim, rows):
 @pytest.mark.parametrize("dim, rows", FORMS)
 def test_maxima_that_rise_tile_after_tile(dim, rows):
     """Some rows' maxima rise in every tile, others' fall (queries of both signs)."""
-    c = make([3, 3], [1100, 513], kv_heads=1, group=rows // 4, dim=dim, seed=rows + 2)
+    c = make(**crowd(1100, 513), group=rows // 4, dim=dim, seed=rows + 2)
     c["q"] = c["q"].abs().clone()
     c["q"][1::2] *= -1
     c["cache"].k &= 0x77
-    for i, n in enumerate(c["lens"]):
+    for i, n in enumerate(c["lens"][:2]):
         page, off = places(c, i, range(n))
         c["cache"].k_scale[page, 0, off] = 0.02 * torch.exp2(torch.arange(n, device="cuda") / 128)
     check(c)
