@@ -477,7 +477,7 @@ __device__ __forceinline__ bool attend_tile(const AttendParams &P, const AttendP
     const int lr = T.r0 + r, hq = T.h * P.group + lr - div_by(lr, L.group) * P.group;
     Part<D> all;
     all.m = fmaxf(fmaxf(J.m[0][r], J.m[1][r]), fmaxf(J.m[2][r], J.m[3][r]));
-    all.l = 0.0f;
+    all.rest = all.l = 0.0f;
 #pragma unroll
     for (int d = 0; d < kDims; ++d) all.o[d] = 0.0f;
 #pragma unroll
@@ -594,7 +594,7 @@ template <int D>
 __device__ __forceinline__ Part<D> no_part() {
   Part<D> p;
   p.m = -INFINITY;
-  p.l = 0.0f;
+  p.rest = p.l = 0.0f;
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) p.o[d] = 0.0f;
   return p;
@@ -764,12 +764,16 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   L.qvec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0;
   L.ovec = (reinterpret_cast<uintptr_t>(p.out) & 7u) == 0 && p.out_token % 4 == 0 && p.out_head % 4 == 0;
   const int64_t rows = static_cast<int64_t>(L.rows) * p.c.num_kv_heads;
-  // the workspace: the prefix's tiles, then M and l, then O
+  // the workspace: the prefix's tiles, then M and l, then what is beside M, then O
   const int64_t image = static_cast<int64_t>(L.image_tiles) * p.c.num_kv_heads * kPrefixKeyTile * p.c.head_dim * 4;
-  if (bytes) *bytes = bound <= 1 ? 0 : image + ((rows * bound * 8 + 15) & ~int64_t{15}) + rows * bound * p.c.head_dim * 4;
+  const auto sums = [&](int64_t slots) { return (rows * slots * 8 + 15) & ~int64_t{15}; };
+  const auto rests = [&](int64_t slots) { return four_bits(p) ? (rows * slots * 4 + 15) & ~int64_t{15} : 0; };
+  if (bytes) *bytes = bound <= 1 ? 0 : image + sums(bound) + rests(bound) + rows * bound * p.c.head_dim * 4;
   L.image = static_cast<uint8_t *>(p.workspace);
   L.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(p.workspace) + image);
-  L.part_o = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + image + ((rows * L.slots * 8 + 15) & ~int64_t{15}));
+  char *const behind = reinterpret_cast<char *>(L.part_ml) + sums(L.slots);
+  L.part_rest = four_bits(p) ? reinterpret_cast<float *>(behind) : nullptr;
+  L.part_o = reinterpret_cast<float *>(behind + rests(L.slots));
   return L;
 }
 

@@ -44,6 +44,7 @@ struct AttendPlan {
   uint8_t *image;         // the prefix as f16 tiles: [num_kv_heads][image_tiles][K, V]
   float *part_o;          // [rows * num_kv_heads][slots][D], row = token * Hq + query head
   float2 *part_ml;        // [rows * num_kv_heads][slots]: M, l
+  float *part_rest;       // [rows * num_kv_heads][slots]: what a maximum kept as two numbers is beside M (8-bit cache: null)
 };
 
 // The prefix on the tensor cores' memory (sv_attend_prefix.cu): tiles of
@@ -147,11 +148,10 @@ __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-
-// One partial result of a row: M, l and the lane's dimensions of O.
+// One partial result of a row: M (and what is beside it), l and the lane's dimensions of O.
 template <int D>
 struct Part {
-  float m, l, o[D / 32];
+  float m, rest, l, o[D / 32];
 };
 constexpr int kJoinAhead = 4;  // partial results of a row in flight
 template <int D>
@@ -160,6 +160,7 @@ __device__ __forceinline__ Part<D> load_part(const AttendPlan &L, int64_t row, i
   const float2 ml = __ldcg(L.part_ml + row * L.slots + s);
   p.m = ml.x;
   p.l = ml.y;
+  p.rest = L.part_rest ? __ldcg(L.part_rest + row * L.slots + s) : 0.0f;
   const float *src = L.part_o + (row * L.slots + s) * D;
   if (D == 128) {
     const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
@@ -187,9 +188,11 @@ __device__ __forceinline__ void store_part(const AttendPlan &L, int64_t row, int
 // zeros, or NaN where all its scores are, and is added as it is.
 template <int D>
 __device__ __forceinline__ void join_part(Part<D> &a, const Part<D> &b) {
-  const float m = fmaxf(a.m, b.m);
-  const float fa = a.m == -INFINITY ? 1.0f : exp2_approx(a.m - m), fb = b.m == -INFINITY ? 1.0f : exp2_approx(b.m - m);
+  const float m = fmaxf(a.m, b.m), rest = b.m > a.m || (b.m == a.m && b.rest > a.rest) ? b.rest : a.rest;
+  const float fa = a.m == -INFINITY ? 1.0f : exp2_approx((a.m - m) + (a.rest - rest));
+  const float fb = b.m == -INFINITY ? 1.0f : exp2_approx((b.m - m) + (b.rest - rest));
   a.m = m;
+  a.rest = rest;
   a.l = fmaf(a.l, fa, b.l * fb);
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) a.o[d] = fmaf(a.o[d], fa, b.o[d] * fb);
@@ -215,7 +218,7 @@ __device__ __forceinline__ void write_row(const AttendParams &P, const AttendPla
       dst[3] = static_cast<uint16_t>(w1 >> 16);
     }
   }
-  if (P.lse && lane == 0) P.lse[token * P.Hq + hq] = p.l == 0.0f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
+  if (P.lse && lane == 0) P.lse[token * P.Hq + hq] = p.l == 0.0f ? -INFINITY : (p.m + (p.rest + log2f(p.l))) * kLn2;
 }
 
 // A CTA of the private part: a request's row tile of one kv head over one chunk of its keys.

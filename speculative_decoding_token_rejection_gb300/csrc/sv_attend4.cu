@@ -658,13 +658,16 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
   if (tid < T.rows) {
     const int lr = T.r0 + tid, j = div_by(lr, L.group), hq = T.h * P.group + lr - j * P.group;
     const float m = lost ? -INFINITY : C.mx[tid] + C.mu[tid];
+    // (the sums are those of both parts where they were subtracted one after the other)
+    const float rest = C.huge && fabsf(m) < INFINITY ? (C.mx[tid] - m) + C.mu[tid] : 0.0f;
     const float sum = lost ? nan : (C.part[0][tid] + C.part[1][tid]) + (C.part[2][tid] + C.part[3][tid]);
     const int64_t at = (T.first + j) * P.Hq + hq;
     const int64_t slot = at * L.slots + L.prefix_splits + T.split;
     if (T.whole) {
-      if (P.lse) P.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+      if (P.lse) P.lse[at] = sum == 0.0f ? -INFINITY : (m + (rest + log2f(sum))) * kLn2;
     } else {
       L.part_ml[slot] = make_float2(m, sum);
+      L.part_rest[slot] = rest;
     }
     C.to[tid] = T.whole ? (T.first + j) * P.out_token + hq * P.out_head : slot * D;
     // (a row without keys that count has the output 0.  Some w was 2^-log2(value_scale / W) at least, so sum is above

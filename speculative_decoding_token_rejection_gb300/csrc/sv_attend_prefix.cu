@@ -546,8 +546,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           float sum = lo(l[x]) + hi(l[x]);
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-          if (c == 0 && at[x] >= 0)
+          if (c == 0 && at[x] >= 0) {
             L.part_ml[at[x]] = ok ? make_float2(m[x], sum) : make_float2(-INFINITY, __uint_as_float(0x7FC00000u));
+            if (L.part_rest) L.part_rest[at[x]] = 0.0f;
+          }
         }
 #pragma unroll
         for (int q = 0; ok && q < D / 32; ++q)

@@ -1,10 +1,12 @@
 """Attention over the 4-bit cache with numbers at the ends of their ranges: NaN keys
 beside weights that pass every bound, scores so large that fp32 has no place for
 anything beside them."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_attend4 import make, run
+from test_gpu_attend4 import make, numbers, run
 from test_gpu_attend4_lanes import FORMS, crowd, places
 
 pytestmark = pytest.mark.gpu
@@ -29,3 +31,53 @@ def test_nan_stays_beside_a_weight_that_passes_the_range(dim, rows, later):
     out, lse, status = run(c)
     assert status == 0 and bool(torch.isnan(out[:4]).all()) and bool(torch.isnan(lse[:4]).all())
     assert torch.equal(out[4:], clean[4:]) and torch.equal(lse[4:], clean_lse[4:])
+
+
+def ties(lens, *, score, prefix=0, dim=128, fmt="int4", **kw):
+    """A batch in which all scores of a row are the same number, of `score` in size (base e), and value scales change by
+    fours and sixteens from 128 keys to the next."""
+    c = make([kw.pop("G", 0)] * len(lens), lens, prefix=prefix, dim=dim, fmt=fmt, uniform=True, seed=len(lens), **kw)
+    c["q"] = torch.ones_like(c["q"])
+    c["q"][:, 1::2] *= -1  # (every other query head has scores of the other sign)
+    cache = c["cache"]
+    cache.k.fill_(0x22 if fmt == "int4" else 0x44)  # 2, twice
+    cache.k_group.copy_(torch.ones(cache.k_group.shape))
+    cache.k_scale.fill_(1.0)
+    c["scale"] = score / (2 * dim)
+    cache.v_scale.fill_(1 / 64)
+    for i, n in enumerate(lens):
+        t = torch.arange(prefix if i else 0, n, device="cuda")
+        page, off = c["table"][i].long()[t // cache.block_size], t % cache.block_size
+        cache.v_scale[page, :, off] = (torch.exp2((t // 128 * 5 % 8).float()) / 64)[:, None].expand(-1, cache.num_kv_heads)
+    return c
+
+
+def check_averages(c):
+    """out is the average of the values that a row sees: bf16 (2^-8 of it), and weights of 11 bits, their exponentials and
+    sums (2^-10 of the average size).  lse is its score plus ln of the number of keys, off by the
+    roundings of the scale, its factors, the product, the maximum and the way back to base e: seven of 2^-24 at most."""
+    out, lse, status = run(c)
+    cache, b, G = c["cache"], c["cache"].block_size, c["G"]
+    assert status == 0
+    for i, n in enumerate(c["lens"]):
+        t = torch.arange(n, device="cuda")
+        page, off = c["table"][i].long()[t // b], t % b
+        raw = cache.v_group.view(torch.uint8)[page, :, off].view(torch.float8_e4m3fn)
+        v = numbers(cache.v[page, :, off], raw, cache.format) * cache.v_scale[page, :, off].double()[..., None]
+        for j in range(G + 1):
+            see, row = n - G + j, i * (G + 1) + j
+            mean = v[:see].mean(0).repeat_interleave(c["group"], 0)
+            size = v[:see].abs().mean(0).repeat_interleave(c["group"], 0)
+            assert bool(((out[row].double() - mean).abs() <= 2.0 ** -8 * mean.abs() + 2.0 ** -10 * size).all())
+            score = c["q"][row, :, 0].double() * 2 * cache.head_dim * c["scale"]
+            assert bool(((lse[row].double() - score - math.log(see)).abs() <= 2.0 ** -21 * (score.abs() + 20)).all())
+
+
+SCORES = [1.0, 3e5, 2.0 ** 22 + 1, 2.0 ** 24 + 2, 3.0 * 2 ** 25, 2.0 ** 28, 3.3 * 2 ** 30, 1e20, 2e38]
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("dim, fmt, group", [(128, "int4", 4), (64, "e2m1", 4), (128, "e2m1", 20)])
+def test_ties_over_several_chunks(dim, fmt, group, score):
+    check_averages(ties([1000, 300, 128, 129], score=score, dim=dim, fmt=fmt, group=group))
+    check_averages(ties([3000], score=score, dim=dim, fmt=fmt, group=group, G=1))
