@@ -767,12 +767,13 @@ AttendPlan make_plan(const AttendParams &p, int num_sms, int64_t *bytes = nullpt
   // the workspace: the prefix's tiles, then M and l, then what is beside M, then O
   const int64_t image = static_cast<int64_t>(L.image_tiles) * p.c.num_kv_heads * kPrefixKeyTile * p.c.head_dim * 4;
   const auto sums = [&](int64_t slots) { return (rows * slots * 8 + 15) & ~int64_t{15}; };
-  const auto rests = [&](int64_t slots) { return four_bits(p) ? (rows * slots * 4 + 15) & ~int64_t{15} : 0; };
+  const bool two = four_bits(p) || L.tensor_tiles > 0;
+  const auto rests = [&](int64_t slots) { return two ? (rows * slots * 4 + 15) & ~int64_t{15} : 0; };
   if (bytes) *bytes = bound <= 1 ? 0 : image + sums(bound) + rests(bound) + rows * bound * p.c.head_dim * 4;
   L.image = static_cast<uint8_t *>(p.workspace);
   L.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(p.workspace) + image);
   char *const behind = reinterpret_cast<char *>(L.part_ml) + sums(L.slots);
-  L.part_rest = four_bits(p) ? reinterpret_cast<float *>(behind) : nullptr;
+  L.part_rest = two ? reinterpret_cast<float *>(behind) : nullptr;
   L.part_o = reinterpret_cast<float *>(behind + rests(L.slots));
   return L;
 }

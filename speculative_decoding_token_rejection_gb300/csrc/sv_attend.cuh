@@ -44,7 +44,7 @@ struct AttendPlan {
   uint8_t *image;         // the prefix as f16 tiles: [num_kv_heads][image_tiles][K, V]
   float *part_o;          // [rows * num_kv_heads][slots][D], row = token * Hq + query head
   float2 *part_ml;        // [rows * num_kv_heads][slots]: M, l
-  float *part_rest;       // [rows * num_kv_heads][slots]: what a maximum kept as two numbers is beside M (8-bit cache: null)
+  float *part_rest;       // [rows * num_kv_heads][slots]: what a maximum kept as two numbers is beside M (null where none is)
 };
 
 // The prefix on the tensor cores' memory (sv_attend_prefix.cu): tiles of
@@ -182,7 +182,10 @@ __device__ __forceinline__ void store_part(const AttendPlan &L, int64_t row, int
     reinterpret_cast<float4 *>(dst)[lane] = make_float4(p.o[0], p.o[1], p.o[D / 32 - 2], p.o[D / 32 - 1]);
   else
     reinterpret_cast<float2 *>(dst)[lane] = make_float2(p.o[0], p.o[1]);
-  if (lane == 0) L.part_ml[row * L.slots + s] = make_float2(p.m, p.l);
+  if (lane == 0) {
+    L.part_ml[row * L.slots + s] = make_float2(p.m, p.l);
+    if (L.part_rest) L.part_rest[row * L.slots + s] = p.rest;
+  }
 }
 // a joined with b: with M the larger maximum, O = sum 2^(M_s - M) O_s and l likewise.  A part without a maximum is
 // zeros, or NaN where all its scores are, and is added as it is.

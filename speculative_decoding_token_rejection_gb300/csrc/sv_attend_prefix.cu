@@ -40,15 +40,18 @@
 // 8, so P stays below 2^8.  Whether it may have is seen from max x and the
 // tile's largest value scale alone.  W is 2^28, the middle of the scales that
 // kv_write gives (2^-64 to 2^121): w and l stay within fp32 for any of them.
-// (One near the first tile's scales sent later ones out of range.)
+// (One near the first tile's scales sent later ones out of range.)  An m of 2^24
+// or more in size is two numbers: one alone would lose what the value scales add,
+// and from 2^30 on P with it its place in f16.
 //
-// Measured: 512 requests x 8 tokens over 16384 keys, 805 us of the call's 1.03
-// ms: 1.37 PFLOP/s, 72 % of a plain matrix product's rate.  A key tile takes a
+// Measured: 512 requests x 8 tokens over 16384 keys, 827 us of the call's 1.05
+// ms: 1.33 PFLOP/s, 69 % of a plain matrix product's rate.  A key tile takes a
 // CTA about 3300 cycles, of which a softmax warp works for 1800 and waits for its row
 // tile's products for 1250; a segment adds 25000 (queries in, results out).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "sv_attend.cuh"
 #include "sv_cache4.cuh"
@@ -64,6 +67,7 @@ constexpr int kVectorThreads = 64;
 constexpr int kPrefixThreads = kSoftmaxThreads + kVectorThreads + 64;
 constexpr int kVectorSlots = 4;
 constexpr float kRaise = 8;
+constexpr float kFar = 0x1p24f;  // maxima of this size are two numbers
 constexpr float kScaleUnit = 0x1p28f;  // W
 constexpr float kLeastUnits = kLeastLog2 - 28;  // log2 of the size that a scale counts as at least, in W
 
@@ -78,6 +82,7 @@ struct Control {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], vec_full[kVectorSlots], vec_empty[kVectorSlots], s_full[2], p_full[2], q_full, done;
   uint32_t tmem, abort;
   float back[2 * kRowsTile];  // what undoes a row's power of two
+  float rest[2 * kRowsTile];  // what a row's maximum is beside m
 };
 
 static_assert(sizeof(Vectors) % 16 == 0, "every slot starts on a 16-byte boundary");
@@ -333,7 +338,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           for (int b = kLanes / 2; b; b >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, b));
           const int shift = query_shift(top), r = w4 * 32 + f * kRowsPass + lane / kLanes, col = lane % kLanes;
           shifted |= shift != 0;
-          if (col == 0) C.back[t * kRowsTile + r] = pow2(-shift);
+          if (col == 0) {
+            C.back[t * kRowsTile + r] = pow2(-shift);
+            C.rest[t * kRowsTile + r] = 0.0f;
+          }
           const float up = pow2(shift);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -373,6 +381,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         l[x] = pair(0.0f, 0.0f);
       }
       uint32_t nan_rows = 0;  // bit x: the row sees a value scale that is no number
+      float *const rest = C.rest + t * kRowsTile + w4 * 32 + g;  // of the lane's rows: x * 8
       for (int i = 0; ok && i < n; ++i) {
         const int it = done_tiles + i;
         const Vectors &V = vec[it % kVectorSlots];
@@ -398,6 +407,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
             tmem_wait_load(s[0] + 16 * q);
             tmem_wait_load(s[1] + 16 * q);
           }
+        };
+        auto is_far = [&]() {  // some row of the warp has such a maximum
+          bool is = false;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) is |= fabsf(m[x]) >= kFar && m[x] != -INFINITY;
+          return __any_sync(0xFFFFFFFFu, is);
         };
         auto get = [&](int x, int j) {  // columns 8j + 2c, + 1 of row x
           return pair(__uint_as_float(s[x >> 1][j * 4 + (x & 1) * 2]), __uint_as_float(s[x >> 1][j * 4 + (x & 1) * 2 + 1]));
@@ -428,7 +443,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           plain = __all_sync(0xFFFFFFFFu, !(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) + over > kRaise));
           if (!plain) load_scores();  // (they are still there)
         }
-        if (!plain) {
+        // Otherwise: x and m, or, where some m of the warp is kFar or more in size, what they are beside `from`.
+        const bool far = !plain && is_far();
+        auto general = [&](auto two) {
+          constexpr bool kTwo = decltype(two)::value;
           // x, and its largest.  A product of its own, rounded: subtracting a maximum that equals it gives 0.
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           int limit[4];
@@ -461,7 +479,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
 #pragma unroll
             for (int x = 0; x < 4; ++x) nan_rows |= key < limit[x] ? 1u << x : 0u;
           }
-          bool raise = false;
+          float from[4];
+          if (kTwo) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              from[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
+              from[x] = fmaxf(fmaxf(from[x], __shfl_xor_sync(0xFFFFFFFFu, from[x], 2)), m[x]);
+              if (fabsf(from[x]) == INFINITY) from[x] = 0.0f;
+              m[x] = (m[x] - from[x]) + rest[x * 8];
+              top[x] -= from[x];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const Pair y = add2(get(x, j), pair(-from[x], -from[x]));
+                put(x, j, lo(y), hi(y));
+              }
+            }
+          }
+          bool raise = kTwo && !far;
 #pragma unroll
           for (int x = 0; x < 4; ++x) raise |= top[x] + over > m[x] + kRaise || (m[x] == -INFINITY && top[x] > -INFINITY);
           if (__any_sync(0xFFFFFFFFu, raise)) {  // (seldom after the first tiles)
@@ -480,7 +514,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
             for (int x = 0; x < 4; ++x) {
               most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 1));
               most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], 2));
-              const float next = most[x] > m[x] + kRaise || m[x] == -INFINITY ? most[x] : m[x];
+              const bool anew = kTwo && !far && fabsf(from[x] + m[x]) >= kFar;  // (raised for this tile, as one number)
+              const float next = most[x] > m[x] + kRaise || anew || m[x] == -INFINITY ? most[x] : m[x];
               r[x] = m[x] == -INFINITY ? 1.0f : exp2_approx(m[x] - next);  // (without a maximum O and l are zeros or NaN)
               m[x] = next;
               l[x] = mul2(l[x], pair(r[x], r[x]));
@@ -499,6 +534,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
                 }
             }
           }
+          if (kTwo) {
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float sum = from[x] + m[x];
+              if (fabsf(sum) < kFar) m[x] = sum - from[x];  // (one number again)
+              if (c == 0) rest[x * 8] = fabsf(sum) < INFINITY ? (from[x] - sum) + m[x] : 0.0f;
+            }
+            __syncwarp();
+          }
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const Pair neg = m[x] == -INFINITY ? pair(0.0f, 0.0f) : pair(-m[x], -m[x]);
@@ -507,7 +552,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
               const Pair y = add2(get(x, j), neg);
               put(x, j, lo(y), hi(y));
             }
+            if (kTwo) m[x] += from[x];
           }
+        };
+        if (!plain && !far) general(std::false_type{});
+        if (!plain && is_far()) {
+          if (!far) load_scores();
+          general(std::true_type{});
         }
         // the weights, sixteen columns of a half at a time
 #pragma unroll
@@ -548,7 +599,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
           if (c == 0 && at[x] >= 0) {
             L.part_ml[at[x]] = ok ? make_float2(m[x], sum) : make_float2(-INFINITY, __uint_as_float(0x7FC00000u));
-            if (L.part_rest) L.part_rest[at[x]] = 0.0f;
+            L.part_rest[at[x]] = ok ? rest[x * 8] : 0.0f;
           }
         }
 #pragma unroll

@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import test_gpu_attend as eight
 from test_gpu_attend4 import make, numbers, run
 from test_gpu_attend4_lanes import FORMS, crowd, places
 
@@ -81,3 +82,43 @@ SCORES = [1.0, 3e5, 2.0 ** 22 + 1, 2.0 ** 24 + 2, 3.0 * 2 ** 25, 2.0 ** 28, 3.3 
 def test_ties_over_several_chunks(dim, fmt, group, score):
     check_averages(ties([1000, 300, 128, 129], score=score, dim=dim, fmt=fmt, group=group))
     check_averages(ties([3000], score=score, dim=dim, fmt=fmt, group=group, G=1))
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("dim, fmt, G, group", [(128, "int4", 4, 4), (64, "e2m1", 4, 4), (128, "e2m1", 0, 1)])
+def test_ties_behind_a_shared_prefix(dim, fmt, G, group, score):
+    """More than one CTA of the prefix for a row, and several chunks behind it."""
+    lens = [7168 + 100 * i for i in range(1, 8)] + [7168, 7169 + G] + [7232] * 71
+    check_averages(ties(lens, score=score, dim=dim, fmt=fmt, prefix=7168, G=G, group=group, kv_heads=2))
+    lens = [16400 + i for i in range(80)]
+    check_averages(ties(lens, score=score, dim=dim, fmt=fmt, prefix=16384, group=1, kv_heads=1))
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_ties_behind_a_shared_prefix_of_eight_bits(fmt, score):
+    """The 8-bit cache's prefix is the same kernel's work."""
+    lens = [7168 + 100 * i for i in range(1, 8)] + [7232] * 73
+    c = eight.make([4] * len(lens), lens, prefix=7168, kv_heads=2, fmt=fmt, uniform=True, seed=1)
+    c["q"] = torch.ones_like(c["q"])
+    c["q"][:, 1::2] *= -1
+    cache, b = c["cache"], c["cache"].block_size
+    cache.k.copy_(torch.full(cache.k.shape, 2.0))
+    cache.k_scale.fill_(1.0)
+    c["scale"] = score / (2 * cache.head_dim)
+    for i, n in enumerate(lens):
+        page, off = places(c, i, range(7168 if i else 0, n))
+        step = torch.arange(7168 if i else 0, n, device="cuda") // 128 * 5 % 8
+        cache.v_scale[page, :, off] = (torch.exp2(step.float()) / 64)[:, None].expand(-1, 2)
+    out, lse, status = eight.run(c)
+    assert status == 0
+    for i, n in enumerate(lens[:8]):
+        page, off = places(c, i, range(n))
+        v = cache.v[page, :, off].double() * cache.v_scale[page, :, off].double()[..., None]
+        for j in range(5):
+            see, row = n - 4 + j, i * 5 + j
+            mean = v[:see].mean(0).repeat_interleave(c["group"], 0)
+            size = v[:see].abs().mean(0).repeat_interleave(c["group"], 0)
+            assert bool(((out[row].double() - mean).abs() <= 2.0 ** -8 * mean.abs() + 2.0 ** -10 * size).all())
+            exact = c["q"][row, :, 0].double() * 2 * cache.head_dim * c["scale"]
+            assert bool(((lse[row].double() - exact - math.log(see)).abs() <= 2.0 ** -21 * (exact.abs() + 20)).all())
