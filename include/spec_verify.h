@@ -586,8 +586,11 @@ sv_status spec_verify_check_attend4_args(const spec_verify_config *config, const
  * table_width pages (or passes 2^31 - 1) raise SV_DATA_BAD_PARAM, and rows that
  * pass num_rows SV_DATA_BAD_CU; such a request is treated as one that got no
  * pages and does not count among those wanted.
- * With a free_range that is negative or wider than free_capacity, or a page
- * outside it, no page is given or taken back (SV_DATA_BAD_PARAM).
+ * With a free_range that is negative or wider than free_capacity, no page is
+ * given or taken back (SV_DATA_BAD_PARAM).  Where the pages that the requests up
+ * to i give back are more than the places of free_pages that are not free pages
+ * already (books that are wrong, or a ring too small), request i's stay with it
+ * (SV_DATA_BAD_PARAM): no free page is overwritten.
  * held_pages_out may be held_pages, free_range_out free_range and seq_lens
  * num_computed_tokens.  Nothing depends on the order in which threads run. */
 typedef struct spec_verify_plan_args {

@@ -136,8 +136,8 @@ __device__ __forceinline__ void give_back(const PlanParams &P, const Workspace &
   const int32_t *const row = P.tables + i * P.table_stride + P.shared;
 #pragma unroll 8
   for (int k = thread; k < count; k += threads) {
-    const int64_t at = to + k;  // (more pages than the ring has places would come round more than once)
-    P.ring[at < P.capacity ? at : at % P.capacity] = row[k];
+    const int64_t at = to + k;  // (below twice the capacity: there is room for them)
+    P.ring[at < P.capacity ? at : at - P.capacity] = row[k];
   }
 }
 
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
   pdl_enter();
   __shared__ Sums warp_sums[kPlanWarps];
   __shared__ int32_t mark[ROWS ? kRowsCta : 1], warp_last[kPlanWarps];
-  __shared__ unsigned long long given;  // pages
+  __shared__ unsigned long long given, returned;  // pages
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Workspace W = workspace_of(P);
   const int64_t head = P.range[0], tail = P.range[1];
@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
   const bool pool = head >= 0 && tail >= head && tail - head <= P.capacity;
   if (!pool) bits |= SV_DATA_BAD_PARAM;
   const int64_t from = pool ? head % P.capacity : 0, to = pool ? tail % P.capacity : 0;
-  if (tid == 0) given = 0;
+  // (places behind the tail: what goes there meets no page that is being taken)
+  const int64_t room = pool ? P.capacity - (tail - head) : 0;
+  if (tid == 0) given = returned = 0;
   Sums before{0, 0, 0};  // of the steps before
   for (int base = 0; base < P.N; base += kPlanThreads) {
     const int i = base + tid;
@@ -177,8 +179,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
       bits |= SV_DATA_BAD_PARAM;
     }
     const int64_t want = good && need > held ? need - held : 0;
-    const bool returns = in && done && pool && holds && held > P.shared;
-    const int back = returns ? held - P.shared : 0;
+    const bool gone = in && done && pool && holds && held > P.shared;
+    const int back = gone ? held - P.shared : 0;
     Sums x = warp_scan(Sums{n, want, back});
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
@@ -200,6 +202,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
       good = false;
       bits |= SV_DATA_NO_PAGES;
     }
+    const bool returns = gone && x.back <= room;
+    if (gone && !returns) bits |= SV_DATA_BAD_PARAM;
     const bool takes = good && want > 0;
     if (in) {
       int64_t place = 0;
@@ -213,12 +217,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanP
       P.seq_lens[i] = good ? static_cast<int32_t>(len) : 0;
     }
     if (takes) atomicMax(&given, static_cast<unsigned long long>(x.want));
+    if (returns) atomicMax(&returned, static_cast<unsigned long long>(x.back));
     __syncthreads();  // (the sums have been read, and the outputs are there)
   }
   if (P.N == 0) __syncthreads();
   if (tid == 0) {
     P.range_out[0] = head + static_cast<int64_t>(given);
-    P.range_out[1] = tail + before.back;
+    P.range_out[1] = tail + static_cast<int64_t>(returned);
   }
   if (P.status) {
     bits = __reduce_or_sync(0xFFFFFFFFu, bits);
