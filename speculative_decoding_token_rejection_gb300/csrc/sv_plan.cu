@@ -15,8 +15,9 @@
 // 4096 requests: 18.0 us.  One CTA is the faster up to 250 requests of 64
 // pages (6.8 us against 9.0) or 16 of 1024 (7.8, 8.0; 32: 10.3 against 8.0).
 //
-// A page newly given to a request is written to its table by the first row that
-// lies in it, which has just read it from the ring.
+// A page newly given to a request is written to its table by the row of the
+// page's first token, which has just read it from the ring.  (There is one: the
+// pages held before hold all computed tokens, so a new page begins with a new one.)
 #include <cstdint>
 
 #include "sv_internal.h"
@@ -105,8 +106,7 @@ __device__ __forceinline__ void do_rows(const PlanParams &P, const Workspace &W,
       } else {
         const int64_t at = static_cast<int64_t>(W.start[i]) + x - held;
         page = P.ring[at < P.capacity ? at : at - P.capacity];
-        const int first = i ? W.end[i - 1] : 0;
-        if (pos == x * P.block || row == first) *entry = page;
+        if (pos == x * P.block) *entry = page;
       }
       slot = static_cast<int64_t>(page) * P.block + (pos - x * P.block);
     }
