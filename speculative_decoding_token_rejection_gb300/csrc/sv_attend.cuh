@@ -260,9 +260,10 @@ __device__ __forceinline__ bool own_tile(const AttendParams &P, const AttendPlan
 
 // The private part over the 4-bit cache (sv_attend4.cu): tiles of 16 rows where every request's rows fit, of 32 where they
 // do or most requests' do, else of 64.  256 requests x 4096 keys, 16 rows each: 289 us in tiles of 16, 327 in tiles of 32;
-// but ragged ones of 12 rows on average and 20 at most 384 against 361.  Requests of 20 rows on average and 36 at most 410
-// us in tiles of 32, 459 in tiles of 64, of 24 and 44 480 against 467, of 36 and 64 541 against 491 (up to 8192 keys).
-constexpr int kOwnRows4 = 64, kOwnRowsMean = 24;
+// but ragged ones of 12 rows on average and 20 at most 384 against 361.  Up to 8192 keys, by mean rows, in tiles of 32 and of
+// 64: with 36 rows at most 20 432 and 479, 23 470 and 486, 24 481 and 490, 26 503 and 496; with 44 at most 20 446 and 469,
+// 23 471 and 474, 24 480 and 478; with 64 at most 20 462 and 477, 22 477 and 483, 23 486 and 482, 24 495 and 483.
+constexpr int kOwnRows4 = 64, kOwnRowsMean = 23;
 inline int own4_rows(const AttendParams &p) {
   const int64_t most = (p.G + 1) * static_cast<int64_t>(p.group), all = (p.T + p.N) * p.group;
   return most <= 16 ? 16 : most <= 32 || all <= static_cast<int64_t>(p.N) * kOwnRowsMean ? 32 : kOwnRows4;
