@@ -692,30 +692,39 @@ int cut(int64_t base, int keys, int num_sms, int &splits, int &chunk, int most_k
 // 1024 77 | 50, 2048 84 | 78, 4096 94 | 136; 512 x 8, 512 305 | 257, 1024 335 | 365;
 // 512 x 1, 256 118 | 95, 512 120 | 126; 2 x 5 (40 rows), 4096 33 | 29, 16384 48 | 38;
 // 16 x 1 (64 rows), 256 17 | 17, 1024 19 | 22.
-// Over the 4-bit cache few rows share a prefix on the tensor cores too, from the
-// same length: 16 requests x 1 token (64 rows) 4096 42 | 35, 8192 45 | 53, 16384 68 | 104,
-// 65536 176 | 303; 80 x 1 of one query head a kv head, 1024 46 | 43, 4096 51 | 124, 16384
-// 78 | 355; 8 x 2, 16384 70 | 56, 65536 178 | 179; 4 x 5, 65536 179 | 93 (never shared).
+// Over the 4-bit cache few rows share a prefix on the tensor cores too.  By a fit
+// to 13 batches at 8 prefixes each, a key read by each costs a CTA of its kernel 36
+// ps and 2 for each row group, shared 150 ps a kv head and 95 for each row tile,
+// and sharing 18 us and 900 ps a row to begin and end.  (On that table it loses 15 %
+// at most.)  Measured, us a call, shared | by each (32 heads over 8 of 128, 128
+// private keys): 8 requests x 4 tokens, prefix 16384 60 | 51, 32768 101 | 90; 16 x 1,
+// 4096 37 | 33, 8192 39 | 57; 64 x 5, 1024 48 | 37, 2048 57 | 66; 512 x 1, 256 108 | 88,
+// 1024 116 | 175; 512 x 8, 1024 285 | 226, 2048 333 | 362; 128 x 8 of 64 heads, 2048
+// 183 | 167, 4096 236 | 292; 30 x 5 of 40 heads over 2, 2048 49 | 47, 4096 56 | 62; 80 x
+// 1 of one head over one, 4096 32 | 25, 8192 34 | 37.
 bool four_bits(const AttendParams &p) { return p.c.format == SV_CACHE_E2M1 || p.c.format == SV_CACHE_INT4; }
 int own_rows(const AttendParams &p) { return four_bits(p) ? own4_rows(p) : 8 * kGroups; }
 
 AttendParams short_prefix(AttendParams p) {
-  const int64_t H = p.c.num_kv_heads, own = (p.G + 1) * static_cast<int64_t>(p.group), own_tiles = ceil_div(own, 8 * kGroups);
+  const int64_t H = p.c.num_kv_heads, own = (p.G + 1) * static_cast<int64_t>(p.group);
+  const int64_t own_tiles = ceil_div(own, four_bits(p) ? kOwnRows4 : 8 * kGroups), own_groups = ceil_div(ceil_div(own, 8), own_tiles);
   // (the rows there may be, so that calls with fewer tokens choose alike)
-  const int64_t rows = p.N * own;
-  int64_t saved = p.N * H * own_tiles * (24 + 7 * ceil_div(ceil_div(own, 8), own_tiles)), begin, most;  // ps a key; ps; keys
-  if (four_bits(p) || rows >= kTensorRows) {
-    saved -= H * (75 + 64 * static_cast<int64_t>(ceil_div(rows, kPrefixRowTile)));
+  const int64_t rows = p.N * own, row_tiles = ceil_div(rows, kPrefixRowTile);
+  int64_t saved, begin, most = INT64_MAX;  // ps a key; ps; keys
+  if (four_bits(p)) {
+    saved = p.N * H * own_tiles * (36 + 2 * own_groups) - H * (150 + 95 * row_tiles);
+    begin = 18000000 + 900 * rows * H;
+  } else if (rows >= kTensorRows) {
+    saved = p.N * H * own_tiles * (24 + 7 * own_groups) - H * (75 + 64 * row_tiles);
     begin = 31000000 + 950 * rows * H;
-    most = rows >= kTensorRows ? 16384 + 1 : INT64_MAX;
+    most = 16384 + 1;
   } else {
-    saved -= H * 5 * (24 * ceil_div(rows, 8 * kGroups) + 7 * ceil_div(rows, 8)) / 2;
+    saved = p.N * H * own_tiles * (24 + 7 * own_groups) -
+            H * 5 * (24 * ceil_div(rows, 8 * kGroups) + 7 * ceil_div(rows, 8)) / 2;
     begin = 200000;
-    most = INT64_MAX;
   }
   // (the 4-bit cache's prefix is shared on the tensor cores or not at all: make_plan's units must be countable)
-  const bool many = four_bits(p) && ceil_div(rows, kPrefixRowTile) * H *
-                                            (ceil_div(p.prefix, kPrefixKeyTile) + kTensorBegin) > 0x3FFFFFFF;
+  const bool many = four_bits(p) && row_tiles * H * (ceil_div(p.prefix, kPrefixKeyTile) + kTensorBegin) > 0x3FFFFFFF;
   if (many || p.prefix < (saved > 0 ? std::min(most, 128 + begin / saved) : most)) {
     p.row0 = p.prefix;
     p.prefix = 0;
