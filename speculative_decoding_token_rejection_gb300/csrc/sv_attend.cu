@@ -652,8 +652,9 @@ constexpr int kTensorLeast = 4;  // key tiles of a CTA of that kernel, where the
 constexpr int kTensorBegin = 7;  // and what beginning another (kv head, row tile) costs it, in key tiles
 constexpr int kChunkMost = 8192;                  // so that the longest request is no long tail
 constexpr int kJoinMany = 16;  // partial results of a row that eight warps join, or half as many where rows are few
-// The same over a 4-bit cache, where a chunk's CTAs do not fill the SMs: 6 requests x 64 rows over 60000 to 131072 keys 310
-// us against 350 with 8192; 64 x 20 over 8192 loses most by it, 200 against 193.
+// The same over a 4-bit cache, where a chunk's CTAs do not fill the SMs.  Us with chunks of at most 2048 | 4096 | 8192 keys:
+// 6 requests x 64 rows over 60000 to 131072 keys 341 | 336 | 373; 40 x 64 over 4096 to 16384 252 | 230 | 258; 32 x 20 over
+// 8192 to 16384 164 | 176 | 193; 64 x 20 over 8192 204 | 191 | 193; 2 x 64 over 100000 131 | 139 | 139.
 constexpr int kChunkFew = 4096;
 
 // Chunks for `keys` keys when `base` CTAs work on every chunk: enough to give
