@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
   // Half (or all) of the keys in krow to tensor memory, and their part of the scores.
   constexpr int kTwos = D / 32 / kHalves;  // pairs of groups in it
   auto unpack_keys = [&](int half) {
-    __syncwarp();
+    if (half) __syncwarp();  // (before the first half the loop's)
 #pragma unroll
     for (int two = 0; two < kTwos; ++two) {
       const int at = half * kTwos + two;
@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
   bool force = true;  // some row has no maximum
   bool ok = true;
   int it = 0;
+  __syncwarp();
   for (; it < ntiles; ++it) {
     const bool dead = !live;
     const float kc = __uint_as_float(ks) * c_all, v_scale = dead ? 0.0f : __uint_as_float(vs);
