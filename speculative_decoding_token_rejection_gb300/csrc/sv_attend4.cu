@@ -19,18 +19,21 @@
 // second.  A tile is 128 keys, its bytes are loaded a tile ahead.  Three to five
 // CTAs an SM hide each other's waits.
 //
-// What bounds it are instructions, about 800 a warp and tile: unpacking 256
-// elements a thread, 4 to 6 for a weight, addresses.  2.1 of an SM's 4 issue slots
-// a cycle are filled, as the pipes of conversions and 16-bit products take an
-// instruction every other cycle.  256 requests x 4096 keys x 8 heads of 128 (1.28
-// GB): 4 rows a head 281 us (0.67 of the copy rate), 16 rows 289, 20 rows 337, 32
-// rows 345, 64 rows 500.  By CTAs an SM (152 requests x 4 rows, tiles of 32): one
-// 385 us, two 241, three 225, four 196.  Lost: 256 threads, two a key, that
-// exchange maxima; K loaded long before V (350 us against 331); chunks of 2048 keys
-// (396 against 361); anything that spills in the loop.  Gained: bytes prefetched to
-// L2 a tile before they are loaded (350 to 331 us); places in shared memory.  One
-// tile alone takes 8.1 us, dependent loads (length, page, bytes) and code met for
-// the first time.
+// What bounds it are its warps' waits for their own stages: about 800 instructions
+// a warp and tile (unpacking 256 elements a thread, 4 to 6 for a weight, addresses),
+// one after another, by 3.5 warps a scheduler, 2.6 in tiles of 64 rows.  They fill 53 %
+// and 47 % of the issue slots and no pipe by half: integer operations and conversions
+// 46 %, fp32 and f16 arithmetic 29 %, shared memory's data 47 %, tensor cores 13 and 21 %
+// (256 ragged requests in tiles of 32 rows; 6 long ones in tiles of 64).  256 requests x
+// 4096 keys x 8 heads of 128 (1.28 GB): 4 rows a head 275 us (0.68 of the copy rate), 16
+// rows 287, 20 rows 339, 32 rows 347, 64 rows 497; head_dim 64, 4 rows 188 (0.53), 32 rows
+// 245.  By CTAs an SM (152 requests x 4 rows, tiles of 32): one 385 us, two 241, three 225,
+// four 196.  Lost: 256 threads, two a key, that exchange maxima; K loaded long before V
+// (350 us against 331); chunks of 2048 keys (396 against 361); anything that spills in
+// the loop (what -Xptxas -v shows is stored once a warp before it and read once or
+// twice behind it).  Gained: bytes prefetched to L2 a tile before they are loaded (350
+// to 331 us); places in shared memory.  One tile alone takes 8.9 us, dependent loads
+// (length, page, bytes) and code met for the first time.
 //
 // Numbers, as in the kernel for the shared prefix: x = (q . n) * (scale * log2 e *
 // key_scale), w = 2^(x - m), l = sum w, P = w * value_scale / W, O = W * sum P n_v.

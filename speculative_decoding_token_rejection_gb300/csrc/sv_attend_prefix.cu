@@ -44,8 +44,8 @@
 // or more in size is two numbers: one alone would lose what the value scales add,
 // and from 2^30 on P with it its place in f16.
 //
-// Measured: 512 requests x 8 tokens over 16384 keys, 827 us of the call's 1.05
-// ms: 1.33 PFLOP/s, 69 % of a plain matrix product's rate.  A key tile takes a
+// Measured: 512 requests x 8 tokens over 16384 keys, 811 us of the call's 1.05
+// ms: 1.36 PFLOP/s, 71 % of a plain matrix product's rate.  A key tile takes a
 // CTA about 3300 cycles, of which a softmax warp works for 1800 and waits for its row
 // tile's products for 1250; a segment adds 25000 (queries in, results out).
 #include <algorithm>

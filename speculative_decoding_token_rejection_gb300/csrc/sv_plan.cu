@@ -9,9 +9,9 @@
 // pages given back, are the same CTA's work, otherwise a second kernel's:
 // kRowsCta rows or kBackCta requests a CTA.
 //
-// Bound by latency.  4 requests x 5 rows: 5.8 us for the launch and the chain
+// Bound by latency.  4 requests x 5 rows: 5.9 us for the launch and the chain
 // (7.2 as two kernels); 512 requests that hold 512 pages each, 2700 rows, a
-// tenth done: 9.3 us (26 in one CTA); 64 prompts, 0.5 million rows: 11.9 us;
+// tenth done: 9.7 us (26 in one CTA); 64 prompts, 0.5 million rows: 12.0 us;
 // 4096 requests: 18.0 us.  One CTA is the faster up to 250 requests of 64
 // pages (6.8 us against 9.0) or 16 of 1024 (7.8, 8.0; 32: 10.3 against 8.0).
 //
