@@ -57,6 +57,7 @@ namespace {
 
 constexpr int kOwnKeys = 128, kOwnThreads = kOwnKeys;  // a thread a key
 constexpr float kRaise = 8;
+constexpr float kHuge = 4096;                   // maxima of this size are two numbers
 constexpr float kScaleUnit = 0x1p28f;           // W
 constexpr float kLeastUnits = kLeastLog2 - 28;  // log2 of the size that a scale counts as at least, in W
 
@@ -486,7 +487,8 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
       by = 1.0f;
     }
     // Weights with the m there is; in the first tile, or where a weight passes 2^8 with it (seldom), with a new one.
-    // (Below 2^20 a fused operation's exact product differs from a rounded one by less than 2^-4.)
+    // (Below kHuge a fused operation's exact product differs from a rounded one by 2^-12 at most.  Beyond, that would part
+    // equal scores, and from 2^28 on send weights out of range: there every product is rounded first.)
     bool fresh = force || C.huge, stop = false;
     for (;;) {
       if (fresh) {
@@ -494,16 +496,14 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
         // The rows' largest (x + part) + add, to the threads that keep the rows' m.
         auto largest = [&](const float *part, float add) {
 #pragma unroll 1
-          for (int g = 0; 2 * g < n8; ++g) {
-            float x[16];
-            exponents(g, x, C.zero);
+          for (int c = 0; c < n8; ++c) {
+            float x[8];
+            tmem_load_row(s_mine + c * 8, x);
+            tmem_wait_row(x);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = (x[e] + part[g * 16 + e]) + add;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float most = reduce_eight<true>(x + 8 * c, lane);
-              if ((lane & 3) == 0 && 2 * g + c < n8) C.part[warp][g * 16 + c * 8 + (lane >> 2)] = most;
-            }
+            for (int e = 0; e < 8; ++e) x[e] = (__fmul_rn(x[e], by) + part[c * 8 + e]) + add;
+            const float most = reduce_eight<true>(x, lane);
+            if ((lane & 3) == 0) C.part[warp][c * 8 + (lane >> 2)] = most;
             __syncwarp();
           }
           __syncthreads();
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
               mu = most;
             } else {
               mx = round == 0 ? most : fmaxf(C.mx[tid], most);
-              if (round == 0 && fabsf(mx) >= 1048576.0f && fabsf(mx) < INFINITY) C.huge = 1;
+              if (round == 0 && fabsf(mx) >= kHuge && fabsf(mx) < INFINITY) C.huge = 1;
               if (round == 1) C.negx[tid] = mx == -INFINITY ? 0.0f : -mx;
             }
           }
@@ -564,12 +564,13 @@ __global__ void __launch_bounds__(kOwnThreads, own4_ctas(D, NMAX))
         }
         if (C.huge) {  // the exponents take the scores' place
 #pragma unroll 1
-          for (int g = 0; 2 * g < n8; ++g) {
-            float x[16];
-            exponents(g, x, C.negx);
+          for (int c = 0; c < n8; ++c) {
+            float x[8];
+            tmem_load_row(s_mine + c * 8, x);
+            tmem_wait_row(x);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = x[e] + C.negu[g * 16 + e];
-            store_scores(g, x);
+            for (int e = 0; e < 8; ++e) x[e] = (__fmul_rn(x[e], by) + C.negx[c * 8 + e]) + C.negu[c * 8 + e];
+            tmem_store_8(s_mine + c * 8, x);
           }
           by = 1.0f;
           neg = C.zero;

@@ -40,7 +40,7 @@
 // 8, so P stays below 2^8.  Whether it may have is seen from max x and the
 // tile's largest value scale alone.  W is 2^28, the middle of the scales that
 // kv_write gives (2^-64 to 2^121): w and l stay within fp32 for any of them.
-// (One near the first tile's scales sent later ones out of range.)  An m of 2^24
+// (One near the first tile's scales sent later ones out of range.)  An m of 2^12
 // or more in size is two numbers: one alone would lose what the value scales add,
 // and from 2^30 on P with it its place in f16.
 //
@@ -67,7 +67,7 @@ constexpr int kVectorThreads = 64;
 constexpr int kPrefixThreads = kSoftmaxThreads + kVectorThreads + 64;
 constexpr int kVectorSlots = 4;
 constexpr float kRaise = 8;
-constexpr float kFar = 0x1p24f;  // maxima of this size are two numbers
+constexpr float kFar = 4096;  // maxima of this size are two numbers
 constexpr float kScaleUnit = 0x1p28f;  // W
 constexpr float kLeastUnits = kLeastLog2 - 28;  // log2 of the size that a scale counts as at least, in W
 
@@ -423,10 +423,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const AttendP
         };
         load_scores();
         // Most tiles: every row sees all keys and has a maximum that holds.  One fused operation an exponent then (below
-        // 2^24 its exact product differs from a rounded one by less than the 2^8 that a weight may grow).
+        // kFar its exact product differs from a rounded one by 2^-12 at most).
         bool plain = !cut;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) plain = plain && fabsf(m[x]) < 16777216.0f;
+        for (int x = 0; x < 4; ++x) plain = plain && fabsf(m[x]) < kFar;
         plain = __all_sync(0xFFFFFFFFu, plain);
         if (plain) {
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

@@ -35,16 +35,16 @@ def test_nan_stays_beside_a_weight_that_passes_the_range(dim, rows, later):
 
 
 def ties(lens, *, score, prefix=0, dim=128, fmt="int4", **kw):
-    """A batch in which all scores of a row are the same number, of `score` in size (base e), and value scales change by
-    fours and sixteens from 128 keys to the next."""
+    """A batch in which all scores of a row are the same number, of about `score` in size (base e) and never a product that
+    fp32 holds exactly, and value scales change by fours and sixteens from 128 keys to the next."""
     c = make([kw.pop("G", 0)] * len(lens), lens, prefix=prefix, dim=dim, fmt=fmt, uniform=True, seed=len(lens), **kw)
     c["q"] = torch.ones_like(c["q"])
     c["q"][:, 1::2] *= -1  # (every other query head has scores of the other sign)
     cache = c["cache"]
-    cache.k.fill_(0x22 if fmt == "int4" else 0x44)  # 2, twice
+    cache.k.fill_(0x33 if fmt == "int4" else 0x55)  # 3, twice
     cache.k_group.copy_(torch.ones(cache.k_group.shape))
     cache.k_scale.fill_(1.0)
-    c["scale"] = score / (2 * dim)
+    c["scale"] = 1.0001 * score / (3 * dim)
     cache.v_scale.fill_(1 / 64)
     for i, n in enumerate(lens):
         t = torch.arange(prefix if i else 0, n, device="cuda")
@@ -70,11 +70,11 @@ def check_averages(c):
             mean = v[:see].mean(0).repeat_interleave(c["group"], 0)
             size = v[:see].abs().mean(0).repeat_interleave(c["group"], 0)
             assert bool(((out[row].double() - mean).abs() <= 2.0 ** -8 * mean.abs() + 2.0 ** -10 * size).all())
-            score = c["q"][row, :, 0].double() * 2 * cache.head_dim * c["scale"]
+            score = c["q"][row, :, 0].double() * 3 * cache.head_dim * c["scale"]
             assert bool(((lse[row].double() - score - math.log(see)).abs() <= 2.0 ** -21 * (score.abs() + 20)).all())
 
 
-SCORES = [1.0, 3e5, 2.0 ** 22 + 1, 2.0 ** 24 + 2, 3.0 * 2 ** 25, 2.0 ** 28, 3.3 * 2 ** 30, 1e20, 2e38]
+SCORES = [1.0, 2000.0, 3e4, 3e5, 3e6, 2.0 ** 24 + 2, 3.0 * 2 ** 25, 2.0 ** 28, 3.3 * 2 ** 30, 1.1e20, 1.9e38]
 
 
 @pytest.mark.parametrize("score", SCORES)
@@ -82,6 +82,8 @@ SCORES = [1.0, 3e5, 2.0 ** 22 + 1, 2.0 ** 24 + 2, 3.0 * 2 ** 25, 2.0 ** 28, 3.3 
 def test_ties_over_several_chunks(dim, fmt, group, score):
     check_averages(ties([1000, 300, 128, 129], score=score, dim=dim, fmt=fmt, group=group))
     check_averages(ties([3000], score=score, dim=dim, fmt=fmt, group=group, G=1))
+    # many tiles a chunk
+    check_averages(ties([1000, 520, 300] + [4] * 317, score=score, dim=dim, fmt=fmt, group=group, G=3, kv_heads=1))
 
 
 @pytest.mark.parametrize("score", SCORES)
@@ -103,9 +105,9 @@ def test_ties_behind_a_shared_prefix_of_eight_bits(fmt, score):
     c["q"] = torch.ones_like(c["q"])
     c["q"][:, 1::2] *= -1
     cache, b = c["cache"], c["cache"].block_size
-    cache.k.copy_(torch.full(cache.k.shape, 2.0))
+    cache.k.copy_(torch.full(cache.k.shape, 3.0))
     cache.k_scale.fill_(1.0)
-    c["scale"] = score / (2 * cache.head_dim)
+    c["scale"] = 1.0001 * score / (3 * cache.head_dim)
     for i, n in enumerate(lens):
         page, off = places(c, i, range(7168 if i else 0, n))
         step = torch.arange(7168 if i else 0, n, device="cuda") // 128 * 5 % 8
@@ -120,5 +122,5 @@ def test_ties_behind_a_shared_prefix_of_eight_bits(fmt, score):
             mean = v[:see].mean(0).repeat_interleave(c["group"], 0)
             size = v[:see].abs().mean(0).repeat_interleave(c["group"], 0)
             assert bool(((out[row].double() - mean).abs() <= 2.0 ** -8 * mean.abs() + 2.0 ** -10 * size).all())
-            exact = c["q"][row, :, 0].double() * 2 * cache.head_dim * c["scale"]
+            exact = c["q"][row, :, 0].double() * 3 * cache.head_dim * c["scale"]
             assert bool(((lse[row].double() - exact - math.log(see)).abs() <= 2.0 ** -21 * (exact.abs() + 20)).all())
