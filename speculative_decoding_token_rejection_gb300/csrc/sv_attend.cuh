@@ -261,8 +261,8 @@ __device__ __forceinline__ bool own_tile(const AttendParams &P, const AttendPlan
 // The private part over the 4-bit cache (sv_attend4.cu): tiles of 16 rows where every request's rows fit, of 32 where they
 // do or most requests' do, else of 64.  256 requests x 4096 keys, 16 rows each: 289 us in tiles of 16, 327 in tiles of 32;
 // but ragged ones of 12 rows on average and 20 at most 384 against 361.  Up to 8192 keys, by mean rows, in tiles of 32 and of
-// 64: with 36 rows at most 20 432 and 479, 23 470 and 486, 24 481 and 490, 26 503 and 496; with 44 at most 20 446 and 469,
-// 23 471 and 474, 24 480 and 478; with 64 at most 20 462 and 477, 22 477 and 483, 23 486 and 482, 24 495 and 483.
+// 64: with 36 rows at most 20 428 and 469, 23 461 and 475, 24 474 and 479, 26 496 and 487; with 44 at most 20 440 and 461,
+// 23 466 and 468, 24 477 and 468; with 64 at most 20 456 and 468, 22 471 and 471, 23 478 and 472, 24 488 and 474.
 constexpr int kOwnRows4 = 64, kOwnRowsMean = 23;
 inline int own4_rows(const AttendParams &p) {
   const int64_t most = (p.G + 1) * static_cast<int64_t>(p.group), all = (p.T + p.N) * p.group;

@@ -25,9 +25,9 @@
 // and 47 % of the issue slots and no pipe by half: integer operations and conversions
 // 46 %, fp32 and f16 arithmetic 29 %, shared memory's data 47 %, tensor cores 13 and 21 %
 // (256 ragged requests in tiles of 32 rows; 6 long ones in tiles of 64).  256 requests x
-// 4096 keys x 8 heads of 128 (1.28 GB): 4 rows a head 275 us (0.68 of the copy rate), 16
-// rows 287, 20 rows 339, 32 rows 347, 64 rows 497; head_dim 64, 4 rows 188 (0.53), 32 rows
-// 245.  By CTAs an SM (152 requests x 4 rows, tiles of 32): one 385 us, two 241, three 225,
+// 4096 keys x 8 heads of 128 (1.28 GB): 4 rows a head 270 us (0.70 of the copy rate), 16
+// rows 283, 20 rows 343, 32 rows 352, 64 rows 495; head_dim 64, 4 rows 185 (0.54), 32 rows
+// 239.  By CTAs an SM (152 requests x 4 rows, tiles of 32): one 385 us, two 241, three 225,
 // four 196.  Lost: 256 threads, two a key, that exchange maxima; K loaded long before V
 // (350 us against 331); chunks of 2048 keys (396 against 361); anything that spills in
 // the loop (what -Xptxas -v shows is stored once a warp before it and read once or
