@@ -30,8 +30,8 @@
 // 239.  By CTAs an SM (152 requests x 4 rows, tiles of 32): one 385 us, two 241, three 225,
 // four 196.  Lost: 256 threads, two a key, that exchange maxima; K loaded long before V
 // (350 us against 331); chunks of 2048 keys (396 against 361); anything that spills in
-// the loop (what -Xptxas -v shows is stored once a warp before it and read once or
-// twice behind it).  Gained: bytes prefetched to L2 a tile before they are loaded (350
+// the loop (what -Xptxas -v shows lies outside: up to two stores and four loads a warp,
+// whatever its tiles).  Gained: bytes prefetched to L2 a tile before they are loaded (350
 // to 331 us); places in shared memory.  One tile alone takes 8.9 us, dependent loads
 // (length, page, bytes) and code met for the first time.
 //
